@@ -14,6 +14,7 @@ Exact Solution from Continuous-Time Dynamics", page es, Metodologia item 3):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -25,6 +26,9 @@ __all__ = [
     "efla_fwd_workspace_size", "efla_bwd_workspace_size", "efla_get_status",
     "efla_fwd_save", "efla_bwd_saved", "efla_fwd_states_size", "efla_bwd_saved_workspace_size",
     "efla_bwd_plan", "efla_mixer_proj", "MixerShape",
+    "efla_gated_fwd", "efla_gated_bwd", "efla_gated_step", "GatedShape", "make_gated_shape",
+    "efla_gated_fwd_workspace_size", "efla_gated_bwd_workspace_size",
+    "efla_norm_fwd", "efla_norm_bwd", "NormShape",
     "F32", "BF16", "EXACT", "EULER", "AUTO", "SIMT", "TENSOR", "efla_tc_selftest", "efla_wait_selftest",
 ]
 
@@ -58,6 +62,21 @@ class Shape(ctypes.Structure):
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("chunk", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("mode", ctypes.c_int),
                 ("path", ctypes.c_int)]
+
+
+_Strides = ctypes.c_longlong * 3
+_GATED_ARRAYS = ("q", "k", "v", "g", "beta", "o", "do", "dq", "dk", "dv")
+
+
+class GatedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "Hk", "L", "dk", "dv", "dtype", "out_dtype", "mode", "path",
+                                            "packed")] + [(n + "_stride", _Strides) for n in _GATED_ARRAYS]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("x_stride", ctypes.c_longlong),
+                ("y_stride", ctypes.c_longlong), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -103,6 +122,23 @@ def load_library(path: Optional[str] = None):
     lib.efla_fwd_noalloc.argtypes = [sp] + [_vp] * 8
     lib.efla_step.restype = ctypes.c_int
     lib.efla_step.argtypes = [sp] + [_vp] * 7
+    gp = ctypes.POINTER(GatedShape)
+    for name in ("efla_gated_fwd_workspace_size", "efla_gated_bwd_workspace_size"):
+        getattr(lib, name).restype = ctypes.c_size_t
+        getattr(lib, name).argtypes = [gp]
+    lib.efla_gated_fwd.restype = ctypes.c_int
+    lib.efla_gated_fwd.argtypes = [gp] + [_vp] * 10 + [ctypes.c_size_t, _vp]
+    lib.efla_gated_bwd.restype = ctypes.c_int
+    lib.efla_gated_bwd.argtypes = [gp] + [_vp] * 16 + [ctypes.c_size_t, _vp]
+    lib.efla_gated_step.restype = ctypes.c_int
+    lib.efla_gated_step.argtypes = [gp] + [_vp] * 7 + [ctypes.c_int, _vp, _vp]
+    np_ = ctypes.POINTER(NormShape)
+    lib.efla_norm_fwd.restype = ctypes.c_int
+    lib.efla_norm_fwd.argtypes = [np_] + [_vp] * 6
+    lib.efla_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.efla_norm_bwd_workspace_size.argtypes = [np_]
+    lib.efla_norm_bwd.restype = ctypes.c_int
+    lib.efla_norm_bwd.argtypes = [np_] + [_vp] * 8 + [ctypes.c_size_t, _vp]
     lib.efla_wait_selftest.restype = ctypes.c_int
     lib.efla_wait_selftest.argtypes = [ctypes.c_int, ctypes.c_int, _vp]
     lib.efla_tc_selftest.restype = ctypes.c_int
@@ -333,6 +369,243 @@ def efla_step(q, k, v, beta, S, *, out_dtype=None, mode: int = EXACT, o=None, st
                                   _ptr(S), _ptr(o), _stream(stream))
     _check(rc, "efla_step")
     return o
+
+
+# ------------------------------------------------------------------ gated delta rule
+def _on_stream(fn):
+    """Fresh outputs and workspaces of a call with stream=... come from that stream's memory pool:
+    its earlier work, and nothing else's, may still be using them."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(s):
+            return fn(*args, stream=stream, **kw)
+    return call
+
+
+def _view(t: Optional[torch.Tensor], name: str, shape, dtype) -> Optional[int]:
+    """Pointer of a strided CUDA tensor of the given shape and type, its last dimension contiguous."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors must be CUDA tensors")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _strides(t: torch.Tensor, packed: bool, scalar: bool):
+    """{batch, head, token} strides of [B,H,L(,d)] (packed: [H,T(,d)])."""
+    s = t.stride() if scalar else t.stride()[:-1]
+    if not scalar and t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return _Strides(*((0,) + tuple(s) if packed else s))
+
+
+def make_gated_shape(B, H, Hk, L, dk, dv, dtype=torch.bfloat16, out_dtype=None, mode: int = EULER,
+                     path: int = AUTO, packed: bool = False, strides=None) -> GatedShape:
+    """strides: {array name: (batch, head, token)} in elements; arrays not named: dense [B,H,L,d]
+    (packed: [H,L,d])."""
+    out_dtype = dtype if out_dtype is None else out_dtype
+    s = GatedShape(B, H, Hk, L, dk, dv, _dt(dtype), _dt(out_dtype), mode, path, int(packed))
+    for n in _GATED_ARRAYS:
+        heads = Hk if n in ("q", "k", "dq", "dk") else H
+        d = 1 if n in ("g", "beta") else dk if n in ("q", "k", "dq", "dk") else dv
+        st = (strides or {}).get(n)
+        setattr(s, n + "_stride", _Strides(*(st if st is not None else (0 if packed else heads * L * d, L * d, d))))
+    return s
+
+
+def efla_gated_fwd_workspace_size(shape: GatedShape) -> int:
+    return load_library().efla_gated_fwd_workspace_size(ctypes.byref(shape))
+
+
+def efla_gated_bwd_workspace_size(shape: GatedShape) -> int:
+    return load_library().efla_gated_bwd_workspace_size(ctypes.byref(shape))
+
+
+def _gated_sizes(q, k, v, offsets):
+    """(B, H, Hk, L, dk, dv, leading dimensions) of a call's tensors."""
+    packed = offsets is not None
+    if v.dim() != (3 if packed else 4) or k.dim() != v.dim():
+        raise ValueError("q, k, v: expected [B,H,L,d], or [H,T,d] with offsets")
+    if packed:
+        if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 \
+                or not offsets.is_contiguous():
+            raise ValueError("offsets: expected a contiguous CUDA int32 tensor [B + 1]")
+        B, lead = offsets.numel() - 1, ()
+    else:
+        B, lead = v.shape[0], (v.shape[0],)
+    return B, v.shape[-3], k.shape[-3], v.shape[-2], k.shape[-1], v.shape[-1], lead
+
+
+def _like(t: torch.Tensor, dtype) -> torch.Tensor:
+    """A fresh tensor of t's shape, in t's order of storage (dense)."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.preserve_format)
+
+
+def _gated_inputs(q, k, v, g, beta, sizes, packed, extra=()):
+    B, H, Hk, L, dk, dv, lead = sizes
+    args = [("q", q, lead + (Hk, L, dk), v.dtype), ("k", k, lead + (Hk, L, dk), v.dtype),
+            ("v", v, lead + (H, L, dv), v.dtype), ("g", g, lead + (H, L), torch.float32),
+            ("beta", beta, lead + (H, L), torch.float32), *extra]
+    ptrs = [_view(t, n, s, dt) for n, t, s, dt in args]
+    return ptrs, {("do" if n == "dO" else n): _strides(t, packed, t.dim() == len(lead) + 2) for n, t, _, _ in args}
+
+
+@_on_stream
+def efla_gated_fwd(q, k, v, g, beta, S0=None, *, offsets=None, out_dtype=None, mode: int = EULER, o=None,
+                   S_final=None, workspace=None, want_state: bool = True, stream=None, path: int = AUTO):
+    """Chunked gated delta rule: S <- e^g S, S <- S + alpha k (v - S^T k)^T, o = S^T q.
+
+    q, k [B,Hk,L,dk], v [B,H,L,dv] (any strides, last dimension contiguous), g (log decay) and beta
+    [B,H,L] fp32, S0 [B,H,dk,dv] fp32.  With offsets (int32 [B+1] on the GPU) the sequences are packed
+    on one axis of tokens: q, k [Hk,T,dk], v [H,T,dv], g, beta [H,T].
+    Returns (o, in v's order of storage, S_final [B,H,dk,dv] fp32 or None)."""
+    sizes = _gated_sizes(q, k, v, offsets)
+    B, H, Hk, L, dk, dv, lead = sizes
+    packed = offsets is not None
+    ptrs, st = _gated_inputs(q, k, v, g, beta, sizes, packed)
+    odt = v.dtype if out_dtype is None else out_dtype
+    o = _like(v, odt) if o is None else o
+    po = _view(o, "o", lead + (H, L, dv), odt)
+    st["o"] = _strides(o, packed, False)
+    if S_final is not None or want_state:
+        S_final = _out(S_final, (B, H, dk, dv), torch.float32, v.device, "S_final")
+    _state_shape(S0, (B, H, dk, dv), "S0")
+    shape = make_gated_shape(B, H, Hk, L, dk, dv, v.dtype, odt, mode, path, packed, st)
+    ws = _workspace(efla_gated_fwd_workspace_size(shape), v.device, workspace)
+    rc = load_library().efla_gated_fwd(ctypes.byref(shape), _ptr(offsets), *ptrs, _ptr(S0), po, _ptr(S_final),
+                                       _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    _check(rc, "efla_gated_fwd")
+    return o, S_final
+
+
+def _state_shape(t, shape, name):
+    if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32):
+        raise ValueError(f"{name}: expected torch.float32 {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+@_on_stream
+def efla_gated_bwd(q, k, v, g, beta, dO, S0=None, dS_final=None, *, offsets=None, out_dtype=None,
+                   mode: int = EULER, dq=None, dk=None, dv=None, want_dS0: bool = True, workspace=None,
+                   stream=None, path: int = AUTO):
+    """Backward of efla_gated_fwd (same shapes; dO as v).  Returns (dq, dk, dv, dg, dbeta, dS0 or None):
+    dq, dk, dv in the order of storage of q, k, v, or into the tensors given (which may be slices of one
+    buffer); dg, dbeta fp32, dense."""
+    sizes = _gated_sizes(q, k, v, offsets)
+    B, H, Hk, L, nk, nv, lead = sizes
+    packed = offsets is not None
+    ptrs, st = _gated_inputs(q, k, v, g, beta, sizes, packed, [("dO", dO, lead + (H, L, nv), v.dtype)])
+    odt = v.dtype if out_dtype is None else out_dtype
+    dq, dk, dv = (_like(t, odt) if x is None else x for x, t in ((dq, q), (dk, k), (dv, v)))
+    pout = [_view(t, n, lead + s, odt) for n, t, s in (("dq", dq, (Hk, L, nk)), ("dk", dk, (Hk, L, nk)),
+                                                      ("dv", dv, (H, L, nv)))]
+    for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        st[n] = _strides(t, packed, False)
+    dg = torch.empty(lead + (H, L), dtype=torch.float32, device=v.device)
+    db = torch.empty_like(dg)
+    dS0 = torch.empty((B, H, nk, nv), dtype=torch.float32, device=v.device) if want_dS0 else None
+    _state_shape(S0, (B, H, nk, nv), "S0")
+    _state_shape(dS_final, (B, H, nk, nv), "dS_final")
+    shape = make_gated_shape(B, H, Hk, L, nk, nv, v.dtype, odt, mode, path, packed, st)
+    ws = _workspace(efla_gated_bwd_workspace_size(shape), v.device, workspace)
+    rc = load_library().efla_gated_bwd(ctypes.byref(shape), _ptr(offsets), *ptrs[:5], _ptr(S0), ptrs[5],
+                                       _ptr(dS_final), *pout, _ptr(dg), _ptr(db), _ptr(dS0), _ptr(ws),
+                                       ws.numel() * ws.element_size(), _stream(stream))
+    _check(rc, "efla_gated_bwd")
+    return dq, dk, dv, dg, db, dS0
+
+
+@_on_stream
+def efla_gated_step(q, k, v, g, beta, S, *, slots=None, out_dtype=None, mode: int = EULER, o=None, stream=None):
+    """One token of the gated delta rule on a cache of states S [n,H,dk,dv] fp32, updated in place.
+
+    q, k [B,Hk,dk], v [B,H,dv] (any strides, last dimension contiguous), g, beta [B,H] fp32.  slots (int32
+    [B] on the GPU): each sequence's place in the cache (outside [0, n): skipped, o = 0); None: place b.
+    Returns o [B,H,dv]."""
+    if v.dim() != 3 or k.dim() != 3 or S.dim() != 4:
+        raise ValueError("expected q, k [B,Hk,dk], v [B,H,dv], S [n,H,dk,dv]")
+    B, H, dv = v.shape
+    Hk, dk = k.shape[1:]
+    args = [("q", q, (B, Hk, dk), v.dtype), ("k", k, (B, Hk, dk), v.dtype), ("v", v, (B, H, dv), v.dtype),
+            ("g", g, (B, H), torch.float32), ("beta", beta, (B, H), torch.float32)]
+    ptrs = [_view(t, n, s, dt) for n, t, s, dt in args]
+    odt = v.dtype if out_dtype is None else out_dtype
+    o = _like(v, odt) if o is None else o
+    po = _view(o, "o", (B, H, dv), odt)
+    st = {}
+    for n, t in [(a[0], a[1]) for a in args] + [("o", o)]:
+        if t.dim() == 3 and t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{n}: the last dimension must be contiguous")
+        st[n] = (t.stride(0), t.stride(1), 0)
+    _state_shape(S, (S.shape[0], H, dk, dv), "S")
+    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (B,)):
+        raise ValueError(f"slots: expected torch.int32 ({B},), got {slots.dtype} {tuple(slots.shape)}")
+    shape = make_gated_shape(B, H, Hk, 1, dk, dv, v.dtype, odt, mode, AUTO, False, st)
+    rc = load_library().efla_gated_step(ctypes.byref(shape), *ptrs, _ptr(S), _ptr(slots), S.shape[0], po,
+                                        _stream(stream))
+    _check(rc, "efla_gated_step")
+    return o
+
+
+# ------------------------------------------------------------------ layer norm
+def _rows2d(t: torch.Tensor, name: str) -> torch.Tensor:
+    """[..., D] as [rows, D] without a copy (rows one stride apart, D contiguous)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors must be CUDA tensors")
+    if t.dim() < 1 or (t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1):
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    try:
+        return t.view(-1, t.shape[-1]) if t.numel() else t.new_empty((0, t.shape[-1]))
+    except RuntimeError:
+        raise ValueError(f"{name}: its rows must lie one stride apart") from None
+
+
+def _norm_shape(x2, y2, weight, eps) -> NormShape:
+    rows, D = x2.shape
+    return NormShape(rows, D, x2.stride(0) if rows > 1 else D, y2.stride(0) if rows > 1 else D, _dt(x2.dtype),
+                     _dt(weight.dtype), eps)
+
+
+@_on_stream
+def efla_norm_fwd(x, weight, bias=None, *, eps: float = 1e-5, y=None, stats=None, stream=None):
+    """Layer norm over the last dimension of x [..., D].  weight, bias [D] (fp32 or bf16).
+
+    Returns (y like x, stats [..., 2] fp32: mean and 1/sqrt(var + eps) of each row)."""
+    x2, D = _rows2d(x, "x"), x.shape[-1]
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+    _view(y, "y", x.shape, x.dtype)
+    for n, t in (("weight", weight), ("bias", bias)):
+        _view(t, n, (D,), weight.dtype)
+    stats = _out(stats, tuple(x.shape[:-1]) + (2,), torch.float32, x.device, "stats")
+    y2 = _rows2d(y, "y")
+    shape = _norm_shape(x2, y2, weight, eps)
+    rc = load_library().efla_norm_fwd(ctypes.byref(shape), x2.data_ptr(), _ptr(weight), _ptr(bias), y2.data_ptr(),
+                                      _ptr(stats), _stream(stream))
+    _check(rc, "efla_norm_fwd")
+    return y, stats
+
+
+@_on_stream
+def efla_norm_bwd(x, weight, dy, stats, *, want_bias: bool = True, workspace=None, stream=None):
+    """Backward of efla_norm_fwd.  Returns (dx dense, dweight, dbias or None), the last two in weight's type."""
+    x2, dy2, D = _rows2d(x, "x"), _rows2d(dy, "dy"), x.shape[-1]
+    _view(dy, "dy", x.shape, x.dtype)
+    _view(weight, "weight", (D,), weight.dtype)
+    _view(stats, "stats", tuple(x.shape[:-1]) + (2,), torch.float32)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty(D, dtype=weight.dtype, device=x.device)
+    db = torch.empty_like(dw) if want_bias else None
+    shape = _norm_shape(x2, dy2, weight, 0.0)
+    ws = _workspace(load_library().efla_norm_bwd_workspace_size(ctypes.byref(shape)), x.device, workspace)
+    rc = load_library().efla_norm_bwd(ctypes.byref(shape), x2.data_ptr(), _ptr(weight), dy2.data_ptr(), _ptr(stats),
+                                      dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream))
+    _check(rc, "efla_norm_bwd")
+    return dx, dw, db
 
 
 def efla_tc_selftest(A, B, C, a_mn_major=False, b_mn_major=False, a_in_tmem=False, stream=None):

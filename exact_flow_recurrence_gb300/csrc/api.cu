@@ -7,6 +7,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/efla.h"
+#include "gated.h"
 #include "launch.h"
 
 namespace {
@@ -493,6 +494,372 @@ efla_status efla_tc_selftest(int N, int K, int flags, const void* A, const void*
     efla::prof_mark(nullptr, stream);
     cudaError_t e = efla::launch_tc_selftest(N, K, flags, A, B, C, D, stream);
     return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_tc_selftest");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ gated delta rule, layer norm
+namespace {
+
+// A [rows][d] array reached through {batch, head, token} strides (elements).
+struct Strided {
+    const void* p;
+    const char* name;
+    int n[3], d, es;
+    const long long* s;
+    size_t bytes() const {
+        if (!n[0] || !n[1] || !n[2]) return 0;
+        long long e = d;
+        for (int i = 0; i < 3; ++i) e += (n[i] - 1LL) * s[i];
+        return (size_t)e * es;
+    }
+    Span span() const { return Span{p, bytes(), name}; }
+    // whether vector copies and tensor maps can read it: 16-byte rows, no broadcast dimension
+    bool wide() const {
+        if (!aligned16(p)) return false;
+        for (int i = 0; i < 3; ++i)
+            if (n[i] > 1 && (s[i] <= 0 || (s[i] * es) % 16 != 0 || s[i] * es >= (1LL << 39))) return false;
+        return true;
+    }
+    // no two rows share an element
+    bool disjoint_rows() const {
+        bool used[3] = {false, false, false};
+        long long ext = d;
+        for (int k = 0; k < 3; ++k) {   // dimensions by growing stride
+            int m = -1;
+            for (int i = 0; i < 3; ++i)
+                if (!used[i] && n[i] > 1 && (m < 0 || s[i] < s[m])) m = i;
+            if (m < 0) break;
+            used[m] = true;
+            if (s[m] < ext) return false;
+            ext += (n[m] - 1LL) * s[m];
+        }
+        return true;
+    }
+};
+
+// Two arrays whose spans overlap but whose elements do not: slices of the same token rows.
+bool interleaved(const Strided& a, const Strided& b) {
+    if (a.es != b.es || a.s[2] != b.s[2] || (a.n[0] > 1 && a.s[0] != b.s[0])) return false;
+    const long long st = a.s[2], wa = a.d + (a.n[1] - 1LL) * a.s[1], wb = b.d + (b.n[1] - 1LL) * b.s[1];
+    const long long bytes = (long long)((uintptr_t)b.p - (uintptr_t)a.p);
+    if (st <= 0 || bytes % a.es || (a.n[0] > 1 && a.s[0] % st)) return false;
+    const long long off = ((bytes / a.es) % st + st) % st;   // b's place in a's token row
+    return off >= wa && off + wb <= st;
+}
+
+efla_status check_gated(const efla_gated_shape* s, bool step, bool bwd, efla::GDims* d) {
+    if (!s) return fail(EFLA_ERR_INVALID_ARG, "shape is NULL");
+    if (s->B < 0 || s->H < 0 || s->Hk < 0 || s->L < 0)
+        return fail(EFLA_ERR_INVALID_ARG, "negative size (B=%d H=%d Hk=%d L=%d)", s->B, s->H, s->Hk, s->L);
+    if (s->H > 0 && (s->Hk == 0 || s->H % s->Hk))
+        return fail(EFLA_ERR_INVALID_ARG, "H=%d value heads are not a multiple of Hk=%d key heads", s->H, s->Hk);
+    if (s->packed != 0 && s->packed != 1) return fail(EFLA_ERR_INVALID_ARG, "packed=%d: need 0 or 1", s->packed);
+    if (step && (s->packed || s->L != 1))
+        return fail(EFLA_ERR_INVALID_ARG, "efla_gated_step needs L == 1 and packed == 0 (got %d, %d)", s->L, s->packed);
+    if (!dim_ok(s->dk) || !dim_ok(s->dv))
+        return fail(EFLA_ERR_UNSUPPORTED, "dk=%d dv=%d: need multiples of 16 in [16,128]", s->dk, s->dv);
+    if (!dtype_ok(s->dtype) || !dtype_ok(s->out_dtype))
+        return fail(EFLA_ERR_UNSUPPORTED, "dtype=%d out_dtype=%d: need EFLA_F32 or EFLA_BF16", (int)s->dtype,
+                    (int)s->out_dtype);
+    if (s->mode != EFLA_EXACT && s->mode != EFLA_EULER)
+        return fail(EFLA_ERR_UNSUPPORTED, "mode=%d: need EFLA_EXACT or EFLA_EULER", (int)s->mode);
+    if (s->path != EFLA_PATH_AUTO && s->path != EFLA_PATH_SIMT && s->path != EFLA_PATH_TENSOR)
+        return fail(EFLA_ERR_UNSUPPORTED, "path=%d: need EFLA_PATH_AUTO, _SIMT or _TENSOR", (int)s->path);
+    if (s->H > 65535) return fail(EFLA_ERR_UNSUPPORTED, "H=%d exceeds 65535", s->H);
+    if ((long long)s->B * s->H > 0x7fffffffLL || (s->packed ? 1LL : s->B) * (s->L / 16 + 1LL) + s->B > 0x7fffffffLL)
+        return fail(EFLA_ERR_UNSUPPORTED, "B=%d H=%d L=%d: too many chunks for one launch", s->B, s->H, s->L);
+    const long long(*all[10])[3] = {&s->q_stride, &s->k_stride, &s->v_stride, &s->g_stride, &s->beta_stride,
+                                    &s->o_stride, &s->do_stride, &s->dq_stride, &s->dk_stride, &s->dv_stride};
+    long long(*to[10])[3] = {&d->qs, &d->ks, &d->vs, &d->gs, &d->bs, &d->os, &d->dos, &d->dqs, &d->dks, &d->dvs};
+    for (int i = 0; i < 10; ++i)
+        for (int j = 0; j < 3; ++j) {
+            if ((*all[i])[j] < 0) return fail(EFLA_ERR_INVALID_ARG, "negative stride");
+            (*to[i])[j] = (*all[i])[j];
+        }
+    d->B = s->B; d->H = s->H; d->Hk = s->Hk; d->L = s->L; d->dk = s->dk; d->dv = s->dv;
+    d->in_bf16 = s->dtype == EFLA_BF16;
+    d->out_bf16 = s->out_dtype == EFLA_BF16;
+    d->euler = s->mode == EFLA_EULER;
+    d->packed = s->packed;
+    d->tensor = 0;
+    d->offsets = nullptr;
+    (void)bwd;
+    return EFLA_OK;
+}
+
+struct GatedIo {
+    Strided x[10];   // q, k, v, g, beta, o, dO, dq, dk, dv (those the call has)
+};
+
+GatedIo gated_io(const efla_gated_shape* s, const void* q, const void* k, const void* v, const void* g,
+                 const void* beta, const void* o, const void* dO, const void* dq, const void* dk, const void* dv) {
+    const int b = s->packed ? 1 : s->B, e = (int)esize(s->dtype), eo = (int)esize(s->out_dtype);
+    return GatedIo{{{q, "q", {b, s->Hk, s->L}, s->dk, e, s->q_stride},
+                    {k, "k", {b, s->Hk, s->L}, s->dk, e, s->k_stride},
+                    {v, "v", {b, s->H, s->L}, s->dv, e, s->v_stride},
+                    {g, "g", {b, s->H, s->L}, 1, 4, s->g_stride},
+                    {beta, "beta", {b, s->H, s->L}, 1, 4, s->beta_stride},
+                    {o, "o", {b, s->H, s->L}, s->dv, eo, s->o_stride},
+                    {dO, "dO", {b, s->H, s->L}, s->dv, e, s->do_stride},
+                    {dq, "dq", {b, s->Hk, s->L}, s->dk, eo, s->dq_stride},
+                    {dk, "dk", {b, s->Hk, s->L}, s->dk, eo, s->dk_stride},
+                    {dv, "dv", {b, s->H, s->L}, s->dv, eo, s->dv_stride}}};
+}
+
+// Required arrays: present, aligned to their element; outputs with rows apart from each other.
+efla_status check_strided(const Strided* x, int n, int first_out) {
+    for (int i = 0; i < n; ++i) {
+        if (x[i].bytes() == 0) continue;
+        if (!x[i].p) return fail(EFLA_ERR_INVALID_ARG, "%s is NULL", x[i].name);
+        if ((uintptr_t)x[i].p % (unsigned)x[i].es)
+            return fail(EFLA_ERR_ALIGNMENT, "%s is not aligned to its elements", x[i].name);
+        if (i >= first_out && !x[i].disjoint_rows())
+            return fail(EFLA_ERR_INVALID_ARG, "%s: strides make its rows overlap", x[i].name);
+    }
+    return EFLA_OK;
+}
+
+// Strided inputs and outputs, dense outputs, and the workspace: every output apart from
+// every input, from the other outputs and from the workspace.
+efla_status check_gated_alias(const Strided* x, int n, int first_out, const Span* ins, int nin, const Span* outs,
+                              int nout, const Span& ws) {
+    for (int i = first_out; i < n; ++i) {
+        const Span o = x[i].span();
+        for (int j = 0; j < first_out; ++j)
+            if (overlap(o, x[j].span())) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input %s", o.name, x[j].name);
+        for (int j = 0; j < nin; ++j)
+            if (overlap(o, ins[j])) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input %s", o.name, ins[j].name);
+        for (int j = 0; j < nout; ++j)
+            if (overlap(o, outs[j])) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps %s", o.name, outs[j].name);
+        for (int j = i + 1; j < n; ++j)
+            if (overlap(o, x[j].span()) && !interleaved(x[i], x[j]) && !interleaved(x[j], x[i]))
+                return fail(EFLA_ERR_INVALID_ARG, "%s overlaps %s", o.name, x[j].name);
+        if (overlap(o, ws)) return fail(EFLA_ERR_INVALID_ARG, "workspace overlaps %s", o.name);
+    }
+    for (int j = 0; j < first_out; ++j) {
+        for (int i = 0; i < nout; ++i)
+            if (overlap(outs[i], x[j].span()))
+                return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input %s", outs[i].name, x[j].name);
+        if (overlap(ws, x[j].span())) return fail(EFLA_ERR_INVALID_ARG, "workspace overlaps %s", x[j].name);
+    }
+    for (int i = 0; i < nout; ++i) {
+        for (int j = i + 1; j < nout; ++j)
+            if (overlap(outs[i], outs[j])) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, outs[j].name);
+        if (overlap(ws, outs[i])) return fail(EFLA_ERR_INVALID_ARG, "workspace overlaps %s", outs[i].name);
+    }
+    for (int j = 0; j < nin; ++j)
+        if (overlap(ws, ins[j])) return fail(EFLA_ERR_INVALID_ARG, "workspace overlaps %s", ins[j].name);
+    return EFLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t efla_gated_fwd_workspace_size(const efla_gated_shape* s) {
+    efla::GDims d;
+    if (check_gated(s, false, false, &d) != EFLA_OK) return 0;
+    return efla::gated_simt_fwd_ws_bytes(d);
+}
+
+size_t efla_gated_bwd_workspace_size(const efla_gated_shape* s) {
+    efla::GDims d;
+    if (check_gated(s, false, true, &d) != EFLA_OK) return 0;
+    return efla::gated_simt_bwd_ws_bytes(d);
+}
+
+efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const void* q, const void* k, const void* v,
+                           const float* g, const float* beta, const float* S0, void* o, float* S_final,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_gated_fwd");
+    g_msg[0] = 0;
+    efla::GDims d;
+    efla_status st = check_gated(s, false, false, &d);
+    if (st != EFLA_OK) return st;
+    if (s->path == EFLA_PATH_TENSOR) return fail(EFLA_ERR_UNSUPPORTED, "efla_gated_fwd: path must be AUTO or SIMT");
+    if (d.BH() == 0) return EFLA_OK;
+    const GatedIo io = gated_io(s, q, k, v, g, beta, o, nullptr, nullptr, nullptr, nullptr);
+    if ((st = check_strided(io.x, 6, 5)) != EFLA_OK) return st;
+    const size_t sbytes = (size_t)d.BH() * d.dk * d.dv * 4;
+    const Span sS0{S0, sbytes, "S0"}, sSf{S_final, sbytes, "S_final"}, sw{workspace, workspace_bytes, "workspace"},
+        soff{offsets, ((size_t)d.B + 1) * 4, "offsets"};
+    const Span opt[] = {sS0, sSf, sw};
+    if ((st = check_ptrs(nullptr, 0, opt, 3)) != EFLA_OK) return st;
+    if (d.packed && !offsets) return fail(EFLA_ERR_INVALID_ARG, "offsets is NULL (packed)");
+    if (d.packed && (uintptr_t)offsets % 4) return fail(EFLA_ERR_ALIGNMENT, "offsets is not 4-byte aligned");
+    d.offsets = d.packed ? offsets : nullptr;
+    if (S_final && S0 && S_final != (float*)S0 && overlap(sSf, sS0))
+        return fail(EFLA_ERR_INVALID_ARG, "S_final partially overlaps S0");
+    {
+        const Span ins[] = {sS0, d.packed ? soff : Span{nullptr, 0, ""}};
+        const Span outs[] = {S_final == (float*)S0 ? Span{nullptr, 0, ""} : sSf};
+        if ((st = check_gated_alias(io.x, 6, 5, ins, 2, outs, 1, sw)) != EFLA_OK) return st;
+    }
+    const size_t need = efla::gated_simt_fwd_ws_bytes(d);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t e = efla::launch_gated_fwd_simt(d, q, k, v, g, beta, S0, o, S_final, workspace, stream);
+    return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_gated_fwd");
+}
+
+efla_status efla_gated_bwd(const efla_gated_shape* s, const int* offsets, const void* q, const void* k, const void* v,
+                           const float* g, const float* beta, const float* S0, const void* dO, const float* dS_final,
+                           void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dS0, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_gated_bwd");
+    g_msg[0] = 0;
+    efla::GDims d;
+    efla_status st = check_gated(s, false, true, &d);
+    if (st != EFLA_OK) return st;
+    if (s->path == EFLA_PATH_TENSOR) return fail(EFLA_ERR_UNSUPPORTED, "efla_gated_bwd: path must be AUTO or SIMT");
+    if (d.BH() == 0) return EFLA_OK;
+    GatedIo io = gated_io(s, q, k, v, g, beta, nullptr, dO, dq, dk, dv);
+    io.x[5] = io.x[6];   // no o here: dO is the sixth input
+    for (int i = 6; i < 9; ++i) io.x[i] = io.x[i + 1];
+    if ((st = check_strided(io.x, 9, 6)) != EFLA_OK) return st;
+    const size_t sbytes = (size_t)d.BH() * d.dk * d.dv * 4, gbytes = (d.packed ? 1 : (size_t)d.B) * d.H * d.L * 4;
+    const Span sS0{S0, sbytes, "S0"}, sdS{dS_final, sbytes, "dS_final"}, sd0{dS0, sbytes, "dS0"},
+        sdg{dg, gbytes, "dg"}, sdb{dbeta, gbytes, "dbeta"}, sw{workspace, workspace_bytes, "workspace"},
+        soff{offsets, ((size_t)d.B + 1) * 4, "offsets"};
+    const Span req[] = {sdg, sdb};
+    const Span opt[] = {sS0, sdS, sd0, sw};
+    if ((st = check_ptrs(req, gbytes ? 2 : 0, opt, 4)) != EFLA_OK) return st;
+    if (d.packed && !offsets) return fail(EFLA_ERR_INVALID_ARG, "offsets is NULL (packed)");
+    if (d.packed && (uintptr_t)offsets % 4) return fail(EFLA_ERR_ALIGNMENT, "offsets is not 4-byte aligned");
+    d.offsets = d.packed ? offsets : nullptr;
+    {
+        const Span ins[] = {sS0, sdS, d.packed ? soff : Span{nullptr, 0, ""}};
+        const Span outs[] = {sdg, sdb, sd0};
+        if ((st = check_gated_alias(io.x, 9, 6, ins, 3, outs, 3, sw)) != EFLA_OK) return st;
+        for (const Span& a : outs)
+            for (const Span& b : ins)
+                if (overlap(a, b)) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input %s", a.name, b.name);
+    }
+    const size_t need = efla::gated_simt_bwd_ws_bytes(d);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t e = efla::launch_gated_bwd_simt(d, q, k, v, g, beta, S0, dO, dS_final, dq, dk, dv, dg, dbeta, dS0,
+                                                      workspace, stream);
+    return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_gated_bwd");
+}
+
+efla_status efla_gated_step(const efla_gated_shape* s, const void* q, const void* k, const void* v, const float* g,
+                            const float* beta, float* S, const int* slots, int nslots, void* o, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_gated_step");
+    g_msg[0] = 0;
+    efla::GDims d;
+    efla_status st = check_gated(s, true, false, &d);
+    if (st != EFLA_OK) return st;
+    if (s->path == EFLA_PATH_TENSOR)
+        return fail(EFLA_ERR_UNSUPPORTED, "efla_gated_step runs on CUDA cores: path must be AUTO or SIMT");
+    if (nslots < 0 || (!slots && nslots < d.B))
+        return fail(EFLA_ERR_INVALID_ARG, "nslots=%d: the cache holds fewer states than the B=%d sequences", nslots, d.B);
+    if (d.BH() == 0) return EFLA_OK;
+    const GatedIo io = gated_io(s, q, k, v, g, beta, o, nullptr, nullptr, nullptr, nullptr);
+    if ((st = check_strided(io.x, 6, 5)) != EFLA_OK) return st;
+    if (slots && (uintptr_t)slots % 4) return fail(EFLA_ERR_ALIGNMENT, "slots is not 4-byte aligned");
+    const Span sS{S, (size_t)nslots * d.H * d.dk * d.dv * 4, "S"}, ssl{slots, (size_t)d.B * 4, "slots"};
+    if ((st = check_ptrs(&sS, nslots ? 1 : 0, nullptr, 0)) != EFLA_OK) return st;
+    if ((st = check_gated_alias(io.x, 6, 5, &ssl, 1, &sS, 1, Span{nullptr, 0, "workspace"})) != EFLA_OK) return st;
+    if (overlap(sS, ssl)) return fail(EFLA_ERR_INVALID_ARG, "S overlaps input slots");
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t e = efla::launch_gated_step(d, q, k, v, g, beta, S, slots, nslots, o, stream);
+    return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_gated_step");
+}
+
+}  // extern "C"
+
+namespace {
+
+efla_status check_norm(const efla_norm_shape* s, efla::NormDims* d) {
+    if (!s) return fail(EFLA_ERR_INVALID_ARG, "shape is NULL");
+    if (s->rows < 0 || s->D < 0) return fail(EFLA_ERR_INVALID_ARG, "negative size (rows=%lld D=%d)", s->rows, s->D);
+    if (s->D < 1 || s->D > 16384) return fail(EFLA_ERR_UNSUPPORTED, "D=%d: need 1 .. 16384", s->D);
+    if (s->rows > 0x7fffffffLL) return fail(EFLA_ERR_UNSUPPORTED, "rows=%lld exceed 2^31-1", s->rows);
+    if (!dtype_ok(s->dtype) || !dtype_ok(s->weight_dtype))
+        return fail(EFLA_ERR_UNSUPPORTED, "dtype=%d weight_dtype=%d: need EFLA_F32 or EFLA_BF16", (int)s->dtype,
+                    (int)s->weight_dtype);
+    if (!(s->eps >= 0.f)) return fail(EFLA_ERR_INVALID_ARG, "eps=%g: need a non-negative number", (double)s->eps);
+    if (s->rows > 1 && (s->x_stride < s->D || s->y_stride < s->D))
+        return fail(EFLA_ERR_INVALID_ARG, "row strides %lld, %lld are below D=%d", s->x_stride, s->y_stride, s->D);
+    *d = efla::NormDims{s->rows, s->rows > 1 ? s->x_stride : s->D, s->rows > 1 ? s->y_stride : s->D, s->D,
+                        s->dtype == EFLA_BF16, s->weight_dtype == EFLA_BF16, s->eps};
+    return EFLA_OK;
+}
+
+// element alignment of the rows and weights (their vector copies ask for more where they are used)
+efla_status check_elems(const Span* x, const size_t* es, int n) {
+    for (int i = 0; i < n; ++i)
+        if (x[i].n && (uintptr_t)x[i].p % es[i])
+            return fail(EFLA_ERR_ALIGNMENT, "%s is not aligned to its elements", x[i].name);
+    return EFLA_OK;
+}
+
+size_t rows_bytes(const efla::NormDims& d, long long stride) {
+    return d.rows ? ((size_t)(d.rows - 1) * stride + d.D) * (d.bf16 ? 2 : 4) : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+efla_status efla_norm_fwd(const efla_norm_shape* s, const void* x, const void* weight, const void* bias, void* y,
+                          float* stats, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_norm_fwd");
+    g_msg[0] = 0;
+    efla::NormDims d;
+    efla_status st = check_norm(s, &d);
+    if (st != EFLA_OK || d.rows == 0) return st;
+    const size_t e = d.bf16 ? 2 : 4, we = d.w_bf16 ? 2 : 4;
+    const Span in[] = {{x, rows_bytes(d, d.x_stride), "x"}, {weight, d.D * we, "weight"}, {bias, d.D * we, "bias"}};
+    const Span out[] = {{y, rows_bytes(d, d.y_stride), "y"}, {stats, (size_t)d.rows * 8, "stats"}};
+    if (!x || !weight || !y || !stats)
+        return fail(EFLA_ERR_INVALID_ARG, "%s is NULL", !x ? "x" : !weight ? "weight" : !y ? "y" : "stats");
+    const Span el[] = {in[0], in[1], in[2], out[0], out[1]};
+    const size_t es[] = {e, we, we, e, 4};
+    if ((st = check_elems(el, es, 5)) != EFLA_OK) return st;
+    if ((st = check_alias(out, 2, in, 3)) != EFLA_OK) return st;
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_norm_fwd(d, x, weight, bias, y, stats, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_norm_fwd");
+}
+
+size_t efla_norm_bwd_workspace_size(const efla_norm_shape* s) {
+    efla::NormDims d;
+    return check_norm(s, &d) == EFLA_OK ? efla::norm_bwd_ws_bytes(d) : 0;
+}
+
+efla_status efla_norm_bwd(const efla_norm_shape* s, const void* x, const void* weight, const void* dy,
+                          const float* stats, void* dx, void* dweight, void* dbias, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_norm_bwd");
+    g_msg[0] = 0;
+    efla::NormDims d;
+    efla_status st = check_norm(s, &d);
+    if (st != EFLA_OK) return st;
+    const size_t e = d.bf16 ? 2 : 4, we = d.w_bf16 ? 2 : 4;
+    const Span in[] = {{x, rows_bytes(d, d.x_stride), "x"}, {weight, d.D * we, "weight"},
+                       {dy, rows_bytes(d, d.y_stride), "dy"}, {stats, (size_t)d.rows * 8, "stats"}};
+    const Span out[] = {{dx, rows_bytes(d, d.D), "dx"}, {dweight, d.D * we, "dweight"}, {dbias, d.D * we, "dbias"},
+                        {workspace, workspace_bytes, "workspace"}};
+    for (const Span& a : in)
+        if (a.n && !a.p) return fail(EFLA_ERR_INVALID_ARG, "%s is NULL", a.name);
+    if (out[0].n && !dx) return fail(EFLA_ERR_INVALID_ARG, "dx is NULL");
+    if (!dweight) return fail(EFLA_ERR_INVALID_ARG, "dweight is NULL");
+    const Span el[] = {in[0], in[1], in[2], in[3], out[0], out[1], out[2]};
+    const size_t es[] = {e, we, e, 4, e, we, we};
+    if ((st = check_elems(el, es, 7)) != EFLA_OK) return st;
+    if ((st = check_ptrs(nullptr, 0, out + 3, 1)) != EFLA_OK) return st;
+    if ((st = check_alias(out, 4, in, 4)) != EFLA_OK) return st;
+    const size_t need = efla::norm_bwd_ws_bytes(d);
+    if (!workspace || workspace_bytes < need)
+        return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_norm_bwd(d, x, weight, dy, stats, dx, dweight, dbias, workspace, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_norm_bwd");
 }
 
 }  // extern "C"

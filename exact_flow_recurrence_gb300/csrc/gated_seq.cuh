@@ -1,0 +1,60 @@
+// gated_seq.cuh -- where a sequence of a gated call lies, and the parts every gated kernel shares.
+#pragma once
+
+#include "common.cuh"
+#include "gated.h"
+
+namespace efla {
+
+// Where sequence b's tokens are: the first one on the token axis, how many, its first chunk
+// slot, and the index to use with batch strides.  Packed offsets are device data that the
+// host cannot check: they are clamped to [0, L] and to a non-negative length here, so that no
+// value of theirs leads outside the arrays.
+struct SeqAt {
+    int start, len, slot0, batch;
+};
+
+__device__ __forceinline__ int clamp_off(const GDims& d, int b) { return min(max(__ldg(d.offsets + b), 0), d.L); }
+
+__device__ __forceinline__ SeqAt seq_at(const GDims& d, int b, int C) {
+    SeqAt s;
+    if (d.packed) {
+        s.start = clamp_off(d, b);
+        s.len = max(clamp_off(d, b + 1) - s.start, 0);
+        s.slot0 = s.start / C + b;
+        s.batch = 0;
+    } else {
+        s.start = 0;
+        s.len = d.L;
+        s.slot0 = b * ((d.L + C - 1) / C);
+        s.batch = b;
+    }
+    return s;
+}
+
+// The sequence that chunk slot `slot` belongs to (slot0(b) <= slot < slot0(b + 1)).
+__device__ __forceinline__ int seq_of_slot(const GDims& d, int slot, int C) {
+    if (!d.packed) return slot / ((d.L + C - 1) / C);
+    int lo = 0, hi = d.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (clamp_off(d, mid) / C + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ long long at3(const long long (&s)[3], int b, int h, int t) {
+    return b * s[0] + h * s[1] + t * s[2];
+}
+
+// Sums of log decays inside a chunk.  A decay below e^-128 is zero in fp32, so g is taken as at
+// least -128 there: an infinite one (a state reset) then leaves no inf - inf behind.  The sums
+// c_i are kept as two floats (hi + lo), since e^{c_i - c_j} needs the difference's absolute
+// error small where c itself may be thousands.
+__device__ __forceinline__ float log_decay(float g) { return g < -128.f ? -128.f : g; }
+__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
+    return expf((hi_i - hi_j) + (lo_i - lo_j));
+}
+
+}  // namespace efla

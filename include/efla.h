@@ -228,6 +228,88 @@ efla_status efla_fwd_noalloc(const efla_shape* shape,
                              const void* q, const void* k, const void* v, const float* beta,
                              const float* S0, void* o, float* S_final, cudaStream_t stream);
 
+/* ---- The gated delta rule: the framework's update with a decay of the state.
+ * For every sequence and value head h, with f_t = e^{g_t} (g_t the log decay, normally <= 0):
+ *     S <- f_t S,   S <- S + alpha_t k_t (v_t - S^T k_t)^T,   o_t = S^T q_t
+ * alpha_t = beta_t (EFLA_EULER, the gated delta rule) or (1 - e^{-beta_t lambda_t}) / lambda_t,
+ * lambda_t = ||k_t||^2 (EFLA_EXACT).  With g = 0 and Hk = H this is efla_fwd's recurrence.
+ * Value head h reads the query and key of head h / (H / Hk): H must be a multiple of Hk.
+ *
+ * Arrays are reached through strides in elements, {batch, head, token}, their last dimension
+ * contiguous: q, k [B,Hk,L,dk], v, o, dO [B,H,L,dv] (dtype; o, dq, dk, dv out_dtype),
+ * g, beta [B,H,L] fp32.  So [B,H,L,d] and [B,L,H,d] storage, and slices of a fused projection,
+ * are read in place.  S0, S_final, dS_final, dS0 are dense [B,H,dk,dv] fp32; dg, dbeta dense
+ * [B,H,L] fp32.  packed = 1: B sequences of any lengths (0 included) lie one after another on
+ * one axis of L tokens, sequence b at tokens offsets[b] .. offsets[b+1]-1 (offsets: B + 1
+ * device ints from 0 to L, non-decreasing; read on the device, where values outside [0, L] are
+ * clamped); batch strides are then unused and dg, dbeta are [H,L].  Tokens outside every
+ * sequence are not read and their outputs not written.
+ *
+ * Rules as in the conventions above, except that these arrays need only the alignment of their
+ * elements (states, workspace, dg and dbeta: 16 bytes): 16-byte aligned bf16 arrays with
+ * strides that are multiples of 8 elements run on the tensor cores, others on the fp32 cores. */
+typedef struct {
+    int B, H, Hk, L, dk, dv;    /* dk, dv: multiples of 16 in [16, 128]; H, Hk: value, key heads */
+    efla_dtype dtype;           /* q, k, v, dO */
+    efla_dtype out_dtype;       /* o, dq, dk, dv */
+    efla_mode mode;
+    efla_path path;
+    int packed;
+    long long q_stride[3], k_stride[3], v_stride[3], g_stride[3], beta_stride[3], o_stride[3], do_stride[3],
+        dq_stride[3], dk_stride[3], dv_stride[3];   /* those of arrays the call does not have: zeros */
+} efla_gated_shape;
+
+/* Bytes of device workspace (0 on an invalid shape, or when none is needed). */
+size_t efla_gated_fwd_workspace_size(const efla_gated_shape* shape);
+size_t efla_gated_bwd_workspace_size(const efla_gated_shape* shape);
+
+/* Chunked forward pass.  S0 NULL: zero initial states; S_final NULL: not written (it may alias
+ * S0 exactly).  An empty sequence's S_final is its S0. */
+efla_status efla_gated_fwd(const efla_gated_shape* shape, const int* offsets,
+                           const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           const float* S0, void* o, float* S_final,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradients of  sum(o * dO) + sum(S_final * dS_final).  dS_final NULL: zeros; dS0 NULL: not
+ * written.  dq, dk are summed over the value heads of a key head; dq, dk, dv may be slices of
+ * one buffer's token rows.  The chunk states are recomputed; nothing is kept by the forward. */
+efla_status efla_gated_bwd(const efla_gated_shape* shape, const int* offsets,
+                           const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           const float* S0, const void* dO, const float* dS_final,
+                           void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dS0,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One new token (L = 1; token strides unused) on a cache of states S [nslots,H,dk,dv] fp32,
+ * updated in place.  slots NULL: sequence b's states are S[b] (nslots >= B).  Else slots[b]
+ * (device int) is its place in the cache: a sequence whose place is outside [0, nslots) is
+ * skipped (its o is zero); places must differ from each other. */
+efla_status efla_gated_step(const efla_gated_shape* shape,
+                            const void* q, const void* k, const void* v, const float* g, const float* beta,
+                            float* S, const int* slots, int nslots, void* o, cudaStream_t stream);
+
+/* ---- Layer norm over the last dimension.
+ *     y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(var + eps)
+ * x, y, dy [rows, D] dtype with row strides (elements; y_stride: of y, and of dy in the
+ * backward), dx dense; weight, bias, dweight, dbias [D] weight_dtype; stats [rows, 2] fp32 =
+ * (mean, rstd) of each row, written by the forward and read by the backward.  Sums and
+ * statistics are fp32; dweight and dbias are added in a fixed order.  Any D in 1 .. 16384.
+ * bias NULL: none; dbias NULL: not written.  rows = 0: dweight and dbias are zero. */
+typedef struct {
+    long long rows;
+    int D;
+    long long x_stride, y_stride;
+    efla_dtype dtype;
+    efla_dtype weight_dtype;
+    float eps;
+} efla_norm_shape;
+
+efla_status efla_norm_fwd(const efla_norm_shape* shape, const void* x, const void* weight, const void* bias,
+                          void* y, float* stats, cudaStream_t stream);
+size_t efla_norm_bwd_workspace_size(const efla_norm_shape* shape);
+efla_status efla_norm_bwd(const efla_norm_shape* shape, const void* x, const void* weight, const void* dy,
+                          const float* stats, void* dx, void* dweight, void* dbias,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, then reports any asynchronous launch/kernel error
  * (EFLA_ERR_CUDA) or a device-side status word set by a bounded wait (EFLA_ERR_TIMEOUT),
  * and clears that word.  A library built with -DEFLA_DEBUG (libefla_gb300_debug.so) also
