@@ -467,14 +467,15 @@ efla_status efla_get_status(cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(sync)");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status");
-    unsigned int word = 0, word2 = 0, word3 = 0, word4 = 0, word5 = 0;
+    unsigned int word = 0, word2 = 0, word3 = 0, word4 = 0, word5 = 0, word6 = 0;
     e = efla::tc_status_read_clear(&word);
     if (e == cudaSuccess) e = efla::proj_status_read_clear(&word2);
     if (e == cudaSuccess) e = efla::bt_status_read_clear(&word3);
     if (e == cudaSuccess) e = efla::gt_status_read_clear(&word4);
     if (e == cudaSuccess) e = efla::sd_status_read_clear(&word5);
+    if (e == cudaSuccess) e = efla::gated_tc_status_read_clear(&word6);
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(status word)");
-    word |= word2 | word3 | word4 | word5;
+    word |= word2 | word3 | word4 | word5 | word6;
     if (word & efla::kStatusBounds)
         return fail(EFLA_ERR_BOUNDS, "a debug-build bounds check skipped a global write (status 0x%x)", word);
     if (word) return fail(EFLA_ERR_TIMEOUT, "a bounded device-side wait expired (status 0x%x)", word);
@@ -620,6 +621,18 @@ efla_status check_strided(const Strided* x, int n, int first_out) {
     return EFLA_OK;
 }
 
+// The tensor-core kernels take bf16 tokens whose rows (of every token array: x[0..2] and the
+// outputs x[5..]) can be copied 16 bytes at a time.
+efla_status pick_gated_path(const efla_gated_shape* s, const Strided* x, int n, efla::GDims* d) {
+    bool ok = efla::gated_tc_supported(*d);
+    for (int i = 0; i < n; ++i)
+        if (i != 3 && i != 4) ok = ok && x[i].wide();
+    if (s->path == EFLA_PATH_TENSOR && !ok && d->L > 0)
+        return fail(EFLA_ERR_UNSUPPORTED, "EFLA_PATH_TENSOR needs bf16 tokens in rows on 16-byte boundaries");
+    d->tensor = ok && s->path != EFLA_PATH_SIMT;
+    return EFLA_OK;
+}
+
 // Strided inputs and outputs, dense outputs, and the workspace: every output apart from
 // every input, from the other outputs and from the workspace.
 efla_status check_gated_alias(const Strided* x, int n, int first_out, const Span* ins, int nin, const Span* outs,
@@ -657,10 +670,13 @@ efla_status check_gated_alias(const Strided* x, int n, int first_out, const Span
 
 extern "C" {
 
+// (of the larger path: which one runs also depends on the arrays' alignment)
 size_t efla_gated_fwd_workspace_size(const efla_gated_shape* s) {
     efla::GDims d;
     if (check_gated(s, false, false, &d) != EFLA_OK) return 0;
-    return efla::gated_simt_fwd_ws_bytes(d);
+    const size_t simt = efla::gated_simt_fwd_ws_bytes(d);
+    const size_t tc = s->path != EFLA_PATH_SIMT && efla::gated_tc_supported(d) ? efla::gated_tc_fwd_ws_bytes(d) : 0;
+    return tc > simt ? tc : simt;
 }
 
 size_t efla_gated_bwd_workspace_size(const efla_gated_shape* s) {
@@ -677,10 +693,10 @@ efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const 
     efla::GDims d;
     efla_status st = check_gated(s, false, false, &d);
     if (st != EFLA_OK) return st;
-    if (s->path == EFLA_PATH_TENSOR) return fail(EFLA_ERR_UNSUPPORTED, "efla_gated_fwd: path must be AUTO or SIMT");
     if (d.BH() == 0) return EFLA_OK;
     const GatedIo io = gated_io(s, q, k, v, g, beta, o, nullptr, nullptr, nullptr, nullptr);
     if ((st = check_strided(io.x, 6, 5)) != EFLA_OK) return st;
+    if ((st = pick_gated_path(s, io.x, 6, &d)) != EFLA_OK) return st;
     const size_t sbytes = (size_t)d.BH() * d.dk * d.dv * 4;
     const Span sS0{S0, sbytes, "S0"}, sSf{S_final, sbytes, "S_final"}, sw{workspace, workspace_bytes, "workspace"},
         soff{offsets, ((size_t)d.B + 1) * 4, "offsets"};
@@ -696,11 +712,13 @@ efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const 
         const Span outs[] = {S_final == (float*)S0 ? Span{nullptr, 0, ""} : sSf};
         if ((st = check_gated_alias(io.x, 6, 5, ins, 2, outs, 1, sw)) != EFLA_OK) return st;
     }
-    const size_t need = efla::gated_simt_fwd_ws_bytes(d);
+    const size_t need = d.tensor ? efla::gated_tc_fwd_ws_bytes(d) : efla::gated_simt_fwd_ws_bytes(d);
     if (need && (!workspace || workspace_bytes < need))
         return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
     efla::prof_mark(nullptr, stream);
-    const cudaError_t e = efla::launch_gated_fwd_simt(d, q, k, v, g, beta, S0, o, S_final, workspace, stream);
+    const cudaError_t e =
+        d.tensor ? efla::launch_gated_fwd_tc(d, q, k, v, g, beta, S0, o, S_final, workspace, stream)
+                 : efla::launch_gated_fwd_simt(d, q, k, v, g, beta, S0, o, S_final, workspace, stream);
     return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_gated_fwd");
 }
 

@@ -32,6 +32,16 @@ cudaError_t launch_gated_bwd_simt(const GDims& d, const void* q, const void* k, 
                                   void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dS0, void* ws,
                                   cudaStream_t st);
 
+// -------------------------------------------------------------- tensor-core kernels (gated_tc.cu)
+// bf16 tokens whose rows start on 16-byte boundaries (the caller checks the strides).
+bool gated_tc_supported(const GDims& d);
+size_t gated_tc_fwd_ws_bytes(const GDims& d);
+cudaError_t launch_gated_fwd_tc(const GDims& d, const void* q, const void* k, const void* v, const float* g,
+                                const float* beta, const float* S0, void* o, float* S_final, void* ws,
+                                cudaStream_t st);
+// Reads and clears the kernels' device status word (synchronous).
+cudaError_t gated_tc_status_read_clear(unsigned int* status);
+
 // ------------------------------------------------------------------- decode (gated_step.cu)
 // slots: null (sequence b's states at S + b H dk dv), or B state indices in [0, nslots); a
 // sequence whose index is outside is skipped (its o is zero).

@@ -1,0 +1,606 @@
+// gated_tc.cu -- the gated delta rule's forward on the tcgen05 tensor cores (bf16 tokens).
+//
+// The chunk form of gated_simt.cu with 64-token chunks, in two kernels:
+//   k_gt_prep, every chunk at once: T = (I + strict_lower(alpha_i D_ij k_i.k_j))^{-1} and
+//     P T (P = lower(D_ij q_i.k_j)), so that U and P U come from one product, as bf16 parts;
+//   k_gt_scan, the chunks of a sequence one after another, one CTA for N columns of a head's
+//     state, which it keeps in fp32 registers.
+#include "common.cuh"
+#include "gated_tc.cuh"
+#include "launch.h"
+
+namespace efla {
+
+namespace {
+
+__device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kStatusBounds (debug builds): a write was skipped
+
+// ------------------------------------------------------------------ preparation
+// One chunk of a value head per CTA of 128 threads:
+//   1. the chunk's K and Q rows by TMA into [K; Q] tiles (128 rows);
+//   2. one product [K; Q] K^T: lanes 0..63 G = K K^T (its diagonal: lambda), 64..127 Q K^T;
+//   3. A and P (fp32, shared memory), from the decays;
+//   4. T by blocked substitution (split tf32, about fp32 accuracy), P T likewise;
+//   5. the [T; P T] image: 128 rows of 64, NP parts in the operand layout, out by bulk copy.
+struct PrepArgs {
+    const float* g;
+    const float* beta;
+    unsigned char* img;   // [H][slots][NP][128 rows x 128 bytes]
+    GVec* vec;            // [H][slots]
+    int slots;
+};
+
+constexpr uint32_t kPrA = 0;            // [64][kLdA] fp32, once the tiles are read
+constexpr uint32_t kPrY = 17408;        // [32][40] fp32
+constexpr uint32_t kPrP = 32768;        // [64][kLd] fp32
+constexpr uint32_t kPrT = 50176;        // [64][kLd] fp32
+constexpr uint32_t kPrVec = 67584;      // GVec
+constexpr uint32_t kPrBar = kPrVec + sizeof(GVec);
+constexpr uint32_t kPrEnd = (kPrBar + 64 + 1023) / 1024 * 1024;
+template <int NP>
+struct PrepSmem {
+    static constexpr uint32_t img = NP == 2 ? 0u : kPrEnd;   // two parts fit over A and Y
+    static constexpr size_t bytes = 1024 + kPrEnd + (NP == 2 ? 0 : NP * 16384);
+};
+
+template <int NP>
+__global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
+                                                 const __grid_constant__ CUtensorMap tm_k) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    const int slot = blockIdx.x, h = blockIdx.y, hk = h / (d.H / d.Hk), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = seq_of_slot(d, slot, kGC);
+    const SeqAt s = seq_at(d, b, kGC);
+    const int t0 = (slot - s.slot0) * kGC, n = min(kGC, s.len - t0), t = s.start + t0;
+    if (n <= 0) return;
+    uint64_t* bar = (uint64_t*)(sm + kPrBar);
+    uint32_t* tslot = (uint32_t*)(bar + 2);
+    GVec* vec = (GVec*)(sm + kPrVec);
+    if (tid == 0) {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&bar[0], 4u * 8192u);
+        for (int blk = 0; blk < 2; ++blk) {
+            tma_load_4d(sm + blk * 16384, &tm_k, 64 * blk, t, hk, s.batch, &bar[0]);
+            tma_load_4d(sm + blk * 16384 + 8192, &tm_q, 64 * blk, t, hk, s.batch, &bar[0]);
+        }
+    }
+    if (warp == 0) {
+        tmem_alloc(tslot, 64);
+        tmem_relinquish();
+    }
+    if (warp == 1) {   // sums of the log decays (two tokens a lane), in fp64 until they are two floats
+        const int i0 = 2 * lane;
+        const double x0 = i0 < n ? (double)log_decay(a.g[at3(d.gs, s.batch, h, t + i0)]) : 0.0;
+        double c1 = x0 + (i0 + 1 < n ? (double)log_decay(a.g[at3(d.gs, s.batch, h, t + i0 + 1)]) : 0.0);
+        const double own = c1 - x0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, c1, o);
+            if (lane >= o) c1 += y;
+        }
+        const double last = __shfl_sync(0xffffffffu, c1, 31);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const double c = e ? c1 : c1 - own;
+            const float hi = (float)c;
+            vec->chi[i0 + e] = hi;
+            vec->clo[i0 + e] = (float)(c - (double)hi);
+            vec->up[i0 + e] = expf(hi);
+            vec->rest[i0 + e] = expf((float)(last - c));
+        }
+    }
+    const float beta = tid < n ? a.beta[at3(d.bs, s.batch, h, t + tid)] : 0.f;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = *tslot;
+    if (tid == 0) {
+        if (mbar_wait(&bar[0], 0, kWaitLimit)) {
+            tc_fence_after();
+            for (int ks = 0; ks < d.dk / 16; ++ks) {
+                const uint64_t x = sdesc_sw128(smem_u32(sm + (ks / 4) * 16384 + (ks % 4) * 32));
+                mma_f16_ss(tb, x, x, idesc_f16(128, 64, false, false, true), ks > 0);
+            }
+            mma_commit(&bar[1]);
+        } else {
+            atomicOr(&g_gt2_status, 1u);
+            mbar_wait(&bar[0], 0, kWaitLimit);   // let the copies land
+        }
+    }
+    const bool ok = __syncthreads_and(mbar_wait(&bar[1], 0, kWaitLimit));
+    tc_fence_after();
+    float* A = (float*)(sm + kPrA);
+    float* P = (float*)(sm + kPrP);
+    float* T = (float*)(sm + kPrT);
+    if (ok) {
+        const int i = tid & 63;   // this lane's token; lanes 0..63 hold A's rows, 64..127 P's
+        float v[64];
+#pragma unroll
+        for (int c = 0; c < 64; c += 16)
+            tmem_ld16(taddr(tb, warp * 32, c), *reinterpret_cast<float(*)[16]>(v + c));
+        tmem_ld_wait();
+        const float chi = vec->chi[i], clo = vec->clo[i];
+        if (tid < 64) {
+            float lam = 0.f;
+#pragma unroll
+            for (int j = 0; j < 64; ++j) lam = j == i ? v[j] : lam;
+            const float al = i < n ? alpha_of(beta, lam, d.euler) : 0.f;
+            vec->al[i] = al;
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+                v[j] = j < i && i < n ? al * decay(chi, clo, vec->chi[j], vec->clo[j]) * v[j] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4)
+                *reinterpret_cast<float4*>(A + i * kLdA + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] = j <= i && i < n ? decay(chi, clo, vec->chi[j], vec->clo[j]) * v[j] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 64; j += 4)
+                *reinterpret_cast<float4*>(P + i * kLd + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        tc_fence_before();
+        group_sync(1);
+        unit_lower_inverse64(A, T, (float*)(sm + kPrY), 1, tid);
+        unsigned char* img = sm + PrepSmem<NP>::img;
+        {   // T's rows, 32 columns a thread (zero above its 16x16 diagonal blocks)
+            const int r = tid >> 1, h0 = 32 * (tid & 1);
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = h0 + j < 16 * (r / 16 + 1) ? T[r * kLd + h0 + j + e] : 0.f;
+                uint4 w[NP];
+                split8<NP>(x, w);
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    *reinterpret_cast<uint4*>(img + p * 16384 + sw128(r, h0 + j)) = w[p];
+            }
+        }
+        // P T: warp w owns the 8-column tiles w and 7 - w, for the four 16-row blocks
+        const int gi = lane >> 2, ti = lane & 3;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            const int n0 = 8 * (half ? 7 - warp : warp);
+#pragma unroll 1
+            for (int m0 = 0; m0 < 64; m0 += 16) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int k0 = n0; k0 < m0 + 16; k0 += 8) {   // T[k][n] = 0 for k < n, P[m][k] = 0 for k > m
+                    uint32_t ah[4], alo[4], bh[2], blo[2];
+                    split_tf32(P[(m0 + gi) * kLd + k0 + ti], ah[0], alo[0]);
+                    split_tf32(P[(m0 + 8 + gi) * kLd + k0 + ti], ah[1], alo[1]);
+                    split_tf32(P[(m0 + gi) * kLd + k0 + ti + 4], ah[2], alo[2]);
+                    split_tf32(P[(m0 + 8 + gi) * kLd + k0 + ti + 4], ah[3], alo[3]);
+                    split_tf32(T[(k0 + ti) * kLd + n0 + gi], bh[0], blo[0]);
+                    split_tf32(T[(k0 + ti + 4) * kLd + n0 + gi], bh[1], blo[1]);
+                    mma_16x8x8_3xtf32(acc, ah, alo, bh, blo);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x0 = acc[2 * e], x1 = acc[2 * e + 1];
+                    const uint32_t at = sw128(64 + m0 + 8 * e + gi, n0 + 2 * ti);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
+                        const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
+                        *reinterpret_cast<uint32_t*>(img + p * 16384 + at) = u;
+                        x0 -= __uint_as_float(u << 16);
+                        x1 -= __uint_as_float(u & 0xffff0000u);
+                    }
+                }
+            }
+        }
+        fence_async_smem();
+    } else {
+        atomicOr(&g_gt2_status, 1u);
+        mbar_wait(&bar[1], 0, kWaitLimit);   // (a product still in flight ends before its tensor memory is freed)
+    }
+    __syncthreads();
+    if (tid == 0 && ok) {
+        const size_t rec = (size_t)h * a.slots + slot, all = (size_t)d.H * a.slots;
+        if (dbg_in(a.img + rec * NP * 16384, NP * 16384, a.img, all * NP * 16384, &g_gt2_status))
+            bulk_s2g(a.img + rec * NP * 16384, sm + PrepSmem<NP>::img, NP * 16384);
+        if (dbg_in(a.vec + rec, sizeof(GVec), a.vec, all * sizeof(GVec), &g_gt2_status))
+            bulk_s2g(a.vec + rec, vec, sizeof(GVec));
+        bulk_commit();
+        bulk_wait_read();
+    }
+    if (warp == 0) tmem_dealloc(tb, 64);
+}
+
+// ------------------------------------------------------------------ forward scan
+// Per chunk, with S [dk][N] (fp32 registers: 8 warps, thread = row x N/2 columns):
+//   S as parts -> shared memory;  D1 = [K; Q] S           (lanes 0..63 K S, 64..127 Q S)
+//   X = alpha (V - e^c K S)  as parts;  D2 = [T; P T] X    (U, P U)
+//   o = e^c Q S + P U  (the warps of lanes 64..127)
+//   U e^{c_last - c} as parts;  D3 = K^T (..);  S = e^{c_last} S + D3
+// A ninth warp issues the copies (one chunk ahead) and the products.
+constexpr int kScThreads = 288;
+
+template <int NP, int N>
+struct ScanSmem {
+    static constexpr int TPS = NP == 2 ? 2 : 1;                      // stages of the [T; P T] image
+    static constexpr uint32_t KQ = 0;                                // 2 stages x 2 blocks of 64 dk x [K rows | Q rows]
+    static constexpr uint32_t TP = 65536;
+    static constexpr uint32_t V = TP + TPS * NP * 16384;             // 2 stages
+    static constexpr uint32_t S = V + 2 * 8192;                      // NP x [128 rows][64]
+    static constexpr uint32_t X = S + NP * 16384;                    // NP x [64 rows][64]
+    static constexpr uint32_t VEC = X + NP * 8192;                   // 2 stages
+    static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
+    static constexpr size_t bytes = 1024 + BAR + 128;
+};
+static_assert(ScanSmem<2, 64>::bytes <= 232448 && ScanSmem<3, 64>::bytes <= 232448, "shared memory per CTA");
+
+struct ScanArgs {
+    const unsigned char* img;
+    const GVec* vec;
+    const float* S0;
+    void* o;
+    float* S_final;
+    int slots;
+};
+
+template <typename Tout>
+__device__ __forceinline__ void st16(Tout* p, const float* x);   // 16 values to 16-byte aligned memory
+template <>
+__device__ __forceinline__ void st16<float>(float* p, const float* x) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+}
+template <>
+__device__ __forceinline__ void st16<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+        uint4 w[1];
+        split8<1>(x + i, w);
+        *reinterpret_cast<uint4*>(p + i) = w[0];
+    }
+}
+
+template <int NP, int N, typename Tout>
+__global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, const __grid_constant__ CUtensorMap tm_q,
+                                                           const __grid_constant__ CUtensorMap tm_k,
+                                                           const __grid_constant__ CUtensorMap tm_v) {
+    using M = ScanSmem<NP, N>;
+    constexpr int NC = N / 2;   // columns a thread
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = (uint64_t*)(sm + M::BAR);   // [2] K, Q, V, vectors
+    uint64_t* full_tp = full + 2;                // [2]
+    uint64_t* s_ready = full + 4;
+    uint64_t* x_ready = full + 5;
+    uint64_t* u_ready = full + 6;
+    uint64_t* d1 = full + 7;
+    uint64_t* d2 = full + 8;
+    uint64_t* d3 = full + 9;
+    uint32_t* tslot = (uint32_t*)(full + 10);
+    const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * N;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const SeqAt s = seq_at(d, b, kGC);
+    const int nch = (s.len + kGC - 1) / kGC;
+    const size_t rec0 = (size_t)h * a.slots + s.slot0;
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(full + i, 1);
+        mbar_init(s_ready, 256);
+        mbar_init(x_ready, 128);
+        mbar_init(u_ready, 128);
+        mbar_init(d1, 1);
+        mbar_init(d2, 1);
+        mbar_init(d3, 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(tslot, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = *tslot, t1 = tb, t2 = tb + 64, t3 = tb + 128;
+
+    if (warp == 8) {
+        if (lane == 0 && nch > 0) {
+            // ---------------- copies and products
+            int issued = 0, issued_tp = 0;   // chunks whose copies are under way
+            const auto load = [&](int c) {
+                unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
+                uint64_t* f = &full[c & 1];
+                const int t = s.start + c * kGC;
+                mbar_arrive_expect_tx(f, 5u * 8192u + (uint32_t)sizeof(GVec));
+                for (int blk = 0; blk < 2; ++blk) {
+                    tma_load_4d(kq + blk * 16384, &tm_k, 64 * blk, t, hk, s.batch, f);
+                    tma_load_4d(kq + blk * 16384 + 8192, &tm_q, 64 * blk, t, hk, s.batch, f);
+                }
+                tma_load_4d(sm + M::V + (c & 1) * 8192, &tm_v, c0, t, h, s.batch, f);
+                bulk_g2s(sm + M::VEC + (c & 1) * sizeof(GVec), a.vec + rec0 + c, sizeof(GVec), f);
+                issued = c + 1;
+            };
+            const auto load_tp = [&](int c) {
+                uint64_t* f = &full_tp[c % M::TPS];
+                mbar_arrive_expect_tx(f, NP * 16384u);
+                bulk_g2s(sm + M::TP + (c % M::TPS) * NP * 16384, a.img + (rec0 + c) * NP * 16384, NP * 16384u, f);
+                issued_tp = c + 1;
+            };
+            const uint32_t id_kq = idesc_f16(128, N, false, true, true);   // A K-major, B MN-major
+            const uint32_t id_kt = idesc_f16(128, N, true, true, true);    // both MN-major
+            load(0);
+            load_tp(0);
+            bool ok = true;
+            for (int c = 0; c < nch && ok; ++c) {
+                const uint32_t ph = c & 1;
+                unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
+                ok = mbar_wait(s_ready, ph, kWaitLimit);
+                if (!ok) break;
+                if (c + 1 < nch) {   // (the stage's last readers were chunk c - 1's)
+                    load(c + 1);
+                    if (M::TPS == 2) load_tp(c + 1);
+                }
+                ok = mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
+                if (!ok) break;
+                tc_fence_after();
+                for (int p = 0; p < NP; ++p)
+                    for (int ks = 0; ks < d.dk / 16; ++ks)
+                        mma_f16_ss(t1, sdesc_sw128(smem_u32(kq + (ks / 4) * 16384 + (ks % 4) * 32)),
+                                   sdesc_sw128(smem_u32(sm + M::S + p * 16384 + ks * 2048)), id_kq, p + ks > 0);
+                mma_commit(d1);
+                ok = mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit) && mbar_wait(x_ready, ph, kWaitLimit);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    unsigned char* tp = sm + M::TP + (c % M::TPS) * NP * 16384;
+                    int any = 0;
+                    for (int p = 0; p < NP; ++p)
+                        for (int x = 0; x + p < NP; ++x)
+                            for (int ks = 0; ks < 4; ++ks, any = 1)
+                                mma_f16_ss(t2, sdesc_sw128(smem_u32(tp + p * 16384 + ks * 32)),
+                                           sdesc_sw128(smem_u32(sm + M::X + x * 8192 + ks * 2048)), id_kq, any);
+                }
+                mma_commit(d2);
+                ok = mbar_wait(u_ready, ph, kWaitLimit);
+                if (!ok) break;
+                tc_fence_after();
+                if (M::TPS == 1 && c + 1 < nch) load_tp(c + 1);   // (D2 is done: u_ready came from it)
+                for (int p = 0; p < NP; ++p)
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16_ss(t3, sdesc_sw128(smem_u32(kq + ks * 2048), 16384),
+                                   sdesc_sw128(smem_u32(sm + M::X + p * 8192 + ks * 2048)), id_kt, p + ks > 0);
+                mma_commit(d3);
+            }
+            if (!ok) {   // a wait gave up: the copies under way land before the CTA ends
+                atomicOr(&g_gt2_status, 1u);
+                for (int c = issued > 1 ? issued - 2 : 0; c < issued; ++c) mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
+                for (int c = issued_tp > M::TPS ? issued_tp - M::TPS : 0; c < issued_tp; ++c)
+                    mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit);
+            }
+        }
+    } else {
+        // ---------------- the state and the epilogues
+        const int row = 32 * (warp & 3) + lane, half = warp >> 2, cc = half * NC;   // columns cc .. cc + NC - 1 of the slice
+        const int i = row & 63;                                                      // token of lanes 0..63 and of 64..127
+        const bool top = row < 64;
+        const int nv = min(max(d.dv - c0 - cc, 0), NC);                              // columns of these that exist
+        const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + c0 + cc;
+        const uint32_t lq = 32 * (warp & 3);
+        float S[NC];
+#pragma unroll
+        for (int e = 0; e < NC; e += 4) {
+            const float4 x = a.S0 && row < d.dk && e < nv ? *reinterpret_cast<const float4*>(a.S0 + sb + e)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+        }
+        bool ok = true;
+        for (int c = 0; c < nch && ok; ++c) {
+            const uint32_t ph = c & 1;
+            const int n = min(kGC, s.len - c * kGC);
+            const GVec* vec = (const GVec*)(sm + M::VEC + (c & 1) * sizeof(GVec));
+#pragma unroll
+            for (int e = 0; e < NC; e += 8) {
+                uint4 w[NP];
+                split8<NP>(S + e, w);
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    *reinterpret_cast<uint4*>(sm + M::S + p * 16384 + sw128(row, cc + e)) = w[p];
+            }
+            if (d.packed && n < kGC) {   // rows past the sequence are another's: zero its keys (0 x NaN is not 0)
+                ok = mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
+                unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
+                for (int e = tid; e < (kGC - n) * 16; e += 256)
+                    *reinterpret_cast<uint4*>(kq + (e & 1) * 16384 + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(s_ready);
+            ok = ok && mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
+            if (!ok) break;
+            const float up = vec->up[i], last = vec->up[63];
+            float y[NC];
+            if (top) {
+                const float al = vec->al[i], rest = vec->rest[i];
+                const unsigned char* vt = sm + M::V + (c & 1) * 8192;
+                if (!(ok = mbar_wait(d1, ph, kWaitLimit))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < NC; e += 16)
+                    tmem_ld16(taddr(t1, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < NC; e += 8) {
+                    const uint4 raw8 = *reinterpret_cast<const uint4*>(vt + sw128(i, cc + e));
+                    const uint32_t* vw = reinterpret_cast<const uint32_t*>(&raw8);
+                    float x[8];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        x[2 * m] = fmaf(-up, y[e + 2 * m], __uint_as_float(vw[m] << 16));
+                        x[2 * m + 1] = fmaf(-up, y[e + 2 * m + 1], __uint_as_float(vw[m] & 0xffff0000u));
+                    }
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) x[m] = i < n ? al * x[m] : 0.f;
+                    uint4 w[NP];
+                    split8<NP>(x, w);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        *reinterpret_cast<uint4*>(sm + M::X + p * 8192 + sw128(i, cc + e)) = w[p];
+                }
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(x_ready);
+                if (!(ok = mbar_wait(d2, ph, kWaitLimit))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < NC; e += 16)
+                    tmem_ld16(taddr(t2, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < NC; e += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) x[m] = rest * y[e + m];
+                    uint4 w[NP];
+                    split8<NP>(x, w);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        *reinterpret_cast<uint4*>(sm + M::X + p * 8192 + sw128(i, cc + e)) = w[p];
+                }
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(u_ready);
+            } else {
+                if (!(ok = mbar_wait(d1, ph, kWaitLimit))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < NC; e += 16)
+                    tmem_ld16(taddr(t1, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
+                tmem_ld_wait();
+                if (!(ok = mbar_wait(d2, ph, kWaitLimit))) break;
+                tc_fence_after();
+                float z[NC];
+#pragma unroll
+                for (int e = 0; e < NC; e += 16)
+                    tmem_ld16(taddr(t2, lq, cc + e), *reinterpret_cast<float(*)[16]>(z + e));
+                tmem_ld_wait();
+                if (i < n) {
+                    Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + c0 + cc;
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) y[e] = fmaf(up, y[e], z[e]);
+#pragma unroll
+                    for (int e = 0; e < NC; e += 16)
+                        if (e < nv) st16(op + e, y + e);
+                }
+            }
+            if (!(ok = mbar_wait(d3, ph, kWaitLimit))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < NC; e += 16)
+                tmem_ld16(taddr(t3, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < NC; ++e) S[e] = fmaf(last, S[e], y[e]);
+        }
+        if (!ok) atomicOr(&g_gt2_status, 1u);
+        if (a.S_final && row < d.dk) {
+#pragma unroll
+            for (int e = 0; e < NC; e += 4)
+                if (e < nv) *reinterpret_cast<float4*>(a.S_final + sb + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tb, 256);
+}
+
+struct TcWs {
+    unsigned char* img;
+    GVec* vec;
+};
+
+size_t carve(const GDims& d, int np, void* base, TcWs* w) {
+    const size_t n = (size_t)d.H * d.slots(kGC);
+    char* p = (char*)base;
+    w->img = (unsigned char*)p;
+    p += align256(n * np * 16384);
+    w->vec = (GVec*)p;
+    p += align256(n * sizeof(GVec));
+    return (size_t)(p - (char*)base);
+}
+
+template <typename K>
+cudaError_t smem_attr(K k, size_t bytes) {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+cudaError_t make_maps(const GDims& d, const void* q, const void* k, const void* v, Maps* m) {
+    const int nb = d.packed ? 1 : d.B;
+    cudaError_t e = strided_rows_map(&m->q, q, d.dk, d.L, d.Hk, nb, d.qs);
+    if (e == cudaSuccess) e = strided_rows_map(&m->k, k, d.dk, d.L, d.Hk, nb, d.ks);
+    if (e == cudaSuccess) e = strided_rows_map(&m->v, v, d.dv, d.L, d.H, nb, d.vs);
+    return e;
+}
+
+template <int NP, int N, typename Tout>
+cudaError_t scan(const GDims& d, const ScanArgs& a, const Maps& m, cudaStream_t st) {
+    constexpr size_t bytes = ScanSmem<NP, N>::bytes;
+    cudaError_t e = smem_attr(k_gt_scan<NP, N, Tout>, bytes);
+    if (e != cudaSuccess) return e;
+    k_gt_scan<NP, N, Tout><<<dim3((unsigned)d.BH(), (d.dv + N - 1) / N), kScThreads, bytes, st>>>(d, a, m.q, m.k, m.v);
+    prof_mark("gated_scan_tc", st);
+    return cudaGetLastError();
+}
+
+template <int NP, typename Tout>
+cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, const float* g, const float* beta,
+                const float* S0, void* o, float* S_final, void* ws, cudaStream_t st) {
+    TcWs w;
+    carve(d, NP, ws, &w);
+    Maps m{};
+    const int slots = d.slots(kGC);
+    cudaError_t e = make_maps(d, q, k, v, &m);
+    if (e == cudaSuccess) e = smem_attr(k_gt_prep<NP>, PrepSmem<NP>::bytes);
+    if (e != cudaSuccess) return e;
+    const PrepArgs pa{g, beta, w.img, w.vec, slots};
+    k_gt_prep<NP><<<dim3(slots, d.H), 128, PrepSmem<NP>::bytes, st>>>(d, pa, m.q, m.k);
+    prof_mark("gated_prep_tc", st);
+    int dev = 0, nsm = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const ScanArgs a{w.img, w.vec, S0, o, S_final, slots};
+    // narrower slices while they still find an SM each: a chunk's products and epilogues shorten
+    // with the columns, but every slice loads the keys, queries and images again
+    if (2 * d.BH() * ((d.dv + 63) / 64) <= nsm) return scan<NP, 32, Tout>(d, a, m, st);
+    return scan<NP, 64, Tout>(d, a, m, st);
+}
+
+}  // namespace
+
+bool gated_tc_supported(const GDims& d) { return d.in_bf16 && d.L > 0; }
+size_t gated_tc_fwd_ws_bytes(const GDims& d) {
+    TcWs w;
+    return carve(d, 3, nullptr, &w);
+}
+
+// The outputs' type decides the operands' parts: three where an fp32 result leaves (the state, or
+// o in fp32), two where only bf16 does.
+cudaError_t launch_gated_fwd_tc(const GDims& d, const void* q, const void* k, const void* v, const float* g,
+                                const float* beta, const float* S0, void* o, float* S_final, void* ws,
+                                cudaStream_t st) {
+    if (!d.out_bf16) return fwd<3, float>(d, q, k, v, g, beta, S0, o, S_final, ws, st);
+    return S_final ? fwd<3, __nv_bfloat16>(d, q, k, v, g, beta, S0, o, S_final, ws, st)
+                   : fwd<2, __nv_bfloat16>(d, q, k, v, g, beta, S0, o, S_final, ws, st);
+}
+
+cudaError_t gated_tc_status_read_clear(unsigned int* status) {
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_gt2_status, sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    return *status ? cudaMemcpyToSymbol(g_gt2_status, &zero, sizeof(unsigned int)) : cudaSuccess;
+}
+
+}  // namespace efla

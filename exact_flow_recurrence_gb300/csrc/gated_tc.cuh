@@ -1,0 +1,76 @@
+// gated_tc.cuh -- pieces shared by the gated delta rule's tensor-core kernels: operands as sums
+// of bf16 parts, the per-chunk record of the preparation, tensor maps of strided arrays.
+//
+// Precision.  The inputs q, k, v, dO are bf16 and enter the tensor cores as they are; every
+// operand that is computed (the state, the chunk's corrected values, T and P T) enters as the
+// sum of NP bf16 parts, x = x_0 + x_1 (+ x_2), each the rounding of what the earlier ones left,
+// and a product of two such operands takes the part pairs a + b < NP.  All products accumulate
+// in fp32.  Two parts carry 17 bits (2^-18 of the value at most): against the fp64 recurrence
+// the outputs and the carried state come out within about 4e-6 of their norm, where one bf16 or
+// fp16 operand leaves 3e-3 or 3e-4.  Parts keep fp32's exponent range, so there is no range to
+// check and no second path.
+#pragma once
+
+#include "gated_seq.cuh"
+#include "tc_common.cuh"
+
+namespace efla {
+
+constexpr int kGC = 64;   // tokens a chunk of the tensor-core kernels
+
+// What the preparation leaves of a chunk and value head besides the T, P T image: five vectors.
+struct GVec {
+    float up[64];     // e^{c_i}
+    float rest[64];   // e^{c_last - c_i}
+    float al[64];     // alpha_i (0 past the sequence's end)
+    float chi[64];    // c_i = chi + clo
+    float clo[64];
+};
+
+// 8 values -> NP 16-byte chunks of bf16 parts
+template <int NP>
+__device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        uint32_t* o = reinterpret_cast<uint32_t*>(&w[p]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(r[2 * i], r[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            if (p + 1 < NP) {
+                r[2 * i] -= __uint_as_float(o[i] << 16);
+                r[2 * i + 1] -= __uint_as_float(o[i] & 0xffff0000u);
+            }
+        }
+    }
+}
+
+// Tensor map of a strided bf16 [batch][head][token][d] array: boxes of 64 tokens x 64 columns
+// with the 128-byte swizzle; elements outside read as zero.
+inline cudaError_t strided_rows_map(CUtensorMap* m, const void* base, int d, int L, int heads, int batch,
+                                    const long long (&s)[3]) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    if (!encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+        encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)heads, (cuuint64_t)batch};
+    // a dimension of one element has no stride of its own
+    const auto bytes = [&](int n, long long st) { return (cuuint64_t)(n > 1 ? st * 2 : 256); };
+    const cuuint64_t strides[3] = {bytes(L, s[2]), bytes(heads, s[1]), bytes(batch, s[0])};
+    const cuuint32_t box[4] = {64, 64, 1, 1};
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace efla

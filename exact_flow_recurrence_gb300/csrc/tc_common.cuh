@@ -149,6 +149,111 @@ __device__ __forceinline__ bool group_sync_and(int id, bool pred, int count = 12
     return r != 0;
 }
 
+// T = (I + A)^{-1} of a strictly lower triangular 64 x 64 A (fp32, row stride kLdA) by a
+// group of 128 threads (named barrier `bid`): the four 16x16 diagonal blocks by substitution,
+// then T21 = -T22 A21 T11 at the 32x32 and at the 64x64 level.  T (row stride kLd) is written
+// in and below its 16x16 diagonal blocks only; Y is [32][40] fp32 scratch.
+__device__ __forceinline__ void unit_lower_inverse64(const float* A, float* T, float* Y, int bid, int tid) {
+    const int warp = tid >> 5, lane = tid & 31;
+    if (tid < 64) {   // 4a. diagonal block b = tid >> 4, column cc = tid & 15: forward substitution
+        const int o = 16 * (tid >> 4), cc = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = (i == cc) ? 1.f : 0.f;
+#pragma unroll
+        for (int jj = 0; jj < 15; ++jj)
+#pragma unroll
+            for (int i = jj + 1; i < 16; ++i) x[i] = fmaf(-A[(o + i) * kLdA + o + jj], x[jj], x[i]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) T[(o + i) * kLd + o + cc] = x[i];
+    }
+    group_sync(bid);
+    {   // 4b. 32x32 level on the tensor pipe: block be = warp >> 1 (rows/cols 32 be ..);
+        // warp (w & 1) owns columns 8 (w & 1) .. +7 of Y = A21 T11 and then of T21 = -T22 Y
+        // (split-tf32 as in 4c; T11[k][n] = 0 for k < n bounds the first k range)
+        const int g = lane >> 2, t = lane & 3, be = warp >> 1, o = 32 * be, n0 = 8 * (warp & 1);
+        float* Yb = Y + be * 16 * 24;   // row stride 24 (= 24 mod 32): conflict-free fragment loads
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k0 = n0; k0 < 16; k0 += 8) {
+            uint32_t ah[4], alo[4], bh[2], blo[2];
+            split_tf32(A[(o + 16 + g) * kLdA + o + k0 + t], ah[0], alo[0]);
+            split_tf32(A[(o + 24 + g) * kLdA + o + k0 + t], ah[1], alo[1]);
+            split_tf32(A[(o + 16 + g) * kLdA + o + k0 + t + 4], ah[2], alo[2]);
+            split_tf32(A[(o + 24 + g) * kLdA + o + k0 + t + 4], ah[3], alo[3]);
+            split_tf32(T[(o + k0 + t) * kLd + o + n0 + g], bh[0], blo[0]);
+            split_tf32(T[(o + k0 + t + 4) * kLd + o + n0 + g], bh[1], blo[1]);
+            mma_16x8x8_3xtf32(acc, ah, alo, bh, blo);
+        }
+        *reinterpret_cast<float2*>(Yb + g * 24 + n0 + 2 * t) = make_float2(acc[0], acc[1]);
+        *reinterpret_cast<float2*>(Yb + (g + 8) * 24 + n0 + 2 * t) = make_float2(acc[2], acc[3]);
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        group_sync(bid);
+        for (int k0 = 0; k0 < 16; k0 += 8) {   // T22[m][k] = 0 for k > m
+            uint32_t ah[4], alo[4], bh[2], blo[2];
+            split_tf32(T[(o + 16 + g) * kLd + o + 16 + k0 + t], ah[0], alo[0]);
+            split_tf32(T[(o + 24 + g) * kLd + o + 16 + k0 + t], ah[1], alo[1]);
+            split_tf32(T[(o + 16 + g) * kLd + o + 16 + k0 + t + 4], ah[2], alo[2]);
+            split_tf32(T[(o + 24 + g) * kLd + o + 16 + k0 + t + 4], ah[3], alo[3]);
+            split_tf32(Yb[(k0 + t) * 24 + n0 + g], bh[0], blo[0]);
+            split_tf32(Yb[(k0 + t + 4) * 24 + n0 + g], bh[1], blo[1]);
+            mma_16x8x8_3xtf32(acc, ah, alo, bh, blo);
+        }
+        *reinterpret_cast<float2*>(T + (o + 16 + g) * kLd + o + n0 + 2 * t) = make_float2(-acc[0], -acc[1]);
+        *reinterpret_cast<float2*>(T + (o + 24 + g) * kLd + o + n0 + 2 * t) = make_float2(-acc[2], -acc[3]);
+        group_sync(bid);
+    }
+    {   // 4c. 64x64 level on the tensor pipe: warp w owns the 16x16 tile (rows 16 (w & 1),
+        // columns 16 (w >> 1)) of Y = A21 T11 and then of T21 = -T22 Y.  Split-tf32 products
+        // (x = hi + lo, hi lo both tf32; hi hi + hi lo + lo hi, fp32 accumulation) keep about
+        // fp32 accuracy; the zero triangles of T11 and T22 bound the k ranges.
+        const int g = lane >> 2, t = lane & 3, m0 = 16 * (warp & 1), n0 = 16 * (warp >> 1);
+        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int k0 = n0; k0 < 32; k0 += 8) {   // T11[k][n] = 0 for k < n
+            uint32_t ah[4], alo[4];
+            split_tf32(A[(32 + m0 + g) * kLdA + k0 + t], ah[0], alo[0]);
+            split_tf32(A[(40 + m0 + g) * kLdA + k0 + t], ah[1], alo[1]);
+            split_tf32(A[(32 + m0 + g) * kLdA + k0 + t + 4], ah[2], alo[2]);
+            split_tf32(A[(40 + m0 + g) * kLdA + k0 + t + 4], ah[3], alo[3]);
+#pragma unroll
+            for (int ni = 0; ni < 2; ++ni) {
+                uint32_t bh[2], blo[2];
+                split_tf32(T[(k0 + t) * kLd + n0 + 8 * ni + g], bh[0], blo[0]);
+                split_tf32(T[(k0 + t + 4) * kLd + n0 + 8 * ni + g], bh[1], blo[1]);
+                mma_16x8x8_3xtf32(acc[ni], ah, alo, bh, blo);
+            }
+        }
+#pragma unroll
+        for (int ni = 0; ni < 2; ++ni) {
+            const int cc = n0 + 8 * ni + 2 * t;
+            *reinterpret_cast<float2*>(Y + (m0 + g) * 40 + cc) = make_float2(acc[ni][0], acc[ni][1]);
+            *reinterpret_cast<float2*>(Y + (m0 + g + 8) * 40 + cc) = make_float2(acc[ni][2], acc[ni][3]);
+            acc[ni][0] = acc[ni][1] = acc[ni][2] = acc[ni][3] = 0.f;
+        }
+        group_sync(bid);
+        for (int k0 = 0; k0 < m0 + 16; k0 += 8) {   // T22[m][k] = 0 for k > m
+            uint32_t ah[4], alo[4];
+            split_tf32(T[(32 + m0 + g) * kLd + 32 + k0 + t], ah[0], alo[0]);
+            split_tf32(T[(40 + m0 + g) * kLd + 32 + k0 + t], ah[1], alo[1]);
+            split_tf32(T[(32 + m0 + g) * kLd + 32 + k0 + t + 4], ah[2], alo[2]);
+            split_tf32(T[(40 + m0 + g) * kLd + 32 + k0 + t + 4], ah[3], alo[3]);
+#pragma unroll
+            for (int ni = 0; ni < 2; ++ni) {
+                uint32_t bh[2], blo[2];
+                split_tf32(Y[(k0 + t) * 40 + n0 + 8 * ni + g], bh[0], blo[0]);
+                split_tf32(Y[(k0 + t + 4) * 40 + n0 + 8 * ni + g], bh[1], blo[1]);
+                mma_16x8x8_3xtf32(acc[ni], ah, alo, bh, blo);
+            }
+        }
+#pragma unroll
+        for (int ni = 0; ni < 2; ++ni) {
+            const int cc = n0 + 8 * ni + 2 * t;
+            *reinterpret_cast<float2*>(T + (32 + m0 + g) * kLd + cc) = make_float2(-acc[ni][0], -acc[ni][1]);
+            *reinterpret_cast<float2*>(T + (40 + m0 + g) * kLd + cc) = make_float2(-acc[ni][2], -acc[ni][3]);
+        }
+        group_sync(bid);
+    }
+}
+
 // One chunk (bh, c) of the preparation by a group of 128 threads: tid 0..127, its four
 // warps aligned to the tensor-memory lane quadrants.  The group owns `sm` (kTmGroupBytes,
 // 1024-aligned), the initialised mbarriers bar[0..1] (this chunk completes their phase
@@ -286,106 +391,8 @@ __device__ __forceinline__ bool tmat_chunk(const CUtensorMap* tm_k, const CUtens
     if (!ok) return false;
 
     // ---- 4. T = (I + A)^{-1}
-    const float* A = (const float*)(sm + kTmA);
     float* T = (float*)(sm + kTmT);
-    float* Y = (float*)(sm + kTmY);
-    if (tid < 64) {   // 4a. diagonal block b = tid >> 4, column cc = tid & 15: forward substitution
-        const int o = 16 * (tid >> 4), cc = tid & 15;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = (i == cc) ? 1.f : 0.f;
-#pragma unroll
-        for (int jj = 0; jj < 15; ++jj)
-#pragma unroll
-            for (int i = jj + 1; i < 16; ++i) x[i] = fmaf(-A[(o + i) * kLdA + o + jj], x[jj], x[i]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) T[(o + i) * kLd + o + cc] = x[i];
-    }
-    group_sync(bid);
-    {   // 4b. 32x32 level on the tensor pipe: block be = warp >> 1 (rows/cols 32 be ..);
-        // warp (w & 1) owns columns 8 (w & 1) .. +7 of Y = A21 T11 and then of T21 = -T22 Y
-        // (split-tf32 as in 4c; T11[k][n] = 0 for k < n bounds the first k range)
-        const int g = lane >> 2, t = lane & 3, be = warp >> 1, o = 32 * be, n0 = 8 * (warp & 1);
-        float* Yb = Y + be * 16 * 24;   // row stride 24 (= 24 mod 32): conflict-free fragment loads
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int k0 = n0; k0 < 16; k0 += 8) {
-            uint32_t ah[4], alo[4], bh[2], blo[2];
-            split_tf32(A[(o + 16 + g) * kLdA + o + k0 + t], ah[0], alo[0]);
-            split_tf32(A[(o + 24 + g) * kLdA + o + k0 + t], ah[1], alo[1]);
-            split_tf32(A[(o + 16 + g) * kLdA + o + k0 + t + 4], ah[2], alo[2]);
-            split_tf32(A[(o + 24 + g) * kLdA + o + k0 + t + 4], ah[3], alo[3]);
-            split_tf32(T[(o + k0 + t) * kLd + o + n0 + g], bh[0], blo[0]);
-            split_tf32(T[(o + k0 + t + 4) * kLd + o + n0 + g], bh[1], blo[1]);
-            mma_16x8x8_3xtf32(acc, ah, alo, bh, blo);
-        }
-        *reinterpret_cast<float2*>(Yb + g * 24 + n0 + 2 * t) = make_float2(acc[0], acc[1]);
-        *reinterpret_cast<float2*>(Yb + (g + 8) * 24 + n0 + 2 * t) = make_float2(acc[2], acc[3]);
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        group_sync(bid);
-        for (int k0 = 0; k0 < 16; k0 += 8) {   // T22[m][k] = 0 for k > m
-            uint32_t ah[4], alo[4], bh[2], blo[2];
-            split_tf32(T[(o + 16 + g) * kLd + o + 16 + k0 + t], ah[0], alo[0]);
-            split_tf32(T[(o + 24 + g) * kLd + o + 16 + k0 + t], ah[1], alo[1]);
-            split_tf32(T[(o + 16 + g) * kLd + o + 16 + k0 + t + 4], ah[2], alo[2]);
-            split_tf32(T[(o + 24 + g) * kLd + o + 16 + k0 + t + 4], ah[3], alo[3]);
-            split_tf32(Yb[(k0 + t) * 24 + n0 + g], bh[0], blo[0]);
-            split_tf32(Yb[(k0 + t + 4) * 24 + n0 + g], bh[1], blo[1]);
-            mma_16x8x8_3xtf32(acc, ah, alo, bh, blo);
-        }
-        *reinterpret_cast<float2*>(T + (o + 16 + g) * kLd + o + n0 + 2 * t) = make_float2(-acc[0], -acc[1]);
-        *reinterpret_cast<float2*>(T + (o + 24 + g) * kLd + o + n0 + 2 * t) = make_float2(-acc[2], -acc[3]);
-        group_sync(bid);
-    }
-    {   // 4c. 64x64 level on the tensor pipe: warp w owns the 16x16 tile (rows 16 (w & 1),
-        // columns 16 (w >> 1)) of Y = A21 T11 and then of T21 = -T22 Y.  Split-tf32 products
-        // (x = hi + lo, hi lo both tf32; hi hi + hi lo + lo hi, fp32 accumulation) keep about
-        // fp32 accuracy; the zero triangles of T11 and T22 bound the k ranges.
-        const int g = lane >> 2, t = lane & 3, m0 = 16 * (warp & 1), n0 = 16 * (warp >> 1);
-        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        for (int k0 = n0; k0 < 32; k0 += 8) {   // T11[k][n] = 0 for k < n
-            uint32_t ah[4], alo[4];
-            split_tf32(A[(32 + m0 + g) * kLdA + k0 + t], ah[0], alo[0]);
-            split_tf32(A[(40 + m0 + g) * kLdA + k0 + t], ah[1], alo[1]);
-            split_tf32(A[(32 + m0 + g) * kLdA + k0 + t + 4], ah[2], alo[2]);
-            split_tf32(A[(40 + m0 + g) * kLdA + k0 + t + 4], ah[3], alo[3]);
-#pragma unroll
-            for (int ni = 0; ni < 2; ++ni) {
-                uint32_t bh[2], blo[2];
-                split_tf32(T[(k0 + t) * kLd + n0 + 8 * ni + g], bh[0], blo[0]);
-                split_tf32(T[(k0 + t + 4) * kLd + n0 + 8 * ni + g], bh[1], blo[1]);
-                mma_16x8x8_3xtf32(acc[ni], ah, alo, bh, blo);
-            }
-        }
-#pragma unroll
-        for (int ni = 0; ni < 2; ++ni) {
-            const int cc = n0 + 8 * ni + 2 * t;
-            *reinterpret_cast<float2*>(Y + (m0 + g) * 40 + cc) = make_float2(acc[ni][0], acc[ni][1]);
-            *reinterpret_cast<float2*>(Y + (m0 + g + 8) * 40 + cc) = make_float2(acc[ni][2], acc[ni][3]);
-            acc[ni][0] = acc[ni][1] = acc[ni][2] = acc[ni][3] = 0.f;
-        }
-        group_sync(bid);
-        for (int k0 = 0; k0 < m0 + 16; k0 += 8) {   // T22[m][k] = 0 for k > m
-            uint32_t ah[4], alo[4];
-            split_tf32(T[(32 + m0 + g) * kLd + 32 + k0 + t], ah[0], alo[0]);
-            split_tf32(T[(40 + m0 + g) * kLd + 32 + k0 + t], ah[1], alo[1]);
-            split_tf32(T[(32 + m0 + g) * kLd + 32 + k0 + t + 4], ah[2], alo[2]);
-            split_tf32(T[(40 + m0 + g) * kLd + 32 + k0 + t + 4], ah[3], alo[3]);
-#pragma unroll
-            for (int ni = 0; ni < 2; ++ni) {
-                uint32_t bh[2], blo[2];
-                split_tf32(Y[(k0 + t) * 40 + n0 + 8 * ni + g], bh[0], blo[0]);
-                split_tf32(Y[(k0 + t + 4) * 40 + n0 + 8 * ni + g], bh[1], blo[1]);
-                mma_16x8x8_3xtf32(acc[ni], ah, alo, bh, blo);
-            }
-        }
-#pragma unroll
-        for (int ni = 0; ni < 2; ++ni) {
-            const int cc = n0 + 8 * ni + 2 * t;
-            *reinterpret_cast<float2*>(T + (32 + m0 + g) * kLd + cc) = make_float2(-acc[ni][0], -acc[ni][1]);
-            *reinterpret_cast<float2*>(T + (40 + m0 + g) * kLd + cc) = make_float2(-acc[ni][2], -acc[ni][3]);
-        }
-        group_sync(bid);
-    }
+    unit_lower_inverse64((const float*)(sm + kTmA), T, (float*)(sm + kTmY), bid, tid);
     if (a.rec_T && dbg_in(a.rec_T + ((size_t)bh * a.NC + c) * 4096, 16384, a.rec_T, (size_t)a.nch * 16384, status) &&
         dbg_in(a.rec_alpha + ((size_t)bh * a.NC + c) * 64, 256, a.rec_alpha, (size_t)a.nch * 256, status)) {
         // the chunk-state record keeps T (fp32, zero above the diagonal) and alpha

@@ -94,4 +94,15 @@ def test_workspaces_grow(lib):
     a, b = (lib.efla_gated_bwd_workspace_size(ctypes.byref(shape(L=n))) for n in (64, 1000))
     assert 0 < a < b
     assert lib.efla_gated_fwd_workspace_size(ctypes.byref(shape(L=0))) == 0
+
+
+def test_tensor_path_needs_bf16_rows_on_16_bytes(lib):
+    assert fwd(lib, shape(path=efla.TENSOR, dtype=efla.F32)) == 2
+    assert fwd(lib, shape(path=efla.TENSOR), k=P[1] + 2) == 2
+    assert fwd(lib, shape(path=efla.TENSOR, strides={"v": (12808, 3200, 36)})) == 2
+    assert fwd(lib, shape(path=efla.TENSOR, strides={"q": (12800, 0, 64)})) == 2
+    assert fwd(lib, shape(path=efla.TENSOR), ws=None) == 4      # accepted up to its workspace
+
+
+def test_packed_slots(lib):
     assert lib.efla_gated_fwd_workspace_size(ctypes.byref(shape(L=0, packed=True))) > 0
