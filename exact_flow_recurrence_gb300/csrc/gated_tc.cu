@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __gr
         for (int c = 0; c < 64; c += 16)
             tmem_ld16(taddr(tb, warp * 32, c), *reinterpret_cast<float(*)[16]>(v + c));
         tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) loaded16(v + c);
         const float chi = vec->chi[i], clo = vec->clo[i];
         if (tid < 64) {
             float lam = 0.f;
@@ -225,9 +227,11 @@ struct ScanSmem {
     static constexpr uint32_t KQ = 0;                                // 2 stages x 2 blocks of 64 dk x [K rows | Q rows]
     static constexpr uint32_t TP = 65536;
     static constexpr uint32_t V = TP + TPS * NP * 16384;             // 2 stages
-    static constexpr uint32_t S = V + 2 * 8192;                      // NP x [128 rows][64]
-    static constexpr uint32_t X = S + NP * 16384;                    // NP x [64 rows][64]
-    static constexpr uint32_t VEC = X + NP * 8192;                   // 2 stages
+    // part p, column j of an operand is column p N + j: blocks of 64 columns, one after another
+    static constexpr int BLK = (NP * N + 63) / 64;
+    static constexpr uint32_t S = V + 2 * 8192;                      // BLK x [128 rows][64]
+    static constexpr uint32_t X = S + BLK * 16384;                   // BLK x [64 rows][64]
+    static constexpr uint32_t VEC = X + BLK * 8192;                  // 2 stages
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
     static constexpr size_t bytes = 1024 + BAR + 128;
 };
@@ -283,22 +287,22 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
     const size_t rec0 = (size_t)h * a.slots + s.slot0;
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(full + i, 1);
-        mbar_init(s_ready, 256);
-        mbar_init(x_ready, 128);
-        mbar_init(u_ready, 128);
+        mbar_init(s_ready, 8);   // warps
+        mbar_init(x_ready, 4);
+        mbar_init(u_ready, 8);
         mbar_init(d1, 1);
         mbar_init(d2, 1);
         mbar_init(d3, 1);
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(tslot, 256);
+        tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tb = *tslot, t1 = tb, t2 = tb + 64, t3 = tb + 128;
+    const uint32_t tb = *tslot, t1 = tb, t2 = tb + 256, t3 = tb;   // D3 over D1: every warp has read D1 by then
 
     if (warp == 8) {
         if (lane == 0 && nch > 0) {
@@ -323,8 +327,12 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                 bulk_g2s(sm + M::TP + (c % M::TPS) * NP * 16384, a.img + (rec0 + c) * NP * 16384, NP * 16384u, f);
                 issued_tp = c + 1;
             };
-            const uint32_t id_kq = idesc_f16(128, N, false, true, true);   // A K-major, B MN-major
-            const uint32_t id_kt = idesc_f16(128, N, true, true, true);    // both MN-major
+            // The products take the operands' parts side by side along N (D keeps a column group for
+            // each part of B; the epilogues add them): an instruction costs about 43 cycles up to
+            // N = 64, 60 at 128 and 91 at 192, so NP parts in one cost less than NP instructions.
+            const int nblk = (d.dk + 63) / 64;
+            const uint32_t id_kt = idesc_f16(128, NP * N, true, true, true);   // A, B MN-major
+            const uint64_t dS = sdesc_sw128(smem_u32(sm + M::S), 16384), dX = sdesc_sw128(smem_u32(sm + M::X), 8192);
             load(0);
             load_tp(0);
             bool ok = true;
@@ -340,32 +348,38 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                 ok = mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
                 if (!ok) break;
                 tc_fence_after();
-                for (int p = 0; p < NP; ++p)
-                    for (int ks = 0; ks < d.dk / 16; ++ks)
-                        mma_f16_ss(t1, sdesc_sw128(smem_u32(kq + (ks / 4) * 16384 + (ks % 4) * 32)),
-                                   sdesc_sw128(smem_u32(sm + M::S + p * 16384 + ks * 2048)), id_kq, p + ks > 0);
+                {
+                    const uint64_t a0 = sdesc_sw128(smem_u32(kq));
+#pragma unroll 1
+                    for (int blk = 0; blk < nblk; ++blk)   // (64 dk at a time, zeros past dk: no branch per instruction)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ss(t1, a0 + blk * 1024 + ks * 2, dS + blk * 512 + ks * 128,
+                                       idesc_f16(128, NP * N, false, true, true), blk + ks > 0);
+                }
                 mma_commit(d1);
                 ok = mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit) && mbar_wait(x_ready, ph, kWaitLimit);
                 if (!ok) break;
                 tc_fence_after();
                 {
-                    unsigned char* tp = sm + M::TP + (c % M::TPS) * NP * 16384;
-                    int any = 0;
-                    for (int p = 0; p < NP; ++p)
-                        for (int x = 0; x + p < NP; ++x)
-                            for (int ks = 0; ks < 4; ++ks, any = 1)
-                                mma_f16_ss(t2, sdesc_sw128(smem_u32(tp + p * 16384 + ks * 32)),
-                                           sdesc_sw128(smem_u32(sm + M::X + x * 8192 + ks * 2048)), id_kq, any);
+                    const uint64_t a0 = sdesc_sw128(smem_u32(sm + M::TP + (c % M::TPS) * NP * 16384));
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)   // with the part pairs p + x < NP
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ss(t2, a0 + p * 1024 + ks * 2, dX + ks * 128,
+                                       idesc_f16(128, (NP - p) * N, false, true, true), p + ks > 0);
                 }
                 mma_commit(d2);
                 ok = mbar_wait(u_ready, ph, kWaitLimit);
                 if (!ok) break;
                 tc_fence_after();
                 if (M::TPS == 1 && c + 1 < nch) load_tp(c + 1);   // (D2 is done: u_ready came from it)
-                for (int p = 0; p < NP; ++p)
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_ss(t3, sdesc_sw128(smem_u32(kq + ks * 2048), 16384),
-                                   sdesc_sw128(smem_u32(sm + M::X + p * 8192 + ks * 2048)), id_kt, p + ks > 0);
+                {
+                    const uint64_t a0 = sdesc_sw128(smem_u32(kq), 16384);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) mma_f16_ss(t3, a0 + ks * 128, dX + ks * 128, id_kt, ks > 0);
+                }
                 mma_commit(d3);
             }
             if (!ok) {   // a wait gave up: the copies under way land before the CTA ends
@@ -383,6 +397,42 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
         const int nv = min(max(d.dv - c0 - cc, 0), NC);                              // columns of these that exist
         const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + c0 + cc;
         const uint32_t lq = 32 * (warp & 3);
+        // 8 values of `r`, column cc + e of the slice, as parts into an operand of 64-column blocks
+        const auto put = [&](uint32_t base, uint32_t blk, int r, int e, const float* x) {
+            uint4 w[NP];
+            split8<NP>(x, w);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const int j = p * N + cc + e;
+                *reinterpret_cast<uint4*>(sm + base + (j >> 6) * blk + sw128(r, j & 63)) = w[p];
+            }
+        };
+        // this thread's lane of an accumulator: the sum of its column groups
+        const auto get = [&](uint32_t t, float* y) {
+#pragma unroll
+            for (int e = 0; e < NC; e += 16) {
+                float x[NP][16];
+#pragma unroll
+                for (int p = 0; p < NP; ++p) tmem_ld16(taddr(t, lq, p * N + cc + e), x[p]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int p = 0; p < NP; ++p) loaded16(x[p]);
+#pragma unroll
+                for (int m = 0; m < 16; ++m) {
+                    y[e + m] = x[NP - 1][m];
+#pragma unroll
+                    for (int p = NP - 2; p >= 0; --p) y[e + m] += x[p][m];   // the small ones first
+                }
+            }
+        };
+        // (the warp leaves together if a wait gives up)
+        const auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, kWaitLimit)) != 0; };
+        const auto arrive = [&](uint64_t* bar) {   // a warp's shared-memory writes and tensor-memory reads are done
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         float S[NC];
 #pragma unroll
         for (int e = 0; e < NC; e += 4) {
@@ -396,36 +446,25 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
             const int n = min(kGC, s.len - c * kGC);
             const GVec* vec = (const GVec*)(sm + M::VEC + (c & 1) * sizeof(GVec));
 #pragma unroll
-            for (int e = 0; e < NC; e += 8) {
-                uint4 w[NP];
-                split8<NP>(S + e, w);
-#pragma unroll
-                for (int p = 0; p < NP; ++p)
-                    *reinterpret_cast<uint4*>(sm + M::S + p * 16384 + sw128(row, cc + e)) = w[p];
-            }
+            for (int e = 0; e < NC; e += 8) put(M::S, 16384, row, e, S + e);
             if (d.packed && n < kGC) {   // rows past the sequence are another's: zero its keys (0 x NaN is not 0)
-                ok = mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
+                ok = wait(&full[c & 1], (c >> 1) & 1);
                 unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
                 for (int e = tid; e < (kGC - n) * 16; e += 256)
                     *reinterpret_cast<uint4*>(kq + (e & 1) * 16384 + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
-            fence_async_smem();
-            tc_fence_before();
-            mbar_arrive(s_ready);
-            ok = ok && mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
+            arrive(s_ready);
+            ok = ok && wait(&full[c & 1], (c >> 1) & 1);
             if (!ok) break;
             const float up = vec->up[i], last = vec->up[63];
             float y[NC];
             if (top) {
                 const float al = vec->al[i], rest = vec->rest[i];
                 const unsigned char* vt = sm + M::V + (c & 1) * 8192;
-                if (!(ok = mbar_wait(d1, ph, kWaitLimit))) break;
+                if (!(ok = wait(d1, ph))) break;
                 tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < NC; e += 16)
-                    tmem_ld16(taddr(t1, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
-                tmem_ld_wait();
+                get(t1, y);
 #pragma unroll
                 for (int e = 0; e < NC; e += 8) {
                     const uint4 raw8 = *reinterpret_cast<const uint4*>(vt + sw128(i, cc + e));
@@ -438,49 +477,29 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                     }
 #pragma unroll
                     for (int m = 0; m < 8; ++m) x[m] = i < n ? al * x[m] : 0.f;
-                    uint4 w[NP];
-                    split8<NP>(x, w);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)
-                        *reinterpret_cast<uint4*>(sm + M::X + p * 8192 + sw128(i, cc + e)) = w[p];
+                    put(M::X, 8192, i, e, x);
                 }
-                fence_async_smem();
-                tc_fence_before();
-                mbar_arrive(x_ready);
-                if (!(ok = mbar_wait(d2, ph, kWaitLimit))) break;
+                arrive(x_ready);
+                if (!(ok = wait(d2, ph))) break;
                 tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < NC; e += 16)
-                    tmem_ld16(taddr(t2, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
-                tmem_ld_wait();
+                get(t2, y);
 #pragma unroll
                 for (int e = 0; e < NC; e += 8) {
                     float x[8];
 #pragma unroll
                     for (int m = 0; m < 8; ++m) x[m] = rest * y[e + m];
-                    uint4 w[NP];
-                    split8<NP>(x, w);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)
-                        *reinterpret_cast<uint4*>(sm + M::X + p * 8192 + sw128(i, cc + e)) = w[p];
+                    put(M::X, 8192, i, e, x);
                 }
-                fence_async_smem();
-                tc_fence_before();
-                mbar_arrive(u_ready);
+                arrive(u_ready);
             } else {
-                if (!(ok = mbar_wait(d1, ph, kWaitLimit))) break;
+                if (!(ok = wait(d1, ph))) break;
                 tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < NC; e += 16)
-                    tmem_ld16(taddr(t1, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
-                tmem_ld_wait();
-                if (!(ok = mbar_wait(d2, ph, kWaitLimit))) break;
+                get(t1, y);
+                arrive(u_ready);
+                if (!(ok = wait(d2, ph))) break;
                 tc_fence_after();
                 float z[NC];
-#pragma unroll
-                for (int e = 0; e < NC; e += 16)
-                    tmem_ld16(taddr(t2, lq, cc + e), *reinterpret_cast<float(*)[16]>(z + e));
-                tmem_ld_wait();
+                get(t2, z);
                 if (i < n) {
                     Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + c0 + cc;
 #pragma unroll
@@ -490,12 +509,9 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                         if (e < nv) st16(op + e, y + e);
                 }
             }
-            if (!(ok = mbar_wait(d3, ph, kWaitLimit))) break;
+            if (!(ok = wait(d3, ph))) break;
             tc_fence_after();
-#pragma unroll
-            for (int e = 0; e < NC; e += 16)
-                tmem_ld16(taddr(t3, lq, cc + e), *reinterpret_cast<float(*)[16]>(y + e));
-            tmem_ld_wait();
+            get(t3, y);
 #pragma unroll
             for (int e = 0; e < NC; ++e) S[e] = fmaf(last, S[e], y[e]);
         }
@@ -509,7 +525,7 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tb, 256);
+    if (warp == 8) tmem_dealloc(tb, 512);
 }
 
 struct TcWs {

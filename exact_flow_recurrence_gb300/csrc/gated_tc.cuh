@@ -27,6 +27,13 @@ struct GVec {
     float clo[64];
 };
 
+// To follow a wait for tensor-memory loads: the loaded values may be used from here on.  (The
+// wait names no registers, so arithmetic on them could otherwise be scheduled before it.)
+__device__ __forceinline__ void loaded16(float* v) {
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+
 // 8 values -> NP 16-byte chunks of bf16 parts
 template <int NP>
 __device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
