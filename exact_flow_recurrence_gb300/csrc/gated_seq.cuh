@@ -53,6 +53,16 @@ __device__ __forceinline__ long long at3(const long long (&s)[3], int b, int h, 
 // c_i are kept as two floats (hi + lo), since e^{c_i - c_j} needs the difference's absolute
 // error small where c itself may be thousands.
 __device__ __forceinline__ float log_decay(float g) { return g < -128.f ? -128.f : g; }
+// The tensor-core kernels keep c in units of log 2.  ex2.approx: 2^-22 of the result.
+constexpr double kLog2e = 1.4426950408889634;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float decay2(float hi_i, float lo_i, float hi_j, float lo_j) {
+    return exp2_fast((hi_i - hi_j) + (lo_i - lo_j));
+}
 __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
     return expf((hi_i - hi_j) + (lo_i - lo_j));
 }

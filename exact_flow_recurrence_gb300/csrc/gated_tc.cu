@@ -19,9 +19,13 @@ __device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kS
 // One chunk of a value head per CTA of 128 threads:
 //   1. the chunk's K and Q rows by TMA into [K; Q] tiles (128 rows);
 //   2. one product [K; Q] K^T: lanes 0..63 G = K K^T (its diagonal: lambda), 64..127 Q K^T;
-//   3. A and P (fp32, shared memory), from the decays;
-//   4. T by blocked substitution (split tf32, about fp32 accuracy), P T likewise;
-//   5. the [T; P T] image: 128 rows of 64, NP parts in the operand layout, out by bulk copy.
+//   3. from the decays: A (fp32, shared memory), and P as bf16 parts in rows 64..127 of the image;
+//   4. T = (I + A)^{-1} in place of A (blocked substitution, split tf32: about fp32 accuracy),
+//      its parts into rows 0..63 of the image;
+//   5. one product [T; P] T, whose lanes 64..127 (P T) replace P's parts;
+//   6. the [T; P T] image, NP parts of 128 rows in the operand layout, out by bulk copy.
+// Bound by its chain of short dependent steps, not by data: what counts is how many chunks an
+// SM has in flight.  The image lies over the dead tiles and T over A, so that four chunks fit.
 struct PrepArgs {
     const float* g;
     const float* beta;
@@ -30,22 +34,19 @@ struct PrepArgs {
     int slots;
 };
 
-constexpr uint32_t kPrA = 0;            // [64][kLdA] fp32, once the tiles are read
-constexpr uint32_t kPrY = 17408;        // [32][40] fp32
-constexpr uint32_t kPrP = 32768;        // [64][kLd] fp32
-constexpr uint32_t kPrT = 50176;        // [64][kLd] fp32
-constexpr uint32_t kPrVec = 67584;      // GVec
-constexpr uint32_t kPrBar = kPrVec + sizeof(GVec);
-constexpr uint32_t kPrEnd = (kPrBar + 64 + 1023) / 1024 * 1024;
 template <int NP>
 struct PrepSmem {
-    static constexpr uint32_t img = NP == 2 ? 0u : kPrEnd;   // two parts fit over A and Y
-    static constexpr size_t bytes = 1024 + kPrEnd + (NP == 2 ? 0 : NP * 16384);
+    static constexpr uint32_t IMG = 0;             // the tiles first; the inverse's scratch in its rows 0..63
+    static constexpr uint32_t A = NP * 16384;      // [64][kLdA] fp32
+    static constexpr uint32_t VEC = A + 64 * kLdA * 4;
+    static constexpr uint32_t BAR = VEC + sizeof(GVec);
+    static constexpr size_t bytes = 1024 + BAR + 64;
 };
 
 template <int NP>
-__global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
-                                                 const __grid_constant__ CUtensorMap tm_k) {
+__global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
+                                                    const __grid_constant__ CUtensorMap tm_k) {
+    using M = PrepSmem<NP>;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int slot = blockIdx.x, h = blockIdx.y, hk = h / (d.H / d.Hk), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -53,12 +54,11 @@ __global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __gr
     const SeqAt s = seq_at(d, b, kGC);
     const int t0 = (slot - s.slot0) * kGC, n = min(kGC, s.len - t0), t = s.start + t0;
     if (n <= 0) return;
-    uint64_t* bar = (uint64_t*)(sm + kPrBar);
-    uint32_t* tslot = (uint32_t*)(bar + 2);
-    GVec* vec = (GVec*)(sm + kPrVec);
+    uint64_t* bar = (uint64_t*)(sm + M::BAR);
+    uint32_t* tslot = (uint32_t*)(bar + 3);
+    GVec* vec = (GVec*)(sm + M::VEC);
     if (tid == 0) {
-        mbar_init(&bar[0], 1);
-        mbar_init(&bar[1], 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
         mbar_arrive_expect_tx(&bar[0], 4u * 8192u);
         for (int blk = 0; blk < 2; ++blk) {
@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __gr
     }
     if (warp == 1) {   // sums of the log decays (two tokens a lane), in fp64 until they are two floats
         const int i0 = 2 * lane;
-        const double x0 = i0 < n ? (double)log_decay(a.g[at3(d.gs, s.batch, h, t + i0)]) : 0.0;
-        double c1 = x0 + (i0 + 1 < n ? (double)log_decay(a.g[at3(d.gs, s.batch, h, t + i0 + 1)]) : 0.0);
-        const double own = c1 - x0;
+        const double x0 = i0 < n ? (double)log_decay(a.g[at3(d.gs, s.batch, h, t + i0)]) * kLog2e : 0.0;
+        const double x1 = i0 + 1 < n ? (double)log_decay(a.g[at3(d.gs, s.batch, h, t + i0 + 1)]) * kLog2e : 0.0;
+        double c1 = x0 + x1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, c1, o);
@@ -83,12 +83,12 @@ __global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __gr
         const double last = __shfl_sync(0xffffffffu, c1, 31);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const double c = e ? c1 : c1 - own;
+            const double c = e ? c1 : c1 - x1;
             const float hi = (float)c;
             vec->chi[i0 + e] = hi;
             vec->clo[i0 + e] = (float)(c - (double)hi);
-            vec->up[i0 + e] = expf(hi);
-            vec->rest[i0 + e] = expf((float)(last - c));
+            vec->up[i0 + e] = exp2_fast(hi);
+            vec->rest[i0 + e] = exp2_fast((float)(last - c));
         }
     }
     const float beta = tid < n ? a.beta[at3(d.bs, s.batch, h, t + tid)] : 0.f;
@@ -99,23 +99,26 @@ __global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __gr
     if (tid == 0) {
         if (mbar_wait(&bar[0], 0, kWaitLimit)) {
             tc_fence_after();
-            for (int ks = 0; ks < d.dk / 16; ++ks) {
-                const uint64_t x = sdesc_sw128(smem_u32(sm + (ks / 4) * 16384 + (ks % 4) * 32));
-                mma_f16_ss(tb, x, x, idesc_f16(128, 64, false, false, true), ks > 0);
-            }
+            const uint64_t x = sdesc_sw128(smem_u32(sm));
+#pragma unroll 1
+            for (int blk = 0; blk < (d.dk + 63) / 64; ++blk)   // (zeros past dk)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f16_ss(tb, x + blk * 1024 + ks * 2, x + blk * 1024 + ks * 2, idesc_f16(128, 64, false, false, true),
+                               blk + ks > 0);
             mma_commit(&bar[1]);
         } else {
             atomicOr(&g_gt2_status, 1u);
             mbar_wait(&bar[0], 0, kWaitLimit);   // let the copies land
         }
     }
-    const bool ok = __syncthreads_and(mbar_wait(&bar[1], 0, kWaitLimit));
+    bool ok = __syncthreads_and(mbar_wait(&bar[1], 0, kWaitLimit));
     tc_fence_after();
-    float* A = (float*)(sm + kPrA);
-    float* P = (float*)(sm + kPrP);
-    float* T = (float*)(sm + kPrT);
+    float* T = (float*)(sm + M::A);
+    unsigned char* img = sm + M::IMG;
     if (ok) {
         const int i = tid & 63;   // this lane's token; lanes 0..63 hold A's rows, 64..127 P's
+        const int cols = 32 * (warp & 1) + 32;   // columns that the warp's rows reach
         float v[64];
 #pragma unroll
         for (int c = 0; c < 64; c += 16)
@@ -124,86 +127,104 @@ __global__ void __launch_bounds__(128) k_gt_prep(GDims d, PrepArgs a, const __gr
 #pragma unroll
         for (int c = 0; c < 64; c += 16) loaded16(v + c);
         const float chi = vec->chi[i], clo = vec->clo[i];
+        float scale = 1.f;
         if (tid < 64) {
             float lam = 0.f;
 #pragma unroll
             for (int j = 0; j < 64; ++j) lam = j == i ? v[j] : lam;
-            const float al = i < n ? alpha_of(beta, lam, d.euler) : 0.f;
-            vec->al[i] = al;
+            scale = i < n ? alpha_of(beta, lam, d.euler) : 0.f;
+            vec->al[i] = scale;
+        }
+        const int diag = tid < 64 ? i : i + 1;   // columns below this are kept
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-                v[j] = j < i && i < n ? al * decay(chi, clo, vec->chi[j], vec->clo[j]) * v[j] : 0.f;
+        for (int j = 0; j < 64; j += 4) {
+            if (j < cols) {
+                const float4 h4 = *reinterpret_cast<const float4*>(vec->chi + j), l4 = *reinterpret_cast<const float4*>(vec->clo + j);
+                v[j] = j < diag && i < n ? scale * decay2(chi, clo, h4.x, l4.x) * v[j] : 0.f;
+                v[j + 1] = j + 1 < diag && i < n ? scale * decay2(chi, clo, h4.y, l4.y) * v[j + 1] : 0.f;
+                v[j + 2] = j + 2 < diag && i < n ? scale * decay2(chi, clo, h4.z, l4.z) * v[j + 2] : 0.f;
+                v[j + 3] = j + 3 < diag && i < n ? scale * decay2(chi, clo, h4.w, l4.w) * v[j + 3] : 0.f;
+            } else {
+                v[j] = v[j + 1] = v[j + 2] = v[j + 3] = 0.f;
+            }
+        }
+        // 64 values as parts into a row of the image
+        const auto put_row = [&](int r, const float* x) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 8) {
+                uint4 w[NP];
+                split8<NP>(x + j, w);
+#pragma unroll
+                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(img + p * 16384 + sw128(r, j)) = w[p];
+            }
+        };
+        if (tid < 64) {
 #pragma unroll
             for (int j = 0; j < 64; j += 4)
-                *reinterpret_cast<float4*>(A + i * kLdA + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                *reinterpret_cast<float4*>(T + i * kLdA + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         } else {
-#pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = j <= i && i < n ? decay(chi, clo, vec->chi[j], vec->clo[j]) * v[j] : 0.f;
-#pragma unroll
-            for (int j = 0; j < 64; j += 4)
-                *reinterpret_cast<float4*>(P + i * kLd + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            put_row(64 + i, v);
         }
         tc_fence_before();
         group_sync(1);
-        unit_lower_inverse64(A, T, (float*)(sm + kPrY), 1, tid);
-        unsigned char* img = sm + PrepSmem<NP>::img;
-        {   // T's rows, 32 columns a thread (zero above its 16x16 diagonal blocks)
+        unit_lower_inverse64(T, T, (float*)img, 1, tid);
+        {   // T's parts, 32 columns a thread (zero above its 16x16 diagonal blocks)
             const int r = tid >> 1, h0 = 32 * (tid & 1);
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
                 float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = h0 + j < 16 * (r / 16 + 1) ? T[r * kLd + h0 + j + e] : 0.f;
+                const bool in = h0 + j < 16 * (r / 16 + 1);
+                const float4 x0 = in ? *reinterpret_cast<const float4*>(T + r * kLd + h0 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 x1 = in ? *reinterpret_cast<const float4*>(T + r * kLd + h0 + j + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[0] = x0.x; x[1] = x0.y; x[2] = x0.z; x[3] = x0.w;
+                x[4] = x1.x; x[5] = x1.y; x[6] = x1.z; x[7] = x1.w;
                 uint4 w[NP];
                 split8<NP>(x, w);
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
-                    *reinterpret_cast<uint4*>(img + p * 16384 + sw128(r, h0 + j)) = w[p];
-            }
-        }
-        // P T: warp w owns the 8-column tiles w and 7 - w, for the four 16-row blocks
-        const int gi = lane >> 2, ti = lane & 3;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            const int n0 = 8 * (half ? 7 - warp : warp);
-#pragma unroll 1
-            for (int m0 = 0; m0 < 64; m0 += 16) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int k0 = n0; k0 < m0 + 16; k0 += 8) {   // T[k][n] = 0 for k < n, P[m][k] = 0 for k > m
-                    uint32_t ah[4], alo[4], bh[2], blo[2];
-                    split_tf32(P[(m0 + gi) * kLd + k0 + ti], ah[0], alo[0]);
-                    split_tf32(P[(m0 + 8 + gi) * kLd + k0 + ti], ah[1], alo[1]);
-                    split_tf32(P[(m0 + gi) * kLd + k0 + ti + 4], ah[2], alo[2]);
-                    split_tf32(P[(m0 + 8 + gi) * kLd + k0 + ti + 4], ah[3], alo[3]);
-                    split_tf32(T[(k0 + ti) * kLd + n0 + gi], bh[0], blo[0]);
-                    split_tf32(T[(k0 + ti + 4) * kLd + n0 + gi], bh[1], blo[1]);
-                    mma_16x8x8_3xtf32(acc, ah, alo, bh, blo);
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x0 = acc[2 * e], x1 = acc[2 * e + 1];
-                    const uint32_t at = sw128(64 + m0 + 8 * e + gi, n0 + 2 * ti);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
-                        const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
-                        *reinterpret_cast<uint32_t*>(img + p * 16384 + at) = u;
-                        x0 -= __uint_as_float(u << 16);
-                        x1 -= __uint_as_float(u & 0xffff0000u);
-                    }
-                }
+                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(img + p * 16384 + sw128(r, h0 + j)) = w[p];
             }
         }
         fence_async_smem();
-    } else {
+        tc_fence_before();
+        group_sync(1);
+        if (tid == 0) {   // [T; P] T, the part pairs p + x < NP (B: T's rows are K indices)
+            tc_fence_after();
+            const uint64_t da = sdesc_sw128(smem_u32(img));
+#pragma unroll
+            for (int p = NP - 1; p >= 0; --p)
+#pragma unroll
+                for (int x = NP - 1 - p; x >= 0; --x)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16_ss(tb, da + p * 1024 + ks * 2, da + x * 1024 + ks * 128, idesc_f16(128, 64, false, true, true),
+                                   !(p == NP - 1 && x == 0 && ks == 0));
+            mma_commit(&bar[2]);
+        }
+        ok = group_sync_and(1, mbar_wait(&bar[2], 0, kWaitLimit));
+        tc_fence_after();
+        if (tid >= 64 && ok) {
+#pragma unroll
+            for (int c = 0; c < 64; c += 16)
+                tmem_ld16(taddr(tb, warp * 32, c), *reinterpret_cast<float(*)[16]>(v + c));
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) loaded16(v + c);
+            put_row(64 + i, v);
+            tc_fence_before();
+        }
+        fence_async_smem();
+    }
+    if (!ok) {
         atomicOr(&g_gt2_status, 1u);
-        mbar_wait(&bar[1], 0, kWaitLimit);   // (a product still in flight ends before its tensor memory is freed)
+        mbar_wait(&bar[1], 0, kWaitLimit);   // (products still in flight end before their tensor memory is freed)
+        mbar_wait(&bar[2], 0, kWaitLimit);
     }
     __syncthreads();
+    tc_fence_after();
     if (tid == 0 && ok) {
         const size_t rec = (size_t)h * a.slots + slot, all = (size_t)d.H * a.slots;
         if (dbg_in(a.img + rec * NP * 16384, NP * 16384, a.img, all * NP * 16384, &g_gt2_status))
-            bulk_s2g(a.img + rec * NP * 16384, sm + PrepSmem<NP>::img, NP * 16384);
+            bulk_s2g(a.img + rec * NP * 16384, img, NP * 16384);
         if (dbg_in(a.vec + rec, sizeof(GVec), a.vec, all * sizeof(GVec), &g_gt2_status))
             bulk_s2g(a.vec + rec, vec, sizeof(GVec));
         bulk_commit();

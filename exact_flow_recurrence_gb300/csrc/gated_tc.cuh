@@ -23,7 +23,7 @@ struct GVec {
     float up[64];     // e^{c_i}
     float rest[64];   // e^{c_last - c_i}
     float al[64];     // alpha_i (0 past the sequence's end)
-    float chi[64];    // c_i = chi + clo
+    float chi[64];    // c_i / log 2 = chi + clo
     float clo[64];
 };
 

@@ -152,7 +152,7 @@ __device__ __forceinline__ bool group_sync_and(int id, bool pred, int count = 12
 // T = (I + A)^{-1} of a strictly lower triangular 64 x 64 A (fp32, row stride kLdA) by a
 // group of 128 threads (named barrier `bid`): the four 16x16 diagonal blocks by substitution,
 // then T21 = -T22 A21 T11 at the 32x32 and at the 64x64 level.  T (row stride kLd) is written
-// in and below its 16x16 diagonal blocks only; Y is [32][40] fp32 scratch.
+// in and below its 16x16 diagonal blocks only and may overwrite A; Y is [32][40] fp32 scratch.
 __device__ __forceinline__ void unit_lower_inverse64(const float* A, float* T, float* Y, int bid, int tid) {
     const int warp = tid >> 5, lane = tid & 31;
     if (tid < 64) {   // 4a. diagonal block b = tid >> 4, column cc = tid & 15: forward substitution
@@ -164,6 +164,7 @@ __device__ __forceinline__ void unit_lower_inverse64(const float* A, float* T, f
         for (int jj = 0; jj < 15; ++jj)
 #pragma unroll
             for (int i = jj + 1; i < 16; ++i) x[i] = fmaf(-A[(o + i) * kLdA + o + jj], x[jj], x[i]);
+        __syncwarp();   // (T may be A itself: a block's columns share a warp)
 #pragma unroll
         for (int i = 0; i < 16; ++i) T[(o + i) * kLd + o + cc] = x[i];
     }
