@@ -467,15 +467,16 @@ efla_status efla_get_status(cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(sync)");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status");
-    unsigned int word = 0, word2 = 0, word3 = 0, word4 = 0, word5 = 0, word6 = 0;
+    unsigned int word = 0, word2 = 0, word3 = 0, word4 = 0, word5 = 0, word6 = 0, word7 = 0;
     e = efla::tc_status_read_clear(&word);
     if (e == cudaSuccess) e = efla::proj_status_read_clear(&word2);
     if (e == cudaSuccess) e = efla::bt_status_read_clear(&word3);
     if (e == cudaSuccess) e = efla::gt_status_read_clear(&word4);
     if (e == cudaSuccess) e = efla::sd_status_read_clear(&word5);
     if (e == cudaSuccess) e = efla::gated_tc_status_read_clear(&word6);
+    if (e == cudaSuccess) e = efla::gated_bwd_tc_status_read_clear(&word7);
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(status word)");
-    word |= word2 | word3 | word4 | word5 | word6;
+    word |= word2 | word3 | word4 | word5 | word6 | word7;
     if (word & efla::kStatusBounds)
         return fail(EFLA_ERR_BOUNDS, "a debug-build bounds check skipped a global write (status 0x%x)", word);
     if (word) return fail(EFLA_ERR_TIMEOUT, "a bounded device-side wait expired (status 0x%x)", word);
@@ -682,7 +683,9 @@ size_t efla_gated_fwd_workspace_size(const efla_gated_shape* s) {
 size_t efla_gated_bwd_workspace_size(const efla_gated_shape* s) {
     efla::GDims d;
     if (check_gated(s, false, true, &d) != EFLA_OK) return 0;
-    return efla::gated_simt_bwd_ws_bytes(d);
+    const size_t simt = efla::gated_simt_bwd_ws_bytes(d);
+    const size_t tc = s->path != EFLA_PATH_SIMT && efla::gated_tc_supported(d) ? efla::gated_tc_bwd_ws_bytes(d) : 0;
+    return tc > simt ? tc : simt;
 }
 
 efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const void* q, const void* k, const void* v,
@@ -731,12 +734,12 @@ efla_status efla_gated_bwd(const efla_gated_shape* s, const int* offsets, const 
     efla::GDims d;
     efla_status st = check_gated(s, false, true, &d);
     if (st != EFLA_OK) return st;
-    if (s->path == EFLA_PATH_TENSOR) return fail(EFLA_ERR_UNSUPPORTED, "efla_gated_bwd: path must be AUTO or SIMT");
     if (d.BH() == 0) return EFLA_OK;
     GatedIo io = gated_io(s, q, k, v, g, beta, nullptr, dO, dq, dk, dv);
     io.x[5] = io.x[6];   // no o here: dO is the sixth input
     for (int i = 6; i < 9; ++i) io.x[i] = io.x[i + 1];
     if ((st = check_strided(io.x, 9, 6)) != EFLA_OK) return st;
+    if ((st = pick_gated_path(s, io.x, 9, &d)) != EFLA_OK) return st;
     const size_t sbytes = (size_t)d.BH() * d.dk * d.dv * 4, gbytes = (d.packed ? 1 : (size_t)d.B) * d.H * d.L * 4;
     const Span sS0{S0, sbytes, "S0"}, sdS{dS_final, sbytes, "dS_final"}, sd0{dS0, sbytes, "dS0"},
         sdg{dg, gbytes, "dg"}, sdb{dbeta, gbytes, "dbeta"}, sw{workspace, workspace_bytes, "workspace"},
@@ -755,12 +758,12 @@ efla_status efla_gated_bwd(const efla_gated_shape* s, const int* offsets, const 
             for (const Span& b : ins)
                 if (overlap(a, b)) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input %s", a.name, b.name);
     }
-    const size_t need = efla::gated_simt_bwd_ws_bytes(d);
+    const size_t need = d.tensor ? efla::gated_tc_bwd_ws_bytes(d) : efla::gated_simt_bwd_ws_bytes(d);
     if (need && (!workspace || workspace_bytes < need))
         return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
     efla::prof_mark(nullptr, stream);
-    const cudaError_t e = efla::launch_gated_bwd_simt(d, q, k, v, g, beta, S0, dO, dS_final, dq, dk, dv, dg, dbeta, dS0,
-                                                      workspace, stream);
+    const auto launch = d.tensor ? efla::launch_gated_bwd_tc : efla::launch_gated_bwd_simt;
+    const cudaError_t e = launch(d, q, k, v, g, beta, S0, dO, dS_final, dq, dk, dv, dg, dbeta, dS0, workspace, stream);
     return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_gated_bwd");
 }
 

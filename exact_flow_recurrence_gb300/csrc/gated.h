@@ -39,7 +39,13 @@ size_t gated_tc_fwd_ws_bytes(const GDims& d);
 cudaError_t launch_gated_fwd_tc(const GDims& d, const void* q, const void* k, const void* v, const float* g,
                                 const float* beta, const float* S0, void* o, float* S_final, void* ws,
                                 cudaStream_t st);
-// Reads and clears the kernels' device status word (synchronous).
+size_t gated_tc_bwd_ws_bytes(const GDims& d);
+cudaError_t launch_gated_bwd_tc(const GDims& d, const void* q, const void* k, const void* v, const float* g,
+                                const float* beta, const float* S0, const void* dO, const float* dS_final,
+                                void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dS0, void* ws,
+                                cudaStream_t st);
+// Read and clear the kernels' device status words (synchronous).
+cudaError_t gated_bwd_tc_status_read_clear(unsigned int* status);
 cudaError_t gated_tc_status_read_clear(unsigned int* status);
 
 // ------------------------------------------------------------------- decode (gated_step.cu)

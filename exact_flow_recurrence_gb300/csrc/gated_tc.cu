@@ -32,6 +32,7 @@ struct PrepArgs {
     unsigned char* img;   // [H][slots][NP][128 rows x 128 bytes]
     GVec* vec;            // [H][slots]
     int slots;
+    float floor_alpha;    // |alpha| below this is taken as it (0: as it is)
 };
 
 template <int NP>
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
 #pragma unroll
             for (int j = 0; j < 64; ++j) lam = j == i ? v[j] : lam;
             scale = i < n ? alpha_of(beta, lam, d.euler) : 0.f;
+            if (i < n && fabsf(scale) < a.floor_alpha) scale = a.floor_alpha;
             vec->al[i] = scale;
         }
         const int diag = tid < 64 ? i : i + 1;   // columns below this are kept
@@ -265,26 +267,12 @@ struct ScanArgs {
     void* o;
     float* S_final;
     int slots;
+    float* rec_S;   // [H][slots][dk][dv]
+    float* rec_U;   // [H][slots][64][dv]
 };
 
-template <typename Tout>
-__device__ __forceinline__ void st16(Tout* p, const float* x);   // 16 values to 16-byte aligned memory
-template <>
-__device__ __forceinline__ void st16<float>(float* p, const float* x) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-}
-template <>
-__device__ __forceinline__ void st16<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-        uint4 w[1];
-        split8<1>(x + i, w);
-        *reinterpret_cast<uint4*>(p + i) = w[0];
-    }
-}
-
-template <int NP, int N, typename Tout>
+// REC: the backward's pass, which writes no o but records every chunk's entering state and U (fp32).
+template <int NP, int N, typename Tout, bool REC>
 __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, const __grid_constant__ CUtensorMap tm_q,
                                                            const __grid_constant__ CUtensorMap tm_k,
                                                            const __grid_constant__ CUtensorMap tm_v) {
@@ -476,6 +464,12 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                         make_uint4(0u, 0u, 0u, 0u);
             }
             arrive(s_ready);
+            if (REC && row < d.dk) {
+                float* rs = a.rec_S + ((rec0 + c) * d.dk + row) * d.dv + c0 + cc;
+#pragma unroll
+                for (int e = 0; e < NC; e += 16)
+                    if (e < nv) st16(rs + e, S + e);
+            }
             ok = ok && wait(&full[c & 1], (c >> 1) & 1);
             if (!ok) break;
             const float up = vec->up[i], last = vec->up[63];
@@ -512,6 +506,12 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                     put(M::X, 8192, i, e, x);
                 }
                 arrive(u_ready);
+                if (REC) {
+                    float* ru = a.rec_U + ((rec0 + c) * kGC + i) * d.dv + c0 + cc;
+#pragma unroll
+                    for (int e = 0; e < NC; e += 16)
+                        if (e < nv) st16(ru + e, y + e);
+                }
             } else {
                 if (!(ok = wait(d1, ph))) break;
                 tc_fence_after();
@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                 if (!(ok = wait(d2, ph))) break;
                 tc_fence_after();
                 float z[NC];
-                get(t2, z);
-                if (i < n) {
+                if (!REC) get(t2, z);
+                if (!REC && i < n) {
                     Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + c0 + cc;
 #pragma unroll
                     for (int e = 0; e < NC; ++e) y[e] = fmaf(up, y[e], z[e]);
@@ -564,11 +564,6 @@ size_t carve(const GDims& d, int np, void* base, TcWs* w) {
     return (size_t)(p - (char*)base);
 }
 
-template <typename K>
-cudaError_t smem_attr(K k, size_t bytes) {
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 struct Maps {
     CUtensorMap q, k, v;
 };
@@ -581,13 +576,22 @@ cudaError_t make_maps(const GDims& d, const void* q, const void* k, const void* 
     return e;
 }
 
-template <int NP, int N, typename Tout>
+template <int NP, int N, typename Tout, bool REC = false>
 cudaError_t scan(const GDims& d, const ScanArgs& a, const Maps& m, cudaStream_t st) {
     constexpr size_t bytes = ScanSmem<NP, N>::bytes;
-    cudaError_t e = smem_attr(k_gt_scan<NP, N, Tout>, bytes);
+    cudaError_t e = smem_attr(k_gt_scan<NP, N, Tout, REC>, bytes);
     if (e != cudaSuccess) return e;
-    k_gt_scan<NP, N, Tout><<<dim3((unsigned)d.BH(), (d.dv + N - 1) / N), kScThreads, bytes, st>>>(d, a, m.q, m.k, m.v);
-    prof_mark("gated_scan_tc", st);
+    k_gt_scan<NP, N, Tout, REC><<<dim3((unsigned)d.BH(), (d.dv + N - 1) / N), kScThreads, bytes, st>>>(d, a, m.q, m.k, m.v);
+    prof_mark(REC ? "gated_record_tc" : "gated_scan_tc", st);
+    return cudaGetLastError();
+}
+
+template <int NP>
+cudaError_t prep(const GDims& d, const PrepArgs& a, const Maps& m, cudaStream_t st) {
+    cudaError_t e = smem_attr(k_gt_prep<NP>, PrepSmem<NP>::bytes);
+    if (e != cudaSuccess) return e;
+    k_gt_prep<NP><<<dim3(a.slots, d.H), 128, PrepSmem<NP>::bytes, st>>>(d, a, m.q, m.k);
+    prof_mark("gated_prep_tc", st);
     return cudaGetLastError();
 }
 
@@ -598,21 +602,13 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
     carve(d, NP, ws, &w);
     Maps m{};
     const int slots = d.slots(kGC);
+    bool narrow = false;
     cudaError_t e = make_maps(d, q, k, v, &m);
-    if (e == cudaSuccess) e = smem_attr(k_gt_prep<NP>, PrepSmem<NP>::bytes);
+    if (e == cudaSuccess) e = narrow_slices(d, &narrow);
+    if (e == cudaSuccess) e = prep<NP>(d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f}, m, st);
     if (e != cudaSuccess) return e;
-    const PrepArgs pa{g, beta, w.img, w.vec, slots};
-    k_gt_prep<NP><<<dim3(slots, d.H), 128, PrepSmem<NP>::bytes, st>>>(d, pa, m.q, m.k);
-    prof_mark("gated_prep_tc", st);
-    int dev = 0, nsm = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    const ScanArgs a{w.img, w.vec, S0, o, S_final, slots};
-    // narrower slices while they still find an SM each: a chunk's products and epilogues shorten
-    // with the columns, but every slice loads the keys, queries and images again
-    if (2 * d.BH() * ((d.dv + 63) / 64) <= nsm) return scan<NP, 32, Tout>(d, a, m, st);
-    return scan<NP, 64, Tout>(d, a, m, st);
+    const ScanArgs a{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr};
+    return narrow ? scan<NP, 32, Tout>(d, a, m, st) : scan<NP, 64, Tout>(d, a, m, st);
 }
 
 }  // namespace
@@ -631,6 +627,28 @@ cudaError_t launch_gated_fwd_tc(const GDims& d, const void* q, const void* k, co
     if (!d.out_bf16) return fwd<3, float>(d, q, k, v, g, beta, S0, o, S_final, ws, st);
     return S_final ? fwd<3, __nv_bfloat16>(d, q, k, v, g, beta, S0, o, S_final, ws, st)
                    : fwd<2, __nv_bfloat16>(d, q, k, v, g, beta, S0, o, S_final, ws, st);
+}
+
+cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
+                                 float floor_alpha, unsigned char* img, GVec* vec, cudaStream_t st) {
+    Maps m{};
+    const int nb = d.packed ? 1 : d.B;
+    cudaError_t e = strided_rows_map(&m.q, q, d.dk, d.L, d.Hk, nb, d.qs);
+    if (e == cudaSuccess) e = strided_rows_map(&m.k, k, d.dk, d.L, d.Hk, nb, d.ks);
+    if (e != cudaSuccess) return e;
+    return prep<3>(d, PrepArgs{g, beta, img, vec, d.slots(kGC), floor_alpha}, m, st);
+}
+
+cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
+                                   const unsigned char* img, const GVec* vec, float* rec_S, float* rec_U,
+                                   cudaStream_t st) {
+    Maps m{};
+    bool narrow = false;
+    cudaError_t e = make_maps(d, q, k, v, &m);
+    if (e == cudaSuccess) e = narrow_slices(d, &narrow);
+    if (e != cudaSuccess) return e;
+    const ScanArgs a{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U};
+    return narrow ? scan<3, 32, float, true>(d, a, m, st) : scan<3, 64, float, true>(d, a, m, st);
 }
 
 cudaError_t gated_tc_status_read_clear(unsigned int* status) {

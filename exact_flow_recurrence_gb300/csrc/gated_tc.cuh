@@ -55,6 +55,23 @@ __device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
     }
 }
 
+template <typename Tout>
+__device__ __forceinline__ void st16(Tout* p, const float* x);   // 16 values to 16-byte aligned memory
+template <>
+__device__ __forceinline__ void st16<float>(float* p, const float* x) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+}
+template <>
+__device__ __forceinline__ void st16<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+        uint4 w[1];
+        split8<1>(x + i, w);
+        *reinterpret_cast<uint4*>(p + i) = w[0];
+    }
+}
+
 // Tensor map of a strided bf16 [batch][head][token][d] array: boxes of 64 tokens x 64 columns
 // with the 128-byte swizzle; elements outside read as zero.
 inline cudaError_t strided_rows_map(CUtensorMap* m, const void* base, int d, int L, int heads, int batch,
@@ -79,5 +96,28 @@ inline cudaError_t strided_rows_map(CUtensorMap* m, const void* base, int d, int
                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+template <typename K>
+inline cudaError_t smem_attr(K k, size_t bytes) {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// Whether slices of 32 state columns (instead of 64) still find an SM each: a chunk's products and
+// epilogues shorten with the columns, but every slice loads the keys, queries and images again.
+inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
+    int dev = 0, nsm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    *narrow = 2 * d.BH() * ((d.dv + 63) / 64) <= nsm;
+    return e;
+}
+
+// The backward's parts of gated_tc.cu: the preparation (three parts; alpha at least `floor_alpha`
+// in magnitude), and the pass that records S [H][slots][dk][dv] and U [H][slots][64][dv] (fp32).
+cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
+                                 float floor_alpha, unsigned char* img, GVec* vec, cudaStream_t st);
+cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
+                                   const unsigned char* img, const GVec* vec, float* rec_S, float* rec_U,
+                                   cudaStream_t st);
 
 }  // namespace efla
