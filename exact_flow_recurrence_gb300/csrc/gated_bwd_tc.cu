@@ -154,20 +154,20 @@ __global__ void __launch_bounds__(kRsThreads, 1) k_gt_rscan(GDims d, RscanArgs a
                 // what does not wait for K G: (P T)^T dO (rows 64..127 of the image, 8 KB in) ...
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_ss(t2, dT + 512 + ks * 128, dDO + ks * 128, idesc_f16(128, N, true, true, true), ks > 0);
+                    mma_f16_ss(t2, dT + (NP - 1) * 1024 + 512 + ks * 128, dDO + ks * 128, idesc_f16(128, N, true, true, true), ks > 0);
 #pragma unroll
-                for (int p = 1; p < NP; ++p)
+                for (int p = NP - 2; p >= 0; --p)   // (small parts first: the accumulator cuts off, it does not round)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_f16_ss(t2, dT + p * 1024 + 512 + ks * 128, dDO + ks * 128, idesc_f16(128, N, true, true, true), 1u);
                 // ... and Q^T E (rows 64..127 of [K; Q])
                 if constexpr (G3 == 1) {
 #pragma unroll
-                    for (int p = 0; p < NP; ++p)
+                    for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             mma_f16_ss(t3, kqM + 512 + ks * 128, dE + p * 512 + ks * 128, idesc_f16(128, N, true, true, true),
-                                       p + ks > 0);
+                                       p < NP - 1 || ks > 0);
                 } else {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kRsThreads, 1) k_gt_rscan(GDims d, RscanArgs a
                 if (it + 1 < nch) load_tp(it + 1);   // (D2 is done: z_ready came from it)
                 if constexpr (G3 == 1) {
 #pragma unroll
-                    for (int p = 0; p < NP; ++p)
+                    for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             mma_f16_ss(t3, kqM + ks * 128, dX + p * 512 + ks * 128, idesc_f16(128, N, true, true, true), 1u);
@@ -379,7 +379,8 @@ constexpr uint32_t kGrS = kGrU + 24576;          // 3 x [128 dk rows][64]; then 
 constexpr uint32_t kGrG = kGrS + 49152;          // 3 x [128 dk rows][64]
 constexpr uint32_t kGrMisc = kGrG + 49152;
 constexpr uint32_t kGrZero = kGrAX + 16384;      // a tile of zeros
-constexpr uint32_t cDa = 0, cD6 = 128, cD3 = 256, cD4 = 320, cD5 = 384;   // tensor-memory columns
+// tensor-memory columns; D5 lies over D3 and D3s (the small part pairs of D3), which are read before it starts
+constexpr uint32_t cDa = 0, cD6 = 128, cD3 = 256, cD3s = 320, cD5 = 256, cD4 = 384;
 
 struct GrMisc {
     GVec vec;
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) k_gt_grad(GDims d, GradArgs a) 
                 const uint64_t ax = sdesc_sw128(smem_u32(sm + kGrAX)), us = sdesc_sw128(smem_u32(sm + kGrU)),
                                ss = sdesc_sw128(smem_u32(sm + kGrS)), gs = sdesc_sw128(smem_u32(sm + kGrG)),
                                qk = sdesc_sw128(smem_u32(sm + kGrQK));
-                if (sl == 0 && h == hk * rep) {
+                if (sl == 0) {
 #pragma unroll 1
                     for (int blk = 0; blk < nblk; ++blk)
 #pragma unroll
@@ -547,30 +548,34 @@ __global__ void __launch_bounds__(kGrThreads, 1) k_gt_grad(GDims d, GradArgs a) 
                             mma_f16_ss(tb + cD4, qk + blk * 1024 + ks * 2, qk + 512 + blk * 1024 + ks * 2,
                                        idesc_f16(128, 64, false, false, true), blk + ks > 0);
                 }
+                // The accumulators cut off what falls below their last bit, at every instruction: the
+                // small part pairs go first (and, for dbeta's D3, into columns of their own), so that
+                // few of them meet a large sum.
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
+                for (int o = NP - 1; o >= 0; --o)   // pairs (p, y) of order o = p + y
 #pragma unroll
-                    for (int y = 0; y + p < NP; ++y)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cD3, ax + p * 1024 + ks * 2, us + y * 512 + ks * 2,
-                                       idesc_f16(128, 64, false, false, true), sl > 0 || p + y + ks > 0);
-#pragma unroll
-                for (int p = 0; p < NP; ++p)
-#pragma unroll
-                    for (int y = 0; y + p < NP; ++y)
+                    for (int p = 0; p <= o; ++p)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cDa, ax + p * 1024 + ks * 2, ss + y * 1024 + ks * 2,
-                                       idesc_f16(128, 128, false, false, true), sl > 0 || p + y + ks > 0);
+                            mma_f16_ss(tb + (o ? cD3s : cD3), ax + p * 1024 + ks * 2, us + (o - p) * 512 + ks * 2,
+                                       idesc_f16(128, 64, false, false, true),
+                                       sl > 0 || !((o == NP - 1 || o == 0) && p == 0 && ks == 0));
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
+                for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
-                    for (int y = 0; y + p < NP; ++y)
+                    for (int p = 0; p <= o; ++p)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cD6, us + p * 512 - 512 + ks * 2, gs + y * 1024 + ks * 2,
-                                       idesc_f16(128, 128, false, false, true), sl > 0 || p + y + ks > 0);
+                            mma_f16_ss(tb + cDa, ax + p * 1024 + ks * 2, ss + (o - p) * 1024 + ks * 2,
+                                       idesc_f16(128, 128, false, false, true), sl > 0 || !(o == NP - 1 && p == 0 && ks == 0));
+#pragma unroll
+                for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                    for (int p = 0; p <= o; ++p)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ss(tb + cD6, us + p * 512 - 512 + ks * 2, gs + (o - p) * 1024 + ks * 2,
+                                       idesc_f16(128, 128, false, false, true), sl > 0 || !(o == NP - 1 && p == 0 && ks == 0));
                 mma_commit(&m.bar);
             }
             done();
@@ -580,10 +585,14 @@ __global__ void __launch_bounds__(kGrThreads, 1) k_gt_grad(GDims d, GradArgs a) 
         {
             float y[16], z[16], w[16], col[16];
             tmem_ld16(taddr(tb, lq, cD3 + 16 * cg), y);
+            tmem_ld16(taddr(tb, lq, cD3s + 16 * cg), w);
             tmem_ld16(taddr(tb, lq, cD4 + 16 * cg), z);
             tmem_ld_wait();
             loaded16(y);
+            loaded16(w);
             loaded16(z);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] += w[e];
             const float chi = m.vec.chi[i], clo = m.vec.clo[i], al = m.vec.al[i];
             float rsum = 0.f;
 #pragma unroll
