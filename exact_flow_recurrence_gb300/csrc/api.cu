@@ -467,7 +467,7 @@ efla_status efla_get_status(cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(sync)");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status");
-    unsigned int word = 0, word2 = 0, word3 = 0, word4 = 0, word5 = 0, word6 = 0, word7 = 0;
+    unsigned int word = 0, word2 = 0, word3 = 0, word4 = 0, word5 = 0, word6 = 0, word7 = 0, word8 = 0;
     e = efla::tc_status_read_clear(&word);
     if (e == cudaSuccess) e = efla::proj_status_read_clear(&word2);
     if (e == cudaSuccess) e = efla::bt_status_read_clear(&word3);
@@ -475,8 +475,9 @@ efla_status efla_get_status(cudaStream_t stream) {
     if (e == cudaSuccess) e = efla::sd_status_read_clear(&word5);
     if (e == cudaSuccess) e = efla::gated_tc_status_read_clear(&word6);
     if (e == cudaSuccess) e = efla::gated_bwd_tc_status_read_clear(&word7);
+    if (e == cudaSuccess) e = efla::norm_status_read_clear(&word8);
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(status word)");
-    word |= word2 | word3 | word4 | word5 | word6 | word7;
+    word |= word2 | word3 | word4 | word5 | word6 | word7 | word8;
     if (word & efla::kStatusBounds)
         return fail(EFLA_ERR_BOUNDS, "a debug-build bounds check skipped a global write (status 0x%x)", word);
     if (word) return fail(EFLA_ERR_TIMEOUT, "a bounded device-side wait expired (status 0x%x)", word);

@@ -66,4 +66,7 @@ cudaError_t launch_norm_fwd(const NormDims& d, const void* x, const void* w, con
 cudaError_t launch_norm_bwd(const NormDims& d, const void* x, const void* w, const void* dy, const float* stats,
                             void* dx, void* dw, void* db, void* ws, cudaStream_t st);
 
+// Reads and clears the kernels' device status word (synchronous).
+cudaError_t norm_status_read_clear(unsigned int* status);
+
 }  // namespace efla

@@ -8,14 +8,16 @@
 // pass over registers, not over memory, and no difference of large sums).  Statistics, sums and
 // the weight's gradient are fp32.
 //
-// Forward: up to 2048 elements a row belong to one warp, so that a row needs shuffles only and
-// an SM has some thirty rows in flight; longer rows to 4 to 32 warps.  Backward: 16 elements a
-// thread (dw and db stay in registers over all rows of a CTA), 32 beyond 8192; the next row is
-// loaded while the present one is reduced.  A second kernel adds the CTAs' partial sums in a
-// fixed order, so that results do not depend on the order in which CTAs finish.
+// A CTA (one an SM) walks rows CTA, CTA + grid, ...; 16 elements a thread, so that weight and bias
+// (forward) or weight and the sums of dw and db (backward) stay in its registers over all its rows.
+// Rows arrive by bulk copies into a ring of shared memory, several ahead: what an SM has in flight
+// then costs no registers.  Rows that are not 16-byte aligned are loaded element by element.
+// A second kernel adds the CTAs' partial sums in a fixed order, so that results do not depend on
+// the order in which CTAs finish.
 #include "common.cuh"
 #include "gated.h"
 #include "launch.h"
+#include "tc_common.cuh"
 
 namespace efla {
 
@@ -90,172 +92,249 @@ __device__ __forceinline__ void weights(const void* w, int c, int bf16, float* x
     }
 }
 
-__device__ __forceinline__ void bar_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
+// two fp32 values an instruction
+__device__ __forceinline__ uint64_t u64(float2 a) { return *reinterpret_cast<const uint64_t*>(&a); }
+__device__ __forceinline__ float2 f2(uint64_t a) { return *reinterpret_cast<const float2*>(&a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)), "l"(u64(c)));
+    return f2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+    return f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+    return f2(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// Sums over the W warps of a row; `red` has room for W pairs and is not in use by an earlier sum
-// that a warp of this row may still be reading.
-template <int W>
+__device__ unsigned int g_nm_status = 0;   // bit 0: a bounded wait expired
+
+// Sums over the W warps of a row (of s.x alone, or of both); `red` has room for W pairs and is not
+// in use by an earlier sum that a warp of this row may still be reading.
+template <int W, bool TWO>
 __device__ __forceinline__ float2 row_sum(float2 s, float2* red, int bar, int warp_in_row) {
     s.x = warp_sum(s.x);
-    s.y = warp_sum(s.y);
+    if (TWO) s.y = warp_sum(s.y);
     if (W == 1) return s;
     if ((threadIdx.x & 31) == 0) red[warp_in_row] = s;
-    bar_sync(bar, 32 * W);
+    group_sync(bar, 32 * W);
     float2 r = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         r.x += red[i].x;
-        r.y += red[i].y;
+        if (TWO) r.y += red[i].y;
     }
     return r;
 }
 
-// W warps a row, NV vectors a lane.
-template <typename T, int VEC, int NV, int W>
-__global__ void __launch_bounds__(W < 8 ? 256 : 32 * W) k_norm_fwd(NormDims d, const T* x, const void* w, const void* b,
-                                                                   T* y, float* stats) {
-    constexpr int RPC = W < 8 ? 8 / W : 1;   // rows a CTA
-    __shared__ float2 red[RPC][2][W];
-    const int row = threadIdx.x / (32 * W), t = threadIdx.x % (32 * W), wr = t >> 5;
-    const long long r = (long long)blockIdx.x * RPC + row;
-    if (r >= d.rows) return;   // (whole rows, so whole barriers)
-    Pack<T, VEC> v[NV];
-#pragma unroll
-    for (int m = 0; m < NV; ++m) {
-        const int c = (m * 32 * W + t) * VEC;
-        if (c < d.D) v[m].load(x + r * d.x_stride + c);
-        else v[m].zero();
-    }
-    float f[VEC];
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int m = 0; m < NV; ++m) {
-        v[m].get(f);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s.x += f[i];
-    }
-    const float inv = 1.f / (float)d.D;
-    const float mean = row_sum<W>(s, red[row][0], row + 1, wr).x * inv;
-    s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int m = 0; m < NV; ++m) {
-        if ((m * 32 * W + t) * VEC < d.D) {
-            v[m].get(f);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s.x = fmaf(f[i] - mean, f[i] - mean, s.x);
-        }
-    }
-    const float rstd = 1.f / sqrtf(row_sum<W>(s, red[row][1], row + 1, wr).x * inv + d.eps);
-#pragma unroll
-    for (int m = 0; m < NV; ++m) {
-        const int c = (m * 32 * W + t) * VEC;
-        if (c < d.D) {
-            float wf[VEC], bf[VEC];
-            weights<VEC>(w, c, d.w_bf16, wf);
-            v[m].get(f);
-            if (b) {
-                weights<VEC>(b, c, d.w_bf16, bf);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[i] = fmaf((f[i] - mean) * rstd, wf[i], bf[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[i] = (f[i] - mean) * rstd * wf[i];
-            }
-            v[m].set(f);
-            v[m].store(y + r * d.y_stride + c);
-        }
-    }
-    if (t == 0) *reinterpret_cast<float2*>(stats + 2 * r) = make_float2(mean, rstd);
-}
+// Threads a CTA: what the registers of 16 elements a thread allow.
+template <int W, int SP, bool BWD>
+struct Cta {
+    static constexpr int threads = BWD || W > 8 || SP > 16 ? 512 : 768;
+};
+constexpr int kStages = 6;       // most stages of a ring
+constexpr size_t kRing = 160 * 1024;
 
-// W warps a row, 16 / W rows at a time in a CTA of 512 threads; NV vectors a lane.
-template <typename T, int VEC, int NV, int W>
-__global__ void __launch_bounds__(512, 1) k_norm_bwd(NormDims d, const T* x, const void* w, const T* dy,
-                                                     const float* stats, T* dx, float* part, int want_db) {
-    constexpr int RPC = 16 / W, SP = NV * VEC;
-    __shared__ float2 red[RPC][2][W];
-    extern __shared__ float comb[];   // [D] when rows share a CTA
-    const int row = threadIdx.x / (32 * W), t = threadIdx.x % (32 * W), wr = t >> 5;
-    const float inv = 1.f / (float)d.D;
-    const long long step = (long long)gridDim.x * RPC;
-    float aw[SP], ab[SP];
-#pragma unroll
-    for (int i = 0; i < SP; ++i) aw[i] = ab[i] = 0.f;
-    Pack<T, VEC> xv[NV], gv[NV];
-    float2 st = make_float2(0.f, 0.f);
-    const auto fetch = [&](long long r) {
-        if (r < d.rows) st = __ldg(reinterpret_cast<const float2*>(stats + 2 * r));
-#pragma unroll
-        for (int m = 0; m < NV; ++m) {
-            const int c = (m * 32 * W + t) * VEC;
-            if (r < d.rows && c < d.D) {
-                xv[m].load(x + r * d.x_stride + c);
-                gv[m].load(dy + r * d.y_stride + c);
-            }
-        }
-    };
-    long long r = (long long)blockIdx.x * RPC + row;
-    fetch(r);
-    for (int it = 0; r < d.rows; r += step, it ^= 1) {
-        float z[SP], p[SP];
-        const float mean = st.x, rstd = st.y;
-        float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int m = 0; m < NV; ++m) {
-            const int c = (m * 32 * W + t) * VEC;
-            if (c < d.D) {
-                float wf[VEC];
-                weights<VEC>(w, c, d.w_bf16, wf);
-                xv[m].get(z + m * VEC);
-                gv[m].get(p + m * VEC);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int e = m * VEC + i;
-                    z[e] = (z[e] - mean) * rstd;
-                    aw[e] = fmaf(p[e], z[e], aw[e]);
-                    ab[e] += p[e];
-                    p[e] *= wf[i];
-                    s.x += p[e];
-                    s.y = fmaf(p[e], z[e], s.y);
-                }
-            }
-        }
-        fetch(r + step);   // in flight over the reduction and the stores
-        s = row_sum<W>(s, red[row][it], row + 1, wr);
-        s.x *= inv;
-        s.y *= inv;
-#pragma unroll
-        for (int m = 0; m < NV; ++m) {
-            const int c = (m * 32 * W + t) * VEC;
-            if (c < d.D) {
-                Pack<T, VEC> o;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int e = m * VEC + i;
-                    p[e] = rstd * (p[e] - s.x - z[e] * s.y);
-                }
-                o.set(p + m * VEC);
-                o.store(dx + r * d.D + c);
-            }
+// One row group's ring: `arrays` rows a stage, each `bytes` long.
+struct Ring {
+    unsigned char* buf;
+    uint64_t* full;   // [stages]
+    uint32_t bytes;
+    int stages, arrays, stage, phase;
+    __device__ __forceinline__ unsigned char* row(int which) const { return buf + (size_t)(stage * arrays + which) * bytes; }
+    // one thread: copies for the row after next use of stage `to`
+    __device__ __forceinline__ void issue(int to, const void* x, const void* g) const {
+        mbar_arrive_expect_tx(&full[to], bytes * arrays);
+        bulk_g2s(buf + (size_t)to * arrays * bytes, x, bytes, &full[to]);
+        if (arrays == 2) bulk_g2s(buf + (size_t)(to * 2 + 1) * bytes, g, bytes, &full[to]);
+    }
+    __device__ __forceinline__ bool wait() const { return mbar_wait(&full[stage], phase, kWaitLimit); }
+    __device__ __forceinline__ void next() {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
         }
     }
+};
+
+// W warps a row, NV vectors a lane; as many rows at a time as the CTA has groups of W warps.
+template <typename T, int VEC, int NV, int W, bool BWD>
+__global__ void __launch_bounds__((Cta<W, NV * VEC, BWD>::threads), 1) k_norm(NormDims d, const T* x, const void* w, const void* b, const T* dy,
+                                                  T* y, float* stats, float* part, int want_db, int stages) {
+    constexpr int SP = NV * VEC, RPC = Cta<W, SP, BWD>::threads / 32 / W;
+    constexpr bool RING = VEC > 1;
+    __shared__ float2 red[RPC][2][W];
+    __shared__ uint64_t full[RPC][kStages];
+    extern __shared__ __align__(128) unsigned char dyn[];   // the rings; at the end [D] fp32 sums of the CTA's rows
+    const int grp = threadIdx.x / (32 * W), t = threadIdx.x % (32 * W), wr = t >> 5;
+    const float inv = 1.f / (float)d.D;
+    const long long step = (long long)gridDim.x * RPC, r0 = (long long)blockIdx.x * RPC + grp;
+    Ring ring{dyn, full[grp], (uint32_t)(d.D * sizeof(T)), stages, BWD ? 2 : 1, 0, 0};
+    long long ahead = r0;   // the next row to copy
+    if (RING) {
+        ring.buf += (size_t)grp * stages * ring.arrays * ring.bytes;
+        if (threadIdx.x < RPC * stages) mbar_init(&full[threadIdx.x / stages][threadIdx.x % stages], 1);
+        if (threadIdx.x == 0) fence_mbar_init();
+        __syncthreads();
+        for (int i = 0; i < stages && ahead < d.rows; ++i, ahead += step)
+            if (t == 0) ring.issue(i, x + ahead * d.x_stride, BWD ? dy + ahead * d.y_stride : nullptr);
+    }
+    // forward: weight and bias; backward: weight, and this thread's columns of dw and db
+    constexpr int H = SP / 2;
+    float2 wv[H], u[H], v[BWD ? H : 1];
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        const int c = (m * 32 * W + t) * VEC;
+        float wf[VEC], bf[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) wf[i] = bf[i] = 0.f;
+        if (c < d.D) {
+            weights<VEC>(w, c, d.w_bf16, wf);
+            if (!BWD && b) weights<VEC>(b, c, d.w_bf16, bf);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int e = m * VEC + i;
+            (e & 1 ? wv[e / 2].y : wv[e / 2].x) = wf[i];
+            (e & 1 ? u[e / 2].y : u[e / 2].x) = bf[i];
+        }
+    }
+    if (BWD)
+#pragma unroll
+        for (int e = 0; e < H; ++e) v[BWD ? e : 0] = make_float2(0.f, 0.f);
+    int it = 0;
+    bool ok = true;
+    float2 st_next = make_float2(0.f, 0.f);
+    if (BWD && r0 < d.rows) st_next = __ldg(reinterpret_cast<const float2*>(stats + 2 * r0));
+    for (long long r = r0; r < d.rows; r += step, it ^= 1) {
+        float2 z[H], p[BWD ? H : 1];
+        float2 st = st_next;
+        if (BWD && r + step < d.rows) st_next = __ldg(reinterpret_cast<const float2*>(stats + 2 * (r + step)));
+        if (RING && ok) ok = ring.wait();   // (after a wait that gave up the rows run on, without copies: barriers stay whole)
+        // columns past D count as the mean (forward) or as a zero gradient (backward)
+        const auto get = [&](int which, const T* from, float2* to) {
+#pragma unroll
+            for (int m = 0; m < NV; ++m) {
+                const int c = (m * 32 * W + t) * VEC;
+                Pack<T, VEC> q;
+                float f[VEC];
+                q.zero();
+                if (c < d.D) {
+                    if (RING) q = *reinterpret_cast<const Pack<T, VEC>*>(ring.row(which) + c * sizeof(T));
+                    else q.load(from + c);
+                }
+                q.get(f);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int e = m * VEC + i;
+                    (e & 1 ? to[e / 2].y : to[e / 2].x) = f[i];
+                }
+            }
+        };
+        get(0, x + r * d.x_stride, z);
+        if (BWD) get(1, dy + r * d.y_stride, p);
+        float2 s = make_float2(0.f, 0.f), s2 = s;
+        if (BWD) {
+            const float2 rs = both(st.y), off = both(-st.x * st.y);
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                const float2 g = p[BWD ? e : 0];
+                z[e] = fma2(z[e], rs, off);
+                u[e] = fma2(g, z[e], u[e]);
+                v[BWD ? e : 0] = add2(v[BWD ? e : 0], g);
+                const float2 q = mul2(g, wv[e]);
+                p[BWD ? e : 0] = q;
+                s = add2(s, q);
+                s2 = fma2(q, z[e], s2);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) s = add2(s, z[e]);
+        }
+        s = row_sum<W, BWD>(make_float2(s.x + s.y, s2.x + s2.y), red[grp][BWD ? it : 0], grp + 1, wr);
+        if (RING) {   // every thread of the row has read the stage
+            if (W == 1) __syncwarp();
+            if (t == 0 && ok && ahead < d.rows) ring.issue(ring.stage, x + ahead * d.x_stride, BWD ? dy + ahead * d.y_stride : nullptr);
+            ahead += step;
+            ring.next();
+        }
+        T* out = y + r * (BWD ? (long long)d.D : d.y_stride);
+        if (BWD) {   // rstd p - rstd mean(p) - xh rstd mean(p xh)
+            const float2 rs = both(st.y), a = both(-st.y * s.x * inv), c = both(-st.y * s.y * inv);
+#pragma unroll
+            for (int e = 0; e < H; ++e) z[e] = fma2(z[e], c, fma2(p[BWD ? e : 0], rs, a));
+        } else {
+            st.x = s.x * inv;
+            const float2 mean = both(-st.x);
+            s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int m = 0; m < NV; ++m) {
+                const bool in = (m * 32 * W + t) * VEC < d.D;
+                if constexpr (VEC > 1) {
+#pragma unroll
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        float2& q = z[m * VEC / 2 + i];
+                        q = add2(q, mean);
+                        if (in) s = fma2(q, q, s);
+                    }
+                } else {
+                    float& q = m & 1 ? z[m / 2].y : z[m / 2].x;
+                    q -= st.x;
+                    if (in) s.x = fmaf(q, q, s.x);
+                }
+            }
+            st.y = 1.f / sqrtf(row_sum<W, false>(make_float2(s.x + s.y, 0.f), red[grp][1], grp + 1, wr).x * inv + d.eps);
+            if (t == 0) *reinterpret_cast<float2*>(stats + 2 * r) = st;
+            const float2 rs = both(st.y);
+#pragma unroll
+            for (int e = 0; e < H; ++e) z[e] = fma2(mul2(z[e], rs), wv[e], u[e]);
+        }
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int c = (m * 32 * W + t) * VEC;
+            float f[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int e = m * VEC + i;
+                f[i] = e & 1 ? z[e / 2].y : z[e / 2].x;
+            }
+            Pack<T, VEC> o;
+            o.set(f);
+            if (c < d.D) o.store(out + c);
+        }
+    }
+    if (!ok) {   // the copies under way land before the CTA ends (a stage's copy completes either phase)
+        atomicOr(&g_nm_status, 1u);
+        if (t == 0)
+            for (int i = 0; i < stages; ++i) mbar_wait(&full[grp][i], i < ring.stage ? ring.phase ^ 1 : ring.phase, kWaitLimit);
+    }
+    if (!BWD) return;
+    griddep_launch_dependents();
     // the CTA's rows together, one group after another in order, then out as one partial row
+    float* comb = (float*)dyn;
     float* pw = part + (size_t)blockIdx.x * (want_db ? 2 : 1) * d.D;
 #pragma unroll 1
     for (int what = 0; what < (want_db ? 2 : 1); ++what) {
 #pragma unroll 1
         for (int k = 0; k < RPC; ++k) {
-            if (RPC > 1) __syncthreads();
-            if (row == k) {
+            __syncthreads();
+            if (grp == k) {
 #pragma unroll
                 for (int m = 0; m < NV; ++m) {
                     const int c = (m * 32 * W + t) * VEC;
                     if (c < d.D)
 #pragma unroll
                         for (int i = 0; i < VEC; ++i) {
-                            const float v = (what ? ab : aw)[m * VEC + i] + (k ? comb[c + i] : 0.f);
-                            if (k + 1 < RPC) comb[c + i] = v;
-                            else pw[(size_t)what * d.D + c + i] = v;
+                            const int e = m * VEC + i;
+                            const float2 h = what ? v[BWD ? e / 2 : 0] : u[e / 2];
+                            const float q = (e & 1 ? h.y : h.x) + (k ? comb[c + i] : 0.f);
+                            if (k + 1 < RPC) comb[c + i] = q;
+                            else pw[(size_t)what * d.D + c + i] = q;
                         }
                 }
             }
@@ -270,6 +349,7 @@ __global__ void __launch_bounds__(1024) k_norm_dw(int D, int w_bf16, int n, int 
     const size_t ld = (size_t)(two ? 2 : 1) * D;
     const float* p = part + (size_t)blockIdx.y * D + c;
     float s = 0.f;
+    griddep_wait();   // (launched while the rows' kernel still runs)
     if (c < D) {
 #pragma unroll 5
         for (int r = g; r < n; r += 32) s += p[r * ld];
@@ -285,81 +365,56 @@ __global__ void __launch_bounds__(1024) k_norm_dw(int D, int w_bf16, int n, int 
     }
 }
 
-constexpr int kGrid = 152;   // CTAs of the backward: one an SM
+constexpr int kGrid = 152;   // CTAs: one an SM
 
 bool al(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-struct FwdArgs {
+struct NormArgs {
     const NormDims& d;
-    const void *x, *w, *b;
+    const void *x, *w, *b, *dy;
     void* y;
     float* stats;
+    float* part;
+    int want_db;
     cudaStream_t st;
 };
 
-template <typename T, int VEC, int NV, int W>
-void fwd_launch(const FwdArgs& a) {
-    constexpr int RPC = W < 8 ? 8 / W : 1;
-    k_norm_fwd<T, VEC, NV, W><<<(unsigned)((a.d.rows + RPC - 1) / RPC), W < 8 ? 256 : 32 * W, 0, a.st>>>(
-        a.d, (const T*)a.x, a.w, a.b, (T*)a.y, a.stats);
-}
-
-// Lanes hold up to 64 elements (32 one by one): a warp a row up to 2048 (1024), else more warps.
-template <typename T, int VEC>
-void fwd(const FwdArgs& a) {
-    const int D = a.d.D;
-    if constexpr (VEC == 8) {
-        if (D <= 512) fwd_launch<T, 8, 2, 1>(a);
-        else if (D <= 1024) fwd_launch<T, 8, 4, 1>(a);
-        else if (D <= 2048) fwd_launch<T, 8, 8, 1>(a);
-        else if (D <= 4096) fwd_launch<T, 8, 4, 4>(a);
-        else if (D <= 8192) fwd_launch<T, 8, 8, 4>(a);
-        else fwd_launch<T, 8, 8, 8>(a);
-    } else if constexpr (VEC == 4) {
-        if (D <= 512) fwd_launch<T, 4, 4, 1>(a);
-        else if (D <= 1024) fwd_launch<T, 4, 8, 1>(a);
-        else if (D <= 2048) fwd_launch<T, 4, 16, 1>(a);
-        else if (D <= 4096) fwd_launch<T, 4, 8, 4>(a);
-        else if (D <= 8192) fwd_launch<T, 4, 16, 4>(a);
-        else fwd_launch<T, 4, 16, 8>(a);
-    } else {
-        if (D <= 256) fwd_launch<T, 1, 8, 1>(a);
-        else if (D <= 1024) fwd_launch<T, 1, 32, 1>(a);
-        else if (D <= 4096) fwd_launch<T, 1, 32, 4>(a);
-        else fwd_launch<T, 1, 32, 16>(a);
-    }
-}
-
-struct BwdArgs {
-    const NormDims& d;
-    const void *x, *w, *dy;
-    const float* stats;
-    void *dx, *dw, *db;
-    float* ws;
-    cudaStream_t st;
-};
-
-template <typename T, int VEC, int NV, int W>
-int bwd_launch(const BwdArgs& a) {   // returns the number of partial rows
-    constexpr int RPC = 16 / W;
+template <typename T, int VEC, int NV, int W, bool BWD>
+cudaError_t launch(const NormArgs& a, int* ctas) {
+    constexpr int CT = Cta<W, NV * VEC, BWD>::threads, RPC = CT / 32 / W;
     const long long need = (a.d.rows + RPC - 1) / RPC;
-    const int grid = (int)(need < 1 ? 1 : need < kGrid ? need : kGrid);
-    const size_t sm = RPC > 1 ? (size_t)a.d.D * 4 : 0;   // (at most 4096 columns where rows share a CTA)
-    k_norm_bwd<T, VEC, NV, W><<<grid, 512, sm, a.st>>>(a.d, (const T*)a.x, a.w, (const T*)a.dy, a.stats, (T*)a.dx, a.ws,
-                                                       a.db != nullptr);
-    return grid;
+    *ctas = (int)(need < 1 ? 1 : need < kGrid ? need : kGrid);
+    // stages: as many as fit, at most kStages; the sums at the end need D fp32
+    const size_t stage = VEC > 1 ? (size_t)RPC * (BWD ? 2 : 1) * a.d.D * sizeof(T) : 0;
+    const int stages = stage ? (int)(kRing / stage < kStages ? kRing / stage : kStages) : 0;
+    size_t bytes = stage * stages;
+    if (BWD && bytes < (size_t)a.d.D * 4) bytes = (size_t)a.d.D * 4;
+    const auto k = k_norm<T, VEC, NV, W, BWD>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    k<<<*ctas, CT, bytes, a.st>>>(a.d, (const T*)a.x, a.w, a.b, (const T*)a.dy, (T*)a.y, a.stats, a.part, a.want_db, stages);
+    return cudaGetLastError();
 }
 
-// 16 elements a lane (32 beyond 8192).
-template <typename T, int VEC>
-int bwd(const BwdArgs& a) {
+// 16 elements a thread; 32 beyond 8192.
+template <typename T, int VEC, bool BWD>
+cudaError_t by_width(const NormArgs& a, int* ctas) {
     const int D = a.d.D;
-    if (D <= 512) return bwd_launch<T, VEC, 16 / VEC, 1>(a);
-    if (D <= 1024) return bwd_launch<T, VEC, 16 / VEC, 2>(a);
-    if (D <= 2048) return bwd_launch<T, VEC, 16 / VEC, 4>(a);
-    if (D <= 4096) return bwd_launch<T, VEC, 16 / VEC, 8>(a);
-    if (D <= 8192) return bwd_launch<T, VEC, 16 / VEC, 16>(a);
-    return bwd_launch<T, VEC, 32 / VEC, 16>(a);
+    if (D <= 512) return launch<T, VEC, 16 / VEC, 1, BWD>(a, ctas);
+    if (D <= 1024) return launch<T, VEC, 16 / VEC, 2, BWD>(a, ctas);
+    if (D <= 2048) return launch<T, VEC, 16 / VEC, 4, BWD>(a, ctas);
+    if (D <= 4096) return launch<T, VEC, 16 / VEC, 8, BWD>(a, ctas);
+    if (D <= 8192) return launch<T, VEC, 16 / VEC, 16, BWD>(a, ctas);
+    return launch<T, VEC, 32 / VEC, 16, BWD>(a, ctas);
+}
+
+template <bool BWD>
+cudaError_t by_type(const NormArgs& a, int* ctas) {
+    const int vec = a.d.bf16 ? 8 : 4;
+    const bool wide = a.d.D % vec == 0 && a.d.x_stride % vec == 0 && a.d.y_stride % vec == 0 && al(a.x, 16) && al(a.y, 16) &&
+                      al(a.w, 16) && al(a.b, 16) && al(a.dy, 16);
+    if (a.d.bf16) return wide ? by_width<__nv_bfloat16, 8, BWD>(a, ctas) : by_width<__nv_bfloat16, 1, BWD>(a, ctas);
+    return wide ? by_width<float, 4, BWD>(a, ctas) : by_width<float, 1, BWD>(a, ctas);
 }
 
 }  // namespace
@@ -368,29 +423,38 @@ size_t norm_bwd_ws_bytes(const NormDims& d) { return align256((size_t)kGrid * 2 
 
 cudaError_t launch_norm_fwd(const NormDims& d, const void* x, const void* w, const void* b, void* y, float* stats,
                             cudaStream_t st) {
-    const int vec = d.bf16 ? 8 : 4;
-    const bool wide = d.D % vec == 0 && d.x_stride % vec == 0 && d.y_stride % vec == 0 && al(x, 16) && al(y, 16) &&
-                      al(w, 16) && al(b, 16);
-    const FwdArgs a{d, x, w, b, y, stats, st};
-    if (d.bf16) wide ? fwd<__nv_bfloat16, 8>(a) : fwd<__nv_bfloat16, 1>(a);
-    else wide ? fwd<float, 4>(a) : fwd<float, 1>(a);
+    int n;
+    const cudaError_t e = by_type<false>(NormArgs{d, x, w, b, nullptr, y, stats, nullptr, 0, st}, &n);
     prof_mark("norm_fwd", st);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_norm_bwd(const NormDims& d, const void* x, const void* w, const void* dy, const float* stats,
                             void* dx, void* dw, void* db, void* ws, cudaStream_t st) {
-    const int vec = d.bf16 ? 8 : 4;
-    const bool wide = d.D % vec == 0 && d.x_stride % vec == 0 && d.y_stride % vec == 0 && al(x, 16) && al(dy, 16) &&
-                      al(dx, 16) && al(w, 16);
-    const BwdArgs a{d, x, w, dy, stats, dx, dw, db, (float*)ws, st};
     int n;
-    if (d.bf16) n = wide ? bwd<__nv_bfloat16, 8>(a) : bwd<__nv_bfloat16, 1>(a);
-    else n = wide ? bwd<float, 4>(a) : bwd<float, 1>(a);
+    cudaError_t e =
+        by_type<true>(NormArgs{d, x, w, nullptr, dy, dx, const_cast<float*>(stats), (float*)ws, db != nullptr, st}, &n);
+    if (e != cudaSuccess) return e;
     prof_mark("norm_bwd", st);
-    k_norm_dw<<<dim3((d.D + 31) / 32, db ? 2 : 1), 1024, 0, st>>>(d.D, d.w_bf16, n, db != nullptr, (const float*)ws, dw, db);
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((d.D + 31) / 32, db ? 2 : 1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_norm_dw, d.D, (int)d.w_bf16, n, (int)(db != nullptr), (const float*)ws, dw, db);
     prof_mark("norm_dw", st);
-    return cudaGetLastError();
+    return e;
+}
+
+cudaError_t norm_status_read_clear(unsigned int* status) {
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_nm_status, sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    return *status ? cudaMemcpyToSymbol(g_nm_status, &zero, sizeof(unsigned int)) : cudaSuccess;
 }
 
 }  // namespace efla
