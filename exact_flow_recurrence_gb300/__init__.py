@@ -14,7 +14,6 @@ Exact Solution from Continuous-Time Dynamics", page es, Metodologia item 3):
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -372,36 +371,54 @@ def efla_step(q, k, v, beta, S, *, out_dtype=None, mode: int = EXACT, o=None, st
 
 
 # ------------------------------------------------------------------ gated delta rule
-def _on_stream(fn):
-    """Fresh outputs and workspaces of a call with stream=... come from that stream's memory pool:
-    its earlier work, and nothing else's, may still be using them."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(s):
-            return fn(*args, stream=stream, **kw)
-    return call
+# A call's geometry (sizes, strides, types, mode) is checked and put into the C struct once, and kept
+# by its values; what a call still checks is that its tensors have that geometry.
+_plans: dict = {}
 
 
-def _view(t: Optional[torch.Tensor], name: str, shape, dtype) -> Optional[int]:
-    """Pointer of a strided CUDA tensor of the given shape and type, its last dimension contiguous."""
+def _plan(key, make):
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) >= 4096:
+            _plans.clear()
+        p = _plans[key] = make()
+    return p
+
+
+def _elsewhere(stream, fn, *args, **kw):
+    """The call on another stream: its fresh outputs and workspace come from that stream's memory pool,
+    where its earlier work, and nothing else's, may still be using them."""
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return fn(*args, **kw)
+
+
+def _current(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _ws(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def _is(t: Optional[torch.Tensor], name: str, shape, dtype, contiguous: bool = False):
+    """Pointer of a CUDA tensor that has to have this shape and type (None stays None)."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError(f"{name}: tensors must be CUDA tensors")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
     return t.data_ptr()
 
 
-def _strides(t: torch.Tensor, packed: bool, scalar: bool):
-    """{batch, head, token} strides of [B,H,L(,d)] (packed: [H,T(,d)])."""
-    s = t.stride() if scalar else t.stride()[:-1]
-    if not scalar and t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
-        raise ValueError("the last dimension must be contiguous")
-    return _Strides(*((0,) + tuple(s) if packed else s))
+def _rows_strides(name: str, shape, stride, packed: bool):
+    """{batch, head, token} strides of [B,H,L,d] (packed: [H,T,d]), d contiguous."""
+    if shape[-1] > 1 and 0 not in shape and stride[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return (0,) + tuple(stride[:-1]) if packed else tuple(stride[:-1])
 
 
 def make_gated_shape(B, H, Hk, L, dk, dv, dtype=torch.bfloat16, out_dtype=None, mode: int = EULER,
@@ -426,36 +443,39 @@ def efla_gated_bwd_workspace_size(shape: GatedShape) -> int:
     return load_library().efla_gated_bwd_workspace_size(ctypes.byref(shape))
 
 
-def _gated_sizes(q, k, v, offsets):
-    """(B, H, Hk, L, dk, dv, leading dimensions) of a call's tensors."""
-    packed = offsets is not None
-    if v.dim() != (3 if packed else 4) or k.dim() != v.dim():
-        raise ValueError("q, k, v: expected [B,H,L,d], or [H,T,d] with offsets")
-    if packed:
-        if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 \
-                or not offsets.is_contiguous():
-            raise ValueError("offsets: expected a contiguous CUDA int32 tensor [B + 1]")
-        B, lead = offsets.numel() - 1, ()
-    else:
-        B, lead = v.shape[0], (v.shape[0],)
-    return B, v.shape[-3], k.shape[-3], v.shape[-2], k.shape[-1], v.shape[-1], lead
+class _GatedPlan:
+    """Shapes of a gated call's tensors, its C struct and its workspace."""
+
+    def __init__(self, qs, vs, B, packed, dtype, odt, mode, path, strides, bwd):
+        if len(vs) != (3 if packed else 4) or len(qs) != len(vs):
+            raise ValueError("q, k, v: expected [B,H,L,d], or [H,T,d] with offsets")
+        self.q, self.v, self.s = torch.Size(qs), torch.Size(vs), torch.Size(vs[:-1])
+        H, L, dv = vs[-3:]
+        Hk, dk = qs[-3], qs[-1]
+        if qs[-2] != L or qs[:-3] != vs[:-3]:
+            raise ValueError(f"q, k: expected {tuple(vs[:-3]) + (Hk, L, dk)}, got {tuple(qs)}")
+        self.state = torch.Size((B, H, dk, dv))
+        st = {}
+        for n, x in strides.items():
+            if x is not None:
+                shape = self.s if n in ("g", "beta") else self.q if n in ("q", "k", "dq", "dk") else self.v
+                if len(x) == len(shape):     # (a tensor of another shape is refused where it is passed)
+                    st[n] = ((0,) + tuple(x) if packed else tuple(x)) if n in ("g", "beta") \
+                        else _rows_strides(n, shape, x, packed)
+        self.shape = make_gated_shape(B, H, Hk, L, dk, dv, dtype, odt, mode, path, packed, st)
+        self.ref = ctypes.byref(self.shape)
+        self.ws = (efla_gated_bwd_workspace_size if bwd else efla_gated_fwd_workspace_size)(self.shape)
 
 
-def _like(t: torch.Tensor, dtype) -> torch.Tensor:
-    """A fresh tensor of t's shape, in t's order of storage (dense)."""
-    return torch.empty_like(t, dtype=dtype, memory_format=torch.preserve_format)
+def _batch(v, offsets):
+    if offsets is None:
+        return v.shape[0]
+    if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 \
+            or not offsets.is_contiguous():
+        raise ValueError("offsets: expected a contiguous CUDA int32 tensor [B + 1]")
+    return offsets.numel() - 1
 
 
-def _gated_inputs(q, k, v, g, beta, sizes, packed, extra=()):
-    B, H, Hk, L, dk, dv, lead = sizes
-    args = [("q", q, lead + (Hk, L, dk), v.dtype), ("k", k, lead + (Hk, L, dk), v.dtype),
-            ("v", v, lead + (H, L, dv), v.dtype), ("g", g, lead + (H, L), torch.float32),
-            ("beta", beta, lead + (H, L), torch.float32), *extra]
-    ptrs = [_view(t, n, s, dt) for n, t, s, dt in args]
-    return ptrs, {("do" if n == "dO" else n): _strides(t, packed, t.dim() == len(lead) + 2) for n, t, _, _ in args}
-
-
-@_on_stream
 def efla_gated_fwd(q, k, v, g, beta, S0=None, *, offsets=None, out_dtype=None, mode: int = EULER, o=None,
                    S_final=None, workspace=None, want_state: bool = True, stream=None, path: int = AUTO):
     """Chunked gated delta rule: S <- e^g S, S <- S + alpha k (v - S^T k)^T, o = S^T q.
@@ -464,146 +484,170 @@ def efla_gated_fwd(q, k, v, g, beta, S0=None, *, offsets=None, out_dtype=None, m
     [B,H,L] fp32, S0 [B,H,dk,dv] fp32.  With offsets (int32 [B+1] on the GPU) the sequences are packed
     on one axis of tokens: q, k [Hk,T,dk], v [H,T,dv], g, beta [H,T].
     Returns (o, in v's order of storage, S_final [B,H,dk,dv] fp32 or None)."""
-    sizes = _gated_sizes(q, k, v, offsets)
-    B, H, Hk, L, dk, dv, lead = sizes
-    packed = offsets is not None
-    ptrs, st = _gated_inputs(q, k, v, g, beta, sizes, packed)
-    odt = v.dtype if out_dtype is None else out_dtype
-    o = _like(v, odt) if o is None else o
-    po = _view(o, "o", lead + (H, L, dv), odt)
-    st["o"] = _strides(o, packed, False)
-    if S_final is not None or want_state:
-        S_final = _out(S_final, (B, H, dk, dv), torch.float32, v.device, "S_final")
-    _state_shape(S0, (B, H, dk, dv), "S0")
-    shape = make_gated_shape(B, H, Hk, L, dk, dv, v.dtype, odt, mode, path, packed, st)
-    ws = _workspace(efla_gated_fwd_workspace_size(shape), v.device, workspace)
-    rc = load_library().efla_gated_fwd(ctypes.byref(shape), _ptr(offsets), *ptrs, _ptr(S0), po, _ptr(S_final),
-                                       _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    if stream is not None:
+        return _elsewhere(stream, efla_gated_fwd, q, k, v, g, beta, S0, offsets=offsets, out_dtype=out_dtype, mode=mode, o=o,
+                          S_final=S_final, workspace=workspace, want_state=want_state, path=path)
+    dt, B = v.dtype, _batch(v, offsets)
+    odt = dt if out_dtype is None else out_dtype
+    if o is None:
+        o = torch.empty_like(v, dtype=odt)
+    strides = (q.stride(), k.stride(), v.stride(), g.stride(), beta.stride(), o.stride())
+    pl = _plan(("gf", q.shape, v.shape, strides, dt, odt, mode, path, B, offsets is None), lambda: _GatedPlan(
+        q.shape, v.shape, B, offsets is not None, dt, odt, mode, path,
+        dict(zip(("q", "k", "v", "g", "beta", "o"), strides)), False))
+    if S_final is None and want_state:
+        S_final = torch.empty(pl.state, dtype=torch.float32, device=v.device)
+    ws = _ws(pl.ws, v.device) if workspace is None else workspace
+    f32 = torch.float32
+    rc = load_library().efla_gated_fwd(
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(q, "q", pl.q, dt), _is(k, "k", pl.q, dt),
+        _is(v, "v", pl.v, dt), _is(g, "g", pl.s, f32), _is(beta, "beta", pl.s, f32), _is(S0, "S0", pl.state, f32, True),
+        _is(o, "o", pl.v, odt), _is(S_final, "S_final", pl.state, f32, True), _ptr(ws), ws.numel() * ws.element_size(),
+        _current(v))
     _check(rc, "efla_gated_fwd")
     return o, S_final
 
 
-def _state_shape(t, shape, name):
-    if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32):
-        raise ValueError(f"{name}: expected torch.float32 {shape}, got {t.dtype} {tuple(t.shape)}")
-
-
-@_on_stream
 def efla_gated_bwd(q, k, v, g, beta, dO, S0=None, dS_final=None, *, offsets=None, out_dtype=None,
                    mode: int = EULER, dq=None, dk=None, dv=None, want_dS0: bool = True, workspace=None,
                    stream=None, path: int = AUTO):
     """Backward of efla_gated_fwd (same shapes; dO as v).  Returns (dq, dk, dv, dg, dbeta, dS0 or None):
     dq, dk, dv in the order of storage of q, k, v, or into the tensors given (which may be slices of one
     buffer); dg, dbeta fp32, dense."""
-    sizes = _gated_sizes(q, k, v, offsets)
-    B, H, Hk, L, nk, nv, lead = sizes
-    packed = offsets is not None
-    ptrs, st = _gated_inputs(q, k, v, g, beta, sizes, packed, [("dO", dO, lead + (H, L, nv), v.dtype)])
-    odt = v.dtype if out_dtype is None else out_dtype
-    dq, dk, dv = (_like(t, odt) if x is None else x for x, t in ((dq, q), (dk, k), (dv, v)))
-    pout = [_view(t, n, lead + s, odt) for n, t, s in (("dq", dq, (Hk, L, nk)), ("dk", dk, (Hk, L, nk)),
-                                                      ("dv", dv, (H, L, nv)))]
-    for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-        st[n] = _strides(t, packed, False)
-    dg = torch.empty(lead + (H, L), dtype=torch.float32, device=v.device)
-    db = torch.empty_like(dg)
-    dS0 = torch.empty((B, H, nk, nv), dtype=torch.float32, device=v.device) if want_dS0 else None
-    _state_shape(S0, (B, H, nk, nv), "S0")
-    _state_shape(dS_final, (B, H, nk, nv), "dS_final")
-    shape = make_gated_shape(B, H, Hk, L, nk, nv, v.dtype, odt, mode, path, packed, st)
-    ws = _workspace(efla_gated_bwd_workspace_size(shape), v.device, workspace)
-    rc = load_library().efla_gated_bwd(ctypes.byref(shape), _ptr(offsets), *ptrs[:5], _ptr(S0), ptrs[5],
-                                       _ptr(dS_final), *pout, _ptr(dg), _ptr(db), _ptr(dS0), _ptr(ws),
-                                       ws.numel() * ws.element_size(), _stream(stream))
+    if stream is not None:
+        return _elsewhere(stream, efla_gated_bwd, q, k, v, g, beta, dO, S0, dS_final, offsets=offsets, out_dtype=out_dtype,
+                          mode=mode, dq=dq, dk=dk, dv=dv, want_dS0=want_dS0, workspace=workspace, path=path)
+    dt, B, f32 = v.dtype, _batch(v, offsets), torch.float32
+    odt = dt if out_dtype is None else out_dtype
+    dq = torch.empty_like(q, dtype=odt) if dq is None else dq
+    dk = torch.empty_like(k, dtype=odt) if dk is None else dk
+    dv = torch.empty_like(v, dtype=odt) if dv is None else dv
+    strides = (q.stride(), k.stride(), v.stride(), g.stride(), beta.stride(), dO.stride(), dq.stride(), dk.stride(),
+               dv.stride())
+    pl = _plan(("gb", q.shape, v.shape, strides, dt, odt, mode, path, B, offsets is None), lambda: _GatedPlan(
+        q.shape, v.shape, B, offsets is not None, dt, odt, mode, path,
+        dict(zip(("q", "k", "v", "g", "beta", "do", "dq", "dk", "dv"), strides)), True))
+    dg = torch.empty(pl.s, dtype=f32, device=v.device)
+    db = torch.empty(pl.s, dtype=f32, device=v.device)
+    dS0 = torch.empty(pl.state, dtype=f32, device=v.device) if want_dS0 else None
+    ws = _ws(pl.ws, v.device) if workspace is None else workspace
+    rc = load_library().efla_gated_bwd(
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(q, "q", pl.q, dt), _is(k, "k", pl.q, dt),
+        _is(v, "v", pl.v, dt), _is(g, "g", pl.s, f32), _is(beta, "beta", pl.s, f32), _is(S0, "S0", pl.state, f32, True),
+        _is(dO, "dO", pl.v, dt), _is(dS_final, "dS_final", pl.state, f32, True), _is(dq, "dq", pl.q, odt),
+        _is(dk, "dk", pl.q, odt), _is(dv, "dv", pl.v, odt), dg.data_ptr(), db.data_ptr(), _ptr(dS0), _ptr(ws),
+        ws.numel() * ws.element_size(), _current(v))
     _check(rc, "efla_gated_bwd")
     return dq, dk, dv, dg, db, dS0
 
 
-@_on_stream
+class _StepPlan:
+    def __init__(self, qs, vs, S, dtype, odt, mode, strides):
+        if len(vs) != 3 or len(qs) != 3 or len(S) != 4:
+            raise ValueError("expected q, k [B,Hk,dk], v [B,H,dv], S [n,H,dk,dv]")
+        (B, H, dv), (Hk, dk) = vs, qs[1:]
+        self.q, self.v, self.s, self.b = torch.Size((B, Hk, dk)), vs, vs[:2], vs[:1]
+        self.S = torch.Size((S[0], H, dk, dv))
+        st = {}
+        for n, x in strides.items():
+            if len(x) == 3 and (dk if n in ("q", "k") else dv) > 1 and B * H * Hk and x[2] != 1:
+                raise ValueError(f"{n}: the last dimension must be contiguous")
+            st[n] = (tuple(x) + (0, 0))[:2] + (0,)
+        self.shape = make_gated_shape(B, H, Hk, 1, dk, dv, dtype, odt, mode, AUTO, False, st)
+        self.ref = ctypes.byref(self.shape)
+
+
 def efla_gated_step(q, k, v, g, beta, S, *, slots=None, out_dtype=None, mode: int = EULER, o=None, stream=None):
     """One token of the gated delta rule on a cache of states S [n,H,dk,dv] fp32, updated in place.
 
     q, k [B,Hk,dk], v [B,H,dv] (any strides, last dimension contiguous), g, beta [B,H] fp32.  slots (int32
     [B] on the GPU): each sequence's place in the cache (outside [0, n): skipped, o = 0); None: place b.
     Returns o [B,H,dv]."""
-    if v.dim() != 3 or k.dim() != 3 or S.dim() != 4:
-        raise ValueError("expected q, k [B,Hk,dk], v [B,H,dv], S [n,H,dk,dv]")
-    B, H, dv = v.shape
-    Hk, dk = k.shape[1:]
-    args = [("q", q, (B, Hk, dk), v.dtype), ("k", k, (B, Hk, dk), v.dtype), ("v", v, (B, H, dv), v.dtype),
-            ("g", g, (B, H), torch.float32), ("beta", beta, (B, H), torch.float32)]
-    ptrs = [_view(t, n, s, dt) for n, t, s, dt in args]
-    odt = v.dtype if out_dtype is None else out_dtype
-    o = _like(v, odt) if o is None else o
-    po = _view(o, "o", (B, H, dv), odt)
-    st = {}
-    for n, t in [(a[0], a[1]) for a in args] + [("o", o)]:
-        if t.dim() == 3 and t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
-            raise ValueError(f"{n}: the last dimension must be contiguous")
-        st[n] = (t.stride(0), t.stride(1), 0)
-    _state_shape(S, (S.shape[0], H, dk, dv), "S")
-    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (B,)):
-        raise ValueError(f"slots: expected torch.int32 ({B},), got {slots.dtype} {tuple(slots.shape)}")
-    shape = make_gated_shape(B, H, Hk, 1, dk, dv, v.dtype, odt, mode, AUTO, False, st)
-    rc = load_library().efla_gated_step(ctypes.byref(shape), *ptrs, _ptr(S), _ptr(slots), S.shape[0], po,
-                                        _stream(stream))
+    if stream is not None:
+        return _elsewhere(stream, efla_gated_step, q, k, v, g, beta, S, slots=slots, out_dtype=out_dtype, mode=mode, o=o)
+    dt, f32 = v.dtype, torch.float32
+    odt = dt if out_dtype is None else out_dtype
+    if o is None:
+        o = torch.empty_like(v, dtype=odt)
+    strides = (q.stride(), k.stride(), v.stride(), g.stride(), beta.stride(), o.stride())
+    pl = _plan(("gs", q.shape, v.shape, S.shape, strides, dt, odt, mode), lambda: _StepPlan(
+        q.shape, v.shape, S.shape, dt, odt, mode, dict(zip(("q", "k", "v", "g", "beta", "o"), strides))))
+    rc = load_library().efla_gated_step(
+        pl.ref, _is(q, "q", pl.q, dt), _is(k, "k", pl.q, dt), _is(v, "v", pl.v, dt), _is(g, "g", pl.s, f32),
+        _is(beta, "beta", pl.s, f32), _is(S, "S", pl.S, f32, True), _is(slots, "slots", pl.b, torch.int32, True), pl.S[0],
+        _is(o, "o", pl.v, odt), _current(v))
     _check(rc, "efla_gated_step")
     return o
 
 
 # ------------------------------------------------------------------ layer norm
-def _rows2d(t: torch.Tensor, name: str) -> torch.Tensor:
-    """[..., D] as [rows, D] without a copy (rows one stride apart, D contiguous)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: tensors must be CUDA tensors")
-    if t.dim() < 1 or (t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1):
+def _row_stride(name: str, shape, stride) -> int:
+    """The one stride that the rows of [..., D] lie apart (D if there is one row, or none)."""
+    if len(shape) < 1 or (shape[-1] > 1 and 0 not in shape and stride[-1] != 1):
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    try:
-        return t.view(-1, t.shape[-1]) if t.numel() else t.new_empty((0, t.shape[-1]))
-    except RuntimeError:
-        raise ValueError(f"{name}: its rows must lie one stride apart") from None
+    if 0 in shape:
+        return shape[-1]
+    step = span = None
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step, span = s, n * s
+        elif s == span:
+            span = n * s
+        else:
+            raise ValueError(f"{name}: its rows must lie one stride apart")
+    return shape[-1] if step is None else step
 
 
-def _norm_shape(x2, y2, weight, eps) -> NormShape:
-    rows, D = x2.shape
-    return NormShape(rows, D, x2.stride(0) if rows > 1 else D, y2.stride(0) if rows > 1 else D, _dt(x2.dtype),
-                     _dt(weight.dtype), eps)
+class _NormPlan:
+    def __init__(self, shape, xs, ys, dtype, wdtype, eps, bwd):
+        D = shape[-1] if len(shape) else 0
+        rows = 1
+        for n in shape[:-1]:
+            rows *= n
+        self.x, self.w, self.stats = shape, torch.Size((D,)), torch.Size(tuple(shape[:-1]) + (2,))
+        s = self.shape = NormShape(rows, D, _row_stride("x", shape, xs), _row_stride("dy" if bwd else "y", shape, ys),
+                                   _dt(dtype), _dt(wdtype), eps)
+        self.ref = ctypes.byref(s)
+        self.ws = load_library().efla_norm_bwd_workspace_size(self.ref) if bwd else 0
 
 
-@_on_stream
 def efla_norm_fwd(x, weight, bias=None, *, eps: float = 1e-5, y=None, stats=None, stream=None):
     """Layer norm over the last dimension of x [..., D].  weight, bias [D] (fp32 or bf16).
 
     Returns (y like x, stats [..., 2] fp32: mean and 1/sqrt(var + eps) of each row)."""
-    x2, D = _rows2d(x, "x"), x.shape[-1]
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
-    _view(y, "y", x.shape, x.dtype)
-    for n, t in (("weight", weight), ("bias", bias)):
-        _view(t, n, (D,), weight.dtype)
-    stats = _out(stats, tuple(x.shape[:-1]) + (2,), torch.float32, x.device, "stats")
-    y2 = _rows2d(y, "y")
-    shape = _norm_shape(x2, y2, weight, eps)
-    rc = load_library().efla_norm_fwd(ctypes.byref(shape), x2.data_ptr(), _ptr(weight), _ptr(bias), y2.data_ptr(),
-                                      _ptr(stats), _stream(stream))
+    if stream is not None:
+        return _elsewhere(stream, efla_norm_fwd, x, weight, bias, eps=eps, y=y, stats=stats)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    pl = _plan(("nf", x.shape, x.stride(), y.stride(), x.dtype, weight.dtype, eps),
+               lambda: _NormPlan(x.shape, x.stride(), y.stride(), x.dtype, weight.dtype, eps, False))
+    if stats is None:
+        stats = torch.empty(pl.stats, dtype=torch.float32, device=x.device)
+    rc = load_library().efla_norm_fwd(
+        pl.ref, _is(x, "x", pl.x, x.dtype), _is(weight, "weight", pl.w, weight.dtype, True),
+        _is(bias, "bias", pl.w, weight.dtype, True), _is(y, "y", pl.x, x.dtype),
+        _is(stats, "stats", pl.stats, torch.float32, True), _current(x))
     _check(rc, "efla_norm_fwd")
     return y, stats
 
 
-@_on_stream
 def efla_norm_bwd(x, weight, dy, stats, *, want_bias: bool = True, workspace=None, stream=None):
     """Backward of efla_norm_fwd.  Returns (dx dense, dweight, dbias or None), the last two in weight's type."""
-    x2, dy2, D = _rows2d(x, "x"), _rows2d(dy, "dy"), x.shape[-1]
-    _view(dy, "dy", x.shape, x.dtype)
-    _view(weight, "weight", (D,), weight.dtype)
-    _view(stats, "stats", tuple(x.shape[:-1]) + (2,), torch.float32)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = torch.empty(D, dtype=weight.dtype, device=x.device)
-    db = torch.empty_like(dw) if want_bias else None
-    shape = _norm_shape(x2, dy2, weight, 0.0)
-    ws = _workspace(load_library().efla_norm_bwd_workspace_size(ctypes.byref(shape)), x.device, workspace)
-    rc = load_library().efla_norm_bwd(ctypes.byref(shape), x2.data_ptr(), _ptr(weight), dy2.data_ptr(), _ptr(stats),
-                                      dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ws),
-                                      ws.numel() * ws.element_size(), _stream(stream))
+    if stream is not None:
+        return _elsewhere(stream, efla_norm_bwd, x, weight, dy, stats, want_bias=want_bias, workspace=workspace)
+    dt, wdt, dev = x.dtype, weight.dtype, x.device
+    pl = _plan(("nb", x.shape, x.stride(), dy.stride(), dt, wdt),
+               lambda: _NormPlan(x.shape, x.stride(), dy.stride(), dt, wdt, 0.0, True))
+    dx = torch.empty(pl.x, dtype=dt, device=dev)
+    dw = torch.empty(pl.w, dtype=wdt, device=dev)
+    db = torch.empty(pl.w, dtype=wdt, device=dev) if want_bias else None
+    ws = _ws(pl.ws, dev) if workspace is None else workspace
+    rc = load_library().efla_norm_bwd(
+        pl.ref, _is(x, "x", pl.x, dt), _is(weight, "weight", pl.w, wdt, True), _is(dy, "dy", pl.x, dt),
+        _is(stats, "stats", pl.stats, torch.float32, True), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ws),
+        ws.numel() * ws.element_size(), _current(x))
     _check(rc, "efla_norm_bwd")
     return dx, dw, db
 
