@@ -4,6 +4,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/efla.h"
@@ -467,17 +469,16 @@ efla_status efla_get_status(cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(sync)");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status");
-    unsigned int word = 0, word2 = 0, word3 = 0, word4 = 0, word5 = 0, word6 = 0, word7 = 0, word8 = 0;
-    e = efla::tc_status_read_clear(&word);
-    if (e == cudaSuccess) e = efla::proj_status_read_clear(&word2);
-    if (e == cudaSuccess) e = efla::bt_status_read_clear(&word3);
-    if (e == cudaSuccess) e = efla::gt_status_read_clear(&word4);
-    if (e == cudaSuccess) e = efla::sd_status_read_clear(&word5);
-    if (e == cudaSuccess) e = efla::gated_tc_status_read_clear(&word6);
-    if (e == cudaSuccess) e = efla::gated_bwd_tc_status_read_clear(&word7);
-    if (e == cudaSuccess) e = efla::norm_status_read_clear(&word8);
-    if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(status word)");
-    word |= word2 | word3 | word4 | word5 | word6 | word7 | word8;
+    unsigned int word = 0;
+    for (const auto read : {efla::tc_status_read_clear, efla::proj_status_read_clear, efla::bt_status_read_clear,
+                            efla::gt_status_read_clear, efla::sd_status_read_clear, efla::gated_tc_status_read_clear,
+                            efla::gated_bwd_tc_status_read_clear, efla::gated_step_status_read_clear,
+                            efla::norm_status_read_clear}) {
+        unsigned int one = 0;
+        e = read(&one);
+        if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(status word)");
+        word |= one;
+    }
     if (word & efla::kStatusBounds)
         return fail(EFLA_ERR_BOUNDS, "a debug-build bounds check skipped a global write (status 0x%x)", word);
     if (word) return fail(EFLA_ERR_TIMEOUT, "a bounded device-side wait expired (status 0x%x)", word);

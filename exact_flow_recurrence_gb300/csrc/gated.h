@@ -54,6 +54,8 @@ cudaError_t gated_tc_status_read_clear(unsigned int* status);
 cudaError_t launch_gated_step(const GDims& d, const void* q, const void* k, const void* v, const float* g,
                               const float* beta, float* S, const int* slots, int nslots, void* o, cudaStream_t st);
 
+cudaError_t gated_step_status_read_clear(unsigned int* status);
+
 // ------------------------------------------------------------------- layer norm (norm.cu)
 struct NormDims {
     long long rows, x_stride, y_stride;   // y_stride: of y, and of dy in the backward

@@ -325,7 +325,8 @@ def test_capture_and_other_stream():
 @pytest.mark.parametrize("mode", [efla.EULER, efla.EXACT])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("shape", [(1, 1, 1, 16, 16), (3, 4, 2, 48, 80), (2, 6, 3, 128, 128), (40, 8, 4, 128, 128),
-                                   (5, 2, 1, 128, 96), (70, 16, 16, 128, 128), (3, 3, 3, 64, 128)])
+                                   (5, 2, 1, 128, 96), (70, 16, 16, 128, 128), (3, 3, 3, 64, 128),
+                                   (60, 8, 4, 112, 64), (80, 4, 4, 48, 128)])
 def test_step(shape, dtype, mode):
     B, H, Hk, dk, dv = shape
     gen = torch.Generator().manual_seed(B)
