@@ -350,10 +350,6 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                 unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
                 ok = mbar_wait(s_ready, ph, kWaitLimit);
                 if (!ok) break;
-                if (c + 1 < nch) {   // (the stage's last readers were chunk c - 1's)
-                    load(c + 1);
-                    if (M::TPS == 2) load_tp(c + 1);
-                }
                 ok = mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
                 if (!ok) break;
                 tc_fence_after();
@@ -367,6 +363,10 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                                        idesc_f16(128, NP * N, false, true, true), blk + ks > 0);
                 }
                 mma_commit(d1);
+                if (c + 1 < nch) {   // (the stage's last readers were chunk c - 1's)
+                    load(c + 1);
+                    if (M::TPS == 2) load_tp(c + 1);
+                }
                 ok = mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit) && mbar_wait(x_ready, ph, kWaitLimit);
                 if (!ok) break;
                 tc_fence_after();
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
         const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + c0 + cc;
         const uint32_t lq = 32 * (warp & 3);
         // 8 values of `r`, column cc + e of the slice, as parts into an operand of 64-column blocks
-        const auto put = [&](uint32_t base, uint32_t blk, int r, int e, const float* x) {
+        const auto put = [&](uint32_t base, uint32_t blk, int r, int e, const float2* x) {
             uint4 w[NP];
             split8<NP>(x, w);
 #pragma unroll
@@ -416,38 +416,21 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                 *reinterpret_cast<uint4*>(sm + base + (j >> 6) * blk + sw128(r, j & 63)) = w[p];
             }
         };
-        // this thread's lane of an accumulator: the sum of its column groups
-        const auto get = [&](uint32_t t, float* y) {
-#pragma unroll
-            for (int e = 0; e < NC; e += 16) {
-                float x[NP][16];
-#pragma unroll
-                for (int p = 0; p < NP; ++p) tmem_ld16(taddr(t, lq, p * N + cc + e), x[p]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int p = 0; p < NP; ++p) loaded16(x[p]);
-#pragma unroll
-                for (int m = 0; m < 16; ++m) {
-                    y[e + m] = x[NP - 1][m];
-#pragma unroll
-                    for (int p = NP - 2; p >= 0; --p) y[e + m] += x[p][m];   // the small ones first
-                }
-            }
-        };
-        // (the warp leaves together if a wait gives up)
-        const auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, kWaitLimit)) != 0; };
         const auto arrive = [&](uint64_t* bar) {   // a warp's shared-memory writes and tensor-memory reads are done
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        float S[NC];
+        // (the warp leaves together if a wait gives up)
+        const auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, kWaitLimit)) != 0; };
+        float2 S[NC / 2];
 #pragma unroll
         for (int e = 0; e < NC; e += 4) {
             const float4 x = a.S0 && row < d.dk && e < nv ? *reinterpret_cast<const float4*>(a.S0 + sb + e)
                                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+            S[e / 2] = make_float2(x.x, x.y);
+            S[e / 2 + 1] = make_float2(x.z, x.w);
         }
         bool ok = true;
         for (int c = 0; c < nch && ok; ++c) {
@@ -455,7 +438,7 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
             const int n = min(kGC, s.len - c * kGC);
             const GVec* vec = (const GVec*)(sm + M::VEC + (c & 1) * sizeof(GVec));
 #pragma unroll
-            for (int e = 0; e < NC; e += 8) put(M::S, 16384, row, e, S + e);
+            for (int e = 0; e < NC; e += 8) put(M::S, 16384, row, e, S + e / 2);
             if (d.packed && n < kGC) {   // rows past the sequence are another's: zero its keys (0 x NaN is not 0)
                 ok = wait(&full[c & 1], (c >> 1) & 1);
                 unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
@@ -468,79 +451,99 @@ __global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, 
                 float* rs = a.rec_S + ((rec0 + c) * d.dk + row) * d.dv + c0 + cc;
 #pragma unroll
                 for (int e = 0; e < NC; e += 16)
-                    if (e < nv) st16(rs + e, S + e);
+                    if (e < nv) st16(rs + e, S + e / 2);
             }
             ok = ok && wait(&full[c & 1], (c >> 1) & 1);
             if (!ok) break;
             const float up = vec->up[i], last = vec->up[63];
-            float y[NC];
             if (top) {
-                const float al = vec->al[i], rest = vec->rest[i];
+                // X = alpha V - (alpha e^c) K S; rows past the end are zero whatever lies there
+                const bool live = i < n;
+                const float2 al = both(vec->al[i]), au = both(-vec->al[i] * up), rest = both(vec->rest[i]);
                 const unsigned char* vt = sm + M::V + (c & 1) * 8192;
-                if (!(ok = wait(d1, ph))) break;
-                tc_fence_after();
-                get(t1, y);
+                float2 v[NC / 2];
 #pragma unroll
                 for (int e = 0; e < NC; e += 8) {
-                    const uint4 raw8 = *reinterpret_cast<const uint4*>(vt + sw128(i, cc + e));
-                    const uint32_t* vw = reinterpret_cast<const uint32_t*>(&raw8);
-                    float x[8];
+                    const uint4 w = *reinterpret_cast<const uint4*>(vt + sw128(i, cc + e));
+                    v[e / 2] = mul2(al, bf16x2(w.x));
+                    v[e / 2 + 1] = mul2(al, bf16x2(w.y));
+                    v[e / 2 + 2] = mul2(al, bf16x2(w.z));
+                    v[e / 2 + 3] = mul2(al, bf16x2(w.w));
+                }
+                if (!(ok = wait(d1, ph))) break;
+                tc_fence_after();
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        x[2 * m] = fmaf(-up, y[e + 2 * m], __uint_as_float(vw[m] << 16));
-                        x[2 * m + 1] = fmaf(-up, y[e + 2 * m + 1], __uint_as_float(vw[m] & 0xffff0000u));
+                for (int e = 0; e < NC; e += 16) {
+                    float2 y[8];
+                    tmem_sum16<NP>(taddr(t1, lq, cc + e), N, y);
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        y[m] = fma2(au, y[m], v[e / 2 + m]);
+                        if (!live) y[m] = both(0.f);
                     }
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) x[m] = i < n ? al * x[m] : 0.f;
-                    put(M::X, 8192, i, e, x);
+                    put(M::X, 8192, i, e, y);
+                    put(M::X, 8192, i, e + 8, y + 4);
                 }
                 arrive(x_ready);
                 if (!(ok = wait(d2, ph))) break;
                 tc_fence_after();
-                get(t2, y);
 #pragma unroll
-                for (int e = 0; e < NC; e += 8) {
-                    float x[8];
+                for (int e = 0; e < NC; e += 16) {
+                    float2 y[8];
+                    tmem_sum16<NP>(taddr(t2, lq, cc + e), N, y);
+                    if (REC) {
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) x[m] = rest * y[e + m];
-                    put(M::X, 8192, i, e, x);
+                        for (int m = 0; m < 8; ++m) v[e / 2 + m] = y[m];
+                    }
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) y[m] = mul2(rest, y[m]);
+                    put(M::X, 8192, i, e, y);
+                    put(M::X, 8192, i, e + 8, y + 4);
                 }
                 arrive(u_ready);
                 if (REC) {
                     float* ru = a.rec_U + ((rec0 + c) * kGC + i) * d.dv + c0 + cc;
 #pragma unroll
                     for (int e = 0; e < NC; e += 16)
-                        if (e < nv) st16(ru + e, y + e);
+                        if (e < nv) st16(ru + e, v + e / 2);
                 }
             } else {
                 if (!(ok = wait(d1, ph))) break;
                 tc_fence_after();
-                get(t1, y);
+                float2 qs[NC / 2];
+#pragma unroll
+                for (int e = 0; e < NC; e += 16) tmem_sum16<NP>(taddr(t1, lq, cc + e), N, *reinterpret_cast<float2(*)[8]>(qs + e / 2));
                 arrive(u_ready);
                 if (!(ok = wait(d2, ph))) break;
                 tc_fence_after();
-                float z[NC];
-                if (!REC) get(t2, z);
-                if (!REC && i < n) {
+                if (!REC) {
                     Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + c0 + cc;
 #pragma unroll
-                    for (int e = 0; e < NC; ++e) y[e] = fmaf(up, y[e], z[e]);
+                    for (int e = 0; e < NC; e += 16) {
+                        float2 y[8];
+                        tmem_sum16<NP>(taddr(t2, lq, cc + e), N, y);
 #pragma unroll
-                    for (int e = 0; e < NC; e += 16)
-                        if (e < nv) st16(op + e, y + e);
+                        for (int m = 0; m < 8; ++m) y[m] = fma2(both(up), qs[e / 2 + m], y[m]);
+                        if (i < n && e < nv) st16(op + e, y);
+                    }
                 }
             }
             if (!(ok = wait(d3, ph))) break;
             tc_fence_after();
-            get(t3, y);
 #pragma unroll
-            for (int e = 0; e < NC; ++e) S[e] = fmaf(last, S[e], y[e]);
+            for (int e = 0; e < NC; e += 16) {
+                float2 y[8];
+                tmem_sum16<NP>(taddr(t3, lq, cc + e), N, y);
+#pragma unroll
+                for (int m = 0; m < 8; ++m) S[e / 2 + m] = fma2(both(last), S[e / 2 + m], y[m]);
+            }
         }
         if (!ok) atomicOr(&g_gt2_status, 1u);
         if (a.S_final && row < d.dk) {
 #pragma unroll
             for (int e = 0; e < NC; e += 4)
-                if (e < nv) *reinterpret_cast<float4*>(a.S_final + sb + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+                if (e < nv) *reinterpret_cast<float4*>(a.S_final + sb + e) =
+                        make_float4(S[e / 2].x, S[e / 2].y, S[e / 2 + 1].x, S[e / 2 + 1].y);
         }
         tc_fence_before();
     }

@@ -12,6 +12,7 @@
 #pragma once
 
 #include "gated_seq.cuh"
+#include "packed2.cuh"
 #include "tc_common.cuh"
 
 namespace efla {
@@ -36,40 +37,70 @@ __device__ __forceinline__ void loaded16(float* v) {
 
 // 8 values -> NP 16-byte chunks of bf16 parts
 template <int NP>
-__device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
-    float r[8];
+__device__ __forceinline__ void split8(const float2* x, uint4 (&w)[NP]) {
+    float2 r[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = x[i];
+    for (int i = 0; i < 4; ++i) r[i] = x[i];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         uint32_t* o = reinterpret_cast<uint32_t*>(&w[p]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(r[2 * i], r[2 * i + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(r[i].x, r[i].y);
             o[i] = *reinterpret_cast<const uint32_t*>(&h);
-            if (p + 1 < NP) {
-                r[2 * i] -= __uint_as_float(o[i] << 16);
-                r[2 * i + 1] -= __uint_as_float(o[i] & 0xffff0000u);
-            }
+            if (p + 1 < NP) r[i] = sub2(r[i], bf16x2(o[i]));
         }
+    }
+}
+template <int NP>
+__device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
+    float2 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
+    split8<NP>(y, w);
+}
+
+// 16 columns of this warp's lanes of an accumulator, summed over G column groups `gap` apart
+// (the last one first: it holds the small parts' products)
+template <int G>
+__device__ __forceinline__ void tmem_sum16(uint32_t t, int gap, float2 (&y)[8]) {
+    float x[G][16];
+#pragma unroll
+    for (int p = 0; p < G; ++p) tmem_ld16(t + p * gap, x[p]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int p = 0; p < G; ++p) loaded16(x[p]);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        y[m] = make_float2(x[G - 1][2 * m], x[G - 1][2 * m + 1]);
+#pragma unroll
+        for (int p = G - 2; p >= 0; --p) y[m] = add2(y[m], make_float2(x[p][2 * m], x[p][2 * m + 1]));
     }
 }
 
 template <typename Tout>
-__device__ __forceinline__ void st16(Tout* p, const float* x);   // 16 values to 16-byte aligned memory
+__device__ __forceinline__ void st16(Tout* p, const float2* x);   // 16 values to 16-byte aligned memory
 template <>
-__device__ __forceinline__ void st16<float>(float* p, const float* x) {
+__device__ __forceinline__ void st16<float>(float* p, const float2* x) {
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    for (int i = 0; i < 8; i += 2) *reinterpret_cast<float4*>(p + 2 * i) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
 }
 template <>
-__device__ __forceinline__ void st16<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
+__device__ __forceinline__ void st16<__nv_bfloat16>(__nv_bfloat16* p, const float2* x) {
 #pragma unroll
-    for (int i = 0; i < 16; i += 8) {
+    for (int i = 0; i < 8; i += 4) {
         uint4 w[1];
         split8<1>(x + i, w);
-        *reinterpret_cast<uint4*>(p + i) = w[0];
+        *reinterpret_cast<uint4*>(p + 2 * i) = w[0];
     }
+}
+
+template <typename Tout>
+__device__ __forceinline__ void st16(Tout* p, const float* x) {
+    float2 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
+    st16(p, y);
 }
 
 // Tensor map of a strided bf16 [batch][head][token][d] array: boxes of 64 tokens x 64 columns

@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "gated.h"
 #include "launch.h"
+#include "packed2.cuh"
 #include "tc_common.cuh"
 
 namespace efla {
@@ -91,26 +92,6 @@ __device__ __forceinline__ void weights(const void* w, int c, int bf16, float* x
         }
     }
 }
-
-// two fp32 values an instruction
-__device__ __forceinline__ uint64_t u64(float2 a) { return *reinterpret_cast<const uint64_t*>(&a); }
-__device__ __forceinline__ float2 f2(uint64_t a) { return *reinterpret_cast<const float2*>(&a); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)), "l"(u64(c)));
-    return f2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
-    return f2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
-    return f2(r);
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 __device__ unsigned int g_nm_status = 0;   // bit 0: a bounded wait expired
 
