@@ -236,29 +236,38 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
 }
 
 // ------------------------------------------------------------------ forward scan
-// Per chunk, with S [dk][N] (fp32 registers: 8 warps, thread = row x N/2 columns):
+// Per chunk and chain, with S [dk][32] in fp32 registers (8 warps, thread = row x 16 columns):
 //   S as parts -> shared memory;  D1 = [K; Q] S           (lanes 0..63 K S, 64..127 Q S)
 //   X = alpha (V - e^c K S)  as parts;  D2 = [T; P T] X    (U, P U)
 //   o = e^c Q S + P U  (the warps of lanes 64..127)
 //   U e^{c_last - c} as parts;  D3 = K^T (..);  S = e^{c_last} S + D3
-// A ninth warp issues the copies (one chunk ahead) and the products.
-constexpr int kScThreads = 288;
-
-template <int NP, int N>
+// Each chain has a warp that issues its products; one more copies the chunks in, one ahead.
+//
+// REC is the backward's recording pass: no queries and no o; the parts of every chunk's entering
+// S, and of its U, go out as they lie in shared memory (a warp of its own copies them).  U's parts
+// take X's place once the chunk's last product has read it, while the next chunk's first one runs.
+//
+// Bound by the latency of the chain of three products and three epilogues a chunk: see the
+// measurements at launch.
+template <int NP, int NCH, bool REC>
 struct ScanSmem {
-    static constexpr int TPS = NP == 2 ? 2 : 1;                      // stages of the [T; P T] image
-    static constexpr uint32_t KQ = 0;                                // 2 stages x 2 blocks of 64 dk x [K rows | Q rows]
-    static constexpr uint32_t TP = 65536;
-    static constexpr uint32_t V = TP + TPS * NP * 16384;             // 2 stages
-    // part p, column j of an operand is column p N + j: blocks of 64 columns, one after another
-    static constexpr int BLK = (NP * N + 63) / 64;
-    static constexpr uint32_t S = V + 2 * 8192;                      // BLK x [128 rows][64]
-    static constexpr uint32_t X = S + BLK * 16384;                   // BLK x [64 rows][64]
-    static constexpr uint32_t VEC = X + BLK * 8192;                  // 2 stages
+    using C = Chain<NP, NCH>;
+    static constexpr int TPS = NP == 2 || REC ? 2 : 1;               // stages of the image
+    static constexpr uint32_t KQB = REC ? 8192 : 16384;              // a 64-dk block: K rows (and Q rows)
+    static constexpr uint32_t TPB = REC ? 8192 : 16384;              // an image part: T rows (and P T rows)
+    static constexpr uint32_t KQ = 0;                                // 2 stages x 2 blocks
+    static constexpr uint32_t TP = 4 * KQB;
+    static constexpr uint32_t V = TP + TPS * NP * TPB;               // 2 stages
+    static constexpr uint32_t S = V + 2 * 8192;                      // blocks of 128 rows
+    static constexpr uint32_t X = S + C::blocks * 16384;             // blocks of 64 rows
+    static constexpr uint32_t VEC = X + C::blocks * 8192;            // 2 stages
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
-    static constexpr size_t bytes = 1024 + BAR + 128;
+    static constexpr int bars = 4 + 2 + TPS + 1 + 9 * NCH;
+    static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
+    static constexpr int warps = 9 * NCH + 1 + (REC ? 1 : 0);
 };
-static_assert(ScanSmem<2, 64>::bytes <= 232448 && ScanSmem<3, 64>::bytes <= 232448, "shared memory per CTA");
+static_assert(ScanSmem<2, 2, false>::bytes <= 232448 && ScanSmem<3, 2, false>::bytes <= 232448 &&
+              ScanSmem<3, 2, true>::bytes <= 232448, "shared memory per CTA");
 
 struct ScanArgs {
     const unsigned char* img;
@@ -267,289 +276,279 @@ struct ScanArgs {
     void* o;
     float* S_final;
     int slots;
-    float* rec_S;   // [H][slots][dk][dv]
-    float* rec_U;   // [H][slots][64][dv]
+    unsigned char* rec_S;   // [H][slots][slices][kRecS]
+    unsigned char* rec_U;   // [H][slots][slices][kRecU]
 };
 
-// REC: the backward's pass, which writes no o but records every chunk's entering state and U (fp32).
-template <int NP, int N, typename Tout, bool REC>
-__global__ void __launch_bounds__(kScThreads, 1) k_gt_scan(GDims d, ScanArgs a, const __grid_constant__ CUtensorMap tm_q,
-                                                           const __grid_constant__ CUtensorMap tm_k,
-                                                           const __grid_constant__ CUtensorMap tm_v) {
-    using M = ScanSmem<NP, N>;
-    constexpr int NC = N / 2;   // columns a thread
+template <int NP, int NCH, typename Tout, bool REC>
+__global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
+    k_gt_scan(GDims d, ScanArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v) {
+    using M = ScanSmem<NP, NCH, REC>;
+    using C = Chain<NP, NCH>;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    uint64_t* full = (uint64_t*)(sm + M::BAR);   // [2] K, Q, V, vectors
-    uint64_t* full_tp = full + 2;                // [2]
-    uint64_t* s_ready = full + 4;
-    uint64_t* x_ready = full + 5;
-    uint64_t* u_ready = full + 6;
-    uint64_t* d1 = full + 7;
-    uint64_t* d2 = full + 8;
-    uint64_t* d3 = full + 9;
-    uint32_t* tslot = (uint32_t*)(full + 10);
-    const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * N;
+    uint64_t* bars = (uint64_t*)(sm + M::BAR);
+    uint64_t* full = bars;               // [2] K, Q, V, vectors
+    uint64_t* freed = bars + 2;          // [2] by every chain
+    uint64_t* full_tp = bars + 4;        // [TPS]
+    uint64_t* freed_tp = full_tp + M::TPS;   // by every chain (one stage only)
+    uint64_t* s_free = freed_tp + 1;     // REC: S's and U's parts have been copied out
+    uint64_t* x_free = s_free + 1;
+    uint64_t* chain0 = x_free + 1;       // per chain: s_ready, x_ready, u_ready, r_ready (REC: U's parts), d1, d2, d3
+    uint32_t* tslot = (uint32_t*)(bars + M::bars);
+    const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * 32 * NCH;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SeqAt s = seq_at(d, b, kGC);
     const int nch = (s.len + kGC - 1) / kGC;
     const size_t rec0 = (size_t)h * a.slots + s.slot0;
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(full + i, 1);
-        mbar_init(s_ready, 8);   // warps
-        mbar_init(x_ready, 4);
-        mbar_init(u_ready, 8);
-        mbar_init(d1, 1);
-        mbar_init(d2, 1);
-        mbar_init(d3, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&freed[i], NCH);
+        }
+        for (int i = 0; i < M::TPS; ++i) mbar_init(&full_tp[i], 1);
+        mbar_init(freed_tp, NCH);
+        mbar_init(s_free, 1);
+        mbar_init(x_free, 1);
+        for (int g = 0; g < NCH; ++g) {
+            uint64_t* q = chain0 + 9 * g;
+            mbar_init(q + 0, 8);               // s_ready (warps)
+            mbar_init(q + 1, 4);               // x_ready
+            mbar_init(q + 2, REC ? 4 : 8);     // u_ready
+            mbar_init(q + 3, 4);               // r_ready
+            for (int i = 4; i < 7; ++i) mbar_init(q + i, 1);
+        }
         fence_mbar_init();
     }
-    if (warp == 8) {
-        tmem_alloc(tslot, 512);
+    if (warp == 8 * NCH) {
+        tmem_alloc(tslot, NCH * 256);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tb = *tslot, t1 = tb, t2 = tb + 256, t3 = tb;   // D3 over D1: every warp has read D1 by then
+    const uint32_t tb = *tslot;
 
-    if (warp == 8) {
+    if (warp >= 8 * NCH) {
         if (lane == 0 && nch > 0) {
-            // ---------------- copies and products
-            int issued = 0, issued_tp = 0;   // chunks whose copies are under way
-            const auto load = [&](int c) {
-                unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
-                uint64_t* f = &full[c & 1];
-                const int t = s.start + c * kGC;
-                mbar_arrive_expect_tx(f, 5u * 8192u + (uint32_t)sizeof(GVec));
-                for (int blk = 0; blk < 2; ++blk) {
-                    tma_load_4d(kq + blk * 16384, &tm_k, 64 * blk, t, hk, s.batch, f);
-                    tma_load_4d(kq + blk * 16384 + 8192, &tm_q, 64 * blk, t, hk, s.batch, f);
-                }
-                tma_load_4d(sm + M::V + (c & 1) * 8192, &tm_v, c0, t, h, s.batch, f);
-                bulk_g2s(sm + M::VEC + (c & 1) * sizeof(GVec), a.vec + rec0 + c, sizeof(GVec), f);
-                issued = c + 1;
-            };
-            const auto load_tp = [&](int c) {
-                uint64_t* f = &full_tp[c % M::TPS];
-                mbar_arrive_expect_tx(f, NP * 16384u);
-                bulk_g2s(sm + M::TP + (c % M::TPS) * NP * 16384, a.img + (rec0 + c) * NP * 16384, NP * 16384u, f);
-                issued_tp = c + 1;
-            };
-            // The products take the operands' parts side by side along N (D keeps a column group for
-            // each part of B; the epilogues add them): an instruction costs about 43 cycles up to
-            // N = 64, 60 at 128 and 91 at 192, so NP parts in one cost less than NP instructions.
-            const int nblk = (d.dk + 63) / 64;
-            const uint32_t id_kt = idesc_f16(128, NP * N, true, true, true);   // A, B MN-major
-            const uint64_t dS = sdesc_sw128(smem_u32(sm + M::S), 16384), dX = sdesc_sw128(smem_u32(sm + M::X), 8192);
-            load(0);
-            load_tp(0);
             bool ok = true;
-            for (int c = 0; c < nch && ok; ++c) {
-                const uint32_t ph = c & 1;
-                unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
-                ok = mbar_wait(s_ready, ph, kWaitLimit);
-                if (!ok) break;
-                ok = mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
-                if (!ok) break;
-                tc_fence_after();
-                {
-                    const uint64_t a0 = sdesc_sw128(smem_u32(kq));
+            if (warp == 9 * NCH) {
+                // ---------------- copies in
+                int n_kq = 0, n_tp = 0;   // chunks whose copies are under way
+                const auto load = [&](int c) {
+                    unsigned char* kq = sm + M::KQ + (c & 1) * 2 * M::KQB;
+                    uint64_t* f = &full[c & 1];
+                    const int t = s.start + c * kGC;
+                    mbar_arrive_expect_tx(f, (REC ? 3u : 5u) * 8192u + (uint32_t)sizeof(GVec));
+                    for (int blk = 0; blk < 2; ++blk) {
+                        tma_load_4d(kq + blk * M::KQB, &tm_k, 64 * blk, t, hk, s.batch, f);
+                        if (!REC) tma_load_4d(kq + blk * M::KQB + 8192, &tm_q, 64 * blk, t, hk, s.batch, f);
+                    }
+                    tma_load_4d(sm + M::V + (c & 1) * 8192, &tm_v, c0, t, h, s.batch, f);
+                    bulk_g2s(sm + M::VEC + (c & 1) * sizeof(GVec), a.vec + rec0 + c, sizeof(GVec), f);
+                    n_kq = c + 1;
+                };
+                const auto load_tp = [&](int c) {
+                    uint64_t* f = &full_tp[c % M::TPS];
+                    unsigned char* to = sm + M::TP + (c % M::TPS) * NP * M::TPB;
+                    const unsigned char* from = a.img + (rec0 + c) * NP * 16384;
+                    mbar_arrive_expect_tx(f, NP * M::TPB);
+                    if (REC) {
+                        for (int p = 0; p < NP; ++p) bulk_g2s(to + p * M::TPB, from + p * 16384, M::TPB, f);
+                    } else {
+                        bulk_g2s(to, from, NP * M::TPB, f);
+                    }
+                    n_tp = c + 1;
+                };
+                load(0);
+                load_tp(0);
+                if (nch > 1) {
+                    load(1);
+                    if (M::TPS == 2) load_tp(1);
+                }
+                for (int c = 0; c + 1 < nch && ok; ++c) {
+                    if (M::TPS == 1) {   // the image's stage is free once every chain has chunk c's D2
+                        ok = mbar_wait(freed_tp, c & 1, kWaitLimit);
+                        if (ok) load_tp(c + 1);
+                    }
+                    if (ok && c + 2 < nch) {
+                        ok = mbar_wait(&freed[c & 1], (c >> 1) & 1, kWaitLimit);
+                        if (!ok) break;
+                        load(c + 2);
+                        if (M::TPS == 2) load_tp(c + 2);
+                    }
+                }
+                if (!ok)   // a wait gave up: the copies under way land before the CTA ends
+                    for (int i = 0; i < 2; ++i) {
+                        if (n_kq > i) mbar_wait(&full[(n_kq - 1 - i) & 1], ((n_kq - 1 - i) >> 1) & 1, kWaitLimit);
+                        if (n_tp > i && i < M::TPS)
+                            mbar_wait(&full_tp[(n_tp - 1 - i) % M::TPS], ((n_tp - 1 - i) / M::TPS) & 1, kWaitLimit);
+                    }
+            } else if (REC && warp == 9 * NCH + 1) {
+                // ---------------- copies out
+                for (int c = 0; c <= nch && ok; ++c) {
+                    const uint32_t ph = c & 1;
+                    if (c < nch) {
+                        for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g, ph, kWaitLimit);
+                        if (!ok) break;
+                        unsigned char* to = a.rec_S + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecS;
+                        bulk_s2g(to, sm + M::S, kRecS);
+                        bulk_commit();
+                    }
+                    if (c > 0) {   // the chunk before's U
+                        for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g + 3, ph ^ 1u, kWaitLimit);
+                        if (!ok) break;
+                        unsigned char* to = a.rec_U + ((rec0 + c - 1) * gridDim.y + blockIdx.y) * kRecU;
+                        bulk_s2g(to, sm + M::X, kRecU);
+                        bulk_commit();
+                    }
+                    bulk_wait_read();
+                    mbar_arrive(s_free);
+                    mbar_arrive(x_free);
+                }
+                bulk_wait_read();
+            } else if (warp < 9 * NCH) {
+                // ---------------- a chain's products
+                const int g = warp - 8 * NCH;
+                uint64_t* q = chain0 + 9 * g;
+                const uint32_t t1 = tb + g * 256, t2 = t1 + 128, t3 = t1;   // D3 over D1, which is read by then
+                const int nblk = (d.dk + 63) / 64;
+                const uint64_t dS = sdesc_sw128(smem_u32(sm + M::S + g * 16384), NP == 3 ? C::lbo(g, 16384) : 16384);
+                const uint64_t dX = sdesc_sw128(smem_u32(sm + M::X + g * 8192), NP == 3 ? C::lbo(g, 8192) : 8192);
+                for (int c = 0; c < nch; ++c) {
+                    const uint32_t ph = c & 1;
+                    const uint32_t kq = smem_u32(sm + M::KQ + (c & 1) * 2 * M::KQB);
+                    const uint64_t ka = sdesc_sw128(kq), km = sdesc_sw128(kq, M::KQB);
+                    const uint64_t ta = sdesc_sw128(smem_u32(sm + M::TP + (c % M::TPS) * NP * M::TPB));
+                    if (!(ok = mbar_wait(q, ph, kWaitLimit) && mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit))) break;
+                    if (c > 0) mbar_arrive(&freed[(c - 1) & 1]);   // the chunk before: every product and epilogue is over
+                    tc_fence_after();
 #pragma unroll 1
                     for (int blk = 0; blk < nblk; ++blk)   // (64 dk at a time, zeros past dk: no branch per instruction)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(t1, a0 + blk * 1024 + ks * 2, dS + blk * 512 + ks * 128,
-                                       idesc_f16(128, NP * N, false, true, true), blk + ks > 0);
-                }
-                mma_commit(d1);
-                if (c + 1 < nch) {   // (the stage's last readers were chunk c - 1's)
-                    load(c + 1);
-                    if (M::TPS == 2) load_tp(c + 1);
-                }
-                ok = mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit) && mbar_wait(x_ready, ph, kWaitLimit);
-                if (!ok) break;
-                tc_fence_after();
-                {
-                    const uint64_t a0 = sdesc_sw128(smem_u32(sm + M::TP + (c % M::TPS) * NP * 16384));
+                            mma_f16_ss(t1, ka + blk * (M::KQB >> 4) + ks * 2, dS + blk * 512 + ks * 128,
+                                       idesc_f16(128, NP * 32, false, true, true), blk + ks > 0);
+                    mma_commit(q + 4);
+                    if (!(ok = mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit) &&
+                               mbar_wait(q + 1, ph, kWaitLimit))) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int p = 0; p < NP; ++p)   // with the part pairs p + x < NP
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(t2, a0 + p * 1024 + ks * 2, dX + ks * 128,
-                                       idesc_f16(128, (NP - p) * N, false, true, true), p + ks > 0);
-                }
-                mma_commit(d2);
-                ok = mbar_wait(u_ready, ph, kWaitLimit);
-                if (!ok) break;
-                tc_fence_after();
-                if (M::TPS == 1 && c + 1 < nch) load_tp(c + 1);   // (D2 is done: u_ready came from it)
-                {
-                    const uint64_t a0 = sdesc_sw128(smem_u32(kq), 16384);
+                            mma_f16_ss(t2, ta + p * (M::TPB >> 4) + ks * 2, dX + ks * 128,
+                                       idesc_f16(128, (NP - p) * 32, false, true, true), p + ks > 0);
+                    mma_commit(q + 5);
+                    if (!(ok = mbar_wait(q + 2, ph, kWaitLimit))) break;
+                    if (M::TPS == 1) mbar_arrive(freed_tp);
+                    tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) mma_f16_ss(t3, a0 + ks * 128, dX + ks * 128, id_kt, ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16_ss(t3, km + ks * 128, dX + ks * 128, idesc_f16(128, NP * 32, true, true, true), ks > 0);
+                    mma_commit(q + 6);
                 }
-                mma_commit(d3);
             }
-            if (!ok) {   // a wait gave up: the copies under way land before the CTA ends
-                atomicOr(&g_gt2_status, 1u);
-                for (int c = issued > 1 ? issued - 2 : 0; c < issued; ++c) mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit);
-                for (int c = issued_tp > M::TPS ? issued_tp - M::TPS : 0; c < issued_tp; ++c)
-                    mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit);
-            }
+            if (!ok) atomicOr(&g_gt2_status, 1u);
         }
     } else {
         // ---------------- the state and the epilogues
-        const int row = 32 * (warp & 3) + lane, half = warp >> 2, cc = half * NC;   // columns cc .. cc + NC - 1 of the slice
-        const int i = row & 63;                                                      // token of lanes 0..63 and of 64..127
-        const bool top = row < 64;
-        const int nv = min(max(d.dv - c0 - cc, 0), NC);                              // columns of these that exist
-        const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + c0 + cc;
-        const uint32_t lq = 32 * (warp & 3);
-        // 8 values of `r`, column cc + e of the slice, as parts into an operand of 64-column blocks
-        const auto put = [&](uint32_t base, uint32_t blk, int r, int e, const float2* x) {
-            uint4 w[NP];
-            split8<NP>(x, w);
+        const int g = warp >> 3, row = 32 * (warp & 3) + lane, cc = ((warp >> 2) & 1) * 16;   // 16 columns from cc of the chain
+        const int i = row & 63, col = c0 + g * 32 + cc;                                      // token of the lane; first column
+        const bool top = row < 64, in = col < d.dv;
+        uint64_t* q = chain0 + 9 * g;
+        const uint32_t lq = taddr(tb, 32 * (warp & 3), g * 256 + cc), t1 = lq, t2 = lq + 128, t3 = lq;
+        const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + col;
+        float2 S[8], U[8];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const int j = p * N + cc + e;
-                *reinterpret_cast<uint4*>(sm + base + (j >> 6) * blk + sw128(r, j & 63)) = w[p];
-            }
-        };
-        const auto arrive = [&](uint64_t* bar) {   // a warp's shared-memory writes and tensor-memory reads are done
-            fence_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-        };
-        // (the warp leaves together if a wait gives up)
-        const auto wait = [&](uint64_t* bar, uint32_t ph) { return __all_sync(0xffffffffu, mbar_wait(bar, ph, kWaitLimit)) != 0; };
-        float2 S[NC / 2];
-#pragma unroll
-        for (int e = 0; e < NC; e += 4) {
-            const float4 x = a.S0 && row < d.dk && e < nv ? *reinterpret_cast<const float4*>(a.S0 + sb + e)
-                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[e / 2] = make_float2(x.x, x.y);
-            S[e / 2 + 1] = make_float2(x.z, x.w);
+        for (int e = 0; e < 8; e += 2) {
+            const float4 x = a.S0 && row < d.dk && in ? *reinterpret_cast<const float4*>(a.S0 + sb + 2 * e)
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[e] = make_float2(x.x, x.y);
+            S[e + 1] = make_float2(x.z, x.w);
+            U[e] = U[e + 1] = both(0.f);
         }
         bool ok = true;
-        for (int c = 0; c < nch && ok; ++c) {
+        for (int c = 0; c < nch; ++c) {
             const uint32_t ph = c & 1;
             const int n = min(kGC, s.len - c * kGC);
             const GVec* vec = (const GVec*)(sm + M::VEC + (c & 1) * sizeof(GVec));
-#pragma unroll
-            for (int e = 0; e < NC; e += 8) put(M::S, 16384, row, e, S + e / 2);
+            if (REC && c > 0 && !(ok = warp_wait(s_free, ph ^ 1u))) break;
+            C::put16(sm + M::S, 16384, g, row, cc, S);
             if (d.packed && n < kGC) {   // rows past the sequence are another's: zero its keys (0 x NaN is not 0)
-                ok = wait(&full[c & 1], (c >> 1) & 1);
-                unsigned char* kq = sm + M::KQ + (c & 1) * 32768;
-                for (int e = tid; e < (kGC - n) * 16; e += 256)
-                    *reinterpret_cast<uint4*>(kq + (e & 1) * 16384 + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16) =
+                if (!(ok = warp_wait(&full[c & 1], (c >> 1) & 1))) break;
+                unsigned char* kq = sm + M::KQ + (c & 1) * 2 * M::KQB;
+                for (int e = tid & 255; e < (kGC - n) * 16; e += 256)   // (every chain: the same zeros)
+                    *reinterpret_cast<uint4*>(kq + (e & 1) * M::KQB + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
-            arrive(s_ready);
-            if (REC && row < d.dk) {
-                float* rs = a.rec_S + ((rec0 + c) * d.dk + row) * d.dv + c0 + cc;
-#pragma unroll
-                for (int e = 0; e < NC; e += 16)
-                    if (e < nv) st16(rs + e, S + e / 2);
+            warp_arrive(q, lane);
+            if (REC && top && c > 0) {   // the chunk before's U, in X's place
+                C::put16(sm + M::X, 8192, g, i, cc, U);
+                warp_arrive(q + 3, lane);
             }
-            ok = ok && wait(&full[c & 1], (c >> 1) & 1);
-            if (!ok) break;
+            if (!(ok = warp_wait(&full[c & 1], (c >> 1) & 1))) break;
             const float up = vec->up[i], last = vec->up[63];
             if (top) {
                 // X = alpha V - (alpha e^c) K S; rows past the end are zero whatever lies there
                 const bool live = i < n;
                 const float2 al = both(vec->al[i]), au = both(-vec->al[i] * up), rest = both(vec->rest[i]);
                 const unsigned char* vt = sm + M::V + (c & 1) * 8192;
-                float2 v[NC / 2];
-#pragma unroll
-                for (int e = 0; e < NC; e += 8) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(vt + sw128(i, cc + e));
-                    v[e / 2] = mul2(al, bf16x2(w.x));
-                    v[e / 2 + 1] = mul2(al, bf16x2(w.y));
-                    v[e / 2 + 2] = mul2(al, bf16x2(w.z));
-                    v[e / 2 + 3] = mul2(al, bf16x2(w.w));
-                }
-                if (!(ok = wait(d1, ph))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < NC; e += 16) {
-                    float2 y[8];
-                    tmem_sum16<NP>(taddr(t1, lq, cc + e), N, y);
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        y[m] = fma2(au, y[m], v[e / 2 + m]);
-                        if (!live) y[m] = both(0.f);
-                    }
-                    put(M::X, 8192, i, e, y);
-                    put(M::X, 8192, i, e + 8, y + 4);
-                }
-                arrive(x_ready);
-                if (!(ok = wait(d2, ph))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < NC; e += 16) {
-                    float2 y[8];
-                    tmem_sum16<NP>(taddr(t2, lq, cc + e), N, y);
-                    if (REC) {
-#pragma unroll
-                        for (int m = 0; m < 8; ++m) v[e / 2 + m] = y[m];
-                    }
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) y[m] = mul2(rest, y[m]);
-                    put(M::X, 8192, i, e, y);
-                    put(M::X, 8192, i, e + 8, y + 4);
-                }
-                arrive(u_ready);
-                if (REC) {
-                    float* ru = a.rec_U + ((rec0 + c) * kGC + i) * d.dv + c0 + cc;
-#pragma unroll
-                    for (int e = 0; e < NC; e += 16)
-                        if (e < nv) st16(ru + e, v + e / 2);
-                }
-            } else {
-                if (!(ok = wait(d1, ph))) break;
-                tc_fence_after();
-                float2 qs[NC / 2];
-#pragma unroll
-                for (int e = 0; e < NC; e += 16) tmem_sum16<NP>(taddr(t1, lq, cc + e), N, *reinterpret_cast<float2(*)[8]>(qs + e / 2));
-                arrive(u_ready);
-                if (!(ok = wait(d2, ph))) break;
-                tc_fence_after();
-                if (!REC) {
-                    Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + c0 + cc;
-#pragma unroll
-                    for (int e = 0; e < NC; e += 16) {
-                        float2 y[8];
-                        tmem_sum16<NP>(taddr(t2, lq, cc + e), N, y);
-#pragma unroll
-                        for (int m = 0; m < 8; ++m) y[m] = fma2(both(up), qs[e / 2 + m], y[m]);
-                        if (i < n && e < nv) st16(op + e, y);
-                    }
-                }
-            }
-            if (!(ok = wait(d3, ph))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int e = 0; e < NC; e += 16) {
+                const uint4 v0 = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc));
+                const uint4 v1 = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc + 8));
+                float2 v[8] = {mul2(al, bf16x2(v0.x)), mul2(al, bf16x2(v0.y)), mul2(al, bf16x2(v0.z)), mul2(al, bf16x2(v0.w)),
+                               mul2(al, bf16x2(v1.x)), mul2(al, bf16x2(v1.y)), mul2(al, bf16x2(v1.z)), mul2(al, bf16x2(v1.w))};
+                if (REC && c > 0 && !(ok = warp_wait(x_free, ph))) break;
+                if (!(ok = warp_wait(q + 4, ph))) break;
                 float2 y[8];
-                tmem_sum16<NP>(taddr(t3, lq, cc + e), N, y);
+                tmem_sum16<NP>(t1, 32, y);
 #pragma unroll
-                for (int m = 0; m < 8; ++m) S[e / 2 + m] = fma2(both(last), S[e / 2 + m], y[m]);
+                for (int m = 0; m < 8; ++m) {
+                    y[m] = fma2(au, y[m], v[m]);
+                    if (!live) y[m] = both(0.f);
+                }
+                C::put16(sm + M::X, 8192, g, i, cc, y);
+                warp_arrive(q + 1, lane);
+                if (!(ok = warp_wait(q + 5, ph))) break;
+                tmem_sum16<NP>(t2, 32, U);
+#pragma unroll
+                for (int m = 0; m < 8; ++m) y[m] = mul2(rest, U[m]);
+                C::put16(sm + M::X, 8192, g, i, cc, y);
+                warp_arrive(q + 2, lane);
+            } else if (!REC) {
+                if (!(ok = warp_wait(q + 4, ph))) break;
+                float2 y[8], z[8];
+                tmem_sum16<NP>(t1, 32, y);
+                warp_arrive(q + 2, lane);
+                if (!(ok = warp_wait(q + 5, ph))) break;
+                tmem_sum16<NP>(t2, 32, z);
+#pragma unroll
+                for (int m = 0; m < 8; ++m) z[m] = fma2(both(up), y[m], z[m]);
+                if (i < n && in) {
+                    Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + col;
+                    if (dbg_in(op, 16 * sizeof(Tout), a.o, o_extent(d) * sizeof(Tout), &g_gt2_status)) st16(op, z);
+                }
             }
-        }
-        if (!ok) atomicOr(&g_gt2_status, 1u);
-        if (a.S_final && row < d.dk) {
+            if (!(ok = warp_wait(q + 6, ph))) break;
+            float2 y[8];
+            tmem_sum16<NP>(t3, 32, y);
 #pragma unroll
-            for (int e = 0; e < NC; e += 4)
-                if (e < nv) *reinterpret_cast<float4*>(a.S_final + sb + e) =
-                        make_float4(S[e / 2].x, S[e / 2].y, S[e / 2 + 1].x, S[e / 2 + 1].y);
+            for (int m = 0; m < 8; ++m) S[m] = fma2(both(last), S[m], y[m]);
         }
+        if (REC && ok && top && nch > 0) {   // the last chunk's U
+            C::put16(sm + M::X, 8192, g, i, cc, U);
+            warp_arrive(q + 3, lane);
+        }
+        if (!ok && lane == 0) atomicOr(&g_gt2_status, 1u);
+        if (a.S_final && row < d.dk && in &&
+            dbg_in(a.S_final + sb, 64, a.S_final, (size_t)d.B * d.H * d.dk * d.dv * 4, &g_gt2_status))
+            st16(a.S_final + sb, S);
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tb, 512);
+    if (warp == 8 * NCH) tmem_dealloc(tb, NCH * 256);
 }
 
 struct TcWs {
@@ -579,12 +578,13 @@ cudaError_t make_maps(const GDims& d, const void* q, const void* k, const void* 
     return e;
 }
 
-template <int NP, int N, typename Tout, bool REC = false>
+template <int NP, int NCH, typename Tout, bool REC = false>
 cudaError_t scan(const GDims& d, const ScanArgs& a, const Maps& m, cudaStream_t st) {
-    constexpr size_t bytes = ScanSmem<NP, N>::bytes;
-    cudaError_t e = smem_attr(k_gt_scan<NP, N, Tout, REC>, bytes);
+    using M = ScanSmem<NP, NCH, REC>;
+    const auto k = k_gt_scan<NP, NCH, Tout, REC>;
+    cudaError_t e = smem_attr(k, M::bytes);
     if (e != cudaSuccess) return e;
-    k_gt_scan<NP, N, Tout, REC><<<dim3((unsigned)d.BH(), (d.dv + N - 1) / N), kScThreads, bytes, st>>>(d, a, m.q, m.k, m.v);
+    k<<<dim3((unsigned)d.BH(), (d.dv + 32 * NCH - 1) / (32 * NCH)), M::warps * 32, M::bytes, st>>>(d, a, m.q, m.k, m.v);
     prof_mark(REC ? "gated_record_tc" : "gated_scan_tc", st);
     return cudaGetLastError();
 }
@@ -611,7 +611,7 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
     if (e == cudaSuccess) e = prep<NP>(d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f}, m, st);
     if (e != cudaSuccess) return e;
     const ScanArgs a{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr};
-    return narrow ? scan<NP, 32, Tout>(d, a, m, st) : scan<NP, 64, Tout>(d, a, m, st);
+    return narrow ? scan<NP, 1, Tout>(d, a, m, st) : scan<NP, 2, Tout>(d, a, m, st);
 }
 
 }  // namespace
@@ -643,15 +643,12 @@ cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, c
 }
 
 cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
-                                   const unsigned char* img, const GVec* vec, float* rec_S, float* rec_U,
+                                   const unsigned char* img, const GVec* vec, unsigned char* rec_S, unsigned char* rec_U,
                                    cudaStream_t st) {
     Maps m{};
-    bool narrow = false;
-    cudaError_t e = make_maps(d, q, k, v, &m);
-    if (e == cudaSuccess) e = narrow_slices(d, &narrow);
+    const cudaError_t e = make_maps(d, q, k, v, &m);
     if (e != cudaSuccess) return e;
-    const ScanArgs a{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U};
-    return narrow ? scan<3, 32, float, true>(d, a, m, st) : scan<3, 64, float, true>(d, a, m, st);
+    return scan<3, 2, float, true>(d, ScanArgs{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U}, m, st);
 }
 
 cudaError_t gated_tc_status_read_clear(unsigned int* status) {

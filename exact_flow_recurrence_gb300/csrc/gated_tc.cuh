@@ -18,6 +18,12 @@
 namespace efla {
 
 constexpr int kGC = 64;   // tokens a chunk of the tensor-core kernels
+constexpr uint32_t kRecS = 3 * 16384, kRecU = 3 * 8192;   // bytes of a recorded slice
+
+// Elements from the first to the last of o (debug builds' bounds).
+__device__ __forceinline__ size_t o_extent(const GDims& d) {
+    return (d.packed ? 0 : (d.B - 1) * d.os[0]) + (d.H - 1) * d.os[1] + (d.L - 1) * d.os[2] + d.dv;
+}
 
 // What the preparation leaves of a chunk and value head besides the T, P T image: five vectors.
 struct GVec {
@@ -60,6 +66,26 @@ __device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
     split8<NP>(y, w);
 }
 
+// A scan CTA runs NCH chains of 32 state columns each: their products and epilogues are
+// independent, so that one chain's products run while the other's epilogue does.  A computed
+// operand of 32 columns lies in blocks of 128-byte rows (64 columns; R rows, BLK = 128 R bytes):
+//   block g < NCH   chain g's part 0 | part 1        block NCH   chain 0's part 2 | chain 1's
+// so that its parts are neighbours along N and one product takes them all (D keeps a column
+// group for each; the epilogues add them).  An instruction costs about 43 cycles up to N = 64
+// and 50 at N = 96: three parts in one cost little more than one.
+template <int NP, int NCH>
+struct Chain {
+    static constexpr int N = 32;
+    static constexpr int blocks = NCH + (NP == 3 ? 1 : 0);
+    // byte offset of part p's first column, and the stride to the block that holds part 2
+    __host__ __device__ static constexpr uint32_t part(int g, int p, uint32_t blk) {
+        return p < 2 ? g * blk + p * 64 : NCH * blk + g * 64;
+    }
+    __host__ __device__ static constexpr uint32_t lbo(int g, uint32_t blk) { return (NCH - g) * blk + g * 64; }
+    // 16 values of row r, columns cc .. cc + 15 of chain g
+    static __device__ __forceinline__ void put16(unsigned char* base, uint32_t blk, int g, int r, int cc, const float2 (&x)[8]);
+};
+
 // 16 columns of this warp's lanes of an accumulator, summed over G column groups `gap` apart
 // (the last one first: it holds the small parts' products)
 template <int G>
@@ -76,6 +102,33 @@ __device__ __forceinline__ void tmem_sum16(uint32_t t, int gap, float2 (&y)[8]) 
 #pragma unroll
         for (int p = G - 2; p >= 0; --p) y[m] = add2(y[m], make_float2(x[p][2 * m], x[p][2 * m + 1]));
     }
+}
+
+template <int NP, int NCH>
+__device__ __forceinline__ void Chain<NP, NCH>::put16(unsigned char* base, uint32_t blk, int g, int r, int cc,
+                                                      const float2 (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 8) {
+        uint4 w[NP];
+        split8<NP>(x + e / 2, w);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            *reinterpret_cast<uint4*>(base + (p < 2 ? g : NCH) * blk + sw128(r, (p < 2 ? p : g) * 32 + cc + e)) = w[p];
+    }
+}
+
+// A warp's shared-memory writes and tensor-memory reads are done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    fence_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+// (the warp leaves together if a wait gives up)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t ph) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, ph, kWaitLimit)) != 0;
+    tc_fence_after();
+    return ok;
 }
 
 template <typename Tout>
@@ -148,7 +201,7 @@ inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
 cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
                                  float floor_alpha, unsigned char* img, GVec* vec, cudaStream_t st);
 cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
-                                   const unsigned char* img, const GVec* vec, float* rec_S, float* rec_U,
+                                   const unsigned char* img, const GVec* vec, unsigned char* rec_S, unsigned char* rec_U,
                                    cudaStream_t st);
 
 }  // namespace efla
