@@ -33,19 +33,19 @@ constexpr float kFloorAlpha = 1e-25f;
 //   D1 = [K; Q] G  (lanes 0..63: K G);   E = e^c dO as parts (the warps of lanes 64..127)
 //   D2 = (P T)^T dO + T^T Y,  Y = e^{c_last - c} K G as parts;   dX = D2
 //   D3 = Q^T E + K^T Z,  Z = -alpha e^c dX as parts;   G = e^{c_last} G + D3
-// dv = alpha dX goes out here.  G's parts, and dX's (in Z's place, once the chunk's last product
-// has read it), are copied out as they lie in shared memory.
+// dv = alpha dX goes out here.  G's parts, and dX's (in E's place, once Q^T E has read it), are
+// copied out as they lie in shared memory.
 struct Rs {
     using C = Chain<NP, 2>;
     static constexpr uint32_t KQ = 0;                     // 2 stages x 2 blocks x [K rows | Q rows]
     static constexpr uint32_t TP = 65536;                 // [T; P T], NP parts, one stage
     static constexpr uint32_t DO = TP + NP * 16384;       // 2 stages
     static constexpr uint32_t G = DO + 2 * 8192;          // 3 blocks of 128 rows
-    static constexpr uint32_t X = G + 3 * 16384;          // 3 blocks of 64 rows: Y, then Z, then dX
-    static constexpr uint32_t E = X + 3 * 8192;
+    static constexpr uint32_t X = G + 3 * 16384;          // 3 blocks of 64 rows: Y, then Z
+    static constexpr uint32_t E = X + 3 * 8192;           // E, then dX
     static constexpr uint32_t VEC = E + 3 * 8192;         // 2 stages of up, rest, al
     static constexpr uint32_t BAR = VEC + 2 * 768;
-    static constexpr int bars = 8 + 2 * 8;
+    static constexpr int bars = 8 + 2 * 10;
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
     static constexpr int warps = 20;                      // 16 epilogue, 2 products, copies in, copies out
 };
@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
     uint64_t* full_tp = bars + 4;
     uint64_t* freed_tp = bars + 5;    // by both chains
     uint64_t* g_free = bars + 6;      // G's and dX's parts have been copied out
-    uint64_t* x_free = bars + 7;
-    uint64_t* chain0 = bars + 8;      // per chain: g_ready, y_ready, z_ready, r_ready (dX's parts), e_ready, d1, d2, d3
+    uint64_t* e_free = bars + 7;
+    uint64_t* chain0 = bars + 8;      // per chain: g_ready, y_ready, z_ready, r_ready (dX's parts), e_ready, d1, d2, d3, turn, d_e (Q^T E)
     uint32_t* tslot = (uint32_t*)(bars + M::bars);
     const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * 64;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -93,12 +93,12 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
         mbar_init(full_tp, 1);
         mbar_init(freed_tp, 2);
         mbar_init(g_free, 1);
-        mbar_init(x_free, 1);
+        mbar_init(e_free, 1);
         for (int g = 0; g < 2; ++g) {
-            uint64_t* q = chain0 + 8 * g;
+            uint64_t* q = chain0 + 10 * g;
             mbar_init(q, 8);   // warps
             for (int i = 1; i < 5; ++i) mbar_init(q + i, 4);
-            for (int i = 5; i < 8; ++i) mbar_init(q + i, 1);
+            for (int i = 5; i < 10; ++i) mbar_init(q + i, 1);
         }
         fence_mbar_init();
     }
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
     const uint32_t tb = *tslot;
 
     if (warp >= 16) {
-        if (lane == 0 && nch > 0) {
-            bool ok = true;
+        bool ok = true;
+        if (warp >= 18 && lane == 0 && nch > 0) {
             if (warp == 18) {
                 // ---------------- copies in (it counts the chunks from the sequence's end)
                 int n_kq = 0, n_tp = 0;
@@ -151,33 +151,32 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                         if (n_kq > i) mbar_wait(&full[(n_kq - 1 - i) & 1], ((n_kq - 1 - i) >> 1) & 1, kWaitLimit);
                     if (n_tp) mbar_wait(full_tp, (n_tp - 1) & 1, kWaitLimit);
                 }
-            } else if (warp == 19) {
+            } else {
                 // ---------------- copies out
-                for (int it = 0; it <= nch && ok; ++it) {
+                for (int it = 0; it < nch; ++it) {
                     const uint32_t ph = it & 1;
-                    if (it < nch) {
-                        ok = mbar_wait(chain0, ph, kWaitLimit) && mbar_wait(chain0 + 8, ph, kWaitLimit);
-                        if (!ok) break;
-                        bulk_s2g(a.rec_G + ((rec0 + nch - 1 - it) * gridDim.y + blockIdx.y) * kRecS, sm + M::G, kRecS);
-                        bulk_commit();
-                    }
-                    if (it > 0) {   // the dX of the chunk before
-                        ok = mbar_wait(chain0 + 3, ph ^ 1u, kWaitLimit) && mbar_wait(chain0 + 11, ph ^ 1u, kWaitLimit);
-                        if (!ok) break;
-                        bulk_s2g(a.rec_dX + ((rec0 + nch - it) * gridDim.y + blockIdx.y) * kRecU, sm + M::X, kRecU);
-                        bulk_commit();
-                    }
-                    bulk_wait_read();
+                    const size_t rec = (rec0 + nch - 1 - it) * gridDim.y + blockIdx.y;
+                    ok = mbar_wait(chain0, ph, kWaitLimit) && mbar_wait(chain0 + 10, ph, kWaitLimit);
+                    if (!ok) break;
+                    bulk_s2g(a.rec_G + rec * kRecS, sm + M::G, kRecS);
+                    bulk_commit();
+                    bulk_wait_read();   // (and the dX of the chunk before)
                     mbar_arrive(g_free);
-                    mbar_arrive(x_free);
+                    if (it > 0) mbar_arrive(e_free);
+                    ok = mbar_wait(chain0 + 3, ph, kWaitLimit) && mbar_wait(chain0 + 13, ph, kWaitLimit);
+                    if (!ok) break;
+                    bulk_s2g(a.rec_dX + rec * kRecU, sm + M::E, kRecU);
+                    bulk_commit();
                 }
                 bulk_wait_read();
-            } else {
+            }
+        } else if (warp < 18) {
                 // ---------------- a chain's products
                 const int g = warp - 16;
-                uint64_t* q = chain0 + 8 * g;
+                uint64_t* q = chain0 + 10 * g;
                 const uint32_t t1 = tb + g * 256, t2 = t1 + 96, t3 = t1;   // D3 over D1, which is read by then
                 const int nblk = (d.dk + 63) / 64;
+                const bool one = elect_one();
                 const uint64_t dG = sdesc_sw128(smem_u32(sm + M::G + g * 16384), C::lbo(g, 16384));
                 const uint64_t dX = sdesc_sw128(smem_u32(sm + M::X + g * 8192), C::lbo(g, 8192));
                 const uint64_t dE = sdesc_sw128(smem_u32(sm + M::E + g * 8192), C::lbo(g, 8192));
@@ -191,64 +190,72 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     const uint32_t kq = smem_u32(sm + M::KQ + (it & 1) * 32768);
                     const uint64_t ka = sdesc_sw128(kq), km = sdesc_sw128(kq, 16384);
                     const uint64_t dDO = sdesc_sw128(smem_u32(sm + M::DO + (it & 1) * 8192)) + g * 4;   // 32 columns in
-                    if (!(ok = mbar_wait(q, ph, kWaitLimit) && mbar_wait(&full[it & 1], (it >> 1) & 1, kWaitLimit))) break;
-                    if (it > 0) mbar_arrive(&freed[(it - 1) & 1]);
-                    tc_fence_after();
+                    if (!(ok = warp_wait(q, ph) && warp_wait(&full[it & 1], (it >> 1) & 1))) break;
+                    if (it > 0 && one) mbar_arrive(&freed[(it - 1) & 1]);
+                    if (g == 1) ok = warp_wait(chain0 + 8, ph);   // the chains take turns: see Chain
+                    else if (it > 0) ok = warp_wait(chain0 + 18, ph ^ 1u);
+                    if (!ok) break;
+                    if (one) {
 #pragma unroll 1
-                    for (int blk = 0; blk < nblk; ++blk)
+                        for (int blk = 0; blk < nblk; ++blk)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(t1, ka + blk * 1024 + ks * 2, dG + blk * 512 + ks * 128, kk, blk + ks > 0);
-                    mma_commit(q + 5);
-                    if (!(ok = mbar_wait(full_tp, ph, kWaitLimit))) break;
-                    tc_fence_after();
-                    // what does not wait for K G: (P T)^T dO (rows 64..127 of the image, 8 KB in), the small parts
-                    // first (the accumulator cuts off, it does not round)
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(t1, ka + blk * 1024 + ks * 2, dG + blk * 512 + ks * 128, kk, blk + ks > 0);
+                        mma_commit(q + 5);
+                    }
+                    if (!(ok = warp_wait(full_tp, ph))) break;
+                    if (one) {
+                        // what does not wait for K G: (P T)^T dO (rows 64..127 of the image, 8 KB in), the small parts
+                        // first (the accumulator cuts off, it does not round)
 #pragma unroll
-                    for (int p = NP - 1; p >= 0; --p)
+                        for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(t2, dT + p * 1024 + 512 + ks * 128, dDO + ks * 128, m1, p < NP - 1 || ks > 0);
-                    if (!(ok = mbar_wait(q + 1, ph, kWaitLimit))) break;
-                    tc_fence_after();
-                    // T^T Y, into column groups of its own
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(t2, dT + p * 1024 + 512 + ks * 128, dDO + ks * 128, m1, p < NP - 1 || ks > 0);
+                    }
+                    if (!(ok = warp_wait(q + 1, ph))) break;
+                    if (one) {
+                        // T^T Y, into column groups of its own
 #pragma unroll
-                    for (int p = 0; p < NP; ++p)
+                        for (int p = 0; p < NP; ++p)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(t2 + 32, dT + p * 1024 + ks * 128, dX + ks * 128,
-                                       idesc_f16(128, (NP - p) * 32, true, true, true), p + ks > 0);
-                    mma_commit(q + 6);
-                    if (!(ok = mbar_wait(q + 4, ph, kWaitLimit))) break;   // (long since)
-                    tc_fence_after();
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(t2 + 32, dT + p * 1024 + ks * 128, dX + ks * 128,
+                                           idesc_f16(128, (NP - p) * 32, true, true, true), p + ks > 0);
+                        mma_commit(q + 6);
+                        mbar_arrive(q + 8);
+                    }
+                    if (!(ok = warp_wait(q + 4, ph))) break;   // (long since)
+                    if (one) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)   // Q^T E (rows 64..127 of [K; Q])
-                        mma_f16_ss(t3, km + 512 + ks * 128, dE + ks * 128, m3, ks > 0);
-                    if (!(ok = mbar_wait(q + 2, ph, kWaitLimit))) break;
-                    mbar_arrive(freed_tp);   // (D2 is done: z_ready came from it)
-                    tc_fence_after();
+                        for (int ks = 0; ks < 4; ++ks)   // Q^T E (rows 64..127 of [K; Q])
+                            mma_f16_ss(t3, km + 512 + ks * 128, dE + ks * 128, m3, ks > 0);
+                        mma_commit(q + 9);
+                    }
+                    if (!(ok = warp_wait(q + 2, ph))) break;
+                    if (one) {
+                        mbar_arrive(freed_tp);   // (D2 is done: z_ready came from it)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) mma_f16_ss(t3, km + ks * 128, dX + ks * 128, m3, 1u);
-                    mma_commit(q + 7);
+                        for (int ks = 0; ks < 4; ++ks) mma_f16_ss(t3, km + ks * 128, dX + ks * 128, m3, 1u);
+                        mma_commit(q + 7);
+                    }
                 }
-            }
-            if (!ok) atomicOr(&g_gb_status, 1u);
         }
+        if (!ok && lane == 0) atomicOr(&g_gb_status, 1u);
     } else {
         const int g = warp >> 3, row = 32 * (warp & 3) + lane, cc = ((warp >> 2) & 1) * 16;
         const int i = row & 63, col = c0 + g * 32 + cc;
         const bool top = row < 64, in = col < d.dv;
-        uint64_t* q = chain0 + 8 * g;
+        uint64_t* q = chain0 + 10 * g;
         const uint32_t t1 = taddr(tb, 32 * (warp & 3), g * 256 + cc), t2 = t1 + 96, t3 = t1;
         const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + col;
-        float2 G[8], X[8];
+        float2 G[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             const float4 x = a.dS_final && row < d.dk && in ? *reinterpret_cast<const float4*>(a.dS_final + sb + 2 * e)
                                                             : make_float4(0.f, 0.f, 0.f, 0.f);
             G[e] = make_float2(x.x, x.y);
             G[e + 1] = make_float2(x.z, x.w);
-            X[e] = X[e + 1] = both(0.f);
         }
         bool ok = true;
         for (int it = 0; it < nch; ++it) {
@@ -267,17 +274,12 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 }
             }
             warp_arrive(q, lane);
-            if (top && it > 0) {   // the dX of the chunk before, in Z's place
-                C::put16(sm + M::X, 8192, g, i, cc, X);
-                warp_arrive(q + 3, lane);
-            }
             if (!(ok = warp_wait(&full[it & 1], (it >> 1) & 1))) break;
             const float up = vec[i], last = vec[63];
             const bool live = i < n;
             float2 y[8];
             if (top) {
                 const float rest = vec[64 + i], al = vec[128 + i];
-                if (it > 0 && !(ok = warp_wait(x_free, ph))) break;
                 if (!(ok = warp_wait(q + 5, ph))) break;
                 tmem_sum16<NP>(t1, 32, y);
 #pragma unroll
@@ -285,11 +287,15 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 1, lane);
                 if (!(ok = warp_wait(q + 6, ph))) break;
+                float2 X[8];
                 tmem_sum16<NP + 1>(t2, 32, X);
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = mul2(both(-al * up), X[m]);
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
+                if (!(ok = warp_wait(q + 9, ph))) break;
+                C::put16(sm + M::E, 8192, g, i, cc, X);
+                warp_arrive(q + 3, lane);
                 if (live && in) {
                     Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
 #pragma unroll
@@ -297,6 +303,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     st16(vp, y);
                 }
             } else {
+                if (it > 0 && !(ok = warp_wait(e_free, ph ^ 1u))) break;
                 const uint4 w0 = *reinterpret_cast<const uint4*>(dt + sw128(i, g * 32 + cc));
                 const uint4 w1 = *reinterpret_cast<const uint4*>(dt + sw128(i, g * 32 + cc + 8));
                 const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -309,10 +316,6 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
             tmem_sum16<NP>(t3, 32, y);
 #pragma unroll
             for (int m = 0; m < 8; ++m) G[m] = fma2(both(last), G[m], y[m]);
-        }
-        if (ok && top && nch > 0) {   // the first chunk's dX
-            C::put16(sm + M::X, 8192, g, i, cc, X);
-            warp_arrive(q + 3, lane);
         }
         if (!ok && lane == 0) atomicOr(&g_gb_status, 1u);
         if (a.dS0 && row < d.dk && in &&
@@ -491,7 +494,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
         }
     } else if (warp == 8) {
         // ---------------- products
-        if (lane == 0) {
+        {
+            const bool one = elect_one();
             const uint64_t ax = sdesc_sw128(smem_u32(sm + kGrAX)), us = sdesc_sw128(smem_u32(sm + kGrU)),
                            ss = sdesc_sw128(smem_u32(sm + kGrS)), gs = sdesc_sw128(smem_u32(sm + kGrG)),
                            qk = sdesc_sw128(smem_u32(sm + kGrQK));
@@ -504,82 +508,87 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 if (place(x, hk, slot, b, s, t0) <= 0) continue;
                 for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h, ++hc) {
                     // the head's [Q; K] and vectors are in, and the epilogue has read the accumulators of the head before
-                    ok = mbar_wait(&m.qk, hc & 1, kWaitLimit);
+                    ok = warp_wait(&m.qk, hc & 1);
                     if (!ok) break;
-                    tc_fence_after();
+                    if (one) {
 #pragma unroll 1
-                    for (int blk = 0; blk < nblk; ++blk)
+                        for (int blk = 0; blk < nblk; ++blk)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cD4, qk + blk * 1024 + ks * 2, qk + 512 + blk * 1024 + ks * 2, n64, blk + ks > 0);
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(tb + cD4, qk + blk * 1024 + ks * 2, qk + 512 + blk * 1024 + ks * 2, n64, blk + ks > 0);
+                    }
                     for (int sl = 0; sl < nsl; ++sl, ++sc) {
                         const uint32_t ph = sc & 1, more = sl > 0;
-                        ok = mbar_wait(&m.f_ax, ph, kWaitLimit) && mbar_wait(&m.f_u, ph, kWaitLimit);
+                        ok = warp_wait(&m.f_ax, ph) && warp_wait(&m.f_u, ph);
                         if (!ok) break;
-                        tc_fence_after();
-                        // The accumulators cut off what falls below their last bit, at every instruction: the
-                        // small part pairs go first (and, for dbeta's D3, into columns of their own), so that
-                        // few of them meet a large sum.
+                        if (one) {
+                            // The accumulators cut off what falls below their last bit, at every instruction: the
+                            // small part pairs go first (and, for dbeta's D3, into columns of their own), so that
+                            // few of them meet a large sum.
 #pragma unroll
-                        for (int o = NP - 1; o >= 0; --o)   // pairs (p, o - p) of order o; 32 columns are two steps of K
+                            for (int o = NP - 1; o >= 0; --o)   // pairs (p, o - p) of order o; 32 columns are two steps of K
 #pragma unroll
-                            for (int p = 0; p <= o; ++p)
+                                for (int p = 0; p <= o; ++p)
 #pragma unroll
-                                for (int ks = 0; ks < 4; ++ks)
-                                    mma_f16_ss(tb + (o ? cD3s : cD3), ax + at_part(ks >> 1, p, 16384) + (ks & 1) * 2,
-                                               us + at_part(ks >> 1, o - p, 8192) + (ks & 1) * 2, n64,
-                                               more | !((o == NP - 1 || o == 0) && p == 0 && ks == 0));
-                        if (sl == nsl - 1) mma_commit(&m.d3);   // the pairs' epilogue can start
-                        ok = mbar_wait(&m.f_s, ph, kWaitLimit);
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        mma_f16_ss(tb + (o ? cD3s : cD3), ax + at_part(ks >> 1, p, 16384) + (ks & 1) * 2,
+                                                   us + at_part(ks >> 1, o - p, 8192) + (ks & 1) * 2, n64,
+                                                   more | !((o == NP - 1 || o == 0) && p == 0 && ks == 0));
+                            if (sl == nsl - 1) mma_commit(&m.d3);   // the pairs' epilogue can start
+                        }
+                        ok = warp_wait(&m.f_s, ph);
                         if (!ok) break;
-                        tc_fence_after();
+                        if (one) {
 #pragma unroll
-                        for (int o = NP - 1; o >= 0; --o)
+                            for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
-                            for (int p = 0; p <= o; ++p)
+                                for (int p = 0; p <= o; ++p)
 #pragma unroll
-                                for (int ks = 0; ks < 4; ++ks)
-                                    mma_f16_ss(tb + cDa, ax + at_part(ks >> 1, p, 16384) + (ks & 1) * 2,
-                                               ss + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
-                                               more | !(o == NP - 1 && p == 0 && ks == 0));
-                        mma_commit(&m.e_ax);
-                        if (sl < nsl - 1) mma_commit(&m.e_s);
-                        ok = mbar_wait(&m.f_g, ph, kWaitLimit);
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        mma_f16_ss(tb + cDa, ax + at_part(ks >> 1, p, 16384) + (ks & 1) * 2,
+                                                   ss + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
+                                                   more | !(o == NP - 1 && p == 0 && ks == 0));
+                            mma_commit(&m.e_ax);
+                            if (sl < nsl - 1) mma_commit(&m.e_s);
+                        }
+                        ok = warp_wait(&m.f_g, ph);
                         if (!ok) break;
-                        tc_fence_after();
+                        if (one) {
 #pragma unroll
-                        for (int o = NP - 1; o >= 0; --o)
+                            for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
-                            for (int p = 0; p <= o; ++p)
+                                for (int p = 0; p <= o; ++p)
 #pragma unroll
-                                for (int ks = 0; ks < 4; ++ks)
-                                    mma_f16_ss(tb + cD6, us + at_part(ks >> 1, p, 8192) - 512 + (ks & 1) * 2,
-                                               gs + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
-                                               more | !(o == NP - 1 && p == 0 && ks == 0));
-                        mma_commit(&m.e_u);
-                        mma_commit(&m.e_g);
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        mma_f16_ss(tb + cD6, us + at_part(ks >> 1, p, 8192) - 512 + (ks & 1) * 2,
+                                                   gs + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
+                                                   more | !(o == NP - 1 && p == 0 && ks == 0));
+                            mma_commit(&m.e_u);
+                            mma_commit(&m.e_g);
+                        }
                     }
                     if (!ok) break;
-                    ok = mbar_wait(&m.p5, hc & 1, kWaitLimit);
+                    ok = warp_wait(&m.p5, hc & 1);
                     if (!ok) break;
-                    tc_fence_after();
+                    if (one) {
 #pragma unroll
-                    for (int p = 1; p >= 0; --p) {
-                        const uint64_t a0 = sdesc_sw128(p5 + p * 16384);
-                        const uint64_t at = sdesc_sw128(z0, p5 + p * 16384 + 8192 - z0);   // [0 | dAD], rows are K indices
-                        const uint64_t pt = sdesc_sw128(z0, p5 + p * 16384 - z0);          // [0 | dPD]
+                        for (int p = 1; p >= 0; --p) {
+                            const uint64_t a0 = sdesc_sw128(p5 + p * 16384);
+                            const uint64_t at = sdesc_sw128(z0, p5 + p * 16384 + 8192 - z0);   // [0 | dAD], rows are K indices
+                            const uint64_t pt = sdesc_sw128(z0, p5 + p * 16384 - z0);          // [0 | dPD]
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cD5, a0 + ks * 2, kb + ks * 128, idesc_f16(128, 128, false, true, true), p < 1 || ks > 0);
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(tb + cD5, a0 + ks * 2, kb + ks * 128, idesc_f16(128, 128, false, true, true), p < 1 || ks > 0);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cD5, at + ks * 128, kb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(tb + cD5, at + ks * 128, kb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cD5, pt + ks * 128, qb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(tb + cD5, pt + ks * 128, qb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
                     }
                     mma_commit(&m.d5);
                     mma_commit(&m.e_s);   // (S's buffer, which held [dPD; dAD], is free again)
+                    }
                 }
             }
         }

@@ -97,21 +97,23 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = *tslot;
-    if (tid == 0) {
-        if (mbar_wait(&bar[0], 0, kWaitLimit)) {
-            tc_fence_after();
+    if (warp == 0) {
+        if (warp_wait(&bar[0], 0)) {
             const uint64_t x = sdesc_sw128(smem_u32(sm));
+            if (elect_one()) {
 #pragma unroll 1
-            for (int blk = 0; blk < (d.dk + 63) / 64; ++blk)   // (zeros past dk)
+                for (int blk = 0; blk < (d.dk + 63) / 64; ++blk)   // (zeros past dk)
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f16_ss(tb, x + blk * 1024 + ks * 2, x + blk * 1024 + ks * 2, idesc_f16(128, 64, false, false, true),
-                               blk + ks > 0);
-            mma_commit(&bar[1]);
-        } else {
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16_ss(tb, x + blk * 1024 + ks * 2, x + blk * 1024 + ks * 2, idesc_f16(128, 64, false, false, true),
+                                   blk + ks > 0);
+                mma_commit(&bar[1]);
+            }
+        } else if (lane == 0) {
             atomicOr(&g_gt2_status, 1u);
             mbar_wait(&bar[0], 0, kWaitLimit);   // let the copies land
         }
+        __syncwarp();
     }
     bool ok = __syncthreads_and(mbar_wait(&bar[1], 0, kWaitLimit));
     tc_fence_after();
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
         fence_async_smem();
         tc_fence_before();
         group_sync(1);
-        if (tid == 0) {   // [T; P] T, the part pairs p + x < NP (B: T's rows are K indices)
+        if (warp == 0 && elect_one()) {   // [T; P] T, the part pairs p + x < NP (B: T's rows are K indices)
             tc_fence_after();
             const uint64_t da = sdesc_sw128(smem_u32(img));
 #pragma unroll
@@ -244,8 +246,7 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
 // Each chain has a warp that issues its products; one more copies the chunks in, one ahead.
 //
 // REC is the backward's recording pass: no queries and no o; the parts of every chunk's entering
-// S, and of its U, go out as they lie in shared memory (a warp of its own copies them).  U's parts
-// take X's place once the chunk's last product has read it, while the next chunk's first one runs.
+// S, and of its U, go out as they lie in shared memory (a warp of its own copies them).
 //
 // Bound by the latency of the chain of three products and three epilogues a chunk: see the
 // measurements at launch.
@@ -260,9 +261,10 @@ struct ScanSmem {
     static constexpr uint32_t V = TP + TPS * NP * TPB;               // 2 stages
     static constexpr uint32_t S = V + 2 * 8192;                      // blocks of 128 rows
     static constexpr uint32_t X = S + C::blocks * 16384;             // blocks of 64 rows
-    static constexpr uint32_t VEC = X + C::blocks * 8192;            // 2 stages
+    static constexpr uint32_t U = X + C::blocks * 8192;              // REC: blocks of 64 rows
+    static constexpr uint32_t VEC = U + (REC ? C::blocks * 8192 : 0);   // 2 stages
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
-    static constexpr int bars = 4 + 2 + TPS + 1 + 9 * NCH;
+    static constexpr int bars = 4 + 2 + TPS + 1 + 9 * NCH;   // (per chain: 7, and its turn)
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
     static constexpr int warps = 9 * NCH + 1 + (REC ? 1 : 0);
 };
@@ -294,8 +296,8 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
     uint64_t* full_tp = bars + 4;        // [TPS]
     uint64_t* freed_tp = full_tp + M::TPS;   // by every chain (one stage only)
     uint64_t* s_free = freed_tp + 1;     // REC: S's and U's parts have been copied out
-    uint64_t* x_free = s_free + 1;
-    uint64_t* chain0 = x_free + 1;       // per chain: s_ready, x_ready, u_ready, r_ready (REC: U's parts), d1, d2, d3
+    uint64_t* u_free = s_free + 1;
+    uint64_t* chain0 = u_free + 1;       // per chain: s_ready, x_ready, u_ready, r_ready (REC: U's parts), d1, d2, d3, turn
     uint32_t* tslot = (uint32_t*)(bars + M::bars);
     const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * 32 * NCH;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -310,14 +312,14 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
         for (int i = 0; i < M::TPS; ++i) mbar_init(&full_tp[i], 1);
         mbar_init(freed_tp, NCH);
         mbar_init(s_free, 1);
-        mbar_init(x_free, 1);
+        mbar_init(u_free, 1);
         for (int g = 0; g < NCH; ++g) {
             uint64_t* q = chain0 + 9 * g;
             mbar_init(q + 0, 8);               // s_ready (warps)
             mbar_init(q + 1, 4);               // x_ready
             mbar_init(q + 2, REC ? 4 : 8);     // u_ready
             mbar_init(q + 3, 4);               // r_ready
-            for (int i = 4; i < 7; ++i) mbar_init(q + i, 1);
+            for (int i = 4; i < 8; ++i) mbar_init(q + i, 1);
         }
         fence_mbar_init();
     }
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
     const uint32_t tb = *tslot;
 
     if (warp >= 8 * NCH) {
-        if (lane == 0 && nch > 0) {
-            bool ok = true;
+        bool ok = true;
+        if (warp >= 9 * NCH && lane == 0 && nch > 0) {
             if (warp == 9 * NCH) {
                 // ---------------- copies in
                 int n_kq = 0, n_tp = 0;   // chunks whose copies are under way
@@ -387,33 +389,29 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     }
             } else if (REC && warp == 9 * NCH + 1) {
                 // ---------------- copies out
-                for (int c = 0; c <= nch && ok; ++c) {
+                for (int c = 0; c < nch; ++c) {
                     const uint32_t ph = c & 1;
-                    if (c < nch) {
-                        for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g, ph, kWaitLimit);
-                        if (!ok) break;
-                        unsigned char* to = a.rec_S + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecS;
-                        bulk_s2g(to, sm + M::S, kRecS);
-                        bulk_commit();
-                    }
-                    if (c > 0) {   // the chunk before's U
-                        for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g + 3, ph ^ 1u, kWaitLimit);
-                        if (!ok) break;
-                        unsigned char* to = a.rec_U + ((rec0 + c - 1) * gridDim.y + blockIdx.y) * kRecU;
-                        bulk_s2g(to, sm + M::X, kRecU);
-                        bulk_commit();
-                    }
-                    bulk_wait_read();
+                    for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g, ph, kWaitLimit);
+                    if (!ok) break;
+                    bulk_s2g(a.rec_S + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecS, sm + M::S, kRecS);
+                    bulk_commit();
+                    bulk_wait_read();   // (and the U of the chunk before)
                     mbar_arrive(s_free);
-                    mbar_arrive(x_free);
+                    if (c > 0) mbar_arrive(u_free);
+                    for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g + 3, ph, kWaitLimit);
+                    if (!ok) break;
+                    bulk_s2g(a.rec_U + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecU, sm + M::U, kRecU);
+                    bulk_commit();
                 }
                 bulk_wait_read();
-            } else if (warp < 9 * NCH) {
+            }
+        } else if (warp < 9 * NCH) {
                 // ---------------- a chain's products
                 const int g = warp - 8 * NCH;
                 uint64_t* q = chain0 + 9 * g;
                 const uint32_t t1 = tb + g * 256, t2 = t1 + 128, t3 = t1;   // D3 over D1, which is read by then
                 const int nblk = (d.dk + 63) / 64;
+                const bool one = elect_one();
                 const uint64_t dS = sdesc_sw128(smem_u32(sm + M::S + g * 16384), NP == 3 ? C::lbo(g, 16384) : 16384);
                 const uint64_t dX = sdesc_sw128(smem_u32(sm + M::X + g * 8192), NP == 3 ? C::lbo(g, 8192) : 8192);
                 for (int c = 0; c < nch; ++c) {
@@ -421,37 +419,44 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     const uint32_t kq = smem_u32(sm + M::KQ + (c & 1) * 2 * M::KQB);
                     const uint64_t ka = sdesc_sw128(kq), km = sdesc_sw128(kq, M::KQB);
                     const uint64_t ta = sdesc_sw128(smem_u32(sm + M::TP + (c % M::TPS) * NP * M::TPB));
-                    if (!(ok = mbar_wait(q, ph, kWaitLimit) && mbar_wait(&full[c & 1], (c >> 1) & 1, kWaitLimit))) break;
-                    if (c > 0) mbar_arrive(&freed[(c - 1) & 1]);   // the chunk before: every product and epilogue is over
-                    tc_fence_after();
+                    if (!(ok = warp_wait(q, ph) && warp_wait(&full[c & 1], (c >> 1) & 1))) break;
+                    if (c > 0 && one) mbar_arrive(&freed[(c - 1) & 1]);   // the chunk before: every product and epilogue is over
+                    if (NCH == 2) {   // (the other chain has issued its second product: of this chunk, of the one before)
+                        if (g == 1) ok = warp_wait(chain0 + 7, ph);
+                        else if (c > 0) ok = warp_wait(chain0 + 16, ph ^ 1u);
+                        if (!ok) break;
+                    }
+                    if (one) {
 #pragma unroll 1
-                    for (int blk = 0; blk < nblk; ++blk)   // (64 dk at a time, zeros past dk: no branch per instruction)
+                        for (int blk = 0; blk < nblk; ++blk)   // (64 dk at a time, zeros past dk: no branch per instruction)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(t1, ka + blk * (M::KQB >> 4) + ks * 2, dS + blk * 512 + ks * 128,
+                                           idesc_f16(128, NP * 32, false, true, true), blk + ks > 0);
+                        mma_commit(q + 4);
+                    }
+                    if (!(ok = warp_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1) && warp_wait(q + 1, ph))) break;
+                    if (one) {
+#pragma unroll
+                        for (int p = 0; p < NP; ++p)   // with the part pairs p + x < NP
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16_ss(t2, ta + p * (M::TPB >> 4) + ks * 2, dX + ks * 128,
+                                           idesc_f16(128, (NP - p) * 32, false, true, true), p + ks > 0);
+                            mma_commit(q + 5);
+                            if (NCH == 2) mbar_arrive(q + 7);
+                    }
+                    if (!(ok = warp_wait(q + 2, ph))) break;
+                    if (one) {
+                        if (M::TPS == 1) mbar_arrive(freed_tp);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(t1, ka + blk * (M::KQB >> 4) + ks * 2, dS + blk * 512 + ks * 128,
-                                       idesc_f16(128, NP * 32, false, true, true), blk + ks > 0);
-                    mma_commit(q + 4);
-                    if (!(ok = mbar_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1, kWaitLimit) &&
-                               mbar_wait(q + 1, ph, kWaitLimit))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)   // with the part pairs p + x < NP
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(t2, ta + p * (M::TPB >> 4) + ks * 2, dX + ks * 128,
-                                       idesc_f16(128, (NP - p) * 32, false, true, true), p + ks > 0);
-                    mma_commit(q + 5);
-                    if (!(ok = mbar_wait(q + 2, ph, kWaitLimit))) break;
-                    if (M::TPS == 1) mbar_arrive(freed_tp);
-                    tc_fence_after();
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_ss(t3, km + ks * 128, dX + ks * 128, idesc_f16(128, NP * 32, true, true, true), ks > 0);
-                    mma_commit(q + 6);
+                            mma_f16_ss(t3, km + ks * 128, dX + ks * 128, idesc_f16(128, NP * 32, true, true, true), ks > 0);
+                        mma_commit(q + 6);
+                    }
                 }
-            }
-            if (!ok) atomicOr(&g_gt2_status, 1u);
         }
+        if (!ok && lane == 0) atomicOr(&g_gt2_status, 1u);
     } else {
         // ---------------- the state and the epilogues
         const int g = warp >> 3, row = 32 * (warp & 3) + lane, cc = ((warp >> 2) & 1) * 16;   // 16 columns from cc of the chain
@@ -460,14 +465,13 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
         uint64_t* q = chain0 + 9 * g;
         const uint32_t lq = taddr(tb, 32 * (warp & 3), g * 256 + cc), t1 = lq, t2 = lq + 128, t3 = lq;
         const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + col;
-        float2 S[8], U[8];
+        float2 S[8];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             const float4 x = a.S0 && row < d.dk && in ? *reinterpret_cast<const float4*>(a.S0 + sb + 2 * e)
                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             S[e] = make_float2(x.x, x.y);
             S[e + 1] = make_float2(x.z, x.w);
-            U[e] = U[e + 1] = both(0.f);
         }
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
@@ -484,10 +488,6 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                         make_uint4(0u, 0u, 0u, 0u);
             }
             warp_arrive(q, lane);
-            if (REC && top && c > 0) {   // the chunk before's U, in X's place
-                C::put16(sm + M::X, 8192, g, i, cc, U);
-                warp_arrive(q + 3, lane);
-            }
             if (!(ok = warp_wait(&full[c & 1], (c >> 1) & 1))) break;
             const float up = vec->up[i], last = vec->up[63];
             if (top) {
@@ -499,7 +499,6 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 const uint4 v1 = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc + 8));
                 float2 v[8] = {mul2(al, bf16x2(v0.x)), mul2(al, bf16x2(v0.y)), mul2(al, bf16x2(v0.z)), mul2(al, bf16x2(v0.w)),
                                mul2(al, bf16x2(v1.x)), mul2(al, bf16x2(v1.y)), mul2(al, bf16x2(v1.z)), mul2(al, bf16x2(v1.w))};
-                if (REC && c > 0 && !(ok = warp_wait(x_free, ph))) break;
                 if (!(ok = warp_wait(q + 4, ph))) break;
                 float2 y[8];
                 tmem_sum16<NP>(t1, 32, y);
@@ -511,11 +510,17 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 1, lane);
                 if (!(ok = warp_wait(q + 5, ph))) break;
+                float2 U[8];
                 tmem_sum16<NP>(t2, 32, U);
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = mul2(rest, U[m]);
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
+                if (REC) {
+                    if (c > 0 && !(ok = warp_wait(u_free, ph ^ 1u))) break;
+                    C::put16(sm + M::U, 8192, g, i, cc, U);
+                    warp_arrive(q + 3, lane);
+                }
             } else if (!REC) {
                 if (!(ok = warp_wait(q + 4, ph))) break;
                 float2 y[8], z[8];
@@ -535,10 +540,6 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
             tmem_sum16<NP>(t3, 32, y);
 #pragma unroll
             for (int m = 0; m < 8; ++m) S[m] = fma2(both(last), S[m], y[m]);
-        }
-        if (REC && ok && top && nch > 0) {   // the last chunk's U
-            C::put16(sm + M::X, 8192, g, i, cc, U);
-            warp_arrive(q + 3, lane);
         }
         if (!ok && lane == 0) atomicOr(&g_gt2_status, 1u);
         if (a.S_final && row < d.dk && in &&

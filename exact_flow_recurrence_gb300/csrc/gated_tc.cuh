@@ -67,7 +67,10 @@ __device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
 }
 
 // A scan CTA runs NCH chains of 32 state columns each: their products and epilogues are
-// independent, so that one chain's products run while the other's epilogue does.  A computed
+// independent, so that one chain's products run while the other's epilogue does.
+// Left to themselves the two fall into step and wait for the same things together; so they take
+// turns: chain 1 starts a chunk when chain 0 has issued the chunk's second product, and chain 0
+// the next one when chain 1 has.  A computed
 // operand of 32 columns lies in blocks of 128-byte rows (64 columns; R rows, BLK = 128 R bytes):
 //   block g < NCH   chain g's part 0 | part 1        block NCH   chain 0's part 2 | chain 1's
 // so that its parts are neighbours along N and one product takes them all (D keeps a column
