@@ -342,9 +342,11 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
 // The recorded parts come by bulk copy in the layout the products read (Chain<3, 2>: a 64-byte
 // half row is 32 columns of one part), each kind into a buffer of its own that is filled again as
 // soon as its products are done: dX and dO (with zeros beside dO, so that the products of dX's
-// second and third part add nothing to dO's lanes), U, S, G.  Warps: 8 epilogue, one that issues
-// products, one that copies.  The epilogue of the pairs runs while the last slice's products do.
-constexpr int kGrWarps = 10;
+// second and third part add nothing to dO's lanes), U, S, G.  Warps: 8 for the epilogues, 4 that
+// stage what is not recorded (q, k, dO, the head's vectors: loaded ahead into registers) and sum
+// <S, G>, one that issues products, one that copies.  The epilogue of the pairs runs while the
+// last slice's products do.
+constexpr int kGrWarps = 14;
 constexpr uint32_t kGrQK = 0;                    // 2 blocks of 64 dk x [Q rows | K rows]
 constexpr uint32_t kGrAX = 32768;                // 3 blocks of [dO | 0 ; dX parts], 64 rows each
 constexpr uint32_t kGrU = kGrAX + 49152;         // 3 blocks of 64 rows (as an A operand, the tile before fills rows 0..63)
@@ -357,16 +359,18 @@ constexpr uint32_t kGrZero = kGrAX + 32768;      // 64 rows of zeros (AX's third
 constexpr uint32_t cDa = 0, cD6 = 128, cD3 = 256, cD3s = 320, cD5 = 256, cD4 = 384;
 
 struct GrMisc {
-    GVec vec;
-    float be[64], lam[64], da[64], dc[64];
+    GVec vec[2];           // (by the head's parity: the next one's are loaded ahead)
+    float be[2][64];
+    float lam[64], da[64], dc[64];
     float rs[2][128];      // row sums of a column group
     float cs[4][64];       // column sums of a lane quadrant
     float dot[2][128];     // per column group: q . dq's, and k . dk's state terms
     float dot2[2][64];     // k . (e^{c_last - c} U G^T)
-    float sg[8];
+    float sg[2][4];
     uint64_t f_ax, f_u, f_s, f_g;      // copies have landed
     uint64_t e_ax, e_u, e_s, e_g;      // products have read (and, S and G, the epilogue)
     uint64_t qk, d3, d5, p5;           // [Q; K] and vectors are in; products; [dPD; dAD]
+    uint64_t sgs, end;                 // the head's <S, G> is in; the epilogue has read everything of the head
     uint32_t tslot;
 };
 constexpr size_t kGrSmem = 1024 + kGrMisc + sizeof(GrMisc);
@@ -428,11 +432,12 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     const long long items = (long long)a.slots * d.Hk;   // key head fastest: neighbours share a sequence's tokens
     if (tid == 0) {
         for (uint64_t* p : {&m.f_u, &m.f_s, &m.f_g, &m.e_ax, &m.e_u, &m.d3, &m.d5}) mbar_init(p, 1);
-        for (uint64_t* p : {&m.f_ax, &m.e_s, &m.e_g}) mbar_init(p, 1 + 8);   // (f_ax: the copy of dX and the epilogue warps' dO)
-        for (uint64_t* p : {&m.qk, &m.p5}) mbar_init(p, 8);
+        for (uint64_t* p : {&m.f_ax, &m.e_s, &m.e_g}) mbar_init(p, 1 + 4);   // (f_ax: the copy of dX and the staging warps' dO)
+        for (uint64_t* p : {&m.qk, &m.sgs}) mbar_init(p, 4);
+        for (uint64_t* p : {&m.p5, &m.end}) mbar_init(p, 8);
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 12) {
         tmem_alloc(&m.tslot, 512);
         tmem_relinquish();
     }
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
         t0 = (slot - s.slot0) * kGC;
         return min(kGC, s.len - t0);
     };
-    if (warp == 9) {
+    if (warp == 13) {
         // ---------------- copies in
         if (lane == 0) {
             for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 mbar_wait(&m.f_g, sc & 1, kWaitLimit);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == 12) {
         // ---------------- products
         {
             const bool one = elect_one();
@@ -592,50 +597,93 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 }
             }
         }
-    } else {
-        // ---------------- epilogues: this lane's token, columns 16 cg + 32 k of the pairs, 64 cg .. + 63 of dq, dk
-        const int qd = warp & 3, cg = warp >> 2, row = 32 * qd + lane, i = row & 63;
-        const bool top = row < 64;
-        const uint32_t lq = taddr(tb, 32 * qd, 0);
-        float* my = a.acc ? a.acc + ((size_t)blockIdx.x * 128 + row) * 128 + 64 * cg : nullptr;
-        for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
-            int hk, slot, b, t0;
-            SeqAt s;
-            const int n = place(x, hk, slot, b, s, t0);
-            if (n <= 0) continue;
-            const int t = s.start + t0;
-            for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h, ++hc) {
-                // [Q; K] (the products of the head before are over), the head's vectors
-                if (h == hk * rep)
-                    for (int e = tid; e < 1024; e += 256) {
-                        const int r = e >> 4, ch = e & 15;
-                        const bool in = r < n && ch * 8 < dk;
+    } else if (warp >= 8) {
+        // ---------------- staging: [Q; K] and vectors of a head, dO of a slice, <S, G>
+        const int st = tid - 256;
+        long long x = blockIdx.x;
+        int hk = 0, slot = 0, b, t0, n = 0, t = 0;
+        SeqAt s;
+        const auto settle = [&]() {   // x: this CTA's next chunk that exists (or past the end)
+            for (; x < items; x += gridDim.x) {
+                n = place(x, hk, slot, b, s, t0);
+                t = s.start + t0;
+                if (n > 0) break;
+            }
+        };
+        settle();
+        const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
+        uint4 qr[8], kr[8], dr[4];
+        float vr[5], br = 0.f;
+        const auto fetch_qk = [&]() {   // rows of 16 chunks
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = (st >> 4) + 8 * e, ch = st & 15;
+                const bool in = x < items && r < n && ch * 8 < dk;
+                qr[e] = in ? __ldg(reinterpret_cast<const uint4*>(a.q + at3(d.qs, s.batch, hk, t + r) + ch * 8)) : z4;
+                kr[e] = in ? __ldg(reinterpret_cast<const uint4*>(a.k + at3(d.ks, s.batch, hk, t + r) + ch * 8)) : z4;
+            }
+        };
+        const auto fetch_head = [&](int h) {
+            if (x >= items) return;
+            const float* v = reinterpret_cast<const float*>(a.vec + (size_t)h * a.slots + slot);
+#pragma unroll
+            for (int e = 0; e < 5; ++e) vr[e] = st < 64 ? __ldg(v + e * 64 + st) : 0.f;
+            br = st < n && st < 64 ? __ldg(a.beta + at3(d.bs, s.batch, h, t + st)) : 0.f;
+        };
+        const auto fetch_do = [&](int h, int sl) {   // rows of eight chunks
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = (st >> 3) + 16 * e, col = sl * 64 + (st & 7) * 8;
+                dr[e] = x < items && r < n && col < dv
+                            ? __ldg(reinterpret_cast<const uint4*>(a.dO + at3(d.dos, s.batch, h, t + r) + col)) : z4;
+            }
+        };
+        fetch_qk();
+        fetch_head(hk * rep);
+        fetch_do(hk * rep, 0);
+        while (x < items && ok) {
+            for (int h = hk * rep, he = (hk + 1) * rep; h < he && ok; ++h, ++hc) {
+                // (the head before: its epilogue is over, and the one before that is with these vectors)
+                if (hc > 0) ok = warp_wait(&m.end, (hc - 1) & 1);
+                if (h == hk * rep) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = (st >> 4) + 8 * e, ch = st & 15;
                         unsigned char* to = sm + kGrQK + (ch >> 3) * 16384 + sw128(r, (ch & 7) * 8);
-                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(to) =
-                            in ? __ldg(reinterpret_cast<const uint4*>(a.q + at3(d.qs, s.batch, hk, t + r) + ch * 8)) : z;
-                        *reinterpret_cast<uint4*>(to + 8192) =
-                            in ? __ldg(reinterpret_cast<const uint4*>(a.k + at3(d.ks, s.batch, hk, t + r) + ch * 8)) : z;
+                        *reinterpret_cast<uint4*>(to) = qr[e];
+                        *reinterpret_cast<uint4*>(to + 8192) = kr[e];
                     }
-                for (int e = tid; e < (int)(sizeof(GVec) / 4); e += 256)
-                    reinterpret_cast<float*>(&m.vec)[e] = reinterpret_cast<const float*>(a.vec + (size_t)h * a.slots + slot)[e];
-                if (tid < 64) m.be[tid] = tid < n ? a.beta[at3(d.bs, s.batch, h, t + tid)] : 0.f;
+                }
+                if (st < 64) {
+#pragma unroll
+                    for (int e = 0; e < 5; ++e) reinterpret_cast<float*>(&m.vec[hc & 1])[e * 64 + st] = vr[e];
+                    m.be[hc & 1][st] = br;
+                }
                 warp_arrive(&m.qk, lane);
-                float sg = 0.f;   // <S, G>, in the products' shadow
+                float sg = 0.f;
                 for (int sl = 0; sl < nsl; ++sl, ++sc) {
                     const uint32_t ph = sc & 1;
                     // dO's 64 columns into the first half rows of AX's blocks 0 and 1 (its products before are over)
                     ok = ok && warp_wait(&m.e_ax, ph ^ 1u);
-                    for (int e = tid; e < 512; e += 256) {
-                        const int r = e >> 3, ch = e & 7, col = sl * 64 + ch * 8;
-                        *reinterpret_cast<uint4*>(sm + kGrAX + (ch >> 2) * 16384 + sw128(r, (ch & 3) * 8)) =
-                            r < n && col < dv ? __ldg(reinterpret_cast<const uint4*>(a.dO + at3(d.dos, s.batch, h, t + r) + col))
-                                              : make_uint4(0u, 0u, 0u, 0u);
-                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(sm + kGrAX + ((st >> 2) & 1) * 16384 + sw128((st >> 3) + 16 * e, (st & 3) * 8)) = dr[e];
                     warp_arrive(&m.f_ax, lane);
+                    if (sl + 1 < nsl) {
+                        fetch_do(h, sl + 1);
+                    } else if (h + 1 < he) {
+                        fetch_head(h + 1);
+                        fetch_do(h + 1, 0);
+                    } else {   // the next chunk's
+                        x += gridDim.x;
+                        settle();
+                        fetch_qk();
+                        fetch_head(hk * rep);
+                        fetch_do(hk * rep, 0);
+                    }
                     ok = ok && warp_wait(&m.f_s, ph) && warp_wait(&m.f_g, ph);
 #pragma unroll 2
-                    for (int e = tid; e < 1024; e += 256) {   // rows of eight 8-column chunks
+                    for (int e = st; e < 1024; e += 128) {   // rows of eight 8-column chunks
                         float2 u[4], v[4];
                         parts8(sm + kGrS, e >> 3, (e >> 2) & 1, e & 3, u);
                         parts8(sm + kGrG, e >> 3, (e >> 2) & 1, e & 3, v);
@@ -647,48 +695,87 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&m.e_g);
-                        if (sl < nsl - 1) mbar_arrive(&m.e_s);   // (the last slice's S buffer goes on to [dPD; dAD])
+                        if (sl + 1 < nsl) mbar_arrive(&m.e_s);   // (the last slice's S buffer goes on to [dPD; dAD])
                     }
                 }
-                // ---- the chunk's pairs (i, j): columns j = 32 cg .. 32 cg + 31 of this lane's row
-                ok = ok && warp_wait(&m.d3, hc & 1);
                 sg = warp_sum(sg);
-                if (lane == 0) m.sg[warp] = sg;
-                const float chi = m.vec.chi[i], clo = m.vec.clo[i], al = m.vec.al[i];
+                if (lane == 0) m.sg[hc & 1][warp - 8] = sg;
+                warp_arrive(&m.sgs, lane);
+            }
+        }
+    } else {
+        // ---------------- epilogues: this lane's token, columns 32 cg .. + 31 of the pairs, 64 cg .. + 63 of dq, dk
+        const int qd = warp & 3, cg = warp >> 2, row = 32 * qd + lane, i = row & 63;
+        const bool top = row < 64;
+        const uint32_t lq = taddr(tb, 32 * qd, 0);
+        float* my = a.acc ? a.acc + ((size_t)blockIdx.x * 128 + row) * 128 + 64 * cg : nullptr;
+        for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
+            int hk, slot, b, t0;
+            SeqAt s;
+            const int n = place(x, hk, slot, b, s, t0);
+            if (n <= 0) continue;
+            const int t = s.start + t0;
+            for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h, ++hc) {
+                const GVec& vec = m.vec[hc & 1];
+                // ---- the chunk's pairs (i, j): columns j = 32 cg .. 32 cg + 31 of this lane's row
+                ok = warp_wait(&m.d3, hc & 1);
+                const float al = vec.al[i], sw = top ? 1.f : -al;
+                const int diag = top ? i + 1 : i;                       // columns below this are kept
+                const bool some = 32 * cg < 32 * (qd & 1) + 32;         // the warp's rows reach these columns
                 float2 w5[16];
                 float rsum = 0.f;
+                if (some) {
+                    const float chi = vec.chi[i], clo = vec.clo[i];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int j0 = 32 * cg + 16 * k;
-                    float y[16], y2[16], z[16], col[16];
-                    tmem_ld16(lq + cD3 + j0, y);
-                    tmem_ld16(lq + cD3s + j0, y2);
-                    tmem_ld16(lq + cD4 + j0, z);
-                    tmem_ld_wait();
-                    loaded16(y);
-                    loaded16(y2);
-                    loaded16(z);
+                    for (int k = 0; k < 2; ++k) {
+                        const int j0 = 32 * cg + 16 * k;
+                        float y[16], y2[16], z[16];
+                        tmem_ld16(lq + cD3 + j0, y);
+                        tmem_ld16(lq + cD3s + j0, y2);
+                        tmem_ld16(lq + cD4 + j0, z);
+                        float g[16];   // the decays, while the loads are under way
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int j = j0 + e;
-                        y[e] += y2[e];
-                        if (!top && j == i) {
-                            m.da[i] = i < n ? y[e] / al : 0.f;
-                            m.lam[i] = z[e];
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 h4 = *reinterpret_cast<const float4*>(vec.chi + j0 + e);
+                            const float4 l4 = *reinterpret_cast<const float4*>(vec.clo + j0 + e);
+                            g[e] = decay2(chi, clo, h4.x, l4.x);
+                            g[e + 1] = decay2(chi, clo, h4.y, l4.y);
+                            g[e + 2] = decay2(chi, clo, h4.z, l4.z);
+                            g[e + 3] = decay2(chi, clo, h4.w, l4.w);
                         }
-                        const bool keep = (top ? j <= i : j < i) && i < n;
-                        const float w = keep ? (top ? y[e] : -al * y[e]) * decay2(chi, clo, m.vec.chi[j], m.vec.clo[j]) : 0.f;
-                        col[e] = keep ? w * z[e] : 0.f;
-                        rsum += col[e];
-                        (e & 1 ? w5[8 * k + e / 2].y : w5[8 * k + e / 2].x) = w;
+                        tmem_ld_wait();
+                        loaded16(y);
+                        loaded16(y2);
+                        loaded16(z);
+                        float dg = 0.f, lam = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const bool keep = j0 + e < diag && i < n;
+                            y[e] += y2[e];
+                            if (j0 + e == i) {
+                                dg = y[e];
+                                lam = z[e];
+                            }
+                            const float w = keep ? sw * y[e] * g[e] : 0.f;
+                            (e & 1 ? w5[8 * k + e / 2].y : w5[8 * k + e / 2].x) = w;
+                            z[e] = keep ? w * z[e] : 0.f;
+                            rsum += z[e];
+                        }
+                        if (!top && (i & ~15) == j0) {   // the diagonal: dalpha alpha, and lambda
+                            m.da[i] = i < n ? dg / al : 0.f;
+                            m.lam[i] = lam;
+                        }
+                        const float cs = lane_sums16(z, lane);
+                        if ((lane & 1) == 0) m.cs[qd][j0 + (lane >> 1)] = cs;
                     }
-                    const float cs = lane_sums16(col, lane);
-                    if ((lane & 1) == 0) m.cs[qd][j0 + (lane >> 1)] = cs;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) w5[k] = both(0.f);
+                    if (lane < 32) m.cs[qd][32 * cg + lane] = 0.f;
                 }
                 m.rs[cg][row] = rsum;
-                // (S's buffer: the last slice's products have read it, and so has every warp's <S, G>)
-                ok = ok && warp_wait(&m.e_u, (sc - 1) & 1);   // D6 follows Da
-                if (!(ok = group_sync_and(1, ok, 256))) break;   // (the warps leave together if a wait gave up)
+                // (S's buffer: the last slice's products have read it, and so has <S, G>)
+                ok = ok && warp_wait(&m.e_u, (nsl * (hc + 1) - 1) & 1) && warp_wait(&m.sgs, hc & 1);   // D6 follows Da
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint4 w[2];
@@ -698,8 +785,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         *reinterpret_cast<uint4*>(sm + kGrP5 + p * 16384 + sw128(row, 32 * cg + 8 * k)) = w[p];
                 }
                 warp_arrive(&m.p5, lane);
-                if (lane == 0) mbar_arrive(&m.e_s);   // with the products' own arrival after D5: the buffer is free
-                group_sync(1, 256);                   // the sums by rows and columns are in
+                if (lane == 0 && warp < 4) mbar_arrive(&m.e_s);   // with the products' own arrival after D5: the buffer is free
+                if (!(ok = group_sync_and(1, ok, 256))) break;   // the sums by rows and columns are in
                 if (tid < 64) {
                     float c = 0.f;
 #pragma unroll
@@ -708,52 +795,55 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                     for (int e = 0; e < 4; ++e) c -= m.cs[e][tid];
                     m.dc[tid] = c;
                 }
+                const float up = vec.up[i], rest = vec.rest[i];
+                const float2 sa = both(top ? up : -al * up), rs2 = both(rest);
+                const float2 dl = both(top ? 0.f : 2.f * m.da[i] * dalpha_dlambda_of(m.be[hc & 1][i], m.lam[i], d.euler));
+                float2 dot = both(0.f), dot2 = both(0.f);
+                Tout* out = top ? (Tout*)a.dq + at3(d.dqs, s.batch, hk, t + i) : (Tout*)a.dk + at3(d.dks, s.batch, hk, t + i);
                 ok = warp_wait(&m.d5, hc & 1);
                 // ---- dq, dk: columns 64 cg .. 64 cg + 63 of this lane's token
-                {
-                    const float up = m.vec.up[i], rest = m.vec.rest[i];
-                    const float sa = top ? up : -al * up;
-                    const float dl = top ? 0.f : 2.f * m.da[i] * dalpha_dlambda_of(m.be[i], m.lam[i], d.euler);
-                    float2 dot = both(0.f), dot2 = both(0.f);
-                    Tout* out = top ? (Tout*)a.dq + at3(d.dqs, s.batch, hk, t + i) : (Tout*)a.dk + at3(d.dks, s.batch, hk, t + i);
 #pragma unroll 1
-                    for (int e0 = 0; e0 < 64; e0 += 16) {
-                        const int c = 64 * cg + e0;
-                        if (c >= dk) break;
-                        float2 da[8], d5[8], d6[8];
-                        tmem_sum16<1>(lq + cDa + c, 0, da);
-                        tmem_sum16<1>(lq + cD5 + c, 0, d5);
-                        if (!top) tmem_sum16<1>(lq + cD6 + c, 0, d6);
-                        const uint4 w0 = *reinterpret_cast<const uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, c & 63));
-                        const uint4 w1 = *reinterpret_cast<const uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, (c & 63) + 8));
-                        const uint32_t wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                for (int e0 = 0; e0 < 64; e0 += 16) {
+                    const int c = 64 * cg + e0;
+                    if (c >= dk) break;
+                    float da[16], y[16], d6[16];
+                    tmem_ld16(lq + cDa + c, da);
+                    tmem_ld16(lq + cD5 + c, y);
+                    if (!top) tmem_ld16(lq + cD6 + c, d6);
+                    const uint4 w0 = *reinterpret_cast<const uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, c & 63));
+                    const uint4 w1 = *reinterpret_cast<const uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, (c & 63) + 8));
+                    const uint32_t wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                    tmem_ld_wait();
+                    loaded16(da);
+                    loaded16(y);
+                    if (!top) loaded16(d6);
+                    float2 o[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 xk = bf16x2(wk[e]), st = mul2(both(sa), da[e]);
-                            dot = fma2(st, xk, dot);
-                            d5[e] = add2(d5[e], st);
-                            if (!top) {
-                                const float2 u = mul2(both(rest), d6[e]);
-                                dot2 = fma2(u, xk, dot2);
-                                d5[e] = add2(d5[e], fma2(both(dl), xk, u));
-                            }
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 xk = bf16x2(wk[e]), st = mul2(sa, make_float2(da[2 * e], da[2 * e + 1]));
+                        dot = fma2(st, xk, dot);
+                        o[e] = add2(make_float2(y[2 * e], y[2 * e + 1]), st);
+                        if (!top) {
+                            const float2 u = mul2(rs2, make_float2(d6[2 * e], d6[2 * e + 1]));
+                            dot2 = fma2(u, xk, dot2);
+                            o[e] = add2(o[e], fma2(dl, xk, u));
                         }
-                        if (my) {   // several value heads: their sum, in fp32
-                            if (h > hk * rep) {
-#pragma unroll
-                                for (int e = 0; e < 8; e += 2) {
-                                    const float4 o = *reinterpret_cast<const float4*>(my + e0 + 2 * e);
-                                    d5[e] = add2(d5[e], make_float2(o.x, o.y));
-                                    d5[e + 1] = add2(d5[e + 1], make_float2(o.z, o.w));
-                                }
-                            }
-                            if (h + 1 < (hk + 1) * rep) st16(my + e0, d5);
-                        }
-                        if (h + 1 == (hk + 1) * rep && i < n) st16(out + c, d5);
                     }
-                    m.dot[cg][row] = dot.x + dot.y;
-                    if (!top) m.dot2[cg][i] = dot2.x + dot2.y;
+                    if (my) {   // several value heads: their sum, in fp32
+                        if (h > hk * rep) {
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                const float4 v = *reinterpret_cast<const float4*>(my + e0 + 2 * e);
+                                o[e] = add2(o[e], make_float2(v.x, v.y));
+                                o[e + 1] = add2(o[e + 1], make_float2(v.z, v.w));
+                            }
+                        }
+                        if (h + 1 < (hk + 1) * rep) st16(my + e0, o);
+                    }
+                    if (h + 1 == (hk + 1) * rep && i < n) st16(out + c, o);
                 }
+                m.dot[cg][row] = dot.x + dot.y;
+                if (!top) m.dot2[cg][i] = dot2.x + dot2.y;
                 tc_fence_before();
                 if (!(ok = group_sync_and(1, ok, 256))) break;
                 if (warp == 0) {   // dc_i, then its sums to the chunk's end (two tokens a lane)
@@ -772,8 +862,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         tot += j < n ? o2[e] : 0.f;
                     }
                     tot = warp_sum(tot);
-                    const float g = warp_sum(lane < 8 ? m.sg[lane] : 0.f);
-                    const float end = fmaf(m.vec.up[63], g, tot);   // everything that decays with the whole chunk
+                    const float g = warp_sum(lane < 4 ? m.sg[hc & 1][lane] : 0.f);
+                    const float end = fmaf(vec.up[63], g, tot);   // everything that decays with the whole chunk
                     if (2 * lane == n - 1) c[0] += end;
                     if (2 * lane + 1 == n - 1) c[1] += end;
                     float sum = c[0] + c[1];
@@ -788,11 +878,11 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         const int j = 2 * lane + e;
                         if (j < n) {
                             a.dg[at + j] = e ? sum - c[0] : sum;
-                            a.dbeta[at + j] = m.da[j] * dalpha_dbeta_of(m.be[j], m.lam[j], d.euler);
+                            a.dbeta[at + j] = m.da[j] * dalpha_dbeta_of(m.be[hc & 1][j], m.lam[j], d.euler);
                         }
                     }
                 }
-                group_sync(1, 256);   // the head's vectors and sums are read
+                warp_arrive(&m.end, lane);
             }
         }
         tc_fence_before();
@@ -800,7 +890,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     if (!ok && lane == 0) atomicOr(&g_gb_status, 1u);
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tb, 512);
+    if (warp == 12) tmem_dealloc(tb, 512);
 }
 
 struct BwdTcWs {
