@@ -33,8 +33,8 @@ constexpr float kFloorAlpha = 1e-25f;
 //   D1 = [K; Q] G  (lanes 0..63: K G);   E = e^c dO as parts (the warps of lanes 64..127)
 //   D2 = (P T)^T dO + T^T Y,  Y = e^{c_last - c} K G as parts;   dX = D2
 //   D3 = Q^T E + K^T Z,  Z = -alpha e^c dX as parts;   G = e^{c_last} G + D3
-// dv = alpha dX goes out here.  G's parts, and dX's (in E's place, once Q^T E has read it), are
-// copied out as they lie in shared memory.
+// dv = alpha dX goes out here, and dX's parts, from registers; G's parts are copied out as they lie
+// in shared memory (a warp of its own does).
 struct Rs {
     using C = Chain<NP, 2>;
     static constexpr uint32_t KQ = 0;                     // 2 stages x 2 blocks x [K rows | Q rows]
@@ -42,10 +42,10 @@ struct Rs {
     static constexpr uint32_t DO = TP + NP * 16384;       // 2 stages
     static constexpr uint32_t G = DO + 2 * 8192;          // 3 blocks of 128 rows
     static constexpr uint32_t X = G + 3 * 16384;          // 3 blocks of 64 rows: Y, then Z
-    static constexpr uint32_t E = X + 3 * 8192;           // E, then dX
+    static constexpr uint32_t E = X + 3 * 8192;
     static constexpr uint32_t VEC = E + 3 * 8192;         // 2 stages of up, rest, al
     static constexpr uint32_t BAR = VEC + 2 * 768;
-    static constexpr int bars = 8 + 2 * 10;
+    static constexpr int bars = 7 + 2 * 8;
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
     static constexpr int warps = 20;                      // 16 epilogue, 2 products, copies in, copies out
 };
@@ -76,9 +76,8 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
     uint64_t* freed = bars + 2;       // [2] by both chains
     uint64_t* full_tp = bars + 4;
     uint64_t* freed_tp = bars + 5;    // by both chains
-    uint64_t* g_free = bars + 6;      // G's and dX's parts have been copied out
-    uint64_t* e_free = bars + 7;
-    uint64_t* chain0 = bars + 8;      // per chain: g_ready, y_ready, z_ready, r_ready (dX's parts), e_ready, d1, d2, d3, turn, d_e (Q^T E)
+    uint64_t* g_free = bars + 6;      // G's parts have been copied out
+    uint64_t* chain0 = bars + 7;      // per chain: g_ready, y_ready, z_ready, e_ready, d1, d2, d3, turn
     uint32_t* tslot = (uint32_t*)(bars + M::bars);
     const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * 64;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -93,12 +92,11 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
         mbar_init(full_tp, 1);
         mbar_init(freed_tp, 2);
         mbar_init(g_free, 1);
-        mbar_init(e_free, 1);
         for (int g = 0; g < 2; ++g) {
-            uint64_t* q = chain0 + 10 * g;
+            uint64_t* q = chain0 + 8 * g;
             mbar_init(q, 8);   // warps
-            for (int i = 1; i < 5; ++i) mbar_init(q + i, 4);
-            for (int i = 5; i < 10; ++i) mbar_init(q + i, 1);
+            for (int i = 1; i < 4; ++i) mbar_init(q + i, 4);
+            for (int i = 4; i < 8; ++i) mbar_init(q + i, 1);
         }
         fence_mbar_init();
     }
@@ -156,24 +154,19 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 for (int it = 0; it < nch; ++it) {
                     const uint32_t ph = it & 1;
                     const size_t rec = (rec0 + nch - 1 - it) * gridDim.y + blockIdx.y;
-                    ok = mbar_wait(chain0, ph, kWaitLimit) && mbar_wait(chain0 + 10, ph, kWaitLimit);
+                    ok = mbar_wait(chain0, ph, kWaitLimit) && mbar_wait(chain0 + 8, ph, kWaitLimit);
                     if (!ok) break;
                     bulk_s2g(a.rec_G + rec * kRecS, sm + M::G, kRecS);
                     bulk_commit();
-                    bulk_wait_read();   // (and the dX of the chunk before)
+                    bulk_wait_read();
                     mbar_arrive(g_free);
-                    if (it > 0) mbar_arrive(e_free);
-                    ok = mbar_wait(chain0 + 3, ph, kWaitLimit) && mbar_wait(chain0 + 13, ph, kWaitLimit);
-                    if (!ok) break;
-                    bulk_s2g(a.rec_dX + rec * kRecU, sm + M::E, kRecU);
-                    bulk_commit();
                 }
                 bulk_wait_read();
             }
         } else if (warp < 18) {
                 // ---------------- a chain's products
                 const int g = warp - 16;
-                uint64_t* q = chain0 + 10 * g;
+                uint64_t* q = chain0 + 8 * g;
                 const uint32_t t1 = tb + g * 256, t2 = t1 + 96, t3 = t1;   // D3 over D1, which is read by then
                 const int nblk = (d.dk + 63) / 64;
                 const bool one = elect_one();
@@ -192,8 +185,8 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     const uint64_t dDO = sdesc_sw128(smem_u32(sm + M::DO + (it & 1) * 8192)) + g * 4;   // 32 columns in
                     if (!(ok = warp_wait(q, ph) && warp_wait(&full[it & 1], (it >> 1) & 1))) break;
                     if (it > 0 && one) mbar_arrive(&freed[(it - 1) & 1]);
-                    if (g == 1) ok = warp_wait(chain0 + 8, ph);   // the chains take turns: see Chain
-                    else if (it > 0) ok = warp_wait(chain0 + 18, ph ^ 1u);
+                    if (g == 1) ok = warp_wait(chain0 + 7, ph);   // the chains take turns: see Chain
+                    else if (it > 0) ok = warp_wait(chain0 + 15, ph ^ 1u);
                     if (!ok) break;
                     if (one) {
 #pragma unroll 1
@@ -201,7 +194,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f16_ss(t1, ka + blk * 1024 + ks * 2, dG + blk * 512 + ks * 128, kk, blk + ks > 0);
-                        mma_commit(q + 5);
+                        mma_commit(q + 4);
                     }
                     if (!(ok = warp_wait(full_tp, ph))) break;
                     if (one) {
@@ -222,22 +215,21 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f16_ss(t2 + 32, dT + p * 1024 + ks * 128, dX + ks * 128,
                                            idesc_f16(128, (NP - p) * 32, true, true, true), p + ks > 0);
-                        mma_commit(q + 6);
-                        mbar_arrive(q + 8);
+                        mma_commit(q + 5);
+                        mbar_arrive(q + 7);
                     }
-                    if (!(ok = warp_wait(q + 4, ph))) break;   // (long since)
+                    if (!(ok = warp_wait(q + 3, ph))) break;   // (long since)
                     if (one) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)   // Q^T E (rows 64..127 of [K; Q])
                             mma_f16_ss(t3, km + 512 + ks * 128, dE + ks * 128, m3, ks > 0);
-                        mma_commit(q + 9);
-                    }
+                        }
                     if (!(ok = warp_wait(q + 2, ph))) break;
                     if (one) {
                         mbar_arrive(freed_tp);   // (D2 is done: z_ready came from it)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) mma_f16_ss(t3, km + ks * 128, dX + ks * 128, m3, 1u);
-                        mma_commit(q + 7);
+                        mma_commit(q + 6);
                     }
                 }
         }
@@ -246,7 +238,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
         const int g = warp >> 3, row = 32 * (warp & 3) + lane, cc = ((warp >> 2) & 1) * 16;
         const int i = row & 63, col = c0 + g * 32 + cc;
         const bool top = row < 64, in = col < d.dv;
-        uint64_t* q = chain0 + 10 * g;
+        uint64_t* q = chain0 + 8 * g;
         const uint32_t t1 = taddr(tb, 32 * (warp & 3), g * 256 + cc), t2 = t1 + 96, t3 = t1;
         const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + col;
         float2 G[8];
@@ -280,22 +272,21 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
             float2 y[8];
             if (top) {
                 const float rest = vec[64 + i], al = vec[128 + i];
-                if (!(ok = warp_wait(q + 5, ph))) break;
+                if (!(ok = warp_wait(q + 4, ph))) break;
                 tmem_sum16<NP>(t1, 32, y);
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = live ? mul2(both(rest), y[m]) : both(0.f);
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 1, lane);
-                if (!(ok = warp_wait(q + 6, ph))) break;
+                if (!(ok = warp_wait(q + 5, ph))) break;
                 float2 X[8];
                 tmem_sum16<NP + 1>(t2, 32, X);
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = mul2(both(-al * up), X[m]);
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
-                if (!(ok = warp_wait(q + 9, ph))) break;
-                C::put16(sm + M::E, 8192, g, i, cc, X);
-                warp_arrive(q + 3, lane);
+                // (tiles of 64 rows, one a part, in the operand layout)
+                put16_parts<NP>(a.rec_dX + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecU, i, g * 32 + cc, X);
                 if (live && in) {
                     Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
 #pragma unroll
@@ -303,16 +294,15 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     st16(vp, y);
                 }
             } else {
-                if (it > 0 && !(ok = warp_wait(e_free, ph ^ 1u))) break;
                 const uint4 w0 = *reinterpret_cast<const uint4*>(dt + sw128(i, g * 32 + cc));
                 const uint4 w1 = *reinterpret_cast<const uint4*>(dt + sw128(i, g * 32 + cc + 8));
                 const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = live ? mul2(both(up), bf16x2(w[m])) : both(0.f);
                 C::put16(sm + M::E, 8192, g, i, cc, y);
-                warp_arrive(q + 4, lane);
+                warp_arrive(q + 3, lane);
             }
-            if (!(ok = warp_wait(q + 7, ph))) break;
+            if (!(ok = warp_wait(q + 6, ph))) break;
             tmem_sum16<NP>(t3, 32, y);
 #pragma unroll
             for (int m = 0; m < 8; ++m) G[m] = fma2(both(last), G[m], y[m]);
@@ -339,47 +329,42 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
 // so that a lane is a token: decays scale lanes, and the dot products with q and k that dg needs
 // are sums within a thread.
 //
-// The recorded parts come by bulk copy in the layout the products read (Chain<3, 2>: a 64-byte
-// half row is 32 columns of one part), each kind into a buffer of its own that is filled again as
-// soon as its products are done: dX and dO (with zeros beside dO, so that the products of dX's
-// second and third part add nothing to dO's lanes), U, S, G.  Warps: 8 for the epilogues, 4 that
-// stage what is not recorded (q, k, dO, the head's vectors: loaded ahead into registers) and sum
-// <S, G>, one that issues products, one that copies.  The epilogue of the pairs runs while the
-// last slice's products do.
-constexpr int kGrWarps = 14;
+// The recorded parts come by bulk copy as the products read them, each kind into a buffer of its
+// own that is filled again as soon as its products are done: [dO; dX_0], [0; dX_1], [0; dX_2], U, S,
+// G; dO, q and k by TMA.  Warps: 8 epilogue (a lane a token; <S, G> in the products' shadow), one
+// that issues products, one that copies.  The epilogue of the pairs runs while the last slice's
+// products do.
+constexpr int kGrWarps = 10;
 constexpr uint32_t kGrQK = 0;                    // 2 blocks of 64 dk x [Q rows | K rows]
-constexpr uint32_t kGrAX = 32768;                // 3 blocks of [dO | 0 ; dX parts], 64 rows each
-constexpr uint32_t kGrU = kGrAX + 49152;         // 3 blocks of 64 rows (as an A operand, the tile before fills rows 0..63)
-constexpr uint32_t kGrS = kGrU + 24576;          // 3 blocks of 128 rows
-constexpr uint32_t kGrG = kGrS + 49152;          // 3 blocks of 128 rows
+constexpr uint32_t kGrAX = 32768;                // dO | dX_0 | 0 | dX_1 | 0 | dX_2, tiles of 64 rows
+constexpr uint32_t kGrU = kGrAX + 49152;         // U_0 | U_1 | U_2 (as an A operand, the tile before fills rows 0..63)
+constexpr uint32_t kGrS = kGrU + 24576;          // 3 blocks of 128 rows: Chain<3, 2>
+constexpr uint32_t kGrG = kGrS + 49152;          // likewise
 constexpr uint32_t kGrP5 = kGrS;                 // [dPD; dAD], two parts, in S's place
 constexpr uint32_t kGrMisc = kGrG + 49152;
-constexpr uint32_t kGrZero = kGrAX + 32768;      // 64 rows of zeros (AX's third block, rows 0..63)
+constexpr uint32_t kGrZero = kGrAX + 16384;      // a tile of zeros
 // tensor-memory columns; D5 lies over D3 and D3s (the small part pairs of D3), which are read before it starts
 constexpr uint32_t cDa = 0, cD6 = 128, cD3 = 256, cD3s = 320, cD5 = 256, cD4 = 384;
 
 struct GrMisc {
-    GVec vec[2];           // (by the head's parity: the next one's are loaded ahead)
-    float be[2][64];
-    float lam[64], da[64], dc[64];
+    GVec vec;
+    float be[64], lam[64], da[64], dc[64];
     float rs[2][128];      // row sums of a column group
     float cs[4][64];       // column sums of a lane quadrant
     float dot[2][128];     // per column group: q . dq's, and k . dk's state terms
     float dot2[2][64];     // k . (e^{c_last - c} U G^T)
-    float sg[2][4];
-    uint64_t f_ax, f_u, f_s, f_g;      // copies have landed
-    uint64_t e_ax, e_u, e_s, e_g;      // products have read (and, S and G, the epilogue)
-    uint64_t qk, d3, d5, p5;           // [Q; K] and vectors are in; products; [dPD; dAD]
-    uint64_t sgs, end;                 // the head's <S, G> is in; the epilogue has read everything of the head
+    float sg[2][8];        // by the head's parity
+    uint64_t f_vec, f_qk, f_ax, f_u, f_s, f_g;   // copies have landed
+    uint64_t e_ax, e_u, e_s, e_g;      // products (and <S, G>) have read
+    uint64_t d3, d5, p5;               // products; [dPD; dAD]
+    uint64_t qk, end;                  // [Q; K] is fit for the products; the epilogue has read everything of the head
     uint32_t tslot;
 };
 constexpr size_t kGrSmem = 1024 + kGrMisc + sizeof(GrMisc);
 static_assert(kGrSmem <= 232448, "shared memory per CTA");
+static_assert(sizeof(GVec) % 16 == 0 && kGrMisc % 1024 == 0, "the vectors are copied in place");
 
 struct GradArgs {
-    const __nv_bfloat16* q;
-    const __nv_bfloat16* k;
-    const __nv_bfloat16* dO;
     const float* beta;
     const GVec* vec;
     const unsigned char* S;
@@ -419,30 +404,46 @@ __device__ __forceinline__ void parts8(const unsigned char* base, int r, int g, 
     x[3] = add2(bf16x2(a.w), add2(bf16x2(b.w), bf16x2(c.w)));
 }
 
+// This thread's share (of 256) of <S, G> over a slice.
+__device__ __forceinline__ float inner256(const unsigned char* S, const unsigned char* G, int id) {
+    float2 w = both(0.f);
+#pragma unroll 2
+    for (int e = id; e < 1024; e += 256) {   // rows of eight 8-column chunks
+        float2 u[4], v[4];
+        parts8(S, e >> 3, (e >> 2) & 1, e & 3, u);
+        parts8(G, e >> 3, (e >> 2) & 1, e & 3, v);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w = fma2(u[x], v[x], w);
+    }
+    return w.x + w.y;
+}
+
 // Descriptor advance (16-byte units) to part p of column group g in blocks of `blk` bytes: Chain<3, 2>.
 __host__ __device__ constexpr uint32_t at_part(int g, int p, uint32_t blk) { return Chain<3, 2>::part(g, p, blk) >> 4; }
 
 template <typename Tout>
-__global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs a) {
+__global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs a, const __grid_constant__ CUtensorMap tm_q,
+                                                              const __grid_constant__ CUtensorMap tm_k,
+                                                              const __grid_constant__ CUtensorMap tm_do) {
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     GrMisc& m = *reinterpret_cast<GrMisc*>(sm + kGrMisc);
     const int rep = d.H / d.Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int dk = d.dk, dv = d.dv, nsl = (dv + 63) / 64, nblk = (dk + 63) / 64;
+    const int dk = d.dk, nsl = (d.dv + 63) / 64, nblk = (dk + 63) / 64;
     const long long items = (long long)a.slots * d.Hk;   // key head fastest: neighbours share a sequence's tokens
     if (tid == 0) {
-        for (uint64_t* p : {&m.f_u, &m.f_s, &m.f_g, &m.e_ax, &m.e_u, &m.d3, &m.d5}) mbar_init(p, 1);
-        for (uint64_t* p : {&m.f_ax, &m.e_s, &m.e_g}) mbar_init(p, 1 + 4);   // (f_ax: the copy of dX and the staging warps' dO)
-        for (uint64_t* p : {&m.qk, &m.sgs}) mbar_init(p, 4);
-        for (uint64_t* p : {&m.p5, &m.end}) mbar_init(p, 8);
+        for (uint64_t* p : {&m.f_vec, &m.f_qk, &m.f_ax, &m.f_u, &m.f_s, &m.f_g, &m.e_ax, &m.e_u, &m.d3, &m.d5})
+            mbar_init(p, 1);
+        for (uint64_t* p : {&m.e_s, &m.e_g}) mbar_init(p, 1 + 8);
+        for (uint64_t* p : {&m.qk, &m.p5, &m.end}) mbar_init(p, 8);
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 8) {
         tmem_alloc(&m.tslot, 512);
         tmem_relinquish();
     }
-    for (int e = tid; e < 3 * 512; e += kGrWarps * 32)   // rows 0..63 of AX: zeros, but for dO
-        *reinterpret_cast<uint4*>(sm + kGrAX + (e >> 9) * 16384 + (e & 511) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int e = tid; e < 1024; e += kGrWarps * 32)
+        *reinterpret_cast<uint4*>(sm + kGrZero + (e >> 9) * 16384 + (e & 511) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     const uint32_t tb = m.tslot;
     bool ok = true;
 
-    // every role walks the same items, value heads and slices; `sc` counts slices, `hc` heads
+    // every role walks the same chunks, value heads and slices; `sc` counts slices, `hc` heads
     uint32_t sc = 0, hc = 0;
     const auto place = [&](long long x, int& hk, int& slot, int& b, SeqAt& s, int& t0) {
         hk = (int)(x % d.Hk);
@@ -460,247 +461,148 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
         t0 = (slot - s.slot0) * kGC;
         return min(kGC, s.len - t0);
     };
-    if (warp == 13) {
+    if (warp == 9) {
         // ---------------- copies in
         if (lane == 0) {
+            uint32_t kc = 0;   // chunks
             for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
                 int hk, slot, b, t0;
                 SeqAt s;
                 if (place(x, hk, slot, b, s, t0) <= 0) continue;
-                for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h)
+                const int t = s.start + t0;
+                for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h, ++hc) {
                     for (int sl = 0; sl < nsl && ok; ++sl, ++sc) {
                         const size_t rec = ((size_t)h * a.slots + slot) * nsl + sl;
                         const uint32_t ph = (sc & 1) ^ 1;   // (the first use of a buffer waits for nothing)
                         const auto next = [&](uint64_t* empty, uint64_t* full, uint32_t bytes) {
                             ok = ok && mbar_wait(empty, ph, kWaitLimit);
                             if (ok) mbar_arrive_expect_tx(full, bytes);
+                            return ok;
                         };
-                        next(&m.e_ax, &m.f_ax, kRecU);
-                        if (!ok) break;
+                        if (!next(&m.e_ax, &m.f_ax, kRecU + 8192)) break;
+                        tma_load_4d(sm + kGrAX, &tm_do, 64 * sl, t, h, s.batch, &m.f_ax);
                         for (int p = 0; p < 3; ++p)
                             bulk_g2s(sm + kGrAX + p * 16384 + 8192, a.dX + rec * kRecU + p * 8192, 8192, &m.f_ax);
-                        next(&m.e_u, &m.f_u, kRecU);
-                        if (!ok) break;
+                        if (!next(&m.e_u, &m.f_u, kRecU)) break;
                         bulk_g2s(sm + kGrU, a.U + rec * kRecU, kRecU, &m.f_u);
-                        next(&m.e_s, &m.f_s, kRecS);
-                        if (!ok) break;
+                        if (!next(&m.e_s, &m.f_s, kRecS)) break;
                         bulk_g2s(sm + kGrS, a.S + rec * kRecS, kRecS, &m.f_s);
-                        next(&m.e_g, &m.f_g, kRecS);
-                        if (!ok) break;
+                        if (!next(&m.e_g, &m.f_g, kRecS)) break;
                         bulk_g2s(sm + kGrG, a.G + rec * kRecS, kRecS, &m.f_g);
+                        if (sl > 0) continue;
+                        // (after what can go ahead of the end of the head before)
+                        if (hc > 0) ok = mbar_wait(&m.end, (hc - 1) & 1, kWaitLimit);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&m.f_vec, (uint32_t)sizeof(GVec));
+                        bulk_g2s(&m.vec, a.vec + (size_t)h * a.slots + slot, sizeof(GVec), &m.f_vec);
+                        if (h == hk * rep) {
+                            mbar_arrive_expect_tx(&m.f_qk, 4 * 8192);
+                            for (int blk = 0; blk < 2; ++blk) {
+                                tma_load_4d(sm + kGrQK + blk * 16384, &tm_q, 64 * blk, t, hk, s.batch, &m.f_qk);
+                                tma_load_4d(sm + kGrQK + blk * 16384 + 8192, &tm_k, 64 * blk, t, hk, s.batch, &m.f_qk);
+                            }
+                            ++kc;
+                        }
                     }
+                }
             }
             if (!ok) {   // what is under way lands before the CTA ends
-                mbar_wait(&m.f_ax, sc & 1, kWaitLimit);
-                mbar_wait(&m.f_u, sc & 1, kWaitLimit);
-                mbar_wait(&m.f_s, sc & 1, kWaitLimit);
-                mbar_wait(&m.f_g, sc & 1, kWaitLimit);
+                for (uint64_t* p : {&m.f_ax, &m.f_u, &m.f_s, &m.f_g}) mbar_wait(p, sc & 1, kWaitLimit);
+                if (kc) mbar_wait(&m.f_qk, (kc - 1) & 1, kWaitLimit);
+                mbar_wait(&m.f_vec, hc & 1, kWaitLimit);
             }
         }
-    } else if (warp == 12) {
+    } else if (warp == 8) {
         // ---------------- products
-        {
-            const bool one = elect_one();
-            const uint64_t ax = sdesc_sw128(smem_u32(sm + kGrAX)), us = sdesc_sw128(smem_u32(sm + kGrU)),
-                           ss = sdesc_sw128(smem_u32(sm + kGrS)), gs = sdesc_sw128(smem_u32(sm + kGrG)),
-                           qk = sdesc_sw128(smem_u32(sm + kGrQK));
-            const uint32_t p5 = smem_u32(sm + kGrP5), z0 = smem_u32(sm + kGrZero), kq = smem_u32(sm + kGrQK);
-            const uint64_t kb = sdesc_sw128(kq + 8192, 16384), qb = sdesc_sw128(kq, 16384);
-            constexpr uint32_t n64 = idesc_f16(128, 64, false, false, true), n128 = idesc_f16(128, 128, false, false, true);
-            for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
-                int hk, slot, b, t0;
-                SeqAt s;
-                if (place(x, hk, slot, b, s, t0) <= 0) continue;
-                for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h, ++hc) {
-                    // the head's [Q; K] and vectors are in, and the epilogue has read the accumulators of the head before
-                    ok = warp_wait(&m.qk, hc & 1);
-                    if (!ok) break;
-                    if (one) {
+        const bool one = elect_one();
+        const uint64_t ax = sdesc_sw128(smem_u32(sm + kGrAX)), us = sdesc_sw128(smem_u32(sm + kGrU)),
+                       ss = sdesc_sw128(smem_u32(sm + kGrS)), gs = sdesc_sw128(smem_u32(sm + kGrG)),
+                       qk = sdesc_sw128(smem_u32(sm + kGrQK));
+        const uint32_t p5 = smem_u32(sm + kGrP5), z0 = smem_u32(sm + kGrZero), kq = smem_u32(sm + kGrQK);
+        const uint64_t kb = sdesc_sw128(kq + 8192, 16384), qb = sdesc_sw128(kq, 16384);
+        constexpr uint32_t n64 = idesc_f16(128, 64, false, false, true), n128 = idesc_f16(128, 128, false, false, true);
+        uint32_t kc = 0;   // chunks
+        for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
+            int hk, slot, b, t0;
+            SeqAt s;
+            if (place(x, hk, slot, b, s, t0) <= 0) continue;
+            if (!(ok = warp_wait(&m.f_qk, kc++ & 1))) break;
+            for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h, ++hc) {
+                // [Q; K] is fit, and the epilogue has read the accumulators of the head before
+                if (!(ok = warp_wait(&m.qk, hc & 1))) break;
+                if (one) {
 #pragma unroll 1
-                        for (int blk = 0; blk < nblk; ++blk)
+                    for (int blk = 0; blk < nblk; ++blk)
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ss(tb + cD4, qk + blk * 1024 + ks * 2, qk + 512 + blk * 1024 + ks * 2, n64, blk + ks > 0);
-                    }
-                    for (int sl = 0; sl < nsl; ++sl, ++sc) {
-                        const uint32_t ph = sc & 1, more = sl > 0;
-                        ok = warp_wait(&m.f_ax, ph) && warp_wait(&m.f_u, ph);
-                        if (!ok) break;
-                        if (one) {
-                            // The accumulators cut off what falls below their last bit, at every instruction: the
-                            // small part pairs go first (and, for dbeta's D3, into columns of their own), so that
-                            // few of them meet a large sum.
-#pragma unroll
-                            for (int o = NP - 1; o >= 0; --o)   // pairs (p, o - p) of order o; 32 columns are two steps of K
-#pragma unroll
-                                for (int p = 0; p <= o; ++p)
-#pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks)
-                                        mma_f16_ss(tb + (o ? cD3s : cD3), ax + at_part(ks >> 1, p, 16384) + (ks & 1) * 2,
-                                                   us + at_part(ks >> 1, o - p, 8192) + (ks & 1) * 2, n64,
-                                                   more | !((o == NP - 1 || o == 0) && p == 0 && ks == 0));
-                            if (sl == nsl - 1) mma_commit(&m.d3);   // the pairs' epilogue can start
-                        }
-                        ok = warp_wait(&m.f_s, ph);
-                        if (!ok) break;
-                        if (one) {
-#pragma unroll
-                            for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-                                for (int p = 0; p <= o; ++p)
-#pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks)
-                                        mma_f16_ss(tb + cDa, ax + at_part(ks >> 1, p, 16384) + (ks & 1) * 2,
-                                                   ss + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
-                                                   more | !(o == NP - 1 && p == 0 && ks == 0));
-                            mma_commit(&m.e_ax);
-                            if (sl < nsl - 1) mma_commit(&m.e_s);
-                        }
-                        ok = warp_wait(&m.f_g, ph);
-                        if (!ok) break;
-                        if (one) {
-#pragma unroll
-                            for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-                                for (int p = 0; p <= o; ++p)
-#pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks)
-                                        mma_f16_ss(tb + cD6, us + at_part(ks >> 1, p, 8192) - 512 + (ks & 1) * 2,
-                                                   gs + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
-                                                   more | !(o == NP - 1 && p == 0 && ks == 0));
-                            mma_commit(&m.e_u);
-                            mma_commit(&m.e_g);
-                        }
-                    }
-                    if (!ok) break;
-                    ok = warp_wait(&m.p5, hc & 1);
-                    if (!ok) break;
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ss(tb + cD4, qk + blk * 1024 + ks * 2, qk + 512 + blk * 1024 + ks * 2, n64, blk + ks > 0);
+                }
+                for (int sl = 0; sl < nsl; ++sl, ++sc) {
+                    const uint32_t ph = sc & 1, more = sl > 0;
+                    if (!(ok = warp_wait(&m.f_ax, ph) && warp_wait(&m.f_u, ph))) break;
+                    // The accumulators cut off what falls below their last bit, at every instruction: the small
+                    // part pairs go first (and, for dbeta's D3, into columns of their own), so that few of them
+                    // meet a large sum.
                     if (one) {
 #pragma unroll
-                        for (int p = 1; p >= 0; --p) {
-                            const uint64_t a0 = sdesc_sw128(p5 + p * 16384);
-                            const uint64_t at = sdesc_sw128(z0, p5 + p * 16384 + 8192 - z0);   // [0 | dAD], rows are K indices
-                            const uint64_t pt = sdesc_sw128(z0, p5 + p * 16384 - z0);          // [0 | dPD]
+                        for (int o = NP - 1; o >= 0; --o)   // pairs (p, o - p) of order o
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ss(tb + cD5, a0 + ks * 2, kb + ks * 128, idesc_f16(128, 128, false, true, true), p < 1 || ks > 0);
+                            for (int p = 0; p <= o; ++p)
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ss(tb + cD5, at + ks * 128, kb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
+                                for (int ks = 0; ks < 4; ++ks)
+                                    mma_f16_ss(tb + (o ? cD3s : cD3), ax + p * 1024 + ks * 2, us + (o - p) * 512 + ks * 2, n64,
+                                               more | !((o == NP - 1 || o == 0) && p == 0 && ks == 0));
+                        if (sl == nsl - 1) mma_commit(&m.d3);   // the pairs' epilogue can start
+                    }
+                    if (!(ok = warp_wait(&m.f_s, ph))) break;
+                    if (one) {   // (S and G: 32 columns are two steps of K)
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ss(tb + cD5, pt + ks * 128, qb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
+                        for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                            for (int p = 0; p <= o; ++p)
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)
+                                    mma_f16_ss(tb + cDa, ax + p * 1024 + ks * 2,
+                                               ss + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
+                                               more | !(o == NP - 1 && p == 0 && ks == 0));
+                        mma_commit(&m.e_ax);
+                        if (sl < nsl - 1) mma_commit(&m.e_s);
+                    }
+                    if (!(ok = warp_wait(&m.f_g, ph))) break;
+                    if (one) {
+#pragma unroll
+                        for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+                            for (int p = 0; p <= o; ++p)
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)
+                                    mma_f16_ss(tb + cD6, us + p * 512 - 512 + ks * 2,
+                                               gs + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
+                                               more | !(o == NP - 1 && p == 0 && ks == 0));
+                        mma_commit(&m.e_u);
+                        mma_commit(&m.e_g);
+                    }
+                }
+                if (!ok || !(ok = warp_wait(&m.p5, hc & 1))) break;
+                if (one) {
+#pragma unroll
+                    for (int p = 1; p >= 0; --p) {
+                        const uint64_t a0 = sdesc_sw128(p5 + p * 16384);
+                        const uint64_t at = sdesc_sw128(z0, p5 + p * 16384 + 8192 - z0);   // [0 | dAD], rows are K indices
+                        const uint64_t pt = sdesc_sw128(z0, p5 + p * 16384 - z0);          // [0 | dPD]
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ss(tb + cD5, a0 + ks * 2, kb + ks * 128, idesc_f16(128, 128, false, true, true), p < 1 || ks > 0);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ss(tb + cD5, at + ks * 128, kb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16_ss(tb + cD5, pt + ks * 128, qb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
                     }
                     mma_commit(&m.d5);
-                    mma_commit(&m.e_s);   // (S's buffer, which held [dPD; dAD], is free again)
-                    }
+                    mma_commit(&m.e_s);   // (S's buffer, which held [dPD; dAD])
                 }
-            }
-        }
-    } else if (warp >= 8) {
-        // ---------------- staging: [Q; K] and vectors of a head, dO of a slice, <S, G>
-        const int st = tid - 256;
-        long long x = blockIdx.x;
-        int hk = 0, slot = 0, b, t0, n = 0, t = 0;
-        SeqAt s;
-        const auto settle = [&]() {   // x: this CTA's next chunk that exists (or past the end)
-            for (; x < items; x += gridDim.x) {
-                n = place(x, hk, slot, b, s, t0);
-                t = s.start + t0;
-                if (n > 0) break;
-            }
-        };
-        settle();
-        const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
-        uint4 qr[8], kr[8], dr[4];
-        float vr[5], br = 0.f;
-        const auto fetch_qk = [&]() {   // rows of 16 chunks
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int r = (st >> 4) + 8 * e, ch = st & 15;
-                const bool in = x < items && r < n && ch * 8 < dk;
-                qr[e] = in ? __ldg(reinterpret_cast<const uint4*>(a.q + at3(d.qs, s.batch, hk, t + r) + ch * 8)) : z4;
-                kr[e] = in ? __ldg(reinterpret_cast<const uint4*>(a.k + at3(d.ks, s.batch, hk, t + r) + ch * 8)) : z4;
-            }
-        };
-        const auto fetch_head = [&](int h) {
-            if (x >= items) return;
-            const float* v = reinterpret_cast<const float*>(a.vec + (size_t)h * a.slots + slot);
-#pragma unroll
-            for (int e = 0; e < 5; ++e) vr[e] = st < 64 ? __ldg(v + e * 64 + st) : 0.f;
-            br = st < n && st < 64 ? __ldg(a.beta + at3(d.bs, s.batch, h, t + st)) : 0.f;
-        };
-        const auto fetch_do = [&](int h, int sl) {   // rows of eight chunks
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = (st >> 3) + 16 * e, col = sl * 64 + (st & 7) * 8;
-                dr[e] = x < items && r < n && col < dv
-                            ? __ldg(reinterpret_cast<const uint4*>(a.dO + at3(d.dos, s.batch, h, t + r) + col)) : z4;
-            }
-        };
-        fetch_qk();
-        fetch_head(hk * rep);
-        fetch_do(hk * rep, 0);
-        while (x < items && ok) {
-            for (int h = hk * rep, he = (hk + 1) * rep; h < he && ok; ++h, ++hc) {
-                // (the head before: its epilogue is over, and the one before that is with these vectors)
-                if (hc > 0) ok = warp_wait(&m.end, (hc - 1) & 1);
-                if (h == hk * rep) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = (st >> 4) + 8 * e, ch = st & 15;
-                        unsigned char* to = sm + kGrQK + (ch >> 3) * 16384 + sw128(r, (ch & 7) * 8);
-                        *reinterpret_cast<uint4*>(to) = qr[e];
-                        *reinterpret_cast<uint4*>(to + 8192) = kr[e];
-                    }
-                }
-                if (st < 64) {
-#pragma unroll
-                    for (int e = 0; e < 5; ++e) reinterpret_cast<float*>(&m.vec[hc & 1])[e * 64 + st] = vr[e];
-                    m.be[hc & 1][st] = br;
-                }
-                warp_arrive(&m.qk, lane);
-                float sg = 0.f;
-                for (int sl = 0; sl < nsl; ++sl, ++sc) {
-                    const uint32_t ph = sc & 1;
-                    // dO's 64 columns into the first half rows of AX's blocks 0 and 1 (its products before are over)
-                    ok = ok && warp_wait(&m.e_ax, ph ^ 1u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint4*>(sm + kGrAX + ((st >> 2) & 1) * 16384 + sw128((st >> 3) + 16 * e, (st & 3) * 8)) = dr[e];
-                    warp_arrive(&m.f_ax, lane);
-                    if (sl + 1 < nsl) {
-                        fetch_do(h, sl + 1);
-                    } else if (h + 1 < he) {
-                        fetch_head(h + 1);
-                        fetch_do(h + 1, 0);
-                    } else {   // the next chunk's
-                        x += gridDim.x;
-                        settle();
-                        fetch_qk();
-                        fetch_head(hk * rep);
-                        fetch_do(hk * rep, 0);
-                    }
-                    ok = ok && warp_wait(&m.f_s, ph) && warp_wait(&m.f_g, ph);
-#pragma unroll 2
-                    for (int e = st; e < 1024; e += 128) {   // rows of eight 8-column chunks
-                        float2 u[4], v[4];
-                        parts8(sm + kGrS, e >> 3, (e >> 2) & 1, e & 3, u);
-                        parts8(sm + kGrG, e >> 3, (e >> 2) & 1, e & 3, v);
-                        float2 w = mul2(u[0], v[0]);
-#pragma unroll
-                        for (int k = 1; k < 4; ++k) w = fma2(u[k], v[k], w);
-                        sg += w.x + w.y;
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&m.e_g);
-                        if (sl + 1 < nsl) mbar_arrive(&m.e_s);   // (the last slice's S buffer goes on to [dPD; dAD])
-                    }
-                }
-                sg = warp_sum(sg);
-                if (lane == 0) m.sg[hc & 1][warp - 8] = sg;
-                warp_arrive(&m.sgs, lane);
             }
         }
     } else {
@@ -709,16 +611,43 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
         const bool top = row < 64;
         const uint32_t lq = taddr(tb, 32 * qd, 0);
         float* my = a.acc ? a.acc + ((size_t)blockIdx.x * 128 + row) * 128 + 64 * cg : nullptr;
-        for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
+        uint32_t kc = 0;   // chunks
+        for (long long x = blockIdx.x; x < items && ok; x += gridDim.x, ++kc) {
             int hk, slot, b, t0;
             SeqAt s;
             const int n = place(x, hk, slot, b, s, t0);
-            if (n <= 0) continue;
+            if (n <= 0) {
+                --kc;
+                continue;
+            }
             const int t = s.start + t0;
             for (int h = hk * rep; h < (hk + 1) * rep && ok; ++h, ++hc) {
-                const GVec& vec = m.vec[hc & 1];
+                const GVec& vec = m.vec;
+                const float be = i < n ? __ldg(a.beta + at3(d.bs, s.batch, h, t + i)) : 0.f;
+                if (h == hk * rep) {
+                    ok = warp_wait(&m.f_qk, kc & 1);
+                    if (d.packed && n < kGC)   // rows past the sequence are another's: zero them (0 x NaN is not 0)
+                        for (int e = tid; e < (kGC - n) * 32; e += 256)
+                            *reinterpret_cast<uint4*>(sm + kGrQK + (e & 3) * 8192 + (n + (e >> 5)) * 128 + ((e >> 2) & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                }
+                warp_arrive(&m.qk, lane);
+                ok = ok && warp_wait(&m.f_vec, hc & 1);
+                // ---- <S, G>, slice by slice
+                float sg = 0.f;
+                for (int sl = 0; sl < nsl; ++sl, ++sc) {
+                    ok = ok && warp_wait(&m.f_s, sc & 1) && warp_wait(&m.f_g, sc & 1);
+                    sg += inner256(sm + kGrS, sm + kGrG, tid);
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&m.e_g);
+                        if (sl + 1 < nsl) mbar_arrive(&m.e_s);   // (the last slice's S buffer goes on to [dPD; dAD])
+                    }
+                }
+                sg = warp_sum(sg);
+                if (lane == 0) m.sg[hc & 1][warp] = sg;
                 // ---- the chunk's pairs (i, j): columns j = 32 cg .. 32 cg + 31 of this lane's row
-                ok = warp_wait(&m.d3, hc & 1);
+                ok = ok && warp_wait(&m.d3, hc & 1);
                 const float al = vec.al[i], sw = top ? 1.f : -al;
                 const int diag = top ? i + 1 : i;                       // columns below this are kept
                 const bool some = 32 * cg < 32 * (qd & 1) + 32;         // the warp's rows reach these columns
@@ -775,7 +704,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 }
                 m.rs[cg][row] = rsum;
                 // (S's buffer: the last slice's products have read it, and so has <S, G>)
-                ok = ok && warp_wait(&m.e_u, (nsl * (hc + 1) - 1) & 1) && warp_wait(&m.sgs, hc & 1);   // D6 follows Da
+                ok = ok && warp_wait(&m.e_u, (nsl * (hc + 1) - 1) & 1);   // D6 follows Da
+                if (!(ok = group_sync_and(1, ok, 256))) break;                  // (the warps leave together if a wait gave up)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint4 w[2];
@@ -785,8 +715,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         *reinterpret_cast<uint4*>(sm + kGrP5 + p * 16384 + sw128(row, 32 * cg + 8 * k)) = w[p];
                 }
                 warp_arrive(&m.p5, lane);
-                if (lane == 0 && warp < 4) mbar_arrive(&m.e_s);   // with the products' own arrival after D5: the buffer is free
-                if (!(ok = group_sync_and(1, ok, 256))) break;   // the sums by rows and columns are in
+                if (lane == 0) mbar_arrive(&m.e_s);   // with the products' own arrival after D5: the buffer is free
                 if (tid < 64) {
                     float c = 0.f;
 #pragma unroll
@@ -794,10 +723,11 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) c -= m.cs[e][tid];
                     m.dc[tid] = c;
+                    m.be[tid] = be;
                 }
                 const float up = vec.up[i], rest = vec.rest[i];
                 const float2 sa = both(top ? up : -al * up), rs2 = both(rest);
-                const float2 dl = both(top ? 0.f : 2.f * m.da[i] * dalpha_dlambda_of(m.be[hc & 1][i], m.lam[i], d.euler));
+                const float2 dl = both(top ? 0.f : 2.f * m.da[i] * dalpha_dlambda_of(be, m.lam[i], d.euler));
                 float2 dot = both(0.f), dot2 = both(0.f);
                 Tout* out = top ? (Tout*)a.dq + at3(d.dqs, s.batch, hk, t + i) : (Tout*)a.dk + at3(d.dks, s.batch, hk, t + i);
                 ok = warp_wait(&m.d5, hc & 1);
@@ -810,8 +740,9 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                     tmem_ld16(lq + cDa + c, da);
                     tmem_ld16(lq + cD5 + c, y);
                     if (!top) tmem_ld16(lq + cD6 + c, d6);
-                    const uint4 w0 = *reinterpret_cast<const uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, c & 63));
-                    const uint4 w1 = *reinterpret_cast<const uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, (c & 63) + 8));
+                    uint4* const q0 = reinterpret_cast<uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, c & 63));
+                    uint4* const q1 = reinterpret_cast<uint4*>(sm + kGrQK + (c >> 6) * 16384 + sw128(row, (c & 63) + 8));
+                    const uint4 w0 = *q0, w1 = *q1;
                     const uint32_t wk[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                     tmem_ld_wait();
                     loaded16(da);
@@ -840,12 +771,33 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         }
                         if (h + 1 < (hk + 1) * rep) st16(my + e0, o);
                     }
-                    if (h + 1 == (hk + 1) * rep && i < n) st16(out + c, o);
+                    if (h + 1 == (hk + 1) * rep) {
+                        if constexpr (sizeof(Tout) == 2) {   // (in place of the q or k just read)
+                            uint4 v[1];
+                            split8<1>(o, v);
+                            *q0 = v[0];
+                            split8<1>(o + 4, v);
+                            *q1 = v[0];
+                        } else if (i < n) {
+                            st16(out + c, o);
+                        }
+                    }
                 }
                 m.dot[cg][row] = dot.x + dot.y;
                 if (!top) m.dot2[cg][i] = dot2.x + dot2.y;
                 tc_fence_before();
                 if (!(ok = group_sync_and(1, ok, 256))) break;
+                if (sizeof(Tout) == 2 && h + 1 == (hk + 1) * rep) {   // whole rows, 16 bytes a lane
+                    Tout* const pq = (Tout*)a.dq + at3(d.dqs, s.batch, hk, t);
+                    Tout* const pk = (Tout*)a.dk + at3(d.dks, s.batch, hk, t);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = e * 16 + (tid >> 4), ch = tid & 15, j = r & 63;
+                        if (j < n && ch * 8 < dk)
+                            *reinterpret_cast<uint4*>((e < 4 ? pq + j * d.dqs[2] : pk + j * d.dks[2]) + ch * 8) =
+                                *reinterpret_cast<const uint4*>(sm + kGrQK + (ch >> 3) * 16384 + sw128(r, (ch & 7) * 8));
+                    }
+                }
                 if (warp == 0) {   // dc_i, then its sums to the chunk's end (two tokens a lane)
                     float c[2], o2[2], tot = 0.f;
 #pragma unroll
@@ -862,7 +814,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         tot += j < n ? o2[e] : 0.f;
                     }
                     tot = warp_sum(tot);
-                    const float g = warp_sum(lane < 4 ? m.sg[hc & 1][lane] : 0.f);
+                    const float g = warp_sum(lane < 8 ? m.sg[hc & 1][lane] : 0.f);
                     const float end = fmaf(vec.up[63], g, tot);   // everything that decays with the whole chunk
                     if (2 * lane == n - 1) c[0] += end;
                     if (2 * lane + 1 == n - 1) c[1] += end;
@@ -878,7 +830,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         const int j = 2 * lane + e;
                         if (j < n) {
                             a.dg[at + j] = e ? sum - c[0] : sum;
-                            a.dbeta[at + j] = m.da[j] * dalpha_dbeta_of(m.be[hc & 1][j], m.lam[j], d.euler);
+                            a.dbeta[at + j] = m.da[j] * dalpha_dbeta_of(m.be[j], m.lam[j], d.euler);
                         }
                     }
                 }
@@ -890,7 +842,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     if (!ok && lane == 0) atomicOr(&g_gb_status, 1u);
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) tmem_dealloc(tb, 512);
+    if (warp == 8) tmem_dealloc(tb, 512);
 }
 
 struct BwdTcWs {
@@ -939,10 +891,9 @@ cudaError_t bwd(const GDims& d, const void* q, const void* k, const void* v, con
     const RscanArgs ra{w.img, w.vec, dS_final, dS0, dv, w.G, w.dX, slots};
     k_gt_rscan<Tout><<<dim3((unsigned)d.BH(), (d.dv + 63) / 64), Rs::warps * 32, Rs::bytes, st>>>(d, ra, mq, mk, mo);
     prof_mark("gated_rscan_tc", st);
-    using B = __nv_bfloat16;
-    const GradArgs ga{(const B*)q, (const B*)k, (const B*)dO, beta, w.vec, w.S, w.U, w.G, w.dX, dq, dk, dg, dbeta, w.acc, slots};
+    const GradArgs ga{beta, w.vec, w.S, w.U, w.G, w.dX, dq, dk, dg, dbeta, w.acc, slots};
     const long long items = (long long)slots * d.Hk;
-    k_gt_grad<Tout><<<(unsigned)(items < kGrCtas ? items : kGrCtas), kGrWarps * 32, kGrSmem, st>>>(d, ga);
+    k_gt_grad<Tout><<<(unsigned)(items < kGrCtas ? items : kGrCtas), kGrWarps * 32, kGrSmem, st>>>(d, ga, mq, mk, mo);
     prof_mark("gated_grad_tc", st);
     return cudaGetLastError();
 }

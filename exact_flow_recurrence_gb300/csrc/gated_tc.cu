@@ -261,7 +261,7 @@ struct ScanSmem {
     static constexpr uint32_t V = TP + TPS * NP * TPB;               // 2 stages
     static constexpr uint32_t S = V + 2 * 8192;                      // blocks of 128 rows
     static constexpr uint32_t X = S + C::blocks * 16384;             // blocks of 64 rows
-    static constexpr uint32_t U = X + C::blocks * 8192;              // REC: blocks of 64 rows
+    static constexpr uint32_t U = X + C::blocks * 8192;              // REC: a tile of 64 rows a part
     static constexpr uint32_t VEC = U + (REC ? C::blocks * 8192 : 0);   // 2 stages
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
     static constexpr int bars = 4 + 2 + TPS + 1 + 9 * NCH;   // (per chain: 7, and its turn)
@@ -497,14 +497,13 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 const unsigned char* vt = sm + M::V + (c & 1) * 8192;
                 const uint4 v0 = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc));
                 const uint4 v1 = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc + 8));
-                float2 v[8] = {mul2(al, bf16x2(v0.x)), mul2(al, bf16x2(v0.y)), mul2(al, bf16x2(v0.z)), mul2(al, bf16x2(v0.w)),
-                               mul2(al, bf16x2(v1.x)), mul2(al, bf16x2(v1.y)), mul2(al, bf16x2(v1.z)), mul2(al, bf16x2(v1.w))};
+                const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
                 if (!(ok = warp_wait(q + 4, ph))) break;
                 float2 y[8];
                 tmem_sum16<NP>(t1, 32, y);
 #pragma unroll
                 for (int m = 0; m < 8; ++m) {
-                    y[m] = fma2(au, y[m], v[m]);
+                    y[m] = fma2(au, y[m], mul2(al, bf16x2(vw[m])));
                     if (!live) y[m] = both(0.f);
                 }
                 C::put16(sm + M::X, 8192, g, i, cc, y);
@@ -518,7 +517,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 warp_arrive(q + 2, lane);
                 if (REC) {
                     if (c > 0 && !(ok = warp_wait(u_free, ph ^ 1u))) break;
-                    C::put16(sm + M::U, 8192, g, i, cc, U);
+                    put16_parts<NP>(sm + M::U, i, g * 32 + cc, U);
                     warp_arrive(q + 3, lane);
                 }
             } else if (!REC) {

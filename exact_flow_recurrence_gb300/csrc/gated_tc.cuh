@@ -89,21 +89,26 @@ struct Chain {
     static __device__ __forceinline__ void put16(unsigned char* base, uint32_t blk, int g, int r, int cc, const float2 (&x)[8]);
 };
 
-// 16 columns of this warp's lanes of an accumulator, summed over G column groups `gap` apart
-// (the last one first: it holds the small parts' products)
+// 16 columns of this warp's lanes of an accumulator, summed over G column groups `gap` apart (the
+// last ones first: they hold the small parts' products; two at a time, for the registers' sake:
+// with all but a few KB of L1 taken by shared memory, a spilled register costs a trip to L2).
 template <int G>
 __device__ __forceinline__ void tmem_sum16(uint32_t t, int gap, float2 (&y)[8]) {
-    float x[G][16];
 #pragma unroll
-    for (int p = 0; p < G; ++p) tmem_ld16(t + p * gap, x[p]);
-    tmem_ld_wait();
+    for (int p = G - 1; p >= 0; p -= 2) {
+        float x[2][16];
+        tmem_ld16(t + p * gap, x[0]);
+        if (p > 0) tmem_ld16(t + (p - 1) * gap, x[1]);
+        tmem_ld_wait();
+        loaded16(x[0]);
+        if (p > 0) loaded16(x[1]);
 #pragma unroll
-    for (int p = 0; p < G; ++p) loaded16(x[p]);
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        y[m] = make_float2(x[G - 1][2 * m], x[G - 1][2 * m + 1]);
-#pragma unroll
-        for (int p = G - 2; p >= 0; --p) y[m] = add2(y[m], make_float2(x[p][2 * m], x[p][2 * m + 1]));
+        for (int m = 0; m < 8; ++m) {
+            float2 z = make_float2(x[0][2 * m], x[0][2 * m + 1]);
+            if (p < G - 1) z = add2(y[m], z);
+            if (p > 0) z = add2(z, make_float2(x[1][2 * m], x[1][2 * m + 1]));
+            y[m] = z;
+        }
     }
 }
 
@@ -117,6 +122,19 @@ __device__ __forceinline__ void Chain<NP, NCH>::put16(unsigned char* base, uint3
 #pragma unroll
         for (int p = 0; p < NP; ++p)
             *reinterpret_cast<uint4*>(base + (p < 2 ? g : NCH) * blk + sw128(r, (p < 2 ? p : g) * 32 + cc + e)) = w[p];
+    }
+}
+
+// 16 values of row r, from column col of a slice's 64, as parts in tiles of 64 rows one after another
+// (the records of U and dX).
+template <int NP>
+__device__ __forceinline__ void put16_parts(unsigned char* base, int r, int col, const float2 (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 8) {
+        uint4 w[NP];
+        split8<NP>(x + e / 2, w);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(base + p * 8192 + sw128(r, col + e)) = w[p];
     }
 }
 
