@@ -33,19 +33,22 @@ constexpr float kFloorAlpha = 1e-25f;
 //   D1 = [K; Q] G  (lanes 0..63: K G);   E = e^c dO as parts (the warps of lanes 64..127)
 //   D2 = (P T)^T dO + T^T Y,  Y = e^{c_last - c} K G as parts;   dX = D2
 //   D3 = Q^T E + K^T Z,  Z = -alpha e^c dX as parts;   G = e^{c_last} G + D3
-// dv = alpha dX goes out here, and dX's parts, from registers; G's parts are copied out as they lie
-// in shared memory (a warp of its own does).
+// dv = alpha dX goes out here.  G's parts, and dX's from a buffer of their own, are copied out as
+// they lie in shared memory (a warp of its own does: stored from registers, a row a lane, they
+// would hold up the load-store unit for everyone).
 struct Rs {
     using C = Chain<NP, 2>;
-    static constexpr uint32_t KQ = 0;                     // 2 stages x 2 blocks x [K rows | Q rows]
-    static constexpr uint32_t TP = 65536;                 // [T; P T], NP parts, one stage
-    static constexpr uint32_t DO = TP + NP * 16384;       // 2 stages
-    static constexpr uint32_t G = DO + 2 * 8192;          // 3 blocks of 128 rows
+    static constexpr uint32_t K = 0;                      // 2 stages x 2 blocks of 64 dk
+    static constexpr uint32_t Q = 32768;                  // 2 blocks
+    static constexpr uint32_t DO = Q + 16384;
+    static constexpr uint32_t TP = DO + 8192;             // [T; P T], NP parts
+    static constexpr uint32_t G = TP + NP * 16384;        // 3 blocks of 128 rows
     static constexpr uint32_t X = G + 3 * 16384;          // 3 blocks of 64 rows: Y, then Z
-    static constexpr uint32_t E = X + 3 * 8192;
-    static constexpr uint32_t VEC = E + 3 * 8192;         // 2 stages of up, rest, al
+    static constexpr uint32_t E = X + 3 * 8192;           // likewise
+    static constexpr uint32_t R = E + 3 * 8192;           // dX, a tile of 64 rows a part
+    static constexpr uint32_t VEC = R + 3 * 8192;         // 2 stages of up, rest, al
     static constexpr uint32_t BAR = VEC + 2 * 768;
-    static constexpr int bars = 7 + 2 * 8;
+    static constexpr int bars = 12 + 2 * 9;
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
     static constexpr int warps = 20;                      // 16 epilogue, 2 products, copies in, copies out
 };
@@ -72,12 +75,15 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = (uint64_t*)(sm + M::BAR);
-    uint64_t* full = bars;            // [2]
+    uint64_t* full = bars;            // [2] K, vectors
     uint64_t* freed = bars + 2;       // [2] by both chains
-    uint64_t* full_tp = bars + 4;
-    uint64_t* freed_tp = bars + 5;    // by both chains
-    uint64_t* g_free = bars + 6;      // G's parts have been copied out
-    uint64_t* chain0 = bars + 7;      // per chain: g_ready, y_ready, z_ready, e_ready, d1, d2, d3, turn
+    uint64_t* full_tp = bars + 4;     // [2] T, P T
+    uint64_t* freed_tp = bars + 6;    // [2] by both chains' products
+    uint64_t* full_qd = bars + 8;     // Q, dO
+    uint64_t* freed_qd = bars + 9;    // by both chains' products
+    uint64_t* g_free = bars + 10;     // G's, dX's parts have been copied out
+    uint64_t* r_free = bars + 11;
+    uint64_t* chain0 = bars + 12;     // per chain: g_ready, y_ready, z_ready, e_ready, d1, d2, d3, turn, r_ready (dX)
     uint32_t* tslot = (uint32_t*)(bars + M::bars);
     const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * 64;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -85,18 +91,16 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
     const int nch = (s.len + kGC - 1) / kGC;
     const size_t rec0 = (size_t)h * a.slots + s.slot0;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&freed[i], 2);
+        for (int i = 0; i < 12; ++i) {
+            const bool two = i == 2 || i == 3 || i == 6 || i == 7 || i == 9;
+            mbar_init(&bars[i], two ? 2 : 1);
         }
-        mbar_init(full_tp, 1);
-        mbar_init(freed_tp, 2);
-        mbar_init(g_free, 1);
         for (int g = 0; g < 2; ++g) {
-            uint64_t* q = chain0 + 8 * g;
+            uint64_t* q = chain0 + 9 * g;
             mbar_init(q, 8);   // warps
             for (int i = 1; i < 4; ++i) mbar_init(q + i, 4);
             for (int i = 4; i < 8; ++i) mbar_init(q + i, 1);
+            mbar_init(q + 8, 4);
         }
         fence_mbar_init();
     }
@@ -114,59 +118,77 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
         if (warp >= 18 && lane == 0 && nch > 0) {
             if (warp == 18) {
                 // ---------------- copies in (it counts the chunks from the sequence's end)
-                int n_kq = 0, n_tp = 0;
+                int n_k = 0, n_tp[2] = {0, 0}, n_qd = 0;
                 const auto load = [&](int it) {
-                    const int c = nch - 1 - it, t = s.start + c * kGC;
-                    unsigned char* kq = sm + M::KQ + (it & 1) * 32768;
+                    const int c = nch - 1 - it;
                     uint64_t* f = &full[it & 1];
-                    mbar_arrive_expect_tx(f, 5u * 8192u + 768u);
-                    for (int blk = 0; blk < 2; ++blk) {
-                        tma_load_4d(kq + blk * 16384, &tm_k, 64 * blk, t, hk, s.batch, f);
-                        tma_load_4d(kq + blk * 16384 + 8192, &tm_q, 64 * blk, t, hk, s.batch, f);
-                    }
-                    tma_load_4d(sm + M::DO + (it & 1) * 8192, &tm_do, c0, t, h, s.batch, f);
+                    mbar_arrive_expect_tx(f, 2u * 8192u + 768u);
+                    for (int blk = 0; blk < 2; ++blk)
+                        tma_load_4d(sm + M::K + (it & 1) * 16384 + blk * 8192, &tm_k, 64 * blk, s.start + c * kGC, hk, s.batch, f);
                     bulk_g2s(sm + M::VEC + (it & 1) * 768, a.vec + rec0 + c, 768, f);
-                    n_kq = it + 1;
+                    n_k = it + 1;
                 };
-                const auto load_tp = [&](int it) {
-                    mbar_arrive_expect_tx(full_tp, NP * 16384u);
-                    bulk_g2s(sm + M::TP, a.img + (rec0 + nch - 1 - it) * NP * 16384, NP * 16384u, full_tp);
-                    n_tp = it + 1;
+                const auto load_qd = [&](int it) {
+                    const int t = s.start + (nch - 1 - it) * kGC;
+                    mbar_arrive_expect_tx(full_qd, 3u * 8192u);
+                    for (int blk = 0; blk < 2; ++blk) tma_load_4d(sm + M::Q + blk * 8192, &tm_q, 64 * blk, t, hk, s.batch, full_qd);
+                    tma_load_4d(sm + M::DO, &tm_do, c0, t, h, s.batch, full_qd);
+                    n_qd = it + 1;
+                };
+                const auto load_tp = [&](int it, int what) {   // T's rows or P T's of every part
+                    const unsigned char* from = a.img + (rec0 + nch - 1 - it) * NP * 16384 + what * 8192;
+                    mbar_arrive_expect_tx(&full_tp[what], NP * 8192u);
+                    for (int p = 0; p < NP; ++p)
+                        bulk_g2s(sm + M::TP + p * 16384 + what * 8192, from + p * 16384, 8192u, &full_tp[what]);
+                    n_tp[what] = it + 1;
                 };
                 load(0);
-                load_tp(0);
+                load_qd(0);
+                load_tp(0, 1);
+                load_tp(0, 0);
                 if (nch > 1) load(1);
-                for (int it = 0; it + 1 < nch && ok; ++it) {
-                    ok = mbar_wait(freed_tp, it & 1, kWaitLimit);
-                    if (ok) load_tp(it + 1);
+                for (int it = 0; it + 1 < nch && ok; ++it) {   // in the order in which the products let go
+                    ok = mbar_wait(&freed_tp[1], it & 1, kWaitLimit);
+                    if (ok) load_tp(it + 1, 1);
+                    ok = ok && mbar_wait(&freed_tp[0], it & 1, kWaitLimit);
+                    if (ok) load_tp(it + 1, 0);
+                    ok = ok && mbar_wait(freed_qd, it & 1, kWaitLimit);
+                    if (ok) load_qd(it + 1);
                     if (ok && it + 2 < nch) {
                         ok = mbar_wait(&freed[it & 1], (it >> 1) & 1, kWaitLimit);
                         if (ok) load(it + 2);
                     }
                 }
                 if (!ok) {   // a wait gave up: the copies under way land before the CTA ends
-                    for (int i = 0; i < 2; ++i)
-                        if (n_kq > i) mbar_wait(&full[(n_kq - 1 - i) & 1], ((n_kq - 1 - i) >> 1) & 1, kWaitLimit);
-                    if (n_tp) mbar_wait(full_tp, (n_tp - 1) & 1, kWaitLimit);
+                    for (int i = 0; i < 2; ++i) {
+                        if (n_k > i) mbar_wait(&full[(n_k - 1 - i) & 1], ((n_k - 1 - i) >> 1) & 1, kWaitLimit);
+                        mbar_wait(&full_tp[i], (n_tp[i] - 1) & 1, kWaitLimit);
+                    }
+                    mbar_wait(full_qd, (n_qd - 1) & 1, kWaitLimit);
                 }
             } else {
                 // ---------------- copies out
                 for (int it = 0; it < nch; ++it) {
                     const uint32_t ph = it & 1;
                     const size_t rec = (rec0 + nch - 1 - it) * gridDim.y + blockIdx.y;
-                    ok = mbar_wait(chain0, ph, kWaitLimit) && mbar_wait(chain0 + 8, ph, kWaitLimit);
+                    ok = mbar_wait(chain0, ph, kWaitLimit) && mbar_wait(chain0 + 9, ph, kWaitLimit);
                     if (!ok) break;
                     bulk_s2g(a.rec_G + rec * kRecS, sm + M::G, kRecS);
                     bulk_commit();
-                    bulk_wait_read();
+                    bulk_wait_read();   // (and the dX of the chunk before)
                     mbar_arrive(g_free);
+                    if (it > 0) mbar_arrive(r_free);
+                    ok = mbar_wait(chain0 + 8, ph, kWaitLimit) && mbar_wait(chain0 + 17, ph, kWaitLimit);
+                    if (!ok) break;
+                    bulk_s2g(a.rec_dX + rec * kRecU, sm + M::R, kRecU);
+                    bulk_commit();
                 }
                 bulk_wait_read();
             }
         } else if (warp < 18) {
                 // ---------------- a chain's products
                 const int g = warp - 16;
-                uint64_t* q = chain0 + 8 * g;
+                uint64_t* q = chain0 + 9 * g;
                 const uint32_t t1 = tb + g * 256, t2 = t1 + 96, t3 = t1;   // D3 over D1, which is read by then
                 const int nblk = (d.dk + 63) / 64;
                 const bool one = elect_one();
@@ -176,27 +198,28 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 // T^T and (P T)^T: the image's rows are K indices and its 64 columns the product's rows 0..63;
                 // rows 64..127 (64 columns further, which do not exist) read what follows and are not used
                 const uint64_t dT = sdesc_sw128(smem_u32(sm + M::TP), 16384);
+                const uint64_t qm = sdesc_sw128(smem_u32(sm + M::Q), 8192);
+                const uint64_t dDO = sdesc_sw128(smem_u32(sm + M::DO)) + g * 4;   // 32 columns in
                 constexpr uint32_t kk = idesc_f16(128, NP * 32, false, true, true), m1 = idesc_f16(128, 32, true, true, true),
                                    m3 = idesc_f16(128, NP * 32, true, true, true);
                 for (int it = 0; it < nch; ++it) {
                     const uint32_t ph = it & 1;
-                    const uint32_t kq = smem_u32(sm + M::KQ + (it & 1) * 32768);
-                    const uint64_t ka = sdesc_sw128(kq), km = sdesc_sw128(kq, 16384);
-                    const uint64_t dDO = sdesc_sw128(smem_u32(sm + M::DO + (it & 1) * 8192)) + g * 4;   // 32 columns in
+                    const uint32_t kt = smem_u32(sm + M::K + (it & 1) * 16384);
+                    const uint64_t ka = sdesc_sw128(kt), km = sdesc_sw128(kt, 8192);   // (64 rows: 64..127 read what follows)
                     if (!(ok = warp_wait(q, ph) && warp_wait(&full[it & 1], (it >> 1) & 1))) break;
                     if (it > 0 && one) mbar_arrive(&freed[(it - 1) & 1]);
                     if (g == 1) ok = warp_wait(chain0 + 7, ph);   // the chains take turns: see Chain
-                    else if (it > 0) ok = warp_wait(chain0 + 15, ph ^ 1u);
+                    else if (it > 0) ok = warp_wait(chain0 + 16, ph ^ 1u);
                     if (!ok) break;
                     if (one) {
 #pragma unroll 1
                         for (int blk = 0; blk < nblk; ++blk)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_f16_ss(t1, ka + blk * 1024 + ks * 2, dG + blk * 512 + ks * 128, kk, blk + ks > 0);
+                                mma_f16_ss(t1, ka + blk * 512 + ks * 2, dG + blk * 512 + ks * 128, kk, blk + ks > 0);
                         mma_commit(q + 4);
                     }
-                    if (!(ok = warp_wait(full_tp, ph))) break;
+                    if (!(ok = warp_wait(full_qd, ph) && warp_wait(&full_tp[1], ph))) break;
                     if (one) {
                         // what does not wait for K G: (P T)^T dO (rows 64..127 of the image, 8 KB in), the small parts
                         // first (the accumulator cuts off, it does not round)
@@ -205,8 +228,9 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f16_ss(t2, dT + p * 1024 + 512 + ks * 128, dDO + ks * 128, m1, p < NP - 1 || ks > 0);
+                        mma_commit(&freed_tp[1]);
                     }
-                    if (!(ok = warp_wait(q + 1, ph))) break;
+                    if (!(ok = warp_wait(&full_tp[0], ph) && warp_wait(q + 1, ph))) break;
                     if (one) {
                         // T^T Y, into column groups of its own
 #pragma unroll
@@ -216,17 +240,18 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                                 mma_f16_ss(t2 + 32, dT + p * 1024 + ks * 128, dX + ks * 128,
                                            idesc_f16(128, (NP - p) * 32, true, true, true), p + ks > 0);
                         mma_commit(q + 5);
+                        mma_commit(&freed_tp[0]);
                         mbar_arrive(q + 7);
                     }
                     if (!(ok = warp_wait(q + 3, ph))) break;   // (long since)
                     if (one) {
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)   // Q^T E (rows 64..127 of [K; Q])
-                            mma_f16_ss(t3, km + 512 + ks * 128, dE + ks * 128, m3, ks > 0);
+                        for (int ks = 0; ks < 4; ++ks)   // Q^T E
+                            mma_f16_ss(t3, qm + ks * 128, dE + ks * 128, m3, ks > 0);
+                        mma_commit(freed_qd);   // (dO too: its products are over, and E came from it)
                         }
                     if (!(ok = warp_wait(q + 2, ph))) break;
                     if (one) {
-                        mbar_arrive(freed_tp);   // (D2 is done: z_ready came from it)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) mma_f16_ss(t3, km + ks * 128, dX + ks * 128, m3, 1u);
                         mma_commit(q + 6);
@@ -238,7 +263,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
         const int g = warp >> 3, row = 32 * (warp & 3) + lane, cc = ((warp >> 2) & 1) * 16;
         const int i = row & 63, col = c0 + g * 32 + cc;
         const bool top = row < 64, in = col < d.dv;
-        uint64_t* q = chain0 + 8 * g;
+        uint64_t* q = chain0 + 9 * g;
         const uint32_t t1 = taddr(tb, 32 * (warp & 3), g * 256 + cc), t2 = t1 + 96, t3 = t1;
         const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + col;
         float2 G[8];
@@ -254,15 +279,15 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
             const uint32_t ph = it & 1;
             const int c = nch - 1 - it, n = min(kGC, s.len - c * kGC);
             const float* vec = (const float*)(sm + M::VEC + (it & 1) * 768);
-            unsigned char* dt = sm + M::DO + (it & 1) * 8192;
+            const unsigned char* dt = sm + M::DO;
             if (it > 0 && !(ok = warp_wait(g_free, ph ^ 1u))) break;
             C::put16(sm + M::G, 16384, g, row, cc, G);
             if (d.packed && n < kGC) {   // rows past the sequence are another's: zero them (0 x NaN is not 0)
-                if (!(ok = warp_wait(&full[it & 1], (it >> 1) & 1))) break;
-                unsigned char* kq = sm + M::KQ + (it & 1) * 32768;
+                if (!(ok = warp_wait(&full[it & 1], (it >> 1) & 1) && warp_wait(full_qd, ph))) break;
                 for (int e = tid & 255; e < (kGC - n) * 40; e += 256) {   // five tiles of 64 rows of eight 16-byte chunks
                     const int tile = e % 5, r = n + e / 40, ch = (e / 5) & 7;
-                    *reinterpret_cast<uint4*>((tile < 4 ? kq + tile * 8192 : dt) + r * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    unsigned char* to = tile < 2 ? sm + M::K + (it & 1) * 16384 + tile * 8192 : sm + M::Q + (tile - 2) * 8192;
+                    *reinterpret_cast<uint4*>(to + r * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);   // (dO follows Q)
                 }
             }
             warp_arrive(q, lane);
@@ -285,8 +310,9 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 for (int m = 0; m < 8; ++m) y[m] = mul2(both(-al * up), X[m]);
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
-                // (tiles of 64 rows, one a part, in the operand layout)
-                put16_parts<NP>(a.rec_dX + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecU, i, g * 32 + cc, X);
+                if (it > 0 && !(ok = warp_wait(r_free, ph ^ 1u))) break;
+                put16_parts<NP>(sm + M::R, i, g * 32 + cc, X);
+                warp_arrive(q + 8, lane);
                 if (live && in) {
                     Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
 #pragma unroll
@@ -294,6 +320,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     st16(vp, y);
                 }
             } else {
+                if (!(ok = warp_wait(full_qd, ph))) break;
                 const uint4 w0 = *reinterpret_cast<const uint4*>(dt + sw128(i, g * 32 + cc));
                 const uint4 w1 = *reinterpret_cast<const uint4*>(dt + sw128(i, g * 32 + cc + 8));
                 const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -465,6 +492,14 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
         // ---------------- copies in
         if (lane == 0) {
             uint32_t kc = 0;   // chunks
+            const auto ahead = [&](int h, int slot, int sl, int t, int batch) {
+                const size_t rec = ((size_t)h * a.slots + slot) * nsl + sl;
+                tma_prefetch_4d(&tm_do, 64 * sl, t, h, batch);
+                bulk_prefetch_l2(a.dX + rec * kRecU, kRecU);
+                bulk_prefetch_l2(a.U + rec * kRecU, kRecU);
+                bulk_prefetch_l2(a.S + rec * kRecS, kRecS);
+                bulk_prefetch_l2(a.G + rec * kRecS, kRecS);
+            };
             for (long long x = blockIdx.x; x < items && ok; x += gridDim.x) {
                 int hk, slot, b, t0;
                 SeqAt s;
@@ -489,6 +524,22 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         bulk_g2s(sm + kGrS, a.S + rec * kRecS, kRecS, &m.f_s);
                         if (!next(&m.e_g, &m.f_g, kRecS)) break;
                         bulk_g2s(sm + kGrG, a.G + rec * kRecS, kRecS, &m.f_g);
+                        // what the buffers take next comes into L2 meanwhile
+                        if (sl + 1 < nsl) {
+                            ahead(h, slot, sl + 1, t, s.batch);
+                        } else if (h + 1 < (hk + 1) * rep) {
+                            ahead(h + 1, slot, 0, t, s.batch);
+                        } else {
+                            int hk2, slot2, b2, t2;
+                            SeqAt s2;
+                            if (x + gridDim.x < items && place(x + gridDim.x, hk2, slot2, b2, s2, t2) > 0) {
+                                ahead(hk2 * rep, slot2, 0, s2.start + t2, s2.batch);
+                                for (int blk = 0; blk < nblk; ++blk) {
+                                    tma_prefetch_4d(&tm_q, 64 * blk, s2.start + t2, hk2, s2.batch);
+                                    tma_prefetch_4d(&tm_k, 64 * blk, s2.start + t2, hk2, s2.batch);
+                                }
+                            }
+                        }
                         if (sl > 0) continue;
                         // (after what can go ahead of the end of the head before)
                         if (hc > 0) ok = mbar_wait(&m.end, (hc - 1) & 1, kWaitLimit);
@@ -633,19 +684,19 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 }
                 warp_arrive(&m.qk, lane);
                 ok = ok && warp_wait(&m.f_vec, hc & 1);
-                // ---- <S, G>, slice by slice
+                // ---- <S, G>, slice by slice (the last one's after the pairs)
                 float sg = 0.f;
-                for (int sl = 0; sl < nsl; ++sl, ++sc) {
+                const auto inner = [&]() {
                     ok = ok && warp_wait(&m.f_s, sc & 1) && warp_wait(&m.f_g, sc & 1);
                     sg += inner256(sm + kGrS, sm + kGrG, tid);
+                    ++sc;
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&m.e_g);
-                        if (sl + 1 < nsl) mbar_arrive(&m.e_s);   // (the last slice's S buffer goes on to [dPD; dAD])
-                    }
+                    if (lane == 0) mbar_arrive(&m.e_g);
+                };
+                for (int sl = 0; sl + 1 < nsl; ++sl) {
+                    inner();
+                    if (lane == 0) mbar_arrive(&m.e_s);   // (the last slice's S buffer goes on to [dPD; dAD])
                 }
-                sg = warp_sum(sg);
-                if (lane == 0) m.sg[hc & 1][warp] = sg;
                 // ---- the chunk's pairs (i, j): columns j = 32 cg .. 32 cg + 31 of this lane's row
                 ok = ok && warp_wait(&m.d3, hc & 1);
                 const float al = vec.al[i], sw = top ? 1.f : -al;
@@ -703,6 +754,9 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                     if (lane < 32) m.cs[qd][32 * cg + lane] = 0.f;
                 }
                 m.rs[cg][row] = rsum;
+                inner();
+                sg = warp_sum(sg);
+                if (lane == 0) m.sg[hc & 1][warp] = sg;
                 // (S's buffer: the last slice's products have read it, and so has <S, G>)
                 ok = ok && warp_wait(&m.e_u, (nsl * (hc + 1) - 1) & 1);   // D6 follows Da
                 if (!(ok = group_sync_and(1, ok, 256))) break;                  // (the warps leave together if a wait gave up)
@@ -798,6 +852,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                                 *reinterpret_cast<const uint4*>(sm + kGrQK + (ch >> 3) * 16384 + sw128(r, (ch & 7) * 8));
                     }
                 }
+                const float up63 = vec.up[63];
+                warp_arrive(&m.end, lane);   // (what warp 0 still reads, the next head writes only after it has come along)
                 if (warp == 0) {   // dc_i, then its sums to the chunk's end (two tokens a lane)
                     float c[2], o2[2], tot = 0.f;
 #pragma unroll
@@ -815,7 +871,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                     }
                     tot = warp_sum(tot);
                     const float g = warp_sum(lane < 8 ? m.sg[hc & 1][lane] : 0.f);
-                    const float end = fmaf(vec.up[63], g, tot);   // everything that decays with the whole chunk
+                    const float end = fmaf(up63, g, tot);   // everything that decays with the whole chunk
                     if (2 * lane == n - 1) c[0] += end;
                     if (2 * lane + 1 == n - 1) c[1] += end;
                     float sum = c[0] + c[1];
@@ -834,7 +890,6 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         }
                     }
                 }
-                warp_arrive(&m.end, lane);
             }
         }
         tc_fence_before();

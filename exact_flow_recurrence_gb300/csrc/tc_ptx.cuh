@@ -105,6 +105,13 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
         : "memory");
 }
 
+// Hint to bring the box of a tiled copy into L2.
+__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(tmap), "r"(x), "r"(y),
+                 "r"(z), "r"(w)
+                 : "memory");
+}
+
 // 2-D forms of the tiled tensor copies: load one box at {x, y} completing on `bar`, and
 // store one box from shared memory (bulk-group completion).  Same alignment rule on x.
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, int y, uint64_t* bar) {
