@@ -112,6 +112,9 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = *tslot;
+    // This kernel reads nothing that the recording pass writes (and the preparation was complete
+    // before that pass let it begin), so the two run side by side on the SMs that there are.
+    griddep_launch_dependents();
 
     if (warp >= 16) {
         bool ok = true;
@@ -343,6 +346,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
     __syncthreads();
     tc_fence_after();
     if (warp == 16) tmem_dealloc(tb, 512);
+    griddep_wait();   // the recording pass ends before this kernel does: what waits for this one waits for both
 }
 
 // ------------------------------------------------------------------ gradients of a chunk
@@ -476,6 +480,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = m.tslot;
+    griddep_wait();   // the records are complete
     bool ok = true;
 
     // every role walks the same chunks, value heads and slices; `sc` counts slices, `hc` heads
@@ -944,13 +949,16 @@ cudaError_t bwd(const GDims& d, const void* q, const void* k, const void* v, con
     if (e == cudaSuccess) e = launch_gated_record_tc(d, q, k, v, S0, w.img, w.vec, w.S, w.U, st);
     if (e != cudaSuccess) return e;
     const RscanArgs ra{w.img, w.vec, dS_final, dS0, dv, w.G, w.dX, slots};
-    k_gt_rscan<Tout><<<dim3((unsigned)d.BH(), (d.dv + 63) / 64), Rs::warps * 32, Rs::bytes, st>>>(d, ra, mq, mk, mo);
+    e = launch_early(k_gt_rscan<Tout>, dim3((unsigned)d.BH(), (d.dv + 63) / 64), Rs::warps * 32, Rs::bytes, st, d, ra,
+                     mq, mk, mo);
     prof_mark("gated_rscan_tc", st);
+    if (e != cudaSuccess) return e;
     const GradArgs ga{beta, w.vec, w.S, w.U, w.G, w.dX, dq, dk, dg, dbeta, w.acc, slots};
     const long long items = (long long)slots * d.Hk;
-    k_gt_grad<Tout><<<(unsigned)(items < kGrCtas ? items : kGrCtas), kGrWarps * 32, kGrSmem, st>>>(d, ga, mq, mk, mo);
+    e = launch_early(k_gt_grad<Tout>, dim3((unsigned)(items < kGrCtas ? items : kGrCtas)), kGrWarps * 32, kGrSmem, st, d,
+                     ga, mq, mk, mo);
     prof_mark("gated_grad_tc", st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
     const float beta = tid < n ? a.beta[at3(d.bs, s.batch, h, t + tid)] : 0.f;
     tc_fence_before();
     __syncthreads();
+    griddep_launch_dependents();   // (the scan's CTAs come as SMs run empty)
     tc_fence_after();
     const uint32_t tb = *tslot;
     if (warp == 0) {
@@ -331,6 +332,8 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = *tslot;
+    griddep_wait();                             // the preparation is complete
+    if (REC) griddep_launch_dependents();       // the reverse scan needs it too, but nothing of this kernel's
 
     if (warp >= 8 * NCH) {
         bool ok = true;
@@ -584,9 +587,10 @@ cudaError_t scan(const GDims& d, const ScanArgs& a, const Maps& m, cudaStream_t 
     const auto k = k_gt_scan<NP, NCH, Tout, REC>;
     cudaError_t e = smem_attr(k, M::bytes);
     if (e != cudaSuccess) return e;
-    k<<<dim3((unsigned)d.BH(), (d.dv + 32 * NCH - 1) / (32 * NCH)), M::warps * 32, M::bytes, st>>>(d, a, m.q, m.k, m.v);
+    e = launch_early(k, dim3((unsigned)d.BH(), (d.dv + 32 * NCH - 1) / (32 * NCH)), M::warps * 32, M::bytes, st, d, a,
+                     m.q, m.k, m.v);
     prof_mark(REC ? "gated_record_tc" : "gated_scan_tc", st);
-    return cudaGetLastError();
+    return e;
 }
 
 template <int NP>

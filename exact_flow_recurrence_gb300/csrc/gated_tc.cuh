@@ -11,6 +11,8 @@
 // check and no second path.
 #pragma once
 
+#include <utility>
+
 #include "gated_seq.cuh"
 #include "packed2.cuh"
 #include "tc_common.cuh"
@@ -205,6 +207,25 @@ inline cudaError_t strided_rows_map(CUtensorMap* m, const void* base, int d, int
 template <typename K>
 inline cudaError_t smem_attr(K k, size_t bytes) {
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// Launch that may begin before the kernel ahead of it in the stream ends: from when all of that
+// one's CTAs have called griddep_launch_dependents (they hold their tensor memory by then, so that
+// none of them waits for columns that an early CTA has taken).  The kernel itself says what it
+// waits for.
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*k)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A&&... args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, std::forward<A>(args)...);
 }
 
 // Whether slices of 32 state columns (instead of 64) still find an SM each: a chunk's products and
