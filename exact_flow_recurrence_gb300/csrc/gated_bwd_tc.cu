@@ -198,9 +198,9 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 const uint64_t dG = sdesc_sw128(smem_u32(sm + M::G + g * 16384), C::lbo(g, 16384));
                 const uint64_t dX = sdesc_sw128(smem_u32(sm + M::X + g * 8192), C::lbo(g, 8192));
                 const uint64_t dE = sdesc_sw128(smem_u32(sm + M::E + g * 8192), C::lbo(g, 8192));
-                // T^T and (P T)^T: the image's rows are K indices and its 64 columns the product's rows 0..63;
-                // rows 64..127 (64 columns further, which do not exist) read what follows and are not used
-                const uint64_t dT = sdesc_sw128(smem_u32(sm + M::TP), 16384);
+                // T^T and (P T)^T: the image's rows are K indices and its 64 columns the product's rows 0..63; rows
+                // 64..127 are the same columns again (a stride of 0), for the warps there to write dX from
+                const uint64_t dT = sdesc_sw128(smem_u32(sm + M::TP), 0);
                 const uint64_t qm = sdesc_sw128(smem_u32(sm + M::Q), 8192);
                 const uint64_t dDO = sdesc_sw128(smem_u32(sm + M::DO)) + g * 4;   // 32 columns in
                 constexpr uint32_t kk = idesc_f16(128, NP * 32, false, true, true), m1 = idesc_f16(128, 32, true, true, true),
@@ -307,21 +307,11 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 1, lane);
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                float2 X[8];
-                tmem_sum16<NP + 1>(t2, 32, X);
+                tmem_sum16<NP + 1>(t2, 32, y);
 #pragma unroll
-                for (int m = 0; m < 8; ++m) y[m] = mul2(both(-al * up), X[m]);
+                for (int m = 0; m < 8; ++m) y[m] = mul2(both(-al * up), y[m]);
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
-                if (it > 0 && !(ok = warp_wait(r_free, ph ^ 1u))) break;
-                put16_parts<NP>(sm + M::R, i, g * 32 + cc, X);
-                warp_arrive(q + 8, lane);
-                if (live && in) {
-                    Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) y[m] = mul2(both(al), X[m]);
-                    st16(vp, y);
-                }
             } else {
                 if (!(ok = warp_wait(full_qd, ph))) break;
                 const uint4 w0 = *reinterpret_cast<const uint4*>(dt + sw128(i, g * 32 + cc));
@@ -331,6 +321,19 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 for (int m = 0; m < 8; ++m) y[m] = live ? mul2(both(up), bf16x2(w[m])) : both(0.f);
                 C::put16(sm + M::E, 8192, g, i, cc, y);
                 warp_arrive(q + 3, lane);
+                // dX once more: its record, and dv = alpha dX
+                const float al = vec[128 + i];
+                if (!(ok = warp_wait(q + 5, ph))) break;
+                tmem_sum16<NP + 1>(t2, 32, y);
+                if (it > 0 && !(ok = warp_wait(r_free, ph ^ 1u))) break;
+                put16_parts<NP>(sm + M::R, i, g * 32 + cc, y);
+                warp_arrive(q + 8, lane);
+                if (live && in) {
+                    Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) y[m] = mul2(both(al), y[m]);
+                    st16(vp, y);
+                }
             }
             if (!(ok = warp_wait(q + 6, ph))) break;
             tmem_sum16<NP>(t3, 32, y);

@@ -247,16 +247,18 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
 // Each chain has a warp that issues its products; one more copies the chunks in, one ahead.
 //
 // REC is the backward's recording pass: no queries and no o; the parts of every chunk's entering
-// S, and of its U, go out as they lie in shared memory (a warp of its own copies them).
+// S, and of its U, go out as they lie in shared memory (a warp of its own copies them).  T fills
+// both halves of the second product, so that the warps of lanes 64..127, which have no queries
+// here, can write U's record while the others go on with the chain.
 //
 // Bound by the latency of the chain of three products and three epilogues a chunk: see the
 // measurements at launch.
 template <int NP, int NCH, bool REC>
 struct ScanSmem {
     using C = Chain<NP, NCH>;
-    static constexpr int TPS = NP == 2 || REC ? 2 : 1;               // stages of the image
+    static constexpr int TPS = NP == 2 ? 2 : 1;                      // stages of the image
     static constexpr uint32_t KQB = REC ? 8192 : 16384;              // a 64-dk block: K rows (and Q rows)
-    static constexpr uint32_t TPB = REC ? 8192 : 16384;              // an image part: T rows (and P T rows)
+    static constexpr uint32_t TPB = 16384;                           // an image part: T rows, P T rows (REC: T's again)
     static constexpr uint32_t KQ = 0;                                // 2 stages x 2 blocks
     static constexpr uint32_t TP = 4 * KQB;
     static constexpr uint32_t V = TP + TPS * NP * TPB;               // 2 stages
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     const unsigned char* from = a.img + (rec0 + c) * NP * 16384;
                     mbar_arrive_expect_tx(f, NP * M::TPB);
                     if (REC) {
-                        for (int p = 0; p < NP; ++p) bulk_g2s(to + p * M::TPB, from + p * 16384, M::TPB, f);
+                        for (int p = 0; p < 2 * NP; ++p) bulk_g2s(to + p * 8192, from + p / 2 * 16384, 8192, f);
                     } else {
                         bulk_g2s(to, from, NP * M::TPB, f);
                     }
@@ -512,18 +514,19 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 1, lane);
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                float2 U[8];
-                tmem_sum16<NP>(t2, 32, U);
+                tmem_sum16<NP>(t2, 32, y);
 #pragma unroll
-                for (int m = 0; m < 8; ++m) y[m] = mul2(rest, U[m]);
+                for (int m = 0; m < 8; ++m) y[m] = mul2(rest, y[m]);
                 C::put16(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
-                if (REC) {
-                    if (c > 0 && !(ok = warp_wait(u_free, ph ^ 1u))) break;
-                    put16_parts<NP>(sm + M::U, i, g * 32 + cc, U);
-                    warp_arrive(q + 3, lane);
-                }
-            } else if (!REC) {
+            } else if (REC) {   // U once more: its record
+                if (!(ok = warp_wait(q + 5, ph))) break;
+                float2 U[8];
+                tmem_sum16<NP>(t2, 32, U);
+                if (c > 0 && !(ok = warp_wait(u_free, ph ^ 1u))) break;
+                put16_parts<NP>(sm + M::U, i, g * 32 + cc, U);
+                warp_arrive(q + 3, lane);
+            } else {
                 if (!(ok = warp_wait(q + 4, ph))) break;
                 float2 y[8], z[8];
                 tmem_sum16<NP>(t1, 32, y);
