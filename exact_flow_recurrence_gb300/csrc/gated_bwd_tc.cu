@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
             const float* vec = (const float*)(sm + M::VEC + (it & 1) * 768);
             const unsigned char* dt = sm + M::DO;
             if (it > 0 && !(ok = warp_wait(g_free, ph ^ 1u))) break;
-            C::put16(sm + M::G, 16384, g, row, cc, G);
+            C::put(sm + M::G, 16384, g, row, cc, G);
             if (d.packed && n < kGC) {   // rows past the sequence are another's: zero them (0 x NaN is not 0)
                 if (!(ok = warp_wait(&full[it & 1], (it >> 1) & 1) && warp_wait(full_qd, ph))) break;
                 for (int e = tid & 255; e < (kGC - n) * 40; e += 256) {   // five tiles of 64 rows of eight 16-byte chunks
@@ -301,16 +301,16 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
             if (top) {
                 const float rest = vec[64 + i], al = vec[128 + i];
                 if (!(ok = warp_wait(q + 4, ph))) break;
-                tmem_sum16<NP>(t1, 32, y);
+                tmem_sum<NP>(t1, 32, y);
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = live ? mul2(both(rest), y[m]) : both(0.f);
-                C::put16(sm + M::X, 8192, g, i, cc, y);
+                C::put(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 1, lane);
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                tmem_sum16<NP + 1>(t2, 32, y);
+                tmem_sum<NP + 1>(t2, 32, y);
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = mul2(both(-al * up), y[m]);
-                C::put16(sm + M::X, 8192, g, i, cc, y);
+                C::put(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
             } else {
                 if (!(ok = warp_wait(full_qd, ph))) break;
@@ -319,31 +319,31 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
                 for (int m = 0; m < 8; ++m) y[m] = live ? mul2(both(up), bf16x2(w[m])) : both(0.f);
-                C::put16(sm + M::E, 8192, g, i, cc, y);
+                C::put(sm + M::E, 8192, g, i, cc, y);
                 warp_arrive(q + 3, lane);
                 // dX once more: its record, and dv = alpha dX
                 const float al = vec[128 + i];
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                tmem_sum16<NP + 1>(t2, 32, y);
+                tmem_sum<NP + 1>(t2, 32, y);
                 if (it > 0 && !(ok = warp_wait(r_free, ph ^ 1u))) break;
-                put16_parts<NP>(sm + M::R, i, g * 32 + cc, y);
+                put_parts<NP>(sm + M::R, i, g * 32 + cc, y);
                 warp_arrive(q + 8, lane);
                 if (live && in) {
                     Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
 #pragma unroll
                     for (int m = 0; m < 8; ++m) y[m] = mul2(both(al), y[m]);
-                    st16(vp, y);
+                    st_row(vp, y);
                 }
             }
             if (!(ok = warp_wait(q + 6, ph))) break;
-            tmem_sum16<NP>(t3, 32, y);
+            tmem_sum<NP>(t3, 32, y);
 #pragma unroll
             for (int m = 0; m < 8; ++m) G[m] = fma2(both(last), G[m], y[m]);
         }
         if (!ok && lane == 0) atomicOr(&g_gb_status, 1u);
         if (a.dS0 && row < d.dk && in &&
             dbg_in(a.dS0 + sb, 64, a.dS0, (size_t)d.B * d.H * d.dk * d.dv * 4, &g_gb_status))
-            st16(a.dS0 + sb, G);
+            st_row(a.dS0 + sb, G);
         tc_fence_before();
     }
     __syncthreads();
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                                 o[e + 1] = add2(o[e + 1], make_float2(v.z, v.w));
                             }
                         }
-                        if (h + 1 < (hk + 1) * rep) st16(my + e0, o);
+                        if (h + 1 < (hk + 1) * rep) st_row(my + e0, o);
                     }
                     if (h + 1 == (hk + 1) * rep) {
                         if constexpr (sizeof(Tout) == 2) {   // (in place of the q or k just read)
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             split8<1>(o + 4, v);
                             *q1 = v[0];
                         } else if (i < n) {
-                            st16(out + c, o);
+                            st_row(out + c, o);
                         }
                     }
                 }

@@ -269,7 +269,13 @@ struct ScanSmem {
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
     static constexpr int bars = 4 + 2 + TPS + 1 + 9 * NCH;   // (per chain: 7, and its turn)
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
-    static constexpr int warps = 9 * NCH + 1 + (REC ? 1 : 0);
+    // a chain's epilogue warps: a thread has one row and CW of the 32 columns (8 leave a single chain's
+    // epilogues half as long; two chains keep the issue slots busier and would need 34 warps)
+    static constexpr int CW = NCH == 1 ? 8 : 16;
+    static constexpr int EW = 4 * 32 / CW;
+    static constexpr int MW = NCH * EW;                      // first product warp
+    static constexpr int IW = MW + NCH;                      // copies in, and (REC) out
+    static constexpr int warps = IW + 1 + (REC ? 1 : 0);
 };
 static_assert(ScanSmem<2, 2, false>::bytes <= 232448 && ScanSmem<3, 2, false>::bytes <= 232448 &&
               ScanSmem<3, 2, true>::bytes <= 232448, "shared memory per CTA");
@@ -318,15 +324,15 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
         mbar_init(u_free, 1);
         for (int g = 0; g < NCH; ++g) {
             uint64_t* q = chain0 + 9 * g;
-            mbar_init(q + 0, 8);               // s_ready (warps)
-            mbar_init(q + 1, 4);               // x_ready
-            mbar_init(q + 2, REC ? 4 : 8);     // u_ready
-            mbar_init(q + 3, 4);               // r_ready
+            mbar_init(q + 0, M::EW);                        // s_ready (warps)
+            mbar_init(q + 1, M::EW / 2);                    // x_ready
+            mbar_init(q + 2, REC ? M::EW / 2 : M::EW);      // u_ready
+            mbar_init(q + 3, M::EW / 2);                    // r_ready
             for (int i = 4; i < 8; ++i) mbar_init(q + i, 1);
         }
         fence_mbar_init();
     }
-    if (warp == 8 * NCH) {
+    if (warp == M::MW) {
         tmem_alloc(tslot, NCH * 256);
         tmem_relinquish();
     }
@@ -337,10 +343,10 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
     griddep_wait();                             // the preparation is complete
     if (REC) griddep_launch_dependents();       // the reverse scan needs it too, but nothing of this kernel's
 
-    if (warp >= 8 * NCH) {
+    if (warp >= M::MW) {
         bool ok = true;
-        if (warp >= 9 * NCH && lane == 0 && nch > 0) {
-            if (warp == 9 * NCH) {
+        if (warp >= M::IW && lane == 0 && nch > 0) {
+            if (warp == M::IW) {
                 // ---------------- copies in
                 int n_kq = 0, n_tp = 0;   // chunks whose copies are under way
                 const auto load = [&](int c) {
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                         if (n_tp > i && i < M::TPS)
                             mbar_wait(&full_tp[(n_tp - 1 - i) % M::TPS], ((n_tp - 1 - i) / M::TPS) & 1, kWaitLimit);
                     }
-            } else if (REC && warp == 9 * NCH + 1) {
+            } else if (REC && warp == M::IW + 1) {
                 // ---------------- copies out
                 for (int c = 0; c < nch; ++c) {
                     const uint32_t ph = c & 1;
@@ -410,9 +416,9 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 }
                 bulk_wait_read();
             }
-        } else if (warp < 9 * NCH) {
+        } else if (warp < M::IW) {
                 // ---------------- a chain's products
-                const int g = warp - 8 * NCH;
+                const int g = warp - M::MW;
                 uint64_t* q = chain0 + 9 * g;
                 const uint32_t t1 = tb + g * 256, t2 = t1 + 128, t3 = t1;   // D3 over D1, which is read by then
                 const int nblk = (d.dk + 63) / 64;
@@ -448,12 +454,12 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_f16_ss(t2, ta + p * (M::TPB >> 4) + ks * 2, dX + ks * 128,
                                            idesc_f16(128, (NP - p) * 32, false, true, true), p + ks > 0);
-                            mma_commit(q + 5);
-                            if (NCH == 2) mbar_arrive(q + 7);
+                        mma_commit(q + 5);
+                        if (M::TPS == 1) mma_commit(freed_tp);   // (the next image is a long load: as early as can be)
+                        if (NCH == 2) mbar_arrive(q + 7);
                     }
                     if (!(ok = warp_wait(q + 2, ph))) break;
                     if (one) {
-                        if (M::TPS == 1) mbar_arrive(freed_tp);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             mma_f16_ss(t3, km + ks * 128, dX + ks * 128, idesc_f16(128, NP * 32, true, true, true), ks > 0);
@@ -464,15 +470,16 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
         if (!ok && lane == 0) atomicOr(&g_gt2_status, 1u);
     } else {
         // ---------------- the state and the epilogues
-        const int g = warp >> 3, row = 32 * (warp & 3) + lane, cc = ((warp >> 2) & 1) * 16;   // 16 columns from cc of the chain
-        const int i = row & 63, col = c0 + g * 32 + cc;                                      // token of the lane; first column
+        constexpr int CW = M::CW;
+        const int g = warp / M::EW, row = 32 * (warp & 3) + lane, cc = (warp % M::EW >> 2) * CW;   // CW columns from cc of the chain
+        const int i = row & 63, col = c0 + g * 32 + cc;                                            // token of the lane; first column
         const bool top = row < 64, in = col < d.dv;
         uint64_t* q = chain0 + 9 * g;
         const uint32_t lq = taddr(tb, 32 * (warp & 3), g * 256 + cc), t1 = lq, t2 = lq + 128, t3 = lq;
         const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + col;
-        float2 S[8];
+        float2 S[CW / 2];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
+        for (int e = 0; e < CW / 2; e += 2) {
             const float4 x = a.S0 && row < d.dk && in ? *reinterpret_cast<const float4*>(a.S0 + sb + 2 * e)
                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             S[e] = make_float2(x.x, x.y);
@@ -484,11 +491,11 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
             const int n = min(kGC, s.len - c * kGC);
             const GVec* vec = (const GVec*)(sm + M::VEC + (c & 1) * sizeof(GVec));
             if (REC && c > 0 && !(ok = warp_wait(s_free, ph ^ 1u))) break;
-            C::put16(sm + M::S, 16384, g, row, cc, S);
+            C::put(sm + M::S, 16384, g, row, cc, S);
             if (d.packed && n < kGC) {   // rows past the sequence are another's: zero its keys (0 x NaN is not 0)
                 if (!(ok = warp_wait(&full[c & 1], (c >> 1) & 1))) break;
                 unsigned char* kq = sm + M::KQ + (c & 1) * 2 * M::KQB;
-                for (int e = tid & 255; e < (kGC - n) * 16; e += 256)   // (every chain: the same zeros)
+                for (int e = tid % (32 * M::EW); e < (kGC - n) * 16; e += 32 * M::EW)   // (every chain: the same zeros)
                     *reinterpret_cast<uint4*>(kq + (e & 1) * M::KQB + (n + (e >> 4)) * 128 + ((e >> 1) & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
             }
@@ -500,61 +507,61 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 const bool live = i < n;
                 const float2 al = both(vec->al[i]), au = both(-vec->al[i] * up), rest = both(vec->rest[i]);
                 const unsigned char* vt = sm + M::V + (c & 1) * 8192;
-                const uint4 v0 = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc));
-                const uint4 v1 = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc + 8));
-                const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                if (!(ok = warp_wait(q + 4, ph))) break;
-                float2 y[8];
-                tmem_sum16<NP>(t1, 32, y);
+                uint4 vw[CW / 8];
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    y[m] = fma2(au, y[m], mul2(al, bf16x2(vw[m])));
+                for (int e = 0; e < CW / 8; ++e) vw[e] = *reinterpret_cast<const uint4*>(vt + sw128(i, g * 32 + cc + 8 * e));
+                if (!(ok = warp_wait(q + 4, ph))) break;
+                float2 y[CW / 2];
+                tmem_sum<NP>(t1, 32, y);
+#pragma unroll
+                for (int m = 0; m < CW / 2; ++m) {
+                    y[m] = fma2(au, y[m], mul2(al, bf16x2(reinterpret_cast<const uint32_t*>(vw)[m])));
                     if (!live) y[m] = both(0.f);
                 }
-                C::put16(sm + M::X, 8192, g, i, cc, y);
+                C::put(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 1, lane);
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                tmem_sum16<NP>(t2, 32, y);
+                tmem_sum<NP>(t2, 32, y);
 #pragma unroll
-                for (int m = 0; m < 8; ++m) y[m] = mul2(rest, y[m]);
-                C::put16(sm + M::X, 8192, g, i, cc, y);
+                for (int m = 0; m < CW / 2; ++m) y[m] = mul2(rest, y[m]);
+                C::put(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
             } else if (REC) {   // U once more: its record
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                float2 U[8];
-                tmem_sum16<NP>(t2, 32, U);
+                float2 U[CW / 2];
+                tmem_sum<NP>(t2, 32, U);
                 if (c > 0 && !(ok = warp_wait(u_free, ph ^ 1u))) break;
-                put16_parts<NP>(sm + M::U, i, g * 32 + cc, U);
+                put_parts<NP>(sm + M::U, i, g * 32 + cc, U);
                 warp_arrive(q + 3, lane);
             } else {
                 if (!(ok = warp_wait(q + 4, ph))) break;
-                float2 y[8], z[8];
-                tmem_sum16<NP>(t1, 32, y);
+                float2 y[CW / 2], z[CW / 2];
+                tmem_sum<NP>(t1, 32, y);
                 warp_arrive(q + 2, lane);
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                tmem_sum16<NP>(t2, 32, z);
+                tmem_sum<NP>(t2, 32, z);
 #pragma unroll
-                for (int m = 0; m < 8; ++m) z[m] = fma2(both(up), y[m], z[m]);
+                for (int m = 0; m < CW / 2; ++m) z[m] = fma2(both(up), y[m], z[m]);
                 if (i < n && in) {
                     Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + col;
-                    if (dbg_in(op, 16 * sizeof(Tout), a.o, o_extent(d) * sizeof(Tout), &g_gt2_status)) st16(op, z);
+                    if (dbg_in(op, CW * sizeof(Tout), a.o, o_extent(d) * sizeof(Tout), &g_gt2_status)) st_row(op, z);
                 }
             }
             if (!(ok = warp_wait(q + 6, ph))) break;
-            float2 y[8];
-            tmem_sum16<NP>(t3, 32, y);
+            float2 y[CW / 2];
+            tmem_sum<NP>(t3, 32, y);
 #pragma unroll
-            for (int m = 0; m < 8; ++m) S[m] = fma2(both(last), S[m], y[m]);
+            for (int m = 0; m < CW / 2; ++m) S[m] = fma2(both(last), S[m], y[m]);
         }
         if (!ok && lane == 0) atomicOr(&g_gt2_status, 1u);
         if (a.S_final && row < d.dk && in &&
-            dbg_in(a.S_final + sb, 64, a.S_final, (size_t)d.B * d.H * d.dk * d.dv * 4, &g_gt2_status))
-            st16(a.S_final + sb, S);
+            dbg_in(a.S_final + sb, CW * 4, a.S_final, (size_t)d.B * d.H * d.dk * d.dv * 4, &g_gt2_status))
+            st_row(a.S_final + sb, S);
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 8 * NCH) tmem_dealloc(tb, NCH * 256);
+    if (warp == M::MW) tmem_dealloc(tb, NCH * 256);
 }
 
 struct TcWs {

@@ -38,9 +38,17 @@ struct GVec {
 
 // To follow a wait for tensor-memory loads: the loaded values may be used from here on.  (The
 // wait names no registers, so arithmetic on them could otherwise be scheduled before it.)
+__device__ __forceinline__ void loaded8(float* v) {
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+}
 __device__ __forceinline__ void loaded16(float* v) {
-    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+    loaded8(v);
+    loaded8(v + 8);
+}
+template <int N>
+__device__ __forceinline__ void loaded(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) loaded8(v + i);
 }
 
 // 8 values -> NP 16-byte chunks of bf16 parts
@@ -87,25 +95,29 @@ struct Chain {
         return p < 2 ? g * blk + p * 64 : NCH * blk + g * 64;
     }
     __host__ __device__ static constexpr uint32_t lbo(int g, uint32_t blk) { return (NCH - g) * blk + g * 64; }
-    // 16 values of row r, columns cc .. cc + 15 of chain g
-    static __device__ __forceinline__ void put16(unsigned char* base, uint32_t blk, int g, int r, int cc, const float2 (&x)[8]);
+    // 2 W2 values of row r, columns from cc of chain g
+    template <int W2>
+    static __device__ __forceinline__ void put(unsigned char* base, uint32_t blk, int g, int r, int cc, const float2 (&x)[W2]);
 };
 
-// 16 columns of this warp's lanes of an accumulator, summed over G column groups `gap` apart (the
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) { tmem_ld16(t, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[8]) { tmem_ld8(t, v); }
+
+// 2 W2 columns of this warp's lanes of an accumulator, summed over G column groups `gap` apart (the
 // last ones first: they hold the small parts' products; two at a time, for the registers' sake:
 // with all but a few KB of L1 taken by shared memory, a spilled register costs a trip to L2).
-template <int G>
-__device__ __forceinline__ void tmem_sum16(uint32_t t, int gap, float2 (&y)[8]) {
+template <int G, int W2>
+__device__ __forceinline__ void tmem_sum(uint32_t t, int gap, float2 (&y)[W2]) {
 #pragma unroll
     for (int p = G - 1; p >= 0; p -= 2) {
-        float x[2][16];
-        tmem_ld16(t + p * gap, x[0]);
-        if (p > 0) tmem_ld16(t + (p - 1) * gap, x[1]);
+        float x[2][2 * W2];
+        tmem_ld(t + p * gap, x[0]);
+        if (p > 0) tmem_ld(t + (p - 1) * gap, x[1]);
         tmem_ld_wait();
-        loaded16(x[0]);
-        if (p > 0) loaded16(x[1]);
+        loaded(x[0]);
+        if (p > 0) loaded(x[1]);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
+        for (int m = 0; m < W2; ++m) {
             float2 z = make_float2(x[0][2 * m], x[0][2 * m + 1]);
             if (p < G - 1) z = add2(y[m], z);
             if (p > 0) z = add2(z, make_float2(x[1][2 * m], x[1][2 * m + 1]));
@@ -115,10 +127,11 @@ __device__ __forceinline__ void tmem_sum16(uint32_t t, int gap, float2 (&y)[8]) 
 }
 
 template <int NP, int NCH>
-__device__ __forceinline__ void Chain<NP, NCH>::put16(unsigned char* base, uint32_t blk, int g, int r, int cc,
-                                                      const float2 (&x)[8]) {
+template <int W2>
+__device__ __forceinline__ void Chain<NP, NCH>::put(unsigned char* base, uint32_t blk, int g, int r, int cc,
+                                                    const float2 (&x)[W2]) {
 #pragma unroll
-    for (int e = 0; e < 16; e += 8) {
+    for (int e = 0; e < 2 * W2; e += 8) {
         uint4 w[NP];
         split8<NP>(x + e / 2, w);
 #pragma unroll
@@ -127,12 +140,12 @@ __device__ __forceinline__ void Chain<NP, NCH>::put16(unsigned char* base, uint3
     }
 }
 
-// 16 values of row r, from column col of a slice's 64, as parts in tiles of 64 rows one after another
+// 2 W2 values of row r, from column col of a slice's 64, as parts in tiles of 64 rows one after another
 // (the records of U and dX).
-template <int NP>
-__device__ __forceinline__ void put16_parts(unsigned char* base, int r, int col, const float2 (&x)[8]) {
+template <int NP, int W2>
+__device__ __forceinline__ void put_parts(unsigned char* base, int r, int col, const float2 (&x)[W2]) {
 #pragma unroll
-    for (int e = 0; e < 16; e += 8) {
+    for (int e = 0; e < 2 * W2; e += 8) {
         uint4 w[NP];
         split8<NP>(x + e / 2, w);
 #pragma unroll
@@ -154,29 +167,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t ph) {
     return ok;
 }
 
-template <typename Tout>
-__device__ __forceinline__ void st16(Tout* p, const float2* x);   // 16 values to 16-byte aligned memory
-template <>
-__device__ __forceinline__ void st16<float>(float* p, const float2* x) {
+// 2 W2 values to 16-byte aligned memory
+template <int W2>
+__device__ __forceinline__ void st_row(float* p, const float2 (&x)[W2]) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) *reinterpret_cast<float4*>(p + 2 * i) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
+    for (int i = 0; i < W2; i += 2) *reinterpret_cast<float4*>(p + 2 * i) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
 }
-template <>
-__device__ __forceinline__ void st16<__nv_bfloat16>(__nv_bfloat16* p, const float2* x) {
+template <int W2>
+__device__ __forceinline__ void st_row(__nv_bfloat16* p, const float2 (&x)[W2]) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
+    for (int i = 0; i < W2; i += 4) {
         uint4 w[1];
         split8<1>(x + i, w);
         *reinterpret_cast<uint4*>(p + 2 * i) = w[0];
     }
-}
-
-template <typename Tout>
-__device__ __forceinline__ void st16(Tout* p, const float* x) {
-    float2 y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
-    st16(p, y);
 }
 
 // Tensor map of a strided bf16 [batch][head][token][d] array: boxes of 64 tokens x 64 columns
