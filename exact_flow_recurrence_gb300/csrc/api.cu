@@ -677,9 +677,7 @@ extern "C" {
 size_t efla_gated_fwd_workspace_size(const efla_gated_shape* s) {
     efla::GDims d;
     if (check_gated(s, false, false, &d) != EFLA_OK) return 0;
-    const size_t simt = efla::gated_simt_fwd_ws_bytes(d);
-    const size_t tc = s->path != EFLA_PATH_SIMT && efla::gated_tc_supported(d) ? efla::gated_tc_fwd_ws_bytes(d) : 0;
-    return tc > simt ? tc : simt;
+    return s->path != EFLA_PATH_SIMT && d.in_bf16 ? efla::gated_tc_fwd_ws_bytes(d) : 0;   // (the fp32 kernel needs none)
 }
 
 size_t efla_gated_bwd_workspace_size(const efla_gated_shape* s) {
@@ -717,13 +715,13 @@ efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const 
         const Span outs[] = {S_final == (float*)S0 ? Span{nullptr, 0, ""} : sSf};
         if ((st = check_gated_alias(io.x, 6, 5, ins, 2, outs, 1, sw)) != EFLA_OK) return st;
     }
-    const size_t need = d.tensor ? efla::gated_tc_fwd_ws_bytes(d) : efla::gated_simt_fwd_ws_bytes(d);
+    const size_t need = d.tensor ? efla::gated_tc_fwd_ws_bytes(d) : 0;
     if (need && (!workspace || workspace_bytes < need))
         return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
     efla::prof_mark(nullptr, stream);
     const cudaError_t e =
         d.tensor ? efla::launch_gated_fwd_tc(d, q, k, v, g, beta, S0, o, S_final, workspace, stream)
-                 : efla::launch_gated_fwd_simt(d, q, k, v, g, beta, S0, o, S_final, workspace, stream);
+                 : efla::launch_gated_fwd_simt(d, q, k, v, g, beta, S0, o, S_final, stream);
     return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_gated_fwd");
 }
 

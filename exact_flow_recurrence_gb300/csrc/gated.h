@@ -22,11 +22,9 @@ struct GDims {
 };
 
 // -------------------------------------------------------------- fp32 CUDA-core kernels
-size_t gated_simt_fwd_ws_bytes(const GDims& d);
 size_t gated_simt_bwd_ws_bytes(const GDims& d);
 cudaError_t launch_gated_fwd_simt(const GDims& d, const void* q, const void* k, const void* v, const float* g,
-                                  const float* beta, const float* S0, void* o, float* S_final, void* ws,
-                                  cudaStream_t st);
+                                  const float* beta, const float* S0, void* o, float* S_final, cudaStream_t st);
 cudaError_t launch_gated_bwd_simt(const GDims& d, const void* q, const void* k, const void* v, const float* g,
                                   const float* beta, const float* S0, const void* dO, const float* dS_final,
                                   void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dS0, void* ws,

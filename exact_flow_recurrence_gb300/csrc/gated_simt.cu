@@ -3,45 +3,45 @@
 //
 // For each sequence and value head, with log decays g_t and alpha_t (beta_t, or the exact
 // flow's (1 - e^{-beta lambda}) / lambda):
-//   S <- e^{g_t} S,   S <- S + alpha_t k_t (v_t - S^T k_t)^T,   o_t = S^T q_t.
-// In chunks of C tokens, with c_i the sum of the chunk's g up to token i, D_ij = e^{c_i - c_j}
+//   S <- e^{g_t} S,   r_t = v_t - S^T k_t,   S <- S + alpha_t k_t r_t^T,   o_t = S^T q_t
+// and backwards, G the gradient of the state after token t, from the tokens that follow:
+//   w_t = (G + q_t dO_t^T)^T k_t,   dv_t = alpha_t w_t,   G <- e^{g_t} (G + q_t dO_t^T - alpha_t k_t w_t^T)
+// Both recurrences are taken a token at a time, on states that stay in registers: the fp32
+// multiply-adds are as many as in chunked products of 32 tokens, and none of their operands
+// but k and q come from shared memory.  A state column needs no other column, so a CTA has 16 of
+// them, and a column's dk rows lie on eight lanes.  Every token is one chain, because
+// o_t = e^g S^T q + alpha (k.q) r takes both sums from the state before it: two dots (32 multiply-adds a
+// lane), three steps of a butterfly, the update.
+//
+// The gradients of q, k and the gates then come from the states recorded every C tokens, in
+// products over a chunk: with c_i the sum of the chunk's g up to token i, D_ij = e^{c_i - c_j}
 // for j <= i (never above 1 for decays: no quotient of two products is formed), S the state
-// entering the chunk:
-//   A = strict_lower(alpha_i D_ij k_i.k_j),  T = (I + A)^{-1},  P = lower(D_ij q_i.k_j)
-//   R = V - diag(e^c) K S,   U = T diag(alpha) R
-//   O = diag(e^c) Q S + P U,   S' = e^{c_last} S + K^T diag(e^{c_last - c}) U
-// and backwards, G the gradient of S':
-//   dU = P^T dO + diag(e^{c_last - c}) K G,   dX = T^T dU,   dV = diag(alpha) dX
-//   dA = -strict_lower(dX U^T),   dP = lower(dO U^T)
+// entering the chunk, G the gradient of the one that leaves it, U = diag(alpha) R:
+//   dA = -strict_lower(W U^T),   dP = lower(dO U^T)
 //   dQ = diag(e^c) dO S^T + (dP D) K
 //   dK = (dP D)^T Q + diag(e^{c_last - c}) U G^T - diag(e^c) dV S^T
 //        + (dA alpha D) K + (dA alpha D)^T K  (+ 2 dlambda k)
-//   dalpha_i = dX_i . R_i + sum_j dA_ij D_ij k_i.k_j
+//   dalpha_i = w_i . r_i
 //   dc_i from every e^{c}, then dg_t = sum_{i >= t} dc_i inside the chunk
-//   G <- e^{c_last} G + (diag(e^c) Q)^T dO - (diag(e^c) K)^T dV
 // These kernels take the calls that the tensor-core kernels do not (fp32 tokens, odd strides).
-// They are bound by the fp32 multiply-adds and by shared-memory reads of their operands; the
-// sequential scans run one CTA for each 16 value columns so that a few heads still fill SMs.
 #include "gated_seq.cuh"
 #include "launch.h"
+#include "packed2.cuh"
 
 namespace efla {
 
 namespace {
 
-constexpr int kC = 32;        // tokens a chunk: the triangular inverse stays short
+constexpr int kC = 32;        // tokens a chunk of the gradients
 constexpr int kNT = 256;
-constexpr int kDVS = 16;      // value columns of a scan CTA
 constexpr int kLd = 129;      // row stride of a [32][<=128] tile in shared memory (odd: no bank conflicts by rows or columns)
 constexpr int kLs = 33;       // of a [32][32] tile
-constexpr int kLv = 17;       // of a [..][16] tile
 
-struct SimtWs {
-    float *T, *P, *cs, *al;       // [H][slots][32][32] x 2, [H][slots][2][32] (c: hi, lo), [H][slots][32]
-    float *S, *R, *U, *G, *dX;    // backward only: [H][slots][dk][dv], [..][32][dv] x 2, [..][dk][dv], [..][32][dv]
+struct SimtWs {   // backward only
+    float *S, *R, *G, *W;    // [H][slots][dk][dv], [..][32][dv], [..][dk][dv], [..][32][dv]
 };
 
-size_t carve(const GDims& d, bool bwd, void* base, SimtWs* w) {
+size_t carve(const GDims& d, void* base, SimtWs* w) {
     const size_t n = (size_t)d.H * d.slots(kC);
     char* p = (char*)base;
     const auto take = [&](size_t floats) {
@@ -49,18 +49,10 @@ size_t carve(const GDims& d, bool bwd, void* base, SimtWs* w) {
         p += align256(floats * 4);
         return r;
     };
-    w->T = take(n * kC * kC);
-    w->P = take(n * kC * kC);
-    w->cs = take(n * 2 * kC);
-    w->al = take(n * kC);
-    w->S = w->R = w->U = w->G = w->dX = nullptr;
-    if (bwd) {
-        w->S = take(n * d.dk * d.dv);
-        w->R = take(n * kC * d.dv);
-        w->U = take(n * kC * d.dv);
-        w->G = take(n * d.dk * d.dv);
-        w->dX = take(n * kC * d.dv);
-    }
+    w->S = take(n * d.dk * d.dv);
+    w->R = take(n * kC * d.dv);
+    w->G = take(n * d.dk * d.dv);
+    w->W = take(n * kC * d.dv);
     return (size_t)(p - (char*)base);
 }
 
@@ -72,198 +64,188 @@ __device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, long
     }
 }
 
-// -------------------------------------------------- per chunk: T, P, c, alpha
-template <typename Tin>
-__global__ void __launch_bounds__(kNT) k_gated_prep(GDims d, const Tin* q, const Tin* k, const float* g,
-                                                    const float* beta, SimtWs w, int slots) {
-    __shared__ float Ks[kC * kLd], Qs[kC * kLd], A[kC * kLs];
-    __shared__ float cs[2 * kC], al[kC];
-    const int slot = blockIdx.x, h = blockIdx.y, hk = h / (d.H / d.Hk), tid = threadIdx.x;
-    const int b = seq_of_slot(d, slot, kC);
-    const SeqAt s = seq_at(d, b, kC);
-    const int t0 = (slot - s.slot0) * kC, n = min(kC, s.len - t0);
-    if (n <= 0) return;
-    load_rows(Ks, kLd, k + at3(d.ks, s.batch, hk, s.start + t0), d.ks[2], n, d.dk);
-    load_rows(Qs, kLd, q + at3(d.qs, s.batch, hk, s.start + t0), d.qs[2], n, d.dk);
-    __syncthreads();
-    if (tid < 32) {
-        const int t = s.start + t0 + tid;
-        double c = tid < n ? (double)log_decay(g[at3(d.gs, s.batch, h, t)]) : 0.0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, c, o);
-            if (tid >= o) c += x;
-        }
-        float lam = 0.f;
-        for (int i = 0; i < d.dk; ++i) lam = fmaf(Ks[tid * kLd + i], Ks[tid * kLd + i], lam);
-        cs[tid] = (float)c;
-        cs[kC + tid] = (float)(c - (double)cs[tid]);
-        al[tid] = tid < n ? alpha_of(beta[at3(d.bs, s.batch, h, t)], lam, d.euler) : 0.f;
-    }
-    __syncthreads();
-    const size_t rec = (size_t)h * slots + slot;
-    float* P = w.P + rec * kC * kC;
-    block_mm<kNT>(kC, kC, d.dk, [&](int i, int x) { return Ks[i * kLd + x]; },
-                  [&](int x, int j) { return Ks[j * kLd + x]; },
-                  [&](int i, int j, float v) { A[i * kLs + j] = j < i ? al[i] * decay(cs[i], cs[kC + i], cs[j], cs[kC + j]) * v : 0.f; });
-    block_mm<kNT>(kC, kC, d.dk, [&](int i, int x) { return Qs[i * kLd + x]; },
-                  [&](int x, int j) { return Ks[j * kLd + x]; },
-                  [&](int i, int j, float v) { P[i * kC + j] = j <= i ? decay(cs[i], cs[kC + i], cs[j], cs[kC + j]) * v : 0.f; });
-    __syncthreads();
-    if (tid < 32) {   // column tid of T by forward substitution
-        float x[kC];
-#pragma unroll
-        for (int i = 0; i < kC; ++i) x[i] = i == tid ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 0; j < kC - 1; ++j)
-#pragma unroll
-            for (int i = j + 1; i < kC; ++i) x[i] = fmaf(-A[i * kLs + j], x[j], x[i]);
-        float* T = w.T + rec * kC * kC;
-#pragma unroll
-        for (int i = 0; i < kC; ++i) T[i * kC + tid] = x[i];
-        w.cs[rec * 2 * kC + tid] = cs[tid];
-        w.cs[rec * 2 * kC + kC + tid] = cs[kC + tid];
-        w.al[rec * kC + tid] = al[tid];
-    }
-}
+// -------------------------------------------------- the recurrences
+constexpr int kRT = 128;      // threads: four warps of four columns
+constexpr int kCols = 16;
+constexpr int kTS = 16;       // tokens a stage of k, q, v in shared memory (two stages)
 
-// -------------------------------------------------- forward scan over the chunks
-template <typename Tin, typename Tout>
-__global__ void __launch_bounds__(kNT) k_gated_scan(GDims d, const Tin* q, const Tin* k, const Tin* v, const float* S0,
-                                                    Tout* o, float* S_final, SimtWs w, int slots) {
-    __shared__ float Ks[kC * kLd], S[128 * kLv], X[kC * kLv], U[kC * kLv], O[kC * kLv];
-    __shared__ float Ts[kC * kLs], cs[2 * kC], al[kC];
-    const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * kDVS;
-    const int tid = threadIdx.x, dk = d.dk, dv = d.dv;
-    const SeqAt s = seq_at(d, b, kC);
-    const size_t sb = (size_t)blockIdx.x * dk * dv + c0;
-    for (int e = tid; e < dk * kDVS; e += kNT) {
-        const int r = e / kDVS, x = e % kDVS;
-        S[r * kLv + x] = S0 ? S0[sb + (size_t)r * dv + x] : 0.f;
-    }
-    for (int t0 = 0; t0 < s.len; t0 += kC) {
-        const int n = min(kC, s.len - t0), t = s.start + t0;
-        const size_t rec = (size_t)h * slots + s.slot0 + t0 / kC;
-        __syncthreads();
-        load_rows(Ks, kLd, q + at3(d.qs, s.batch, hk, t), d.qs[2], n, dk);   // the queries first
-        load_rows(X, kLv, v + at3(d.vs, s.batch, h, t) + c0, d.vs[2], n, kDVS);
-        if (tid < 2 * kC) cs[tid] = w.cs[rec * 2 * kC + tid];
-        if (tid < kC) {
-            al[tid] = w.al[rec * kC + tid];
-        }
-        for (int e = tid; e < kC * kC; e += kNT) Ts[(e / kC) * kLs + e % kC] = w.T[rec * kC * kC + e];
-        if (w.S)
-            for (int e = tid; e < dk * kDVS; e += kNT)
-                w.S[rec * dk * dv + (size_t)(e / kDVS) * dv + c0 + e % kDVS] = S[(e / kDVS) * kLv + e % kDVS];
-        __syncthreads();
-        block_mm<kNT>(kC, kDVS, dk, [&](int i, int x) { return Ks[i * kLd + x]; },
-                      [&](int x, int j) { return S[x * kLv + j]; },
-                      [&](int i, int j, float y) { O[i * kLv + j] = expf(cs[i]) * y; });
-        __syncthreads();
-        load_rows(Ks, kLd, k + at3(d.ks, s.batch, hk, t), d.ks[2], n, dk);
-        __syncthreads();
-        block_mm<kNT>(kC, kDVS, dk, [&](int i, int x) { return Ks[i * kLd + x]; },
-                      [&](int x, int j) { return S[x * kLv + j]; },
-                      [&](int i, int j, float y) {
-                          const float r = i < n ? X[i * kLv + j] - expf(cs[i]) * y : 0.f;
-                          if (w.R) w.R[(rec * kC + i) * dv + c0 + j] = r;
-                          X[i * kLv + j] = al[i] * r;
-                      });
-        __syncthreads();
-        block_mm_ranged<kNT>(kC, kDVS, [&](int i, int x) { return Ts[i * kLs + x]; },
-                             [&](int x, int j) { return X[x * kLv + j]; },
-                             [&](int i, int, int& lo, int& hi) { lo = 0; hi = i + 1; },
-                             [&](int i, int j, float y) {
-                                 U[i * kLv + j] = y;
-                                 if (w.U) w.U[(rec * kC + i) * dv + c0 + j] = y;
-                             });
-        __syncthreads();
-        for (int e = tid; e < kC * kC; e += kNT) Ts[(e / kC) * kLs + e % kC] = w.P[rec * kC * kC + e];
-        const float cl = cs[n - 1], el = expf(cl);
-        block_mm<kNT>(dk, kDVS, kC, [&](int r, int i) { return Ks[i * kLd + r]; },
-                      [&](int i, int j) { return i < n ? decay(cl, cs[kC + n - 1], cs[i], cs[kC + i]) * U[i * kLv + j] : 0.f; },
-                      [&](int r, int j, float y) { S[r * kLv + j] = fmaf(el, S[r * kLv + j], y); });
-        __syncthreads();
-        if (o)
-            block_mm_ranged<kNT>(kC, kDVS, [&](int i, int x) { return Ts[i * kLs + x]; },
-                                 [&](int x, int j) { return U[x * kLv + j]; },
-                                 [&](int i, int, int& lo, int& hi) { lo = 0; hi = i < n ? i + 1 : 0; },
-                                 [&](int i, int j, float y) {
-                                     if (i < n) st_elem(o + at3(d.os, s.batch, h, t + i) + c0 + j, O[i * kLv + j] + y);
-                                 });
-    }
-    __syncthreads();
-    if (S_final)
-        for (int e = tid; e < dk * kDVS; e += kNT)
-            S_final[sb + (size_t)(e / kDVS) * dv + e % kDVS] = S[(e / kDVS) * kLv + e % kDVS];
-}
+enum { FWD, RECORD, REVERSE };
 
-// -------------------------------------------------- reverse scan: G and dX of every chunk
-template <typename Tin>
-__global__ void __launch_bounds__(kNT) k_gated_rscan(GDims d, const Tin* q, const Tin* k, const Tin* dO,
-                                                     const float* dS_final, float* dS0, SimtWs w, int slots) {
-    __shared__ float Ks[kC * kLd], G[128 * kLv], X[kC * kLv], D[kC * kLv], U[kC * kLv];
-    __shared__ float Ts[kC * kLs], cs[2 * kC], al[kC];
-    const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * kDVS;
-    const int tid = threadIdx.x, dk = d.dk, dv = d.dv;
+struct RecArgs {
+    const void *q, *k, *v;    // REVERSE: v is dO
+    const float *g, *beta;
+    const float* state;       // S0, or the final state's gradient
+    void* o;                  // FWD
+    float* last;              // the final state, or S0's gradient
+    float *rec_S, *rec_R;     // RECORD: S and r;  REVERSE: G and w
+    int slots;
+};
+
+template <typename Tin, typename Tout, int KW, int MODE>
+__global__ void __launch_bounds__(kRT, 3) k_gated_rec(GDims d, RecArgs a) {
+    constexpr int RJ = KW / 32, NL = kTS * KW / kRT;   // float4s of a lane's rows; elements a thread stages
+    constexpr bool Q = MODE != RECORD;
+    __shared__ __align__(16) float Ks[2][kTS][KW], Qs[2][Q ? kTS : 1][KW], Vs[2][kTS][kCols], Eg[2][kTS], Al[2][kTS], Kq[2][kTS];
+    const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * kCols;
+    const int tid = threadIdx.x, lane = tid & 31, l = lane & 7, cx = (tid >> 5) * 4 + (lane >> 3), col = c0 + cx;
+    const int dk = d.dk, dv = d.dv;
     const SeqAt s = seq_at(d, b, kC);
-    const size_t sb = (size_t)blockIdx.x * dk * dv + c0;
-    for (int e = tid; e < dk * kDVS; e += kNT)
-        G[(e / kDVS) * kLv + e % kDVS] = dS_final ? dS_final[sb + (size_t)(e / kDVS) * dv + e % kDVS] : 0.f;
-    for (int t0 = (s.len - 1) / kC * kC; s.len > 0 && t0 >= 0; t0 -= kC) {
-        const int n = min(kC, s.len - t0), t = s.start + t0;
-        const size_t rec = (size_t)h * slots + s.slot0 + t0 / kC;
-        __syncthreads();
-        load_rows(Ks, kLd, k + at3(d.ks, s.batch, hk, t), d.ks[2], n, dk);
-        load_rows(D, kLv, dO + at3(d.dos, s.batch, h, t) + c0, d.dos[2], n, kDVS);
-        if (tid < 2 * kC) cs[tid] = w.cs[rec * 2 * kC + tid];
-        if (tid < kC) {
-            al[tid] = w.al[rec * kC + tid];
-        }
-        for (int e = tid; e < kC * kC; e += kNT) Ts[(e / kC) * kLs + e % kC] = w.P[rec * kC * kC + e];
-        for (int e = tid; e < dk * kDVS; e += kNT)
-            w.G[rec * dk * dv + (size_t)(e / kDVS) * dv + c0 + e % kDVS] = G[(e / kDVS) * kLv + e % kDVS];
-        __syncthreads();
-        const float cl = cs[n - 1], el = expf(cl);
-        block_mm<kNT>(kC, kDVS, dk, [&](int i, int x) { return Ks[i * kLd + x]; },
-                      [&](int x, int j) { return G[x * kLv + j]; },
-                      [&](int i, int j, float y) { U[i * kLv + j] = i < n ? decay(cl, cs[kC + n - 1], cs[i], cs[kC + i]) * y : 0.f; });
-        __syncthreads();
-        block_mm_ranged<kNT>(kC, kDVS, [&](int i, int x) { return Ts[x * kLs + i]; },
-                             [&](int x, int j) { return D[x * kLv + j]; },
-                             [&](int i, int, int& lo, int& hi) { lo = i; hi = n; },
-                             [&](int i, int j, float y) { U[i * kLv + j] += y; });
-        __syncthreads();
-        for (int e = tid; e < kC * kC; e += kNT) Ts[(e / kC) * kLs + e % kC] = w.T[rec * kC * kC + e];
-        __syncthreads();
-        block_mm_ranged<kNT>(kC, kDVS, [&](int i, int x) { return Ts[x * kLs + i]; },
-                             [&](int x, int j) { return U[x * kLv + j]; },
-                             [&](int i, int, int& lo, int& hi) { lo = i; hi = n; },
-                             [&](int i, int j, float y) {
-                                 w.dX[(rec * kC + i) * dv + c0 + j] = y;
-                                 X[i * kLv + j] = al[i] * y;
-                             });
-        __syncthreads();
-        block_mm<kNT>(dk, kDVS, kC, [&](int r, int i) { return Ks[i * kLd + r]; },
-                      [&](int i, int j) { return expf(cs[i]) * X[i * kLv + j]; },
-                      [&](int r, int j, float y) { G[r * kLv + j] = fmaf(el, G[r * kLv + j], -y); });
-        __syncthreads();
-        load_rows(Ks, kLd, q + at3(d.qs, s.batch, hk, t), d.qs[2], n, dk);
-        __syncthreads();
-        block_mm<kNT>(dk, kDVS, kC, [&](int r, int i) { return Ks[i * kLd + r]; },
-                      [&](int i, int j) { return expf(cs[i]) * D[i * kLv + j]; },
-                      [&](int r, int j, float y) { G[r * kLv + j] += y; });
+    // rows 4 (l + 8 j) .. + 3 of column col, two a register pair
+    float2 S[2 * RJ];
+    const size_t sb = (size_t)blockIdx.x * dk * dv + col;
+    const auto row = [&](int j, int e) { return 4 * (l + 8 * j) + e; };
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = a.state && row(j, e) < dk ? a.state[sb + (size_t)row(j, e) * dv] : 0.f;
+        S[2 * j] = make_float2(x[0], x[1]);
+        S[2 * j + 1] = make_float2(x[2], x[3]);
     }
-    __syncthreads();
-    if (dS0)
-        for (int e = tid; e < dk * kDVS; e += kNT)
-            dS0[sb + (size_t)(e / kDVS) * dv + e % kDVS] = G[(e / kDVS) * kLv + e % kDVS];
+    const auto put_state = [&](float* p) {
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+            if (row(j, 0) < dk) {   // (dk is a multiple of 4)
+                p[(size_t)row(j, 0) * dv] = S[2 * j].x;
+                p[(size_t)row(j, 1) * dv] = S[2 * j].y;
+                p[(size_t)row(j, 2) * dv] = S[2 * j + 1].x;
+                p[(size_t)row(j, 3) * dv] = S[2 * j + 1].y;
+            }
+        }
+    };
+    float kr[NL], qr[Q ? NL : 1], vr[2], gr = 0.f, br = 0.f;   // the next stage, on its way
+    const auto fetch = [&](int t0) {
+        const int n = min(kTS, s.len - t0), t = s.start + t0;
+        const Tin* kp = (const Tin*)a.k + at3(d.ks, s.batch, hk, t);
+        const Tin* qp = (const Tin*)a.q + at3(d.qs, s.batch, hk, t);
+#pragma unroll
+        for (int e = 0; e < NL; ++e) {
+            const int r = (tid + e * kRT) / KW, x = (tid + e * kRT) % KW;
+            const bool in = r < n && x < dk;
+            kr[e] = in ? ld_elem(kp + r * d.ks[2] + x) : 0.f;
+            if (Q) qr[e] = in ? ld_elem(qp + r * d.qs[2] + x) : 0.f;
+        }
+        const long long (&vst)[3] = MODE == REVERSE ? d.dos : d.vs;
+        const Tin* vp = (const Tin*)a.v + at3(vst, s.batch, h, t) + c0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = (tid + e * kRT) / kCols, x = tid % kCols;
+            vr[e] = r < n ? ld_elem(vp + r * vst[2] + x) : 0.f;
+        }
+        if ((tid & 7) == 0) {   // eight threads a token below: the first of them
+            const bool in = tid / 8 < n;
+            gr = in ? a.g[at3(d.gs, s.batch, h, t + tid / 8)] : 0.f;
+            br = in ? a.beta[at3(d.bs, s.batch, h, t + tid / 8)] : 0.f;
+        }
+    };
+    const int stages = (s.len + kTS - 1) / kTS;
+    const auto begin = [&](int it) { return (MODE == REVERSE ? stages - 1 - it : it) * kTS; };
+    if (stages) fetch(begin(0));
+    for (int it = 0; it < stages; ++it) {
+        const int u = it & 1, t0 = begin(it), n = min(kTS, s.len - t0);
+        const size_t rec = (size_t)h * a.slots + s.slot0 + t0 / kC;
+#pragma unroll
+        for (int e = 0; e < NL; ++e) {
+            const int r = (tid + e * kRT) / KW, x = (tid + e * kRT) % KW;
+            Ks[u][r][x] = kr[e];
+            if (Q) Qs[u][r][x] = qr[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) Vs[u][(tid + e * kRT) / kCols][tid % kCols] = vr[e];
+        __syncthreads();
+        {   // the stage's k.q, lambda, alpha and decays: eight threads a token
+            float2 kq = both(0.f), lam = both(0.f);
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) {
+                const float4 x = *reinterpret_cast<const float4*>(&Ks[u][tid >> 3][4 * (l + 8 * j)]);
+                lam = fma2(make_float2(x.x, x.y), make_float2(x.x, x.y), lam);
+                lam = fma2(make_float2(x.z, x.w), make_float2(x.z, x.w), lam);
+                if (Q) {
+                    const float4 y = *reinterpret_cast<const float4*>(&Qs[u][tid >> 3][4 * (l + 8 * j)]);
+                    kq = fma2(make_float2(x.x, x.y), make_float2(y.x, y.y), kq);
+                    kq = fma2(make_float2(x.z, x.w), make_float2(y.z, y.w), kq);
+                }
+            }
+            float x = lam.x + lam.y, y = kq.x + kq.y;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                x += __shfl_xor_sync(0xffffffffu, x, o);
+                y += __shfl_xor_sync(0xffffffffu, y, o);
+            }
+            if (l == 0) {
+                Eg[u][tid >> 3] = expf(log_decay(gr));
+                Al[u][tid >> 3] = tid >> 3 < n ? alpha_of(br, x, d.euler) : 0.f;
+                Kq[u][tid >> 3] = y;
+            }
+        }
+        __syncthreads();
+        if (it + 1 < stages) fetch(begin(it + 1));
+        if (MODE == RECORD && t0 % kC == 0) put_state(a.rec_S + rec * dk * dv + col);
+        if (MODE == REVERSE && (it == 0 || t0 % kC != 0)) put_state(a.rec_S + rec * dk * dv + col);
+        float keep = 0.f;   // lane l's of eight tokens' results of this column
+#pragma unroll 4
+        for (int m = 0; m < n; ++m) {
+            const int i = MODE == REVERSE ? n - 1 - m : m;
+            float2 k[2 * RJ], q[2 * RJ];
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) {
+                const float4 x = *reinterpret_cast<const float4*>(&Ks[u][i][4 * (l + 8 * j)]);
+                k[2 * j] = make_float2(x.x, x.y);
+                k[2 * j + 1] = make_float2(x.z, x.w);
+                if (Q) {
+                    const float4 y = *reinterpret_cast<const float4*>(&Qs[u][i][4 * (l + 8 * j)]);
+                    q[2 * j] = make_float2(y.x, y.y);
+                    q[2 * j + 1] = make_float2(y.z, y.w);
+                }
+            }
+            const float eg = Eg[u][i], al = Al[u][i], kq = Q ? Kq[u][i] : 0.f, v = Vs[u][i][cx];
+            float2 x[2] = {mul2(S[0], k[0]), mul2(S[1], k[1])}, y[2] = {both(0.f), both(0.f)};
+#pragma unroll
+            for (int j = 2; j < 2 * RJ; ++j) x[j & 1] = fma2(S[j], k[j], x[j & 1]);
+            x[0] = add2(x[0], x[1]);
+            float sk = x[0].x + x[0].y, sq = 0.f;
+            if (MODE == FWD) {
+                y[0] = mul2(S[0], q[0]);
+                y[1] = mul2(S[1], q[1]);
+#pragma unroll
+                for (int j = 2; j < 2 * RJ; ++j) y[j & 1] = fma2(S[j], q[j], y[j & 1]);
+                y[0] = add2(y[0], y[1]);
+                sq = y[0].x + y[0].y;
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                sk += __shfl_xor_sync(0xffffffffu, sk, o);
+                if (MODE == FWD) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            }
+            float res;
+            if (MODE == REVERSE) {
+                res = fmaf(kq, v, sk);   // w
+                const float2 a1 = both(eg * v), a2 = both(-eg * al * res);
+#pragma unroll
+                for (int j = 0; j < 2 * RJ; ++j) S[j] = fma2(both(eg), S[j], fma2(a1, q[j], mul2(a2, k[j])));
+            } else {
+                const float r = fmaf(-eg, sk, v), ar = al * r;
+                res = MODE == FWD ? fmaf(kq, ar, eg * sq) : r;
+#pragma unroll
+                for (int j = 0; j < 2 * RJ; ++j) S[j] = fma2(both(ar), k[j], mul2(both(eg), S[j]));
+            }
+            if ((i & 7) == l) keep = res;
+            if (MODE == REVERSE ? (i & 7) == 0 : (i & 7) == 7 || i == n - 1) {
+                const int ti = (i & ~7) + l;
+                if (ti < n) {
+                    if (MODE == FWD) st_elem((Tout*)a.o + at3(d.os, s.batch, h, s.start + t0 + ti) + col, keep);
+                    else a.rec_R[(rec * kC + t0 % kC + ti) * dv + col] = keep;
+                }
+            }
+        }
+    }
+    if (a.last) put_state(a.last + sb);
 }
 
 // -------------------------------------------------- gradients of a chunk, all value heads of a key head
 struct GradSmem {
     float K[kC * kLd], Q[kC * kLd], dQ[kC * kLd], dK[kC * kLd], V[kC * kLd], Y[kC * kLd], Z[kC * kLd];
-    float dP[kC * kLs], dA[kC * kLs], KK[kC * kLs], P[kC * kLs], W[kC * kLs];
+    float dP[kC * kLs], dA[kC * kLs], KK[kC * kLs], QK[kC * kLs], W[kC * kLs];
     float cs[2 * kC], al[kC], be[kC], lam[kC], dc[kC], da[kC], dl[kC], part[8];
 };
 
@@ -286,8 +268,8 @@ __device__ __forceinline__ void add_rows(float* acc, const float* Z, const float
 
 template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const Tin* k, const Tin* dO,
-                                                    const float* beta, Tout* dq, Tout* dk_, Tout* dv_, float* dg,
-                                                    float* dbeta, SimtWs w, int slots) {
+                                                    const float* g, const float* beta, Tout* dq, Tout* dk_, Tout* dv_,
+                                                    float* dg, float* dbeta, SimtWs w, int slots) {
     extern __shared__ float gsm[];
     GradSmem& m = *reinterpret_cast<GradSmem*>(gsm);
     const int slot = blockIdx.x, hk = blockIdx.y, rep = d.H / d.Hk, tid = threadIdx.x, dk = d.dk, dv = d.dv;
@@ -302,24 +284,37 @@ __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const
     block_mm<kNT>(kC, kC, dk, [&](int i, int x) { return m.K[i * kLd + x]; },
                   [&](int x, int j) { return m.K[j * kLd + x]; },
                   [&](int i, int j, float y) { m.KK[i * kLs + j] = y; });
+    block_mm<kNT>(kC, kC, dk, [&](int i, int x) { return m.Q[i * kLd + x]; },
+                  [&](int x, int j) { return m.K[j * kLd + x]; },
+                  [&](int i, int j, float y) { m.QK[i * kLs + j] = y; });
     for (int h = hk * rep; h < (hk + 1) * rep; ++h) {
         const size_t rec = (size_t)h * slots + slot;
         const float* S = w.S + rec * dk * dv;
         const float* G = w.G + rec * dk * dv;
         const float* R = w.R + rec * kC * dv;
-        const float* U = w.U + rec * kC * dv;
-        const float* dX = w.dX + rec * kC * dv;
+        const float* dX = w.W + rec * kC * dv;
         __syncthreads();
-        if (tid < 2 * kC) m.cs[tid] = w.cs[rec * 2 * kC + tid];
         if (tid < kC) {
-            m.al[tid] = w.al[rec * kC + tid];
-            m.be[tid] = tid < n ? beta[at3(d.bs, s.batch, h, t + tid)] : 0.f;
-            m.lam[tid] = m.KK[tid * kLs + tid];
+            double c = tid < n ? (double)log_decay(g[at3(d.gs, s.batch, h, t + tid)]) : 0.0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_up_sync(0xffffffffu, c, o);
+                if (tid >= o) c += x;
+            }
+            const float be = tid < n ? beta[at3(d.bs, s.batch, h, t + tid)] : 0.f, lam = m.KK[tid * kLs + tid];
+            m.cs[tid] = (float)c;
+            m.cs[kC + tid] = (float)(c - (double)m.cs[tid]);
+            m.be[tid] = be;
+            m.lam[tid] = lam;
+            m.al[tid] = tid < n ? alpha_of(be, lam, d.euler) : 0.f;
             m.da[tid] = m.dc[tid] = m.dl[tid] = 0.f;
         }
-        for (int e = tid; e < kC * kC; e += kNT) m.P[(e / kC) * kLs + e % kC] = w.P[rec * kC * kC + e];
         load_rows(m.V, kLd, dO + at3(d.dos, s.batch, h, t), d.dos[2], n, dv);
-        load_rows(m.Y, kLd, U, dv, n, dv);
+        __syncthreads();
+        for (int e = tid; e < kC * dv; e += kNT) {   // U = alpha r
+            const int i = e / dv, x = e - i * dv;
+            m.Y[i * kLd + x] = i < n ? m.al[i] * R[e] : 0.f;
+        }
         __syncthreads();
         const float cl = m.cs[n - 1];
         // dP = lower(dO U^T); dO S^T; U G^T
@@ -364,29 +359,23 @@ __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const
         if (tid % 32 == 0) m.part[tid / 32] = gs;
         __syncthreads();
         // the chunk's own pairs: dP D, dA alpha D, and the sums by rows and columns of
-        // dP P + dA A (into dc) and of dA D K K^T (into dalpha)
+        // dP P + dA A (into dc)
         for (int e = tid; e < kC * kC; e += kNT) {
             const int i = e / kC, j = e % kC, at = i * kLs + j;
             if (j > i || i >= n) {
-                m.dP[at] = m.dA[at] = m.W[at] = m.Z[i * kLd + j] = 0.f;
+                m.dP[at] = m.dA[at] = m.W[at] = 0.f;
                 continue;
             }
             const float D = decay(m.cs[i], m.cs[kC + i], m.cs[j], m.cs[kC + j]), p = m.dP[at], a = m.dA[at];
-            const float ak = a * D * m.KK[at];
-            m.W[at] = fmaf(p, m.P[at], m.al[i] * ak);
-            m.Z[i * kLd + j] = ak;
+            m.W[at] = D * fmaf(p, m.QK[at], m.al[i] * a * m.KK[at]);
             m.dP[at] = p * D;
             m.dA[at] = m.al[i] * a * D;
         }
         __syncthreads();
         if (tid < kC) {
-            float c = m.dc[tid] - m.dl[tid], a = m.da[tid];
-            for (int j = 0; j < kC; ++j) {
-                c += m.W[tid * kLs + j] - m.W[j * kLs + tid];
-                a += m.Z[tid * kLd + j];
-            }
+            float c = m.dc[tid] - m.dl[tid];
+            for (int j = 0; j < kC; ++j) c += m.W[tid * kLs + j] - m.W[j * kLs + tid];
             m.dc[tid] = c;
-            m.da[tid] = a;
         }
         __syncthreads();
         block_mm<kNT>(kC, dk, kC, [&](int i, int x) { return m.dP[i * kLs + x]; },
@@ -431,17 +420,11 @@ __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const
     }
 }
 
-template <typename Tin, typename Tout>
-cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, const float* g, const float* beta,
-                const float* S0, void* o, float* S_final, const SimtWs& w, cudaStream_t st) {
-    const int slots = d.slots(kC);
-    if (slots) {
-        k_gated_prep<Tin><<<dim3(slots, d.H), kNT, 0, st>>>(d, (const Tin*)q, (const Tin*)k, g, beta, w, slots);
-        prof_mark("gated_prep_simt", st);
-    }
-    k_gated_scan<Tin, Tout><<<dim3((unsigned)d.BH(), d.dv / kDVS), kNT, 0, st>>>(
-        d, (const Tin*)q, (const Tin*)k, (const Tin*)v, S0, (Tout*)o, S_final, w, slots);
-    prof_mark("gated_scan_simt", st);
+template <typename Tin, typename Tout, int MODE>
+cudaError_t rec(const GDims& d, const RecArgs& a, cudaStream_t st) {
+    const auto k = d.dk <= 64 ? k_gated_rec<Tin, Tout, 64, MODE> : k_gated_rec<Tin, Tout, 128, MODE>;
+    k<<<dim3((unsigned)d.BH(), d.dv / kCols), kRT, 0, st>>>(d, a);
+    prof_mark(MODE == FWD ? "gated_scan_simt" : MODE == RECORD ? "gated_record_simt" : "gated_rscan_simt", st);
     return cudaGetLastError();
 }
 
@@ -449,43 +432,33 @@ template <typename Tin, typename Tout>
 cudaError_t bwd(const GDims& d, const void* q, const void* k, const void* v, const float* g, const float* beta,
                 const float* S0, const void* dO, const float* dS_final, void* dq, void* dk, void* dv, float* dg,
                 float* dbeta, float* dS0, const SimtWs& w, cudaStream_t st) {
+    const int slots = d.slots(kC);
     cudaError_t e = cudaFuncSetAttribute(k_gated_grad<Tin, Tout>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(GradSmem));
-    if (e == cudaSuccess) e = fwd<Tin, Tout>(d, q, k, v, g, beta, S0, nullptr, nullptr, w, st);
-    if (e != cudaSuccess) return e;
-    const int slots = d.slots(kC);
-    k_gated_rscan<Tin><<<dim3((unsigned)d.BH(), d.dv / kDVS), kNT, 0, st>>>(
-        d, (const Tin*)q, (const Tin*)k, (const Tin*)dO, dS_final, dS0, w, slots);
-    prof_mark("gated_rscan_simt", st);
-    if (!slots) return cudaGetLastError();
+    if (e == cudaSuccess && slots)
+        e = rec<Tin, float, RECORD>(d, RecArgs{q, k, v, g, beta, S0, nullptr, nullptr, w.S, w.R, slots}, st);
+    if (e == cudaSuccess)
+        e = rec<Tin, float, REVERSE>(d, RecArgs{q, k, dO, g, beta, dS_final, nullptr, dS0, w.G, w.W, slots}, st);
+    if (e != cudaSuccess || !slots) return e;
     k_gated_grad<Tin, Tout><<<dim3(slots, d.Hk), kNT, sizeof(GradSmem), st>>>(
-        d, (const Tin*)q, (const Tin*)k, (const Tin*)dO, beta, (Tout*)dq, (Tout*)dk, (Tout*)dv, dg, dbeta, w, slots);
+        d, (const Tin*)q, (const Tin*)k, (const Tin*)dO, g, beta, (Tout*)dq, (Tout*)dk, (Tout*)dv, dg, dbeta, w, slots);
     prof_mark("gated_grad_simt", st);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t gated_simt_fwd_ws_bytes(const GDims& d) {
-    SimtWs w;
-    return carve(d, false, nullptr, &w);
-}
 size_t gated_simt_bwd_ws_bytes(const GDims& d) {
     SimtWs w;
-    return carve(d, true, nullptr, &w);
+    return carve(d, nullptr, &w);
 }
 
 cudaError_t launch_gated_fwd_simt(const GDims& d, const void* q, const void* k, const void* v, const float* g,
-                                  const float* beta, const float* S0, void* o, float* S_final, void* ws,
-                                  cudaStream_t st) {
-    SimtWs w;
-    carve(d, false, ws, &w);
+                                  const float* beta, const float* S0, void* o, float* S_final, cudaStream_t st) {
+    const RecArgs a{q, k, v, g, beta, S0, o, S_final, nullptr, nullptr, 0};
     using B = __nv_bfloat16;
-    if (d.in_bf16)
-        return d.out_bf16 ? fwd<B, B>(d, q, k, v, g, beta, S0, o, S_final, w, st)
-                          : fwd<B, float>(d, q, k, v, g, beta, S0, o, S_final, w, st);
-    return d.out_bf16 ? fwd<float, B>(d, q, k, v, g, beta, S0, o, S_final, w, st)
-                      : fwd<float, float>(d, q, k, v, g, beta, S0, o, S_final, w, st);
+    if (d.in_bf16) return d.out_bf16 ? rec<B, B, FWD>(d, a, st) : rec<B, float, FWD>(d, a, st);
+    return d.out_bf16 ? rec<float, B, FWD>(d, a, st) : rec<float, float, FWD>(d, a, st);
 }
 
 cudaError_t launch_gated_bwd_simt(const GDims& d, const void* q, const void* k, const void* v, const float* g,
@@ -493,7 +466,7 @@ cudaError_t launch_gated_bwd_simt(const GDims& d, const void* q, const void* k, 
                                   void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dS0, void* ws,
                                   cudaStream_t st) {
     SimtWs w;
-    carve(d, true, ws, &w);
+    carve(d, ws, &w);
     using B = __nv_bfloat16;
     if (d.in_bf16)
         return d.out_bf16 ? bwd<B, B>(d, q, k, v, g, beta, S0, dO, dS_final, dq, dk, dv, dg, dbeta, dS0, w, st)
