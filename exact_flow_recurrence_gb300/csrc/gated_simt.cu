@@ -34,8 +34,8 @@ namespace {
 
 constexpr int kC = 32;        // tokens a chunk of the gradients
 constexpr int kNT = 256;
-constexpr int kLd = 129;      // row stride of a [32][<=128] tile in shared memory (odd: no bank conflicts by rows or columns)
-constexpr int kLs = 33;       // of a [32][32] tile
+constexpr int kLd = 132;      // row strides of a [32][<= 128] tile in shared memory and of a [..][32] one: 16-byte
+constexpr int kLs = 36;       // reads of the same columns in eight rows find different banks
 
 struct SimtWs {   // backward only
     float *S, *R, *G, *W;    // [H][slots][dk][dv], [..][32][dv], [..][dk][dv], [..][32][dv]
@@ -243,56 +243,127 @@ __global__ void __launch_bounds__(kRT, 3) k_gated_rec(GDims d, RecArgs a) {
 }
 
 // -------------------------------------------------- gradients of a chunk, all value heads of a key head
+// A thread has rows i = warp + 8 r and columns j = lane + 32 c of every product (r, c < 4), dQ's and
+// dK's among them, which stay in registers over the value heads.  A row's columns are one warp's, so
+// the sums by rows are warp sums, in a fixed order.  Bound by the fp32 multiply-adds and the
+// shared-memory reads that feed them (one 16-byte read for 8 multiply-adds).
 struct GradSmem {
-    float K[kC * kLd], Q[kC * kLd], dQ[kC * kLd], dK[kC * kLd], V[kC * kLd], Y[kC * kLd], Z[kC * kLd];
+    float K[kC * kLd], Q[kC * kLd], V[kC * kLd], Y[kC * kLd];
+    float St[128 * kLs];                                            // 32 columns of S or G
     float dP[kC * kLs], dA[kC * kLs], KK[kC * kLs], QK[kC * kLs], W[kC * kLs];
     float cs[2 * kC], al[kC], be[kC], lam[kC], dc[kC], da[kC], dl[kC], part[8];
 };
+using Acc = float[4][4];
 
-// acc += diag(f) Z and sum[i] += w sum_x f_i Z[i][x] Y[i][x], one warp a row (a fixed order: no atomics)
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+}
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// y[r][c] += sum_x A[i][x] B[j][x], x < width (a multiple of 4), rows j < nj of B
+template <int NC>
+__device__ __forceinline__ void mm_nt(float (&y)[4][NC], const float* A, int lda, const float* B, int ldb, int width, int nj) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int x = 0; x < width; x += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] = ld4(A + (w + 8 * r) * lda + x);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if (32 * c >= nj) break;
+            const float4 q = ld4(B + (lane + 32 * c) * ldb + x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r][c] = dot4(p[r], q, y[r][c]);
+        }
+    }
+}
+// y[r][c] += sum_x A(i, x) B[x][j], x < 32
 template <typename F>
-__device__ __forceinline__ void add_rows(float* acc, const float* Z, const float* Y, int width, F f, float w, float* sum) {
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < kC; i += kNT / 32) {
-        const float c = f(i);
+__device__ __forceinline__ void mm_nn(Acc& y, F A, const float* B, int nj) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 4
+    for (int x = 0; x < kC; ++x) {
+        float p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] = A(w + 8 * r, x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (32 * c >= nj) break;
+            const float q = B[x * kLd + lane + 32 * c];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r][c] = fmaf(p[r], q, y[r][c]);
+        }
+    }
+}
+// y = A M^T for a recorded M [dk][dv], 32 of its columns at a time
+__device__ __forceinline__ void mm_state(GradSmem& m, Acc& y, const float* A, const float* M, int dk, int dv) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[r][c] = 0.f;
+    for (int x0 = 0; x0 < dv; x0 += 32) {
+        const int nx = min(32, dv - x0);
+        __syncthreads();
+        for (int e = threadIdx.x; e < dk * 8; e += kNT)   // (a row's 32 columns: eight 16-byte pieces)
+            if (4 * (e & 7) < nx)
+                *reinterpret_cast<float4*>(m.St + (e >> 3) * kLs + 4 * (e & 7)) = ld4(M + (size_t)(e >> 3) * dv + x0 + 4 * (e & 7));
+        __syncthreads();
+        mm_nt<4>(y, A + x0, kLd, m.St, kLs, nx, dk);
+    }
+}
+// acc += f_i y and sum[i] += f_i sum_j y X[i][j]
+template <typename F>
+__device__ __forceinline__ void add_rows(Acc& acc, const Acc& y, const float* X, F f, float* sum, int dk) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = w + 8 * r;
+        const float fi = f(i);
         float dot = 0.f;
-        for (int x = lane; x < width; x += 32) {
-            const float z = c * Z[i * kLd + x];
-            acc[i * kLd + x] += z;
-            dot = fmaf(z, Y[i * kLd + x], dot);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (lane + 32 * c >= dk) break;
+            const float z = fi * y[r][c];
+            acc[r][c] += z;
+            dot = fmaf(z, X[i * kLd + lane + 32 * c], dot);
         }
         dot = warp_sum(dot);
-        if (lane == 0) sum[i] = fmaf(w, dot, sum[i]);
+        if (lane == 0) sum[i] += dot;
     }
 }
 
 template <typename Tin, typename Tout>
-__global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const Tin* k, const Tin* dO,
-                                                    const float* g, const float* beta, Tout* dq, Tout* dk_, Tout* dv_,
-                                                    float* dg, float* dbeta, SimtWs w, int slots) {
-    extern __shared__ float gsm[];
+__global__ void __launch_bounds__(kNT, 2) k_gated_grad(GDims d, const Tin* q, const Tin* k, const Tin* dO,
+                                                       const float* g, const float* beta, Tout* dq, Tout* dk_, Tout* dv_,
+                                                       float* dg, float* dbeta, SimtWs w, int slots) {
+    extern __shared__ __align__(16) float gsm[];
     GradSmem& m = *reinterpret_cast<GradSmem*>(gsm);
     const int slot = blockIdx.x, hk = blockIdx.y, rep = d.H / d.Hk, tid = threadIdx.x, dk = d.dk, dv = d.dv;
+    const int wp = tid >> 5, lane = tid & 31;
     const int b = seq_of_slot(d, slot, kC);
     const SeqAt s = seq_at(d, b, kC);
     const int t0 = (slot - s.slot0) * kC, n = min(kC, s.len - t0), t = s.start + t0;
     if (n <= 0) return;
     load_rows(m.K, kLd, k + at3(d.ks, s.batch, hk, t), d.ks[2], n, dk);
     load_rows(m.Q, kLd, q + at3(d.qs, s.batch, hk, t), d.qs[2], n, dk);
-    for (int e = tid; e < kC * kLd; e += kNT) m.dQ[e] = m.dK[e] = 0.f;
     __syncthreads();
-    block_mm<kNT>(kC, kC, dk, [&](int i, int x) { return m.K[i * kLd + x]; },
-                  [&](int x, int j) { return m.K[j * kLd + x]; },
-                  [&](int i, int j, float y) { m.KK[i * kLs + j] = y; });
-    block_mm<kNT>(kC, kC, dk, [&](int i, int x) { return m.Q[i * kLd + x]; },
-                  [&](int x, int j) { return m.K[j * kLd + x]; },
-                  [&](int i, int j, float y) { m.QK[i * kLs + j] = y; });
+    {
+        float y[4][1] = {}, z[4][1] = {};
+        mm_nt<1>(y, m.K, kLd, m.K, kLd, dk, kC);
+        mm_nt<1>(z, m.Q, kLd, m.K, kLd, dk, kC);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            m.KK[(wp + 8 * r) * kLs + lane] = y[r][0];
+            m.QK[(wp + 8 * r) * kLs + lane] = z[r][0];
+        }
+    }
+    Acc aq = {}, ak = {};
     for (int h = hk * rep; h < (hk + 1) * rep; ++h) {
         const size_t rec = (size_t)h * slots + slot;
         const float* S = w.S + rec * dk * dv;
         const float* G = w.G + rec * dk * dv;
         const float* R = w.R + rec * kC * dv;
-        const float* dX = w.W + rec * kC * dv;
+        const float* W = w.W + rec * kC * dv;
         __syncthreads();
         if (tid < kC) {
             double c = tid < n ? (double)log_decay(g[at3(d.gs, s.batch, h, t + tid)]) : 0.0;
@@ -307,7 +378,7 @@ __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const
             m.be[tid] = be;
             m.lam[tid] = lam;
             m.al[tid] = tid < n ? alpha_of(be, lam, d.euler) : 0.f;
-            m.da[tid] = m.dc[tid] = m.dl[tid] = 0.f;
+            m.dc[tid] = m.dl[tid] = 0.f;
         }
         load_rows(m.V, kLd, dO + at3(d.dos, s.batch, h, t), d.dos[2], n, dv);
         __syncthreads();
@@ -316,47 +387,43 @@ __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const
             m.Y[i * kLd + x] = i < n ? m.al[i] * R[e] : 0.f;
         }
         __syncthreads();
-        const float cl = m.cs[n - 1];
-        // dP = lower(dO U^T); dO S^T; U G^T
-        block_mm<kNT>(kC, kC, dv, [&](int i, int x) { return m.V[i * kLd + x]; },
-                      [&](int x, int j) { return m.Y[j * kLd + x]; },
-                      [&](int i, int j, float y) { m.dP[i * kLs + j] = j <= i ? y : 0.f; });
-        block_mm<kNT>(kC, dk, dv, [&](int i, int x) { return m.V[i * kLd + x]; },
-                      [&](int x, int j) { return S[(size_t)j * dv + x]; },
-                      [&](int i, int j, float y) { m.Z[i * kLd + j] = y; });
+        const float cl = m.cs[n - 1], cl2 = m.cs[kC + n - 1];
+        const auto rest = [&](int i) { return i < n ? decay(cl, cl2, m.cs[i], m.cs[kC + i]) : 0.f; };
+        Acc y;
+        {   // dP = lower(dO U^T)
+            float z[4][1] = {};
+            mm_nt<1>(z, m.V, kLd, m.Y, kLd, dv, kC);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m.dP[(wp + 8 * r) * kLs + lane] = lane <= wp + 8 * r ? z[r][0] : 0.f;
+        }
+        mm_state(m, y, m.V, S, dk, dv);      // dO S^T
+        add_rows(aq, y, m.Q, [&](int i) { return expf(m.cs[i]); }, m.dc, dk);
+        mm_state(m, y, m.Y, G, dk, dv);      // U G^T
+        add_rows(ak, y, m.K, rest, m.dl, dk);
+        load_rows(m.V, kLd, W, dv, n, dv);   // (the products with dO are over: mm_state's barriers)
         __syncthreads();
-        add_rows(m.dQ, m.Z, m.Q, dk, [&](int i) { return expf(m.cs[i]); }, 1.f, m.dc);
-        __syncthreads();
-        block_mm<kNT>(kC, dk, dv, [&](int i, int x) { return m.Y[i * kLd + x]; },
-                      [&](int x, int j) { return G[(size_t)j * dv + x]; },
-                      [&](int i, int j, float y) { m.Z[i * kLd + j] = y; });
-        load_rows(m.V, kLd, dX, dv, n, dv);
-        __syncthreads();
-        add_rows(m.dK, m.Z, m.K, dk, [&](int i) { return i < n ? decay(cl, m.cs[kC + n - 1], m.cs[i], m.cs[kC + i]) : 0.f; }, 1.f, m.dl);
-        // dA = -strict_lower(dX U^T); dV; (alpha dX) S^T
-        block_mm<kNT>(kC, kC, dv, [&](int i, int x) { return m.V[i * kLd + x]; },
-                      [&](int x, int j) { return m.Y[j * kLd + x]; },
-                      [&](int i, int j, float y) { m.dA[i * kLs + j] = j < i ? -y : 0.f; });
-        for (int i = tid >> 5; i < n; i += kNT / 32) {
+        {   // dA = -strict_lower(W U^T); dV, dalpha
+            float z[4][1] = {};
+            mm_nt<1>(z, m.V, kLd, m.Y, kLd, dv, kC);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m.dA[(wp + 8 * r) * kLs + lane] = lane < wp + 8 * r ? -z[r][0] : 0.f;
+        }
+        for (int i = wp; i < n; i += kNT / 32) {
             float dot = 0.f;
-            for (int x = tid & 31; x < dv; x += 32) {
-                const float y = m.V[i * kLd + x];
-                st_elem(dv_ + at3(d.dvs, s.batch, h, t + i) + x, m.al[i] * y);
-                dot = fmaf(y, R[(size_t)i * dv + x], dot);
+            for (int x = lane; x < dv; x += 32) {
+                const float z = m.V[i * kLd + x];
+                st_elem(dv_ + at3(d.dvs, s.batch, h, t + i) + x, m.al[i] * z);
+                dot = fmaf(z, R[(size_t)i * dv + x], dot);
             }
             dot = warp_sum(dot);
-            if ((tid & 31) == 0) m.da[i] = dot;
+            if (lane == 0) m.da[i] = dot;
         }
-        __syncthreads();
-        block_mm<kNT>(kC, dk, dv, [&](int i, int x) { return m.al[i] * m.V[i * kLd + x]; },
-                      [&](int x, int j) { return S[(size_t)j * dv + x]; },
-                      [&](int i, int j, float y) { m.Z[i * kLd + j] = -y; });
-        __syncthreads();
-        add_rows(m.dK, m.Z, m.K, dk, [&](int i) { return expf(m.cs[i]); }, 1.f, m.dc);
+        mm_state(m, y, m.V, S, dk, dv);      // W S^T
+        add_rows(ak, y, m.K, [&](int i) { return -expf(m.cs[i]) * m.al[i]; }, m.dc, dk);
         float gs = 0.f;   // <G, S> e^{c_last}, through the decay of the whole chunk
-        for (int e = tid; e < dk * dv; e += kNT) gs = fmaf(S[e], G[e], gs);
+        for (int e = 4 * tid; e < dk * dv; e += 4 * kNT) gs = dot4(ld4(S + e), ld4(G + e), gs);
         gs = warp_sum(gs);
-        if (tid % 32 == 0) m.part[tid / 32] = gs;
+        if (lane == 0) m.part[wp] = gs;
         __syncthreads();
         // the chunk's own pairs: dP D, dA alpha D, and the sums by rows and columns of
         // dP P + dA A (into dc)
@@ -372,36 +439,31 @@ __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const
             m.dA[at] = m.al[i] * a * D;
         }
         __syncthreads();
-        if (tid < kC) {
-            float c = m.dc[tid] - m.dl[tid];
-            for (int j = 0; j < kC; ++j) c += m.W[tid * kLs + j] - m.W[j * kLs + tid];
-            m.dc[tid] = c;
+        mm_nn(aq, [&](int i, int x) { return m.dP[i * kLs + x]; }, m.K, dk);
+        mm_nn(ak, [&](int i, int x) { return m.dP[x * kLs + i]; }, m.Q, dk);
+        mm_nn(ak, [&](int i, int x) { return m.dA[i * kLs + x] + m.dA[x * kLs + i]; }, m.K, dk);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = wp + 8 * r;
+            const float dl = i < n ? 2.f * m.da[i] * dalpha_dlambda_of(m.be[i], m.lam[i], d.euler) : 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (lane + 32 * c < dk) ak[r][c] = fmaf(dl, m.K[i * kLd + lane + 32 * c], ak[r][c]);
         }
-        __syncthreads();
-        block_mm<kNT>(kC, dk, kC, [&](int i, int x) { return m.dP[i * kLs + x]; },
-                      [&](int x, int j) { return m.K[x * kLd + j]; },
-                      [&](int i, int j, float y) { m.dQ[i * kLd + j] += y; });
-        block_mm<kNT>(kC, dk, kC, [&](int i, int x) { return m.dP[x * kLs + i]; },
-                      [&](int x, int j) { return m.Q[x * kLd + j]; },
-                      [&](int i, int j, float y) { m.dK[i * kLd + j] += y; });
-        block_mm<kNT>(kC, dk, kC, [&](int i, int x) { return m.dA[i * kLs + x] + m.dA[x * kLs + i]; },
-                      [&](int x, int j) { return m.K[x * kLd + j]; },
-                      [&](int i, int j, float y) {
-                          const float dl = m.da[i] * dalpha_dlambda_of(m.be[i], m.lam[i], d.euler);
-                          m.dK[i * kLd + j] += fmaf(2.f * dl, m.K[i * kLd + j], y);
-                      });
         if (tid < 32) {
-            float x = tid < n ? m.dc[tid] : 0.f;
+            float x = m.dc[tid] - m.dl[tid];
+            for (int j = 0; j < kC; ++j) x += m.W[tid * kLs + j] - m.W[j * kLs + tid];
+            if (tid >= n) x = 0.f;
             if (tid == n - 1) {
-                float y = 0.f;
-                for (int e = 0; e < 8; ++e) y += m.part[e];
-                x = fmaf(expf(cl), y, x);
+                float z = 0.f;
+                for (int e = 0; e < 8; ++e) z += m.part[e];
+                x = fmaf(expf(cl), z, x);
                 for (int i = 0; i < n; ++i) x += m.dl[i];   // U G^T's e^{c_last - c_i}
             }
 #pragma unroll
             for (int o2 = 1; o2 < 32; o2 <<= 1) {   // sums from token tid to the chunk's end
-                const float y = __shfl_down_sync(0xffffffffu, x, o2);
-                if (tid + o2 < 32) x += y;
+                const float z = __shfl_down_sync(0xffffffffu, x, o2);
+                if (tid + o2 < 32) x += z;
             }
             if (tid < n) {
                 const size_t at = ((size_t)(d.packed ? 0 : b) * d.H + h) * d.L + t + tid;
@@ -410,12 +472,16 @@ __global__ void __launch_bounds__(kNT) k_gated_grad(GDims d, const Tin* q, const
             }
         }
     }
-    __syncthreads();
-    for (int e = tid; e < kC * dk; e += kNT) {
-        const int i = e / dk, x = e - i * dk;
-        if (i < n) {
-            st_elem(dq + at3(d.dqs, s.batch, hk, t + i) + x, m.dQ[i * kLd + x]);
-            st_elem(dk_ + at3(d.dks, s.batch, hk, t + i) + x, m.dK[i * kLd + x]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = wp + 8 * r;
+        if (i >= n) continue;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int j = lane + 32 * c;
+            if (j >= dk) continue;
+            st_elem(dq + at3(d.dqs, s.batch, hk, t + i) + j, aq[r][c]);
+            st_elem(dk_ + at3(d.dks, s.batch, hk, t + i) + j, ak[r][c]);
         }
     }
 }
