@@ -718,6 +718,7 @@ efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const 
     const size_t need = d.tensor ? efla::gated_tc_fwd_ws_bytes(d) : 0;
     if (need && (!workspace || workspace_bytes < need))
         return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    if (s->path == EFLA_PATH_AUTO && efla::gated_fwd_short(d)) d.tensor = 0;   // (the workspace asked for is the shape's all the same)
     efla::prof_mark(nullptr, stream);
     const cudaError_t e =
         d.tensor ? efla::launch_gated_fwd_tc(d, q, k, v, g, beta, S0, o, S_final, workspace, stream)

@@ -23,6 +23,8 @@ struct GDims {
 
 // -------------------------------------------------------------- fp32 CUDA-core kernels
 size_t gated_simt_bwd_ws_bytes(const GDims& d);
+// Whether the recurrence is the faster forward pass where the tensor-core kernels would do too.
+bool gated_fwd_short(const GDims& d);
 cudaError_t launch_gated_fwd_simt(const GDims& d, const void* q, const void* k, const void* v, const float* g,
                                   const float* beta, const float* S0, void* o, float* S_final, cudaStream_t st);
 cudaError_t launch_gated_bwd_simt(const GDims& d, const void* q, const void* k, const void* v, const float* g,

@@ -514,6 +514,13 @@ cudaError_t bwd(const GDims& d, const void* q, const void* k, const void* v, con
 
 }  // namespace
 
+// The tensor-core kernels take two launches and a whole chunk's products for any length: 14 us up to
+// 64 tokens (d 128).  The recurrence takes one launch and a time that grows with the tokens and, once
+// its CTAs no longer all run at once, with their number.  H 4 / H 32, B 1, in us, tensor cores first:
+//   L 1: 13.7, 3.5 / 14.3, 4.3    L 16: 13.7, 5.5 / 14.5, 7.5    L 32: 13.9, 8.6 / 14.5, 12.0
+//   L 64: 13.9, 15.0 / 14.7, 20.9;    B 16 H 16 (2048 CTAs) L 32: 41, 63
+bool gated_fwd_short(const GDims& d) { return d.L <= 32 && d.BH() * (d.dv / kCols) <= 3 * 152; }
+
 size_t gated_simt_bwd_ws_bytes(const GDims& d) {
     SimtWs w;
     return carve(d, nullptr, &w);
