@@ -19,13 +19,14 @@ __device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kS
 // One chunk of a value head per CTA of 128 threads:
 //   1. the chunk's K and Q rows by TMA into [K; Q] tiles (128 rows);
 //   2. one product [K; Q] K^T: lanes 0..63 G = K K^T (its diagonal: lambda), 64..127 Q K^T;
-//   3. from the decays: A (fp32, shared memory), and P as bf16 parts in rows 64..127 of the image;
+//   3. from the decays: A (fp32, shared memory), and P, which stays in registers meanwhile;
 //   4. T = (I + A)^{-1} in place of A (blocked substitution, split tf32: about fp32 accuracy),
-//      its parts into rows 0..63 of the image;
-//   5. one product [T; P] T, whose lanes 64..127 (P T) replace P's parts;
-//   6. the [T; P T] image, NP parts of 128 rows in the operand layout, out by bulk copy.
+//      its bf16 parts on their way out by bulk copy; then P's parts in place of A and T;
+//   5. one product P T, whose parts replace P's and go out too: the [T; P T] image, NP parts of
+//      128 rows in the operand layout.
 // Bound by its chain of short dependent steps, not by data: what counts is how many chunks an
-// SM has in flight.  The image lies over the dead tiles and T over A, so that four chunks fit.
+// SM has in flight.  P's parts lie over A and T, and both over the dead tiles, so that four
+// chunks fit (as many as the registers allow).
 struct PrepArgs {
     const float* g;
     const float* beta;
@@ -37,9 +38,9 @@ struct PrepArgs {
 
 template <int NP>
 struct PrepSmem {
-    static constexpr uint32_t IMG = 0;             // the tiles first; the inverse's scratch in its rows 0..63
-    static constexpr uint32_t A = NP * 16384;      // [64][kLdA] fp32
-    static constexpr uint32_t VEC = A + 64 * kLdA * 4;
+    static constexpr uint32_t P = 0;               // NP tiles of 64 rows; [64][kLdA] fp32 before (and the K, Q tiles first)
+    static constexpr uint32_t T = NP == 2 ? 64 * kLdA * 4 / 1024 * 1024 + 1024 : NP * 8192;   // NP tiles; the inverse's scratch before
+    static constexpr uint32_t VEC = T + NP * 8192;
     static constexpr uint32_t BAR = VEC + sizeof(GVec);
     static constexpr size_t bytes = 1024 + BAR + 64;
 };
@@ -116,10 +117,12 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
         }
         __syncwarp();
     }
+    const size_t rec = (size_t)h * a.slots + slot, all = (size_t)d.H * a.slots;
+    unsigned char* const out = a.img + rec * NP * 16384;
+    const bool out_ok = dbg_in(out, NP * 16384, a.img, all * NP * 16384, &g_gt2_status);
     bool ok = __syncthreads_and(mbar_wait(&bar[1], 0, kWaitLimit));
     tc_fence_after();
-    float* T = (float*)(sm + M::A);
-    unsigned char* img = sm + M::IMG;
+    float* T = (float*)(sm + M::P);
     if (ok) {
         const int i = tid & 63;   // this lane's token; lanes 0..63 hold A's rows, 64..127 P's
         const int cols = 32 * (warp & 1) + 32;   // columns that the warp's rows reach
@@ -153,26 +156,24 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
                 v[j] = v[j + 1] = v[j + 2] = v[j + 3] = 0.f;
             }
         }
-        // 64 values as parts into a row of the image
-        const auto put_row = [&](int r, const float* x) {
+        // 64 values as parts into row i of P's tiles
+        const auto put_row = [&](const float* x) {
 #pragma unroll
             for (int j = 0; j < 64; j += 8) {
                 uint4 w[NP];
                 split8<NP>(x + j, w);
 #pragma unroll
-                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(img + p * 16384 + sw128(r, j)) = w[p];
+                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(sm + M::P + p * 8192 + sw128(i, j)) = w[p];
             }
         };
         if (tid < 64) {
 #pragma unroll
             for (int j = 0; j < 64; j += 4)
                 *reinterpret_cast<float4*>(T + i * kLdA + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        } else {
-            put_row(64 + i, v);
         }
         tc_fence_before();
         group_sync(1);
-        unit_lower_inverse64(T, T, (float*)img, 1, tid);
+        unit_lower_inverse64(T, T, (float*)(sm + M::T), 1, tid);
         {   // T's parts, 32 columns a thread (zero above its 16x16 diagonal blocks)
             const int r = tid >> 1, h0 = 32 * (tid & 1);
 #pragma unroll
@@ -186,35 +187,40 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
                 uint4 w[NP];
                 split8<NP>(x, w);
 #pragma unroll
-                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(img + p * 16384 + sw128(r, h0 + j)) = w[p];
+                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(sm + M::T + p * 8192 + sw128(r, h0 + j)) = w[p];
             }
         }
         fence_async_smem();
+        group_sync(1);
+        if (tid == 0 && out_ok)
+            for (int p = 0; p < NP; ++p) bulk_s2g(out + p * 16384, sm + M::T + p * 8192, 8192);
+        if (tid >= 64) put_row(v);
+        fence_async_smem();
         tc_fence_before();
         group_sync(1);
-        if (warp == 0 && elect_one()) {   // [T; P] T, the part pairs p + x < NP (B: T's rows are K indices)
-            tc_fence_after();
-            const uint64_t da = sdesc_sw128(smem_u32(img));
+        if (warp == 0 && elect_one()) {   // P T, the part pairs p + x < NP (B: T's rows are K indices; rows 64..127 of A
+            tc_fence_after();             // are what follows P's tiles, and not used)
+            const uint64_t da = sdesc_sw128(smem_u32(sm + M::P)), db = sdesc_sw128(smem_u32(sm + M::T));
 #pragma unroll
             for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
                 for (int x = NP - 1 - p; x >= 0; --x)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_ss(tb, da + p * 1024 + ks * 2, da + x * 1024 + ks * 128, idesc_f16(128, 64, false, true, true),
+                        mma_f16_ss(tb, da + p * 512 + ks * 2, db + x * 512 + ks * 128, idesc_f16(128, 64, false, true, true),
                                    !(p == NP - 1 && x == 0 && ks == 0));
             mma_commit(&bar[2]);
         }
         ok = group_sync_and(1, mbar_wait(&bar[2], 0, kWaitLimit));
         tc_fence_after();
-        if (tid >= 64 && ok) {
+        if (tid < 64 && ok) {
 #pragma unroll
             for (int c = 0; c < 64; c += 16)
                 tmem_ld16(taddr(tb, warp * 32, c), *reinterpret_cast<float(*)[16]>(v + c));
             tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 64; c += 16) loaded16(v + c);
-            put_row(64 + i, v);
+            put_row(v);
             tc_fence_before();
         }
         fence_async_smem();
@@ -227,11 +233,12 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && ok) {
-        const size_t rec = (size_t)h * a.slots + slot, all = (size_t)d.H * a.slots;
-        if (dbg_in(a.img + rec * NP * 16384, NP * 16384, a.img, all * NP * 16384, &g_gt2_status))
-            bulk_s2g(a.img + rec * NP * 16384, img, NP * 16384);
+        if (out_ok)
+            for (int p = 0; p < NP; ++p) bulk_s2g(out + p * 16384 + 8192, sm + M::P + p * 8192, 8192);
         if (dbg_in(a.vec + rec, sizeof(GVec), a.vec, all * sizeof(GVec), &g_gt2_status))
             bulk_s2g(a.vec + rec, vec, sizeof(GVec));
+    }
+    if (tid == 0) {   // (T's parts are on their way even if a wait has given up since)
         bulk_commit();
         bulk_wait_read();
     }
