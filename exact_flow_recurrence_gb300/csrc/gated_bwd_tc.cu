@@ -176,14 +176,16 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     const size_t rec = (rec0 + nch - 1 - it) * gridDim.y + blockIdx.y;
                     ok = mbar_wait(chain0, ph, kWaitLimit) && mbar_wait(chain0 + 9, ph, kWaitLimit);
                     if (!ok) break;
-                    bulk_s2g(a.rec_G + rec * kRecS, sm + M::G, kRecS);
+                    if (dbg_in(a.rec_G + rec * kRecS, kRecS, a.rec_G, records(d, a.slots, kRecS), &g_gb_status))
+                        bulk_s2g(a.rec_G + rec * kRecS, sm + M::G, kRecS);
                     bulk_commit();
                     bulk_wait_read();   // (and the dX of the chunk before)
                     mbar_arrive(g_free);
                     if (it > 0) mbar_arrive(r_free);
                     ok = mbar_wait(chain0 + 8, ph, kWaitLimit) && mbar_wait(chain0 + 17, ph, kWaitLimit);
                     if (!ok) break;
-                    bulk_s2g(a.rec_dX + rec * kRecU, sm + M::R, kRecU);
+                    if (dbg_in(a.rec_dX + rec * kRecU, kRecU, a.rec_dX, records(d, a.slots, kRecU), &g_gb_status))
+                        bulk_s2g(a.rec_dX + rec * kRecU, sm + M::R, kRecU);
                     bulk_commit();
                 }
                 bulk_wait_read();
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
 #pragma unroll
                     for (int m = 0; m < 8; ++m) y[m] = mul2(both(al), y[m]);
-                    st_row(vp, y);
+                    if (dbg_in(vp, 16 * sizeof(Tout), a.dv, extent(d, d.dvs, d.H, d.dv) * sizeof(Tout), &g_gb_status)) st_row(vp, y);
                 }
             }
             if (!(ok = warp_wait(q + 6, ph))) break;
@@ -840,7 +842,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             *q0 = v[0];
                             split8<1>(o + 4, v);
                             *q1 = v[0];
-                        } else if (i < n) {
+                        } else if (i < n && dbg_in(out + c, 64, top ? a.dq : a.dk,
+                                                   extent(d, top ? d.dqs : d.dks, d.Hk, dk) * 4, &g_gb_status)) {
                             st_row(out + c, o);
                         }
                     }
@@ -855,8 +858,10 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int r = e * 16 + (tid >> 4), ch = tid & 15, j = r & 63;
-                        if (j < n && ch * 8 < dk)
-                            *reinterpret_cast<uint4*>((e < 4 ? pq + j * d.dqs[2] : pk + j * d.dks[2]) + ch * 8) =
+                        Tout* const to = (e < 4 ? pq + j * d.dqs[2] : pk + j * d.dks[2]) + ch * 8;
+                        if (j < n && ch * 8 < dk &&
+                            dbg_in(to, 16, e < 4 ? a.dq : a.dk, extent(d, e < 4 ? d.dqs : d.dks, d.Hk, dk) * 2, &g_gb_status))
+                            *reinterpret_cast<uint4*>(to) =
                                 *reinterpret_cast<const uint4*>(sm + kGrQK + (ch >> 3) * 16384 + sw128(r, (ch & 7) * 8));
                     }
                 }
@@ -892,7 +897,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int j = 2 * lane + e;
-                        if (j < n) {
+                        const size_t all = (size_t)(d.packed ? 1 : d.B) * d.H * d.L * 4;
+                        if (j < n && dbg_in(a.dg + at + j, 4, a.dg, all, &g_gb_status)) {   // (dbeta: the same places)
                             a.dg[at + j] = e ? sum - c[0] : sum;
                             a.dbeta[at + j] = m.da[j] * dalpha_dbeta_of(m.be[j], m.lam[j], d.euler);
                         }

@@ -411,14 +411,16 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     const uint32_t ph = c & 1;
                     for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g, ph, kWaitLimit);
                     if (!ok) break;
-                    bulk_s2g(a.rec_S + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecS, sm + M::S, kRecS);
+                    unsigned char* const to_S = a.rec_S + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecS;
+                    if (dbg_in(to_S, kRecS, a.rec_S, records(d, a.slots, kRecS), &g_gt2_status)) bulk_s2g(to_S, sm + M::S, kRecS);
                     bulk_commit();
                     bulk_wait_read();   // (and the U of the chunk before)
                     mbar_arrive(s_free);
                     if (c > 0) mbar_arrive(u_free);
                     for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g + 3, ph, kWaitLimit);
                     if (!ok) break;
-                    bulk_s2g(a.rec_U + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecU, sm + M::U, kRecU);
+                    unsigned char* const to_U = a.rec_U + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecU;
+                    if (dbg_in(to_U, kRecU, a.rec_U, records(d, a.slots, kRecU), &g_gt2_status)) bulk_s2g(to_U, sm + M::U, kRecU);
                     bulk_commit();
                 }
                 bulk_wait_read();
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                 for (int m = 0; m < CW / 2; ++m) z[m] = fma2(both(up), y[m], z[m]);
                 if (i < n && in) {
                     Tout* op = (Tout*)a.o + at3(d.os, s.batch, h, s.start + c * kGC + i) + col;
-                    if (dbg_in(op, CW * sizeof(Tout), a.o, o_extent(d) * sizeof(Tout), &g_gt2_status)) st_row(op, z);
+                    if (dbg_in(op, CW * sizeof(Tout), a.o, extent(d, d.os, d.H, d.dv) * sizeof(Tout), &g_gt2_status)) st_row(op, z);
                 }
             }
             if (!(ok = warp_wait(q + 6, ph))) break;

@@ -22,9 +22,13 @@ namespace efla {
 constexpr int kGC = 64;   // tokens a chunk of the tensor-core kernels
 constexpr uint32_t kRecS = 3 * 16384, kRecU = 3 * 8192;   // bytes of a recorded slice
 
-// Elements from the first to the last of o (debug builds' bounds).
-__device__ __forceinline__ size_t o_extent(const GDims& d) {
-    return (d.packed ? 0 : (d.B - 1) * d.os[0]) + (d.H - 1) * d.os[1] + (d.L - 1) * d.os[2] + d.dv;
+// Elements from the first to the last of a strided [batch][heads][token][width] array, and the bytes
+// of all records of a kind (debug builds' bounds).
+__device__ __forceinline__ size_t extent(const GDims& d, const long long (&s)[3], int heads, int width) {
+    return (d.packed ? 0 : (d.B - 1) * s[0]) + (heads - 1) * s[1] + (d.L - 1) * s[2] + width;
+}
+__device__ __forceinline__ size_t records(const GDims& d, int slots, size_t bytes) {
+    return (size_t)d.H * slots * ((d.dv + 63) / 64) * bytes;
 }
 
 // What the preparation leaves of a chunk and value head besides the T, P T image: five vectors.
