@@ -552,7 +552,7 @@ bool interleaved(const Strided& a, const Strided& b) {
     return off >= wa && off + wb <= st;
 }
 
-efla_status check_gated(const efla_gated_shape* s, bool step, bool bwd, efla::GDims* d) {
+efla_status check_gated(const efla_gated_shape* s, bool step, efla::GDims* d) {
     if (!s) return fail(EFLA_ERR_INVALID_ARG, "shape is NULL");
     if (s->B < 0 || s->H < 0 || s->Hk < 0 || s->L < 0)
         return fail(EFLA_ERR_INVALID_ARG, "negative size (B=%d H=%d Hk=%d L=%d)", s->B, s->H, s->Hk, s->L);
@@ -588,7 +588,6 @@ efla_status check_gated(const efla_gated_shape* s, bool step, bool bwd, efla::GD
     d->packed = s->packed;
     d->tensor = 0;
     d->offsets = nullptr;
-    (void)bwd;
     return EFLA_OK;
 }
 
@@ -676,13 +675,13 @@ extern "C" {
 // (of the larger path: which one runs also depends on the arrays' alignment)
 size_t efla_gated_fwd_workspace_size(const efla_gated_shape* s) {
     efla::GDims d;
-    if (check_gated(s, false, false, &d) != EFLA_OK) return 0;
+    if (check_gated(s, false, &d) != EFLA_OK) return 0;
     return s->path != EFLA_PATH_SIMT && d.in_bf16 ? efla::gated_tc_fwd_ws_bytes(d) : 0;   // (the fp32 kernel needs none)
 }
 
 size_t efla_gated_bwd_workspace_size(const efla_gated_shape* s) {
     efla::GDims d;
-    if (check_gated(s, false, true, &d) != EFLA_OK) return 0;
+    if (check_gated(s, false, &d) != EFLA_OK) return 0;
     const size_t simt = efla::gated_simt_bwd_ws_bytes(d);
     const size_t tc = s->path != EFLA_PATH_SIMT && efla::gated_tc_supported(d) ? efla::gated_tc_bwd_ws_bytes(d) : 0;
     return tc > simt ? tc : simt;
@@ -694,7 +693,7 @@ efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const 
     NvtxRange nvtx_range("efla_gated_fwd");
     g_msg[0] = 0;
     efla::GDims d;
-    efla_status st = check_gated(s, false, false, &d);
+    efla_status st = check_gated(s, false, &d);
     if (st != EFLA_OK) return st;
     if (d.BH() == 0) return EFLA_OK;
     const GatedIo io = gated_io(s, q, k, v, g, beta, o, nullptr, nullptr, nullptr, nullptr);
@@ -733,7 +732,7 @@ efla_status efla_gated_bwd(const efla_gated_shape* s, const int* offsets, const 
     NvtxRange nvtx_range("efla_gated_bwd");
     g_msg[0] = 0;
     efla::GDims d;
-    efla_status st = check_gated(s, false, true, &d);
+    efla_status st = check_gated(s, false, &d);
     if (st != EFLA_OK) return st;
     if (d.BH() == 0) return EFLA_OK;
     GatedIo io = gated_io(s, q, k, v, g, beta, nullptr, dO, dq, dk, dv);
@@ -773,7 +772,7 @@ efla_status efla_gated_step(const efla_gated_shape* s, const void* q, const void
     NvtxRange nvtx_range("efla_gated_step");
     g_msg[0] = 0;
     efla::GDims d;
-    efla_status st = check_gated(s, true, false, &d);
+    efla_status st = check_gated(s, true, &d);
     if (st != EFLA_OK) return st;
     if (s->path == EFLA_PATH_TENSOR)
         return fail(EFLA_ERR_UNSUPPORTED, "efla_gated_step runs on CUDA cores: path must be AUTO or SIMT");

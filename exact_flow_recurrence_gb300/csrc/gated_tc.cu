@@ -26,7 +26,10 @@ __device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kS
 //      128 rows in the operand layout.
 // Bound by its chain of short dependent steps, not by data: what counts is how many chunks an
 // SM has in flight.  P's parts lie over A and T, and both over the dead tiles, so that four
-// chunks fit (as many as the registers allow).
+// chunks fit (as many as the registers allow).  With three of them an SM a chunk took 11 us from its
+// start: 2.2 us until its tiles were there, 2 us the first product, decays and A, 3.2 us the inverse,
+// 1.8 us T's parts, P T and its parts, 1.8 us the copies out.  4096 chunks (three parts): 101 us, 15% of the DRAM rate (three
+// chunks an SM: 113 us); 2048 (two parts): 48 us.
 struct PrepArgs {
     const float* g;
     const float* beta;
@@ -258,8 +261,15 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
 // both halves of the second product, so that the warps of lanes 64..127, which have no queries
 // here, can write U's record while the others go on with the chain.
 //
-// Bound by the latency of the chain of three products and three epilogues a chunk: see the
-// measurements at launch.
+// Bound by the latency of the chain of three products and three epilogues a chunk, not by data
+// (10 to 30% of the DRAM rate) nor by the tensor pipe (33 to 45% busy).  A chunk of a single chain
+// takes about 2.1 us: 0.6 us of products (D1, D2, D3: 8, 12 and 4 instructions of 43 to 50 cycles),
+// three times 0.11 us from a commit to the wait that sees it, and three epilogues of 0.3 to 0.4 us
+// each (tensor memory to registers, parts to shared memory, the proxy fence).  Twice the epilogue
+// warps with half the columns each change nothing: it is fixed latencies.  Two chains of a CTA
+// overlap: 2.5 us a chunk for both with two parts, 3.3 us with three.  Measured (d 128):
+// B8 H8 L2048 (two parts, 32 chunks) 79 us; B1 H16 L16384 (three parts, one chain a CTA, 256 chunks)
+// 545 us; the recording pass at B4 H16 L4096 (64 chunks) 210 us.
 template <int NP, int NCH, bool REC>
 struct ScanSmem {
     using C = Chain<NP, NCH>;

@@ -236,8 +236,10 @@ inline cudaError_t launch_early(void (*k)(P...), dim3 grid, unsigned threads, si
     return cudaLaunchKernelEx(&cfg, k, std::forward<A>(args)...);
 }
 
-// Whether slices of 32 state columns (instead of 64) still find an SM each: a chunk's products and
-// epilogues shorten with the columns, but every slice loads the keys, queries and images again.
+// Whether slices of 32 state columns (instead of 64) still find an SM each: a chain that shares its
+// CTA with no other takes 2.1 us a chunk, two take 3.3 us (2.5 us with two parts), but twice the CTAs
+// that do not all run at once take twice the time.  L 4096, d 128, final state (three parts): 38 heads,
+// the last that fit narrow slices, 206 us; 39 heads in wide ones 254 us.  Without it (two parts) 159, 194.
 inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
     int dev = 0, nsm = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -247,7 +249,8 @@ inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
 }
 
 // The backward's parts of gated_tc.cu: the preparation (three parts; alpha at least `floor_alpha`
-// in magnitude), and the pass that records S [H][slots][dk][dv] and U [H][slots][64][dv] (fp32).
+// in magnitude), and the pass that records every chunk's S and U as parts, in the operand layout
+// ([H][slots][slices of 64 columns][kRecS or kRecU bytes]).
 cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
                                  float floor_alpha, unsigned char* img, GVec* vec, cudaStream_t st);
 cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,

@@ -13,7 +13,10 @@
 // Rows arrive by bulk copies into a ring of shared memory, several ahead: what an SM has in flight
 // then costs no registers.  Rows that are not 16-byte aligned are loaded element by element.
 // A second kernel adds the CTAs' partial sums in a fixed order, so that results do not depend on
-// the order in which CTAs finish.
+// the order in which CTAs finish; it is launched while the first one ends.
+// 16384 x 2048 bf16: forward 22.7 to 24.6 us (134 MB: 5.5 to 5.9 TB/s; a plain copy's rate would take
+// 19.8 us), backward 42 to 45 us (201 MB, 4.5 to 4.8 TB/s; 29.7 us), of which 38 us the rows and the
+// rest the sums over CTAs.  2047 columns, element by element: 36 and 56 us.  4 x 1024: 2.7 us, a launch.
 #include "common.cuh"
 #include "gated.h"
 #include "launch.h"

@@ -247,7 +247,9 @@ efla_status efla_fwd_noalloc(const efla_shape* shape,
  *
  * Rules as in the conventions above, except that these arrays need only the alignment of their
  * elements (states, workspace, dg and dbeta: 16 bytes): 16-byte aligned bf16 arrays with
- * strides that are multiples of 8 elements run on the tensor cores, others on the fp32 cores. */
+ * strides that are multiples of 8 elements run on the tensor cores, others on the fp32 cores.
+ * EFLA_PATH_AUTO also takes the fp32 cores for forward passes of at most 32 tokens while they
+ * are the faster ones; the workspace size does not depend on that choice. */
 typedef struct {
     int B, H, Hk, L, dk, dv;    /* dk, dv: multiples of 16 in [16, 128]; H, Hk: value, key heads */
     efla_dtype dtype;           /* q, k, v, dO */
