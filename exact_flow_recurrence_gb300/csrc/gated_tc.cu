@@ -30,6 +30,8 @@ __device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kS
 // start: 2.2 us until its tiles were there, 2 us the first product, decays and A, 3.2 us the inverse,
 // 1.8 us T's parts, P T and its parts, 1.8 us the copies out.  4096 chunks (three parts): 101 us, 15% of the DRAM rate (three
 // chunks an SM: 113 us); 2048 (two parts): 48 us.
+constexpr uint32_t kPolls = 1u << 22;   // of a chunk's flag, at 32 ns or more each
+
 struct PrepArgs {
     const float* g;
     const float* beta;
@@ -48,32 +50,23 @@ struct PrepSmem {
     static constexpr size_t bytes = 1024 + BAR + 64;
 };
 
+// One chunk, by four warps (named barrier `bid`) whose bars[0..2] count phases `ph` and whose 64 columns
+// of tensor memory are at *tslot (valid after the first barrier).  `flag`: set once the results are in global memory.
 template <int NP>
-__global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
-                                                    const __grid_constant__ CUtensorMap tm_k) {
+__device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
+                           unsigned char* sm, int bid, int tid, int slot, int h, const SeqAt& s, uint32_t ph,
+                           const uint32_t* tslot, int* flag) {
     using M = PrepSmem<NP>;
-    extern __shared__ unsigned char raw[];
-    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    const int slot = blockIdx.x, h = blockIdx.y, hk = h / (d.H / d.Hk), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = seq_of_slot(d, slot, kGC);
-    const SeqAt s = seq_at(d, b, kGC);
+    const int hk = h / (d.H / d.Hk), warp = tid >> 5, lane = tid & 31;
     const int t0 = (slot - s.slot0) * kGC, n = min(kGC, s.len - t0), t = s.start + t0;
-    if (n <= 0) return;
     uint64_t* bar = (uint64_t*)(sm + M::BAR);
-    uint32_t* tslot = (uint32_t*)(bar + 3);
     GVec* vec = (GVec*)(sm + M::VEC);
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
-        fence_mbar_init();
         mbar_arrive_expect_tx(&bar[0], 4u * 8192u);
         for (int blk = 0; blk < 2; ++blk) {
-            tma_load_4d(sm + blk * 16384, &tm_k, 64 * blk, t, hk, s.batch, &bar[0]);
-            tma_load_4d(sm + blk * 16384 + 8192, &tm_q, 64 * blk, t, hk, s.batch, &bar[0]);
+            tma_load_4d(sm + blk * 16384, tm_k, 64 * blk, t, hk, s.batch, &bar[0]);
+            tma_load_4d(sm + blk * 16384 + 8192, tm_q, 64 * blk, t, hk, s.batch, &bar[0]);
         }
-    }
-    if (warp == 0) {
-        tmem_alloc(tslot, 64);
-        tmem_relinquish();
     }
     if (warp == 1) {   // sums of the log decays (two tokens a lane), in fp64 until they are two floats
         const int i0 = 2 * lane;
@@ -98,12 +91,12 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
     }
     const float beta = tid < n ? a.beta[at3(d.bs, s.batch, h, t + tid)] : 0.f;
     tc_fence_before();
-    __syncthreads();
-    griddep_launch_dependents();   // (the scan's CTAs come as SMs run empty)
+    group_sync(bid);
+    if (!flag) griddep_launch_dependents();   // (the scan's CTAs come as SMs run empty)
     tc_fence_after();
     const uint32_t tb = *tslot;
     if (warp == 0) {
-        if (warp_wait(&bar[0], 0)) {
+        if (warp_wait(&bar[0], ph)) {
             const uint64_t x = sdesc_sw128(smem_u32(sm));
             if (elect_one()) {
 #pragma unroll 1
@@ -116,14 +109,14 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
             }
         } else if (lane == 0) {
             atomicOr(&g_gt2_status, 1u);
-            mbar_wait(&bar[0], 0, kWaitLimit);   // let the copies land
+            mbar_wait(&bar[0], ph, kWaitLimit);   // let the copies land
         }
         __syncwarp();
     }
     const size_t rec = (size_t)h * a.slots + slot, all = (size_t)d.H * a.slots;
     unsigned char* const out = a.img + rec * NP * 16384;
     const bool out_ok = dbg_in(out, NP * 16384, a.img, all * NP * 16384, &g_gt2_status);
-    bool ok = __syncthreads_and(mbar_wait(&bar[1], 0, kWaitLimit));
+    bool ok = group_sync_and(bid, mbar_wait(&bar[1], ph, kWaitLimit));
     tc_fence_after();
     float* T = (float*)(sm + M::P);
     if (ok) {
@@ -175,8 +168,8 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
                 *reinterpret_cast<float4*>(T + i * kLdA + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
         tc_fence_before();
-        group_sync(1);
-        unit_lower_inverse64(T, T, (float*)(sm + M::T), 1, tid);
+        group_sync(bid);
+        unit_lower_inverse64(T, T, (float*)(sm + M::T), bid, tid);
         {   // T's parts, 32 columns a thread (zero above its 16x16 diagonal blocks)
             const int r = tid >> 1, h0 = 32 * (tid & 1);
 #pragma unroll
@@ -194,13 +187,13 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
             }
         }
         fence_async_smem();
-        group_sync(1);
+        group_sync(bid);
         if (tid == 0 && out_ok)
             for (int p = 0; p < NP; ++p) bulk_s2g(out + p * 16384, sm + M::T + p * 8192, 8192);
         if (tid >= 64) put_row(v);
         fence_async_smem();
         tc_fence_before();
-        group_sync(1);
+        group_sync(bid);
         if (warp == 0 && elect_one()) {   // P T, the part pairs p + x < NP (B: T's rows are K indices; rows 64..127 of A
             tc_fence_after();             // are what follows P's tiles, and not used)
             const uint64_t da = sdesc_sw128(smem_u32(sm + M::P)), db = sdesc_sw128(smem_u32(sm + M::T));
@@ -214,7 +207,7 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
                                    !(p == NP - 1 && x == 0 && ks == 0));
             mma_commit(&bar[2]);
         }
-        ok = group_sync_and(1, mbar_wait(&bar[2], 0, kWaitLimit));
+        ok = group_sync_and(bid, mbar_wait(&bar[2], ph, kWaitLimit));
         tc_fence_after();
         if (tid < 64 && ok) {
 #pragma unroll
@@ -230,10 +223,10 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
     }
     if (!ok) {
         atomicOr(&g_gt2_status, 1u);
-        mbar_wait(&bar[1], 0, kWaitLimit);   // (products still in flight end before their tensor memory is freed)
-        mbar_wait(&bar[2], 0, kWaitLimit);
+        mbar_wait(&bar[1], ph, kWaitLimit);   // (products still in flight end before their tensor memory is freed)
+        mbar_wait(&bar[2], ph, kWaitLimit);
     }
-    __syncthreads();
+    group_sync(bid);
     tc_fence_after();
     if (tid == 0 && ok) {
         if (out_ok)
@@ -243,9 +236,38 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
     }
     if (tid == 0) {   // (T's parts are on their way even if a wait has given up since)
         bulk_commit();
-        bulk_wait_read();
+        if (flag && ok) {
+            bulk_wait_all();
+            fence_proxy_async_global();
+            st_release_gpu(flag, 1);
+        } else {
+            bulk_wait_read();
+        }
     }
-    if (warp == 0) tmem_dealloc(tb, 64);
+    return ok;
+}
+
+template <int NP>
+__global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
+                                                    const __grid_constant__ CUtensorMap tm_k) {
+    using M = PrepSmem<NP>;
+    extern __shared__ unsigned char raw[];
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    const int slot = blockIdx.x, tid = threadIdx.x;
+    const SeqAt s = seq_at(d, seq_of_slot(d, slot, kGC), kGC);
+    if ((slot - s.slot0) * kGC >= s.len) return;
+    uint64_t* bar = (uint64_t*)(sm + M::BAR);
+    uint32_t* tslot = (uint32_t*)(bar + 3);
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+        fence_mbar_init();
+    }
+    if (tid < 32) {
+        tmem_alloc(tslot, 64);
+        tmem_relinquish();
+    }
+    prep_chunk<NP>(d, a, &tm_q, &tm_k, sm, 1, tid, slot, blockIdx.y, s, 0, tslot, nullptr);
+    if (tid < 32) tmem_dealloc(*tslot, 64);
 }
 
 // ------------------------------------------------------------------ forward scan
@@ -286,9 +308,8 @@ struct ScanSmem {
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
     static constexpr int bars = 4 + 2 + TPS + 1 + 9 * NCH;   // (per chain: 7, and its turn)
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
-    // a chain's epilogue warps: a thread has one row and CW of the 32 columns (8 leave a single chain's
-    // epilogues half as long; two chains keep the issue slots busier and would need 34 warps)
-    static constexpr int CW = NCH == 1 ? 8 : 16;
+    // a chain's epilogue warps: a thread has one row and CW of the 32 columns (8 columns: the same times)
+    static constexpr int CW = 16;
     static constexpr int EW = 4 * 32 / CW;
     static constexpr int MW = NCH * EW;                      // first product warp
     static constexpr int IW = MW + NCH;                      // copies in, and (REC) out
@@ -306,12 +327,13 @@ struct ScanArgs {
     int slots;
     unsigned char* rec_S;   // [H][slots][slices][kRecS]
     unsigned char* rec_U;   // [H][slots][slices][kRecU]
+    const int* flags;       // [H][slots], or null: set as the chunks' preparations are complete
 };
 
+// bx: sequence and value head; by: slice (of `slices`)
 template <int NP, int NCH, typename Tout, bool REC>
-__global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
-    k_gt_scan(GDims d, ScanArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_v) {
+__device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                         const CUtensorMap& tm_v, int bx, int by, int slices) {
     using M = ScanSmem<NP, NCH, REC>;
     using C = Chain<NP, NCH>;
     extern __shared__ unsigned char raw[];
@@ -325,7 +347,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
     uint64_t* u_free = s_free + 1;
     uint64_t* chain0 = u_free + 1;       // per chain: s_ready, x_ready, u_ready, r_ready (REC: U's parts), d1, d2, d3, turn
     uint32_t* tslot = (uint32_t*)(bars + M::bars);
-    const int b = blockIdx.x / d.H, h = blockIdx.x % d.H, hk = h / (d.H / d.Hk), c0 = blockIdx.y * 32 * NCH;
+    const int b = bx / d.H, h = bx % d.H, hk = h / (d.H / d.Hk), c0 = by * 32 * NCH;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SeqAt s = seq_at(d, b, kGC);
     const int nch = (s.len + kGC - 1) / kGC;
@@ -357,7 +379,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = *tslot;
-    griddep_wait();                             // the preparation is complete
+    if (!a.flags) griddep_wait();               // the preparation is complete
     if (REC) griddep_launch_dependents();       // the reverse scan needs it too, but nothing of this kernel's
 
     if (warp >= M::MW) {
@@ -366,6 +388,14 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
             if (warp == M::IW) {
                 // ---------------- copies in
                 int n_kq = 0, n_tp = 0;   // chunks whose copies are under way
+                const auto prepared = [&](int c) {   // (chunk 0 with patience: its preparation starts as this does)
+                    if (!a.flags) return true;
+                    const int* f = a.flags + rec0 + c;
+                    uint32_t n = 0;
+                    while (ld_acquire_gpu(f) == 0 && ++n < kPolls) __nanosleep(32);
+                    fence_proxy_async_global();
+                    return n < kPolls;
+                };
                 const auto load = [&](int c) {
                     unsigned char* kq = sm + M::KQ + (c & 1) * 2 * M::KQB;
                     uint64_t* f = &full[c & 1];
@@ -391,9 +421,12 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     }
                     n_tp = c + 1;
                 };
-                load(0);
-                load_tp(0);
-                if (nch > 1) {
+                ok = prepared(0);
+                if (ok) {
+                    load(0);
+                    load_tp(0);
+                }
+                if (ok && nch > 1 && (ok = prepared(1))) {
                     load(1);
                     if (M::TPS == 2) load_tp(1);
                 }
@@ -404,6 +437,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     }
                     if (ok && c + 2 < nch) {
                         ok = mbar_wait(&freed[c & 1], (c >> 1) & 1, kWaitLimit);
+                        ok = ok && prepared(c + 2);
                         if (!ok) break;
                         load(c + 2);
                         if (M::TPS == 2) load_tp(c + 2);
@@ -421,7 +455,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     const uint32_t ph = c & 1;
                     for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g, ph, kWaitLimit);
                     if (!ok) break;
-                    unsigned char* const to_S = a.rec_S + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecS;
+                    unsigned char* const to_S = a.rec_S + ((rec0 + c) * slices + by) * kRecS;
                     if (dbg_in(to_S, kRecS, a.rec_S, records(d, a.slots, kRecS), &g_gt2_status)) bulk_s2g(to_S, sm + M::S, kRecS);
                     bulk_commit();
                     bulk_wait_read();   // (and the U of the chunk before)
@@ -429,7 +463,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
                     if (c > 0) mbar_arrive(u_free);
                     for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g + 3, ph, kWaitLimit);
                     if (!ok) break;
-                    unsigned char* const to_U = a.rec_U + ((rec0 + c) * gridDim.y + blockIdx.y) * kRecU;
+                    unsigned char* const to_U = a.rec_U + ((rec0 + c) * slices + by) * kRecU;
                     if (dbg_in(to_U, kRecU, a.rec_U, records(d, a.slots, kRecU), &g_gt2_status)) bulk_s2g(to_U, sm + M::U, kRecU);
                     bulk_commit();
                 }
@@ -495,7 +529,7 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
         const bool top = row < 64, in = col < d.dv;
         uint64_t* q = chain0 + 9 * g;
         const uint32_t lq = taddr(tb, 32 * (warp & 3), g * 256 + cc), t1 = lq, t2 = lq + 128, t3 = lq;
-        const size_t sb = ((size_t)blockIdx.x * d.dk + row) * d.dv + col;
+        const size_t sb = ((size_t)bx * d.dk + row) * d.dv + col;
         float2 S[CW / 2];
 #pragma unroll
         for (int e = 0; e < CW / 2; e += 2) {
@@ -583,6 +617,73 @@ __global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
     if (warp == M::MW) tmem_dealloc(tb, NCH * 256);
 }
 
+template <int NP, int NCH, typename Tout, bool REC>
+__global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
+    k_gt_scan(GDims d, ScanArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v) {
+    scan_cta<NP, NCH, Tout, REC>(d, a, tm_q, tm_k, tm_v, blockIdx.x, blockIdx.y, gridDim.y);
+}
+
+// ------------------------------------------------------------------ few heads, many chunks
+// The scan's CTAs and, on the other SMs, the chunks' preparation, in one cooperative launch (all CTAs run
+// at once, which makes waiting for their flags safe).  Three groups of four warps a preparing CTA take the
+// chunks in the order in which the scans come to them.
+template <int NP>
+struct LongSmem {
+    static constexpr int groups = 3, threads = 128 * groups;
+    static constexpr size_t group = PrepSmem<NP>::bytes / 1024 * 1024 + 1024;
+    static constexpr size_t scan = ScanSmem<NP, 1, false>::bytes;
+    static constexpr size_t bytes = groups * group > scan ? groups * group : scan;
+};
+
+template <int NP, typename Tout>
+__global__ void __launch_bounds__(LongSmem<NP>::threads, 1)
+    k_gt_long(GDims d, PrepArgs p, ScanArgs a, int* flags, int slices, const __grid_constant__ CUtensorMap tm_q,
+              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    static_assert(ScanSmem<NP, 1, false>::warps * 32 <= LongSmem<NP>::threads, "the scan's warps");
+    const int bh = d.B * d.H, nscan = bh * slices;
+    if ((int)blockIdx.x < nscan) {
+        scan_cta<NP, 1, Tout, false>(d, a, tm_q, tm_k, tm_v, blockIdx.x % bh, blockIdx.x / bh, slices);
+        return;
+    }
+    using M = PrepSmem<NP>;
+    extern __shared__ unsigned char raw[];
+    const int gid = threadIdx.x >> 7, tid = threadIdx.x & 127;
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023) + gid * LongSmem<NP>::group;
+    uint64_t* bar = (uint64_t*)(sm + M::BAR);
+    uint32_t* tslot = (uint32_t*)(bar + 3);
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+        fence_mbar_init();
+    }
+    uint32_t* const base = (uint32_t*)(sm - gid * LongSmem<NP>::group + M::BAR) + 8;   // (past the first group's barriers and slot)
+    if (threadIdx.x < 32) {   // for all groups (no allocation may follow the relinquishing)
+        tmem_alloc(base, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0) *tslot = *base + gid * 64;
+    const long long items = (long long)((d.L + kGC - 1) / kGC) * bh;
+    bool ok = true;
+    uint32_t ph = 0;
+    for (long long x = (long long)(blockIdx.x - nscan) * LongSmem<NP>::groups + gid; x < items && ok;
+         x += (long long)(gridDim.x - nscan) * LongSmem<NP>::groups) {
+        const int c = (int)(x / bh), b = (int)(x % bh) / d.H, h = (int)(x % bh) % d.H;
+        const SeqAt s = seq_at(d, b, kGC);
+        if (c * kGC >= s.len) continue;
+        const int slot = s.slot0 + c;
+        ok = prep_chunk<NP>(d, p, &tm_q, &tm_k, sm, 1 + gid, tid, slot, h, s, ph, tslot, flags + (size_t)h * p.slots + slot);
+        ph ^= 1;
+        group_sync(1 + gid);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x < 32) tmem_dealloc(*base, 256);
+}
+
 struct TcWs {
     unsigned char* img;
     GVec* vec;
@@ -595,8 +696,12 @@ size_t carve(const GDims& d, int np, void* base, TcWs* w) {
     p += align256(n * np * 16384);
     w->vec = (GVec*)p;
     p += align256(n * sizeof(GVec));
+    p += align256(n * sizeof(int));
     return (size_t)(p - (char*)base);
 }
+
+// Flags of the joint launch, behind the images and vectors.
+int* flags_of(const GDims& d, const TcWs& w) { return (int*)((char*)w.vec + align256((size_t)d.H * d.slots(kGC) * sizeof(GVec))); }
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -631,6 +736,20 @@ cudaError_t prep(const GDims& d, const PrepArgs& a, const Maps& m, cudaStream_t 
     return cudaGetLastError();
 }
 
+// Whether preparation and scan go in one launch (*nsm: its CTAs, else 0): where the scan leaves a third of the
+// SMs to the preparation, which takes about 4 us a chunk and SM where the scan takes 2 us a chunk, and the
+// chunks are many enough to pay for the launch.
+cudaError_t long_form(const GDims& d, bool narrow, int* nsm) {
+    int dev = 0, n = 0;
+    const long long scan = d.BH() * ((d.dv + 31) / 32);
+    *nsm = 0;
+    if (!narrow || d.L < 16 * kGC) return cudaSuccess;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && 3 * scan <= 2 * n) *nsm = n;
+    return e;
+}
+
 template <int NP, typename Tout>
 cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, const float* g, const float* beta,
                 const float* S0, void* o, float* S_final, void* ws, cudaStream_t st) {
@@ -641,9 +760,32 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
     bool narrow = false;
     cudaError_t e = make_maps(d, q, k, v, &m);
     if (e == cudaSuccess) e = narrow_slices(d, &narrow);
+    int nsm = 0;
+    if (e == cudaSuccess) e = long_form(d, narrow, &nsm);
+    if (e == cudaSuccess && nsm) {
+        const auto k = k_gt_long<NP, Tout>;
+        if ((e = smem_attr(k, LongSmem<NP>::bytes)) != cudaSuccess) return e;
+        int* flags = flags_of(d, w);
+        if ((e = cudaMemsetAsync(flags, 0, (size_t)d.H * slots * sizeof(int), st)) != cudaSuccess) return e;
+        cudaLaunchAttribute coop{};
+        coop.id = cudaLaunchAttributeCooperative;
+        coop.val.cooperative = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(nsm);
+        cfg.blockDim = dim3(LongSmem<NP>::threads);
+        cfg.dynamicSmemBytes = LongSmem<NP>::bytes;
+        cfg.stream = st;
+        cfg.attrs = &coop;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, k, d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f},
+                               ScanArgs{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr, flags}, flags, (d.dv + 31) / 32,
+                               m.q, m.k, m.v);
+        prof_mark("gated_long_tc", st);
+        return e;
+    }
     if (e == cudaSuccess) e = prep<NP>(d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f}, m, st);
     if (e != cudaSuccess) return e;
-    const ScanArgs a{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr};
+    const ScanArgs a{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr, nullptr};
     return narrow ? scan<NP, 1, Tout>(d, a, m, st) : scan<NP, 2, Tout>(d, a, m, st);
 }
 
@@ -681,7 +823,7 @@ cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k,
     Maps m{};
     const cudaError_t e = make_maps(d, q, k, v, &m);
     if (e != cudaSuccess) return e;
-    return scan<3, 2, float, true>(d, ScanArgs{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U}, m, st);
+    return scan<3, 2, float, true>(d, ScanArgs{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U, nullptr}, m, st);
 }
 
 cudaError_t gated_tc_status_read_clear(unsigned int* status) {
