@@ -736,14 +736,18 @@ cudaError_t prep(const GDims& d, const PrepArgs& a, const Maps& m, cudaStream_t 
     return cudaGetLastError();
 }
 
-// Whether preparation and scan go in one launch (*nsm: its CTAs, else 0): where the scan leaves a third of the
-// SMs to the preparation, which takes about 4 us a chunk and SM where the scan takes 2 us a chunk, and the
-// chunks are many enough to pay for the launch.
+// Whether preparation and scan go in one launch (*nsm: its CTAs, else 0).  Two kernels: the preparation takes
+// 4 us a chunk and SM on all of them, then the scan starts.  One: it starts with the first chunk, 9 us
+// later than it could (the flags, the launch, a chunk's preparation on its own), and the rest costs nothing
+// as long as the scan leaves a third of the SMs.  In us, two kernels first, d 128, with / without the final state:
+//   H 8 L 4096 (512 chunks of a head)  161, 155 / 122, 125      H 16 L 4096 (1024)  174, 156 / 132, 127
+//   H 25 L 1024 (400)                   52, 54 /  41, 45        H 25 L 2048 (800)    94, 90 /  76, 74
+//   H 16 L 16384 (4096)                684, 563 (with)
 cudaError_t long_form(const GDims& d, bool narrow, int* nsm) {
     int dev = 0, n = 0;
     const long long scan = d.BH() * ((d.dv + 31) / 32);
     *nsm = 0;
-    if (!narrow || d.L < 16 * kGC) return cudaSuccess;
+    if (!narrow || (long long)d.H * d.slots(kGC) < 640) return cudaSuccess;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess && 3 * scan <= 2 * n) *nsm = n;

@@ -1,5 +1,5 @@
 """The gated rule's forward forms that the other tests' sizes do not reach: preparation and scan in one
-launch (few heads, at least 16 chunks), the tensor cores on a few tokens, and the recurrence past its rule.
+launch (few heads, at least 640 chunks of a head in all), the tensor cores on a few tokens, and the recurrence past its rule.
 Bounds as in test_gated."""
 import pytest
 import torch
@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("mode", [efla.EULER, efla.EXACT])
-@pytest.mark.parametrize("shape", [(1, 3, 3, 1024, 128, 128), (2, 2, 1, 1151, 64, 80), (1, 1, 1, 2100, 128, 32)])
+@pytest.mark.parametrize("shape", [(1, 20, 20, 2100, 128, 128), (2, 20, 10, 1151, 64, 64), (1, 48, 48, 1000, 112, 32)])
 def test_one_launch(shape, mode):
     x = draw(*shape, BF, mode, rate=0.05, seed=11, token_first=True)
     want = (og.fwd(*(x[n].double() for n in ("q", "k", "v", "g", "beta", "S0")), exact=mode == efla.EXACT), None)
@@ -29,12 +29,12 @@ def test_one_launch(shape, mode):
 
 def test_one_launch_packed_and_repeated():
     """Sequences of unequal lengths, one empty; the same call twice and in a graph gives the same bits."""
-    ends = [0, 700, 700, 701, 1900]
-    x = draw(1, 2, 2, 1900, 128, 64, BF, efla.EULER, rate=0.05, seed=12)
+    ends = [0, 700, 700, 701, 2400]
+    x = draw(1, 16, 8, 2400, 128, 32, BF, efla.EULER, rate=0.05, seed=12)
     y = {n: t[0] for n, t in gpu(x).items()}
     off = torch.tensor(ends, dtype=torch.int32, device=DEV)
     gen = torch.Generator().manual_seed(13)
-    S0 = torch.randn(4, 2, 128, 64, generator=gen).to(DEV)
+    S0 = torch.randn(4, 16, 128, 32, generator=gen).to(DEV)
     args = [y[n] for n in ("q", "k", "v", "g", "beta")]
     o, S = efla.efla_gated_fwd(*args, S0, offsets=off, out_dtype=F32)
     efla.efla_get_status()
