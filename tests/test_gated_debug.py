@@ -27,7 +27,8 @@ def _draw(B, H, Hk, L, dk, dv, packed, seed=0):
     return q, k, v, g, beta, dO, S0, dS, off if packed else None
 
 
-@pytest.mark.parametrize("sizes", [(2, 4, 2, 200, 128, 128, False), (3, 2, 2, 333, 64, 96, True), (1, 80, 80, 130, 48, 64, False)])
+@pytest.mark.parametrize("sizes", [(2, 4, 2, 200, 128, 128, False), (3, 2, 2, 333, 64, 96, True), (1, 80, 80, 130, 48, 64, False),
+                                   (1, 20, 10, 2100, 128, 128, False)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 def test_gated(libs, sizes, out):  # noqa: F811
     q, k, v, g, beta, dO, S0, dS, off = _draw(*sizes)
