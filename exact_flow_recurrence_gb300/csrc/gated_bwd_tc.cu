@@ -29,7 +29,6 @@ namespace {
 
 __device__ unsigned int g_gb_status = 0;   // bit 0: a bounded wait expired; kStatusBounds (debug builds): a write was skipped
 
-constexpr int NP = 3;
 constexpr float kFloorAlpha = 1e-25f;
 
 // ------------------------------------------------------------------ reverse scan
@@ -43,7 +42,7 @@ constexpr float kFloorAlpha = 1e-25f;
 // would hold up the load-store unit for everyone).  Bound as k_gt_scan by its chain: 64 chunks in
 // 264 us at B4 H16 L4096 d 128, the tensor pipe 52% and DRAM 38% busy.
 struct Rs {
-    using C = Chain<NP, 2>;
+    using C = Chain<2>;
     static constexpr uint32_t K = 0;                      // 2 stages x 2 blocks of 64 dk
     static constexpr uint32_t Q = 32768;                  // 2 blocks
     static constexpr uint32_t DO = Q + 16384;
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                 if (!(ok = warp_wait(q + 5, ph))) break;
                 tmem_sum<NP + 1>(t2, 32, y);
                 if (it > 0 && !(ok = warp_wait(r_free, ph ^ 1u))) break;
-                put_parts<NP>(sm + M::R, i, g * 32 + cc, y);
+                put_parts(sm + M::R, i, g * 32 + cc, y);
                 warp_arrive(q + 8, lane);
                 if (live && in) {
                     Tout* vp = (Tout*)a.dv + at3(d.dvs, s.batch, h, s.start + c * kGC + i) + col;
@@ -383,7 +382,7 @@ constexpr int kGrWarps = 10;
 constexpr uint32_t kGrQK = 0;                    // 2 blocks of 64 dk x [Q rows | K rows]
 constexpr uint32_t kGrAX = 32768;                // dO | dX_0 | 0 | dX_1 | 0 | dX_2, tiles of 64 rows
 constexpr uint32_t kGrU = kGrAX + 49152;         // U_0 | U_1 | U_2 (as an A operand, the tile before fills rows 0..63)
-constexpr uint32_t kGrS = kGrU + 24576;          // 3 blocks of 128 rows: Chain<3, 2>
+constexpr uint32_t kGrS = kGrU + 24576;          // 3 blocks of 128 rows: Chain<2>
 constexpr uint32_t kGrG = kGrS + 49152;          // likewise
 constexpr uint32_t kGrP5 = kGrS;                 // [dPD; dAD], two parts, in S's place
 constexpr uint32_t kGrMisc = kGrG + 49152;
@@ -463,8 +462,8 @@ __device__ __forceinline__ float inner256(const unsigned char* S, const unsigned
     return w.x + w.y;
 }
 
-// Descriptor advance (16-byte units) to part p of column group g in blocks of `blk` bytes: Chain<3, 2>.
-__host__ __device__ constexpr uint32_t at_part(int g, int p, uint32_t blk) { return Chain<3, 2>::part(g, p, blk) >> 4; }
+// Descriptor advance (16-byte units) to part p of column group g in blocks of `blk` bytes: Chain<2>.
+__host__ __device__ constexpr uint32_t at_part(int g, int p, uint32_t blk) { return Chain<2>::part(g, p, blk) >> 4; }
 
 template <typename Tout>
 __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs a, const __grid_constant__ CUtensorMap tm_q,

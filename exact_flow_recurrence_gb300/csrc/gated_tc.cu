@@ -28,8 +28,8 @@ __device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kS
 // SM has in flight.  P's parts lie over A and T, and both over the dead tiles, so that four
 // chunks fit (as many as the registers allow).  With three of them an SM a chunk took 11 us from its
 // start: 2.2 us until its tiles were there, 2 us the first product, decays and A, 3.2 us the inverse,
-// 1.8 us T's parts, P T and its parts, 1.8 us the copies out.  4096 chunks (three parts): 101 us, 15% of the DRAM rate (three
-// chunks an SM: 113 us); 2048 (two parts): 48 us.
+// 1.8 us T's parts, P T and its parts, 1.8 us the copies out.  4096 chunks: 101 us, 15% of the DRAM rate (three
+// chunks an SM: 113 us).
 constexpr uint32_t kPolls = 1u << 22;   // of a chunk's flag, at 32 ns or more each
 
 struct PrepArgs {
@@ -41,10 +41,9 @@ struct PrepArgs {
     float floor_alpha;    // |alpha| below this is taken as it (0: as it is)
 };
 
-template <int NP>
 struct PrepSmem {
     static constexpr uint32_t P = 0;               // NP tiles of 64 rows; [64][kLdA] fp32 before (and the K, Q tiles first)
-    static constexpr uint32_t T = NP == 2 ? 64 * kLdA * 4 / 1024 * 1024 + 1024 : NP * 8192;   // NP tiles; the inverse's scratch before
+    static constexpr uint32_t T = NP * 8192;       // NP tiles; the inverse's scratch before
     static constexpr uint32_t VEC = T + NP * 8192;
     static constexpr uint32_t BAR = VEC + sizeof(GVec);
     static constexpr size_t bytes = 1024 + BAR + 64;
@@ -52,11 +51,10 @@ struct PrepSmem {
 
 // One chunk, by four warps (named barrier `bid`) whose bars[0..2] count phases `ph` and whose 64 columns
 // of tensor memory are at *tslot (valid after the first barrier).  `flag`: set once the results are in global memory.
-template <int NP>
 __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                            unsigned char* sm, int bid, int tid, int slot, int h, const SeqAt& s, uint32_t ph,
                            const uint32_t* tslot, int* flag) {
-    using M = PrepSmem<NP>;
+    using M = PrepSmem;
     const int hk = h / (d.H / d.Hk), warp = tid >> 5, lane = tid & 31;
     const int t0 = (slot - s.slot0) * kGC, n = min(kGC, s.len - t0), t = s.start + t0;
     uint64_t* bar = (uint64_t*)(sm + M::BAR);
@@ -247,10 +245,9 @@ __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap*
     return ok;
 }
 
-template <int NP>
 __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
                                                     const __grid_constant__ CUtensorMap tm_k) {
-    using M = PrepSmem<NP>;
+    using M = PrepSmem;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int slot = blockIdx.x, tid = threadIdx.x;
@@ -266,7 +263,7 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
         tmem_alloc(tslot, 64);
         tmem_relinquish();
     }
-    prep_chunk<NP>(d, a, &tm_q, &tm_k, sm, 1, tid, slot, blockIdx.y, s, 0, tslot, nullptr);
+    prep_chunk(d, a, &tm_q, &tm_k, sm, 1, tid, slot, blockIdx.y, s, 0, tslot, nullptr);
     if (tid < 32) tmem_dealloc(*tslot, 64);
 }
 
@@ -289,24 +286,23 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
 // three times 0.11 us from a commit to the wait that sees it, and three epilogues of 0.3 to 0.4 us
 // each (tensor memory to registers, parts to shared memory, the proxy fence).  Twice the epilogue
 // warps with half the columns each change nothing: it is fixed latencies.  Two chains of a CTA
-// overlap: 2.5 us a chunk for both with two parts, 3.3 us with three.  Measured (d 128):
-// B8 H8 L2048 (two parts, 32 chunks) 79 us; B1 H16 L16384 (three parts, one chain a CTA, 256 chunks)
-// 545 us; the recording pass at B4 H16 L4096 (64 chunks) 210 us.
-template <int NP, int NCH, bool REC>
+// overlap: 3.3 us a chunk for both.  Measured (d 128): B8 H8 L2048 (32 chunks) 151 us with its
+// preparation; B1 H16 L16384 (one chain a CTA, 256 chunks) 545 us; the recording pass at B4 H16
+// L4096 (64 chunks) 210 us.
+template <int NCH, bool REC>
 struct ScanSmem {
-    using C = Chain<NP, NCH>;
-    static constexpr int TPS = NP == 2 ? 2 : 1;                      // stages of the image
+    using C = Chain<NCH>;
     static constexpr uint32_t KQB = REC ? 8192 : 16384;              // a 64-dk block: K rows (and Q rows)
     static constexpr uint32_t TPB = 16384;                           // an image part: T rows, P T rows (REC: T's again)
     static constexpr uint32_t KQ = 0;                                // 2 stages x 2 blocks
     static constexpr uint32_t TP = 4 * KQB;
-    static constexpr uint32_t V = TP + TPS * NP * TPB;               // 2 stages
+    static constexpr uint32_t V = TP + NP * TPB;                     // 2 stages
     static constexpr uint32_t S = V + 2 * 8192;                      // blocks of 128 rows
     static constexpr uint32_t X = S + C::blocks * 16384;             // blocks of 64 rows
     static constexpr uint32_t U = X + C::blocks * 8192;              // REC: a tile of 64 rows a part
     static constexpr uint32_t VEC = U + (REC ? C::blocks * 8192 : 0);   // 2 stages
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
-    static constexpr int bars = 4 + 2 + TPS + 1 + 9 * NCH;   // (per chain: 7, and its turn)
+    static constexpr int bars = 4 + 2 + 1 + 1 + 9 * NCH;   // (per chain: 7, and its turn)
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
     // a chain's epilogue warps: a thread has one row and CW of the 32 columns (8 columns: the same times)
     static constexpr int CW = 16;
@@ -315,8 +311,7 @@ struct ScanSmem {
     static constexpr int IW = MW + NCH;                      // copies in, and (REC) out
     static constexpr int warps = IW + 1 + (REC ? 1 : 0);
 };
-static_assert(ScanSmem<2, 2, false>::bytes <= 232448 && ScanSmem<3, 2, false>::bytes <= 232448 &&
-              ScanSmem<3, 2, true>::bytes <= 232448, "shared memory per CTA");
+static_assert(ScanSmem<2, false>::bytes <= 232448 && ScanSmem<2, true>::bytes <= 232448, "shared memory per CTA");
 
 struct ScanArgs {
     const unsigned char* img;
@@ -331,18 +326,18 @@ struct ScanArgs {
 };
 
 // bx: sequence and value head; by: slice (of `slices`)
-template <int NP, int NCH, typename Tout, bool REC>
+template <int NCH, typename Tout, bool REC>
 __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                          const CUtensorMap& tm_v, int bx, int by, int slices) {
-    using M = ScanSmem<NP, NCH, REC>;
-    using C = Chain<NP, NCH>;
+    using M = ScanSmem<NCH, REC>;
+    using C = Chain<NCH>;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = (uint64_t*)(sm + M::BAR);
     uint64_t* full = bars;               // [2] K, Q, V, vectors
     uint64_t* freed = bars + 2;          // [2] by every chain
-    uint64_t* full_tp = bars + 4;        // [TPS]
-    uint64_t* freed_tp = full_tp + M::TPS;   // by every chain (one stage only)
+    uint64_t* full_tp = bars + 4;        // the image
+    uint64_t* freed_tp = full_tp + 1;    // by every chain
     uint64_t* s_free = freed_tp + 1;     // REC: S's and U's parts have been copied out
     uint64_t* u_free = s_free + 1;
     uint64_t* chain0 = u_free + 1;       // per chain: s_ready, x_ready, u_ready, r_ready (REC: U's parts), d1, d2, d3, turn
@@ -357,7 +352,7 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
             mbar_init(&full[i], 1);
             mbar_init(&freed[i], NCH);
         }
-        for (int i = 0; i < M::TPS; ++i) mbar_init(&full_tp[i], 1);
+        mbar_init(full_tp, 1);
         mbar_init(freed_tp, NCH);
         mbar_init(s_free, 1);
         mbar_init(u_free, 1);
@@ -410,14 +405,13 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                     n_kq = c + 1;
                 };
                 const auto load_tp = [&](int c) {
-                    uint64_t* f = &full_tp[c % M::TPS];
-                    unsigned char* to = sm + M::TP + (c % M::TPS) * NP * M::TPB;
+                    unsigned char* to = sm + M::TP;
                     const unsigned char* from = a.img + (rec0 + c) * NP * 16384;
-                    mbar_arrive_expect_tx(f, NP * M::TPB);
+                    mbar_arrive_expect_tx(full_tp, NP * M::TPB);
                     if (REC) {
-                        for (int p = 0; p < 2 * NP; ++p) bulk_g2s(to + p * 8192, from + p / 2 * 16384, 8192, f);
+                        for (int p = 0; p < 2 * NP; ++p) bulk_g2s(to + p * 8192, from + p / 2 * 16384, 8192, full_tp);
                     } else {
-                        bulk_g2s(to, from, NP * M::TPB, f);
+                        bulk_g2s(to, from, NP * M::TPB, full_tp);
                     }
                     n_tp = c + 1;
                 };
@@ -426,29 +420,22 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                     load(0);
                     load_tp(0);
                 }
-                if (ok && nch > 1 && (ok = prepared(1))) {
-                    load(1);
-                    if (M::TPS == 2) load_tp(1);
-                }
+                if (ok && nch > 1 && (ok = prepared(1))) load(1);
                 for (int c = 0; c + 1 < nch && ok; ++c) {
-                    if (M::TPS == 1) {   // the image's stage is free once every chain has chunk c's D2
-                        ok = mbar_wait(freed_tp, c & 1, kWaitLimit);
-                        if (ok) load_tp(c + 1);
-                    }
+                    ok = mbar_wait(freed_tp, c & 1, kWaitLimit);   // the image's place is free once every chain has chunk c's D2
+                    if (ok) load_tp(c + 1);
                     if (ok && c + 2 < nch) {
                         ok = mbar_wait(&freed[c & 1], (c >> 1) & 1, kWaitLimit);
                         ok = ok && prepared(c + 2);
                         if (!ok) break;
                         load(c + 2);
-                        if (M::TPS == 2) load_tp(c + 2);
                     }
                 }
-                if (!ok)   // a wait gave up: the copies under way land before the CTA ends
-                    for (int i = 0; i < 2; ++i) {
+                if (!ok) {   // a wait gave up: the copies under way land before the CTA ends
+                    for (int i = 0; i < 2; ++i)
                         if (n_kq > i) mbar_wait(&full[(n_kq - 1 - i) & 1], ((n_kq - 1 - i) >> 1) & 1, kWaitLimit);
-                        if (n_tp > i && i < M::TPS)
-                            mbar_wait(&full_tp[(n_tp - 1 - i) % M::TPS], ((n_tp - 1 - i) / M::TPS) & 1, kWaitLimit);
-                    }
+                    if (n_tp > 0) mbar_wait(full_tp, (n_tp - 1) & 1, kWaitLimit);
+                }
             } else if (REC && warp == M::IW + 1) {
                 // ---------------- copies out
                 for (int c = 0; c < nch; ++c) {
@@ -476,13 +463,13 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                 const uint32_t t1 = tb + g * 256, t2 = t1 + 128, t3 = t1;   // D3 over D1, which is read by then
                 const int nblk = (d.dk + 63) / 64;
                 const bool one = elect_one();
-                const uint64_t dS = sdesc_sw128(smem_u32(sm + M::S + g * 16384), NP == 3 ? C::lbo(g, 16384) : 16384);
-                const uint64_t dX = sdesc_sw128(smem_u32(sm + M::X + g * 8192), NP == 3 ? C::lbo(g, 8192) : 8192);
+                const uint64_t dS = sdesc_sw128(smem_u32(sm + M::S + g * 16384), C::lbo(g, 16384));
+                const uint64_t dX = sdesc_sw128(smem_u32(sm + M::X + g * 8192), C::lbo(g, 8192));
+                const uint64_t ta = sdesc_sw128(smem_u32(sm + M::TP));
                 for (int c = 0; c < nch; ++c) {
                     const uint32_t ph = c & 1;
                     const uint32_t kq = smem_u32(sm + M::KQ + (c & 1) * 2 * M::KQB);
                     const uint64_t ka = sdesc_sw128(kq), km = sdesc_sw128(kq, M::KQB);
-                    const uint64_t ta = sdesc_sw128(smem_u32(sm + M::TP + (c % M::TPS) * NP * M::TPB));
                     if (!(ok = warp_wait(q, ph) && warp_wait(&full[c & 1], (c >> 1) & 1))) break;
                     if (c > 0 && one) mbar_arrive(&freed[(c - 1) & 1]);   // the chunk before: every product and epilogue is over
                     if (NCH == 2) {   // (the other chain has issued its second product: of this chunk, of the one before)
@@ -499,7 +486,7 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                                            idesc_f16(128, NP * 32, false, true, true), blk + ks > 0);
                         mma_commit(q + 4);
                     }
-                    if (!(ok = warp_wait(&full_tp[c % M::TPS], (c / M::TPS) & 1) && warp_wait(q + 1, ph))) break;
+                    if (!(ok = warp_wait(full_tp, ph) && warp_wait(q + 1, ph))) break;
                     if (one) {
 #pragma unroll
                         for (int p = 0; p < NP; ++p)   // with the part pairs p + x < NP
@@ -508,7 +495,7 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                                 mma_f16_ss(t2, ta + p * (M::TPB >> 4) + ks * 2, dX + ks * 128,
                                            idesc_f16(128, (NP - p) * 32, false, true, true), p + ks > 0);
                         mma_commit(q + 5);
-                        if (M::TPS == 1) mma_commit(freed_tp);   // (the next image is a long load: as early as can be)
+                        mma_commit(freed_tp);   // (the next image is a long load: as early as can be)
                         if (NCH == 2) mbar_arrive(q + 7);
                     }
                     if (!(ok = warp_wait(q + 2, ph))) break;
@@ -584,7 +571,7 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                 float2 U[CW / 2];
                 tmem_sum<NP>(t2, 32, U);
                 if (c > 0 && !(ok = warp_wait(u_free, ph ^ 1u))) break;
-                put_parts<NP>(sm + M::U, i, g * 32 + cc, U);
+                put_parts(sm + M::U, i, g * 32 + cc, U);
                 warp_arrive(q + 3, lane);
             } else {
                 if (!(ok = warp_wait(q + 4, ph))) break;
@@ -617,46 +604,45 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
     if (warp == M::MW) tmem_dealloc(tb, NCH * 256);
 }
 
-template <int NP, int NCH, typename Tout, bool REC>
-__global__ void __launch_bounds__((ScanSmem<NP, NCH, REC>::warps * 32), 1)
+template <int NCH, typename Tout, bool REC>
+__global__ void __launch_bounds__((ScanSmem<NCH, REC>::warps * 32), 1)
     k_gt_scan(GDims d, ScanArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v) {
-    scan_cta<NP, NCH, Tout, REC>(d, a, tm_q, tm_k, tm_v, blockIdx.x, blockIdx.y, gridDim.y);
+    scan_cta<NCH, Tout, REC>(d, a, tm_q, tm_k, tm_v, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
 // ------------------------------------------------------------------ few heads, many chunks
 // The scan's CTAs and, on the other SMs, the chunks' preparation, in one cooperative launch (all CTAs run
 // at once, which makes waiting for their flags safe).  Three groups of four warps a preparing CTA take the
 // chunks in the order in which the scans come to them.
-template <int NP>
 struct LongSmem {
     static constexpr int groups = 3, threads = 128 * groups;
-    static constexpr size_t group = PrepSmem<NP>::bytes / 1024 * 1024 + 1024;
-    static constexpr size_t scan = ScanSmem<NP, 1, false>::bytes;
+    static constexpr size_t group = PrepSmem::bytes / 1024 * 1024 + 1024;
+    static constexpr size_t scan = ScanSmem<1, false>::bytes;
     static constexpr size_t bytes = groups * group > scan ? groups * group : scan;
 };
 
-template <int NP, typename Tout>
-__global__ void __launch_bounds__(LongSmem<NP>::threads, 1)
+template <typename Tout>
+__global__ void __launch_bounds__(LongSmem::threads, 1)
     k_gt_long(GDims d, PrepArgs p, ScanArgs a, int* flags, int slices, const __grid_constant__ CUtensorMap tm_q,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-    static_assert(ScanSmem<NP, 1, false>::warps * 32 <= LongSmem<NP>::threads, "the scan's warps");
+    static_assert(ScanSmem<1, false>::warps * 32 <= LongSmem::threads, "the scan's warps");
     const int bh = d.B * d.H, nscan = bh * slices;
     if ((int)blockIdx.x < nscan) {
-        scan_cta<NP, 1, Tout, false>(d, a, tm_q, tm_k, tm_v, blockIdx.x % bh, blockIdx.x / bh, slices);
+        scan_cta<1, Tout, false>(d, a, tm_q, tm_k, tm_v, blockIdx.x % bh, blockIdx.x / bh, slices);
         return;
     }
-    using M = PrepSmem<NP>;
+    using M = PrepSmem;
     extern __shared__ unsigned char raw[];
     const int gid = threadIdx.x >> 7, tid = threadIdx.x & 127;
-    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023) + gid * LongSmem<NP>::group;
+    unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023) + gid * LongSmem::group;
     uint64_t* bar = (uint64_t*)(sm + M::BAR);
     uint32_t* tslot = (uint32_t*)(bar + 3);
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
     }
-    uint32_t* const base = (uint32_t*)(sm - gid * LongSmem<NP>::group + M::BAR) + 8;   // (past the first group's barriers and slot)
+    uint32_t* const base = (uint32_t*)(sm - gid * LongSmem::group + M::BAR) + 8;   // (past the first group's barriers and slot)
     if (threadIdx.x < 32) {   // for all groups (no allocation may follow the relinquishing)
         tmem_alloc(base, 256);
         tmem_relinquish();
@@ -668,13 +654,13 @@ __global__ void __launch_bounds__(LongSmem<NP>::threads, 1)
     const long long items = (long long)((d.L + kGC - 1) / kGC) * bh;
     bool ok = true;
     uint32_t ph = 0;
-    for (long long x = (long long)(blockIdx.x - nscan) * LongSmem<NP>::groups + gid; x < items && ok;
-         x += (long long)(gridDim.x - nscan) * LongSmem<NP>::groups) {
+    for (long long x = (long long)(blockIdx.x - nscan) * LongSmem::groups + gid; x < items && ok;
+         x += (long long)(gridDim.x - nscan) * LongSmem::groups) {
         const int c = (int)(x / bh), b = (int)(x % bh) / d.H, h = (int)(x % bh) % d.H;
         const SeqAt s = seq_at(d, b, kGC);
         if (c * kGC >= s.len) continue;
         const int slot = s.slot0 + c;
-        ok = prep_chunk<NP>(d, p, &tm_q, &tm_k, sm, 1 + gid, tid, slot, h, s, ph, tslot, flags + (size_t)h * p.slots + slot);
+        ok = prep_chunk(d, p, &tm_q, &tm_k, sm, 1 + gid, tid, slot, h, s, ph, tslot, flags + (size_t)h * p.slots + slot);
         ph ^= 1;
         group_sync(1 + gid);
     }
@@ -689,11 +675,11 @@ struct TcWs {
     GVec* vec;
 };
 
-size_t carve(const GDims& d, int np, void* base, TcWs* w) {
+size_t carve(const GDims& d, void* base, TcWs* w) {
     const size_t n = (size_t)d.H * d.slots(kGC);
     char* p = (char*)base;
     w->img = (unsigned char*)p;
-    p += align256(n * np * 16384);
+    p += align256(n * NP * 16384);
     w->vec = (GVec*)p;
     p += align256(n * sizeof(GVec));
     p += align256(n * sizeof(int));
@@ -715,10 +701,10 @@ cudaError_t make_maps(const GDims& d, const void* q, const void* k, const void* 
     return e;
 }
 
-template <int NP, int NCH, typename Tout, bool REC = false>
+template <int NCH, typename Tout, bool REC = false>
 cudaError_t scan(const GDims& d, const ScanArgs& a, const Maps& m, cudaStream_t st) {
-    using M = ScanSmem<NP, NCH, REC>;
-    const auto k = k_gt_scan<NP, NCH, Tout, REC>;
+    using M = ScanSmem<NCH, REC>;
+    const auto k = k_gt_scan<NCH, Tout, REC>;
     cudaError_t e = smem_attr(k, M::bytes);
     if (e != cudaSuccess) return e;
     e = launch_early(k, dim3((unsigned)d.BH(), (d.dv + 32 * NCH - 1) / (32 * NCH)), M::warps * 32, M::bytes, st, d, a,
@@ -727,11 +713,10 @@ cudaError_t scan(const GDims& d, const ScanArgs& a, const Maps& m, cudaStream_t 
     return e;
 }
 
-template <int NP>
 cudaError_t prep(const GDims& d, const PrepArgs& a, const Maps& m, cudaStream_t st) {
-    cudaError_t e = smem_attr(k_gt_prep<NP>, PrepSmem<NP>::bytes);
+    cudaError_t e = smem_attr(k_gt_prep, PrepSmem::bytes);
     if (e != cudaSuccess) return e;
-    k_gt_prep<NP><<<dim3(a.slots, d.H), 128, PrepSmem<NP>::bytes, st>>>(d, a, m.q, m.k);
+    k_gt_prep<<<dim3(a.slots, d.H), 128, PrepSmem::bytes, st>>>(d, a, m.q, m.k);
     prof_mark("gated_prep_tc", st);
     return cudaGetLastError();
 }
@@ -739,10 +724,10 @@ cudaError_t prep(const GDims& d, const PrepArgs& a, const Maps& m, cudaStream_t 
 // Whether preparation and scan go in one launch (*nsm: its CTAs, else 0).  Two kernels: the preparation takes
 // 4 us a chunk and SM on all of them, then the scan starts.  One: it starts with the first chunk, 9 us
 // later than it could (the flags, the launch, a chunk's preparation on its own), and the rest costs nothing
-// as long as the scan leaves a third of the SMs.  In us, two kernels first, d 128, with / without the final state:
-//   H 8 L 4096 (512 chunks of a head)  161, 155 / 122, 125      H 16 L 4096 (1024)  174, 156 / 132, 127
-//   H 25 L 1024 (400)                   52, 54 /  41, 45        H 25 L 2048 (800)    94, 90 /  76, 74
-//   H 16 L 16384 (4096)                684, 563 (with)
+// as long as the scan leaves a third of the SMs.  In us, d 128, two kernels, one:
+//   H 8 L 4096 (512 chunks of a head)  161, 155      H 16 L 4096 (1024)  174, 156
+//   H 25 L 1024 (400)                   52,  54      H 25 L 2048 (800)    94,  90
+//   H 16 L 16384 (4096)                684, 563
 cudaError_t long_form(const GDims& d, bool narrow, int* nsm) {
     int dev = 0, n = 0;
     const long long scan = d.BH() * ((d.dv + 31) / 32);
@@ -754,11 +739,11 @@ cudaError_t long_form(const GDims& d, bool narrow, int* nsm) {
     return e;
 }
 
-template <int NP, typename Tout>
+template <typename Tout>
 cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, const float* g, const float* beta,
                 const float* S0, void* o, float* S_final, void* ws, cudaStream_t st) {
     TcWs w;
-    carve(d, NP, ws, &w);
+    carve(d, ws, &w);
     Maps m{};
     const int slots = d.slots(kGC);
     bool narrow = false;
@@ -767,8 +752,8 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
     int nsm = 0;
     if (e == cudaSuccess) e = long_form(d, narrow, &nsm);
     if (e == cudaSuccess && nsm) {
-        const auto k = k_gt_long<NP, Tout>;
-        if ((e = smem_attr(k, LongSmem<NP>::bytes)) != cudaSuccess) return e;
+        const auto k = k_gt_long<Tout>;
+        if ((e = smem_attr(k, LongSmem::bytes)) != cudaSuccess) return e;
         int* flags = flags_of(d, w);
         if ((e = cudaMemsetAsync(flags, 0, (size_t)d.H * slots * sizeof(int), st)) != cudaSuccess) return e;
         cudaLaunchAttribute coop{};
@@ -776,8 +761,8 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
         coop.val.cooperative = 1;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(nsm);
-        cfg.blockDim = dim3(LongSmem<NP>::threads);
-        cfg.dynamicSmemBytes = LongSmem<NP>::bytes;
+        cfg.blockDim = dim3(LongSmem::threads);
+        cfg.dynamicSmemBytes = LongSmem::bytes;
         cfg.stream = st;
         cfg.attrs = &coop;
         cfg.numAttrs = 1;
@@ -787,10 +772,10 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
         prof_mark("gated_long_tc", st);
         return e;
     }
-    if (e == cudaSuccess) e = prep<NP>(d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f}, m, st);
+    if (e == cudaSuccess) e = prep(d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f}, m, st);
     if (e != cudaSuccess) return e;
     const ScanArgs a{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr, nullptr};
-    return narrow ? scan<NP, 1, Tout>(d, a, m, st) : scan<NP, 2, Tout>(d, a, m, st);
+    return narrow ? scan<1, Tout>(d, a, m, st) : scan<2, Tout>(d, a, m, st);
 }
 
 }  // namespace
@@ -798,17 +783,14 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
 bool gated_tc_supported(const GDims& d) { return d.in_bf16 && d.L > 0; }
 size_t gated_tc_fwd_ws_bytes(const GDims& d) {
     TcWs w;
-    return carve(d, 3, nullptr, &w);
+    return carve(d, nullptr, &w);
 }
 
-// The outputs' type decides the operands' parts: three where an fp32 result leaves (the state, or
-// o in fp32), two where only bf16 does.
 cudaError_t launch_gated_fwd_tc(const GDims& d, const void* q, const void* k, const void* v, const float* g,
                                 const float* beta, const float* S0, void* o, float* S_final, void* ws,
                                 cudaStream_t st) {
-    if (!d.out_bf16) return fwd<3, float>(d, q, k, v, g, beta, S0, o, S_final, ws, st);
-    return S_final ? fwd<3, __nv_bfloat16>(d, q, k, v, g, beta, S0, o, S_final, ws, st)
-                   : fwd<2, __nv_bfloat16>(d, q, k, v, g, beta, S0, o, S_final, ws, st);
+    return d.out_bf16 ? fwd<__nv_bfloat16>(d, q, k, v, g, beta, S0, o, S_final, ws, st)
+                      : fwd<float>(d, q, k, v, g, beta, S0, o, S_final, ws, st);
 }
 
 cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
@@ -818,7 +800,7 @@ cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, c
     cudaError_t e = strided_rows_map(&m.q, q, d.dk, d.L, d.Hk, nb, d.qs);
     if (e == cudaSuccess) e = strided_rows_map(&m.k, k, d.dk, d.L, d.Hk, nb, d.ks);
     if (e != cudaSuccess) return e;
-    return prep<3>(d, PrepArgs{g, beta, img, vec, d.slots(kGC), floor_alpha}, m, st);
+    return prep(d, PrepArgs{g, beta, img, vec, d.slots(kGC), floor_alpha}, m, st);
 }
 
 cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
@@ -827,7 +809,7 @@ cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k,
     Maps m{};
     const cudaError_t e = make_maps(d, q, k, v, &m);
     if (e != cudaSuccess) return e;
-    return scan<3, 2, float, true>(d, ScanArgs{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U, nullptr}, m, st);
+    return scan<2, float, true>(d, ScanArgs{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U, nullptr}, m, st);
 }
 
 cudaError_t gated_tc_status_read_clear(unsigned int* status) {

@@ -3,12 +3,13 @@
 //
 // Precision.  The inputs q, k, v, dO are bf16 and enter the tensor cores as they are; every
 // operand that is computed (the state, the chunk's corrected values, T and P T) enters as the
-// sum of NP bf16 parts, x = x_0 + x_1 (+ x_2), each the rounding of what the earlier ones left,
-// and a product of two such operands takes the part pairs a + b < NP.  All products accumulate
-// in fp32.  Two parts carry 17 bits (2^-18 of the value at most): against the fp64 recurrence
-// the outputs and the carried state come out within about 4e-6 of their norm, where one bf16 or
-// fp16 operand leaves 3e-3 or 3e-4.  Parts keep fp32's exponent range, so there is no range to
-// check and no second path.
+// sum of three bf16 parts, x = x_0 + x_1 + x_2, each the rounding of what the earlier ones left,
+// and a product of two such operands takes the part pairs a + b < 3.  All products accumulate
+// in fp32.  Three parts carry the 24 bits of an fp32 value: against the fp64 recurrence the
+// outputs and the carried state come out within about 1e-6 of their norm, where two parts leave
+// 4e-6 and one bf16 or fp16 operand 3e-3 or 3e-4.  Parts keep fp32's exponent range, so there is
+// no range to check and no second path, and what a call returns does not depend on what else it
+// returns.
 #pragma once
 
 #include <utility>
@@ -20,6 +21,7 @@
 namespace efla {
 
 constexpr int kGC = 64;   // tokens a chunk of the tensor-core kernels
+constexpr int NP = 3;     // bf16 parts of a computed operand
 constexpr uint32_t kRecS = 3 * 16384, kRecU = 3 * 8192;   // bytes of a recorded slice
 
 // Elements from the first to the last of a strided [batch][heads][token][width] array, and the bytes
@@ -55,29 +57,29 @@ __device__ __forceinline__ void loaded(float (&v)[N]) {
     for (int i = 0; i < N; i += 8) loaded8(v + i);
 }
 
-// 8 values -> NP 16-byte chunks of bf16 parts
-template <int NP>
-__device__ __forceinline__ void split8(const float2* x, uint4 (&w)[NP]) {
+// 8 values -> N 16-byte chunks of bf16 parts
+template <int N>
+__device__ __forceinline__ void split8(const float2* x, uint4 (&w)[N]) {
     float2 r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = x[i];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
+    for (int p = 0; p < N; ++p) {
         uint32_t* o = reinterpret_cast<uint32_t*>(&w[p]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(r[i].x, r[i].y);
             o[i] = *reinterpret_cast<const uint32_t*>(&h);
-            if (p + 1 < NP) r[i] = sub2(r[i], bf16x2(o[i]));
+            if (p + 1 < N) r[i] = sub2(r[i], bf16x2(o[i]));
         }
     }
 }
-template <int NP>
-__device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
+template <int N>
+__device__ __forceinline__ void split8(const float* x, uint4 (&w)[N]) {
     float2 y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
-    split8<NP>(y, w);
+    split8<N>(y, w);
 }
 
 // A scan CTA runs NCH chains of 32 state columns each: their products and epilogues are
@@ -90,10 +92,10 @@ __device__ __forceinline__ void split8(const float* x, uint4 (&w)[NP]) {
 // so that its parts are neighbours along N and one product takes them all (D keeps a column
 // group for each; the epilogues add them).  An instruction costs about 43 cycles up to N = 64
 // and 50 at N = 96: three parts in one cost little more than one.
-template <int NP, int NCH>
+template <int NCH>
 struct Chain {
     static constexpr int N = 32;
-    static constexpr int blocks = NCH + (NP == 3 ? 1 : 0);
+    static constexpr int blocks = NCH + 1;
     // byte offset of part p's first column, and the stride to the block that holds part 2
     __host__ __device__ static constexpr uint32_t part(int g, int p, uint32_t blk) {
         return p < 2 ? g * blk + p * 64 : NCH * blk + g * 64;
@@ -130,9 +132,9 @@ __device__ __forceinline__ void tmem_sum(uint32_t t, int gap, float2 (&y)[W2]) {
     }
 }
 
-template <int NP, int NCH>
+template <int NCH>
 template <int W2>
-__device__ __forceinline__ void Chain<NP, NCH>::put(unsigned char* base, uint32_t blk, int g, int r, int cc,
+__device__ __forceinline__ void Chain<NCH>::put(unsigned char* base, uint32_t blk, int g, int r, int cc,
                                                     const float2 (&x)[W2]) {
 #pragma unroll
     for (int e = 0; e < 2 * W2; e += 8) {
@@ -146,7 +148,7 @@ __device__ __forceinline__ void Chain<NP, NCH>::put(unsigned char* base, uint32_
 
 // 2 W2 values of row r, from column col of a slice's 64, as parts in tiles of 64 rows one after another
 // (the records of U and dX).
-template <int NP, int W2>
+template <int W2>
 __device__ __forceinline__ void put_parts(unsigned char* base, int r, int col, const float2 (&x)[W2]) {
 #pragma unroll
     for (int e = 0; e < 2 * W2; e += 8) {
@@ -237,9 +239,9 @@ inline cudaError_t launch_early(void (*k)(P...), dim3 grid, unsigned threads, si
 }
 
 // Whether slices of 32 state columns (instead of 64) still find an SM each: a chain that shares its
-// CTA with no other takes 2.1 us a chunk, two take 3.3 us (2.5 us with two parts), but twice the CTAs
-// that do not all run at once take twice the time.  L 4096, d 128, final state (three parts): 38 heads,
-// the last that fit narrow slices, 206 us; 39 heads in wide ones 254 us.  Without it (two parts) 159, 194.
+// CTA with no other takes 2.1 us a chunk, two take 3.3 us, but twice the CTAs that do not all run
+// at once take twice the time.  L 4096, d 128: 38 heads, the last that fit narrow slices, 206 us;
+// 39 heads in wide ones 254 us.
 inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
     int dev = 0, nsm = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -248,8 +250,7 @@ inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
     return e;
 }
 
-// The backward's parts of gated_tc.cu: the preparation (three parts; alpha at least `floor_alpha`
-// in magnitude), and the pass that records every chunk's S and U as parts, in the operand layout
+// The backward's parts of gated_tc.cu: the preparation (alpha at least `floor_alpha` in magnitude), and the pass that records every chunk's S and U as parts, in the operand layout
 // ([H][slots][slices of 64 columns][kRecS or kRecU bytes]).
 cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
                                  float floor_alpha, unsigned char* img, GVec* vec, cudaStream_t st);
