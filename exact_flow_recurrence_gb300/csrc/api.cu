@@ -811,11 +811,12 @@ efla_status check_norm(const efla_norm_shape* s, efla::NormDims* d) {
     return EFLA_OK;
 }
 
-// element alignment of the rows and weights (their vector copies ask for more where they are used)
+// alignment of the rows and weights to their elements (their vector copies ask for more where they are
+// used) and of stats to its pairs, which are read and written as one
 efla_status check_elems(const Span* x, const size_t* es, int n) {
     for (int i = 0; i < n; ++i)
         if (x[i].n && (uintptr_t)x[i].p % es[i])
-            return fail(EFLA_ERR_ALIGNMENT, "%s is not aligned to its elements", x[i].name);
+            return fail(EFLA_ERR_ALIGNMENT, "%s is not aligned to %zu bytes", x[i].name, es[i]);
     return EFLA_OK;
 }
 
@@ -840,7 +841,7 @@ efla_status efla_norm_fwd(const efla_norm_shape* s, const void* x, const void* w
     if (!x || !weight || !y || !stats)
         return fail(EFLA_ERR_INVALID_ARG, "%s is NULL", !x ? "x" : !weight ? "weight" : !y ? "y" : "stats");
     const Span el[] = {in[0], in[1], in[2], out[0], out[1]};
-    const size_t es[] = {e, we, we, e, 4};
+    const size_t es[] = {e, we, we, e, 8};
     if ((st = check_elems(el, es, 5)) != EFLA_OK) return st;
     if ((st = check_alias(out, 2, in, 3)) != EFLA_OK) return st;
     efla::prof_mark(nullptr, stream);
@@ -871,7 +872,7 @@ efla_status efla_norm_bwd(const efla_norm_shape* s, const void* x, const void* w
     if (out[0].n && !dx) return fail(EFLA_ERR_INVALID_ARG, "dx is NULL");
     if (!dweight) return fail(EFLA_ERR_INVALID_ARG, "dweight is NULL");
     const Span el[] = {in[0], in[1], in[2], in[3], out[0], out[1], out[2]};
-    const size_t es[] = {e, we, e, 4, e, we, we};
+    const size_t es[] = {e, we, e, 8, e, we, we};
     if ((st = check_elems(el, es, 7)) != EFLA_OK) return st;
     if ((st = check_ptrs(nullptr, 0, out + 3, 1)) != EFLA_OK) return st;
     if ((st = check_alias(out, 4, in, 4)) != EFLA_OK) return st;

@@ -293,7 +293,8 @@ efla_status efla_gated_step(const efla_gated_shape* shape,
  *     y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(var + eps)
  * x, y, dy [rows, D] dtype with row strides (elements; y_stride: of y, and of dy in the
  * backward), dx dense; weight, bias, dweight, dbias [D] weight_dtype; stats [rows, 2] fp32 =
- * (mean, rstd) of each row, written by the forward and read by the backward.  Sums and
+ * (mean, rstd) of each row, written by the forward and read by the backward.  Alignment: rows
+ * and weights to their elements, stats to 8 bytes, the workspace to 16.  Sums and
  * statistics are fp32; dweight and dbias are added in a fixed order.  Any D in 1 .. 16384.
  * bias NULL: none; dbias NULL: not written.  rows = 0: dweight and dbias are zero. */
 typedef struct {
