@@ -1,8 +1,8 @@
 // gated_bwd_tc.cu -- the gated delta rule's backward on the tcgen05 tensor cores (bf16 tokens).
 //
 // The formulas of gated_simt.cu's head comment with 64-token chunks, in four kernels:
-//   k_gt_prep (gated_tc.cu)  T, P T, decays of every chunk, three bf16 parts
-//   k_gt_scan (gated_tc.cu)  recording pass: S entering every chunk and its U
+//   k_gt_prep (gated_tc.cu)  T, P T, the residuals' inverse, decays of every chunk, three bf16 parts
+//   k_gt_scan (gated_tc.cu)  recording pass: S entering every chunk and its residuals R
 //   k_gt_rscan               the chunks backwards: G (the gradient of the state that leaves the
 //                            chunk) and dX; dv = alpha dX; dS0
 //   k_gt_grad                every chunk at once: dq, dk, dg, dbeta
@@ -14,9 +14,9 @@
 // The records are the operands of the last kernel as it reads them (parts, swizzled), so that it
 // copies and multiplies: 1.5 times the bytes of fp32, and no conversion between copy and product.
 //
-// dalpha needs the token's residual r_i = v_i - f_i S^T k_i, and U_i = alpha_i r_i: then dalpha_i =
-// dX_i . r_i is the diagonal of dX U^T over alpha_i, and neither r nor a second product is kept.
-// For this alpha = 0 (beta = 0) is taken as 1e-25, which no fp32 result can tell from 0.
+// dalpha needs the token's residual r_i = v_i - f_i S^T k_i, and everything else U_i = alpha_i r_i.
+// R is what is recorded: dalpha_i = dX_i . r_i is the diagonal of dX R^T, alpha scales the columns of
+// the other products with it, and a token with alpha = 0 (beta = 0) is one like any other.
 #include "common.cuh"
 #include "gated_tc.cuh"
 #include "launch.h"
@@ -28,8 +28,6 @@ namespace efla {
 namespace {
 
 __device__ unsigned int g_gb_status = 0;   // bit 0: a bounded wait expired; kStatusBounds (debug builds): a write was skipped
-
-constexpr float kFloorAlpha = 1e-25f;
 
 // ------------------------------------------------------------------ reverse scan
 // As k_gt_scan: one CTA for 64 columns of a head's G, two chains of 32 in fp32 registers.  Per
@@ -361,17 +359,17 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
 
 // ------------------------------------------------------------------ gradients of a chunk
 // One chunk of a key head at a time, its value heads one after another, the value columns in
-// slices of 64; a persistent CTA an SM.  With (dX, U, S, G as three parts)
-//   Da = [dO; dX] S^T    D6 = [.; U] G^T    D3 = [dO; dX] U^T    D4 = [Q; K] K^T
+// slices of 64; a persistent CTA an SM.  With (dX, R, S, G as three parts)
+//   Da = [dO; dX] S^T    D6 = [.; R] G^T    D3 = [dO; dX] R^T    D4 = [Q; K] K^T
 //   (lanes 0..63 the first row block, 64..127 the second; every D with M = 128)
-//   dPD = lower(D3 D)  and  dAD = -strict_lower(alpha D3 D)  from lanes 0..63 and 64..127
+//   dPD = lower(D3 alpha_j D)  and  dAD = -strict_lower(alpha_i D3 alpha_j D)  from lanes 0..63 and 64..127
 //   D5 = [dPD; dAD] K + [0; dAD^T] K + [0; dPD^T] Q
-//   dQ = e^c Da + D5 (lanes 0..63);  dK = -alpha e^c Da + e^{c_last - c} D6 + D5 (lanes 64..127)
+//   dQ = e^c Da + D5 (lanes 0..63);  dK = -alpha e^c Da + alpha e^{c_last - c} D6 + D5 (lanes 64..127)
 // so that a lane is a token: decays scale lanes, and the dot products with q and k that dg needs
 // are sums within a thread.
 //
 // The recorded parts come by bulk copy as the products read them, each kind into a buffer of its
-// own that is filled again as soon as its products are done: [dO; dX_0], [0; dX_1], [0; dX_2], U, S,
+// own that is filled again as soon as its products are done: [dO; dX_0], [0; dX_1], [0; dX_2], R, S,
 // G; dO, q and k by TMA.  Warps: 8 epilogue (a lane a token; <S, G> in the products' shadow), one
 // that issues products, one that copies.  The epilogue of the pairs runs while the last slice's
 // products do.  4096 chunks of two slices: 355 us at B4 H16 L4096, 1.3 GB from DRAM (3.6 TB/s, 42% of
@@ -381,8 +379,8 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
 constexpr int kGrWarps = 10;
 constexpr uint32_t kGrQK = 0;                    // 2 blocks of 64 dk x [Q rows | K rows]
 constexpr uint32_t kGrAX = 32768;                // dO | dX_0 | 0 | dX_1 | 0 | dX_2, tiles of 64 rows
-constexpr uint32_t kGrU = kGrAX + 49152;         // U_0 | U_1 | U_2 (as an A operand, the tile before fills rows 0..63)
-constexpr uint32_t kGrS = kGrU + 24576;          // 3 blocks of 128 rows: Chain<2>
+constexpr uint32_t kGrR = kGrAX + 49152;         // R_0 | R_1 | R_2 (as an A operand, the tile before fills rows 0..63)
+constexpr uint32_t kGrS = kGrR + 24576;          // 3 blocks of 128 rows: Chain<2>
 constexpr uint32_t kGrG = kGrS + 49152;          // likewise
 constexpr uint32_t kGrP5 = kGrS;                 // [dPD; dAD], two parts, in S's place
 constexpr uint32_t kGrMisc = kGrG + 49152;
@@ -396,10 +394,10 @@ struct GrMisc {
     float rs[2][128];      // row sums of a column group
     float cs[4][64];       // column sums of a lane quadrant
     float dot[2][128];     // per column group: q . dq's, and k . dk's state terms
-    float dot2[2][64];     // k . (e^{c_last - c} U G^T)
+    float dot2[2][64];     // k . (alpha e^{c_last - c} R G^T)
     float sg[2][8];        // by the head's parity
-    uint64_t f_vec, f_qk, f_ax, f_u, f_s, f_g;   // copies have landed
-    uint64_t e_ax, e_u, e_s, e_g;      // products (and <S, G>) have read
+    uint64_t f_vec, f_qk, f_ax, f_r, f_s, f_g;   // copies have landed
+    uint64_t e_ax, e_r, e_s, e_g;      // products (and <S, G>) have read
     uint64_t d3, d5, p5;               // products; [dPD; dAD]
     uint64_t qk, end;                  // [Q; K] is fit for the products; the epilogue has read everything of the head
     uint32_t tslot;
@@ -412,7 +410,7 @@ struct GradArgs {
     const float* beta;
     const GVec* vec;
     const unsigned char* S;
-    const unsigned char* U;
+    const unsigned char* R;
     const unsigned char* G;
     const unsigned char* dX;
     void* dq;
@@ -476,7 +474,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     const int dk = d.dk, nsl = (d.dv + 63) / 64, nblk = (dk + 63) / 64;
     const long long items = (long long)a.slots * d.Hk;   // key head fastest: neighbours share a sequence's tokens
     if (tid == 0) {
-        for (uint64_t* p : {&m.f_vec, &m.f_qk, &m.f_ax, &m.f_u, &m.f_s, &m.f_g, &m.e_ax, &m.e_u, &m.d3, &m.d5})
+        for (uint64_t* p : {&m.f_vec, &m.f_qk, &m.f_ax, &m.f_r, &m.f_s, &m.f_g, &m.e_ax, &m.e_r, &m.d3, &m.d5})
             mbar_init(p, 1);
         for (uint64_t* p : {&m.e_s, &m.e_g}) mbar_init(p, 1 + 8);
         for (uint64_t* p : {&m.qk, &m.p5, &m.end}) mbar_init(p, 8);
@@ -514,7 +512,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 const size_t rec = ((size_t)h * a.slots + slot) * nsl + sl;
                 tma_prefetch_4d(&tm_do, 64 * sl, t, h, batch);
                 bulk_prefetch_l2(a.dX + rec * kRecU, kRecU);
-                bulk_prefetch_l2(a.U + rec * kRecU, kRecU);
+                bulk_prefetch_l2(a.R + rec * kRecU, kRecU);
                 bulk_prefetch_l2(a.S + rec * kRecS, kRecS);
                 bulk_prefetch_l2(a.G + rec * kRecS, kRecS);
             };
@@ -536,8 +534,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         tma_load_4d(sm + kGrAX, &tm_do, 64 * sl, t, h, s.batch, &m.f_ax);
                         for (int p = 0; p < 3; ++p)
                             bulk_g2s(sm + kGrAX + p * 16384 + 8192, a.dX + rec * kRecU + p * 8192, 8192, &m.f_ax);
-                        if (!next(&m.e_u, &m.f_u, kRecU)) break;
-                        bulk_g2s(sm + kGrU, a.U + rec * kRecU, kRecU, &m.f_u);
+                        if (!next(&m.e_r, &m.f_r, kRecU)) break;
+                        bulk_g2s(sm + kGrR, a.R + rec * kRecU, kRecU, &m.f_r);
                         if (!next(&m.e_s, &m.f_s, kRecS)) break;
                         bulk_g2s(sm + kGrS, a.S + rec * kRecS, kRecS, &m.f_s);
                         if (!next(&m.e_g, &m.f_g, kRecS)) break;
@@ -576,7 +574,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 }
             }
             if (!ok) {   // what is under way lands before the CTA ends
-                for (uint64_t* p : {&m.f_ax, &m.f_u, &m.f_s, &m.f_g}) mbar_wait(p, sc & 1, kWaitLimit);
+                for (uint64_t* p : {&m.f_ax, &m.f_r, &m.f_s, &m.f_g}) mbar_wait(p, sc & 1, kWaitLimit);
                 if (kc) mbar_wait(&m.f_qk, (kc - 1) & 1, kWaitLimit);
                 mbar_wait(&m.f_vec, hc & 1, kWaitLimit);
             }
@@ -584,7 +582,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     } else if (warp == 8) {
         // ---------------- products
         const bool one = elect_one();
-        const uint64_t ax = sdesc_sw128(smem_u32(sm + kGrAX)), us = sdesc_sw128(smem_u32(sm + kGrU)),
+        const uint64_t ax = sdesc_sw128(smem_u32(sm + kGrAX)), rs = sdesc_sw128(smem_u32(sm + kGrR)),
                        ss = sdesc_sw128(smem_u32(sm + kGrS)), gs = sdesc_sw128(smem_u32(sm + kGrG)),
                        qk = sdesc_sw128(smem_u32(sm + kGrQK));
         const uint32_t p5 = smem_u32(sm + kGrP5), z0 = smem_u32(sm + kGrZero), kq = smem_u32(sm + kGrQK);
@@ -608,7 +606,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 }
                 for (int sl = 0; sl < nsl; ++sl, ++sc) {
                     const uint32_t ph = sc & 1, more = sl > 0;
-                    if (!(ok = warp_wait(&m.f_ax, ph) && warp_wait(&m.f_u, ph))) break;
+                    if (!(ok = warp_wait(&m.f_ax, ph) && warp_wait(&m.f_r, ph))) break;
                     // The accumulators cut off what falls below their last bit, at every instruction: the small
                     // part pairs go first (and, for dbeta's D3, into columns of their own), so that few of them
                     // meet a large sum.
@@ -619,7 +617,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             for (int p = 0; p <= o; ++p)
 #pragma unroll
                                 for (int ks = 0; ks < 4; ++ks)
-                                    mma_f16_ss(tb + (o ? cD3s : cD3), ax + p * 1024 + ks * 2, us + (o - p) * 512 + ks * 2, n64,
+                                    mma_f16_ss(tb + (o ? cD3s : cD3), ax + p * 1024 + ks * 2, rs + (o - p) * 512 + ks * 2, n64,
                                                more | !((o == NP - 1 || o == 0) && p == 0 && ks == 0));
                         if (sl == nsl - 1) mma_commit(&m.d3);   // the pairs' epilogue can start
                     }
@@ -645,10 +643,10 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             for (int p = 0; p <= o; ++p)
 #pragma unroll
                                 for (int ks = 0; ks < 4; ++ks)
-                                    mma_f16_ss(tb + cD6, us + p * 512 - 512 + ks * 2,
+                                    mma_f16_ss(tb + cD6, rs + p * 512 - 512 + ks * 2,
                                                gs + at_part(ks >> 1, o - p, 16384) + (ks & 1) * 2, n128,
                                                more | !(o == NP - 1 && p == 0 && ks == 0));
-                        mma_commit(&m.e_u);
+                        mma_commit(&m.e_r);
                         mma_commit(&m.e_g);
                     }
                 }
@@ -731,15 +729,16 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                         tmem_ld16(lq + cD3 + j0, y);
                         tmem_ld16(lq + cD3s + j0, y2);
                         tmem_ld16(lq + cD4 + j0, z);
-                        float g[16];   // the decays, while the loads are under way
+                        float g[16];   // alpha_j times the decays, while the loads are under way
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             const float4 h4 = *reinterpret_cast<const float4*>(vec.chi + j0 + e);
                             const float4 l4 = *reinterpret_cast<const float4*>(vec.clo + j0 + e);
-                            g[e] = decay2(chi, clo, h4.x, l4.x);
-                            g[e + 1] = decay2(chi, clo, h4.y, l4.y);
-                            g[e + 2] = decay2(chi, clo, h4.z, l4.z);
-                            g[e + 3] = decay2(chi, clo, h4.w, l4.w);
+                            const float4 a4 = *reinterpret_cast<const float4*>(vec.al + j0 + e);
+                            g[e] = a4.x * decay2(chi, clo, h4.x, l4.x);
+                            g[e + 1] = a4.y * decay2(chi, clo, h4.y, l4.y);
+                            g[e + 2] = a4.z * decay2(chi, clo, h4.z, l4.z);
+                            g[e + 3] = a4.w * decay2(chi, clo, h4.w, l4.w);
                         }
                         tmem_ld_wait();
                         loaded16(y);
@@ -759,8 +758,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             z[e] = keep ? w * z[e] : 0.f;
                             rsum += z[e];
                         }
-                        if (!top && (i & ~15) == j0) {   // the diagonal: dalpha alpha, and lambda
-                            m.da[i] = i < n ? dg / al : 0.f;
+                        if (!top && (i & ~15) == j0) {   // the diagonal: dalpha, and lambda
+                            m.da[i] = i < n ? dg : 0.f;
                             m.lam[i] = lam;
                         }
                         const float cs = lane_sums16(z, lane);
@@ -776,7 +775,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 sg = warp_sum(sg);
                 if (lane == 0) m.sg[hc & 1][warp] = sg;
                 // (S's buffer: the last slice's products have read it, and so has <S, G>)
-                ok = ok && warp_wait(&m.e_u, (nsl * (hc + 1) - 1) & 1);   // D6 follows Da
+                ok = ok && warp_wait(&m.e_r, (nsl * (hc + 1) - 1) & 1);   // D6 follows Da
                 if (!(ok = group_sync_and(1, ok, 256))) break;                  // (the warps leave together if a wait gave up)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -798,7 +797,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                     m.be[tid] = be;
                 }
                 const float up = vec.up[i], rest = vec.rest[i];
-                const float2 sa = both(top ? up : -al * up), rs2 = both(rest);
+                const float2 sa = both(top ? up : -al * up), rs2 = both(al * rest);
                 const float2 dl = both(top ? 0.f : 2.f * m.da[i] * dalpha_dlambda_of(be, m.lam[i], d.euler));
                 float2 dot = both(0.f), dot2 = both(0.f);
                 Tout* out = top ? (Tout*)a.dq + at3(d.dqs, s.batch, hk, t + i) : (Tout*)a.dk + at3(d.dks, s.batch, hk, t + i);
@@ -923,9 +922,9 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
 }
 
 struct BwdTcWs {
-    unsigned char* img;
+    unsigned char *img, *img_r;
     GVec* vec;
-    unsigned char *S, *U, *G, *dX;
+    unsigned char *S, *R, *G, *dX;
     float* acc;
 };
 
@@ -940,9 +939,10 @@ size_t carve(const GDims& d, void* base, BwdTcWs* w) {
         return (unsigned char*)r;
     };
     w->img = take(n * NP * 16384);
+    w->img_r = take(n * NP * 8192);
     w->vec = (GVec*)take(n * sizeof(GVec));
     w->S = take(n * nsl * kRecS);
-    w->U = take(n * nsl * kRecU);
+    w->R = take(n * nsl * kRecU);
     w->G = take(n * nsl * kRecS);
     w->dX = take(n * nsl * kRecU);
     w->acc = d.H > d.Hk ? (float*)take((size_t)kGrCtas * 128 * 128 * 4) : nullptr;
@@ -962,15 +962,15 @@ cudaError_t bwd(const GDims& d, const void* q, const void* k, const void* v, con
     if (e == cudaSuccess) e = strided_rows_map(&mo, dO, d.dv, d.L, d.H, nb, d.dos);
     if (e == cudaSuccess) e = smem_attr(k_gt_rscan<Tout>, Rs::bytes);
     if (e == cudaSuccess) e = smem_attr(k_gt_grad<Tout>, kGrSmem);
-    if (e == cudaSuccess) e = launch_gated_prep_tc(d, q, k, g, beta, kFloorAlpha, w.img, w.vec, st);
-    if (e == cudaSuccess) e = launch_gated_record_tc(d, q, k, v, S0, w.img, w.vec, w.S, w.U, st);
+    if (e == cudaSuccess) e = launch_gated_prep_tc(d, q, k, g, beta, w.img, w.img_r, w.vec, st);
+    if (e == cudaSuccess) e = launch_gated_record_tc(d, q, k, v, S0, w.img_r, w.vec, w.S, w.R, st);
     if (e != cudaSuccess) return e;
     const RscanArgs ra{w.img, w.vec, dS_final, dS0, dv, w.G, w.dX, slots};
     e = launch_early(k_gt_rscan<Tout>, dim3((unsigned)d.BH(), (d.dv + 63) / 64), Rs::warps * 32, Rs::bytes, st, d, ra,
                      mq, mk, mo);
     prof_mark("gated_rscan_tc", st);
     if (e != cudaSuccess) return e;
-    const GradArgs ga{beta, w.vec, w.S, w.U, w.G, w.dX, dq, dk, dg, dbeta, w.acc, slots};
+    const GradArgs ga{beta, w.vec, w.S, w.R, w.G, w.dX, dq, dk, dg, dbeta, w.acc, slots};
     const long long items = (long long)slots * d.Hk;
     e = launch_early(k_gt_grad<Tout>, dim3((unsigned)(items < kGrCtas ? items : kGrCtas)), kGrWarps * 32, kGrSmem, st, d,
                      ga, mq, mk, mo);

@@ -24,6 +24,10 @@ __device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kS
 //      its bf16 parts on their way out by bulk copy; then P's parts in place of A and T;
 //   5. one product P T, whose parts replace P's and go out too: the [T; P T] image, NP parts of
 //      128 rows in the operand layout.
+// The backward also wants the tokens' residuals r = U / alpha, where alpha is zero too.  With A =
+// diag(alpha) N they are r = (I + N diag(alpha))^{-1} (V - e^c K S), and that inverse is
+// I - N T diag(alpha): N's parts fill the other 64 rows of the product of step 5, and no quotient
+// by alpha is formed.  It goes out as an image of its own (three chunks an SM then: N needs room).
 // Bound by its chain of short dependent steps, not by data: what counts is how many chunks an
 // SM has in flight.  P's parts lie over A and T, and both over the dead tiles, so that four
 // chunks fit (as many as the registers allow).  With three of them an SM a chunk took 11 us from its
@@ -38,12 +42,14 @@ struct PrepArgs {
     unsigned char* img;   // [H][slots][NP][128 rows x 128 bytes]
     GVec* vec;            // [H][slots]
     int slots;
-    float floor_alpha;    // |alpha| below this is taken as it (0: as it is)
+    unsigned char* img_r;   // BWD: [H][slots][NP][64 rows x 128 bytes], the residuals' inverse
 };
 
+template <bool BWD>
 struct PrepSmem {
-    static constexpr uint32_t P = 0;               // NP tiles of 64 rows; [64][kLdA] fp32 before (and the K, Q tiles first)
-    static constexpr uint32_t T = NP * 8192;       // NP tiles; the inverse's scratch before
+    static constexpr uint32_t P = 0;               // P's tiles of 64 rows (BWD: [P; N], 128 rows); [64][kLdA] fp32 before
+    static constexpr uint32_t PB = BWD ? 16384 : 8192;   // (and the K, Q tiles first): bytes of a part
+    static constexpr uint32_t T = NP * PB;         // NP tiles; the inverse's scratch before
     static constexpr uint32_t VEC = T + NP * 8192;
     static constexpr uint32_t BAR = VEC + sizeof(GVec);
     static constexpr size_t bytes = 1024 + BAR + 64;
@@ -51,10 +57,11 @@ struct PrepSmem {
 
 // One chunk, by four warps (named barrier `bid`) whose bars[0..2] count phases `ph` and whose 64 columns
 // of tensor memory are at *tslot (valid after the first barrier).  `flag`: set once the results are in global memory.
+template <bool BWD>
 __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                            unsigned char* sm, int bid, int tid, int slot, int h, const SeqAt& s, uint32_t ph,
                            const uint32_t* tslot, int* flag) {
-    using M = PrepSmem;
+    using M = PrepSmem<BWD>;
     const int hk = h / (d.H / d.Hk), warp = tid >> 5, lane = tid & 31;
     const int t0 = (slot - s.slot0) * kGC, n = min(kGC, s.len - t0), t = s.start + t0;
     uint64_t* bar = (uint64_t*)(sm + M::BAR);
@@ -134,36 +141,37 @@ __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap*
 #pragma unroll
             for (int j = 0; j < 64; ++j) lam = j == i ? v[j] : lam;
             scale = i < n ? alpha_of(beta, lam, d.euler) : 0.f;
-            if (i < n && fabsf(scale) < a.floor_alpha) scale = a.floor_alpha;
             vec->al[i] = scale;
         }
+        const float row = BWD ? 1.f : scale;     // BWD: N first, alpha as A is stored
         const int diag = tid < 64 ? i : i + 1;   // columns below this are kept
 #pragma unroll
         for (int j = 0; j < 64; j += 4) {
             if (j < cols) {
                 const float4 h4 = *reinterpret_cast<const float4*>(vec->chi + j), l4 = *reinterpret_cast<const float4*>(vec->clo + j);
-                v[j] = j < diag && i < n ? scale * decay2(chi, clo, h4.x, l4.x) * v[j] : 0.f;
-                v[j + 1] = j + 1 < diag && i < n ? scale * decay2(chi, clo, h4.y, l4.y) * v[j + 1] : 0.f;
-                v[j + 2] = j + 2 < diag && i < n ? scale * decay2(chi, clo, h4.z, l4.z) * v[j + 2] : 0.f;
-                v[j + 3] = j + 3 < diag && i < n ? scale * decay2(chi, clo, h4.w, l4.w) * v[j + 3] : 0.f;
+                v[j] = j < diag && i < n ? row * decay2(chi, clo, h4.x, l4.x) * v[j] : 0.f;
+                v[j + 1] = j + 1 < diag && i < n ? row * decay2(chi, clo, h4.y, l4.y) * v[j + 1] : 0.f;
+                v[j + 2] = j + 2 < diag && i < n ? row * decay2(chi, clo, h4.z, l4.z) * v[j + 2] : 0.f;
+                v[j + 3] = j + 3 < diag && i < n ? row * decay2(chi, clo, h4.w, l4.w) * v[j + 3] : 0.f;
             } else {
                 v[j] = v[j + 1] = v[j + 2] = v[j + 3] = 0.f;
             }
         }
-        // 64 values as parts into row i of P's tiles
-        const auto put_row = [&](const float* x) {
+        // 64 values as parts into row r of P's tiles
+        const auto put_row = [&](int r, const float* x) {
 #pragma unroll
             for (int j = 0; j < 64; j += 8) {
                 uint4 w[NP];
                 split8<NP>(x + j, w);
 #pragma unroll
-                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(sm + M::P + p * 8192 + sw128(i, j)) = w[p];
+                for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(sm + M::P + p * M::PB + sw128(r, j)) = w[p];
             }
         };
         if (tid < 64) {
+            const float al = BWD ? scale : 1.f;
 #pragma unroll
             for (int j = 0; j < 64; j += 4)
-                *reinterpret_cast<float4*>(T + i * kLdA + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                *reinterpret_cast<float4*>(T + i * kLdA + j) = make_float4(al * v[j], al * v[j + 1], al * v[j + 2], al * v[j + 3]);
         }
         tc_fence_before();
         group_sync(bid);
@@ -188,12 +196,12 @@ __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap*
         group_sync(bid);
         if (tid == 0 && out_ok)
             for (int p = 0; p < NP; ++p) bulk_s2g(out + p * 16384, sm + M::T + p * 8192, 8192);
-        if (tid >= 64) put_row(v);
+        if (BWD || tid >= 64) put_row(BWD ? tid ^ 64 : i, v);   // BWD: P's rows, then N's
         fence_async_smem();
         tc_fence_before();
         group_sync(bid);
-        if (warp == 0 && elect_one()) {   // P T, the part pairs p + x < NP (B: T's rows are K indices; rows 64..127 of A
-            tc_fence_after();             // are what follows P's tiles, and not used)
+        if (warp == 0 && elect_one()) {   // P T (BWD: N T too), the part pairs p + x < NP (B: T's rows are K indices;
+            tc_fence_after();             // else rows 64..127 of A are what follows P's tiles, and not used)
             const uint64_t da = sdesc_sw128(smem_u32(sm + M::P)), db = sdesc_sw128(smem_u32(sm + M::T));
 #pragma unroll
             for (int p = NP - 1; p >= 0; --p)
@@ -201,20 +209,24 @@ __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap*
                 for (int x = NP - 1 - p; x >= 0; --x)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_ss(tb, da + p * 512 + ks * 2, db + x * 512 + ks * 128, idesc_f16(128, 64, false, true, true),
+                        mma_f16_ss(tb, da + p * (M::PB >> 4) + ks * 2, db + x * 512 + ks * 128, idesc_f16(128, 64, false, true, true),
                                    !(p == NP - 1 && x == 0 && ks == 0));
             mma_commit(&bar[2]);
         }
         ok = group_sync_and(bid, mbar_wait(&bar[2], ph, kWaitLimit));
         tc_fence_after();
-        if (tid < 64 && ok) {
+        if ((BWD || tid < 64) && ok) {
 #pragma unroll
             for (int c = 0; c < 64; c += 16)
                 tmem_ld16(taddr(tb, warp * 32, c), *reinterpret_cast<float(*)[16]>(v + c));
             tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 64; c += 16) loaded16(v + c);
-            put_row(v);
+            if (BWD && tid >= 64) {   // I - N T diag(alpha)
+#pragma unroll
+                for (int j = 0; j < 64; ++j) v[j] = fmaf(-vec->al[j], v[j], j == i ? 1.f : 0.f);
+            }
+            put_row(tid, v);
             tc_fence_before();
         }
         fence_async_smem();
@@ -228,7 +240,12 @@ __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap*
     tc_fence_after();
     if (tid == 0 && ok) {
         if (out_ok)
-            for (int p = 0; p < NP; ++p) bulk_s2g(out + p * 16384 + 8192, sm + M::P + p * 8192, 8192);
+            for (int p = 0; p < NP; ++p) bulk_s2g(out + p * 16384 + 8192, sm + M::P + p * M::PB, 8192);
+        if constexpr (BWD) {
+            unsigned char* const out_r = a.img_r + rec * NP * 8192;
+            if (dbg_in(out_r, NP * 8192, a.img_r, all * NP * 8192, &g_gt2_status))
+                for (int p = 0; p < NP; ++p) bulk_s2g(out_r + p * 8192, sm + M::P + p * M::PB + 8192, 8192);
+        }
         if (dbg_in(a.vec + rec, sizeof(GVec), a.vec, all * sizeof(GVec), &g_gt2_status))
             bulk_s2g(a.vec + rec, vec, sizeof(GVec));
     }
@@ -245,9 +262,10 @@ __device__ bool prep_chunk(const GDims& d, const PrepArgs& a, const CUtensorMap*
     return ok;
 }
 
-__global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
+template <bool BWD>
+__global__ void __launch_bounds__(128, BWD ? 3 : 4) k_gt_prep(GDims d, PrepArgs a, const __grid_constant__ CUtensorMap tm_q,
                                                     const __grid_constant__ CUtensorMap tm_k) {
-    using M = PrepSmem;
+    using M = PrepSmem<BWD>;
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int slot = blockIdx.x, tid = threadIdx.x;
@@ -263,7 +281,7 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
         tmem_alloc(tslot, 64);
         tmem_relinquish();
     }
-    prep_chunk(d, a, &tm_q, &tm_k, sm, 1, tid, slot, blockIdx.y, s, 0, tslot, nullptr);
+    prep_chunk<BWD>(d, a, &tm_q, &tm_k, sm, 1, tid, slot, blockIdx.y, s, 0, tslot, nullptr);
     if (tid < 32) tmem_dealloc(*tslot, 64);
 }
 
@@ -276,9 +294,10 @@ __global__ void __launch_bounds__(128, 4) k_gt_prep(GDims d, PrepArgs a, const _
 // Each chain has a warp that issues its products; one more copies the chunks in, one ahead.
 //
 // REC is the backward's recording pass: no queries and no o; the parts of every chunk's entering
-// S, and of its U, go out as they lie in shared memory (a warp of its own copies them).  T fills
-// both halves of the second product, so that the warps of lanes 64..127, which have no queries
-// here, can write U's record while the others go on with the chain.
+// S, and of its residuals R, go out as they lie in shared memory (a warp of its own copies them).
+// Its second product is R = (I + N diag(alpha))^{-1} (V - e^c K S), and U = alpha R.  The inverse
+// fills both halves of that product, so that the warps of lanes 64..127, which have no queries
+// here, can write R's record while the others go on with the chain.
 //
 // Bound by the latency of the chain of three products and three epilogues a chunk, not by data
 // (10 to 30% of the DRAM rate) nor by the tensor pipe (33 to 45% busy).  A chunk of a single chain
@@ -293,14 +312,14 @@ template <int NCH, bool REC>
 struct ScanSmem {
     using C = Chain<NCH>;
     static constexpr uint32_t KQB = REC ? 8192 : 16384;              // a 64-dk block: K rows (and Q rows)
-    static constexpr uint32_t TPB = 16384;                           // an image part: T rows, P T rows (REC: T's again)
+    static constexpr uint32_t TPB = 16384;                           // an image part: T rows, P T rows (REC: the inverse twice)
     static constexpr uint32_t KQ = 0;                                // 2 stages x 2 blocks
     static constexpr uint32_t TP = 4 * KQB;
     static constexpr uint32_t V = TP + NP * TPB;                     // 2 stages
     static constexpr uint32_t S = V + 2 * 8192;                      // blocks of 128 rows
     static constexpr uint32_t X = S + C::blocks * 16384;             // blocks of 64 rows
-    static constexpr uint32_t U = X + C::blocks * 8192;              // REC: a tile of 64 rows a part
-    static constexpr uint32_t VEC = U + (REC ? C::blocks * 8192 : 0);   // 2 stages
+    static constexpr uint32_t R = X + C::blocks * 8192;              // REC: a tile of 64 rows a part
+    static constexpr uint32_t VEC = R + (REC ? C::blocks * 8192 : 0);   // 2 stages
     static constexpr uint32_t BAR = VEC + 2 * sizeof(GVec);
     static constexpr int bars = 4 + 2 + 1 + 1 + 9 * NCH;   // (per chain: 7, and its turn)
     static constexpr size_t bytes = 1024 + BAR + bars * 8 + 16;
@@ -314,14 +333,14 @@ struct ScanSmem {
 static_assert(ScanSmem<2, false>::bytes <= 232448 && ScanSmem<2, true>::bytes <= 232448, "shared memory per CTA");
 
 struct ScanArgs {
-    const unsigned char* img;
+    const unsigned char* img;   // (REC: the residuals' inverse)
     const GVec* vec;
     const float* S0;
     void* o;
     float* S_final;
     int slots;
     unsigned char* rec_S;   // [H][slots][slices][kRecS]
-    unsigned char* rec_U;   // [H][slots][slices][kRecU]
+    unsigned char* rec_R;   // [H][slots][slices][kRecU]
     const int* flags;       // [H][slots], or null: set as the chunks' preparations are complete
 };
 
@@ -338,9 +357,9 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
     uint64_t* freed = bars + 2;          // [2] by every chain
     uint64_t* full_tp = bars + 4;        // the image
     uint64_t* freed_tp = full_tp + 1;    // by every chain
-    uint64_t* s_free = freed_tp + 1;     // REC: S's and U's parts have been copied out
-    uint64_t* u_free = s_free + 1;
-    uint64_t* chain0 = u_free + 1;       // per chain: s_ready, x_ready, u_ready, r_ready (REC: U's parts), d1, d2, d3, turn
+    uint64_t* s_free = freed_tp + 1;     // REC: S's and R's parts have been copied out
+    uint64_t* r_free = s_free + 1;
+    uint64_t* chain0 = r_free + 1;       // per chain: s_ready, x_ready, u_ready, r_ready (REC: R's parts), d1, d2, d3, turn
     uint32_t* tslot = (uint32_t*)(bars + M::bars);
     const int b = bx / d.H, h = bx % d.H, hk = h / (d.H / d.Hk), c0 = by * 32 * NCH;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -355,7 +374,7 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
         mbar_init(full_tp, 1);
         mbar_init(freed_tp, NCH);
         mbar_init(s_free, 1);
-        mbar_init(u_free, 1);
+        mbar_init(r_free, 1);
         for (int g = 0; g < NCH; ++g) {
             uint64_t* q = chain0 + 9 * g;
             mbar_init(q + 0, M::EW);                        // s_ready (warps)
@@ -406,10 +425,10 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                 };
                 const auto load_tp = [&](int c) {
                     unsigned char* to = sm + M::TP;
-                    const unsigned char* from = a.img + (rec0 + c) * NP * 16384;
+                    const unsigned char* from = a.img + (rec0 + c) * NP * (REC ? 8192 : 16384);
                     mbar_arrive_expect_tx(full_tp, NP * M::TPB);
                     if (REC) {
-                        for (int p = 0; p < 2 * NP; ++p) bulk_g2s(to + p * 8192, from + p / 2 * 16384, 8192, full_tp);
+                        for (int p = 0; p < 2 * NP; ++p) bulk_g2s(to + p * 8192, from + p / 2 * 8192, 8192, full_tp);
                     } else {
                         bulk_g2s(to, from, NP * M::TPB, full_tp);
                     }
@@ -445,13 +464,13 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                     unsigned char* const to_S = a.rec_S + ((rec0 + c) * slices + by) * kRecS;
                     if (dbg_in(to_S, kRecS, a.rec_S, records(d, a.slots, kRecS), &g_gt2_status)) bulk_s2g(to_S, sm + M::S, kRecS);
                     bulk_commit();
-                    bulk_wait_read();   // (and the U of the chunk before)
+                    bulk_wait_read();   // (and the R of the chunk before)
                     mbar_arrive(s_free);
-                    if (c > 0) mbar_arrive(u_free);
+                    if (c > 0) mbar_arrive(r_free);
                     for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g + 3, ph, kWaitLimit);
                     if (!ok) break;
-                    unsigned char* const to_U = a.rec_U + ((rec0 + c) * slices + by) * kRecU;
-                    if (dbg_in(to_U, kRecU, a.rec_U, records(d, a.slots, kRecU), &g_gt2_status)) bulk_s2g(to_U, sm + M::U, kRecU);
+                    unsigned char* const to_R = a.rec_R + ((rec0 + c) * slices + by) * kRecU;
+                    if (dbg_in(to_R, kRecU, a.rec_R, records(d, a.slots, kRecU), &g_gt2_status)) bulk_s2g(to_R, sm + M::R, kRecU);
                     bulk_commit();
                 }
                 bulk_wait_read();
@@ -543,9 +562,11 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
             if (!(ok = warp_wait(&full[c & 1], (c >> 1) & 1))) break;
             const float up = vec->up[i], last = vec->up[63];
             if (top) {
-                // X = alpha V - (alpha e^c) K S; rows past the end are zero whatever lies there
+                // X = alpha V - (alpha e^c) K S (REC: without alpha, which R takes on its way to U); rows past the
+                // end are zero whatever lies there
                 const bool live = i < n;
-                const float2 al = both(vec->al[i]), au = both(-vec->al[i] * up), rest = both(vec->rest[i]);
+                const float xa = REC ? 1.f : vec->al[i], ua = REC ? vec->al[i] * vec->rest[i] : vec->rest[i];
+                const float2 al = both(xa), au = both(-xa * up);
                 const unsigned char* vt = sm + M::V + (c & 1) * 8192;
                 uint4 vw[CW / 8];
 #pragma unroll
@@ -563,15 +584,15 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                 if (!(ok = warp_wait(q + 5, ph))) break;
                 tmem_sum<NP>(t2, 32, y);
 #pragma unroll
-                for (int m = 0; m < CW / 2; ++m) y[m] = mul2(rest, y[m]);
+                for (int m = 0; m < CW / 2; ++m) y[m] = mul2(both(ua), y[m]);
                 C::put(sm + M::X, 8192, g, i, cc, y);
                 warp_arrive(q + 2, lane);
-            } else if (REC) {   // U once more: its record
+            } else if (REC) {   // R once more: its record
                 if (!(ok = warp_wait(q + 5, ph))) break;
-                float2 U[CW / 2];
-                tmem_sum<NP>(t2, 32, U);
-                if (c > 0 && !(ok = warp_wait(u_free, ph ^ 1u))) break;
-                put_parts(sm + M::U, i, g * 32 + cc, U);
+                float2 R[CW / 2];
+                tmem_sum<NP>(t2, 32, R);
+                if (c > 0 && !(ok = warp_wait(r_free, ph ^ 1u))) break;
+                put_parts(sm + M::R, i, g * 32 + cc, R);
                 warp_arrive(q + 3, lane);
             } else {
                 if (!(ok = warp_wait(q + 4, ph))) break;
@@ -617,7 +638,7 @@ __global__ void __launch_bounds__((ScanSmem<NCH, REC>::warps * 32), 1)
 // chunks in the order in which the scans come to them.
 struct LongSmem {
     static constexpr int groups = 3, threads = 128 * groups;
-    static constexpr size_t group = PrepSmem::bytes / 1024 * 1024 + 1024;
+    static constexpr size_t group = PrepSmem<false>::bytes / 1024 * 1024 + 1024;
     static constexpr size_t scan = ScanSmem<1, false>::bytes;
     static constexpr size_t bytes = groups * group > scan ? groups * group : scan;
 };
@@ -632,7 +653,7 @@ __global__ void __launch_bounds__(LongSmem::threads, 1)
         scan_cta<1, Tout, false>(d, a, tm_q, tm_k, tm_v, blockIdx.x % bh, blockIdx.x / bh, slices);
         return;
     }
-    using M = PrepSmem;
+    using M = PrepSmem<false>;
     extern __shared__ unsigned char raw[];
     const int gid = threadIdx.x >> 7, tid = threadIdx.x & 127;
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023) + gid * LongSmem::group;
@@ -660,7 +681,7 @@ __global__ void __launch_bounds__(LongSmem::threads, 1)
         const SeqAt s = seq_at(d, b, kGC);
         if (c * kGC >= s.len) continue;
         const int slot = s.slot0 + c;
-        ok = prep_chunk(d, p, &tm_q, &tm_k, sm, 1 + gid, tid, slot, h, s, ph, tslot, flags + (size_t)h * p.slots + slot);
+        ok = prep_chunk<false>(d, p, &tm_q, &tm_k, sm, 1 + gid, tid, slot, h, s, ph, tslot, flags + (size_t)h * p.slots + slot);
         ph ^= 1;
         group_sync(1 + gid);
     }
@@ -713,10 +734,11 @@ cudaError_t scan(const GDims& d, const ScanArgs& a, const Maps& m, cudaStream_t 
     return e;
 }
 
+template <bool BWD>
 cudaError_t prep(const GDims& d, const PrepArgs& a, const Maps& m, cudaStream_t st) {
-    cudaError_t e = smem_attr(k_gt_prep, PrepSmem::bytes);
+    cudaError_t e = smem_attr(k_gt_prep<BWD>, PrepSmem<BWD>::bytes);
     if (e != cudaSuccess) return e;
-    k_gt_prep<<<dim3(a.slots, d.H), 128, PrepSmem::bytes, st>>>(d, a, m.q, m.k);
+    k_gt_prep<BWD><<<dim3(a.slots, d.H), 128, PrepSmem<BWD>::bytes, st>>>(d, a, m.q, m.k);
     prof_mark("gated_prep_tc", st);
     return cudaGetLastError();
 }
@@ -766,13 +788,13 @@ cudaError_t fwd(const GDims& d, const void* q, const void* k, const void* v, con
         cfg.stream = st;
         cfg.attrs = &coop;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, k, d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f},
+        e = cudaLaunchKernelEx(&cfg, k, d, PrepArgs{g, beta, w.img, w.vec, slots, nullptr},
                                ScanArgs{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr, flags}, flags, (d.dv + 31) / 32,
                                m.q, m.k, m.v);
         prof_mark("gated_long_tc", st);
         return e;
     }
-    if (e == cudaSuccess) e = prep(d, PrepArgs{g, beta, w.img, w.vec, slots, 0.f}, m, st);
+    if (e == cudaSuccess) e = prep<false>(d, PrepArgs{g, beta, w.img, w.vec, slots, nullptr}, m, st);
     if (e != cudaSuccess) return e;
     const ScanArgs a{w.img, w.vec, S0, o, S_final, slots, nullptr, nullptr, nullptr};
     return narrow ? scan<1, Tout>(d, a, m, st) : scan<2, Tout>(d, a, m, st);
@@ -794,22 +816,22 @@ cudaError_t launch_gated_fwd_tc(const GDims& d, const void* q, const void* k, co
 }
 
 cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
-                                 float floor_alpha, unsigned char* img, GVec* vec, cudaStream_t st) {
+                                 unsigned char* img, unsigned char* img_r, GVec* vec, cudaStream_t st) {
     Maps m{};
     const int nb = d.packed ? 1 : d.B;
     cudaError_t e = strided_rows_map(&m.q, q, d.dk, d.L, d.Hk, nb, d.qs);
     if (e == cudaSuccess) e = strided_rows_map(&m.k, k, d.dk, d.L, d.Hk, nb, d.ks);
     if (e != cudaSuccess) return e;
-    return prep(d, PrepArgs{g, beta, img, vec, d.slots(kGC), floor_alpha}, m, st);
+    return prep<true>(d, PrepArgs{g, beta, img, vec, d.slots(kGC), img_r}, m, st);
 }
 
 cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
-                                   const unsigned char* img, const GVec* vec, unsigned char* rec_S, unsigned char* rec_U,
+                                   const unsigned char* img_r, const GVec* vec, unsigned char* rec_S, unsigned char* rec_R,
                                    cudaStream_t st) {
     Maps m{};
     const cudaError_t e = make_maps(d, q, k, v, &m);
     if (e != cudaSuccess) return e;
-    return scan<2, float, true>(d, ScanArgs{img, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_U, nullptr}, m, st);
+    return scan<2, float, true>(d, ScanArgs{img_r, vec, S0, nullptr, nullptr, d.slots(kGC), rec_S, rec_R, nullptr}, m, st);
 }
 
 cudaError_t gated_tc_status_read_clear(unsigned int* status) {

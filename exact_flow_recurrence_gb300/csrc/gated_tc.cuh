@@ -250,12 +250,13 @@ inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
     return e;
 }
 
-// The backward's parts of gated_tc.cu: the preparation (alpha at least `floor_alpha` in magnitude), and the pass that records every chunk's S and U as parts, in the operand layout
+// The backward's parts of gated_tc.cu: the preparation, with the image of the residuals' inverse, and
+// the pass that records every chunk's S and residuals R as parts, in the operand layout
 // ([H][slots][slices of 64 columns][kRecS or kRecU bytes]).
 cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
-                                 float floor_alpha, unsigned char* img, GVec* vec, cudaStream_t st);
+                                 unsigned char* img, unsigned char* img_r, GVec* vec, cudaStream_t st);
 cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
-                                   const unsigned char* img, const GVec* vec, unsigned char* rec_S, unsigned char* rec_U,
+                                   const unsigned char* img_r, const GVec* vec, unsigned char* rec_S, unsigned char* rec_R,
                                    cudaStream_t st);
 
 }  // namespace efla

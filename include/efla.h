@@ -234,6 +234,8 @@ efla_status efla_fwd_noalloc(const efla_shape* shape,
  * alpha_t = beta_t (EFLA_EULER, the gated delta rule) or (1 - e^{-beta_t lambda_t}) / lambda_t,
  * lambda_t = ||k_t||^2 (EFLA_EXACT).  With g = 0 and Hk = H this is efla_fwd's recurrence.
  * Value head h reads the query and key of head h / (H / Hk): H must be a multiple of Hk.
+ * beta = 0 masks a token (alpha = 0): its key and value, of any size whose products are finite
+ * in fp32, reach no other token's results and no state, forward and backward.
  *
  * Arrays are reached through strides in elements, {batch, head, token}, their last dimension
  * contiguous: q, k [B,Hk,L,dk], v, o, dO [B,H,L,dv] (dtype; o, dq, dk, dv out_dtype),

@@ -33,3 +33,63 @@ def test_output_does_not_depend_on_the_state_asked_for(shape):
         without = efla.efla_gated_fwd(*a, out_dtype=out, path=efla.TENSOR, want_state=False)
         efla.efla_get_status()
         assert without[1] is None and torch.equal(with_state[0], without[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("mode", [efla.EULER, efla.EXACT])
+@pytest.mark.parametrize("size", [1.0, 1e12])
+def test_masked_tokens_of_any_size(size, mode, dtype):
+    """beta = 0 masks a token: whatever its key and value (as long as products of keys are finite), the others'
+    results are those of the definition, and so is its own beta's gradient."""
+    x = draw(1, 4, 2, 200, 128, 64, dtype, mode, rate=0.1, seed=23)
+    mask = torch.zeros(200, dtype=torch.bool)
+    mask[[0, 20, 21, 22, 63, 64, 130, 199]] = True
+    gen = torch.Generator().manual_seed(24)
+    for n in ("k", "v"):
+        x[n][:, :, mask] = (size * torch.randn(x[n][:, :, mask].shape, generator=gen)).to(dtype)
+    x["beta"][:, :, mask] = 0.0
+    o, S, d = run(x, mode)
+    (o_ref, S_ref), g_ref = ref64(x, mode)
+    assert_close("o", o, o_ref, TOL_F32)
+    assert_close("S_final", S, S_ref, TOL_F32)
+    for n, a, b in zip(GRADS, d, g_ref):
+        if n == "dS0":
+            assert_close(n, a, b, TOL_F32)
+            continue
+        assert_close(n, a[:, :, ~mask], b[:, :, ~mask], TOL_F32)
+        if n in ("dk", "dv"):
+            assert float(a[:, :, mask].abs().max()) == 0.0, n
+        else:
+            assert_close(n + " of the masked", a[:, :, mask], b[:, :, mask], TOL_F32)
+
+
+@pytest.mark.parametrize("beta", [0.0, 1e-30])
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** 40])
+def test_masked_tokens_at_scales(scale, beta):
+    """beta's gradient where beta is zero or next to it, with values far from 1."""
+    x = draw(1, 2, 2, 100, 128, 128, BF, efla.EULER, seed=25)
+    x["v"], x["S0"] = (x["v"].float() * scale).to(BF), x["S0"] * scale
+    x["dO"], x["dS"] = (x["dO"].float() / scale).to(BF), x["dS"] / scale
+    x["beta"][:, :, 10:50] = beta
+    d = run(x, efla.EULER)[2]
+    for n, a, b in zip(GRADS, d, ref64(x, efla.EULER)[1]):
+        assert_close(n, a, b, TOL_F32)
+        if n == "dbeta":
+            assert_close("dbeta of the masked", a[:, :, 10:50], b[:, :, 10:50], TOL_F32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_keys_in_exact_mode(dtype):
+    """||k||^2 about 1e26: alpha is 1 / ||k||^2, a projection, and stays one in the gradients."""
+    x = draw(1, 2, 2, 150, 128, 128, dtype, efla.EXACT, rate=0.1, seed=26)
+    x["k"][:, 0] = (x["k"][:, 0].float() * 2.0 ** 43).to(dtype)
+    o, S, d = run(x, efla.EXACT)
+    (o_ref, S_ref), g_ref = ref64(x, efla.EXACT)
+    for h in (0, 1):   # (each head on the scale of its own)
+        assert_close("o", o[:, h], o_ref[:, h], TOL_F32)
+        assert_close("S_final", S[:, h], S_ref[:, h], TOL_F32)
+        for n, a, b in zip(GRADS, d, g_ref):
+            if n == "dbeta" and h == 0:   # e^{-beta ||k||^2} of it
+                assert float(a[:, h].abs().max()) == 0.0
+            elif n != "dk" or h == 1:
+                assert_close(n, a[:, h], b[:, h], TOL_F32)
