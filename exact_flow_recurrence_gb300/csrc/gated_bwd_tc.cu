@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 }
                 const float up = vec.up[i], rest = vec.rest[i];
                 const float2 sa = both(top ? up : -al * up), rs2 = both(al * rest);
-                const float2 dl = both(top ? 0.f : 2.f * m.da[i] * dalpha_dlambda_of(be, m.lam[i], d.euler));
+                const float2 dl = both(top ? 0.f : 2.f * dlambda_of(m.da[i], be, m.lam[i], d.euler));
                 float2 dot = both(0.f), dot2 = both(0.f);
                 Tout* out = top ? (Tout*)a.dq + at3(d.dqs, s.batch, hk, t + i) : (Tout*)a.dk + at3(d.dks, s.batch, hk, t + i);
                 ok = warp_wait(&m.d5, hc & 1);

@@ -48,6 +48,15 @@ __device__ __forceinline__ long long at3(const long long (&s)[3], int b, int h, 
     return b * s[0] + h * s[1] + t * s[2];
 }
 
+// da dalpha/dlambda.  Away from x = beta lambda = 0 it is da (x e^{-x} + expm1(-x)) / lambda^2, and lambda
+// divides each factor by itself: its square, and the derivative alone, leave fp32's range for keys of
+// ||k|| = 1e10 and more, where the product does not.
+__device__ __forceinline__ float dlambda_of(float da, float beta, float lambda, int euler) {
+    const float x = beta * lambda;
+    if (euler || fabsf(x) < 0.5f) return da * dalpha_dlambda_of(beta, lambda, euler);
+    return da / lambda * ((x * expf(-x) + expm1f(-x)) / lambda);
+}
+
 // Sums of log decays inside a chunk.  A decay below e^-128 is zero in fp32, so g is taken as at
 // least -128 there: an infinite one (a state reset) then leaves no inf - inf behind.  The sums
 // c_i are kept as two floats (hi + lo), since e^{c_i - c_j} needs the difference's absolute

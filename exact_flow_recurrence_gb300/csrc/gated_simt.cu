@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kNT, 2) k_gated_grad(GDims d, const Tin* q, co
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = wp + 8 * r;
-            const float dl = i < n ? 2.f * m.da[i] * dalpha_dlambda_of(m.be[i], m.lam[i], d.euler) : 0.f;
+            const float dl = i < n ? 2.f * dlambda_of(m.da[i], m.be[i], m.lam[i], d.euler) : 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (lane + 32 * c < dk) ak[r][c] = fmaf(dl, m.K[i * kLd + lane + 32 * c], ak[r][c]);

@@ -93,3 +93,13 @@ def test_long_keys_in_exact_mode(dtype):
                 assert float(a[:, h].abs().max()) == 0.0
             elif n != "dk" or h == 1:
                 assert_close(n, a[:, h], b[:, h], TOL_F32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("power", [30, 43])
+def test_key_gradient_of_long_keys_in_exact_mode(power, dtype):
+    """dk through ||k||^2, where 1 / ||k||^4 is below what fp32 holds."""
+    x = draw(1, 2, 2, 70, 128, 128, dtype, efla.EXACT, rate=0.1, seed=28)
+    x["k"] = (x["k"].float() * 2.0 ** power).to(dtype)
+    d = run(x, efla.EXACT)[2]
+    assert_close("dk", d[1], ref64(x, efla.EXACT)[1][1], TOL_F32)
