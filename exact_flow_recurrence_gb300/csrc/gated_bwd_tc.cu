@@ -6,8 +6,7 @@
 //   k_gt_rscan               the chunks backwards: G (the gradient of the state that leaves the
 //                            chunk) and dX; dv = alpha dX; dS0
 //   k_gt_grad                every chunk at once: dq, dk, dg, dbeta
-// dg and dbeta are fp32 results of the whole chain, so every computed operand enters as three
-// bf16 parts (about fp32 accuracy); only the last products, which reach dq and dk alone, take two.
+// Every computed operand enters as three bf16 parts (about fp32 accuracy), whatever the outputs' type.
 //
 // The two scans need nothing of each other and run side by side where their CTAs find SMs (B7 H8
 // T6001 packed, dv 64: 56 CTAs each; the backward takes 0.26 ms, 0.40 ms one after the other).
@@ -382,7 +381,7 @@ constexpr uint32_t kGrAX = 32768;                // dO | dX_0 | 0 | dX_1 | 0 | d
 constexpr uint32_t kGrR = kGrAX + 49152;         // R_0 | R_1 | R_2 (as an A operand, the tile before fills rows 0..63)
 constexpr uint32_t kGrS = kGrR + 24576;          // 3 blocks of 128 rows: Chain<2>
 constexpr uint32_t kGrG = kGrS + 49152;          // likewise
-constexpr uint32_t kGrP5 = kGrS;                 // [dPD; dAD], two parts, in S's place
+constexpr uint32_t kGrP5 = kGrS;                 // [dPD; dAD], a block of 128 rows a part, in S's place
 constexpr uint32_t kGrMisc = kGrG + 49152;
 constexpr uint32_t kGrZero = kGrAX + 16384;      // a tile of zeros
 // tensor-memory columns; D5 lies over D3 and D3s (the small part pairs of D3), which are read before it starts
@@ -653,13 +652,13 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 if (!ok || !(ok = warp_wait(&m.p5, hc & 1))) break;
                 if (one) {
 #pragma unroll
-                    for (int p = 1; p >= 0; --p) {
+                    for (int p = NP - 1; p >= 0; --p) {   // (q and k are one part)
                         const uint64_t a0 = sdesc_sw128(p5 + p * 16384);
                         const uint64_t at = sdesc_sw128(z0, p5 + p * 16384 + 8192 - z0);   // [0 | dAD], rows are K indices
                         const uint64_t pt = sdesc_sw128(z0, p5 + p * 16384 - z0);          // [0 | dPD]
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_f16_ss(tb + cD5, a0 + ks * 2, kb + ks * 128, idesc_f16(128, 128, false, true, true), p < 1 || ks > 0);
+                            mma_f16_ss(tb + cD5, a0 + ks * 2, kb + ks * 128, idesc_f16(128, 128, false, true, true), p < NP - 1 || ks > 0);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             mma_f16_ss(tb + cD5, at + ks * 128, kb + ks * 128, idesc_f16(128, 128, true, true, true), 1u);
@@ -779,10 +778,10 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                 if (!(ok = group_sync_and(1, ok, 256))) break;                  // (the warps leave together if a wait gave up)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint4 w[2];
-                    split8<2>(w5 + 4 * k, w);
+                    uint4 w[NP];
+                    split8<NP>(w5 + 4 * k, w);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p)
+                    for (int p = 0; p < NP; ++p)
                         *reinterpret_cast<uint4*>(sm + kGrP5 + p * 16384 + sw128(row, 32 * cg + 8 * k)) = w[p];
                 }
                 warp_arrive(&m.p5, lane);

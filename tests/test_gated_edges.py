@@ -103,3 +103,14 @@ def test_key_gradient_of_long_keys_in_exact_mode(power, dtype):
     x["k"] = (x["k"].float() * 2.0 ** power).to(dtype)
     d = run(x, efla.EXACT)[2]
     assert_close("dk", d[1], ref64(x, efla.EXACT)[1][1], TOL_F32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_fp32_gradients_carry_fp32(dtype):
+    """dq and dk of an fp32 call, by the norm of their error: about eight products of up to 128 terms one
+    after another, sqrt(128) 2^-24 each, are 2e-6 of the result (an operand of 17 bits would add 4e-6)."""
+    x = draw(1, 2, 2, 200, 128, 128, dtype, efla.EULER, rate=0.1, seed=22)
+    d = run(x, efla.EULER)[2]
+    for n, a, b in zip(GRADS, d, ref64(x, efla.EULER)[1]):
+        err = float((a.double().cpu() - b).norm() / b.norm())
+        assert err <= 2e-6, (n, err)
