@@ -498,10 +498,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
     const auto place = [&](long long x, int& hk, int& slot, int& b, SeqAt& s, int& t0) {
         hk = (int)(x % d.Hk);
         slot = (int)(x / d.Hk);
-        b = seq_of_slot(d, slot, kGC);
-        s = seq_at(d, b, kGC);
-        t0 = (slot - s.slot0) * kGC;
-        return min(kGC, s.len - t0);
+        return chunk_at(d, slot, kGC, b, s, t0);
     };
     if (warp == 9) {
         // ---------------- copies in

@@ -32,7 +32,8 @@ __device__ __forceinline__ SeqAt seq_at(const GDims& d, int b, int C) {
     return s;
 }
 
-// The sequence that chunk slot `slot` belongs to (slot0(b) <= slot < slot0(b + 1)).
+// The sequence that chunk slot `slot` belongs to (slot0(b) <= slot < slot0(b + 1)); slots before the first
+// sequence's (packed tokens may start past 0) count as sequence 0's, in front of its first chunk.
 __device__ __forceinline__ int seq_of_slot(const GDims& d, int slot, int C) {
     if (!d.packed) return slot / ((d.L + C - 1) / C);
     int lo = 0, hi = d.B - 1;
@@ -42,6 +43,15 @@ __device__ __forceinline__ int seq_of_slot(const GDims& d, int slot, int C) {
         else hi = mid - 1;
     }
     return lo;
+}
+
+// The tokens of chunk slot `slot`: the sequence b and its place s, the chunk's first token t0 in it, and how
+// many there are (none: the slot holds no chunk).
+__device__ __forceinline__ int chunk_at(const GDims& d, int slot, int C, int& b, SeqAt& s, int& t0) {
+    b = seq_of_slot(d, slot, C);
+    s = seq_at(d, b, C);
+    t0 = (slot - s.slot0) * C;
+    return t0 < 0 ? 0 : min(C, s.len - t0);
 }
 
 __device__ __forceinline__ long long at3(const long long (&s)[3], int b, int h, int t) {

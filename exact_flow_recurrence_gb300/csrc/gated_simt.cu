@@ -346,9 +346,9 @@ __global__ void __launch_bounds__(kNT, 2) k_gated_grad(GDims d, const Tin* q, co
     GradSmem& m = *reinterpret_cast<GradSmem*>(gsm);
     const int slot = blockIdx.x, hk = blockIdx.y, rep = d.H / d.Hk, tid = threadIdx.x, dk = d.dk, dv = d.dv;
     const int wp = tid >> 5, lane = tid & 31;
-    const int b = seq_of_slot(d, slot, kC);
-    const SeqAt s = seq_at(d, b, kC);
-    const int t0 = (slot - s.slot0) * kC, n = min(kC, s.len - t0), t = s.start + t0;
+    int b, t0;
+    SeqAt s;
+    const int n = chunk_at(d, slot, kC, b, s, t0), t = s.start + t0;
     if (n <= 0) return;
     load_rows(m.K, kLd, k + at3(d.ks, s.batch, hk, t), d.ks[2], n, dk);
     load_rows(m.Q, kLd, q + at3(d.qs, s.batch, hk, t), d.qs[2], n, dk);

@@ -269,8 +269,9 @@ __global__ void __launch_bounds__(128, BWD ? 3 : 4) k_gt_prep(GDims d, PrepArgs 
     extern __shared__ unsigned char raw[];
     unsigned char* sm = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     const int slot = blockIdx.x, tid = threadIdx.x;
-    const SeqAt s = seq_at(d, seq_of_slot(d, slot, kGC), kGC);
-    if ((slot - s.slot0) * kGC >= s.len) return;
+    int b, t0;
+    SeqAt s;
+    if (chunk_at(d, slot, kGC, b, s, t0) <= 0) return;
     uint64_t* bar = (uint64_t*)(sm + M::BAR);
     uint32_t* tslot = (uint32_t*)(bar + 3);
     if (tid == 0) {

@@ -114,3 +114,36 @@ def test_fp32_gradients_carry_fp32(dtype):
     for n, a, b in zip(GRADS, d, ref64(x, efla.EULER)[1]):
         err = float((a.double().cpu() - b).norm() / b.norm())
         assert err <= 2e-6, (n, err)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ends", [[150, 250, 250, 391], [40, 41], [300, 300]])
+def test_tokens_outside_every_sequence(ends, dtype):
+    """Tokens before the first offset and behind the last: not read (they are NaN), not written."""
+    H, Hk, dk, dv, T = 4, 2, 128, 64, 420
+    x = draw(1, H, Hk, T, dk, dv, dtype, efla.EULER, seed=27, state=False)
+    live = torch.zeros(T, dtype=torch.bool)
+    live[ends[0]:ends[-1]] = True
+    y = {n: t[0].clone() for n, t in x.items() if t is not None}
+    for t in y.values():
+        t[:, ~live] = float("nan")
+    y = {n: t.to(DEV) for n, t in y.items()}
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    args = [y[n] for n in ("q", "k", "v", "g", "beta")]
+    for out in (F32, BF):
+        o, dq, dk_, dv_ = (torch.full_like(y[n], 7.0, dtype=out) for n in ("v", "q", "k", "v"))
+        _, S = efla.efla_gated_fwd(*args, offsets=off, o=o, out_dtype=out)
+        d = efla.efla_gated_bwd(*args, y["dO"], offsets=off, out_dtype=out, dq=dq, dk=dk_, dv=dv_)
+        efla.efla_get_status()
+        for n, t in (("o", o), ("dq", dq), ("dk", dk_), ("dv", dv_)):
+            assert bool((t[:, ~live.to(DEV)] == 7.0).all()), n
+        for b, (a, e) in enumerate(zip(ends, ends[1:])):
+            if a == e:
+                assert float(S[b].abs().max()) == 0.0
+                continue
+            s = {n: None if t is None else t[:, :, a:e] for n, t in x.items()}
+            (o_ref, S_ref), g_ref = ref64(s, efla.EULER)
+            assert_close("o", o[None, :, a:e], o_ref, TOL_F32, stored_bf16=out == BF)
+            assert_close("S_final", S[b:b + 1], S_ref, TOL_F32)
+            for n, got, want in zip(GRADS[:5], d, g_ref):
+                assert_close(n, got[None, :, a:e], want, TOL_F32, stored_bf16=got.dtype == BF)
