@@ -372,7 +372,7 @@ def efla_step(q, k, v, beta, S, *, out_dtype=None, mode: int = EXACT, o=None, st
 
 # ------------------------------------------------------------------ gated delta rule
 # A call's geometry (sizes, strides, types, mode) is checked and put into the C struct once, and kept
-# by its values; what a call still checks is that its tensors have that geometry.
+# by its values; what a call still checks is that its tensors have that geometry and lie on one device.
 _plans: dict = {}
 
 
@@ -385,28 +385,52 @@ def _plan(key, make):
     return p
 
 
-def _elsewhere(stream, fn, *args, **kw):
-    """The call on another stream: its fresh outputs and workspace come from that stream's memory pool,
-    where its earlier work, and nothing else's, may still be using them."""
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(s):
-        return fn(*args, **kw)
+def _away(t: torch.Tensor, stream) -> bool:
+    """Whether the call has to go to another stream, or to another device than the current one."""
+    return stream is not None or (t.is_cuda and t.get_device() != torch.cuda.current_device())
+
+
+def _elsewhere(t: torch.Tensor, stream, fn, *args, **kw):
+    """The call on t's device, where its kernels, their attributes and its stream belong, and on `stream`
+    if there is one: its fresh outputs and workspace come from that stream's memory pool, where its
+    earlier work, and nothing else's, may still be using them."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    with torch.cuda.device(t.device):
+        if stream is None:
+            return fn(*args, **kw)
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=t.device)
+        if s.device != t.device:
+            raise ValueError(f"stream: expected one of {t.device}, got one of {s.device}")
+        with torch.cuda.stream(s):
+            return fn(*args, **kw)
 
 
 def _current(t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _ws(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+def _ws(nbytes: int, t: torch.Tensor, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    """The caller's workspace as given (the library checks its size), else a fresh one beside t."""
+    if ws is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=t.device)
+    _at(ws, "workspace", t.get_device())
+    return ws
 
 
-def _is(t: Optional[torch.Tensor], name: str, shape, dtype, contiguous: bool = False):
-    """Pointer of a CUDA tensor that has to have this shape and type (None stays None)."""
-    if t is None:
-        return None
+def _at(t: torch.Tensor, name: str, dev: int):
     if not t.is_cuda:
         raise ValueError(f"{name}: tensors must be CUDA tensors")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+
+
+def _is(t: Optional[torch.Tensor], name: str, dev: int, shape, dtype, contiguous: bool = False):
+    """Pointer of a tensor that has to lie on CUDA device `dev` and have this shape and type (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != dev:
+        _at(t, name, dev)
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
@@ -468,8 +492,10 @@ class _GatedPlan:
 
 
 def _batch(v, offsets):
+    _at(v, "v", v.get_device())
     if offsets is None:
         return v.shape[0]
+    _at(offsets, "offsets", v.get_device())
     if not offsets.is_cuda or offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 \
             or not offsets.is_contiguous():
         raise ValueError("offsets: expected a contiguous CUDA int32 tensor [B + 1]")
@@ -484,10 +510,10 @@ def efla_gated_fwd(q, k, v, g, beta, S0=None, *, offsets=None, out_dtype=None, m
     [B,H,L] fp32, S0 [B,H,dk,dv] fp32.  With offsets (int32 [B+1] on the GPU) the sequences are packed
     on one axis of tokens: q, k [Hk,T,dk], v [H,T,dv], g, beta [H,T].
     Returns (o, in v's order of storage, S_final [B,H,dk,dv] fp32 or None)."""
-    if stream is not None:
-        return _elsewhere(stream, efla_gated_fwd, q, k, v, g, beta, S0, offsets=offsets, out_dtype=out_dtype, mode=mode, o=o,
+    if _away(v, stream):
+        return _elsewhere(v, stream, efla_gated_fwd, q, k, v, g, beta, S0, offsets=offsets, out_dtype=out_dtype, mode=mode, o=o,
                           S_final=S_final, workspace=workspace, want_state=want_state, path=path)
-    dt, B = v.dtype, _batch(v, offsets)
+    dt, B, dev = v.dtype, _batch(v, offsets), v.get_device()
     odt = dt if out_dtype is None else out_dtype
     if o is None:
         o = torch.empty_like(v, dtype=odt)
@@ -497,12 +523,13 @@ def efla_gated_fwd(q, k, v, g, beta, S0=None, *, offsets=None, out_dtype=None, m
         dict(zip(("q", "k", "v", "g", "beta", "o"), strides)), False))
     if S_final is None and want_state:
         S_final = torch.empty(pl.state, dtype=torch.float32, device=v.device)
-    ws = _ws(pl.ws, v.device) if workspace is None else workspace
+    ws = _ws(pl.ws, v, workspace)
     f32 = torch.float32
     rc = load_library().efla_gated_fwd(
-        pl.ref, None if offsets is None else offsets.data_ptr(), _is(q, "q", pl.q, dt), _is(k, "k", pl.q, dt),
-        _is(v, "v", pl.v, dt), _is(g, "g", pl.s, f32), _is(beta, "beta", pl.s, f32), _is(S0, "S0", pl.state, f32, True),
-        _is(o, "o", pl.v, odt), _is(S_final, "S_final", pl.state, f32, True), _ptr(ws), ws.numel() * ws.element_size(),
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(q, "q", dev, pl.q, dt), _is(k, "k", dev, pl.q, dt),
+        _is(v, "v", dev, pl.v, dt), _is(g, "g", dev, pl.s, f32), _is(beta, "beta", dev, pl.s, f32),
+        _is(S0, "S0", dev, pl.state, f32, True),
+        _is(o, "o", dev, pl.v, odt), _is(S_final, "S_final", dev, pl.state, f32, True), _ptr(ws), ws.numel() * ws.element_size(),
         _current(v))
     _check(rc, "efla_gated_fwd")
     return o, S_final
@@ -514,10 +541,10 @@ def efla_gated_bwd(q, k, v, g, beta, dO, S0=None, dS_final=None, *, offsets=None
     """Backward of efla_gated_fwd (same shapes; dO as v).  Returns (dq, dk, dv, dg, dbeta, dS0 or None):
     dq, dk, dv in the order of storage of q, k, v, or into the tensors given (which may be slices of one
     buffer); dg, dbeta fp32, dense."""
-    if stream is not None:
-        return _elsewhere(stream, efla_gated_bwd, q, k, v, g, beta, dO, S0, dS_final, offsets=offsets, out_dtype=out_dtype,
+    if _away(v, stream):
+        return _elsewhere(v, stream, efla_gated_bwd, q, k, v, g, beta, dO, S0, dS_final, offsets=offsets, out_dtype=out_dtype,
                           mode=mode, dq=dq, dk=dk, dv=dv, want_dS0=want_dS0, workspace=workspace, path=path)
-    dt, B, f32 = v.dtype, _batch(v, offsets), torch.float32
+    dt, B, f32, dev = v.dtype, _batch(v, offsets), torch.float32, v.get_device()
     odt = dt if out_dtype is None else out_dtype
     dq = torch.empty_like(q, dtype=odt) if dq is None else dq
     dk = torch.empty_like(k, dtype=odt) if dk is None else dk
@@ -530,12 +557,13 @@ def efla_gated_bwd(q, k, v, g, beta, dO, S0=None, dS_final=None, *, offsets=None
     dg = torch.empty(pl.s, dtype=f32, device=v.device)
     db = torch.empty(pl.s, dtype=f32, device=v.device)
     dS0 = torch.empty(pl.state, dtype=f32, device=v.device) if want_dS0 else None
-    ws = _ws(pl.ws, v.device) if workspace is None else workspace
+    ws = _ws(pl.ws, v, workspace)
     rc = load_library().efla_gated_bwd(
-        pl.ref, None if offsets is None else offsets.data_ptr(), _is(q, "q", pl.q, dt), _is(k, "k", pl.q, dt),
-        _is(v, "v", pl.v, dt), _is(g, "g", pl.s, f32), _is(beta, "beta", pl.s, f32), _is(S0, "S0", pl.state, f32, True),
-        _is(dO, "dO", pl.v, dt), _is(dS_final, "dS_final", pl.state, f32, True), _is(dq, "dq", pl.q, odt),
-        _is(dk, "dk", pl.q, odt), _is(dv, "dv", pl.v, odt), dg.data_ptr(), db.data_ptr(), _ptr(dS0), _ptr(ws),
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(q, "q", dev, pl.q, dt), _is(k, "k", dev, pl.q, dt),
+        _is(v, "v", dev, pl.v, dt), _is(g, "g", dev, pl.s, f32), _is(beta, "beta", dev, pl.s, f32),
+        _is(S0, "S0", dev, pl.state, f32, True),
+        _is(dO, "dO", dev, pl.v, dt), _is(dS_final, "dS_final", dev, pl.state, f32, True), _is(dq, "dq", dev, pl.q, odt),
+        _is(dk, "dk", dev, pl.q, odt), _is(dv, "dv", dev, pl.v, odt), dg.data_ptr(), db.data_ptr(), _ptr(dS0), _ptr(ws),
         ws.numel() * ws.element_size(), _current(v))
     _check(rc, "efla_gated_bwd")
     return dq, dk, dv, dg, db, dS0
@@ -563,9 +591,9 @@ def efla_gated_step(q, k, v, g, beta, S, *, slots=None, out_dtype=None, mode: in
     q, k [B,Hk,dk], v [B,H,dv] (any strides, last dimension contiguous), g, beta [B,H] fp32.  slots (int32
     [B] on the GPU): each sequence's place in the cache (outside [0, n): skipped, o = 0); None: place b.
     Returns o [B,H,dv]."""
-    if stream is not None:
-        return _elsewhere(stream, efla_gated_step, q, k, v, g, beta, S, slots=slots, out_dtype=out_dtype, mode=mode, o=o)
-    dt, f32 = v.dtype, torch.float32
+    if _away(v, stream):
+        return _elsewhere(v, stream, efla_gated_step, q, k, v, g, beta, S, slots=slots, out_dtype=out_dtype, mode=mode, o=o)
+    dt, f32, dev = v.dtype, torch.float32, v.get_device()
     odt = dt if out_dtype is None else out_dtype
     if o is None:
         o = torch.empty_like(v, dtype=odt)
@@ -573,9 +601,9 @@ def efla_gated_step(q, k, v, g, beta, S, *, slots=None, out_dtype=None, mode: in
     pl = _plan(("gs", q.shape, v.shape, S.shape, strides, dt, odt, mode), lambda: _StepPlan(
         q.shape, v.shape, S.shape, dt, odt, mode, dict(zip(("q", "k", "v", "g", "beta", "o"), strides))))
     rc = load_library().efla_gated_step(
-        pl.ref, _is(q, "q", pl.q, dt), _is(k, "k", pl.q, dt), _is(v, "v", pl.v, dt), _is(g, "g", pl.s, f32),
-        _is(beta, "beta", pl.s, f32), _is(S, "S", pl.S, f32, True), _is(slots, "slots", pl.b, torch.int32, True), pl.S[0],
-        _is(o, "o", pl.v, odt), _current(v))
+        pl.ref, _is(q, "q", dev, pl.q, dt), _is(k, "k", dev, pl.q, dt), _is(v, "v", dev, pl.v, dt), _is(g, "g", dev, pl.s, f32),
+        _is(beta, "beta", dev, pl.s, f32), _is(S, "S", dev, pl.S, f32, True),
+        _is(slots, "slots", dev, pl.b, torch.int32, True), pl.S[0], _is(o, "o", dev, pl.v, odt), _current(v))
     _check(rc, "efla_gated_step")
     return o
 
@@ -617,8 +645,9 @@ def efla_norm_fwd(x, weight, bias=None, *, eps: float = 1e-5, y=None, stats=None
     """Layer norm over the last dimension of x [..., D].  weight, bias [D] (fp32 or bf16).
 
     Returns (y like x, stats [..., 2] fp32: mean and 1/sqrt(var + eps) of each row)."""
-    if stream is not None:
-        return _elsewhere(stream, efla_norm_fwd, x, weight, bias, eps=eps, y=y, stats=stats)
+    if _away(x, stream):
+        return _elsewhere(x, stream, efla_norm_fwd, x, weight, bias, eps=eps, y=y, stats=stats)
+    dev = x.get_device()
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     pl = _plan(("nf", x.shape, x.stride(), y.stride(), x.dtype, weight.dtype, eps),
@@ -626,27 +655,27 @@ def efla_norm_fwd(x, weight, bias=None, *, eps: float = 1e-5, y=None, stats=None
     if stats is None:
         stats = torch.empty(pl.stats, dtype=torch.float32, device=x.device)
     rc = load_library().efla_norm_fwd(
-        pl.ref, _is(x, "x", pl.x, x.dtype), _is(weight, "weight", pl.w, weight.dtype, True),
-        _is(bias, "bias", pl.w, weight.dtype, True), _is(y, "y", pl.x, x.dtype),
-        _is(stats, "stats", pl.stats, torch.float32, True), _current(x))
+        pl.ref, _is(x, "x", dev, pl.x, x.dtype), _is(weight, "weight", dev, pl.w, weight.dtype, True),
+        _is(bias, "bias", dev, pl.w, weight.dtype, True), _is(y, "y", dev, pl.x, x.dtype),
+        _is(stats, "stats", dev, pl.stats, torch.float32, True), _current(x))
     _check(rc, "efla_norm_fwd")
     return y, stats
 
 
 def efla_norm_bwd(x, weight, dy, stats, *, want_bias: bool = True, workspace=None, stream=None):
     """Backward of efla_norm_fwd.  Returns (dx dense, dweight, dbias or None), the last two in weight's type."""
-    if stream is not None:
-        return _elsewhere(stream, efla_norm_bwd, x, weight, dy, stats, want_bias=want_bias, workspace=workspace)
-    dt, wdt, dev = x.dtype, weight.dtype, x.device
+    if _away(x, stream):
+        return _elsewhere(x, stream, efla_norm_bwd, x, weight, dy, stats, want_bias=want_bias, workspace=workspace)
+    dt, wdt, dev = x.dtype, weight.dtype, x.get_device()
     pl = _plan(("nb", x.shape, x.stride(), dy.stride(), dt, wdt),
                lambda: _NormPlan(x.shape, x.stride(), dy.stride(), dt, wdt, 0.0, True))
-    dx = torch.empty(pl.x, dtype=dt, device=dev)
-    dw = torch.empty(pl.w, dtype=wdt, device=dev)
-    db = torch.empty(pl.w, dtype=wdt, device=dev) if want_bias else None
-    ws = _ws(pl.ws, dev) if workspace is None else workspace
+    dx = torch.empty(pl.x, dtype=dt, device=x.device)
+    dw = torch.empty(pl.w, dtype=wdt, device=x.device)
+    db = torch.empty(pl.w, dtype=wdt, device=x.device) if want_bias else None
+    ws = _ws(pl.ws, x, workspace)
     rc = load_library().efla_norm_bwd(
-        pl.ref, _is(x, "x", pl.x, dt), _is(weight, "weight", pl.w, wdt, True), _is(dy, "dy", pl.x, dt),
-        _is(stats, "stats", pl.stats, torch.float32, True), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ws),
+        pl.ref, _is(x, "x", dev, pl.x, dt), _is(weight, "weight", dev, pl.w, wdt, True), _is(dy, "dy", dev, pl.x, dt),
+        _is(stats, "stats", dev, pl.stats, torch.float32, True), dx.data_ptr(), dw.data_ptr(), _ptr(db), _ptr(ws),
         ws.numel() * ws.element_size(), _current(x))
     _check(rc, "efla_norm_bwd")
     return dx, dw, db
