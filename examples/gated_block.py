@@ -28,7 +28,7 @@ class LayerNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, weight, stats = ctx.saved_tensors
-        return efla.efla_norm_bwd(x, weight, dy, stats)
+        return efla.efla_norm_bwd(x, weight, dy.contiguous(), stats)
 
 
 class GatedRule(torch.autograd.Function):
@@ -41,6 +41,8 @@ class GatedRule(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dO):
+        if dO.stride(-1) != 1 or 0 in dO.stride():   # broadcast, as the gradient of a sum is
+            dO = dO.contiguous()
         return efla.efla_gated_bwd(*ctx.saved_tensors, dO, mode=efla.EXACT, want_dS0=False)[:5]
 
 
