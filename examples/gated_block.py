@@ -12,6 +12,7 @@ import math
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 import exact_flow_recurrence_gb300 as efla
 
@@ -26,6 +27,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, stats = ctx.saved_tensors
         return efla.efla_norm_bwd(x, weight, dy.contiguous(), stats)
@@ -40,6 +42,7 @@ class GatedRule(torch.autograd.Function):
         return efla.efla_gated_fwd(q, k, v, g, beta, mode=efla.EXACT, want_state=False)[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dO):
         if dO.stride(-1) != 1 or 0 in dO.stride():   # broadcast, as the gradient of a sum is
             dO = dO.contiguous()

@@ -40,3 +40,12 @@ def test_broadcast_gradients(which):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     out.sum().backward()
     assert all(t.grad is not None for t in args)
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_second_derivatives_are_refused(which):
+    """The kernels' share of a second derivative is not there: autograd says so instead of leaving it out."""
+    fn, args = _cases()[which]
+    first = torch.autograd.grad(fn.apply(*args).float().square().sum(), args, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        sum(t.float().sum() for t in first).backward()
