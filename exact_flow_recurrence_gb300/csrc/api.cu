@@ -4,7 +4,7 @@
 #include <stdint.h>
 #include <stdio.h>
 
-#include <initializer_list>
+#include <atomic>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -26,6 +26,9 @@ struct NvtxRange {
 namespace {
 
 thread_local char g_msg[512] = "";
+
+// Whether this process has launched, or captured, kernels that keep a status word of their own.
+std::atomic<bool> g_used_gated{false}, g_used_step{false}, g_used_norm{false};
 
 efla_status fail(efla_status s, const char* fmt, ...) {
     va_list ap;
@@ -469,13 +472,20 @@ efla_status efla_get_status(cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(sync)");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "efla_get_status");
+    // A read is a copy of 9 us: the words of kernels that no call of this process has launched stay unread.
+    const struct {
+        bool used;
+        cudaError_t (*read)(unsigned int*);
+    } words[] = {{true, efla::tc_status_read_clear},     {true, efla::proj_status_read_clear},
+                 {true, efla::bt_status_read_clear},     {true, efla::gt_status_read_clear},
+                 {true, efla::sd_status_read_clear},     {g_used_gated, efla::gated_tc_status_read_clear},
+                 {g_used_gated, efla::gated_bwd_tc_status_read_clear}, {g_used_step, efla::gated_step_status_read_clear},
+                 {g_used_norm, efla::norm_status_read_clear}};
     unsigned int word = 0;
-    for (const auto read : {efla::tc_status_read_clear, efla::proj_status_read_clear, efla::bt_status_read_clear,
-                            efla::gt_status_read_clear, efla::sd_status_read_clear, efla::gated_tc_status_read_clear,
-                            efla::gated_bwd_tc_status_read_clear, efla::gated_step_status_read_clear,
-                            efla::norm_status_read_clear}) {
+    for (const auto& w : words) {
         unsigned int one = 0;
-        e = read(&one);
+        if (!w.used) continue;
+        e = w.read(&one);
         if (e != cudaSuccess) return cuda_fail(e, "efla_get_status(status word)");
         word |= one;
     }
@@ -718,6 +728,7 @@ efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const 
     if (need && (!workspace || workspace_bytes < need))
         return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
     if (s->path == EFLA_PATH_AUTO && efla::gated_fwd_short(d)) d.tensor = 0;   // (the workspace asked for is the shape's all the same)
+    g_used_gated = true;
     efla::prof_mark(nullptr, stream);
     const cudaError_t e =
         d.tensor ? efla::launch_gated_fwd_tc(d, q, k, v, g, beta, S0, o, S_final, workspace, stream)
@@ -761,6 +772,7 @@ efla_status efla_gated_bwd(const efla_gated_shape* s, const int* offsets, const 
     const size_t need = d.tensor ? efla::gated_tc_bwd_ws_bytes(d) : efla::gated_simt_bwd_ws_bytes(d);
     if (need && (!workspace || workspace_bytes < need))
         return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    g_used_gated = true;
     efla::prof_mark(nullptr, stream);
     const auto launch = d.tensor ? efla::launch_gated_bwd_tc : efla::launch_gated_bwd_simt;
     const cudaError_t e = launch(d, q, k, v, g, beta, S0, dO, dS_final, dq, dk, dv, dg, dbeta, dS0, workspace, stream);
@@ -786,6 +798,7 @@ efla_status efla_gated_step(const efla_gated_shape* s, const void* q, const void
     if ((st = check_ptrs(&sS, nslots ? 1 : 0, nullptr, 0)) != EFLA_OK) return st;
     if ((st = check_gated_alias(io.x, 6, 5, &ssl, 1, &sS, 1, Span{nullptr, 0, "workspace"})) != EFLA_OK) return st;
     if (overlap(sS, ssl)) return fail(EFLA_ERR_INVALID_ARG, "S overlaps input slots");
+    g_used_step = true;
     efla::prof_mark(nullptr, stream);
     const cudaError_t e = efla::launch_gated_step(d, q, k, v, g, beta, S, slots, nslots, o, stream);
     return e == cudaSuccess ? EFLA_OK : cuda_fail(e, "efla_gated_step");
@@ -844,6 +857,7 @@ efla_status efla_norm_fwd(const efla_norm_shape* s, const void* x, const void* w
     const size_t es[] = {e, we, we, e, 8};
     if ((st = check_elems(el, es, 5)) != EFLA_OK) return st;
     if ((st = check_alias(out, 2, in, 3)) != EFLA_OK) return st;
+    g_used_norm = true;
     efla::prof_mark(nullptr, stream);
     const cudaError_t r = efla::launch_norm_fwd(d, x, weight, bias, y, stats, stream);
     return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_norm_fwd");
@@ -879,6 +893,7 @@ efla_status efla_norm_bwd(const efla_norm_shape* s, const void* x, const void* w
     const size_t need = efla::norm_bwd_ws_bytes(d);
     if (!workspace || workspace_bytes < need)
         return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    g_used_norm = true;
     efla::prof_mark(nullptr, stream);
     const cudaError_t r = efla::launch_norm_bwd(d, x, weight, dy, stats, dx, dweight, dbias, workspace, stream);
     return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_norm_bwd");
