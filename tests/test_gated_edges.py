@@ -147,3 +147,107 @@ def test_tokens_outside_every_sequence(ends, dtype):
             assert_close("S_final", S[b:b + 1], S_ref, TOL_F32)
             for n, got, want in zip(GRADS[:5], d, g_ref):
                 assert_close(n, got[None, :, a:e], want, TOL_F32, stored_bf16=got.dtype == BF)
+
+
+def gpu64(x, mode):
+    """The reference on the GPU (fp64 too), for sizes that take the CPU too long."""
+    y = {n: t.to(DEV).double() for n, t in x.items()}
+    a, e = [y[n] for n in ("q", "k", "v", "g", "beta")], mode == efla.EXACT
+    return og.fwd(*a, y["S0"], exact=e), og.bwd(*a, y["dO"], y["S0"], y["dS"], exact=e)
+
+
+@pytest.mark.parametrize("mode,shape", [(efla.EULER, (4, 32, 32, 130, 128, 128)), (efla.EXACT, (10, 16, 8, 260, 128, 128)),
+                                        (efla.EULER, (1, 8, 8, 2600, 64, 96)), (efla.EXACT, (6, 32, 8, 333, 128, 64))])
+def test_more_chunks_than_ctas(mode, shape):
+    """The gradient kernel's CTAs, one an SM, take several chunks each: q and k again, sums over value heads
+    again, outputs in place of the operands before."""
+    B, _, Hk, L = shape[:4]
+    assert B * -(-L // 64) * Hk > 2 * 152 or Hk < shape[1]
+    x = draw(*shape, BF, mode, rate=0.1, seed=29, token_first=L % 2 == 1)
+    (o_ref, S_ref), g_ref = gpu64(x, mode)
+    for out in (F32, BF):
+        o, S, d = run(x, mode, out)
+        assert_close("o", o, o_ref, TOL_F32, stored_bf16=out == BF)
+        assert_close("S_final", S, S_ref, TOL_F32)
+        for n, a, b in zip(GRADS, d, g_ref):
+            assert_close(n, a, b, TOL_F32, stored_bf16=a.dtype == BF)
+
+
+@pytest.mark.parametrize("H,Hk", [(8, 8), (16, 8)])
+def test_more_packed_chunks_than_ctas(H, Hk):
+    """The same with ragged, single-token and empty sequences between full chunks."""
+    ends = [0, 130, 130, 131, 700, 1341, 1405, 2300, 2300, 3001]
+    B, T, dk, dv = len(ends) - 1, ends[-1], 128, 128
+    assert (T // 64 + B) * Hk > 304
+    x = draw(1, H, Hk, T, dk, dv, BF, efla.EULER, rate=0.1, seed=30, token_first=True, state=False)
+    gen = torch.Generator().manual_seed(31)
+    S0, dS = (0.3 * torch.randn(B, H, dk, dv, generator=gen) for _ in range(2))
+    y = {n: t.to(DEV)[0] for n, t in x.items() if t is not None}
+    args = [y[n] for n in ("q", "k", "v", "g", "beta")]
+    off = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    for out in (F32, BF):
+        d = efla.efla_gated_bwd(*args, y["dO"], S0.to(DEV), dS.to(DEV), offsets=off, out_dtype=out)
+        efla.efla_get_status()
+        for b, (a, e) in enumerate(zip(ends, ends[1:])):
+            if a == e:
+                assert torch.equal(d[5][b].cpu(), dS[b])
+                continue
+            s = {n: t[:, :, a:e] for n, t in x.items() if t is not None}
+            s["S0"], s["dS"] = S0[b:b + 1], dS[b:b + 1]
+            want = gpu64(s, efla.EULER)[1]
+            for n, got, ref in zip(GRADS[:5], d, want):
+                assert_close(n, got[None, :, a:e], ref, TOL_F32, stored_bf16=got.dtype == BF)
+            assert_close("dS0", d[5][b:b + 1], want[5], TOL_F32)
+
+
+def inside(shape, dtype, pad):
+    """A strided view in the middle of a buffer of sevens, `pad` elements between its rows, and the buffer."""
+    buf = torch.full((shape[0] + 2, *shape[1:-1], shape[-1] + pad), 7.0, dtype=dtype, device=DEV)
+    return buf[1:-1][..., :shape[-1]], buf
+
+
+def untouched(view, buf):
+    """Every element of the buffer outside the view is still seven, and none inside is NaN."""
+    w = buf.clone()
+    w[1:-1][..., :view.shape[-1]] = 7.0
+    return bool((w == 7.0).all()) and not bool(view.isnan().any())
+
+
+@pytest.mark.parametrize("pad", [8, 3])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(2, 2, 1, 33, 64, 48), (2, 4, 2, 150, 128, 80)])
+def test_nothing_is_written_around_the_outputs(shape, dtype, pad):
+    """o, dq, dk, dv, states and the norm's outputs as views: what lies around and between their rows stays."""
+    B, H, Hk, L, dk, dv = shape
+    x = draw(*shape, dtype, efla.EULER, seed=32)
+    (o_ref, S_ref), _ = ref64(x, efla.EULER)
+    x = gpu(x)
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    o = inside((B, H, L, dv), dtype, pad)
+    Sbuf = torch.full((B + 2, H, dk, dv), 7.0, device=DEV)
+    S = Sbuf[1:-1]
+    efla.efla_gated_fwd(*a, x["S0"], o=o[0], S_final=S)
+    d = [inside(t.shape, dtype, pad) for t in (x["q"], x["k"], x["v"])]
+    efla.efla_gated_bwd(*a, x["dO"], x["S0"], x["dS"], dq=d[0][0], dk=d[1][0], dv=d[2][0])
+    efla.efla_get_status()
+    assert untouched(*o) and all(untouched(*t) for t in d)
+    assert bool((Sbuf[0] == 7).all()) and bool((Sbuf[-1] == 7).all())
+    assert_close("o", o[0], o_ref, TOL_F32, stored_bf16=dtype == BF)
+    assert_close("S_final", S, S_ref, TOL_F32)
+    # the step, on the states in the middle of their buffer
+    po = inside((B, H, dv), dtype, pad)
+    efla.efla_gated_step(*(t[:, :, 0] for t in a), S, o=po[0])
+    efla.efla_get_status()
+    assert untouched(*po) and bool((Sbuf[0] == 7).all()) and bool((Sbuf[-1] == 7).all())
+
+
+@pytest.mark.parametrize("pad", [8, 3])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_nothing_is_written_around_the_norm(dtype, pad):
+    y, ybuf = inside((70, 264), dtype, pad)
+    x = torch.randn(70, 264, device=DEV).to(dtype)
+    sbuf = torch.full((72, 2), 7.0, device=DEV)
+    efla.efla_norm_fwd(x, torch.ones(264, device=DEV), y=y, stats=sbuf[1:-1])
+    efla.efla_get_status()
+    assert untouched(y, ybuf) and bool((sbuf[0] == 7).all()) and bool((sbuf[-1] == 7).all())
+    assert not bool((sbuf[1:-1] == 7).any())

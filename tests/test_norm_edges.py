@@ -1,7 +1,20 @@
 """Layer norm where its calls are easiest to get wrong.  Bounds as in test_norm."""
 import ctypes
 
+import pytest
+
 import exact_flow_recurrence_gb300 as efla
+from test_norm import BF, F32, _check
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,D", [(40000, 64), (20000, 1024), (4500, 4096), (1600, 8192), (1500, 16384), (5000, 333)])
+def test_many_rows_a_group(rows, D, dtype):
+    """Every group of warps takes ten rows and more: the ring's stages (six at most, one in the widest fp32
+    backward) are filled again and change phase."""
+    _check(rows, D, dtype, F32, True, seed=D)
+    _check(rows, D, dtype, BF, False, pad=8, seed=D + 1)
 
 
 def test_stats_must_lie_on_8_bytes():
