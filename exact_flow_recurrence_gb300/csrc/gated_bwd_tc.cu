@@ -64,7 +64,7 @@ struct RscanArgs {
     float* dS0;
     void* dv;
     unsigned char* rec_G;    // [H][slots][slices][kRecS]
-    unsigned char* rec_dX;   // [H][slots][slices][kRecU]
+    unsigned char* rec_dX;   // [H][slots][slices][kRecT]
     int slots;
 };
 
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
                     if (it > 0) mbar_arrive(r_free);
                     ok = mbar_wait(chain0 + 8, ph, kWaitLimit) && mbar_wait(chain0 + 17, ph, kWaitLimit);
                     if (!ok) break;
-                    if (dbg_in(a.rec_dX + rec * kRecU, kRecU, a.rec_dX, records(d, a.slots, kRecU), &g_gb_status))
-                        bulk_s2g(a.rec_dX + rec * kRecU, sm + M::R, kRecU);
+                    if (dbg_in(a.rec_dX + rec * kRecT, kRecT, a.rec_dX, records(d, a.slots, kRecT), &g_gb_status))
+                        bulk_s2g(a.rec_dX + rec * kRecT, sm + M::R, kRecT);
                     bulk_commit();
                 }
                 bulk_wait_read();
@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
             const auto ahead = [&](int h, int slot, int sl, int t, int batch) {
                 const size_t rec = ((size_t)h * a.slots + slot) * nsl + sl;
                 tma_prefetch_4d(&tm_do, 64 * sl, t, h, batch);
-                bulk_prefetch_l2(a.dX + rec * kRecU, kRecU);
-                bulk_prefetch_l2(a.R + rec * kRecU, kRecU);
+                bulk_prefetch_l2(a.dX + rec * kRecT, kRecT);
+                bulk_prefetch_l2(a.R + rec * kRecT, kRecT);
                 bulk_prefetch_l2(a.S + rec * kRecS, kRecS);
                 bulk_prefetch_l2(a.G + rec * kRecS, kRecS);
             };
@@ -526,12 +526,12 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             if (ok) mbar_arrive_expect_tx(full, bytes);
                             return ok;
                         };
-                        if (!next(&m.e_ax, &m.f_ax, kRecU + 8192)) break;
+                        if (!next(&m.e_ax, &m.f_ax, kRecT + 8192)) break;
                         tma_load_4d(sm + kGrAX, &tm_do, 64 * sl, t, h, s.batch, &m.f_ax);
                         for (int p = 0; p < 3; ++p)
-                            bulk_g2s(sm + kGrAX + p * 16384 + 8192, a.dX + rec * kRecU + p * 8192, 8192, &m.f_ax);
-                        if (!next(&m.e_r, &m.f_r, kRecU)) break;
-                        bulk_g2s(sm + kGrR, a.R + rec * kRecU, kRecU, &m.f_r);
+                            bulk_g2s(sm + kGrAX + p * 16384 + 8192, a.dX + rec * kRecT + p * 8192, 8192, &m.f_ax);
+                        if (!next(&m.e_r, &m.f_r, kRecT)) break;
+                        bulk_g2s(sm + kGrR, a.R + rec * kRecT, kRecT, &m.f_r);
                         if (!next(&m.e_s, &m.f_s, kRecS)) break;
                         bulk_g2s(sm + kGrS, a.S + rec * kRecS, kRecS, &m.f_s);
                         if (!next(&m.e_g, &m.f_g, kRecS)) break;
@@ -938,9 +938,9 @@ size_t carve(const GDims& d, void* base, BwdTcWs* w) {
     w->img_r = take(n * NP * 8192);
     w->vec = (GVec*)take(n * sizeof(GVec));
     w->S = take(n * nsl * kRecS);
-    w->R = take(n * nsl * kRecU);
+    w->R = take(n * nsl * kRecT);
     w->G = take(n * nsl * kRecS);
-    w->dX = take(n * nsl * kRecU);
+    w->dX = take(n * nsl * kRecT);
     w->acc = d.H > d.Hk ? (float*)take((size_t)kGrCtas * 128 * 128 * 4) : nullptr;
     return (size_t)(p - (char*)base);
 }

@@ -341,7 +341,7 @@ struct ScanArgs {
     float* S_final;
     int slots;
     unsigned char* rec_S;   // [H][slots][slices][kRecS]
-    unsigned char* rec_R;   // [H][slots][slices][kRecU]
+    unsigned char* rec_R;   // [H][slots][slices][kRecT]
     const int* flags;       // [H][slots], or null: set as the chunks' preparations are complete
 };
 
@@ -470,8 +470,8 @@ __device__ void scan_cta(const GDims& d, const ScanArgs& a, const CUtensorMap& t
                     if (c > 0) mbar_arrive(r_free);
                     for (int g = 0; g < NCH; ++g) ok = ok && mbar_wait(chain0 + 9 * g + 3, ph, kWaitLimit);
                     if (!ok) break;
-                    unsigned char* const to_R = a.rec_R + ((rec0 + c) * slices + by) * kRecU;
-                    if (dbg_in(to_R, kRecU, a.rec_R, records(d, a.slots, kRecU), &g_gt2_status)) bulk_s2g(to_R, sm + M::R, kRecU);
+                    unsigned char* const to_R = a.rec_R + ((rec0 + c) * slices + by) * kRecT;
+                    if (dbg_in(to_R, kRecT, a.rec_R, records(d, a.slots, kRecT), &g_gt2_status)) bulk_s2g(to_R, sm + M::R, kRecT);
                     bulk_commit();
                 }
                 bulk_wait_read();

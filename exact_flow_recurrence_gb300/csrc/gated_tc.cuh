@@ -22,7 +22,7 @@ namespace efla {
 
 constexpr int kGC = 64;   // tokens a chunk of the tensor-core kernels
 constexpr int NP = 3;     // bf16 parts of a computed operand
-constexpr uint32_t kRecS = 3 * 16384, kRecU = 3 * 8192;   // bytes of a recorded slice
+constexpr uint32_t kRecS = 3 * 16384, kRecT = 3 * 8192;   // bytes of a recorded slice of S or G, of R or dX
 
 // Elements from the first to the last of a strided [batch][heads][token][width] array, and the bytes
 // of all records of a kind (debug builds' bounds).
@@ -94,7 +94,6 @@ __device__ __forceinline__ void split8(const float* x, uint4 (&w)[N]) {
 // and 50 at N = 96: three parts in one cost little more than one.
 template <int NCH>
 struct Chain {
-    static constexpr int N = 32;
     static constexpr int blocks = NCH + 1;
     // byte offset of part p's first column, and the stride to the block that holds part 2
     __host__ __device__ static constexpr uint32_t part(int g, int p, uint32_t blk) {
@@ -106,9 +105,6 @@ struct Chain {
     static __device__ __forceinline__ void put(unsigned char* base, uint32_t blk, int g, int r, int cc, const float2 (&x)[W2]);
 };
 
-__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) { tmem_ld16(t, v); }
-__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[8]) { tmem_ld8(t, v); }
-
 // 2 W2 columns of this warp's lanes of an accumulator, summed over G column groups `gap` apart (the
 // last ones first: they hold the small parts' products; two at a time, for the registers' sake:
 // with all but a few KB of L1 taken by shared memory, a spilled register costs a trip to L2).
@@ -117,8 +113,8 @@ __device__ __forceinline__ void tmem_sum(uint32_t t, int gap, float2 (&y)[W2]) {
 #pragma unroll
     for (int p = G - 1; p >= 0; p -= 2) {
         float x[2][2 * W2];
-        tmem_ld(t + p * gap, x[0]);
-        if (p > 0) tmem_ld(t + (p - 1) * gap, x[1]);
+        tmem_ld16(t + p * gap, x[0]);
+        if (p > 0) tmem_ld16(t + (p - 1) * gap, x[1]);
         tmem_ld_wait();
         loaded(x[0]);
         if (p > 0) loaded(x[1]);
@@ -147,7 +143,7 @@ __device__ __forceinline__ void Chain<NCH>::put(unsigned char* base, uint32_t bl
 }
 
 // 2 W2 values of row r, from column col of a slice's 64, as parts in tiles of 64 rows one after another
-// (the records of U and dX).
+// (the records of R and dX).
 template <int W2>
 __device__ __forceinline__ void put_parts(unsigned char* base, int r, int col, const float2 (&x)[W2]) {
 #pragma unroll
@@ -252,7 +248,7 @@ inline cudaError_t narrow_slices(const GDims& d, bool* narrow) {
 
 // The backward's parts of gated_tc.cu: the preparation, with the image of the residuals' inverse, and
 // the pass that records every chunk's S and residuals R as parts, in the operand layout
-// ([H][slots][slices of 64 columns][kRecS or kRecU bytes]).
+// ([H][slots][slices of 64 columns][kRecS or kRecT bytes]).
 cudaError_t launch_gated_prep_tc(const GDims& d, const void* q, const void* k, const float* g, const float* beta,
                                  unsigned char* img, unsigned char* img_r, GVec* vec, cudaStream_t st);
 cudaError_t launch_gated_record_tc(const GDims& d, const void* q, const void* k, const void* v, const float* S0,
