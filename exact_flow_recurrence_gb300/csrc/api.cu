@@ -723,6 +723,7 @@ efla_status efla_gated_fwd(const efla_gated_shape* s, const int* offsets, const 
         const Span ins[] = {sS0, d.packed ? soff : Span{nullptr, 0, ""}};
         const Span outs[] = {S_final == (float*)S0 ? Span{nullptr, 0, ""} : sSf};
         if ((st = check_gated_alias(io.x, 6, 5, ins, 2, outs, 1, sw)) != EFLA_OK) return st;
+        if (overlap(sSf, ins[1])) return fail(EFLA_ERR_INVALID_ARG, "S_final overlaps input offsets");
     }
     const size_t need = d.tensor ? efla::gated_tc_fwd_ws_bytes(d) : 0;
     if (need && (!workspace || workspace_bytes < need))
