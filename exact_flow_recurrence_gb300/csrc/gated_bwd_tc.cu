@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(Rs::warps * 32, 1) k_gt_rscan(GDims d, RscanAr
 // own that is filled again as soon as its products are done: [dO; dX_0], [0; dX_1], [0; dX_2], R, S,
 // G; dO, q and k by TMA.  Warps: 8 epilogue (a lane a token; <S, G> in the products' shadow), one
 // that issues products, one that copies.  The epilogue of the pairs runs while the last slice's
-// products do.  4096 chunks of two slices: 355 us at B4 H16 L4096, 1.3 GB from DRAM (3.6 TB/s, 42% of
-// the pins' rate), the tensor pipe 36% busy: a head's products, pairs, last products and epilogue
-// follow one another, because its accumulators take all of the tensor memory and its operands
-// (222 KB) all of shared memory, so only the copies of the next head run ahead.
+// products do.  4096 chunks of two slices: 394 us at B4 H16 L4096, 1.3 GB of records: a head's
+// products, pairs, last products and epilogue follow one another, because its accumulators take all
+// of the tensor memory and its operands (222 KB) all of shared memory, so only the copies of the next
+// head run ahead.  (Of the 394, alpha on the pairs' columns takes 22 and the third part of [dPD; dAD] 17.)
 constexpr int kGrWarps = 10;
 constexpr uint32_t kGrQK = 0;                    // 2 blocks of 64 dk x [Q rows | K rows]
 constexpr uint32_t kGrAX = 32768;                // dO | dX_0 | 0 | dX_1 | 0 | dX_2, tiles of 64 rows

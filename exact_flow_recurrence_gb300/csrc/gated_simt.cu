@@ -27,7 +27,9 @@
 // short forward passes (gated_fwd_short).  A token takes 0.17 us at dk 128 where a warp has its scheduler to
 // itself, 0.13 us at dk 64; with every SM full, the shared-memory reads of k and q (eight 16-byte reads a
 // lane and token for 96 multiply-adds) bound them.  H4 L77 dk 64 dv 48 fp32: 13 us; chunked
-// products of 32 tokens in shared memory, this file's first form, took 45 us.  Taking the dots
+// products of 32 tokens in shared memory, this file's first form, took 45 us.  One chain of tokens is
+// what a long fp32 prompt costs, whatever the rest of the GPU does: B1 H16 L4096 d 128 0.70 ms (its
+// bytes: 0.02), B8 H8 L2048 1.01 ms; backward B8 H8 L256 0.40 ms, B4 H16 L1024 1.48 ms.  Taking the dots
 // one token early, from a state that lacks the token between, costs more instructions than the
 // overlap gives a warp that issues in order: 0.23 us a token.
 #include "gated_seq.cuh"

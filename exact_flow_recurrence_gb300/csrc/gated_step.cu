@@ -14,7 +14,7 @@
 // two states an SM are on their way in at any time and cost no registers.  Else (k_gated_step) a
 // CTA owns 16 columns of one state, so that a few states still use every SM.  dk = dv = 128, states
 // that fit L2: 151 states 6.5 us (16 columns a CTA), 152 states 4.6 us (ring).  4096 states (B256 H16,
-// 537 MB both ways): 89.5 us, 6.0 TB/s, 0.89 of a plain copy's rate; 16 states: 3.9 us, a launch.
+// 537 MB both ways): 90.8 us, 5.95 TB/s, 0.88 of a plain copy's rate; 16 states: 3.9 us, a launch.
 #include "gated_seq.cuh"
 #include "launch.h"
 #include "tc_common.cuh"

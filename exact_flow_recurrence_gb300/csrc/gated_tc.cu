@@ -27,7 +27,8 @@ __device__ unsigned int g_gt2_status = 0;   // bit 0: a bounded wait expired; kS
 // The backward also wants the tokens' residuals r = U / alpha, where alpha is zero too.  With A =
 // diag(alpha) N they are r = (I + N diag(alpha))^{-1} (V - e^c K S), and that inverse is
 // I - N T diag(alpha): N's parts fill the other 64 rows of the product of step 5, and no quotient
-// by alpha is formed.  It goes out as an image of its own (three chunks an SM then: N needs room).
+// by alpha is formed.  It goes out as an image of its own.  N needs room: three chunks an SM, 4096
+// chunks in 121 us.
 // Bound by its chain of short dependent steps, not by data: what counts is how many chunks an
 // SM has in flight.  P's parts lie over A and T, and both over the dead tiles, so that four
 // chunks fit (as many as the registers allow).  With three of them an SM a chunk took 11 us from its
@@ -306,9 +307,10 @@ __global__ void __launch_bounds__(128, BWD ? 3 : 4) k_gt_prep(GDims d, PrepArgs 
 // three times 0.11 us from a commit to the wait that sees it, and three epilogues of 0.3 to 0.4 us
 // each (tensor memory to registers, parts to shared memory, the proxy fence).  Twice the epilogue
 // warps with half the columns each change nothing: it is fixed latencies.  Two chains of a CTA
-// overlap: 3.3 us a chunk for both.  Measured (d 128): B8 H8 L2048 (32 chunks) 151 us with its
-// preparation; B1 H16 L16384 (one chain a CTA, 256 chunks) 545 us; the recording pass at B4 H16
-// L4096 (64 chunks) 210 us.
+// overlap: 3.2 us a chunk for both.  Measured (d 128): B8 H8 L2048 (32 chunks) 102 us; B1 H16
+// L16384 (one chain a CTA, 256 chunks) 545 us; the recording pass at B4 H16 L4096 (64 chunks)
+// 212 us.  CTAs start in the order of the sequences: packed prompts that do not fit at once take
+// longer when a long one comes late (13 of them, 16384 tokens: 226 us longest first, 295 shortest first).
 template <int NCH, bool REC>
 struct ScanSmem {
     using C = Chain<NCH>;

@@ -6,8 +6,8 @@
 // sum of three bf16 parts, x = x_0 + x_1 + x_2, each the rounding of what the earlier ones left,
 // and a product of two such operands takes the part pairs a + b < 3.  All products accumulate
 // in fp32.  Three parts carry the 24 bits of an fp32 value: against the fp64 recurrence the
-// outputs and the carried state come out within about 1e-6 of their norm, where two parts leave
-// 4e-6 and one bf16 or fp16 operand 3e-3 or 3e-4.  Parts keep fp32's exponent range, so there is
+// outputs and the carried state come out within 5e-7 of their norm, where two parts leave 4e-6
+// and one bf16 or fp16 operand 3e-3 or 3e-4.  Parts keep fp32's exponent range, so there is
 // no range to check and no second path, and what a call returns does not depend on what else it
 // returns.
 #pragma once

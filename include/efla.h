@@ -24,7 +24,8 @@
  *    (S is dk x dv, the shape of k v^T; row index = key dimension.)
  *  - Element types: q, k, v (and dO) are `dtype`; o (and dq, dk, dv) are
  *    `out_dtype`; beta, states and dbeta are always fp32.  All arithmetic is
- *    fp32 (accumulation, state, alpha).
+ *    fp32 (accumulation, state, alpha), but for the operands that tensor-core
+ *    paths stage in fewer bits: each path says which.
  *  - Every pointer must be 16-byte aligned.
  *  - Supported sizes: dk, dv multiples of 16 in [16, 128]; chunk in {16, 32, 64};
  *    L >= 0 (L % chunk != 0 is allowed: the tail is handled exactly); B, H >= 0.
@@ -251,7 +252,12 @@ efla_status efla_fwd_noalloc(const efla_shape* shape,
  * elements (states, workspace, dg and dbeta: 16 bytes): 16-byte aligned bf16 arrays with
  * strides that are multiples of 8 elements run on the tensor cores, others on the fp32 cores.
  * EFLA_PATH_AUTO also takes the fp32 cores for forward passes of at most 32 tokens while they
- * are the faster ones; the workspace size does not depend on that choice. */
+ * are the faster ones; the workspace size does not depend on that choice.
+ *
+ * Precision on the tensor cores: q, k, v and dO enter as they are, every computed operand as the
+ * sum of three bf16 parts (24 bits), whatever the outputs' type and whether a state is asked for.
+ * Sums and states are fp32, decays are ex2.approx (2^-22 of each), the triangular inverse uses
+ * split-tf32 products.  fp32 results come within 1e-6 of their norm. */
 typedef struct {
     int B, H, Hk, L, dk, dv;    /* dk, dv: multiples of 16 in [16, 128]; H, Hk: value, key heads */
     efla_dtype dtype;           /* q, k, v, dO */
