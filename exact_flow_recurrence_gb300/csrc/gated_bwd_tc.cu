@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             }
                             const float w = keep ? sw * y[e] * g[e] : 0.f;
                             (e & 1 ? w5[8 * k + e / 2].y : w5[8 * k + e / 2].x) = w;
-                            z[e] = keep ? w * z[e] : 0.f;
+                            z[e] = keep && j0 + e < i ? w * z[e] : 0.f;   // (a token's own pair does not decay)
                             rsum += z[e];
                         }
                         if (!top && (i & ~15) == j0) {   // the diagonal: dalpha, and lambda
@@ -882,8 +882,9 @@ __global__ void __launch_bounds__(kGrWarps * 32, 1) k_gt_grad(GDims d, GradArgs 
                             v += m.dot[k][j] + m.dot[k][64 + j];
                             o2[e] += m.dot2[k][j];
                         }
+                        if (j >= n - 1) o2[e] = 0.f;   // (the chunk's last token does not decay inside it)
                         c[e] = j < n ? v - o2[e] : 0.f;
-                        tot += j < n ? o2[e] : 0.f;
+                        tot += o2[e];
                     }
                     tot = warp_sum(tot);
                     const float g = warp_sum(lane < 8 ? m.sg[hc & 1][lane] : 0.f);

@@ -459,14 +459,15 @@ __global__ void __launch_bounds__(kNT, 2) k_gated_grad(GDims d, const Tin* q, co
                 if (lane + 32 * c < dk) ak[r][c] = fmaf(dl, m.K[i * kLd + lane + 32 * c], ak[r][c]);
         }
         if (tid < 32) {
-            float x = m.dc[tid] - m.dl[tid];
+            // (the last token's U G^T decays by nothing inside the chunk: left out of both sums, not added and taken off)
+            float x = m.dc[tid] - (tid == n - 1 ? 0.f : m.dl[tid]);
             for (int j = 0; j < kC; ++j) x += m.W[tid * kLs + j] - m.W[j * kLs + tid];
             if (tid >= n) x = 0.f;
             if (tid == n - 1) {
                 float z = 0.f;
                 for (int e = 0; e < 8; ++e) z += m.part[e];
                 x = fmaf(expf(cl), z, x);
-                for (int i = 0; i < n; ++i) x += m.dl[i];   // U G^T's e^{c_last - c_i}
+                for (int i = 0; i < n - 1; ++i) x += m.dl[i];   // U G^T's e^{c_last - c_i}
             }
 #pragma unroll
             for (int o2 = 1; o2 < 32; o2 <<= 1) {   // sums from token tid to the chunk's end

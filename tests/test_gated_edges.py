@@ -251,3 +251,15 @@ def test_nothing_is_written_around_the_norm(dtype, pad):
     efla.efla_get_status()
     assert untouched(y, ybuf) and bool((sbuf[0] == 7).all()) and bool((sbuf[-1] == 7).all())
     assert not bool((sbuf[1:-1] == 7).any())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(1, 2, 2, 1, 64, 64), (3, 2, 1, 2, 128, 64), (1, 2, 2, 70, 64, 128)])
+def test_gate_gradients_under_strong_decay(shape, dtype):
+    """Gates that forget nearly everything at every token (e^-15 and less) have gradients that small: what does
+    not decay is in none of the sums that make them, so each is right on its own scale."""
+    x = draw(*shape, dtype, efla.EULER, seed=33)
+    gen = torch.Generator().manual_seed(34)
+    x["g"] = -(15.0 + 3.0 * torch.rand(x["g"].shape, generator=gen))
+    for n, a, b in zip(GRADS, run(x, efla.EULER)[2], ref64(x, efla.EULER)[1]):
+        assert_close(n, a, b, TOL_F32)
