@@ -28,6 +28,9 @@ __all__ = [
     "efla_gated_fwd", "efla_gated_bwd", "efla_gated_step", "GatedShape", "make_gated_shape",
     "efla_gated_fwd_workspace_size", "efla_gated_bwd_workspace_size",
     "efla_norm_fwd", "efla_norm_bwd", "NormShape",
+    "efla_conv_fwd", "efla_conv_bwd", "efla_conv_step", "ConvShape", "efla_conv_bwd_workspace_size",
+    "efla_scan_fwd", "efla_scan_bwd", "efla_scan_step", "ScanShape", "efla_scan_fwd_workspace_size",
+    "efla_scan_bwd_workspace_size", "efla_rms_fwd", "efla_rms_bwd", "RmsShape", "efla_rms_bwd_workspace_size",
     "F32", "BF16", "EXACT", "EULER", "AUTO", "SIMT", "TENSOR", "efla_tc_selftest", "efla_wait_selftest",
 ]
 
@@ -76,6 +79,26 @@ class NormShape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("x_stride", ctypes.c_longlong),
                 ("y_stride", ctypes.c_longlong), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
                 ("eps", ctypes.c_float)]
+
+
+_Pair = ctypes.c_longlong * 2
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "D", "W", "dtype", "weight_dtype", "silu", "packed")] + [
+        (n + "_stride", _Pair) for n in ("x", "y", "dy", "dx")]
+
+
+class ScanShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "D", "G", "N", "dtype", "softplus", "packed")] + [
+        (n + "_stride", _Pair) for n in ("u", "delta", "z", "y", "dy", "du", "ddelta", "dz")] + [
+        (n + "_stride", _Strides) for n in ("B", "C")]
+
+
+class RmsShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("group", ctypes.c_int)] + [
+        (n + "_stride", ctypes.c_longlong) for n in ("x", "residual", "y", "h", "dy", "dh", "dx")] + [
+        ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -132,6 +155,22 @@ def load_library(path: Optional[str] = None):
     lib.efla_gated_step.restype = ctypes.c_int
     lib.efla_gated_step.argtypes = [gp] + [_vp] * 7 + [ctypes.c_int, _vp, _vp]
     np_ = ctypes.POINTER(NormShape)
+    cs, ss, rs, sz = ctypes.POINTER(ConvShape), ctypes.POINTER(ScanShape), ctypes.POINTER(RmsShape), ctypes.c_size_t
+    for name, res, args in (
+            ("efla_conv_fwd", ctypes.c_int, [cs] + [_vp] * 8),
+            ("efla_conv_bwd_workspace_size", sz, [cs]),
+            ("efla_conv_bwd", ctypes.c_int, [cs] + [_vp] * 12 + [sz, _vp]),
+            ("efla_conv_step", ctypes.c_int, [cs] + [_vp] * 5 + [ctypes.c_int] + [_vp] * 2),
+            ("efla_scan_fwd_workspace_size", sz, [ss]),
+            ("efla_scan_fwd", ctypes.c_int, [ss] + [_vp] * 13 + [sz, _vp]),
+            ("efla_scan_bwd_workspace_size", sz, [ss]),
+            ("efla_scan_bwd", ctypes.c_int, [ss] + [_vp] * 22 + [sz, _vp]),
+            ("efla_scan_step", ctypes.c_int, [ss] + [_vp] * 10 + [ctypes.c_int] + [_vp] * 2),
+            ("efla_rms_fwd", ctypes.c_int, [rs] + [_vp] * 8),
+            ("efla_rms_bwd_workspace_size", sz, [rs]),
+            ("efla_rms_bwd", ctypes.c_int, [rs] + [_vp] * 8 + [sz, _vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
     lib.efla_norm_fwd.restype = ctypes.c_int
     lib.efla_norm_fwd.argtypes = [np_] + [_vp] * 6
     lib.efla_norm_bwd_workspace_size.restype = ctypes.c_size_t
@@ -679,6 +718,333 @@ def efla_norm_bwd(x, weight, dy, stats, *, want_bias: bool = True, workspace=Non
         ws.numel() * ws.element_size(), _current(x))
     _check(rc, "efla_norm_bwd")
     return dx, dw, db
+
+
+# ------------------------------------------------------------------ short convolution
+def _token_strides(name: str, shape, stride, packed: bool):
+    """{batch, token} strides of [B,L,D] (packed: [T,D]), D contiguous."""
+    if shape[-1] > 1 and 0 not in shape and stride[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _Pair(0, stride[0]) if packed else _Pair(stride[0], stride[1])
+
+
+def _step_strides(name: str, shape, stride):
+    """{batch, token} strides of one token [B,D]."""
+    if shape[-1] > 1 and 0 not in shape and stride[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _Pair(stride[0], 0)
+
+
+class _ConvPlan:
+    """Shapes of a convolution's tensors, its C struct and its workspace.  kind: "fwd", "bwd" or "step"."""
+
+    def __init__(self, xs, ws, B, packed, dtype, wdtype, silu, strides, kind):
+        lead = 2 if kind == "step" or packed else 3
+        if len(xs) != lead or len(ws) != 2:
+            raise ValueError("expected weight [D,W] and x [B,L,D], [T,D] with offsets, or [B,D] for one token")
+        L, D, W = 1 if kind == "step" else xs[-2], xs[-1], ws[1]
+        self.x, self.w, self.b, self.B = xs, torch.Size((D, W)), torch.Size((D,)), torch.Size((B,))
+        self.state = torch.Size((B, max(W - 1, 0), D))
+        s = self.shape = ConvShape(B, L, D, W, _dt(dtype), _dt(wdtype), int(silu), int(packed))
+        for n, x in strides.items():
+            if x is not None and len(x) == len(xs):   # (a tensor of another shape is refused where it is passed)
+                setattr(s, n + "_stride", _step_strides(n, xs, x) if kind == "step" else _token_strides(n, xs, x, packed))
+        self.ref = ctypes.byref(s)
+        self.ws = load_library().efla_conv_bwd_workspace_size(self.ref) if kind == "bwd" else 0
+
+
+def efla_conv_bwd_workspace_size(shape: ConvShape) -> int:
+    return load_library().efla_conv_bwd_workspace_size(ctypes.byref(shape))
+
+
+def _sequences(x, offsets, name: str):
+    """How many sequences a call has: those of the batch, or those that the offsets pack on one axis."""
+    _at(x, name, x.get_device())
+    if offsets is None:
+        return x.shape[0] if x.dim() else 0
+    _at(offsets, "offsets", x.get_device())
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets: expected a contiguous CUDA int32 tensor [B + 1]")
+    return offsets.numel() - 1
+
+
+def efla_conv_fwd(x, weight, bias=None, S0=None, *, offsets=None, silu: bool = True, y=None, S_final=None,
+                  want_state: bool = True, stream=None):
+    """Short causal convolution: y_t = act(bias + sum_j weight[:, j] x_{t-(W-1)+j}), act x sigmoid(x) or (silu=False) none.
+
+    x [B,L,D] (any strides, last dimension contiguous), weight [D,W], bias [D] (fp32 or bf16), S0 [B,W-1,D] in x's type: the
+    tokens in front of each sequence.  With offsets (int32 [B+1] on the GPU) the sequences are packed on one axis: x [T,D].
+    Returns (y, S_final [B,W-1,D], the sequences' last tokens, or None)."""
+    if _away(x, stream):
+        return _elsewhere(x, stream, efla_conv_fwd, x, weight, bias, S0, offsets=offsets, silu=silu, y=y, S_final=S_final,
+                          want_state=want_state)
+    dt, wdt, B, dev = x.dtype, weight.dtype, _sequences(x, offsets, "x"), x.get_device()
+    if y is None:
+        y = torch.empty(x.shape, dtype=dt, device=x.device)
+    strides = (x.stride(), y.stride())
+    pl = _plan(("cf", x.shape, weight.shape, strides, dt, wdt, bool(silu), B, offsets is None), lambda: _ConvPlan(
+        x.shape, weight.shape, B, offsets is not None, dt, wdt, silu, dict(zip(("x", "y"), strides)), "fwd"))
+    if S_final is None and want_state:
+        S_final = torch.empty(pl.state, dtype=dt, device=x.device)
+    rc = load_library().efla_conv_fwd(
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(x, "x", dev, pl.x, dt), _is(weight, "weight", dev, pl.w, wdt, True),
+        _is(bias, "bias", dev, pl.b, wdt, True), _is(S0, "S0", dev, pl.state, dt, True), _is(y, "y", dev, pl.x, dt),
+        _is(S_final, "S_final", dev, pl.state, dt, True), _current(x))
+    _check(rc, "efla_conv_fwd")
+    return y, S_final
+
+
+def efla_conv_bwd(x, weight, dy, bias=None, S0=None, dS_final=None, *, offsets=None, silu: bool = True, dx=None,
+                  want_dS0: bool = True, workspace=None, stream=None):
+    """Backward of efla_conv_fwd (same shapes; dy as x).  Returns (dx, dweight, dbias or None, dS0 or None): dx dense or into
+    the tensor given (which may be a slice of a buffer), dweight and dbias in weight's type, dbias where there is a bias."""
+    if _away(x, stream):
+        return _elsewhere(x, stream, efla_conv_bwd, x, weight, dy, bias, S0, dS_final, offsets=offsets, silu=silu, dx=dx,
+                          want_dS0=want_dS0, workspace=workspace)
+    dt, wdt, B, dev = x.dtype, weight.dtype, _sequences(x, offsets, "x"), x.get_device()
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=dt, device=x.device)
+    strides = (x.stride(), dy.stride(), dx.stride())
+    pl = _plan(("cb", x.shape, weight.shape, strides, dt, wdt, bool(silu), B, offsets is None), lambda: _ConvPlan(
+        x.shape, weight.shape, B, offsets is not None, dt, wdt, silu, dict(zip(("x", "dy", "dx"), strides)), "bwd"))
+    dw = torch.empty(pl.w, dtype=wdt, device=x.device)
+    db = None if bias is None else torch.empty(pl.b, dtype=wdt, device=x.device)
+    dS0 = torch.empty(pl.state, dtype=dt, device=x.device) if want_dS0 else None
+    ws = _ws(pl.ws, x, workspace)
+    rc = load_library().efla_conv_bwd(
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(x, "x", dev, pl.x, dt), _is(weight, "weight", dev, pl.w, wdt, True),
+        _is(bias, "bias", dev, pl.b, wdt, True), _is(S0, "S0", dev, pl.state, dt, True), _is(dy, "dy", dev, pl.x, dt),
+        _is(dS_final, "dS_final", dev, pl.state, dt, True), _is(dx, "dx", dev, pl.x, dt), dw.data_ptr(), _ptr(db), _ptr(dS0), _ptr(ws),
+        ws.numel() * ws.element_size(), _current(x))
+    _check(rc, "efla_conv_bwd")
+    return dx, dw, db, dS0
+
+
+def efla_conv_step(x, weight, S, bias=None, *, slots=None, silu: bool = True, y=None, stream=None):
+    """One token x [B,D] of the convolution on a cache of states S [n,W-1,D] (x's type), shifted in place.  slots (int32 [B]
+    on the GPU): each sequence's place in the cache (outside [0, n): skipped, y = 0); None: place b.  Returns y [B,D]."""
+    if _away(x, stream):
+        return _elsewhere(x, stream, efla_conv_step, x, weight, S, bias, slots=slots, silu=silu, y=y)
+    dt, wdt, dev = x.dtype, weight.dtype, x.get_device()
+    if y is None:
+        y = torch.empty(x.shape, dtype=dt, device=x.device)
+    strides = (x.stride(), y.stride())
+    pl = _plan(("cs", x.shape, weight.shape, strides, dt, wdt, bool(silu)), lambda: _ConvPlan(
+        x.shape, weight.shape, x.shape[0] if len(x.shape) else 0, False, dt, wdt, silu, dict(zip(("x", "y"), strides)), "step"))
+    n = S.shape[0] if len(S.shape) == 3 else 0
+    rc = load_library().efla_conv_step(
+        pl.ref, _is(x, "x", dev, pl.x, dt), _is(weight, "weight", dev, pl.w, wdt, True), _is(bias, "bias", dev, pl.b, wdt, True),
+        _is(S, "S", dev, torch.Size((n,) + pl.state[1:]), dt, True), _is(slots, "slots", dev, pl.B, torch.int32, True), n,
+        _is(y, "y", dev, pl.x, dt), _current(x))
+    _check(rc, "efla_conv_step")
+    return y
+
+
+# ------------------------------------------------------------------ selective scan
+class _ScanPlan:
+    """Shapes of a scan's tensors, its C struct and its workspace.  kind: "fwd", "bwd" or "step"."""
+
+    def __init__(self, us, As, Cs, B, packed, dtype, softplus, strides, kind):
+        lead = 1 if kind == "step" or packed else 2
+        if len(us) != lead + 1 or len(As) != 2 or len(Cs) != lead + 2:
+            raise ValueError("expected A [D,N] and u [B,L,D] with B, C [B,L,G,N]; [T,D] and [T,G,N] with offsets; [B,D] and [B,G,N] for one token")
+        L, D, (G, N) = 1 if kind == "step" else us[-2], us[-1], Cs[-2:]
+        self.u, self.A, self.d, self.B = us, torch.Size((D, N)), torch.Size((D,)), torch.Size((B,))
+        self.bc, self.state = torch.Size(us[:-1] + (G, N)), torch.Size((B, D, N))
+        s = self.shape = ScanShape(B, L, D, G, N, _dt(dtype), int(softplus), int(packed))
+        for n, x in strides.items():
+            if x is None:
+                continue
+            if n in ("B", "C"):
+                if len(x) == len(Cs):       # (a tensor of another shape is refused where it is passed)
+                    if N > 1 and 0 not in self.bc and x[-1] != 1:
+                        raise ValueError(f"{n}: the last dimension must be contiguous")
+                    setattr(s, n + "_stride", _Strides(x[0], 0, x[1]) if kind == "step" else _Strides(0, x[0], x[1]) if packed
+                            else _Strides(*x[:3]))
+            elif len(x) == len(us):
+                setattr(s, n + "_stride", _step_strides(n, us, x) if kind == "step" else _token_strides(n, us, x, packed))
+        self.ref = ctypes.byref(s)
+        self.ws = {"fwd": efla_scan_fwd_workspace_size, "bwd": efla_scan_bwd_workspace_size, "step": lambda s: 0}[kind](s)
+
+
+def efla_scan_fwd_workspace_size(shape: ScanShape) -> int:
+    return load_library().efla_scan_fwd_workspace_size(ctypes.byref(shape))
+
+
+def efla_scan_bwd_workspace_size(shape: ScanShape) -> int:
+    return load_library().efla_scan_bwd_workspace_size(ctypes.byref(shape))
+
+
+def _opt_stride(x):
+    return None if x is None else x.stride()
+
+
+def efla_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, S0=None, *, offsets=None, softplus: bool = True, y=None,
+                  S_final=None, want_state: bool = True, workspace=None, stream=None):
+    """Selective scan: h <- e^{dt A} h + dt u B, y = (sum_n C h + D u) z sigmoid(z), dt = softplus(delta + delta_bias), or
+    (softplus=False) delta + delta_bias.
+
+    u, delta, z [B,L,Di], B, C [B,L,G,N] (any strides, last dimension contiguous; channel d reads group d // (Di / G)), A [Di,N],
+    D, delta_bias [Di] fp32, S0 [B,Di,N] fp32.  With offsets (int32 [B+1] on the GPU) the sequences are packed on one axis:
+    [T,Di] and [T,G,N].  D, z, delta_bias, S0 may be None.  Returns (y [B,L,Di], S_final [B,Di,N] fp32 or None)."""
+    if _away(u, stream):
+        return _elsewhere(u, stream, efla_scan_fwd, u, delta, A, B, C, D, z, delta_bias, S0, offsets=offsets, softplus=softplus,
+                          y=y, S_final=S_final, want_state=want_state, workspace=workspace)
+    dt, f32, n, dev = u.dtype, torch.float32, _sequences(u, offsets, "u"), u.get_device()
+    if y is None:
+        y = torch.empty(u.shape, dtype=dt, device=u.device)
+    strides = (u.stride(), delta.stride(), _opt_stride(z), y.stride(), B.stride(), C.stride())
+    pl = _plan(("sf", u.shape, A.shape, C.shape, strides, dt, bool(softplus), n, offsets is None), lambda: _ScanPlan(
+        u.shape, A.shape, C.shape, n, offsets is not None, dt, softplus, dict(zip(("u", "delta", "z", "y", "B", "C"), strides)), "fwd"))
+    if S_final is None and want_state:
+        S_final = torch.empty(pl.state, dtype=f32, device=u.device)
+    ws = _ws(pl.ws, u, workspace) if pl.ws or workspace is not None else None
+    rc = load_library().efla_scan_fwd(
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(u, "u", dev, pl.u, dt), _is(delta, "delta", dev, pl.u, dt),
+        _is(A, "A", dev, pl.A, f32, True), _is(B, "B", dev, pl.bc, dt), _is(C, "C", dev, pl.bc, dt), _is(D, "D", dev, pl.d, f32, True),
+        _is(z, "z", dev, pl.u, dt), _is(delta_bias, "delta_bias", dev, pl.d, f32, True), _is(S0, "S0", dev, pl.state, f32, True),
+        _is(y, "y", dev, pl.u, dt), _is(S_final, "S_final", dev, pl.state, f32, True), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _current(u))
+    _check(rc, "efla_scan_fwd")
+    return y, S_final
+
+
+def efla_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, S0=None, dS_final=None, *, offsets=None,
+                  softplus: bool = True, du=None, ddelta=None, dz=None, want_dS0: bool = True, workspace=None, stream=None):
+    """Backward of efla_scan_fwd (same shapes; dy as u).  Returns (du, ddelta, dA, dB, dC, dD, dz, ddelta_bias, dS0), None for
+    those of inputs that are None (and for dS0 unless it is wanted): du, ddelta, dz dense or into the tensors given (which may be
+    slices of one buffer), dB, dC dense, all in u's type; dA, dD, ddelta_bias, dS0 fp32."""
+    if _away(u, stream):
+        return _elsewhere(u, stream, efla_scan_bwd, u, delta, A, B, C, dy, D, z, delta_bias, S0, dS_final, offsets=offsets,
+                          softplus=softplus, du=du, ddelta=ddelta, dz=dz, want_dS0=want_dS0, workspace=workspace)
+    dt, f32, n, dev = u.dtype, torch.float32, _sequences(u, offsets, "u"), u.get_device()
+    if z is None and dz is not None:
+        raise ValueError("dz: there is no z")
+    du = torch.empty(u.shape, dtype=dt, device=u.device) if du is None else du
+    ddelta = torch.empty(u.shape, dtype=dt, device=u.device) if ddelta is None else ddelta
+    dz = torch.empty(u.shape, dtype=dt, device=u.device) if dz is None and z is not None else dz
+    strides = (u.stride(), delta.stride(), _opt_stride(z), dy.stride(), du.stride(), ddelta.stride(), _opt_stride(dz), B.stride(),
+               C.stride())
+    pl = _plan(("sb", u.shape, A.shape, C.shape, strides, dt, bool(softplus), n, offsets is None), lambda: _ScanPlan(
+        u.shape, A.shape, C.shape, n, offsets is not None, dt, softplus,
+        dict(zip(("u", "delta", "z", "dy", "du", "ddelta", "dz", "B", "C"), strides)), "bwd"))
+    dA = torch.empty(pl.A, dtype=f32, device=u.device)
+    dB = torch.empty(pl.bc, dtype=dt, device=u.device)
+    dC = torch.empty(pl.bc, dtype=dt, device=u.device)
+    dD = None if D is None else torch.empty(pl.d, dtype=f32, device=u.device)
+    dbias = None if delta_bias is None else torch.empty(pl.d, dtype=f32, device=u.device)
+    dS0 = torch.empty(pl.state, dtype=f32, device=u.device) if want_dS0 else None
+    ws = _ws(pl.ws, u, workspace)
+    rc = load_library().efla_scan_bwd(
+        pl.ref, None if offsets is None else offsets.data_ptr(), _is(u, "u", dev, pl.u, dt), _is(delta, "delta", dev, pl.u, dt),
+        _is(A, "A", dev, pl.A, f32, True), _is(B, "B", dev, pl.bc, dt), _is(C, "C", dev, pl.bc, dt), _is(D, "D", dev, pl.d, f32, True),
+        _is(z, "z", dev, pl.u, dt), _is(delta_bias, "delta_bias", dev, pl.d, f32, True), _is(S0, "S0", dev, pl.state, f32, True),
+        _is(dy, "dy", dev, pl.u, dt), _is(dS_final, "dS_final", dev, pl.state, f32, True), _is(du, "du", dev, pl.u, dt),
+        _is(ddelta, "ddelta", dev, pl.u, dt), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _ptr(dD), _is(dz, "dz", dev, pl.u, dt),
+        _ptr(dbias), _ptr(dS0), _ptr(ws), ws.numel() * ws.element_size(), _current(u))
+    _check(rc, "efla_scan_bwd")
+    return du, ddelta, dA, dB, dC, dD, dz, dbias, dS0
+
+
+def efla_scan_step(u, delta, A, B, C, S, D=None, z=None, delta_bias=None, *, slots=None, softplus: bool = True, y=None, stream=None):
+    """One token of the selective scan on a cache of states S [n,Di,N] fp32, updated in place.
+
+    u, delta, z [B,Di], B, C [B,G,N] (any strides, last dimension contiguous).  slots (int32 [B] on the GPU): each sequence's place
+    in the cache (outside [0, n): skipped, y = 0); None: place b.  Returns y [B,Di]."""
+    if _away(u, stream):
+        return _elsewhere(u, stream, efla_scan_step, u, delta, A, B, C, S, D, z, delta_bias, slots=slots, softplus=softplus, y=y)
+    dt, f32, dev = u.dtype, torch.float32, u.get_device()
+    if y is None:
+        y = torch.empty(u.shape, dtype=dt, device=u.device)
+    strides = (u.stride(), delta.stride(), _opt_stride(z), y.stride(), B.stride(), C.stride())
+    pl = _plan(("ss", u.shape, A.shape, C.shape, strides, dt, bool(softplus)), lambda: _ScanPlan(
+        u.shape, A.shape, C.shape, u.shape[0] if len(u.shape) else 0, False, dt, softplus,
+        dict(zip(("u", "delta", "z", "y", "B", "C"), strides)), "step"))
+    n = S.shape[0] if len(S.shape) == 3 else 0
+    rc = load_library().efla_scan_step(
+        pl.ref, _is(u, "u", dev, pl.u, dt), _is(delta, "delta", dev, pl.u, dt), _is(A, "A", dev, pl.A, f32, True),
+        _is(B, "B", dev, pl.bc, dt), _is(C, "C", dev, pl.bc, dt), _is(D, "D", dev, pl.d, f32, True), _is(z, "z", dev, pl.u, dt),
+        _is(delta_bias, "delta_bias", dev, pl.d, f32, True), _is(S, "S", dev, torch.Size((n,) + pl.state[1:]), f32, True),
+        _is(slots, "slots", dev, pl.B, torch.int32, True), n, _is(y, "y", dev, pl.u, dt), _current(u))
+    _check(rc, "efla_scan_step")
+    return y
+
+
+# ------------------------------------------------------------------ RMS norm of a residual stream
+class _RmsPlan:
+    def __init__(self, shape, strides, dtype, wdtype, eps, group, bwd):
+        D = shape[-1] if len(shape) else 0
+        rows = 1
+        for n in shape[:-1]:
+            rows *= n
+        self.x, self.w, self.rows = shape, torch.Size((D,)), torch.Size(shape[:-1])
+        self.scale = torch.Size(shape[:-1] + (-(-D // group) if group > 0 else 0,))
+        s = self.shape = RmsShape(rows=rows, D=D, group=group, dtype=_dt(dtype), weight_dtype=_dt(wdtype), eps=eps)
+        for n, x in strides.items():
+            if x is not None and len(x) == len(shape):   # (a tensor of another shape is refused where it is passed)
+                setattr(s, n + "_stride", _row_stride(n, shape, x))
+        self.ref = ctypes.byref(s)
+        self.ws = efla_rms_bwd_workspace_size(s) if bwd else 0
+
+
+def efla_rms_bwd_workspace_size(shape: RmsShape) -> int:
+    return load_library().efla_rms_bwd_workspace_size(ctypes.byref(shape))
+
+
+def efla_rms_fwd(x, weight, residual=None, *, eps: float = 1e-5, group: int = 0, y=None, scale=None, h=None, rstd=None, stream=None):
+    """RMS norm over the last dimension of h = x + residual (rounded to x's type): y = h rstd weight.  x, residual [..., D],
+    weight [D] (fp32 or bf16).  group = 0: y in x's type; 128 or D: y in float8_e4m3fn with fp32 scales [..., ceil(D / group)],
+    y ~ scale q for `group` columns each.
+
+    Returns (y, scale or None, h (x itself without a residual), rstd [...] fp32).  h may be given as x or residual: in place."""
+    if _away(x, stream):
+        return _elsewhere(x, stream, efla_rms_fwd, x, weight, residual, eps=eps, group=group, y=y, scale=scale, h=h, rstd=rstd)
+    dt, dev, f32 = x.dtype, x.get_device(), torch.float32
+    ydt = torch.float8_e4m3fn if group else dt
+    if residual is None and h is not None and h is not x:
+        raise ValueError("h: without a residual the stream is x itself")
+    if y is None:
+        y = torch.empty(x.shape, dtype=ydt, device=x.device)
+    if residual is not None and h is None:
+        h = torch.empty(x.shape, dtype=dt, device=x.device)
+    out = None if residual is None else h
+    strides = (x.stride(), _opt_stride(residual), y.stride(), _opt_stride(out))
+    pl = _plan(("rf", x.shape, strides, dt, weight.dtype, eps, group), lambda: _RmsPlan(
+        x.shape, dict(zip(("x", "residual", "y", "h"), strides)), dt, weight.dtype, eps, group, False))
+    if rstd is None:
+        rstd = torch.empty(pl.rows, dtype=f32, device=x.device)
+    if group and scale is None:
+        scale = torch.empty(pl.scale, dtype=f32, device=x.device)
+    if not group and scale is not None:
+        raise ValueError("scale: y has none without a group")
+    rc = load_library().efla_rms_fwd(
+        pl.ref, _is(x, "x", dev, pl.x, dt), _is(residual, "residual", dev, pl.x, dt), _is(weight, "weight", dev, pl.w, weight.dtype, True),
+        _is(y, "y", dev, pl.x, ydt), _is(scale, "scale", dev, pl.scale, f32, True), _is(out, "h", dev, pl.x, dt),
+        _is(rstd, "rstd", dev, pl.rows, f32, True), _current(x))
+    _check(rc, "efla_rms_fwd")
+    return y, scale, x if residual is None else h, rstd
+
+
+def efla_rms_bwd(h, weight, dy, rstd, *, dh=None, dx=None, workspace=None, stream=None):
+    """Backward of efla_rms_fwd from the h and rstd that it left; dh: the gradient that reaches the stream h from elsewhere (None:
+    zeros).  Returns (dx, dweight in weight's type); dx is the gradient of x and of the residual, dense or into the tensor given
+    (dh itself: in place)."""
+    if _away(h, stream):
+        return _elsewhere(h, stream, efla_rms_bwd, h, weight, dy, rstd, dh=dh, dx=dx, workspace=workspace)
+    dt, wdt, dev = h.dtype, weight.dtype, h.get_device()
+    if dx is None:
+        dx = torch.empty(h.shape, dtype=dt, device=h.device)
+    strides = (h.stride(), dy.stride(), _opt_stride(dh), dx.stride())
+    pl = _plan(("rb", h.shape, strides, dt, wdt), lambda: _RmsPlan(
+        h.shape, dict(zip(("h", "dy", "dh", "dx"), strides)), dt, wdt, 0.0, 0, True))
+    dw = torch.empty(pl.w, dtype=wdt, device=h.device)
+    ws = _ws(pl.ws, h, workspace)
+    rc = load_library().efla_rms_bwd(
+        pl.ref, _is(h, "h", dev, pl.x, dt), _is(weight, "weight", dev, pl.w, wdt, True), _is(dy, "dy", dev, pl.x, dt),
+        _is(rstd, "rstd", dev, pl.rows, torch.float32, True), _is(dh, "dh", dev, pl.x, dt), _is(dx, "dx", dev, pl.x, dt),
+        dw.data_ptr(), _ptr(ws), ws.numel() * ws.element_size(), _current(h))
+    _check(rc, "efla_rms_bwd")
+    return dx, dw
 
 
 def efla_tc_selftest(A, B, C, a_mn_major=False, b_mn_major=False, a_in_tmem=False, stream=None):

@@ -11,6 +11,7 @@
 #include "../../include/efla.h"
 #include "gated.h"
 #include "launch.h"
+#include "mix.h"
 
 namespace {
 // An NVTX range around an entry point's host-side work (argument checks, launches), for
@@ -28,7 +29,7 @@ namespace {
 thread_local char g_msg[512] = "";
 
 // Whether this process has launched, or captured, kernels that keep a status word of their own.
-std::atomic<bool> g_used_gated{false}, g_used_step{false}, g_used_norm{false};
+std::atomic<bool> g_used_gated{false}, g_used_step{false}, g_used_norm{false}, g_used_rms{false};
 
 efla_status fail(efla_status s, const char* fmt, ...) {
     va_list ap;
@@ -480,7 +481,8 @@ efla_status efla_get_status(cudaStream_t stream) {
                  {true, efla::bt_status_read_clear},     {true, efla::gt_status_read_clear},
                  {true, efla::sd_status_read_clear},     {g_used_gated, efla::gated_tc_status_read_clear},
                  {g_used_gated, efla::gated_bwd_tc_status_read_clear}, {g_used_step, efla::gated_step_status_read_clear},
-                 {g_used_norm, efla::norm_status_read_clear}};
+                 {g_used_norm, efla::norm_status_read_clear},
+                 {g_used_rms, efla::rms_status_read_clear}};
     unsigned int word = 0;
     for (const auto& w : words) {
         unsigned int one = 0;
@@ -898,6 +900,464 @@ efla_status efla_norm_bwd(const efla_norm_shape* s, const void* x, const void* w
     efla::prof_mark(nullptr, stream);
     const cudaError_t r = efla::launch_norm_bwd(d, x, weight, dy, stats, dx, dweight, dbias, workspace, stream);
     return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_norm_bwd");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ short convolution, selective scan, RMS norm
+namespace {
+
+// A [axes][tokens][channels] array through {axis, token} strides, as a Strided of one head.
+struct TokenRows {
+    long long s[3];
+    Strided x;
+    TokenRows(const void* p, const char* name, int axes, int L, int d, int es, const long long (&st)[2])
+        : s{st[0], 0, st[1]}, x{p, name, {axes, 1, L}, d, es, s} {}
+    TokenRows(const TokenRows&) = delete;
+};
+
+efla_status check_axes(int B, int L, int packed, bool step, const char* what, efla::Axes* a) {
+    if (B < 0 || L < 0) return fail(EFLA_ERR_INVALID_ARG, "negative size (B=%d L=%d)", B, L);
+    if (packed != 0 && packed != 1) return fail(EFLA_ERR_INVALID_ARG, "packed=%d: need 0 or 1", packed);
+    if (step && (packed || L != 1))
+        return fail(EFLA_ERR_INVALID_ARG, "%s needs L == 1 and packed == 0 (got %d, %d)", what, L, packed);
+    if (L > (1 << 30)) return fail(EFLA_ERR_UNSUPPORTED, "L=%d exceeds 2^30", L);
+    *a = efla::Axes{B, L, packed, nullptr};
+    return EFLA_OK;
+}
+
+efla_status check_offsets(const int* offsets, efla::Axes* a) {
+    if (!a->packed) return EFLA_OK;
+    if (!offsets) return fail(EFLA_ERR_INVALID_ARG, "offsets is NULL (packed)");
+    if ((uintptr_t)offsets % 4) return fail(EFLA_ERR_ALIGNMENT, "offsets is not 4-byte aligned");
+    a->offsets = offsets;
+    return EFLA_OK;
+}
+
+efla_status take_strides(const long long (&from)[2], long long (&to)[2]) {
+    for (int i = 0; i < 2; ++i) {
+        if (from[i] < 0) return fail(EFLA_ERR_INVALID_ARG, "negative stride");
+        to[i] = from[i];
+    }
+    return EFLA_OK;
+}
+
+// A dense array: present where it has elements (unless optional), aligned, and apart from what it must not overlap.
+struct Dense {
+    Span s;
+    int align;
+    bool needed;
+};
+efla_status check_dense(const Dense* x, int n) {
+    for (int i = 0; i < n; ++i) {
+        if (!x[i].s.p && x[i].needed && x[i].s.n) return fail(EFLA_ERR_INVALID_ARG, "%s is NULL", x[i].s.name);
+        if ((uintptr_t)x[i].s.p % x[i].align)
+            return fail(EFLA_ERR_ALIGNMENT, "%s is not aligned to %d bytes", x[i].s.name, x[i].align);
+    }
+    return EFLA_OK;
+}
+
+// Token arrays x[0 .. n-1] (outputs from first_out on), dense inputs, dense outputs: every output apart from every
+// input, from the other outputs and from the workspace (which is one of the dense outputs).
+efla_status check_apart(const Strided* const* x, int n, int first_out, const Dense* ins, int nin, const Dense* outs, int nout) {
+    for (int i = first_out; i < n; ++i) {
+        const Span o = x[i]->span();
+        for (int j = 0; j < n; ++j) {
+            if (j == i || (j >= first_out && j < i) || !overlap(o, x[j]->span())) continue;
+            if (!interleaved(*x[i], *x[j]) && !interleaved(*x[j], *x[i]))
+                return fail(EFLA_ERR_INVALID_ARG, "%s overlaps %s%s", o.name, j < first_out ? "input " : "", x[j]->name);
+        }
+        for (int j = 0; j < nin; ++j)
+            if (overlap(o, ins[j].s)) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input %s", o.name, ins[j].s.name);
+    }
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < n; ++j)
+            if (overlap(outs[i].s, x[j]->span()))
+                return fail(EFLA_ERR_INVALID_ARG, "%s overlaps %s%s", outs[i].s.name, j < first_out ? "input " : "", x[j]->name);
+        for (int j = 0; j < nin; ++j)
+            if (overlap(outs[i].s, ins[j].s))
+                return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input %s", outs[i].s.name, ins[j].s.name);
+        for (int j = i + 1; j < nout; ++j)
+            if (overlap(outs[i].s, outs[j].s))
+                return fail(EFLA_ERR_INVALID_ARG, "%s overlaps %s", outs[i].s.name, outs[j].s.name);
+    }
+    return EFLA_OK;
+}
+
+efla_status check_token_rows(const Strided* const* x, int n, int first_out) {
+    for (int i = 0; i < n; ++i) {
+        const efla_status st = check_strided(x[i], 1, i < first_out ? 1 : 0);
+        if (st != EFLA_OK) return st;
+    }
+    return EFLA_OK;
+}
+
+efla_status check_conv(const efla_conv_shape* s, bool step, efla::ConvDims* d) {
+    if (!s) return fail(EFLA_ERR_INVALID_ARG, "shape is NULL");
+    efla_status st = check_axes(s->B, s->L, s->packed, step, "efla_conv_step", &d->at);
+    if (st != EFLA_OK) return st;
+    if (s->D < 1 || s->D > 65536) return fail(EFLA_ERR_UNSUPPORTED, "D=%d: need 1 .. 65536", s->D);
+    if (s->W < 2 || s->W > 4) return fail(EFLA_ERR_UNSUPPORTED, "W=%d: need 2 .. 4", s->W);
+    if (!dtype_ok(s->dtype) || !dtype_ok(s->weight_dtype))
+        return fail(EFLA_ERR_UNSUPPORTED, "dtype=%d weight_dtype=%d: need EFLA_F32 or EFLA_BF16", (int)s->dtype, (int)s->weight_dtype);
+    if (s->silu != 0 && s->silu != 1) return fail(EFLA_ERR_INVALID_ARG, "silu=%d: need 0 or 1", s->silu);
+    // (threads of a launch: one for four tokens of a channel at most, and for a row of a state)
+    if (((double)d->at.rows() * (s->L / 4 + 1.0) + 3.0 * s->B) * s->D / 256 > 2.0e9)
+        return fail(EFLA_ERR_UNSUPPORTED, "B=%d L=%d D=%d: too many tokens for one launch", s->B, s->L, s->D);
+    d->D = s->D; d->W = s->W;
+    d->bf16 = s->dtype == EFLA_BF16;
+    d->w_bf16 = s->weight_dtype == EFLA_BF16;
+    d->silu = s->silu;
+    if ((st = take_strides(s->x_stride, d->xs)) != EFLA_OK || (st = take_strides(s->y_stride, d->ys)) != EFLA_OK ||
+        (st = take_strides(s->dy_stride, d->dys)) != EFLA_OK || (st = take_strides(s->dx_stride, d->dxs)) != EFLA_OK)
+        return st;
+    return EFLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+efla_status efla_conv_fwd(const efla_conv_shape* s, const int* offsets, const void* x, const void* weight, const void* bias,
+                          const void* S0, void* y, void* S_final, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_conv_fwd");
+    g_msg[0] = 0;
+    efla::ConvDims d;
+    efla_status st = check_conv(s, false, &d);
+    if (st != EFLA_OK) return st;
+    if (d.at.B == 0) return EFLA_OK;
+    const int e = (int)esize(s->dtype), we = (int)esize(s->weight_dtype), axes = d.at.rows();
+    const TokenRows rx(x, "x", axes, s->L, s->D, e, s->x_stride), ry(y, "y", axes, s->L, s->D, e, s->y_stride);
+    const Strided* const io[] = {&rx.x, &ry.x};
+    if ((st = check_token_rows(io, 2, 1)) != EFLA_OK) return st;
+    const size_t state = (size_t)s->B * (s->W - 1) * s->D * e;
+    const Dense in[] = {{{weight, (size_t)s->D * s->W * we, "weight"}, we, true}, {{bias, (size_t)s->D * we, "bias"}, we, false},
+                        {{S0, state, "S0"}, e, false}, {{d.at.packed ? offsets : nullptr, ((size_t)s->B + 1) * 4, "offsets"}, 1, false}};
+    const Dense out[] = {{{S_final, state, "S_final"}, e, false}};
+    if ((st = check_dense(in, 4)) != EFLA_OK || (st = check_dense(out, 1)) != EFLA_OK) return st;
+    if ((st = check_offsets(offsets, &d.at)) != EFLA_OK) return st;
+    if ((st = check_apart(io, 2, 1, in, 4, out, 1)) != EFLA_OK) return st;
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_conv_fwd(d, x, weight, bias, S0, y, S_final, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_conv_fwd");
+}
+
+size_t efla_conv_bwd_workspace_size(const efla_conv_shape* s) {
+    efla::ConvDims d;
+    return check_conv(s, false, &d) == EFLA_OK ? efla::conv_bwd_ws_bytes(d) : 0;
+}
+
+efla_status efla_conv_bwd(const efla_conv_shape* s, const int* offsets, const void* x, const void* weight, const void* bias,
+                          const void* S0, const void* dy, const void* dS_final, void* dx, void* dweight, void* dbias,
+                          void* dS0, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_conv_bwd");
+    g_msg[0] = 0;
+    efla::ConvDims d;
+    efla_status st = check_conv(s, false, &d);
+    if (st != EFLA_OK) return st;
+    const int e = (int)esize(s->dtype), we = (int)esize(s->weight_dtype), axes = d.at.rows();
+    const TokenRows rx(x, "x", axes, s->L, s->D, e, s->x_stride), rg(dy, "dy", axes, s->L, s->D, e, s->dy_stride),
+        rd(dx, "dx", axes, s->L, s->D, e, s->dx_stride);
+    const Strided* const io[] = {&rx.x, &rg.x, &rd.x};
+    if ((st = check_token_rows(io, 3, 2)) != EFLA_OK) return st;
+    const size_t state = (size_t)s->B * (s->W - 1) * s->D * e, nw = (size_t)s->D * s->W * we, nb = (size_t)s->D * we;
+    const Dense in[] = {{{weight, nw, "weight"}, we, true}, {{bias, nb, "bias"}, we, false}, {{S0, state, "S0"}, e, false},
+                        {{dS_final, state, "dS_final"}, e, false},
+                        {{d.at.packed ? offsets : nullptr, ((size_t)s->B + 1) * 4, "offsets"}, 1, false}};
+    const Dense out[] = {{{dweight, nw, "dweight"}, we, true}, {{dbias, nb, "dbias"}, we, false}, {{dS0, state, "dS0"}, e, false},
+                         {{workspace, workspace_bytes, "workspace"}, 16, false}};
+    if ((st = check_dense(in, 5)) != EFLA_OK || (st = check_dense(out, 4)) != EFLA_OK) return st;
+    if (dbias && !bias) return fail(EFLA_ERR_INVALID_ARG, "dbias is asked for, but bias is NULL");
+    if ((st = check_offsets(offsets, &d.at)) != EFLA_OK) return st;
+    if ((st = check_apart(io, 3, 2, in, 5, out, 4)) != EFLA_OK) return st;
+    const size_t need = efla::conv_bwd_ws_bytes(d);
+    if (!workspace || workspace_bytes < need)
+        return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_conv_bwd(d, x, weight, bias, S0, dy, dS_final, dx, dweight, dbias, dS0, workspace, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_conv_bwd");
+}
+
+efla_status efla_conv_step(const efla_conv_shape* s, const void* x, const void* weight, const void* bias, void* S,
+                           const int* slots, int nslots, void* y, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_conv_step");
+    g_msg[0] = 0;
+    efla::ConvDims d;
+    efla_status st = check_conv(s, true, &d);
+    if (st != EFLA_OK) return st;
+    if (nslots < 0 || (!slots && nslots < s->B))
+        return fail(EFLA_ERR_INVALID_ARG, "nslots=%d: the cache holds fewer states than the B=%d sequences", nslots, s->B);
+    if (d.at.B == 0) return EFLA_OK;
+    const int e = (int)esize(s->dtype), we = (int)esize(s->weight_dtype);
+    const TokenRows rx(x, "x", s->B, 1, s->D, e, s->x_stride), ry(y, "y", s->B, 1, s->D, e, s->y_stride);
+    const Strided* const io[] = {&rx.x, &ry.x};
+    if ((st = check_token_rows(io, 2, 1)) != EFLA_OK) return st;
+    const Dense in[] = {{{weight, (size_t)s->D * s->W * we, "weight"}, we, true}, {{bias, (size_t)s->D * we, "bias"}, we, false},
+                        {{slots, (size_t)s->B * 4, "slots"}, 4, false}};
+    const Dense out[] = {{{S, (size_t)nslots * (s->W - 1) * s->D * e, "S"}, e, true}};
+    if ((st = check_dense(in, 3)) != EFLA_OK || (st = check_dense(out, 1)) != EFLA_OK) return st;
+    if ((st = check_apart(io, 2, 1, in, 3, out, 1)) != EFLA_OK) return st;
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_conv_step(d, x, weight, bias, S, slots, nslots, y, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_conv_step");
+}
+
+}  // extern "C"
+
+namespace {
+
+efla_status check_scan(const efla_scan_shape* s, bool step, efla::ScanDims* d) {
+    if (!s) return fail(EFLA_ERR_INVALID_ARG, "shape is NULL");
+    efla_status st = check_axes(s->B, s->L, s->packed, step, "efla_scan_step", &d->at);
+    if (st != EFLA_OK) return st;
+    if (s->D < 1 || s->D > 65536) return fail(EFLA_ERR_UNSUPPORTED, "D=%d: need 1 .. 65536", s->D);
+    if (s->G < 1 || s->D % s->G) return fail(EFLA_ERR_INVALID_ARG, "D=%d channels are not a multiple of G=%d groups", s->D, s->G);
+    if (s->N < 1 || s->N > 64) return fail(EFLA_ERR_UNSUPPORTED, "N=%d: need 1 .. 64 states", s->N);
+    if (!dtype_ok(s->dtype)) return fail(EFLA_ERR_UNSUPPORTED, "dtype=%d: need EFLA_F32 or EFLA_BF16", (int)s->dtype);
+    if (s->softplus != 0 && s->softplus != 1) return fail(EFLA_ERR_INVALID_ARG, "softplus=%d: need 0 or 1", s->softplus);
+    if (!step && !s->packed && s->B > 65535) return fail(EFLA_ERR_UNSUPPORTED, "B=%d sequences exceed 65535 (pack them)", s->B);
+    // (threads of a launch: one for a token's B and C of each group, or for four states of a sequence's channel)
+    if ((double)d->at.rows() * s->L * s->G / 2 > 2.0e9 || (step && (double)s->B * s->D * 16 / 256 > 2.0e9) || s->G > 32767)
+        return fail(EFLA_ERR_UNSUPPORTED, "B=%d L=%d D=%d G=%d: too many for one launch", s->B, s->L, s->D, s->G);
+    d->D = s->D; d->G = s->G; d->N = s->N;
+    d->bf16 = s->dtype == EFLA_BF16;
+    d->softplus = s->softplus;
+    const long long(*from[])[2] = {&s->u_stride, &s->delta_stride, &s->z_stride, &s->y_stride, &s->dy_stride, &s->du_stride, &s->ddelta_stride,
+                                   &s->dz_stride};
+    long long(*to[])[2] = {&d->us, &d->ds, &d->zs, &d->ys, &d->dys, &d->dus, &d->dds, &d->dzs};
+    for (int i = 0; i < 8; ++i)
+        if ((st = take_strides(*from[i], *to[i])) != EFLA_OK) return st;
+    for (int i = 0; i < 3; ++i) {
+        if (s->B_stride[i] < 0 || s->C_stride[i] < 0) return fail(EFLA_ERR_INVALID_ARG, "negative stride");
+        d->bs[i] = s->B_stride[i];
+        d->cs[i] = s->C_stride[i];
+    }
+    return EFLA_OK;
+}
+
+// B or C: {axis, token, group} strides as a Strided's {axis, head, token}
+struct GroupRows {
+    long long s[3];
+    Strided x;
+    GroupRows(const void* p, const char* name, int axes, int L, int G, int N, int es, const long long (&st)[3])
+        : s{st[0], st[2], st[1]}, x{p, name, {axes, G, L}, N, es, s} {}
+    GroupRows(const GroupRows&) = delete;
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t efla_scan_fwd_workspace_size(const efla_scan_shape* s) {
+    efla::ScanDims d;
+    return check_scan(s, false, &d) == EFLA_OK && d.at.B ? efla::scan_fwd_ws_bytes(d) : 0;
+}
+
+efla_status efla_scan_fwd(const efla_scan_shape* s, const int* offsets, const void* u, const void* delta, const float* A,
+                          const void* Bm, const void* C, const float* skip, const void* z, const float* delta_bias, const float* S0,
+                          void* y, float* S_final, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_scan_fwd");
+    g_msg[0] = 0;
+    efla::ScanDims d;
+    efla_status st = check_scan(s, false, &d);
+    if (st != EFLA_OK) return st;
+    if (d.at.B == 0) return EFLA_OK;
+    const int e = (int)esize(s->dtype), axes = d.at.rows();
+    const TokenRows ru(u, "u", axes, s->L, s->D, e, s->u_stride), rdt(delta, "delta", axes, s->L, s->D, e, s->delta_stride),
+        rz(z, "z", z ? axes : 0, s->L, s->D, e, s->z_stride), ry(y, "y", axes, s->L, s->D, e, s->y_stride);
+    const GroupRows rb(Bm, "B", axes, s->L, s->G, s->N, e, s->B_stride), rc(C, "C", axes, s->L, s->G, s->N, e, s->C_stride);
+    const Strided* const io[] = {&ru.x, &rdt.x, &rb.x, &rc.x, &rz.x, &ry.x};
+    if ((st = check_token_rows(io, 6, 5)) != EFLA_OK) return st;
+    const size_t state = (size_t)s->B * s->D * s->N * 4, ch = (size_t)s->D * 4;
+    const Dense in[] = {{{A, ch * s->N, "A"}, 4, true}, {{skip, ch, "skip"}, 4, false}, {{delta_bias, ch, "delta_bias"}, 4, false},
+                        {{S0, state, "S0"}, 16, false},
+                        {{d.at.packed ? offsets : nullptr, ((size_t)s->B + 1) * 4, "offsets"}, 1, false}};
+    const Dense out[] = {{{S_final, state, "S_final"}, 16, false}, {{workspace, workspace_bytes, "workspace"}, 16, false}};
+    if ((st = check_dense(in, 5)) != EFLA_OK || (st = check_dense(out, 2)) != EFLA_OK) return st;
+    if ((st = check_offsets(offsets, &d.at)) != EFLA_OK) return st;
+    if ((st = check_apart(io, 6, 5, in, 5, out, 2)) != EFLA_OK) return st;
+    const size_t need = efla::scan_fwd_ws_bytes(d);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    const efla::ScanIn i{u, delta, A, Bm, C, skip, z, delta_bias, S0};
+    efla::prof_mark(nullptr, stream);
+    cudaError_t r;
+    if (s->L == 0) r = S_final ? efla::launch_state_copy((long long)s->B * s->D * s->N, S0, S_final, stream) : cudaSuccess;
+    else r = efla::launch_scan_fwd(d, i, y, S_final, workspace, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_scan_fwd");
+}
+
+size_t efla_scan_bwd_workspace_size(const efla_scan_shape* s) {
+    efla::ScanDims d;
+    return check_scan(s, false, &d) == EFLA_OK ? efla::scan_bwd_ws_bytes(d) : 0;
+}
+
+efla_status efla_scan_bwd(const efla_scan_shape* s, const int* offsets, const void* u, const void* delta, const float* A,
+                          const void* Bm, const void* C, const float* skip, const void* z, const float* delta_bias, const float* S0,
+                          const void* dy, const float* dS_final, void* du, void* ddelta, float* dA, void* dB, void* dC, float* dskip,
+                          void* dz, float* ddelta_bias, float* dS0, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_scan_bwd");
+    g_msg[0] = 0;
+    efla::ScanDims d;
+    efla_status st = check_scan(s, false, &d);
+    if (st != EFLA_OK) return st;
+    const int e = (int)esize(s->dtype), axes = d.at.rows();
+    if (!z != !dz && axes && s->L) return fail(EFLA_ERR_INVALID_ARG, "z and dz go together: one of them is NULL");
+    const TokenRows ru(u, "u", axes, s->L, s->D, e, s->u_stride), rdt(delta, "delta", axes, s->L, s->D, e, s->delta_stride),
+        rz(z, "z", z ? axes : 0, s->L, s->D, e, s->z_stride), rg(dy, "dy", axes, s->L, s->D, e, s->dy_stride),
+        rdu(du, "du", axes, s->L, s->D, e, s->du_stride), rdd(ddelta, "ddelta", axes, s->L, s->D, e, s->ddelta_stride),
+        rdz(dz, "dz", dz ? axes : 0, s->L, s->D, e, s->dz_stride);
+    const GroupRows rb(Bm, "B", axes, s->L, s->G, s->N, e, s->B_stride), rc(C, "C", axes, s->L, s->G, s->N, e, s->C_stride);
+    const Strided* const io[] = {&ru.x, &rdt.x, &rb.x, &rc.x, &rz.x, &rg.x, &rdu.x, &rdd.x, &rdz.x};
+    if ((st = check_token_rows(io, 9, 6)) != EFLA_OK) return st;
+    const size_t state = (size_t)s->B * s->D * s->N * 4, ch = (size_t)s->D * 4, bc = (size_t)axes * s->L * s->G * s->N * e;
+    const Dense in[] = {{{A, ch * s->N, "A"}, 4, true}, {{skip, ch, "skip"}, 4, false}, {{delta_bias, ch, "delta_bias"}, 4, false},
+                        {{S0, state, "S0"}, 16, false}, {{dS_final, state, "dS_final"}, 16, false},
+                        {{d.at.packed ? offsets : nullptr, ((size_t)s->B + 1) * 4, "offsets"}, 1, false}};
+    const Dense out[] = {{{dA, ch * s->N, "dA"}, 4, true}, {{dB, bc, "dB"}, e, true}, {{dC, bc, "dC"}, e, true},
+                         {{dskip, ch, "dskip"}, 4, false}, {{ddelta_bias, ch, "ddelta_bias"}, 4, false},
+                         {{dS0, state, "dS0"}, 16, false}, {{workspace, workspace_bytes, "workspace"}, 16, false}};
+    if ((st = check_dense(in, 6)) != EFLA_OK || (st = check_dense(out, 7)) != EFLA_OK) return st;
+    if (dskip && !skip) return fail(EFLA_ERR_INVALID_ARG, "dskip is asked for, but skip is NULL");
+    if (ddelta_bias && !delta_bias) return fail(EFLA_ERR_INVALID_ARG, "ddelta_bias is asked for, but delta_bias is NULL");
+    if ((st = check_offsets(offsets, &d.at)) != EFLA_OK) return st;
+    if ((st = check_apart(io, 9, 6, in, 6, out, 7)) != EFLA_OK) return st;
+    const size_t need = efla::scan_bwd_ws_bytes(d);
+    if (!workspace || workspace_bytes < need)
+        return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    const efla::ScanIn i{u, delta, A, Bm, C, skip, z, delta_bias, S0};
+    const efla::ScanGrads g{dy, dS_final, du, ddelta, dA, dB, dC, dskip, dz, ddelta_bias, dS0};
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_scan_bwd(d, i, g, workspace, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_scan_bwd");
+}
+
+efla_status efla_scan_step(const efla_scan_shape* s, const void* u, const void* delta, const float* A, const void* Bm, const void* C,
+                           const float* skip, const void* z, const float* delta_bias, float* S, const int* slots, int nslots,
+                           void* y, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_scan_step");
+    g_msg[0] = 0;
+    efla::ScanDims d;
+    efla_status st = check_scan(s, true, &d);
+    if (st != EFLA_OK) return st;
+    if (nslots < 0 || (!slots && nslots < s->B))
+        return fail(EFLA_ERR_INVALID_ARG, "nslots=%d: the cache holds fewer states than the B=%d sequences", nslots, s->B);
+    if (d.at.B == 0) return EFLA_OK;
+    const int e = (int)esize(s->dtype);
+    const TokenRows ru(u, "u", s->B, 1, s->D, e, s->u_stride), rdt(delta, "delta", s->B, 1, s->D, e, s->delta_stride),
+        rz(z, "z", z ? s->B : 0, 1, s->D, e, s->z_stride), ry(y, "y", s->B, 1, s->D, e, s->y_stride);
+    const GroupRows rb(Bm, "B", s->B, 1, s->G, s->N, e, s->B_stride), rc(C, "C", s->B, 1, s->G, s->N, e, s->C_stride);
+    const Strided* const io[] = {&ru.x, &rdt.x, &rb.x, &rc.x, &rz.x, &ry.x};
+    if ((st = check_token_rows(io, 6, 5)) != EFLA_OK) return st;
+    const size_t ch = (size_t)s->D * 4;
+    const Dense in[] = {{{A, ch * s->N, "A"}, 4, true}, {{skip, ch, "skip"}, 4, false}, {{delta_bias, ch, "delta_bias"}, 4, false},
+                        {{slots, (size_t)s->B * 4, "slots"}, 4, false}};
+    const Dense out[] = {{{S, (size_t)nslots * s->D * s->N * 4, "S"}, 16, true}};
+    if ((st = check_dense(in, 4)) != EFLA_OK || (st = check_dense(out, 1)) != EFLA_OK) return st;
+    if ((st = check_apart(io, 6, 5, in, 4, out, 1)) != EFLA_OK) return st;
+    const efla::ScanIn i{u, delta, A, Bm, C, skip, z, delta_bias, nullptr};
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_scan_step(d, i, S, slots, nslots, y, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_scan_step");
+}
+
+}  // extern "C"
+
+namespace {
+
+// x_s, r_s, y_s, h_s: the strides of the arrays that launch_rms_fwd (or, backward: h, dh, dy, dx) reads and writes
+efla_status check_rms(const efla_rms_shape* s, bool bwd, efla::RmsDims* d) {
+    if (!s) return fail(EFLA_ERR_INVALID_ARG, "shape is NULL");
+    if (s->rows < 0 || s->D < 0) return fail(EFLA_ERR_INVALID_ARG, "negative size (rows=%lld D=%d)", s->rows, s->D);
+    if (s->D < 1 || s->D > 16384) return fail(EFLA_ERR_UNSUPPORTED, "D=%d: need 1 .. 16384", s->D);
+    if (s->rows > 0x7fffffffLL) return fail(EFLA_ERR_UNSUPPORTED, "rows=%lld exceed 2^31-1", s->rows);
+    if (!dtype_ok(s->dtype) || !dtype_ok(s->weight_dtype))
+        return fail(EFLA_ERR_UNSUPPORTED, "dtype=%d weight_dtype=%d: need EFLA_F32 or EFLA_BF16", (int)s->dtype, (int)s->weight_dtype);
+    if (!bwd && s->group != 0 && s->group != 128 && s->group != s->D)
+        return fail(EFLA_ERR_UNSUPPORTED, "group=%d: need 0, 128 or D=%d", s->group, s->D);
+    if (!bwd && !(s->eps >= 0.f)) return fail(EFLA_ERR_INVALID_ARG, "eps=%g: need a non-negative number", (double)s->eps);
+    const long long one = s->D;
+    const bool many = s->rows > 1;
+    *d = efla::RmsDims{s->rows, many ? (bwd ? s->h_stride : s->x_stride) : one, many ? (bwd ? s->dh_stride : s->residual_stride) : one,
+                       many ? (bwd ? s->dy_stride : s->y_stride) : one, many ? (bwd ? s->dx_stride : s->h_stride) : one, s->D,
+                       s->dtype == EFLA_BF16, s->weight_dtype == EFLA_BF16, bwd ? 0 : s->group, s->eps};
+    return EFLA_OK;
+}
+
+size_t rms_bytes(const efla::RmsDims& d, long long stride, int es) { return d.rows ? ((size_t)(d.rows - 1) * stride + d.D) * es : 0; }
+
+efla_status check_stride(const char* name, const void* p, long long stride, int D) {
+    return p && stride < D ? fail(EFLA_ERR_INVALID_ARG, "%s: row stride %lld is below D=%d", name, stride, D) : EFLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+efla_status efla_rms_fwd(const efla_rms_shape* s, const void* x, const void* residual, const void* weight, void* y, float* scale,
+                         void* h, float* rstd, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_rms_fwd");
+    g_msg[0] = 0;
+    efla::RmsDims d;
+    efla_status st = check_rms(s, false, &d);
+    if (st != EFLA_OK || d.rows == 0) return st;
+    if ((!residual) != (!h)) return fail(EFLA_ERR_INVALID_ARG, "residual and h go together: one of them is NULL");
+    if ((st = check_stride("x", x, d.x_stride, d.D)) != EFLA_OK || (st = check_stride("residual", residual, d.r_stride, d.D)) != EFLA_OK ||
+        (st = check_stride("y", y, d.y_stride, d.D)) != EFLA_OK || (st = check_stride("h", h, d.h_stride, d.D)) != EFLA_OK)
+        return st;
+    const int e = d.bf16 ? 2 : 4, we = d.w_bf16 ? 2 : 4, ye = d.group ? 1 : e;
+    const size_t groups = d.group ? (d.D + d.group - 1) / d.group : 0;
+    const bool on_x = h && h == x && d.h_stride == d.x_stride, on_r = h && h == residual && d.h_stride == d.r_stride;   // in place
+    const Dense in[] = {{{x, rms_bytes(d, d.x_stride, e), "x"}, e, true}, {{residual, rms_bytes(d, d.r_stride, e), "residual"}, e, false},
+                        {{weight, (size_t)d.D * we, "weight"}, we, true}};
+    const Dense out[] = {{{y, rms_bytes(d, d.y_stride, ye), "y"}, ye, true}, {{scale, groups * d.rows * 4, "scale"}, 4, true},
+                         {{rstd, (size_t)d.rows * 4, "rstd"}, 4, true}, {{h, rms_bytes(d, d.h_stride, e), "h"}, e, false}};
+    if ((st = check_dense(in, 3)) != EFLA_OK || (st = check_dense(out, 4)) != EFLA_OK) return st;
+    if ((st = check_apart(nullptr, 0, 0, in, 3, out, 3)) != EFLA_OK) return st;
+    for (int i = 0; i < 3; ++i) {
+        if (overlap(out[3].s, out[i].s)) return fail(EFLA_ERR_INVALID_ARG, "h overlaps %s", out[i].s.name);
+        if ((i != 0 || !on_x) && (i != 1 || !on_r) && overlap(out[3].s, in[i].s))
+            return fail(EFLA_ERR_INVALID_ARG, "h overlaps input %s", in[i].s.name);
+    }
+    g_used_rms = true;
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_rms_fwd(d, x, residual, weight, y, scale, h, rstd, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_rms_fwd");
+}
+
+size_t efla_rms_bwd_workspace_size(const efla_rms_shape* s) {
+    efla::RmsDims d;
+    return check_rms(s, true, &d) == EFLA_OK ? efla::rms_bwd_ws_bytes(d) : 0;
+}
+
+efla_status efla_rms_bwd(const efla_rms_shape* s, const void* h, const void* weight, const void* dy, const float* rstd, const void* dh,
+                         void* dx, void* dweight, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    NvtxRange nvtx_range("efla_rms_bwd");
+    g_msg[0] = 0;
+    efla::RmsDims d;
+    efla_status st = check_rms(s, true, &d);
+    if (st != EFLA_OK) return st;
+    if ((st = check_stride("h", h, d.x_stride, d.D)) != EFLA_OK || (st = check_stride("dh", dh, d.r_stride, d.D)) != EFLA_OK ||
+        (st = check_stride("dy", dy, d.y_stride, d.D)) != EFLA_OK || (st = check_stride("dx", dx, d.h_stride, d.D)) != EFLA_OK)
+        return st;
+    const int e = d.bf16 ? 2 : 4, we = d.w_bf16 ? 2 : 4;
+    const bool on_dh = dx && dx == dh && d.h_stride == d.r_stride;   // in place
+    const Dense in[] = {{{h, rms_bytes(d, d.x_stride, e), "h"}, e, true}, {{weight, (size_t)d.D * we, "weight"}, we, true},
+                        {{dy, rms_bytes(d, d.y_stride, e), "dy"}, e, true}, {{rstd, (size_t)d.rows * 4, "rstd"}, 4, true},
+                        {{dh, rms_bytes(d, d.r_stride, e), "dh"}, e, false}};
+    const Dense out[] = {{{dx, rms_bytes(d, d.h_stride, e), "dx"}, e, true}, {{dweight, (size_t)d.D * we, "dweight"}, we, true},
+                         {{workspace, workspace_bytes, "workspace"}, 16, false}};
+    if ((st = check_dense(in, 5)) != EFLA_OK || (st = check_dense(out, 3)) != EFLA_OK) return st;
+    if ((st = check_apart(nullptr, 0, 0, in, 4, out, 3)) != EFLA_OK) return st;
+    for (int i = 0; i < 3; ++i)
+        if ((i != 0 || !on_dh) && overlap(out[i].s, in[4].s)) return fail(EFLA_ERR_INVALID_ARG, "%s overlaps input dh", out[i].s.name);
+    const size_t need = efla::rms_bwd_ws_bytes(d);
+    if (!workspace || workspace_bytes < need)
+        return fail(EFLA_ERR_WORKSPACE, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    g_used_rms = true;
+    efla::prof_mark(nullptr, stream);
+    const cudaError_t r = efla::launch_rms_bwd(d, h, weight, dy, rstd, dh, dx, dweight, workspace, stream);
+    return r == cudaSuccess ? EFLA_OK : cuda_fail(r, "efla_rms_bwd");
 }
 
 }  // extern "C"

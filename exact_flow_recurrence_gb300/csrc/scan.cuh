@@ -1,0 +1,197 @@
+// scan.cuh -- parts that the selective scan's forward and backward kernels share.
+//
+// Channel d keeps N states; with the A, B, C of its group:
+//   dt = softplus(delta + bias)  (or delta + bias),   h <- e^{dt A} h + dt u B,   y = (sum_n C h + skip u) z sigmoid(z)
+//
+// A thread owns four neighbouring channels and four neighbouring states of each: N/4 lanes (rounded up to a
+// power of two, NL) lie side by side along the states, the warp's other lanes along the channels.  Four warps
+// make a CTA: channels of one group, all on the same tokens.  Tiles of kTile tokens pass through shared memory:
+// what depends on a channel alone (dt, dt u, the gated gradient) is worked out once there.
+// Tokens outside every sequence, and channels and states past the last, are zeros: e^0 h + 0 leaves a state alone.
+#pragma once
+
+#include "mix.cuh"
+
+namespace efla {
+
+constexpr int kTile = 16;        // tokens a tile
+constexpr int kScanThreads = 128;
+
+// NL: lanes along the states
+template <int NL>
+struct ScanTile {
+    static constexpr int states = 4 * NL;               // states, padded
+    static constexpr int warp_ch = 4 * (32 / NL);       // channels a warp
+    static constexpr int ch = 4 * warp_ch;              // channels a CTA
+};
+
+// A CTA's channels c0 .. c0 + n - 1, of group g; block `cb` of that group's.
+struct ChBlock {
+    int g, cb, c0, n;
+};
+template <int NL>
+__device__ __forceinline__ ChBlock ch_block(const ScanDims& d, int index) {
+    const int per = d.D / d.G, blocks = (per + ScanTile<NL>::ch - 1) / ScanTile<NL>::ch;
+    const int g = index / blocks, cb = index % blocks;
+    return ChBlock{g, cb, g * per + cb * ScanTile<NL>::ch, min(ScanTile<NL>::ch, per - cb * ScanTile<NL>::ch)};
+}
+inline int ch_blocks(const ScanDims& d, int ch) { return d.G * ((d.D / d.G + ch - 1) / ch); }
+
+// n (0 .. 4) neighbouring elements as fp32, zeros behind them; WIDE: whole and aligned where n = 4
+template <typename T, bool WIDE>
+__device__ __forceinline__ float4 load4(const T* p, int n) {
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (WIDE && n >= 4) {
+        Vec<T, 4> v;
+        v.load(p);
+        v.get(f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) f[i] = (float)p[i];
+    }
+    return make_float4(f[0], f[1], f[2], f[3]);
+}
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store4(T* p, float4 x, int n) {
+    const float f[4] = {x.x, x.y, x.z, x.w};
+    if (WIDE && n >= 4) {
+        Vec<T, 4> v;
+        v.set(f);
+        v.store(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = (T)f[i];
+    }
+}
+
+__device__ __forceinline__ float softplus_of(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+__device__ __forceinline__ float step_of(const ScanDims& d, float x) { return d.softplus ? softplus_of(x) : x; }
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
+__device__ __forceinline__ float at4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// e^{dt A} from a2 = A log2(e).  ex2.approx gives a little too small a result: -5e-9 of it on average for exponents of
+// -2^-17 .. -2^-9, -1e-8 to -3e-8 up to -2^-3 (measured over all of each binade).  A state that remembers a thousand tokens
+// would collect that, so 1.1e-8 is added to the exponent, in the product's own rounding (it leaves e^0 = 1 as it is).
+constexpr float kEx2Mean = 1.1e-8f * kLog2eF;
+__device__ __forceinline__ float2 decay2(float2 dt, float2 a2) {
+    const float2 x = fma2(dt, a2, both(kEx2Mean));
+    return make_float2(ex2(x.x), ex2(x.y));
+}
+
+// What a token is, a bit each: the first or last of its sequence, outside every sequence.
+enum { kFirst = 1, kLast = 2, kOutside = 4 };
+struct TokenAt {
+    int what, seq;
+};
+__device__ __forceinline__ TokenAt token_at(const Axes& a, int axis, int t, int t1) {
+    if (t >= t1) return TokenAt{kOutside, 0};
+    const Seq s = seq_of(a, axis, t);
+    if (t < s.start || t >= s.end) return TokenAt{kOutside, 0};
+    return TokenAt{(t == s.start ? kFirst : 0) | (t == s.end - 1 ? kLast : 0), s.b};
+}
+
+// The thread's four channels of four states: its place in a warp, and where its values lie.
+template <int NL>
+struct ScanLane {
+    int nl, cl;      // first state / 4; first channel in the CTA
+    __device__ __forceinline__ ScanLane() {
+        const int lane = threadIdx.x & 31;
+        nl = lane % NL;
+        cl = (threadIdx.x >> 5) * ScanTile<NL>::warp_ch + lane / NL * 4;
+    }
+    // of x [D][N] fp32: channel i's states, zeros past the last
+    __device__ __forceinline__ float4 states(const float* x, const ScanDims& d, const ChBlock& b, int i) const {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (cl + i < b.n) {
+            const float* p = x + (size_t)(b.c0 + cl + i) * d.N + 4 * nl;
+            if (4 * nl < d.N) v.x = p[0];
+            if (4 * nl + 1 < d.N) v.y = p[1];
+            if (4 * nl + 2 < d.N) v.z = p[2];
+            if (4 * nl + 3 < d.N) v.w = p[3];
+        }
+        return v;
+    }
+    __device__ __forceinline__ void put_states(float* x, const ScanDims& d, const ChBlock& b, int i, float4 v) const {
+        if (cl + i < b.n) {
+            float* p = x + (size_t)(b.c0 + cl + i) * d.N + 4 * nl;
+            if (4 * nl < d.N) p[0] = v.x;
+            if (4 * nl + 1 < d.N) p[1] = v.y;
+            if (4 * nl + 2 < d.N) p[2] = v.z;
+            if (4 * nl + 3 < d.N) p[3] = v.w;
+        }
+    }
+};
+
+// Sum over a channel's NL lanes of a value for each of the thread's four channels.  Afterwards lane nl < 4 holds
+// the sums of 4 / min(NL, 4) channels from its_channel() on.
+template <int NL>
+__device__ __forceinline__ int its_channel(int nl) { return NL == 1 ? 0 : NL == 2 ? 2 * (nl & 1) : 2 * (nl & 1) + (nl >> 1 & 1); }
+template <int NL>
+__device__ __forceinline__ void sum_states(const float (&v)[4], int nl, float (&out)[NL == 1 ? 4 : NL == 2 ? 2 : 1]) {
+    if constexpr (NL == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = v[i];
+    } else {
+        const bool b0 = nl & 1;
+        float z0 = (b0 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[2], 1);
+        float z1 = (b0 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b0 ? v[1] : v[3], 1);
+        if constexpr (NL == 2) {
+            out[0] = z0;
+            out[1] = z1;
+        } else {
+            const bool b1 = nl & 2;
+            float z = (b1 ? z1 : z0) + __shfl_xor_sync(0xffffffffu, b1 ? z0 : z1, 2);
+            if constexpr (NL >= 8) z += __shfl_xor_sync(0xffffffffu, z, 4);
+            if constexpr (NL >= 16) z += __shfl_xor_sync(0xffffffffu, z, 8);
+            out[0] = z;
+        }
+    }
+}
+// ... and into row[channel in the CTA]
+template <int NL>
+__device__ __forceinline__ void put_sums(float* row, const ScanLane<NL>& l, const float (&v)[4]) {
+    float o[NL == 1 ? 4 : NL == 2 ? 2 : 1];
+    sum_states<NL>(v, l.nl, o);
+    float* p = row + l.cl + its_channel<NL>(l.nl);
+    if constexpr (NL == 1) *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+    else if constexpr (NL == 2) *reinterpret_cast<float2*>(p) = make_float2(o[0], o[1]);
+    else if (l.nl < 4) *p = o[0];
+}
+
+// Tile of B or C: [kTile][states] fp32, zeros past N and outside the sequences
+template <typename T, int NL>
+__device__ __forceinline__ void load_bc(float* to, const T* from, long long token_stride, int N, int t0, const int* what) {
+    constexpr int S = ScanTile<NL>::states;
+    for (int i = threadIdx.x; i < kTile * S; i += kScanThreads) {
+        const int t = i / S, n = i % S;
+        to[i] = n < N && !(what[t] & kOutside) ? (float)from[(t0 + t) * token_stride + n] : 0.f;
+    }
+}
+
+// Lanes along the states for N of them
+inline int state_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+
+constexpr int kScanSms = 152;
+
+// Calls f with an integral_constant: the lanes along the states
+template <typename F>
+cudaError_t by_lanes(int N, F f) {
+    switch (state_lanes(N)) {
+        case 1: return f(std::integral_constant<int, 1>{});
+        case 2: return f(std::integral_constant<int, 2>{});
+        case 4: return f(std::integral_constant<int, 4>{});
+        case 8: return f(std::integral_constant<int, 8>{});
+        default: return f(std::integral_constant<int, 16>{});
+    }
+}
+
+// Whether rows of an array of T can be read four elements at a time
+inline bool wide4(const ScanDims& d, const void* p, const long long (&s)[2]) {
+    const int es = d.bf16 ? 2 : 4;
+    return !p || ((d.D / d.G) % 4 == 0 && aligned_rows(p, s, d.at.rows(), d.at.L, 4 * es, es));
+}
+
+}  // namespace efla

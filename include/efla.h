@@ -321,6 +321,115 @@ efla_status efla_norm_bwd(const efla_norm_shape* shape, const void* x, const voi
                           const float* stats, void* dx, void* dweight, void* dbias,
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- Short causal convolution of every channel by itself (in front of a mixer's q, k, v or of a scan).
+ *     pre_t = bias + sum_{j < W} weight[d][j] x_{t - (W - 1) + j},   y_t = pre_t, or pre_t sigmoid(pre_t) (silu = 1)
+ * x, y, dy, dx [B,L,D] dtype, reached through strides in elements {batch, token}, channels contiguous (slices of a
+ * fused projection are read and written in place); weight [D,W], bias [D] weight_dtype; S0, S_final, dS_final, dS0
+ * dense [B,W-1,D] dtype: the W - 1 tokens in front of a sequence, oldest first (NULL: zeros), and its last W - 1.
+ * packed and offsets as in the gated rule: B sequences on one axis of L tokens, [L,D]; tokens outside every sequence
+ * are not read and their outputs not written.
+ * Alignment: to the elements (rows that lie on 16 bytes, or 8, run faster).  Sums are fp32, added in a fixed order.
+ * W 2 .. 4, D 1 .. 65536, L up to 2^30.  Outputs overlap neither inputs nor each other (dx and dy, x and y may be
+ * slices of one buffer's token rows that do not share elements). */
+typedef struct {
+    int B, L, D, W;
+    efla_dtype dtype;           /* x, y, dy, dx, states */
+    efla_dtype weight_dtype;    /* weight, bias, dweight, dbias */
+    int silu, packed;
+    long long x_stride[2], y_stride[2], dy_stride[2], dx_stride[2];   /* those of arrays the call does not have: zeros */
+} efla_conv_shape;
+
+/* S_final NULL: not written (a sequence shorter than W - 1 keeps S0's latest rows in front of its own). */
+efla_status efla_conv_fwd(const efla_conv_shape* shape, const int* offsets, const void* x, const void* weight,
+                          const void* bias, const void* S0, void* y, void* S_final, cudaStream_t stream);
+
+/* Gradients of  sum(y * dy) + sum(S_final * dS_final).  dS_final NULL: zeros; dbias, dS0 NULL: not written (dbias may
+ * be asked for only where there is a bias).  Without tokens dweight and dbias are zero. */
+size_t efla_conv_bwd_workspace_size(const efla_conv_shape* shape);
+efla_status efla_conv_bwd(const efla_conv_shape* shape, const int* offsets, const void* x, const void* weight,
+                          const void* bias, const void* S0, const void* dy, const void* dS_final, void* dx, void* dweight,
+                          void* dbias, void* dS0, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One new token (L = 1; token strides unused) on a cache of states S [nslots,W-1,D], shifted in place.  slots as in
+ * efla_gated_step: NULL, or B places that differ from each other; a place outside [0, nslots) is skipped (y = 0). */
+efla_status efla_conv_step(const efla_conv_shape* shape, const void* x, const void* weight, const void* bias, void* S,
+                           const int* slots, int nslots, void* y, cudaStream_t stream);
+
+/* ---- Selective scan: a diagonal state space whose step size, input and output vary with the token.
+ * Channel d keeps N states and reads A[d], and the B and C of its group d / (D / G):
+ *     dt = softplus(delta + delta_bias)  (softplus = 1), or delta + delta_bias
+ *     h <- e^{dt A} h + dt u B,   y = (sum_n C h + skip u) z sigmoid(z)
+ * u, delta, z, y (and dy, du, ddelta, dz) [B,L,D] dtype through strides {batch, token}; Bm, C [B,L,G,N] dtype through
+ * strides {batch, token, group}, their last dimension contiguous; A [D,N], skip [D], delta_bias [D] fp32 dense; S0,
+ * S_final, dS_final, dS0 dense [B,D,N] fp32; dB, dC dense [B,L,G,N] dtype; dA, dskip, ddelta_bias fp32 dense.
+ * skip, z, delta_bias NULL: none (y has no gate, no skip).  A token with dt = 0 leaves the state alone.
+ * packed and offsets as in the gated rule ([L,D] and [L,G,N]).  Any N in 1 .. 64, D a multiple of G (1 .. 65536), L up to
+ * 2^30, at most 65535 sequences unless packed.  Alignment: to the elements (states, workspace: 16 bytes).
+ * Arithmetic is fp32; e^x is ex2.approx of x log2(e) (at most 2^-22, on average -2e-8, of the result).  Sums over tokens
+ * and channels are added in a fixed order.  Outputs overlap neither inputs nor each other, but du, ddelta and dz may be
+ * slices of one buffer's token rows. */
+typedef struct {
+    int B, L, D, G, N;
+    efla_dtype dtype;
+    int softplus, packed;
+    long long u_stride[2], delta_stride[2], z_stride[2], y_stride[2], dy_stride[2], du_stride[2], ddelta_stride[2],
+        dz_stride[2];                       /* those of arrays the call does not have: zeros */
+    long long B_stride[3], C_stride[3];
+} efla_scan_shape;
+
+/* S0 NULL: zero states; S_final NULL: not written.  An empty sequence's S_final is its S0.  Workspace: of one call,
+ * 0 bytes where the channels fill the GPU. */
+size_t efla_scan_fwd_workspace_size(const efla_scan_shape* shape);
+efla_status efla_scan_fwd(const efla_scan_shape* shape, const int* offsets, const void* u, const void* delta, const float* A,
+                          const void* Bm, const void* C, const float* skip, const void* z, const float* delta_bias,
+                          const float* S0, void* y, float* S_final, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/* Gradients of  sum(y * dy) + sum(S_final * dS_final).  The states are recomputed; nothing is kept by the forward.
+ * dz goes with z; dskip, ddelta_bias, dS0 NULL: not written (the first two may be asked for only where their input is
+ * there).  Without tokens dA, dskip and ddelta_bias are zero. */
+size_t efla_scan_bwd_workspace_size(const efla_scan_shape* shape);
+efla_status efla_scan_bwd(const efla_scan_shape* shape, const int* offsets, const void* u, const void* delta, const float* A,
+                          const void* Bm, const void* C, const float* skip, const void* z, const float* delta_bias,
+                          const float* S0, const void* dy, const float* dS_final, void* du, void* ddelta, float* dA,
+                          void* dB, void* dC, float* dskip, void* dz, float* ddelta_bias, float* dS0, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* One new token (L = 1; token strides unused) on a cache of states S [nslots,D,N] fp32, updated in place.  slots as in
+ * efla_gated_step. */
+efla_status efla_scan_step(const efla_scan_shape* shape, const void* u, const void* delta, const float* A, const void* Bm,
+                           const void* C, const float* skip, const void* z, const float* delta_bias, float* S,
+                           const int* slots, int nslots, void* y, cudaStream_t stream);
+
+/* ---- RMS norm of a residual stream over the last dimension.
+ *     h = x + residual, rounded to dtype (residual NULL: h is x),   rstd = 1 / sqrt(mean(h^2) + eps),   y = h rstd weight
+ * x, residual, h [rows, D] dtype with row strides (elements); weight [D] weight_dtype; rstd [rows] fp32.
+ * group = 0: y [rows, D] dtype.  group = 128 or D: y is e4m3 (a byte each), y ~ scale q, with one fp32 scale for `group`
+ * columns (the last group of a row may be shorter): scale [rows, ceil(D / group)] dense, the largest |y| / 448, at least
+ * 2^-126 (a row of zeros gives q = 0); rounding is to nearest even, from fp32.
+ * h may be x or residual itself (the same rows: in place); otherwise outputs overlap neither inputs nor each other.
+ * Backward, from h as the forward left it, of  sum(y * dy) + sum(h * dh):  with p = dy weight
+ *     dx = rstd (p - h rstd^2 mean(p h)) + dh   (the gradient of x and of residual alike),   dweight = sum_rows dy h rstd
+ * (y as it is before it is rounded to 8 bits.)  dh NULL: zeros; dx may be dh itself.
+ * Alignment: to the elements, the workspace to 16 bytes.  Any D in 1 .. 16384.  rows = 0: dweight is zero.
+ * Sums are fp32; dweight is added in a fixed order. */
+typedef struct {
+    long long rows;
+    int D, group;
+    long long x_stride, residual_stride, y_stride, h_stride;     /* forward */
+    long long dy_stride, dh_stride, dx_stride;                   /* backward, which also uses h_stride */
+    efla_dtype dtype;
+    efla_dtype weight_dtype;
+    float eps;
+} efla_rms_shape;
+
+efla_status efla_rms_fwd(const efla_rms_shape* shape, const void* x, const void* residual, const void* weight, void* y,
+                         float* scale, void* h, float* rstd, cudaStream_t stream);
+size_t efla_rms_bwd_workspace_size(const efla_rms_shape* shape);
+efla_status efla_rms_bwd(const efla_rms_shape* shape, const void* h, const void* weight, const void* dy, const float* rstd,
+                         const void* dh, void* dx, void* dweight, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+
 /* Synchronises `stream`, then reports any asynchronous launch/kernel error
  * (EFLA_ERR_CUDA) or a device-side status word set by a bounded wait (EFLA_ERR_TIMEOUT),
  * and clears that word.  A library built with -DEFLA_DEBUG (libefla_gb300_debug.so) also
