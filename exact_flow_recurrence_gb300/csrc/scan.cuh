@@ -66,8 +66,31 @@ __device__ __forceinline__ void store4(T* p, float4 x, int n) {
     }
 }
 
-__device__ __forceinline__ float softplus_of(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-__device__ __forceinline__ float step_of(const ScanDims& d, float x) { return d.softplus ? softplus_of(x) : x; }
+// log(1 + e^x) = max(x, 0) + log1p(w), w = e^{-|x|}: log1p(w) / w on [0, 1] as its Chebyshev fit of degree 9 (5e-9 of it),
+// two values an instruction.  A few 2^-24 of the result, however small.
+__device__ __forceinline__ float2 softplus2(float2 x) {
+    const float2 w = make_float2(ex2(-kLog2eF * fabsf(x.x)), ex2(-kLog2eF * fabsf(x.y)));
+    float2 p = both(-0.0032438531052321196f);
+    p = fma2(p, w, both(0.01985068805515766f));
+    p = fma2(p, w, both(-0.05695807933807373f));
+    p = fma2(p, w, both(0.10603507608175278f));
+    p = fma2(p, w, both(-0.15305505692958832f));
+    p = fma2(p, w, both(0.19675908982753754f));
+    p = fma2(p, w, both(-0.2495412826538086f));
+    p = fma2(p, w, both(0.3332996070384979f));
+    p = fma2(p, w, both(-0.4999990165233612f));
+    p = fma2(p, w, both(1.f));
+    return fma2(p, w, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+__device__ __forceinline__ float step_of(const ScanDims& d, float x) { return d.softplus ? softplus2(both(x)).x : x; }
+// dt of four channels from their delta + bias, zeros past the n-th
+__device__ __forceinline__ float4 steps(const ScanDims& d, float4 raw, int n) {
+    if (d.softplus) {
+        const float2 a = softplus2(make_float2(raw.x, raw.y)), b = softplus2(make_float2(raw.z, raw.w));
+        raw = make_float4(a.x, a.y, b.x, b.y);
+    }
+    return make_float4(raw.x, n > 1 ? raw.y : 0.f, n > 2 ? raw.z : 0.f, n > 3 ? raw.w : 0.f);
+}
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 __device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
 __device__ __forceinline__ float at4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -161,16 +184,6 @@ __device__ __forceinline__ void put_sums(float* row, const ScanLane<NL>& l, cons
     else if (l.nl < 4) *p = o[0];
 }
 
-// Tile of B or C: [kTile][states] fp32, zeros past N and outside the sequences
-template <typename T, int NL>
-__device__ __forceinline__ void load_bc(float* to, const T* from, long long token_stride, int N, int t0, const int* what) {
-    constexpr int S = ScanTile<NL>::states;
-    for (int i = threadIdx.x; i < kTile * S; i += kScanThreads) {
-        const int t = i / S, n = i % S;
-        to[i] = n < N && !(what[t] & kOutside) ? (float)from[(t0 + t) * token_stride + n] : 0.f;
-    }
-}
-
 // Lanes along the states for N of them
 inline int state_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
@@ -188,10 +201,15 @@ cudaError_t by_lanes(int N, F f) {
     }
 }
 
-// Whether rows of an array of T can be read four elements at a time
+// Whether rows of channels, or of B and C, can be read four elements at a time
 inline bool wide4(const ScanDims& d, const void* p, const long long (&s)[2]) {
     const int es = d.bf16 ? 2 : 4;
     return !p || ((d.D / d.G) % 4 == 0 && aligned_rows(p, s, d.at.rows(), d.at.L, 4 * es, es));
+}
+inline bool wide4(const ScanDims& d, const void* p, const long long (&s)[3]) {
+    const int es = d.bf16 ? 2 : 4;
+    const long long rows[2] = {s[0], s[1]};
+    return d.N % 4 == 0 && (d.G < 2 || s[2] % 4 == 0) && aligned_rows(p, rows, d.at.rows(), d.at.L, 4 * es, es);
 }
 
 }  // namespace efla

@@ -41,10 +41,6 @@ __device__ __forceinline__ float4 gated(const T* dy, const T* z, int n) {   // d
     return mul4(g, make_float4(silu_of(v.x), silu_of(v.y), silu_of(v.z), silu_of(v.w)));
 }
 
-__device__ __forceinline__ float4 steps(const ScanDims& d, float4 raw, int n) {
-    return make_float4(step_of(d, raw.x), n > 1 ? step_of(d, raw.y) : 0.f, n > 2 ? step_of(d, raw.z) : 0.f, n > 3 ? step_of(d, raw.w) : 0.f);
-}
-
 // The arrays of one axis from a CTA's first channel on
 template <typename T>
 struct Rows {
