@@ -20,34 +20,68 @@ struct Segments {
     int* alive;
 };
 
+constexpr int kCarry = 256, kBring = 256;   // threads that carry states, and that bring tokens
+
 // Named barriers of a CTA: a buffer filled, and a buffer's states done.
-__device__ __forceinline__ void bar_wait(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void bar_wait(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kCarry + kBring) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kCarry + kBring) : "memory"); }
 __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
     if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
 }
 
-// Tiles of TT tokens: two buffers of dt, dt u, y [TT][CH] and B, C [TT][S], and a ring of kRing raw tiles.
+// Tiles of TT tokens.  Two buffers: (dt, dt, dt u, dt u) of two channels [TT][CH / 2], y [TT][CH], and (B, C) of four states as
+// they are stored [TT][NL]; and a ring of kRing raw tiles.
 constexpr int kRing = 4, kWhat = 4;
 template <typename T, int NL, bool PART>
 struct FwdTile {
     static constexpr int CH = ScanTile<NL>::ch, S = ScanTile<NL>::states;
     static constexpr int TT = NL == 1 ? 4 : NL == 2 ? 8 : 16;
-    static constexpr int items = TT * CH / 4 / kScanThreads;                       // a producer's groups of four channels a tile
+    static constexpr int items = (TT * CH / 4 + kBring - 1) / kBring;               // a thread's groups of four channels a tile
     static constexpr int bc = TT * NL * (PART ? 1 : 2);                            // groups of four states of B and C a tile
-    static constexpr int bc_items = (bc + kScanThreads - 1) / kScanThreads;
+    static constexpr int bc_items = (bc + kBring - 1) / kBring;
     static constexpr int arrays = PART ? 2 : 3;
-    static constexpr int buffer = TT * CH * (PART ? 2 : 3) + TT * S * 2;           // floats
-    static constexpr int slot = (items * arrays + bc_items) * kScanThreads;        // Vec<T, 4>
+    static constexpr int y_at = TT * CH * 2, bc_at = y_at + (PART ? 0 : TT * CH);  // floats
+    static constexpr int buffer = bc_at + TT * NL * 8 * (int)sizeof(T) / 4;
+    static constexpr int slot = (items * arrays + bc_items) * kBring;              // Vec<T, 4>
     static constexpr size_t bytes = 2 * buffer * sizeof(float) + kRing * slot * sizeof(Vec<T, 4>);
 };
 
-// Warps 0 .. 3 carry the states; warps 4 .. 7 bring the tokens (asynchronous copies, kRing tiles ahead), work out dt and dt u
-// for them, and finish the y that they left: skip, gate, store.
+// The four B and four C of a token
+template <typename T>
+struct Bc;
+template <>
+struct Bc<float> {
+    float4 b, c;
+    __device__ __forceinline__ void load(const float* p, bool both_) {
+        b = *reinterpret_cast<const float4*>(p);
+        if (both_) c = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ float bn(int n) const { return at4(b, n); }
+    __device__ __forceinline__ float cn(int n) const { return at4(c, n); }
+};
+template <>
+struct Bc<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool both_) {
+        if (both_) {
+            v = *reinterpret_cast<const uint4*>(p);
+        } else {
+            const uint2 h = *reinterpret_cast<const uint2*>(p);
+            v = make_uint4(h.x, h.y, 0u, 0u);
+        }
+    }
+    __device__ static __forceinline__ float one(uint32_t w, int n) { return __uint_as_float(n & 1 ? w & 0xffff0000u : w << 16); }
+    __device__ __forceinline__ float bn(int n) const { return one(n < 2 ? v.x : v.y, n); }
+    __device__ __forceinline__ float cn(int n) const { return one(n < 2 ? v.z : v.w, n); }
+};
+
+// Warps 0 .. 7 carry the states, two neighbouring channels of four states a thread (the two channels in one instruction's
+// halves); the other warps bring the tokens (asynchronous copies, kRing tiles ahead), work out dt and dt u for them, and
+// finish the y that they left: skip, gate, store.
 template <typename T, int NL, bool WIDE, bool PART>
-__global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_fwd(ScanDims d, ScanIn in, T* y, float* S_final, Segments sg) {
+__global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, ScanIn in, T* y, float* S_final, Segments sg) {
     using Tile = FwdTile<T, NL, PART>;
     using V = Vec<T, 4>;
     constexpr int CH = Tile::CH, S = Tile::S, TT = Tile::TT;
@@ -56,9 +90,9 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_fwd(ScanDims d, Sc
     const ChBlock cb = ch_block<NL>(d, blockIdx.y);
     const int axis = blockIdx.z, k = blockIdx.x, ta = k * sg.seg, tb = min(ta + sg.seg, d.at.L);
     const int tiles = (tb - ta + TT - 1) / TT;
-    const auto buffer = [&](int i) { return dyn + (i & 1) * Tile::buffer; };   // dt, dt u, B, C, y
-    if (threadIdx.x >= kScanThreads) {
-        const int tid = threadIdx.x - kScanThreads;
+    const auto buffer = [&](int i) { return dyn + (i & 1) * Tile::buffer; };
+    if (threadIdx.x >= kCarry) {
+        const int tid = threadIdx.x - kCarry;
         const T* u = (const T*)in.u + axis * d.us[0] + cb.c0;
         const T* delta = (const T*)in.delta + axis * d.ds[0] + cb.c0;
         const T* z = in.z ? (const T*)in.z + axis * d.zs[0] + cb.c0 : nullptr;
@@ -67,8 +101,8 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_fwd(ScanDims d, Sc
         if (!PART) y += axis * d.ys[0] + cb.c0;
         V* raw = reinterpret_cast<V*>(dyn + 2 * Tile::buffer) + tid;
         // its channels c .. c + n - 1 (n <= 4), and tokens row, row + rows, .. of a tile
-        constexpr int rows = kScanThreads / (CH / 4 < kScanThreads ? CH / 4 : kScanThreads);
-        const int c = tid % (CH / 4) * 4, row = tid / (CH / 4), n = min(4, cb.n - c);
+        constexpr int rows = kBring / (CH / 4);
+        const int c = tid % (CH / 4) * 4, row = tid / (CH / 4), n = row < TT ? min(4, cb.n - c) : 0;
         const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
         const float4 bias = in.dbias ? load4<float, false>(in.dbias + cb.c0 + c, n) : none;
         const float4 skip = in.skip ? load4<float, false>(in.skip + cb.c0 + c, n) : none;
@@ -90,16 +124,16 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_fwd(ScanDims d, Sc
                     for (int j = 0; j < Tile::items; ++j) {
                         const long long t = t0 + row + j * rows;
                         if (t >= tb) continue;
-                        bring(slot + j * Tile::arrays * kScanThreads, u + t * d.us[1] + c, n);
-                        bring(slot + (j * Tile::arrays + 1) * kScanThreads, delta + t * d.ds[1] + c, n);
-                        if (!PART && z) bring(slot + (j * Tile::arrays + 2) * kScanThreads, z + t * d.zs[1] + c, n);
+                        bring(slot + j * Tile::arrays * kBring, u + t * d.us[1] + c, n);
+                        bring(slot + (j * Tile::arrays + 1) * kBring, delta + t * d.ds[1] + c, n);
+                        if (!PART && z) bring(slot + (j * Tile::arrays + 2) * kBring, z + t * d.zs[1] + c, n);
                     }
 #pragma unroll
                 for (int j = 0; j < Tile::bc_items; ++j) {
-                    const int e = tid + j * kScanThreads, q = e % NL * 4, t = e / NL % TT;
+                    const int e = tid + j * kBring, q = e % NL * 4, t = e / NL % TT;
                     if (e >= Tile::bc || t0 + t >= tb || q >= d.N) continue;
                     const T* from = e < TT * NL ? Bm + (t0 + t) * d.bs[1] + q : C + (t0 + t) * d.cs[1] + q;
-                    bring(slot + (Tile::items * Tile::arrays + j) * kScanThreads, from, min(4, d.N - q));
+                    bring(slot + (Tile::items * Tile::arrays + j) * kBring, from, min(4, d.N - q));
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -123,49 +157,67 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_fwd(ScanDims d, Sc
         };
         const auto fill = [&](int i) {
             const V* slot = raw + (i % kRing) * Tile::slot;
-            float *s_dt = buffer(i), *s_du = s_dt + TT * CH, *s_bc = s_du + TT * CH;
+            float* const s_dd = buffer(i);
+            T* const s_bc = reinterpret_cast<T*>(s_dd + Tile::bc_at);
             const int* w = what[i % kWhat];
+            // (every load before the first store: a store holds back the loads behind it)
+            float4 dt[Tile::items], du[Tile::items];
 #pragma unroll
             for (int j = 0; j < Tile::items; ++j) {
-                const int t = row + j * rows;
-                float4 dt = none, du = none;
-                if (!(w[t] & kOutside) && n > 0) {
-                    dt = steps(d, add4(get(slot + (j * Tile::arrays + 1) * kScanThreads), bias), n);
-                    du = mul4(dt, get(slot + j * Tile::arrays * kScanThreads));
-                }
-                *reinterpret_cast<float4*>(s_dt + t * CH + c) = dt;
-                *reinterpret_cast<float4*>(s_du + t * CH + c) = du;
+                dt[j] = get(slot + (j * Tile::arrays + 1) * kBring);
+                du[j] = get(slot + j * Tile::arrays * kBring);
             }
 #pragma unroll
+            for (int j = 0; j < Tile::items; ++j) {
+                const bool in_range = n > 0 && !(w[row + j * rows] & kOutside);
+                dt[j] = steps(d, add4(dt[j], bias), n);
+                du[j] = in_range ? mul4(dt[j], du[j]) : none;
+                if (!in_range) dt[j] = none;
+            }
+            if (row < TT)
+#pragma unroll
+                for (int j = 0; j < Tile::items; ++j) {
+                    float4* p = reinterpret_cast<float4*>(s_dd + ((row + j * rows) * CH + c) * 2);
+                    p[0] = make_float4(dt[j].x, dt[j].y, du[j].x, du[j].y);
+                    p[1] = make_float4(dt[j].z, dt[j].w, du[j].z, du[j].w);
+                }
+#pragma unroll
             for (int j = 0; j < Tile::bc_items; ++j) {
-                const int e = tid + j * kScanThreads, q = e % NL * 4, t = e / NL % TT;
+                const int e = tid + j * kBring, q = e % NL, t = e / NL % TT;
                 if (e >= Tile::bc) continue;
-                const bool in_range = !(w[t] & kOutside) && q < d.N;
-                *reinterpret_cast<float4*>(s_bc + (e / NL) * S + q) = in_range ? get(slot + (Tile::items * Tile::arrays + j) * kScanThreads) : none;
+                V v;
+                v.zero();
+                if (!(w[t] & kOutside) && 4 * q < d.N) v = slot[(Tile::items * Tile::arrays + j) * kBring];
+                *reinterpret_cast<V*>(s_bc + (t * NL + q) * 8 + (e < TT * NL ? 0 : 4)) = v;
             }
         };
         const auto finish = [&](int i) {
             const V* slot = raw + (i % kRing) * Tile::slot;
-            const float* s_y = buffer(i) + 2 * TT * CH + 2 * TT * S;
+            const float* s_y = buffer(i) + Tile::y_at;
+            if (n <= 0) return;
+            float4 v[Tile::items], uu[Tile::items], g[Tile::items];
+            bool in_range[Tile::items];
 #pragma unroll
             for (int j = 0; j < Tile::items; ++j) {
-                const int t = row + j * rows;
-                if ((what[i % kWhat][t] & kOutside) || n <= 0) continue;
-                const long long tt = ta + i * TT + t;
-                float4 v = *reinterpret_cast<const float4*>(s_y + t * CH + c);
-                const float4 uu = get(slot + j * Tile::arrays * kScanThreads);
-                v = make_float4(fmaf(skip.x, uu.x, v.x), fmaf(skip.y, uu.y, v.y), fmaf(skip.z, uu.z, v.z), fmaf(skip.w, uu.w, v.w));
-                if (z) {
-                    const float4 g = get(slot + (j * Tile::arrays + 2) * kScanThreads);
-                    v = mul4(v, make_float4(silu_of(g.x), silu_of(g.y), silu_of(g.z), silu_of(g.w)));
-                }
-                store4<T, WIDE>(y + tt * d.ys[1] + c, v, n);
+                in_range[j] = !(what[i % kWhat][row + j * rows] & kOutside);
+                v[j] = *reinterpret_cast<const float4*>(s_y + (row + j * rows) * CH + c);
+                uu[j] = get(slot + j * Tile::arrays * kBring);
+                if (z) g[j] = get(slot + (j * Tile::arrays + 2) * kBring);
             }
+#pragma unroll
+            for (int j = 0; j < Tile::items; ++j) {
+                v[j] = make_float4(fmaf(skip.x, uu[j].x, v[j].x), fmaf(skip.y, uu[j].y, v[j].y), fmaf(skip.z, uu[j].z, v[j].z),
+                                   fmaf(skip.w, uu[j].w, v[j].w));
+                if (z) v[j] = mul4(v[j], make_float4(silu_of(g[j].x), silu_of(g[j].y), silu_of(g[j].z), silu_of(g[j].w)));
+            }
+#pragma unroll
+            for (int j = 0; j < Tile::items; ++j)
+                if (in_range[j]) store4<T, WIDE>(y + (long long)(ta + i * TT + row + j * rows) * d.ys[1] + c, v[j], n);
         };
         for (int i = 0; i < kRing; ++i) issue(i);
         look(0);
         look(1);
-        asm volatile("bar.sync 5, 128;" ::: "memory");
+        asm volatile("bar.sync 5, %0;" ::"n"(kBring) : "memory");
         for (int i = 0; i < tiles; ++i) {
             // tile i is group i, and i + 2 is the last one under way (a thread reads only what it copied itself)
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
@@ -182,72 +234,122 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_fwd(ScanDims d, Sc
         if (!PART) finish(tiles - 1);
         return;
     }
-    const ScanLane<NL> l;
-    float2 a2[4][2], h[4][2];
+    // channels cl and cl + 1, states 4 nl .. 4 nl + 3 of the padded ones
+    const int lane = threadIdx.x & 31;
+    ScanLane<NL> l;
+    l.nl = lane % NL;
+    l.cl = (threadIdx.x >> 5) * (64 / NL) + lane / NL * 2;
+    float2 a2[4], h[4];
+    const auto two = [](const float4& x, const float4& y, float2 (&to)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = l.states(in.A, d, cb, i);
-        a2[i][0] = make_float2(v.x * kLog2eF, v.y * kLog2eF);
-        a2[i][1] = make_float2(v.z * kLog2eF, v.w * kLog2eF);
-        h[i][0] = h[i][1] = make_float2(0.f, 0.f);
+        for (int n = 0; n < 4; ++n) to[n] = make_float2(at4(x, n), at4(y, n));
+    };
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto set_states = [&](const float* S0, size_t at) {
+        if (S0) two(l.states(S0 + at, d, cb, 0), l.states(S0 + at, d, cb, 1), h);
+        else two(none, none, h);
+    };
+    const auto put_states = [&](float* to) {
+        l.put_states(to, d, cb, 0, make_float4(h[0].x, h[1].x, h[2].x, h[3].x));
+        l.put_states(to, d, cb, 1, make_float4(h[0].y, h[1].y, h[2].y, h[3].y));
+    };
+    two(l.states(in.A, d, cb, 0), l.states(in.A, d, cb, 1), a2);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        a2[n] = mul2(a2[n], both(kLog2eF));
+        h[n] = make_float2(0.f, 0.f);
     }
     if (!PART)   // the state that this segment starts from
         for (int j = 0; j < k; ++j) {
-            const size_t at = (size_t)axis * sg.count + j;
-            const bool alive = sg.alive[at];
+            const size_t at = (size_t)axis * sg.count + j, ch = at * d.D + cb.c0 + l.cl;
+            const bool alive = sg.alive[at], in0 = l.cl < cb.n, in1 = l.cl + 1 < cb.n;
+            float2 e[4];
+            two(in0 ? *reinterpret_cast<const float4*>(sg.ends + ch * S + 4 * l.nl) : none,
+                in1 ? *reinterpret_cast<const float4*>(sg.ends + (ch + 1) * S + 4 * l.nl) : none, e);
+            const float2 sum = make_float2(in0 ? sg.dts[ch] : 0.f, in1 ? sg.dts[ch + 1] : 0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (l.cl + i >= cb.n) continue;
-                const float4 e = *reinterpret_cast<const float4*>(sg.ends + (at * d.D + cb.c0 + l.cl + i) * S + 4 * l.nl);
-                const float2 sum = both(sg.dts[at * d.D + cb.c0 + l.cl + i]);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float2 x = mul2(a2[i][p], sum), f = p ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
-                    h[i][p] = alive ? fma2(make_float2(ex2(x.x), ex2(x.y)), h[i][p], f) : f;
-                }
+            for (int n = 0; n < 4; ++n) {
+                const float2 x = mul2(a2[n], sum);
+                h[n] = alive ? fma2(make_float2(ex2(x.x), ex2(x.y)), h[n], e[n]) : e[n];
             }
         }
     // empty sequences hand their states on
-    if (!PART && S_final && d.at.packed && k == 0)
+    if (!PART && S_final && d.at.packed && k == 0) {
+        float2 keep[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) keep[n] = h[n];
         for (int b = 0; b < d.at.B; ++b) {
             const Seq s = seq_at(d.at, b);
             if (s.end > s.start) continue;
             const size_t at = (size_t)b * d.D * d.N;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                l.put_states(S_final + at, d, cb, i, in.S0 ? l.states(in.S0 + at, d, cb, i) : make_float4(0.f, 0.f, 0.f, 0.f));
+            set_states(in.S0, at);
+            put_states(S_final + at);
         }
-    float4 dts = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) h[n] = keep[n];
+    }
+    float2 dts = make_float2(0.f, 0.f);
     bool alive = true;
     for (int i = 0; i < tiles; ++i) {
-        float* const s_dt = buffer(i);
-        const float *s_du = s_dt + TT * CH, *s_b = s_du + TT * CH, *s_c = s_b + TT * S;
-        float* const s_y = s_dt + 2 * TT * CH + 2 * TT * S;
+        const float* const s_dd = buffer(i) + l.cl * 2;
+        const T* const s_bc = reinterpret_cast<const T*>(buffer(i) + Tile::bc_at) + l.nl * 8;
+        float* const s_y = buffer(i) + Tile::y_at;
         bar_wait(1 + (i & 1));
-        const auto token = [&](int t) {
-            const float4 dt = *reinterpret_cast<const float4*>(s_dt + t * CH + l.cl), du = *reinterpret_cast<const float4*>(s_du + t * CH + l.cl);
-            const float4 b = *reinterpret_cast<const float4*>(s_b + t * S + 4 * l.nl);
-            float4 c = b;
-            if (!PART) c = *reinterpret_cast<const float4*>(s_c + t * S + 4 * l.nl);
-            float out[4];
+        // what KT tokens read, and the tokens: a store holds back the loads behind it, so that the next tokens' are loaded before
+        const auto load = [&](int t, auto& dd, auto& bc, auto kt) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 dt2 = both(at4(dt, j)), du2 = both(at4(du, j));
-                float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float2 bp = p ? make_float2(b.z, b.w) : make_float2(b.x, b.y), cp = p ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
-                    h[j][p] = fma2(decay2(dt2, a2[j][p]), h[j][p], mul2(du2, bp));
-                    if (!PART) acc = p ? fma2(cp, h[j][p], acc) : mul2(cp, h[j][p]);
-                }
-                out[j] = acc.x + acc.y;
+            for (int e = 0; e < decltype(kt)::value; ++e) {
+                dd[e] = *reinterpret_cast<const float4*>(s_dd + (t + e) * CH * 2);
+                bc[e].load(s_bc + (t + e) * NL * 8, !PART);
             }
-            if (PART) dts = add4(dts, dt);
-            else put_sums<NL>(s_y + t * CH, l, out);
+        };
+        const auto tokens = [&](int t, const auto& dd, const auto& bc, auto kt) {
+            constexpr int KT = decltype(kt)::value;
+            float2 out[KT];
+#pragma unroll
+            for (int e = 0; e < KT; ++e) {
+                const float2 dt = make_float2(dd[e].x, dd[e].y), du = make_float2(dd[e].z, dd[e].w);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    h[n] = fma2(decay2(dt, a2[n]), h[n], mul2(du, both(bc[e].bn(n))));
+                    if (!PART) out[e] = n ? fma2(both(bc[e].cn(n)), h[n], out[e]) : mul2(both(bc[e].cn(n)), h[n]);
+                }
+                if (PART) dts = add2(dts, dt);
+            }
+            if constexpr (PART) {
+            } else if constexpr (KT == 4 && NL >= 4) {   // lane nl < 4 gets the sums of token t + nl
+                const bool b0 = l.nl & 1, b1 = l.nl & 2;
+                float2 z[2];
+                const auto add_other = [](float2 keep, float2 give, int mask) {
+                    return make_float2(keep.x + __shfl_xor_sync(0xffffffffu, give.x, mask), keep.y + __shfl_xor_sync(0xffffffffu, give.y, mask));
+                };
+#pragma unroll
+                for (int e = 0; e < 2; ++e) z[e] = add_other(b1 ? out[e + 2] : out[e], b1 ? out[e] : out[e + 2], 2);
+                float2 s = add_other(b0 ? z[1] : z[0], b0 ? z[0] : z[1], 1);
+                if constexpr (NL >= 8) s = add_other(s, s, 4);
+                if constexpr (NL >= 16) s = add_other(s, s, 8);
+                if (NL == 4 || l.nl < 4) *reinterpret_cast<float2*>(s_y + (t + (l.nl & 3)) * CH + l.cl) = s;
+            } else {
+#pragma unroll
+                for (int e = 0; e < KT; ++e) {
+                    float2 s = out[e];
+#pragma unroll
+                    for (int o = 1; o < NL; o <<= 1)
+                        s = make_float2(s.x + __shfl_xor_sync(0xffffffffu, s.x, o), s.y + __shfl_xor_sync(0xffffffffu, s.y, o));
+                    if (l.nl == 0) *reinterpret_cast<float2*>(s_y + (t + e) * CH + l.cl) = s;
+                }
+            }
         };
         if (!any[i % kWhat]) {
-#pragma unroll 4
-            for (int t = 0; t < TT; ++t) token(t);
+            constexpr std::integral_constant<int, 4> four{};
+            float4 dd[2][4];
+            Bc<T> bc[2][4];
+            load(0, dd[0], bc[0], four);
+#pragma unroll
+            for (int t = 0; t < TT; t += 4) {
+                if (t + 4 < TT) load(t + 4, dd[(t / 4 + 1) & 1], bc[(t / 4 + 1) & 1], four);
+                tokens(t, dd[t / 4 & 1], bc[t / 4 & 1], four);
+            }
         } else {
 #pragma unroll 1
             for (int t = 0; t < TT; ++t) {
@@ -255,31 +357,28 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_fwd(ScanDims d, Sc
                 const size_t at = (size_t)seq[i % kWhat][t] * d.D * d.N;
                 if (w & kFirst) {
                     alive = false;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 v = in.S0 ? l.states(in.S0 + at, d, cb, j) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        h[j][0] = make_float2(v.x, v.y);
-                        h[j][1] = make_float2(v.z, v.w);
-                    }
+                    set_states(in.S0, at);
                 }
-                token(t);
-                if (!PART && S_final && (w & kLast))
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        l.put_states(S_final + at, d, cb, j, make_float4(h[j][0].x, h[j][0].y, h[j][1].x, h[j][1].y));
+                constexpr std::integral_constant<int, 1> one{};
+                float4 dd[1];
+                Bc<T> bc[1];
+                load(t, dd, bc, one);
+                tokens(t, dd, bc, one);
+                if (!PART && S_final && (w & kLast)) put_states(S_final + at);
             }
         }
         bar_arrive(3 + (i & 1));
     }
     if (PART) {
-        const size_t at = (size_t)axis * sg.count + k;
+        const size_t at = (size_t)axis * sg.count + k, ch = at * d.D + cb.c0 + l.cl;
         if (threadIdx.x == 0 && blockIdx.y == 0) sg.alive[at] = alive;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (l.cl + i >= cb.n) continue;
-            const size_t ch = at * d.D + cb.c0 + l.cl + i;
-            *reinterpret_cast<float4*>(sg.ends + ch * S + 4 * l.nl) = make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
-            if (l.nl == 0) sg.dts[ch] = at4(dts, i);
+        if (l.cl < cb.n) {
+            *reinterpret_cast<float4*>(sg.ends + ch * S + 4 * l.nl) = make_float4(h[0].x, h[1].x, h[2].x, h[3].x);
+            if (l.nl == 0) sg.dts[ch] = dts.x;
+        }
+        if (l.cl + 1 < cb.n) {
+            *reinterpret_cast<float4*>(sg.ends + (ch + 1) * S + 4 * l.nl) = make_float4(h[0].y, h[1].y, h[2].y, h[3].y);
+            if (l.nl == 0) sg.dts[ch + 1] = dts.y;
         }
     }
 }
@@ -324,11 +423,11 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, void* y, float* S_final, vo
     if (sg.count > 1) {
         e = cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Part::bytes);
         if (e != cudaSuccess) return e;
-        part<<<dim3(sg.count - 1, grid.y, grid.z), 2 * kScanThreads, Part::bytes, st>>>(d, in, nullptr, nullptr, sg);
+        part<<<dim3(sg.count - 1, grid.y, grid.z), kCarry + kBring, Part::bytes, st>>>(d, in, nullptr, nullptr, sg);
         prof_mark("scan_part", st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    whole<<<grid, 2 * kScanThreads, Whole::bytes, st>>>(d, in, (T*)y, S_final, sg);
+    whole<<<grid, kCarry + kBring, Whole::bytes, st>>>(d, in, (T*)y, S_final, sg);
     prof_mark("scan_fwd", st);
     return cudaGetLastError();
 }
