@@ -5,8 +5,8 @@
 //
 // A thread owns four neighbouring channels and four neighbouring states of each: N/4 lanes (rounded up to a
 // power of two, NL) lie side by side along the states, the warp's other lanes along the channels.  Four warps
-// make a CTA: channels of one group, all on the same tokens.  Tiles of kTile tokens pass through shared memory:
-// what depends on a channel alone (dt, dt u, the gated gradient) is worked out once there.
+// make a CTA: channels of one group, all on the same tokens, which pass through shared memory in tiles:
+// what depends on a channel alone (dt, the gated gradient) is worked out once there.
 // Tokens outside every sequence, and channels and states past the last, are zeros: e^0 h + 0 leaves a state alone.
 #pragma once
 
@@ -14,7 +14,6 @@
 
 namespace efla {
 
-constexpr int kTile = 16;        // tokens a tile
 constexpr int kScanThreads = 128;
 
 // NL: lanes along the states
@@ -183,6 +182,35 @@ __device__ __forceinline__ void put_sums(float* row, const ScanLane<NL>& l, cons
     else if constexpr (NL == 2) *reinterpret_cast<float2*>(p) = make_float2(o[0], o[1]);
     else if (l.nl < 4) *p = o[0];
 }
+
+// The four B and four C of a token
+template <typename T>
+struct Bc;
+template <>
+struct Bc<float> {
+    float4 b, c;
+    __device__ __forceinline__ void load(const float* p, bool both_) {
+        b = *reinterpret_cast<const float4*>(p);
+        if (both_) c = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ float bn(int n) const { return at4(b, n); }
+    __device__ __forceinline__ float cn(int n) const { return at4(c, n); }
+};
+template <>
+struct Bc<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool both_) {
+        if (both_) {
+            v = *reinterpret_cast<const uint4*>(p);
+        } else {
+            const uint2 h = *reinterpret_cast<const uint2*>(p);
+            v = make_uint4(h.x, h.y, 0u, 0u);
+        }
+    }
+    __device__ static __forceinline__ float one(uint32_t w, int n) { return __uint_as_float(n & 1 ? w & 0xffff0000u : w << 16); }
+    __device__ __forceinline__ float bn(int n) const { return one(n < 2 ? v.x : v.y, n); }
+    __device__ __forceinline__ float cn(int n) const { return one(n < 2 ? v.z : v.w, n); }
+};
 
 // Lanes along the states for N of them
 inline int state_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }

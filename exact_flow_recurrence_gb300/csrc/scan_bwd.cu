@@ -3,8 +3,8 @@
 // With g_t = dy_t z sigmoid(z), a_t = e^{dt_t A} and p_t the gradient of the state behind token t:
 //   p_t = C_t g_t + a_{t+1} p_{t+1},   dC_t = sum_d h_t g_t,   dB_t = sum_d p_t dt_t u_t
 //   s1 = sum_n p_t B_t,   e_t = a_t p_t h_{t-1},   du = dt s1 + skip g,   d(dt) = sum_n A e_t + u s1,   dA = sum_t dt e_t
-// The tokens are cut into chunks of kChunk.  Both recurrences are linear, so one launch takes every chunk from a
-// zero state to its last token and, with the running product of its decays, its gradients back to its first:
+// The tokens are cut into chunks (32 tokens from 9 states on).  Both recurrences are linear, so one launch takes every chunk
+// from a zero state to its last token and, with the running product of its decays, its gradients back to its first:
 // all chunks at once.  A second launch chains the chunks' maps, and the third has every chunk's entering state and
 // gradient at hand: it walks the chunk forward to the state in front of every kSub tokens (shared memory),
 // then back, kSub tokens' states in registers.  Sums over channels (dB, dC) and tokens (dA, dskip, dbias) are
@@ -16,8 +16,11 @@ namespace efla {
 
 namespace {
 
-constexpr int kChunk = 64, kSub = 8;
+constexpr int kSub = 4;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Tokens a chunk: dt, u and the gated gradient of a CTA's channels take 48 KB at most
+constexpr int chunk_of(int lanes) { return lanes >= 4 ? 32 : lanes == 2 ? 16 : 8; }
 
 // ends, grads [axis][chunk][D][states]: the chunk's last state from a zero one, and its gradient in front of its first
 // token; after the chain: the state that it starts from, and the gradient that reaches its last token from behind.
@@ -33,14 +36,6 @@ struct ScanWs {
 // floats a CTA row of `ch`: whole float4
 __host__ __device__ inline size_t ch_stride(const ScanDims& d, int S) { return ((size_t)d.D * (S + 2) + 3) / 4 * 4; }
 
-template <typename T, bool WIDE>
-__device__ __forceinline__ float4 gated(const T* dy, const T* z, int n) {   // dy z sigmoid(z)
-    const float4 g = load4<T, WIDE>(dy, n);
-    if (!z) return g;
-    const float4 v = load4<T, WIDE>(z, n);
-    return mul4(g, make_float4(silu_of(v.x), silu_of(v.y), silu_of(v.z), silu_of(v.w)));
-}
-
 // The arrays of one axis from a CTA's first channel on
 template <typename T>
 struct Rows {
@@ -55,32 +50,81 @@ struct Rows {
     }
 };
 
-// dt, dt u and g of TT tokens from t0 on
-template <typename T, bool WIDE, int CH, int TT, bool GRAD>
-__device__ __forceinline__ void load_tile(const ScanDims& d, const ScanIn& in, const Rows<T>& r, const ChBlock& cb, int t0, const int* what,
-                                          float* s_dt, float* s_du, float* s_g) {
-    for (int i = threadIdx.x; i < TT * CH / 4; i += kScanThreads) {
-        const int t = i / (CH / 4), c = i % (CH / 4) * 4, n = min(4, cb.n - c);
-        float4 dt = make_float4(0.f, 0.f, 0.f, 0.f), du = dt, g = dt;
-        if (!(what[t] & kOutside) && n > 0) {
-            const long long tt = t0 + t;
-            const float4 raw = load4<T, WIDE>(r.delta + tt * d.ds[1] + c, n);
-            dt = steps(d, in.dbias ? add4(raw, load4<float, false>(in.dbias + cb.c0 + c, n)) : raw, n);
-            du = mul4(dt, load4<T, WIDE>(r.u + tt * d.us[1] + c, n));
-            if (GRAD) g = gated<T, WIDE>(r.dy + tt * d.dys[1] + c, r.z ? r.z + tt * d.zs[1] + c : nullptr, n);
+// A chunk in shared memory: dt, u, g [tokens][CH] fp32 (g = dy z sigmoid(z)), B and C as they are stored [tokens][NL][4 and 4],
+// and what its tokens are.
+template <typename T, int NL>
+struct Chunk {
+    static constexpr int CH = ScanTile<NL>::ch, S = ScanTile<NL>::states, C = chunk_of(NL);
+    static constexpr int floats = 3 * C * CH + C * NL * 8 * (int)sizeof(T) / 4;
+    float *dt, *u, *g;
+    T* bc;
+    int *what, *seq;    // [C]
+    __device__ __forceinline__ Chunk(float* base, int* flags)
+        : dt(base), u(base + C * CH), g(base + 2 * C * CH), bc(reinterpret_cast<T*>(base + 3 * C * CH)), what(flags), seq(flags + C) {}
+    // tokens ta .. tb-1 (every thread of the CTA; ends with a barrier)
+    template <bool WIDE>
+    __device__ __forceinline__ void load(const ScanDims& d, const Rows<T>& r, const ChBlock& cb, int axis, int ta, int tb, float4 bias) const {
+        constexpr int V = CH / 4, rows = kScanThreads / V, items = C / rows, batch = items < 4 ? items : 4;
+        const int tid = threadIdx.x, c = tid % V * 4, row = tid / V, n = min(4, cb.n - c);
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncthreads();   // (the last readers of what was here)
+        if (tid < C) {
+            const TokenAt a = token_at(d.at, axis, ta + tid, tb);
+            what[tid] = a.what;
+            seq[tid] = a.seq;
         }
-        *reinterpret_cast<float4*>(s_dt + t * CH + c) = dt;
-        *reinterpret_cast<float4*>(s_du + t * CH + c) = du;
-        if (GRAD) *reinterpret_cast<float4*>(s_g + t * CH + c) = g;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < C * NL * 2 / kScanThreads + (C * NL * 2 % kScanThreads ? 1 : 0); ++j) {
+            const int e = tid + j * kScanThreads, q = e % NL, t = e / NL % C;
+            const bool isC = e >= C * NL;
+            if (e < 2 * C * NL) {
+                Vec<T, 4> v;
+                v.zero();
+                if (!(what[t] & kOutside) && 4 * q < d.N) {
+                    const T* from = (isC ? r.C + (ta + t) * d.cs[1] : r.Bm + (ta + t) * d.bs[1]) + 4 * q;
+                    if (WIDE) {
+                        v.load(from);
+                    } else {
+                        const float4 x = load4<T, false>(from, min(4, d.N - 4 * q));
+                        const float f[4] = {x.x, x.y, x.z, x.w};
+                        v.set(f);
+                    }
+                }
+                *reinterpret_cast<Vec<T, 4>*>(bc + (t * NL + q) * 8 + (isC ? 4 : 0)) = v;
+            }
+        }
+#pragma unroll 1
+        for (int j0 = 0; j0 < items; j0 += batch) {
+            float4 xd[batch], xu[batch], xg[batch], xz[batch];   // (every load before the first store: a store holds back the loads behind it)
+            bool in_range[batch];
+#pragma unroll
+            for (int j = 0; j < batch; ++j) {
+                const int t = row + (j0 + j) * rows;
+                const long long tt = ta + t;
+                in_range[j] = n > 0 && !(what[t] & kOutside);
+                xd[j] = in_range[j] ? load4<T, WIDE>(r.delta + tt * d.ds[1] + c, n) : none;
+                xu[j] = in_range[j] ? load4<T, WIDE>(r.u + tt * d.us[1] + c, n) : none;
+                xg[j] = in_range[j] ? load4<T, WIDE>(r.dy + tt * d.dys[1] + c, n) : none;
+                if (r.z) xz[j] = in_range[j] ? load4<T, WIDE>(r.z + tt * d.zs[1] + c, n) : none;
+            }
+#pragma unroll
+            for (int j = 0; j < batch; ++j) {
+                xd[j] = steps(d, add4(xd[j], bias), n);
+                if (!in_range[j]) xd[j] = none;
+                if (r.z) xg[j] = mul4(xg[j], make_float4(silu_of(xz[j].x), silu_of(xz[j].y), silu_of(xz[j].z), silu_of(xz[j].w)));
+            }
+#pragma unroll
+            for (int j = 0; j < batch; ++j) {
+                const int o = (row + (j0 + j) * rows) * CH + c;
+                *reinterpret_cast<float4*>(dt + o) = xd[j];
+                *reinterpret_cast<float4*>(u + o) = xu[j];
+                *reinterpret_cast<float4*>(g + o) = xg[j];
+            }
+        }
+        __syncthreads();
     }
-}
-template <typename T, int S, int TT>
-__device__ __forceinline__ void load_rows(float* to, const T* from, long long stride, int N, int t0, const int* what) {
-    for (int i = threadIdx.x; i < TT * S; i += kScanThreads) {
-        const int t = i / S, n = i % S;
-        to[i] = n < N && !(what[t] & kOutside) ? (float)from[(t0 + t) * stride + n] : 0.f;
-    }
-}
+};
 
 __device__ __forceinline__ float2 lo(const float4& v) { return make_float2(v.x, v.y); }
 __device__ __forceinline__ float2 hi(const float4& v) { return make_float2(v.z, v.w); }
@@ -88,78 +132,77 @@ __device__ __forceinline__ float2 hi(const float4& v) { return make_float2(v.z, 
 // ------------------------------------------------------------------- every chunk by itself
 template <typename T, int NL, bool WIDE>
 __global__ void __launch_bounds__(kScanThreads) k_scan_local(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
-    using Tile = ScanTile<NL>;
-    constexpr int CH = Tile::ch, S = Tile::states;
+    using Ck = Chunk<T, NL>;
+    constexpr int CH = Ck::CH, S = Ck::S, C = Ck::C;
     extern __shared__ __align__(16) float dyn[];
-    float *s_dt = dyn, *s_du = s_dt + kTile * CH, *s_g = s_du + kTile * CH, *s_b = s_g + kTile * CH, *s_c = s_b + kTile * S;
-    __shared__ int what[kTile], seq[kTile];
+    __shared__ int flags[2 * C];
+    const Ck ck(dyn, flags);
     const ChBlock cb = ch_block<NL>(d, blockIdx.y);
-    const int axis = blockIdx.z, k = blockIdx.x, ta = k * kChunk, tb = min(ta + kChunk, d.at.L);
+    const int axis = blockIdx.z, k = blockIdx.x, ta = k * C, tb = min(ta + C, d.at.L);
     const ScanLane<NL> l;
     const Rows<T> r(d, in, gr.dy, axis, cb);
-    float2 a2[4][2], h[4][2], cp[4][2], q[4][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = l.states(in.A, d, cb, i);
-        a2[i][0] = mul2(lo(v), both(kLog2eF));
-        a2[i][1] = mul2(hi(v), both(kLog2eF));
-        h[i][0] = h[i][1] = q[i][0] = q[i][1] = make_float2(0.f, 0.f);
-        cp[i][0] = cp[i][1] = make_float2(1.f, 1.f);
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    {
+        const int c = threadIdx.x % (CH / 4) * 4;
+        ck.template load<WIDE>(d, r, cb, axis, ta, tb, in.dbias ? load4<float, false>(in.dbias + cb.c0 + c, min(4, cb.n - c)) : none);
     }
-    float4 dts = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool alive = true, open = true;   // whether the state before the chunk, and gradients back to it, still pass
-    for (int t0 = ta; t0 < tb; t0 += kTile) {
-        __syncthreads();
-        if (threadIdx.x < kTile) {
-            const TokenAt a = token_at(d.at, axis, t0 + threadIdx.x, tb);
-            what[threadIdx.x] = a.what;
-            seq[threadIdx.x] = a.seq;
+    // pairs of channels (2 i, 2 i + 1), states 4 nl + n
+    float2 a2[2][4], h[2][4], cp[2][4], q[2][4];
+    const auto two = [](const float4& x, const float4& y, float2 (&to)[4]) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) to[n] = make_float2(at4(x, n), at4(y, n));
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        two(l.states(in.A, d, cb, 2 * i), l.states(in.A, d, cb, 2 * i + 1), a2[i]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            a2[i][n] = mul2(a2[i][n], both(kLog2eF));
+            h[i][n] = q[i][n] = make_float2(0.f, 0.f);
+            cp[i][n] = both(1.f);
         }
-        __syncthreads();
-        if (t0 == ta && (what[0] & kOutside)) open = false;
-        load_rows<T, S, kTile>(s_b, r.Bm, d.bs[1], d.N, t0, what);
-        load_rows<T, S, kTile>(s_c, r.C, d.cs[1], d.N, t0, what);
-        load_tile<T, WIDE, CH, kTile, true>(d, in, r, cb, t0, what, s_dt, s_du, s_g);
-        __syncthreads();
-        for (int t = 0; t < kTile; ++t) {
-            const int w = what[t];
-            const size_t at = (size_t)seq[t] * d.D * d.N;
-            if (w & kFirst) {
-                alive = false;
+    }
+    float4 dts = none;
+    // whether the state before the chunk, and gradients back to it, still pass
+    bool alive = true, open = !(ck.what[0] & kOutside);
+#pragma unroll 2
+    for (int t = 0; t < tb - ta; ++t) {
+        const int w = ck.what[t];
+        const size_t at = (size_t)ck.seq[t] * d.D * d.N;
+        if (w & kFirst) {
+            alive = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 v = in.S0 ? l.states(in.S0 + at, d, cb, i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    h[i][0] = lo(v);
-                    h[i][1] = hi(v);
+            for (int i = 0; i < 2; ++i)
+                two(in.S0 ? l.states(in.S0 + at, d, cb, 2 * i) : none, in.S0 ? l.states(in.S0 + at, d, cb, 2 * i + 1) : none, h[i]);
+        }
+        const float4 dt = *reinterpret_cast<const float4*>(ck.dt + t * CH + l.cl), u = *reinterpret_cast<const float4*>(ck.u + t * CH + l.cl),
+                     g = *reinterpret_cast<const float4*>(ck.g + t * CH + l.cl);
+        Bc<T> bc;
+        bc.load(ck.bc + (t * NL + l.nl) * 8, true);
+        dts = add4(dts, dt);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 dt2 = i ? hi(dt) : lo(dt), du2 = mul2(dt2, i ? hi(u) : lo(u)), g2 = i ? hi(g) : lo(g);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 a = decay2(dt2, a2[i][n]);
+                h[i][n] = fma2(a, h[i][n], mul2(du2, both(bc.bn(n))));
+                if (open) {
+                    cp[i][n] = mul2(cp[i][n], a);
+                    q[i][n] = fma2(cp[i][n], mul2(g2, both(bc.cn(n))), q[i][n]);
                 }
             }
-            const float4 dt = *reinterpret_cast<const float4*>(s_dt + t * CH + l.cl), du = *reinterpret_cast<const float4*>(s_du + t * CH + l.cl),
-                         g = *reinterpret_cast<const float4*>(s_g + t * CH + l.cl), b = *reinterpret_cast<const float4*>(s_b + t * S + 4 * l.nl),
-                         c = *reinterpret_cast<const float4*>(s_c + t * S + 4 * l.nl);
-            dts = add4(dts, dt);
+        }
+        if (open && (w & kLast)) {
+            open = false;
+            if (gr.dS)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 dt2 = both(at4(dt, i)), du2 = both(at4(du, i)), g2 = both(at4(g, i));
+                for (int i = 0; i < 2; ++i) {
+                    float2 f[4];
+                    two(l.states(gr.dS + at, d, cb, 2 * i), l.states(gr.dS + at, d, cb, 2 * i + 1), f);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float2 a = decay2(dt2, a2[i][p]);
-                    h[i][p] = fma2(a, h[i][p], mul2(du2, p ? hi(b) : lo(b)));
-                    if (open) {
-                        cp[i][p] = mul2(cp[i][p], a);
-                        q[i][p] = fma2(cp[i][p], mul2(g2, p ? hi(c) : lo(c)), q[i][p]);
-                    }
+                    for (int n = 0; n < 4; ++n) q[i][n] = fma2(cp[i][n], f[n], q[i][n]);
                 }
-            }
-            if (open && (w & kLast)) {
-                open = false;
-                if (gr.dS)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = l.states(gr.dS + at, d, cb, i);
-                        q[i][0] = fma2(cp[i][0], lo(v), q[i][0]);
-                        q[i][1] = fma2(cp[i][1], hi(v), q[i][1]);
-                    }
-            }
         }
     }
     const size_t at = (size_t)axis * ws.chunks + k;
@@ -171,8 +214,10 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_local(ScanDims d, ScanIn 
     for (int i = 0; i < 4; ++i) {
         if (l.cl + i >= cb.n) continue;
         const size_t ch = at * d.D + cb.c0 + l.cl + i;
-        *reinterpret_cast<float4*>(ws.ends + ch * S + 4 * l.nl) = make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
-        *reinterpret_cast<float4*>(ws.grads + ch * S + 4 * l.nl) = make_float4(q[i][0].x, q[i][0].y, q[i][1].x, q[i][1].y);
+        const float2 *hh = h[i / 2], *qq = q[i / 2];
+        const auto one = [&](const float2& v) { return i & 1 ? v.y : v.x; };
+        *reinterpret_cast<float4*>(ws.ends + ch * S + 4 * l.nl) = make_float4(one(hh[0]), one(hh[1]), one(hh[2]), one(hh[3]));
+        *reinterpret_cast<float4*>(ws.grads + ch * S + 4 * l.nl) = make_float4(one(qq[0]), one(qq[1]), one(qq[2]), one(qq[3]));
         if (l.nl == 0) ws.dts[ch] = at4(dts, i);
     }
 }
@@ -249,38 +294,53 @@ struct ChannelSum {
     }
 };
 
-template <int NL>
+// Shared memory of the gradients: the chunk, the states in front of its subs but the first ([sub][warp][4][lane] float4 of four
+// states each), and room for the first sub's sums.  A sub's sums of dB and dC ([token][2 states] a warp) take the place of
+// the warp's states in front of it.
+template <typename T, int NL>
 struct GradSmem {
-    using Tile = ScanTile<NL>;
-    static constexpr int CH = Tile::ch, S = Tile::states;
-    static constexpr int entries = kChunk / kSub * 4 * kScanThreads * 4;   // floats
-    static constexpr size_t bytes = sizeof(float) * (entries + 6 * kSub * CH + 2 * kSub * S + 4 * kSub * 2 * S);
+    using Ck = Chunk<T, NL>;
+    static constexpr int subs = Ck::C / kSub, warp = 4 * 32 * 4;   // floats of a warp's states
+    static constexpr int sums = kSub * 2 * Ck::S;                  // floats of a warp's sums
+    static_assert(sums <= warp, "a sub's sums fit in its states' place");
+    static constexpr size_t bytes = sizeof(float) * (Ck::floats + (subs - 1) * 4 * warp + 4 * sums);
 };
 
 template <typename T, int NL, bool WIDE>
-__global__ void __launch_bounds__(kScanThreads, NL == 1 ? 1 : 2) k_scan_grad(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
-    using Tile = ScanTile<NL>;
-    constexpr int CH = Tile::ch, S = Tile::states, V = CH / 4;
+__global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
+    using Ck = Chunk<T, NL>;
+    using Sm = GradSmem<T, NL>;
+    constexpr int CH = Ck::CH, S = Ck::S, C = Ck::C, V = CH / 4;
     extern __shared__ __align__(16) float dyn[];
-    float4* entry = reinterpret_cast<float4*>(dyn);   // [sub][channel i][thread]
-    float *s_dt = dyn + GradSmem<NL>::entries, *s_du = s_dt + kSub * CH, *s_g = s_du + kSub * CH, *s_1 = s_g + kSub * CH, *s_2 = s_1 + kSub * CH,
-          *s_y = s_2 + kSub * CH, *s_b = s_y + kSub * CH, *s_c = s_b + kSub * S, *s_bc = s_c + kSub * S;   // s_bc [warp][token][2 S]
-    __shared__ int what[kSub], seq[kSub];
+    __shared__ int flags[2 * C];
+    const Ck ck(dyn, flags);
+    float* const place = dyn + Ck::floats;   // of subs 1 .. , then the first sub's sums
     const ChBlock cb = ch_block<NL>(d, blockIdx.y);
     const ScanLane<NL> l;
     const ChannelSum<NL> cs;
-    const int warp = threadIdx.x >> 5;
-    float2 a2[4][2], dA[4][2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const auto sums_of = [&](int sub, int w) { return sub ? place + ((sub - 1) * 4 + w) * Sm::warp : place + (Sm::subs - 1) * 4 * Sm::warp + w * Sm::sums; };
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto two = [](const float4& x, const float4& y, float2 (&to)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = l.states(in.A, d, cb, i);
-        a2[i][0] = mul2(lo(v), both(kLog2eF));
-        a2[i][1] = mul2(hi(v), both(kLog2eF));
-        dA[i][0] = dA[i][1] = make_float2(0.f, 0.f);
-    }
+        for (int n = 0; n < 4; ++n) to[n] = make_float2(at4(x, n), at4(y, n));
+    };
+    const auto fetch = [&](const float* x, size_t at, float2 (&to)[2][4]) {   // the thread's states of [D][N] at x + at (null: zeros)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) two(x ? l.states(x + at, d, cb, 2 * i) : none, x ? l.states(x + at, d, cb, 2 * i + 1) : none, to[i]);
+    };
+    // pairs of channels (2 i, 2 i + 1), states 4 nl + n
+    float2 a2[2][4], dA[2][4];
+    fetch(in.A, 0, a2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            a2[i][n] = mul2(a2[i][n], both(kLog2eF));
+            dA[i][n] = make_float2(0.f, 0.f);
+        }
     // what the thread adds up over tokens: channels ec .. ec + 3
     const int ec = threadIdx.x % V * 4, en = min(4, cb.n - ec);
-    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 dskip = none, dbias = none;
     const float4 skip = in.skip ? load4<float, false>(in.skip + cb.c0 + ec, en) : none;
     const float4 bias = in.dbias ? load4<float, false>(in.dbias + cb.c0 + ec, en) : none;
@@ -294,190 +354,234 @@ __global__ void __launch_bounds__(kScanThreads, NL == 1 ? 1 : 2) k_scan_grad(Sca
         }
     const int tasks = d.at.rows() * ws.chunks;
     for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-        const int axis = task / ws.chunks, ta = task % ws.chunks * kChunk, tb = min(ta + kChunk, d.at.L);
+        const int axis = task / ws.chunks, ta = task % ws.chunks * C, tb = min(ta + C, d.at.L);
         const int subs = (tb - ta + kSub - 1) / kSub;
         const Rows<T> r(d, in, gr.dy, axis, cb);
-        float2 q[4][2], hs[kSub][4][2];
-        // the chunk's entering state and gradient
-        const size_t at0 = ((size_t)task * d.D + cb.c0 + l.cl) * S + 4 * l.nl;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in_range = l.cl + i < cb.n;
-            const float4 e = in_range ? *reinterpret_cast<const float4*>(ws.ends + at0 + (size_t)i * S) : none;
-            const float4 f = in_range ? *reinterpret_cast<const float4*>(ws.grads + at0 + (size_t)i * S) : none;
-            entry[i * kScanThreads + threadIdx.x] = e;
-            q[i][0] = lo(f);
-            q[i][1] = hi(f);
-        }
-        const auto fetch = [&](int sub, bool grad) {   // the sub's tokens into shared memory
-            const int t0 = ta + sub * kSub;
-            __syncthreads();
-            if (threadIdx.x < kSub) {
-                const TokenAt a = token_at(d.at, axis, t0 + threadIdx.x, tb);
-                what[threadIdx.x] = a.what;
-                seq[threadIdx.x] = a.seq;
-            }
-            __syncthreads();
-            load_rows<T, S, kSub>(s_b, r.Bm, d.bs[1], d.N, t0, what);
-            if (grad) {
-                load_rows<T, S, kSub>(s_c, r.C, d.cs[1], d.N, t0, what);
-                load_tile<T, WIDE, CH, kSub, true>(d, in, r, cb, t0, what, s_dt, s_du, s_g);
-            } else {
-                load_tile<T, WIDE, CH, kSub, false>(d, in, r, cb, t0, what, s_dt, s_du, s_g);
-            }
-            __syncthreads();
-        };
-        // the sub's states from its entering one
-        const auto forward = [&](int sub) {
-            float2 h[4][2];
+        ck.template load<WIDE>(d, r, cb, axis, ta, tb, bias);
+        float2 q[2][4], h0[2][4];   // the gradient from behind, and the chunk's entering state
+        {
+            const size_t at0 = ((size_t)task * d.D + cb.c0 + l.cl) * S + 4 * l.nl;
+            float4 e[4], f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 e = entry[(sub * 4 + i) * kScanThreads + threadIdx.x];
-                h[i][0] = lo(e);
-                h[i][1] = hi(e);
+                const bool in_range = l.cl + i < cb.n;
+                e[i] = in_range ? *reinterpret_cast<const float4*>(ws.ends + at0 + (size_t)i * S) : none;
+                f[i] = in_range ? *reinterpret_cast<const float4*>(ws.grads + at0 + (size_t)i * S) : none;
             }
 #pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-                if (what[t] & kFirst)
+            for (int i = 0; i < 2; ++i) {
+                two(e[2 * i], e[2 * i + 1], h0[i]);
+                two(f[2 * i], f[2 * i + 1], q[i]);
+            }
+        }
+        // the state behind token t from the one before it
+        const auto advance = [&](int t, float2 (&h)[2][4]) {
+            const float4 dt = *reinterpret_cast<const float4*>(ck.dt + t * CH + l.cl), u = *reinterpret_cast<const float4*>(ck.u + t * CH + l.cl);
+            Bc<T> bc;
+            bc.load(ck.bc + (t * NL + l.nl) * 8, false);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = in.S0 ? l.states(in.S0 + (size_t)seq[t] * d.D * d.N, d, cb, i) : none;
-                        h[i][0] = lo(v);
-                        h[i][1] = hi(v);
-                    }
-                const float4 dt = *reinterpret_cast<const float4*>(s_dt + t * CH + l.cl), du = *reinterpret_cast<const float4*>(s_du + t * CH + l.cl),
-                             b = *reinterpret_cast<const float4*>(s_b + t * S + 4 * l.nl);
+            for (int i = 0; i < 2; ++i) {
+                const float2 dt2 = i ? hi(dt) : lo(dt), du2 = mul2(dt2, i ? hi(u) : lo(u));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const float2 a = decay2(both(at4(dt, i)), a2[i][p]);
-                        h[i][p] = fma2(a, h[i][p], mul2(both(at4(du, i)), p ? hi(b) : lo(b)));
-                        hs[t][i][p] = h[i][p];
-                    }
+                for (int n = 0; n < 4; ++n) h[i][n] = fma2(decay2(dt2, a2[i][n]), h[i][n], mul2(du2, both(bc.bn(n))));
             }
         };
-        for (int sub = 0; sub + 1 < subs; ++sub) {
-            fetch(sub, false);
-            forward(sub);
+        const auto enter = [&](int sub, float2 (&h)[2][4]) {   // the state in front of a sub
+            const float4* p = reinterpret_cast<const float4*>(place + ((sub - 1) * 4 + warp) * Sm::warp) + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                entry[((sub + 1) * 4 + i) * kScanThreads + threadIdx.x] =
-                    make_float4(hs[kSub - 1][i][0].x, hs[kSub - 1][i][0].y, hs[kSub - 1][i][1].x, hs[kSub - 1][i][1].y);
+            for (int i = 0; i < 2; ++i) {
+                if (sub) two(p[2 * i * 32], p[(2 * i + 1) * 32], h[i]);
+                else
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) h[i][n] = h0[i][n];
+            }
+        };
+        const auto mixed = [&](int sub) {   // whether a sequence begins or ends in a sub
+            int w = 0;
+#pragma unroll
+            for (int e = 0; e < kSub; ++e) w |= ck.what[sub * kSub + e];
+            return (w & (kFirst | kLast)) != 0;
+        };
+        {   // the states in front of the subs
+            float2 h[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) h[i][n] = h0[i][n];
+#pragma unroll 1
+            for (int sub = 0; sub + 1 < subs; ++sub) {
+                if (!mixed(sub)) {
+#pragma unroll
+                    for (int e = 0; e < kSub; ++e) advance(sub * kSub + e, h);
+                } else {
+#pragma unroll 1
+                    for (int e = 0; e < kSub; ++e) {
+                        const int t = sub * kSub + e;
+                        if (ck.what[t] & kFirst) fetch(in.S0, (size_t)ck.seq[t] * d.D * d.N, h);
+                        advance(t, h);
+                    }
+                }
+                float4* p = reinterpret_cast<float4*>(place + (sub * 4 + warp) * Sm::warp) + lane;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    p[2 * i * 32] = make_float4(h[i][0].x, h[i][1].x, h[i][2].x, h[i][3].x);
+                    p[(2 * i + 1) * 32] = make_float4(h[i][0].y, h[i][1].y, h[i][2].y, h[i][3].y);
+                }
+            }
         }
+        // token t backwards, from the states behind (h) and in front of it (hp); its results take the place of its inputs:
+        // dt s1 of u, the gradient of dt of dt, sum_n C h of g
+        const auto back = [&](int t, float* sums, const float2 (&h)[2][4], const float2 (&hp)[2][4]) {
+            const int o = t * CH + l.cl;
+            const float4 dt = *reinterpret_cast<const float4*>(ck.dt + o), u = *reinterpret_cast<const float4*>(ck.u + o),
+                         g = *reinterpret_cast<const float4*>(ck.g + o);
+            Bc<T> bc;
+            bc.load(ck.bc + (t * NL + l.nl) * 8, true);
+            float2 db[4], dc[4], x1[2], x2[2], xy[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 dt2 = i ? hi(dt) : lo(dt), du2 = mul2(dt2, i ? hi(u) : lo(u)), g2 = i ? hi(g) : lo(g);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 b = both(bc.bn(n)), c = both(bc.cn(n));
+                    const float2 p = fma2(g2, c, q[i][n]);
+                    dc[n] = i ? fma2(g2, h[i][n], dc[n]) : mul2(g2, h[i][n]);
+                    db[n] = i ? fma2(du2, p, db[n]) : mul2(du2, p);
+                    x1[i] = n ? fma2(p, b, x1[i]) : mul2(p, b);
+                    xy[i] = n ? fma2(c, h[i][n], xy[i]) : mul2(c, h[i][n]);
+                    q[i][n] = mul2(p, decay2(dt2, a2[i][n]));
+                    const float2 e = mul2(q[i][n], hp[i][n]);
+                    dA[i][n] = fma2(dt2, e, dA[i][n]);
+                    x2[i] = n ? fma2(a2[i][n], e, x2[i]) : mul2(a2[i][n], e);
+                }
+            }
+            float v[8] = {db[0].x + db[0].y, db[1].x + db[1].y, db[2].x + db[2].y, db[3].x + db[3].y,
+                          dc[0].x + dc[0].y, dc[1].x + dc[1].y, dc[2].x + dc[2].y, dc[3].x + dc[3].y};
+            cs.sum(v);
+            if (cs.writes)
+#pragma unroll
+                for (int i = 0; i < ChannelSum<NL>::held; ++i) {
+                    const int j = cs.first + i;
+                    sums[(j >> 2) * S + 4 * l.nl + (j & 3)] = v[i];
+                }
+            constexpr int K = NL == 1 ? 4 : NL == 2 ? 2 : 1;
+            const float w1[4] = {x1[0].x, x1[0].y, x1[1].x, x1[1].y}, w2[4] = {x2[0].x, x2[0].y, x2[1].x, x2[1].y},
+                        wy[4] = {xy[0].x, xy[0].y, xy[1].x, xy[1].y};
+            float s1[K], s2[K], sy[K];
+            sum_states<NL>(w1, l.nl, s1);
+            sum_states<NL>(w2, l.nl, s2);
+            if (r.z) sum_states<NL>(wy, l.nl, sy);
+            if (NL <= 4 || l.nl < 4) {
+                const int first = o + its_channel<NL>(l.nl);
+#pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    const float dti = ck.dt[first + i], ui = ck.u[first + i];
+                    ck.u[first + i] = dti * s1[i];
+                    ck.dt[first + i] = fmaf(ui, s1[i], kLn2 * s2[i]);
+                    if (r.z) ck.g[first + i] = sy[i];
+                }
+            }
+        };
+#pragma unroll 1
         for (int sub = subs - 1; sub >= 0; --sub) {
-            const int t0 = ta + sub * kSub;
-            fetch(sub, true);
-            forward(sub);
+            float* const sums = sums_of(sub, warp);
+            const int t0 = sub * kSub;
+            float2 hp[2][4];
+            enter(sub, hp);
+            __syncwarp();   // (the sums take the states' place)
+            if (!mixed(sub)) {
+                float2 hs[kSub][2][4];
 #pragma unroll
-            for (int t = kSub - 1; t >= 0; --t) {
-                const int w = what[t];
-                const size_t at = (size_t)seq[t] * d.D * d.N;
-                if (w & kLast)
+                for (int e = 0; e < kSub; ++e) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = gr.dS ? l.states(gr.dS + at, d, cb, i) : none;
-                        q[i][0] = lo(v);
-                        q[i][1] = hi(v);
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) hs[e][i][n] = e ? hs[e ? e - 1 : 0][i][n] : hp[i][n];
+                    advance(t0 + e, hs[e]);
+                }
+#pragma unroll
+                for (int e = kSub - 1; e > 0; --e) back(t0 + e, sums + e * 2 * S, hs[e], hs[e - 1]);
+                back(t0, sums, hs[0], hp);
+            } else {
+#pragma unroll 1
+                for (int e = kSub - 1; e >= 0; --e) {
+                    const int t = t0 + e, w = ck.what[t];
+                    const size_t at = (size_t)ck.seq[t] * d.D * d.N;
+                    float2 h[2][4], before[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) h[i][n] = hp[i][n];
+#pragma unroll 1
+                    for (int f = 0; f <= e; ++f) {
+                        if (ck.what[t0 + f] & kFirst) fetch(in.S0, (size_t)ck.seq[t0 + f] * d.D * d.N, h);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) before[i][n] = h[i][n];
+                        advance(t0 + f, h);
                     }
-                const float4 dt = *reinterpret_cast<const float4*>(s_dt + t * CH + l.cl), du = *reinterpret_cast<const float4*>(s_du + t * CH + l.cl),
-                             g = *reinterpret_cast<const float4*>(s_g + t * CH + l.cl), b = *reinterpret_cast<const float4*>(s_b + t * S + 4 * l.nl),
-                             c = *reinterpret_cast<const float4*>(s_c + t * S + 4 * l.nl);
-                float2 db[2], dc[2];
-                db[0] = db[1] = dc[0] = dc[1] = make_float2(0.f, 0.f);
-                float o1[4], o2[4], oy[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 dt2 = both(at4(dt, i)), du2 = both(at4(du, i)), g2 = both(at4(g, i));
-                    float2 hp[2];
+                    if (w & kLast) fetch(gr.dS, at, q);
+                    back(t, sums + e * 2 * S, h, before);
                     if (w & kFirst) {
-                        const float4 v = in.S0 ? l.states(in.S0 + at, d, cb, i) : none;
-                        hp[0] = lo(v);
-                        hp[1] = hi(v);
-                    } else if (t > 0) {
-                        hp[0] = hs[t > 0 ? t - 1 : 0][i][0];
-                        hp[1] = hs[t > 0 ? t - 1 : 0][i][1];
-                    } else {
-                        const float4 e = entry[(sub * 4 + i) * kScanThreads + threadIdx.x];
-                        hp[0] = lo(e);
-                        hp[1] = hi(e);
-                    }
-                    float2 x1 = make_float2(0.f, 0.f), x2 = x1, xy = x1;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const float2 bp = p ? hi(b) : lo(b), cp = p ? hi(c) : lo(c), h = hs[t][i][p];
-                        const float2 pt = fma2(g2, cp, q[i][p]);
-                        dc[p] = fma2(g2, h, dc[p]);
-                        db[p] = fma2(du2, pt, db[p]);
-                        x1 = fma2(pt, bp, x1);
-                        xy = fma2(cp, h, xy);
-                        q[i][p] = mul2(pt, decay2(dt2, a2[i][p]));
-                        const float2 e = mul2(q[i][p], hp[p]);
-                        dA[i][p] = fma2(dt2, e, dA[i][p]);
-                        x2 = fma2(a2[i][p], e, x2);
+                        for (int i = 0; i < 2; ++i) {
+                            if (gr.dS0) {
+                                l.put_states(gr.dS0 + at, d, cb, 2 * i, make_float4(q[i][0].x, q[i][1].x, q[i][2].x, q[i][3].x));
+                                l.put_states(gr.dS0 + at, d, cb, 2 * i + 1, make_float4(q[i][0].y, q[i][1].y, q[i][2].y, q[i][3].y));
+                            }
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) q[i][n] = make_float2(0.f, 0.f);
+                        }
                     }
-                    o1[i] = x1.x + x1.y;
-                    o2[i] = x2.x + x2.y;
-                    oy[i] = xy.x + xy.y;
                 }
-                if (w & kFirst)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (gr.dS0) l.put_states(gr.dS0 + at, d, cb, i, make_float4(q[i][0].x, q[i][0].y, q[i][1].x, q[i][1].y));
-                        q[i][0] = q[i][1] = make_float2(0.f, 0.f);
-                    }
-                put_sums<NL>(s_1 + t * CH, l, o1);
-                put_sums<NL>(s_2 + t * CH, l, o2);
-                if (r.z) put_sums<NL>(s_y + t * CH, l, oy);
-                float v[8] = {db[0].x, db[0].y, db[1].x, db[1].y, dc[0].x, dc[0].y, dc[1].x, dc[1].y};
-                cs.sum(v);
-                if (cs.writes)
-#pragma unroll
-                    for (int i = 0; i < ChannelSum<NL>::held; ++i) {
-                        const int j = cs.first + i;
-                        s_bc[(warp * kSub + t) * 2 * S + (j >> 2) * S + 4 * l.nl + (j & 3)] = v[i];
-                    }
             }
-            __syncthreads();
-            for (int i = threadIdx.x; i < kSub * 2 * S; i += kScanThreads) {
-                const int t = i / (2 * S), j = i % (2 * S);
-                if (what[t] & kOutside) continue;
-                float v = s_bc[i];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < subs * kSub * 2 * S; i += kScanThreads) {
+            const int t = i / (2 * S), j = i % (2 * S), at = (t % kSub) * 2 * S + j;
+            if (ck.what[t] & kOutside) continue;
+            float v = sums_of(t / kSub, 0)[at];
 #pragma unroll
-                for (int k = 1; k < 4; ++k) v += s_bc[k * kSub * 2 * S + i];
-                ws.bc[((((size_t)cb.cb * d.at.rows() + axis) * d.at.L + t0 + t) * d.G + cb.g) * 2 * S + j] = v;
-            }
-            for (int t = threadIdx.x / V; t < kSub; t += kScanThreads / V) {
-                if ((what[t] & kOutside) || en <= 0) continue;
-                const long long tt = t0 + t;
+            for (int w = 1; w < 4; ++w) v += sums_of(t / kSub, w)[at];
+            ws.bc[((((size_t)cb.cb * d.at.rows() + axis) * d.at.L + ta + t) * d.G + cb.g) * 2 * S + j] = v;
+        }
+        if (en > 0)
+#pragma unroll 2
+            for (int t = threadIdx.x / V; t < tb - ta; t += kScanThreads / V) {
+                if (ck.what[t] & kOutside) continue;
+                const long long tt = ta + t;
                 const int o = t * CH + ec;
-                const float4 dt = *reinterpret_cast<const float4*>(s_dt + o), g = *reinterpret_cast<const float4*>(s_g + o),
-                             x1 = *reinterpret_cast<const float4*>(s_1 + o), x2 = *reinterpret_cast<const float4*>(s_2 + o);
-                const float4 u = load4<T, WIDE>(r.u + tt * d.us[1] + ec, en);
-                store4<T, WIDE>((T*)gr.du + axis * d.dus[0] + tt * d.dus[1] + cb.c0 + ec, add4(mul4(dt, x1), mul4(skip, g)), en);
-                float4 dd = add4(mul4(x2, make_float4(kLn2, kLn2, kLn2, kLn2)), mul4(u, x1));
-                if (d.softplus) {
-                    const float4 raw = add4(load4<T, WIDE>(r.delta + tt * d.ds[1] + ec, en), bias);
-                    dd = mul4(dd, make_float4(sigmoid_of(raw.x), sigmoid_of(raw.y), sigmoid_of(raw.z), sigmoid_of(raw.w)));
+                const float4 u = load4<T, WIDE>(r.u + tt * d.us[1] + ec, en), dy = load4<T, WIDE>(r.dy + tt * d.dys[1] + ec, en);
+                float4 raw = none, z = none;
+                if (d.softplus) raw = add4(load4<T, WIDE>(r.delta + tt * d.ds[1] + ec, en), bias);
+                if (r.z) z = load4<T, WIDE>(r.z + tt * d.zs[1] + ec, en);
+                const float4 x1 = *reinterpret_cast<const float4*>(ck.u + o), y = *reinterpret_cast<const float4*>(ck.g + o);
+                float4 dd = *reinterpret_cast<const float4*>(ck.dt + o), g = dy;
+                if (r.z) {
+                    const float4 s = make_float4(sigmoid_of(z.x), sigmoid_of(z.y), sigmoid_of(z.z), sigmoid_of(z.w)), f = mul4(z, s);
+                    // dz = dy (y + skip u) (s + z s (1 - s))
+                    const float4 yy = mul4(dy, add4(y, mul4(skip, u)));
+                    store4<T, WIDE>((T*)gr.dz + axis * d.dzs[0] + tt * d.dzs[1] + cb.c0 + ec,
+                                    mul4(yy, make_float4(fmaf(f.x, 1.f - s.x, s.x), fmaf(f.y, 1.f - s.y, s.y), fmaf(f.z, 1.f - s.z, s.z),
+                                                         fmaf(f.w, 1.f - s.w, s.w))), en);
+                    g = mul4(dy, f);
                 }
+                store4<T, WIDE>((T*)gr.du + axis * d.dus[0] + tt * d.dus[1] + cb.c0 + ec, add4(x1, mul4(skip, g)), en);
+                if (d.softplus) dd = mul4(dd, make_float4(sigmoid_of(raw.x), sigmoid_of(raw.y), sigmoid_of(raw.z), sigmoid_of(raw.w)));
                 store4<T, WIDE>((T*)gr.ddelta + axis * d.dds[0] + tt * d.dds[1] + cb.c0 + ec, dd, en);
                 dbias = add4(dbias, dd);
                 dskip = add4(dskip, mul4(g, u));
-                if (r.z) {
-                    const float4 y = add4(*reinterpret_cast<const float4*>(s_y + o), mul4(skip, u)), z = load4<T, WIDE>(r.z + tt * d.zs[1] + ec, en);
-                    const float4 dy = load4<T, WIDE>(r.dy + tt * d.dys[1] + ec, en);
-                    const float4 f = make_float4(dsilu_of(z.x), dsilu_of(z.y), dsilu_of(z.z), dsilu_of(z.w));
-                    store4<T, WIDE>((T*)gr.dz + axis * d.dzs[0] + tt * d.dzs[1] + cb.c0 + ec, mul4(mul4(dy, y), f), en);
-                }
             }
-        }
     }
     // the CTA's sums over its tokens
     float* out = ws.ch + blockIdx.x * ch_stride(d, S);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (l.cl + i < cb.n)
-            *reinterpret_cast<float4*>(out + (size_t)(cb.c0 + l.cl + i) * S + 4 * l.nl) = make_float4(dA[i][0].x, dA[i][0].y, dA[i][1].x, dA[i][1].y);
+            *reinterpret_cast<float4*>(out + (size_t)(cb.c0 + l.cl + i) * S + 4 * l.nl) =
+                i & 1 ? make_float4(dA[i / 2][0].y, dA[i / 2][1].y, dA[i / 2][2].y, dA[i / 2][3].y)
+                      : make_float4(dA[i / 2][0].x, dA[i / 2][1].x, dA[i / 2][2].x, dA[i / 2][3].x);
     __syncthreads();
     float4* red = reinterpret_cast<float4*>(dyn);
     red[threadIdx.x] = dskip;
@@ -541,7 +645,8 @@ __global__ void __launch_bounds__(256) k_scan_sum_ch(ScanDims d, const float* ch
 // Sizes of a backward call's workspace; CTAs along the chunks: about two an SM in all.
 size_t carve(const ScanDims& d, char* base, ScanWs* ws) {
     const int S = 4 * state_lanes(d.N), ch = 16 * 32 / (S / 4), blocks = ch_blocks(d, ch) / d.G;
-    ws->chunks = (d.at.L + kChunk - 1) / kChunk;
+    const int C = chunk_of(state_lanes(d.N));
+    ws->chunks = (d.at.L + C - 1) / C;
     const long long tasks = (long long)d.at.rows() * ws->chunks, all = (long long)blocks * d.G;
     const long long most = (2 * kScanSms + all - 1) / all, per = tasks ? (tasks + most - 1) / most : 1;
     ws->gx = (int)(tasks ? (tasks + per - 1) / per : 1);
@@ -563,10 +668,11 @@ size_t carve(const ScanDims& d, char* base, ScanWs* ws) {
 template <typename T, int NL, bool WIDE>
 cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const ScanWs& ws, cudaStream_t st) {
     using Tile = ScanTile<NL>;
+    using Sm = GradSmem<T, NL>;
     const int blocks = ch_blocks(d, Tile::ch), rows = d.at.rows();
     cudaError_t e;
     if (ws.chunks && rows) {
-        const size_t smem = sizeof(float) * kTile * (3 * Tile::ch + 2 * Tile::states);
+        constexpr size_t smem = sizeof(float) * Chunk<T, NL>::floats;
         const auto local = k_scan_local<T, NL, WIDE>;
         if ((e = cudaFuncSetAttribute(local, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
         local<<<dim3(ws.chunks, blocks, rows), kScanThreads, smem, st>>>(d, in, g, ws);
@@ -577,8 +683,8 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const S
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     const auto grad = k_scan_grad<T, NL, WIDE>;
-    if ((e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradSmem<NL>::bytes)) != cudaSuccess) return e;
-    grad<<<dim3(ws.gx, blocks), kScanThreads, GradSmem<NL>::bytes, st>>>(d, in, g, ws);
+    if ((e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sm::bytes)) != cudaSuccess) return e;
+    grad<<<dim3(ws.gx, blocks), kScanThreads, Sm::bytes, st>>>(d, in, g, ws);
     prof_mark("scan_grad", st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long n = (long long)rows * d.at.L * d.G * 2 * Tile::states;
@@ -591,7 +697,8 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const S
 template <typename T>
 cudaError_t bwd(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const ScanWs& ws, cudaStream_t st) {
     const bool wide = wide4(d, in.u, d.us) && wide4(d, in.delta, d.ds) && wide4(d, in.z, d.zs) && wide4(d, g.dy, d.dys) &&
-                      wide4(d, g.du, d.dus) && wide4(d, g.ddelta, d.dds) && wide4(d, g.dz, d.dzs);
+                      wide4(d, g.du, d.dus) && wide4(d, g.ddelta, d.dds) && wide4(d, g.dz, d.dzs) && wide4(d, in.Bm, d.bs) &&
+                      wide4(d, in.C, d.cs);
     return by_lanes(d.N, [&](auto nl) {
         constexpr int NL = decltype(nl)::value;
         return wide ? run<T, NL, true>(d, in, g, ws, st) : run<T, NL, false>(d, in, g, ws, st);

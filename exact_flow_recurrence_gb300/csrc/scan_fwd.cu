@@ -48,35 +48,6 @@ struct FwdTile {
     static constexpr size_t bytes = 2 * buffer * sizeof(float) + kRing * slot * sizeof(Vec<T, 4>);
 };
 
-// The four B and four C of a token
-template <typename T>
-struct Bc;
-template <>
-struct Bc<float> {
-    float4 b, c;
-    __device__ __forceinline__ void load(const float* p, bool both_) {
-        b = *reinterpret_cast<const float4*>(p);
-        if (both_) c = *reinterpret_cast<const float4*>(p + 4);
-    }
-    __device__ __forceinline__ float bn(int n) const { return at4(b, n); }
-    __device__ __forceinline__ float cn(int n) const { return at4(c, n); }
-};
-template <>
-struct Bc<__nv_bfloat16> {
-    uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool both_) {
-        if (both_) {
-            v = *reinterpret_cast<const uint4*>(p);
-        } else {
-            const uint2 h = *reinterpret_cast<const uint2*>(p);
-            v = make_uint4(h.x, h.y, 0u, 0u);
-        }
-    }
-    __device__ static __forceinline__ float one(uint32_t w, int n) { return __uint_as_float(n & 1 ? w & 0xffff0000u : w << 16); }
-    __device__ __forceinline__ float bn(int n) const { return one(n < 2 ? v.x : v.y, n); }
-    __device__ __forceinline__ float cn(int n) const { return one(n < 2 ? v.z : v.w, n); }
-};
-
 // Warps 0 .. 7 carry the states, two neighbouring channels of four states a thread (the two channels in one instruction's
 // halves); the other warps bring the tokens (asynchronous copies, kRing tiles ahead), work out dt and dt u for them, and
 // finish the y that they left: skip, gate, store.
