@@ -51,6 +51,23 @@ __device__ __forceinline__ float4 load4(const T* p, int n) {
     }
     return make_float4(f[0], f[1], f[2], f[3]);
 }
+// ... and as they are stored, into v
+template <typename T, bool WIDE>
+__device__ __forceinline__ void take4(Vec<T, 4>& v, const T* p, int n) {
+    if (WIDE) {
+        v.load(p);
+    } else {
+        const float4 x = load4<T, false>(p, n);
+        const float f[4] = {x.x, x.y, x.z, x.w};
+        v.set(f);
+    }
+}
+template <typename T>
+__device__ __forceinline__ float4 as4(const Vec<T, 4>& v) {
+    float f[4];
+    v.get(f);
+    return make_float4(f[0], f[1], f[2], f[3]);
+}
 template <typename T, bool WIDE>
 __device__ __forceinline__ void store4(T* p, float4 x, int n) {
     const float f[4] = {x.x, x.y, x.z, x.w};

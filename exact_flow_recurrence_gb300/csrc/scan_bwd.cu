@@ -50,6 +50,8 @@ struct Rows {
     }
 };
 
+constexpr int kBatch = 8;   // tokens of four channels a thread loads at once
+
 // A chunk in shared memory: dt, u, g [tokens][CH] fp32 (g = dy z sigmoid(z)), B and C as they are stored [tokens][NL][4 and 4],
 // and what its tokens are.
 template <typename T, int NL>
@@ -64,7 +66,7 @@ struct Chunk {
     // tokens ta .. tb-1 (every thread of the CTA; ends with a barrier)
     template <bool WIDE>
     __device__ __forceinline__ void load(const ScanDims& d, const Rows<T>& r, const ChBlock& cb, int axis, int ta, int tb, float4 bias) const {
-        constexpr int V = CH / 4, rows = kScanThreads / V, items = C / rows, batch = items < 4 ? items : 4;
+        constexpr int V = CH / 4, rows = kScanThreads / V, items = C / rows, batch = items < kBatch ? items : kBatch;
         const int tid = threadIdx.x, c = tid % V * 4, row = tid / V, n = min(4, cb.n - c);
         const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();   // (the last readers of what was here)
@@ -74,53 +76,51 @@ struct Chunk {
             seq[tid] = a.seq;
         }
         __syncthreads();
+        // (every load of a batch before its first use, and before the first store, which would hold the loads behind it back; tokens
+        // past the last read the last one again, and count as zeros)
+        constexpr int groups = 2 * C * NL, bcs = (groups + kScanThreads - 1) / kScanThreads;
+        Vec<T, 4> vb[bcs];
 #pragma unroll
-        for (int j = 0; j < C * NL * 2 / kScanThreads + (C * NL * 2 % kScanThreads ? 1 : 0); ++j) {
+        for (int j = 0; j < bcs; ++j) {
             const int e = tid + j * kScanThreads, q = e % NL, t = e / NL % C;
-            const bool isC = e >= C * NL;
-            if (e < 2 * C * NL) {
-                Vec<T, 4> v;
-                v.zero();
-                if (!(what[t] & kOutside) && 4 * q < d.N) {
-                    const T* from = (isC ? r.C + (ta + t) * d.cs[1] : r.Bm + (ta + t) * d.bs[1]) + 4 * q;
-                    if (WIDE) {
-                        v.load(from);
-                    } else {
-                        const float4 x = load4<T, false>(from, min(4, d.N - 4 * q));
-                        const float f[4] = {x.x, x.y, x.z, x.w};
-                        v.set(f);
-                    }
-                }
-                *reinterpret_cast<Vec<T, 4>*>(bc + (t * NL + q) * 8 + (isC ? 4 : 0)) = v;
-            }
+            vb[j].zero();
+            if (e < groups && !(what[t] & kOutside) && 4 * q < d.N)
+                take4<T, WIDE>(vb[j], (e >= C * NL ? r.C + (ta + t) * d.cs[1] : r.Bm + (ta + t) * d.bs[1]) + 4 * q, min(4, d.N - 4 * q));
         }
-#pragma unroll 1
-        for (int j0 = 0; j0 < items; j0 += batch) {
-            float4 xd[batch], xu[batch], xg[batch], xz[batch];   // (every load before the first store: a store holds back the loads behind it)
-            bool in_range[batch];
+        const auto batch_of = [&](int j0) {
+            Vec<T, 4> vd[batch], vu[batch], vg[batch], vz[batch];
 #pragma unroll
             for (int j = 0; j < batch; ++j) {
-                const int t = row + (j0 + j) * rows;
-                const long long tt = ta + t;
-                in_range[j] = n > 0 && !(what[t] & kOutside);
-                xd[j] = in_range[j] ? load4<T, WIDE>(r.delta + tt * d.ds[1] + c, n) : none;
-                xu[j] = in_range[j] ? load4<T, WIDE>(r.u + tt * d.us[1] + c, n) : none;
-                xg[j] = in_range[j] ? load4<T, WIDE>(r.dy + tt * d.dys[1] + c, n) : none;
-                if (r.z) xz[j] = in_range[j] ? load4<T, WIDE>(r.z + tt * d.zs[1] + c, n) : none;
+                const long long tt = min(ta + row + (j0 + j) * rows, tb - 1);
+                vd[j].zero(); vu[j].zero(); vg[j].zero(); vz[j].zero();
+                if (n > 0) {
+                    take4<T, WIDE>(vd[j], r.delta + tt * d.ds[1] + c, n);
+                    take4<T, WIDE>(vu[j], r.u + tt * d.us[1] + c, n);
+                    take4<T, WIDE>(vg[j], r.dy + tt * d.dys[1] + c, n);
+                    if (r.z) take4<T, WIDE>(vz[j], r.z + tt * d.zs[1] + c, n);
+                }
             }
 #pragma unroll
             for (int j = 0; j < batch; ++j) {
-                xd[j] = steps(d, add4(xd[j], bias), n);
-                if (!in_range[j]) xd[j] = none;
-                if (r.z) xg[j] = mul4(xg[j], make_float4(silu_of(xz[j].x), silu_of(xz[j].y), silu_of(xz[j].z), silu_of(xz[j].w)));
+                const int t = row + (j0 + j) * rows, o = t * CH + c;
+                const bool in_range = n > 0 && !(what[t] & kOutside);
+                float4 xg = as4(vg[j]);
+                const float4 xd = steps(d, add4(as4(vd[j]), bias), n), xu = as4(vu[j]);
+                if (r.z) {
+                    const float4 z = as4(vz[j]);
+                    xg = mul4(xg, make_float4(silu_of(z.x), silu_of(z.y), silu_of(z.z), silu_of(z.w)));
+                }
+                *reinterpret_cast<float4*>(dt + o) = in_range ? xd : none;
+                *reinterpret_cast<float4*>(u + o) = in_range ? xu : none;
+                *reinterpret_cast<float4*>(g + o) = in_range ? xg : none;
             }
+        };
 #pragma unroll
-            for (int j = 0; j < batch; ++j) {
-                const int o = (row + (j0 + j) * rows) * CH + c;
-                *reinterpret_cast<float4*>(dt + o) = xd[j];
-                *reinterpret_cast<float4*>(u + o) = xu[j];
-                *reinterpret_cast<float4*>(g + o) = xg[j];
-            }
+        for (int j0 = 0; j0 < items; j0 += batch) batch_of(j0);
+#pragma unroll
+        for (int j = 0; j < bcs; ++j) {
+            const int e = tid + j * kScanThreads, q = e % NL, t = e / NL % C;
+            if (e < groups) *reinterpret_cast<Vec<T, 4>*>(bc + (t * NL + q) * 8 + (e >= C * NL ? 4 : 0)) = vb[j];
         }
         __syncthreads();
     }
@@ -357,7 +357,6 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
         const int axis = task / ws.chunks, ta = task % ws.chunks * C, tb = min(ta + C, d.at.L);
         const int subs = (tb - ta + kSub - 1) / kSub;
         const Rows<T> r(d, in, gr.dy, axis, cb);
-        ck.template load<WIDE>(d, r, cb, axis, ta, tb, bias);
         float2 q[2][4], h0[2][4];   // the gradient from behind, and the chunk's entering state
         {
             const size_t at0 = ((size_t)task * d.D + cb.c0 + l.cl) * S + 4 * l.nl;
@@ -368,6 +367,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
                 e[i] = in_range ? *reinterpret_cast<const float4*>(ws.ends + at0 + (size_t)i * S) : none;
                 f[i] = in_range ? *reinterpret_cast<const float4*>(ws.grads + at0 + (size_t)i * S) : none;
             }
+            ck.template load<WIDE>(d, r, cb, axis, ta, tb, bias);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 two(e[2 * i], e[2 * i + 1], h0[i]);
@@ -546,33 +546,49 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
             for (int w = 1; w < 4; ++w) v += sums_of(t / kSub, w)[at];
             ws.bc[((((size_t)cb.cb * d.at.rows() + axis) * d.at.L + ta + t) * d.G + cb.g) * 2 * S + j] = v;
         }
-        if (en > 0)
-#pragma unroll 2
-            for (int t = threadIdx.x / V; t < tb - ta; t += kScanThreads / V) {
-                if (ck.what[t] & kOutside) continue;
-                const long long tt = ta + t;
-                const int o = t * CH + ec;
-                const float4 u = load4<T, WIDE>(r.u + tt * d.us[1] + ec, en), dy = load4<T, WIDE>(r.dy + tt * d.dys[1] + ec, en);
-                float4 raw = none, z = none;
-                if (d.softplus) raw = add4(load4<T, WIDE>(r.delta + tt * d.ds[1] + ec, en), bias);
-                if (r.z) z = load4<T, WIDE>(r.z + tt * d.zs[1] + ec, en);
-                const float4 x1 = *reinterpret_cast<const float4*>(ck.u + o), y = *reinterpret_cast<const float4*>(ck.g + o);
-                float4 dd = *reinterpret_cast<const float4*>(ck.dt + o), g = dy;
-                if (r.z) {
-                    const float4 s = make_float4(sigmoid_of(z.x), sigmoid_of(z.y), sigmoid_of(z.z), sigmoid_of(z.w)), f = mul4(z, s);
-                    // dz = dy (y + skip u) (s + z s (1 - s))
-                    const float4 yy = mul4(dy, add4(y, mul4(skip, u)));
-                    store4<T, WIDE>((T*)gr.dz + axis * d.dzs[0] + tt * d.dzs[1] + cb.c0 + ec,
-                                    mul4(yy, make_float4(fmaf(f.x, 1.f - s.x, s.x), fmaf(f.y, 1.f - s.y, s.y), fmaf(f.z, 1.f - s.z, s.z),
-                                                         fmaf(f.w, 1.f - s.w, s.w))), en);
-                    g = mul4(dy, f);
+        if (en > 0) {
+            constexpr int rows = kScanThreads / V, items = C / rows, batch = items < kBatch ? items : kBatch;
+#pragma unroll
+            for (int j0 = 0; j0 < items; j0 += batch) {
+                Vec<T, 4> vd[batch], vu[batch], vg[batch], vz[batch];
+#pragma unroll
+                for (int j = 0; j < batch; ++j) {
+                    const long long tt = min(ta + (int)threadIdx.x / V + (j0 + j) * rows, tb - 1);
+                    vd[j].zero(); vz[j].zero();
+                    take4<T, WIDE>(vu[j], r.u + tt * d.us[1] + ec, en);
+                    take4<T, WIDE>(vg[j], r.dy + tt * d.dys[1] + ec, en);
+                    if (d.softplus) take4<T, WIDE>(vd[j], r.delta + tt * d.ds[1] + ec, en);
+                    if (r.z) take4<T, WIDE>(vz[j], r.z + tt * d.zs[1] + ec, en);
                 }
-                store4<T, WIDE>((T*)gr.du + axis * d.dus[0] + tt * d.dus[1] + cb.c0 + ec, add4(x1, mul4(skip, g)), en);
-                if (d.softplus) dd = mul4(dd, make_float4(sigmoid_of(raw.x), sigmoid_of(raw.y), sigmoid_of(raw.z), sigmoid_of(raw.w)));
-                store4<T, WIDE>((T*)gr.ddelta + axis * d.dds[0] + tt * d.dds[1] + cb.c0 + ec, dd, en);
-                dbias = add4(dbias, dd);
-                dskip = add4(dskip, mul4(g, u));
+#pragma unroll
+                for (int j = 0; j < batch; ++j) {
+                    const int t = threadIdx.x / V + (j0 + j) * rows, o = t * CH + ec;
+                    if (ck.what[t] & kOutside) continue;
+                    const long long tt = ta + t;
+                    const float4 u = as4(vu[j]), dy = as4(vg[j]);
+                    const float4 x1 = *reinterpret_cast<const float4*>(ck.u + o), y = *reinterpret_cast<const float4*>(ck.g + o);
+                    float4 dd = *reinterpret_cast<const float4*>(ck.dt + o), g = dy;
+                    if (r.z) {
+                        const float4 z = as4(vz[j]);
+                        const float4 s = make_float4(sigmoid_of(z.x), sigmoid_of(z.y), sigmoid_of(z.z), sigmoid_of(z.w)), f = mul4(z, s);
+                        // dz = dy (y + skip u) (s + z s (1 - s))
+                        const float4 yy = mul4(dy, add4(y, mul4(skip, u)));
+                        store4<T, WIDE>((T*)gr.dz + axis * d.dzs[0] + tt * d.dzs[1] + cb.c0 + ec,
+                                        mul4(yy, make_float4(fmaf(f.x, 1.f - s.x, s.x), fmaf(f.y, 1.f - s.y, s.y), fmaf(f.z, 1.f - s.z, s.z),
+                                                             fmaf(f.w, 1.f - s.w, s.w))), en);
+                        g = mul4(dy, f);
+                    }
+                    store4<T, WIDE>((T*)gr.du + axis * d.dus[0] + tt * d.dus[1] + cb.c0 + ec, add4(x1, mul4(skip, g)), en);
+                    if (d.softplus) {
+                        const float4 raw = add4(as4(vd[j]), bias);
+                        dd = mul4(dd, make_float4(sigmoid_of(raw.x), sigmoid_of(raw.y), sigmoid_of(raw.z), sigmoid_of(raw.w)));
+                    }
+                    store4<T, WIDE>((T*)gr.ddelta + axis * d.dds[0] + tt * d.dds[1] + cb.c0 + ec, dd, en);
+                    dbias = add4(dbias, dd);
+                    dskip = add4(dskip, mul4(g, u));
+                }
             }
+        }
     }
     // the CTA's sums over its tokens
     float* out = ws.ch + blockIdx.x * ch_stride(d, S);
