@@ -13,34 +13,76 @@ namespace efla {
 
 namespace {
 
-// weights [VEC channels][W] and bias of a thread's channels
+// VEC values as pairs (a single one with a zero)
+template <int VEC>
+constexpr int kPairs = (VEC + 1) / 2;
+template <typename T, int VEC>
+__device__ __forceinline__ void pairs_of(const Vec<T, VEC>& v, float2 (&to)[kPairs<VEC>]) {
+    float f[VEC + 1];
+    f[VEC] = 0.f;
+    v.get(f);
+#pragma unroll
+    for (int i = 0; i < kPairs<VEC>; ++i) to[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pairs(T* p, const float2 (&x)[kPairs<VEC>]) {
+    float f[VEC + 1];
+#pragma unroll
+    for (int i = 0; i < kPairs<VEC>; ++i) {
+        f[2 * i] = x[i].x;
+        f[2 * i + 1 < VEC ? 2 * i + 1 : VEC] = x[i].y;
+    }
+    Vec<T, VEC> v;
+    v.set(f);
+    v.store(p);
+}
+
+// weights [VEC channels][W] and bias of a thread's channels, as pairs of channels
 template <int VEC, int W>
-__device__ __forceinline__ void conv_weights(const ConvDims& d, const void* w, const void* bias, int c, float (&wv)[W][VEC], float (&bv)[VEC]) {
+__device__ __forceinline__ void conv_weights(const ConvDims& d, const void* w, const void* bias, int c, float2 (&wv)[W][kPairs<VEC>],
+                                             float2 (&bv)[kPairs<VEC>]) {
+    float f[VEC * W], b[VEC + 1];
+    if (VEC % 4 == 0 && !d.w_bf16 && ((uintptr_t)w & 15) == 0) {   // (16 bytes at a time: VEC W elements from element c W on)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+        for (int i = 0; i < VEC * W; i += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>((const float*)w + (size_t)c * W + i));
+            f[i] = v.x;
+            f[(i + 1) % (VEC * W)] = v.y;
+            f[(i + 2) % (VEC * W)] = v.z;
+            f[(i + 3) % (VEC * W)] = v.w;
+        }
+    } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            wv[j][i] = d.w_bf16 ? __bfloat162float(((const __nv_bfloat16*)w)[(size_t)(c + i) * W + j])
-                                : __ldg((const float*)w + (size_t)(c + i) * W + j);
-        bv[i] = !bias ? 0.f : d.w_bf16 ? __bfloat162float(((const __nv_bfloat16*)bias)[c + i]) : __ldg((const float*)bias + c + i);
+        for (int i = 0; i < VEC * W; ++i)
+            f[i] = d.w_bf16 ? __bfloat162float(((const __nv_bfloat16*)w)[(size_t)c * W + i]) : __ldg((const float*)w + (size_t)c * W + i);
+    }
+    b[VEC] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        b[i] = !bias ? 0.f : d.w_bf16 ? __bfloat162float(((const __nv_bfloat16*)bias)[c + i]) : __ldg((const float*)bias + c + i);
+#pragma unroll
+    for (int i = 0; i < kPairs<VEC>; ++i) {
+        bv[i] = make_float2(b[2 * i], b[2 * i + 1]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) wv[j][i] = make_float2(f[2 * i * W + j], 2 * i + 1 < VEC ? f[(2 * i + 1) % VEC * W + j] : 0.f);
     }
 }
 
 // The row at place t of sequence s (t may lie up to W - 1 before its start).  xa: the axis's rows.
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void conv_row(const ConvDims& d, const T* xa, const T* S0, const Seq& s, int t, int c, float (&out)[VEC]) {
+__device__ __forceinline__ void conv_row(const ConvDims& d, const T* xa, const T* S0, const Seq& s, int t, int c, float2 (&out)[kPairs<VEC>]) {
     Vec<T, VEC> v;
     if (t >= s.start) v.load(xa + t * d.xs[1] + c);
     else if (S0) v.load(S0 + ((size_t)s.b * (W - 1) + (W - 1 + t - s.start)) * d.D + c);
     else v.zero();
-    v.get(out);
+    pairs_of(v, out);
 }
 
 // Threads past `items` copy the final states: one row and VEC channels each.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(256) k_conv_fwd(ConvDims d, const T* x, const void* w, const void* bias, const T* S0, T* y,
+__global__ void __launch_bounds__(256, 3) k_conv_fwd(ConvDims d, const T* x, const void* w, const void* bias, const T* S0, T* y,
                                                    T* S_final, int nv, int run, int runs, long long items) {
-    constexpr int NB = 4;   // rows in flight
+    constexpr int NB = 4, P = kPairs<VEC>;   // rows a batch
     const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
     const int c = (int)(idx % nv) * VEC;
     if (idx >= items) {
@@ -49,54 +91,54 @@ __global__ void __launch_bounds__(256) k_conv_fwd(ConvDims d, const T* x, const 
         const int b = (int)(r / (W - 1)), row = (int)(r % (W - 1));
         const Seq s = seq_at(d.at, b);
         const T* xa = x + (d.at.packed ? 0 : b * d.xs[0]);
-        float f[VEC];
+        float2 f[P];
         conv_row<T, VEC, W>(d, xa, S0, s, s.end - (W - 1) + row, c, f);
-        Vec<T, VEC> v;
-        v.set(f);
-        v.store(S_final + ((size_t)b * (W - 1) + row) * d.D + c);
+        store_pairs<T, VEC>(S_final + ((size_t)b * (W - 1) + row) * d.D + c, f);
         return;
     }
     const long long r = idx / nv;
     const int axis = (int)(r / runs), t0 = (int)(r % runs) * run, t1 = min(t0 + run, d.at.L);
     const T* xa = x + axis * d.xs[0];
     T* ya = y + axis * d.ys[0] + c;
-    float wv[W][VEC], bv[VEC];
+    float2 wv[W][P], bv[P];
     conv_weights<VEC, W>(d, w, bias, c, wv, bv);
     Seq s = seq_of(d.at, axis, t0);
     for (int t = next_inside(d.at, s, t0, t1); t < t1; t = next_inside(d.at, s, t, t1)) {
         const int hi = min(t1, s.end);
-        float win[W - 1][VEC];
+        float2 win[W - 1][P];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) conv_row<T, VEC, W>(d, xa, S0, s, t - (W - 1) + j, c, win[j]);
-#pragma unroll 1
-        for (; t < hi; t += NB) {
-            Vec<T, VEC> q[NB];
+        Vec<T, VEC> q[2][NB];   // a batch ahead: a store holds back the loads behind it
+        const auto bring = [&](int u, int k) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) q[k][i].load(xa + min(u + i, hi - 1) * d.xs[1] + c);   // (past the last: the last again)
+        };
+        const auto walk = [&](int u, int k) {
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                q[i].zero();
-                if (t + i < hi) q[i].load(xa + (t + i) * d.xs[1] + c);
-            }
+                float2 cur[P], o[P];
+                pairs_of(q[k][i], cur);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                float cur[VEC], o[VEC];
-                q[i].get(cur);
+                for (int e = 0; e < P; ++e) {
+                    float2 a = bv[e];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    float a = bv[e];
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) a = fmaf(wv[j][e], win[j][e], a);
-                    a = fmaf(wv[W - 1][e], cur[e], a);
-                    o[e] = d.silu ? silu_of(a) : a;
+                    for (int j = 0; j < W - 1; ++j) a = fma2(wv[j][e], win[j][e], a);
+                    a = fma2(wv[W - 1][e], cur[e], a);
+                    o[e] = d.silu ? mul2(a, sigmoid2(a)) : a;
 #pragma unroll
                     for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
                     win[W - 2][e] = cur[e];
                 }
-                if (t + i < hi) {
-                    Vec<T, VEC> v;
-                    v.set(o);
-                    v.store(ya + (t + i) * d.ys[1]);
-                }
+                if (u + i < hi) store_pairs<T, VEC>(ya + (u + i) * d.ys[1], o);
             }
+        };
+        bring(t, 0);
+#pragma unroll 1
+        for (; t < hi; t += 2 * NB) {
+            bring(t + NB, 1);
+            walk(t, 0);
+            bring(t + 2 * NB, 0);
+            walk(t + NB, 1);
         }
         t = hi;
     }
@@ -105,32 +147,36 @@ __global__ void __launch_bounds__(256) k_conv_fwd(ConvDims d, const T* x, const 
 constexpr int kBwdWarps = 8;   // runs a CTA
 
 // A warp walks one run of tokens of 32 VEC channels.  part [CTA rows][W + 1][D]: the CTA's sums of dw and db.
-// CTAs with blockIdx.z = 1 compute dS0, a thread a channel vector of a sequence.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(32 * kBwdWarps) k_conv_bwd(ConvDims d, const T* x, const void* w, const void* bias, const T* S0,
+__global__ void __launch_bounds__(32 * kBwdWarps, 2) k_conv_bwd(ConvDims d, const T* x, const void* w, const void* bias, const T* S0,
                                                             const T* dy, const T* dS, T* dx, T* dS0, float* part, int run, int runs,
                                                             long long nruns) {
-    constexpr int NB = 4;
-    __shared__ float red[kBwdWarps][W + 1][32 * VEC];
+    constexpr int NB = 4, P = kPairs<VEC>;
+    __shared__ float2 red[kBwdWarps][W + 1][32 * P];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (blockIdx.y * 32 + lane) * VEC;
     const bool in = c < d.D;
-    float wv[W][VEC], bv[VEC], dw[W][VEC], db[VEC];
+    float2 wv[W][P], bv[P], dw[W][P], db[P];
     if (in) conv_weights<VEC, W>(d, w, bias, c, wv, bv);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        db[e] = 0.f;
+    for (int e = 0; e < P; ++e) {
+        db[e] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][e] = make_float2(0.f, 0.f);
     }
     // dp of one token from its window
-    const auto grad = [&](const float (&win)[W][VEC], const float (&g)[VEC], float (&dp)[VEC]) {
+    const auto grad = [&](const float2 (&win)[W][P], const float2 (&g)[P], float2 (&dp)[P]) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float a = bv[e];
+        for (int e = 0; e < P; ++e) {
+            if (d.silu) {
+                float2 a = bv[e];
 #pragma unroll
-            for (int j = 0; j < W; ++j) a = fmaf(wv[j][e], win[j][e], a);
-            dp[e] = d.silu ? g[e] * dsilu_of(a) : g[e];
+                for (int j = 0; j < W; ++j) a = fma2(wv[j][e], win[j][e], a);
+                const float2 s = sigmoid2(a);   // s (1 + a (1 - s))
+                dp[e] = mul2(mul2(g[e], s), fma2(a, fma2(s, both(-1.f), both(1.f)), both(1.f)));
+            } else {
+                dp[e] = g[e];
+            }
         }
     };
     const long long r = (long long)blockIdx.x * kBwdWarps + warp;
@@ -142,68 +188,72 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_conv_bwd(ConvDims d, const T
         Seq s = seq_of(d.at, axis, t0);
         for (int t = next_inside(d.at, s, t0, t1); t < t1; t = next_inside(d.at, s, t, t1)) {
             const int lo = t, hi = min(t1, s.end), stop = hi + W - 1;   // dx_{u - (W - 1)} leaves at step u
-            float win[W][VEC], old[W][VEC];                             // x_{u - (W - 1)} .. x_u, dp_{u - (W - 1)} .. dp_u
+            float2 win[W][P], old[W][P];                                // x_{u - (W - 1)} .. x_u, dp_{u - (W - 1)} .. dp_u
 #pragma unroll
             for (int j = 1; j < W; ++j) conv_row<T, VEC, W>(d, xa, S0, s, lo - W + j, c, win[j]);
 #pragma unroll
             for (int j = 0; j < W; ++j)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) old[j][e] = 0.f;
-#pragma unroll 1
-            for (int u = lo; u < stop; u += NB) {
-                Vec<T, VEC> qx[NB], qg[NB];
+                for (int e = 0; e < P; ++e) old[j][e] = make_float2(0.f, 0.f);
+            const int last = min(stop, s.end) - 1;   // the last token read
+            Vec<T, VEC> qx[2][NB], qg[2][NB];        // a batch ahead: a store holds back the loads behind it
+            const auto bring = [&](int u, int k) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    qx[i].zero();
-                    qg[i].zero();
-                    if (u + i < min(stop, s.end)) {
-                        qx[i].load(xa + (u + i) * d.xs[1] + c);
-                        qg[i].load(ga + (u + i) * d.dys[1]);
-                    }
+                    qx[k][i].load(xa + min(u + i, last) * d.xs[1] + c);
+                    qg[k][i].load(ga + min(u + i, last) * d.dys[1]);
                 }
+            };
+            const auto walk = [&](int u, int k) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     const int v = u + i;
-                    float g[VEC], dp[VEC];
+                    float2 g[P], dp[P];
 #pragma unroll
                     for (int j = 0; j + 1 < W; ++j)
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
+                        for (int e = 0; e < P; ++e) {
                             win[j][e] = win[j + 1][e];
                             old[j][e] = old[j + 1][e];
                         }
-                    qx[i].get(win[W - 1]);
-                    qg[i].get(g);
+                    pairs_of(qx[k][i], win[W - 1]);
+                    pairs_of(qg[k][i], g);
                     grad(win, g, dp);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) old[W - 1][e] = v < s.end ? dp[e] : 0.f;
+                    for (int e = 0; e < P; ++e) old[W - 1][e] = v < s.end ? dp[e] : make_float2(0.f, 0.f);
                     if (v < hi)
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            db[e] += dp[e];
+                        for (int e = 0; e < P; ++e) {
+                            db[e] = add2(db[e], dp[e]);
 #pragma unroll
-                            for (int j = 0; j < W; ++j) dw[j][e] = fmaf(dp[e], win[j][e], dw[j][e]);
+                            for (int j = 0; j < W; ++j) dw[j][e] = fma2(dp[e], win[j][e], dw[j][e]);
                         }
                     const int q = v - (W - 1);
                     if (q >= lo && v < stop) {
-                        float o[VEC];
+                        float2 o[P];
                         if (dS && q >= s.end - (W - 1)) {
                             Vec<T, VEC> f;
                             f.load(dS + ((size_t)s.b * (W - 1) + (q - (s.end - (W - 1)))) * d.D + c);
-                            f.get(o);
+                            pairs_of(f, o);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < VEC; ++e) o[e] = 0.f;
+                            for (int e = 0; e < P; ++e) o[e] = make_float2(0.f, 0.f);
                         }
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e)
+                        for (int e = 0; e < P; ++e)
 #pragma unroll
-                            for (int j = 0; j < W; ++j) o[e] = fmaf(wv[W - 1 - j][e], old[j][e], o[e]);
-                        Vec<T, VEC> f;
-                        f.set(o);
-                        f.store(da + q * d.dxs[1]);
+                            for (int j = 0; j < W; ++j) o[e] = fma2(wv[W - 1 - j][e], old[j][e], o[e]);
+                        store_pairs<T, VEC>(da + q * d.dxs[1], o);
                     }
                 }
+            };
+            bring(lo, 0);
+#pragma unroll 1
+            for (int u = lo; u < stop; u += 2 * NB) {
+                bring(u + NB, 1);
+                walk(u, 0);
+                bring(u + 2 * NB, 0);
+                walk(u + NB, 1);
             }
             t = hi;
         }
@@ -216,51 +266,52 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_conv_bwd(ConvDims d, const T
             const int len = s.end - s.start;
             const T* xa = x + (d.at.packed ? 0 : b * d.xs[0]);
             const T* ga = dy + (d.at.packed ? 0 : b * d.dys[0]) + c;
-            float dp[W - 1][VEC];
+            float2 dp[W - 1][P];
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) dp[i][e] = 0.f;
+                for (int e = 0; e < P; ++e) dp[i][e] = make_float2(0.f, 0.f);
                 if (i < len) {
-                    float win[W][VEC], g[VEC];
+                    float2 win[W][P], g[P];
 #pragma unroll
                     for (int j = 0; j < W; ++j) conv_row<T, VEC, W>(d, xa, S0, s, s.start + i - (W - 1) + j, c, win[j]);
                     Vec<T, VEC> v;
                     v.load(ga + (s.start + i) * d.dys[1]);
-                    v.get(g);
+                    pairs_of(v, g);
                     grad(win, g, dp[i]);
                 }
             }
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) {
-                float o[VEC];
+                float2 o[P];
                 Vec<T, VEC> v;
                 v.zero();
                 if (dS && k >= len) v.load(dS + ((size_t)b * (W - 1) + (k - len)) * d.D + c);
-                v.get(o);
+                pairs_of(v, o);
 #pragma unroll
                 for (int i = 0; i <= k; ++i)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) o[e] = fmaf(wv[k - i][e], dp[i][e], o[e]);
-                v.set(o);
-                v.store(dS0 + ((size_t)b * (W - 1) + k) * d.D + c);
+                    for (int e = 0; e < P; ++e) o[e] = fma2(wv[k - i][e], dp[i][e], o[e]);
+                store_pairs<T, VEC>(dS0 + ((size_t)b * (W - 1) + k) * d.D + c, o);
             }
         }
     }
     // the CTA's runs together, in order
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
+    for (int e = 0; e < P; ++e) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) red[warp][j][lane * VEC + e] = dw[j][e];
-        red[warp][W][lane * VEC + e] = db[e];
+        for (int j = 0; j < W; ++j) red[warp][j][lane * P + e] = dw[j][e];
+        red[warp][W][lane * P + e] = db[e];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < (W + 1) * 32 * VEC; i += 32 * kBwdWarps) {
-        const int j = i / (32 * VEC), e = i % (32 * VEC), ch = blockIdx.y * 32 * VEC + e;
-        float sum = 0.f;
+    for (int i = threadIdx.x; i < (W + 1) * 32 * P; i += 32 * kBwdWarps) {
+        const int j = i / (32 * P), e = i % (32 * P), ch = VEC == 1 ? blockIdx.y * 32 + e : blockIdx.y * 32 * VEC + 2 * e;
+        float2 sum = red[0][j][e];
 #pragma unroll
-        for (int k = 0; k < kBwdWarps; ++k) sum += red[k][j][e];
-        if (ch < d.D) part[((size_t)blockIdx.x * (W + 1) + j) * d.D + ch] = sum;
+        for (int k = 1; k < kBwdWarps; ++k) sum = add2(sum, red[k][j][e]);
+        float* p = part + ((size_t)blockIdx.x * (W + 1) + j) * d.D + ch;
+        if (ch < d.D) p[0] = sum.x;
+        if (VEC > 1 && ch < d.D) p[1] = sum.y;   // (D is a multiple of VEC)
     }
 }
 
@@ -303,21 +354,25 @@ __global__ void __launch_bounds__(256) k_conv_step(ConvDims d, const T* x, const
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) q[j] = *reinterpret_cast<const Vec<T, VEC>*>(Sb + (size_t)j * d.D);
         q[W - 1].load(x + b * d.xs[0] + c);
-        float wv[W][VEC], bv[VEC], a[VEC];
-        conv_weights<VEC, W>(d, w, bias, c, wv, bv);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) a[e] = bv[e];
+        constexpr int P = kPairs<VEC>;
+        float2 wv[W][P], a[P];
+        conv_weights<VEC, W>(d, w, bias, c, wv, a);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            float f[VEC];
-            q[j].get(f);
+            float2 f[P];
+            pairs_of(q[j], f);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) a[e] = fmaf(wv[j][e], f[e], a[e]);
+            for (int e = 0; e < P; ++e) a[e] = fma2(wv[j][e], f[e], a[e]);
             if (j) q[j].store(Sb + (size_t)(j - 1) * d.D);
         }
+        float f[VEC + 1];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) a[e] = d.silu ? silu_of(a[e]) : a[e];
-        o.set(a);
+        for (int e = 0; e < P; ++e) {
+            const float2 v = d.silu ? mul2(a[e], sigmoid2(a[e])) : a[e];
+            f[2 * e] = v.x;
+            f[2 * e + 1 < VEC ? 2 * e + 1 : VEC] = v.y;
+        }
+        o.set(f);
     }
     o.store(y + b * d.ys[0] + c);
 }
@@ -332,13 +387,23 @@ struct ConvArgs {
     int nslots;
 };
 
+// Tokens a run: as many CTAs as run at once (`each` an SM), or a multiple of them, so that none comes late; 128 at most, since
+// a longer run saves no more of the rows that two of them share, and `least` at least.
+int run_of(int L, double ctas_a_run, int each, int least) {
+    int run = L;
+    if (ctas_a_run <= 0) return least;
+    for (int m = 1; m == 1 || run > 128; ++m) {
+        const double runs = each * kSms * (double)m / ctas_a_run;
+        run = runs <= 1 ? L : (int)((L + (long long)runs - 1) / (long long)runs);
+        if (runs > L) break;
+    }
+    return run < least ? least : run > 128 ? 128 : run;
+}
+
 template <typename T, int VEC, int W>
 cudaError_t fwd(const ConvDims& d, const ConvArgs& a, cudaStream_t st) {
     const int nv = d.D / VEC;
-    // runs of 32 tokens, shorter while they do not fill the SMs with 512 threads each
-    int run = 32;
-    while (run > 4 && (long long)nv * d.at.rows() * ((d.at.L + run - 1) / run) < 512LL * kSms) run /= 2;
-    const int runs = (d.at.L + run - 1) / run;
+    const int run = run_of(d.at.L, (double)nv * d.at.rows() / 256, 3, 4), runs = (d.at.L + run - 1) / run;
     const long long items = (long long)nv * d.at.rows() * runs;
     const long long all = items + (a.S_final ? (long long)nv * d.at.B * (W - 1) : 0);
     if (all == 0) return cudaSuccess;
@@ -356,8 +421,7 @@ BwdGrid bwd_grid(const ConvDims& d) {
     const int vec = 4;
     const long long cols = (d.D + 32 * vec - 1) / (32 * vec);
     BwdGrid g;
-    g.run = 64;   // shorter while the SMs are not full with 2 CTAs each
-    while (g.run > 8 && cols * d.at.rows() * ((d.at.L + g.run - 1) / g.run) < 2LL * kSms * kBwdWarps) g.run /= 2;
+    g.run = run_of(d.at.L, (double)cols * d.at.rows() / kBwdWarps, 2, 8);
     g.runs = (d.at.L + g.run - 1) / g.run;
     g.nruns = (long long)d.at.rows() * g.runs;
     const long long n = (g.nruns + kBwdWarps - 1) / kBwdWarps;
@@ -411,10 +475,10 @@ bool wide(const ConvDims& d, const ConvArgs& a, int vec, bool step) {
     return ok(a.x, d.xs) && ok(a.y, d.ys) && ok(a.dy, d.dys) && ok(a.dx, d.dxs);
 }
 
-// 8 channels a thread forward and 4 backward (bf16), where rows allow it
+// Four channels a thread where rows allow it (eight bf16, 16 bytes, leave half the threads: 32 registers of weights each)
 template <Which K>
 cudaError_t by_type(const ConvDims& d, const ConvArgs& a, cudaStream_t st) {
-    constexpr int V = K == kBwd ? 4 : 8;
+    constexpr int V = 4;
     if (d.bf16)
         return wide(d, a, V, K == kStep) ? by_taps<K, __nv_bfloat16, V>(d, a, st) : by_taps<K, __nv_bfloat16, 1>(d, a, st);
     return wide(d, a, 4, K == kStep) ? by_taps<K, float, 4>(d, a, st) : by_taps<K, float, 1>(d, a, st);

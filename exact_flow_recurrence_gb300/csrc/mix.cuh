@@ -114,10 +114,9 @@ constexpr float kLog2eF = 1.4426950408889634f;
 // 1 / (1 + e^{-x}): a few 2^-24 of the result
 __device__ __forceinline__ float sigmoid_of(float x) { return rcp(1.f + ex2(-kLog2eF * x)); }
 __device__ __forceinline__ float silu_of(float x) { return x * sigmoid_of(x); }
-// d(x sigmoid(x)) / dx
-__device__ __forceinline__ float dsilu_of(float x) {
-    const float s = sigmoid_of(x);
-    return s * fmaf(x, 1.f - s, 1.f);
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+    const float2 e = mul2(x, both(-kLog2eF)), s = add2(make_float2(ex2(e.x), ex2(e.y)), both(1.f));
+    return make_float2(rcp(s.x), rcp(s.y));
 }
 
 inline bool aligned_rows(const void* p, const long long (&s)[2], int rows, int tokens, int bytes, int es) {

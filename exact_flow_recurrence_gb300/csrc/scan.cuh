@@ -109,6 +109,10 @@ __device__ __forceinline__ float4 steps(const ScanDims& d, float4 raw, int n) {
 }
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 __device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
+__device__ __forceinline__ float4 sigmoid4(float4 x) {
+    const float2 a = sigmoid2(make_float2(x.x, x.y)), b = sigmoid2(make_float2(x.z, x.w));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
 __device__ __forceinline__ float at4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // e^{dt A} from a2 = A log2(e).  ex2.approx gives a little too small a result: -5e-9 of it on average for exponents of

@@ -108,7 +108,7 @@ struct Chunk {
                 const float4 xd = steps(d, add4(as4(vd[j]), bias), n), xu = as4(vu[j]);
                 if (r.z) {
                     const float4 z = as4(vz[j]);
-                    xg = mul4(xg, make_float4(silu_of(z.x), silu_of(z.y), silu_of(z.z), silu_of(z.w)));
+                    xg = mul4(xg, mul4(z, sigmoid4(z)));
                 }
                 *reinterpret_cast<float4*>(dt + o) = in_range ? xd : none;
                 *reinterpret_cast<float4*>(u + o) = in_range ? xu : none;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
                     float4 dd = *reinterpret_cast<const float4*>(ck.dt + o), g = dy;
                     if (r.z) {
                         const float4 z = as4(vz[j]);
-                        const float4 s = make_float4(sigmoid_of(z.x), sigmoid_of(z.y), sigmoid_of(z.z), sigmoid_of(z.w)), f = mul4(z, s);
+                        const float4 s = sigmoid4(z), f = mul4(z, s);
                         // dz = dy (y + skip u) (s + z s (1 - s))
                         const float4 yy = mul4(dy, add4(y, mul4(skip, u)));
                         store4<T, WIDE>((T*)gr.dz + axis * d.dzs[0] + tt * d.dzs[1] + cb.c0 + ec,
@@ -580,8 +580,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
                     }
                     store4<T, WIDE>((T*)gr.du + axis * d.dus[0] + tt * d.dus[1] + cb.c0 + ec, add4(x1, mul4(skip, g)), en);
                     if (d.softplus) {
-                        const float4 raw = add4(as4(vd[j]), bias);
-                        dd = mul4(dd, make_float4(sigmoid_of(raw.x), sigmoid_of(raw.y), sigmoid_of(raw.z), sigmoid_of(raw.w)));
+                        dd = mul4(dd, sigmoid4(add4(as4(vd[j]), bias)));
                     }
                     store4<T, WIDE>((T*)gr.ddelta + axis * d.dds[0] + tt * d.dds[1] + cb.c0 + ec, dd, en);
                     dbias = add4(dbias, dd);

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, Sca
             for (int j = 0; j < Tile::items; ++j) {
                 v[j] = make_float4(fmaf(skip.x, uu[j].x, v[j].x), fmaf(skip.y, uu[j].y, v[j].y), fmaf(skip.z, uu[j].z, v[j].z),
                                    fmaf(skip.w, uu[j].w, v[j].w));
-                if (z) v[j] = mul4(v[j], make_float4(silu_of(g[j].x), silu_of(g[j].y), silu_of(g[j].z), silu_of(g[j].w)));
+                if (z) v[j] = mul4(v[j], mul4(g[j], sigmoid4(g[j])));
             }
 #pragma unroll
             for (int j = 0; j < Tile::items; ++j)
@@ -404,57 +404,151 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, void* y, float* S_final, vo
 }
 
 // ------------------------------------------------------------------- one token
-// A thread takes four states of a channel; S [nslots][D][N].
+// S [nslots][D][N].  Bound by HBM: the states, read and written once.
+//   h <- e^{dt A} h + dt u B of four states, and their part of sum_n C h
+__device__ __forceinline__ float step4(float dt, float u, float2 a0, float2 a1, float4& h, const float4& B, const float4& C) {
+    const float2 du = both(dt * u), h0 = fma2(decay2(both(dt), a0), make_float2(h.x, h.y), mul2(du, make_float2(B.x, B.y))),
+                 h1 = fma2(decay2(both(dt), a1), make_float2(h.z, h.w), mul2(du, make_float2(B.z, B.w)));
+    h = make_float4(h0.x, h0.y, h1.x, h1.y);
+    const float2 s = fma2(make_float2(C.z, C.w), h1, mul2(make_float2(C.x, C.y), h0));
+    return s.x + s.y;
+}
+
+// A thread takes four states of a channel of a sequence; nl lanes a channel, a power of two, so that they lie in one warp.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) k_scan_step(ScanDims d, ScanIn in, float* S, const int* slots, int nslots, T* y, int nl) {
-    // (nl lanes a channel: a power of two, so that they lie in one warp)
-    const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long ch = idx / nl, b = ch / d.D;
-    const int q = (int)(idx % nl) * 4, c = (int)(ch % d.D);
-    float acc = 0.f;
-    const bool in_range = b < d.at.B;
-    long long sl = -1;
-    if (in_range) {
-        sl = slots ? __ldg(slots + b) : b;
-        if (sl >= nslots) sl = -1;
-    }
-    float x = 0.f;
+    const long long idx = (long long)blockIdx.x * 256 + threadIdx.x, ch = idx / nl, b = ch / d.D;
+    const int q = (int)(idx % nl) * 4, c = (int)(ch % d.D), n = min(4, d.N - q);
+    const bool here = b < d.at.B;
+    long long sl = !here ? -1 : slots ? __ldg(slots + b) : b;
+    if (sl >= nslots) sl = -1;
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 h = none, A = none, Bv = none, Cv = none;
+    float u = 0.f, raw = 0.f, acc = 0.f;
+    float* p = S + (sl * d.D + c) * d.N + q;
     if (sl >= 0) {
-        float* p = S + (sl * d.D + c) * d.N + q;
-        const int n = min(4, d.N - q);
-        float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n > 0) h = WIDE ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
-        const int g = c / (d.D / d.G);
-        x = ld_elem((const T*)in.u + b * d.us[0] + c);
-        const float dt = step_of(d, ld_elem((const T*)in.delta + b * d.ds[0] + c) + (in.dbias ? __ldg(in.dbias + c) : 0.f));
         if (n > 0) {
-            const float4 A = load4<float, WIDE>(in.A + (size_t)c * d.N + q, n);
-            const float4 Bv = load4<T, false>((const T*)in.Bm + b * d.bs[0] + g * d.bs[2] + q, n);
-            const float4 Cv = load4<T, false>((const T*)in.C + b * d.cs[0] + g * d.cs[2] + q, n);
-            const float du = dt * x;
-            const float2 a0 = decay2(both(dt), make_float2(A.x * kLog2eF, A.y * kLog2eF)), a1 = decay2(both(dt), make_float2(A.z * kLog2eF, A.w * kLog2eF));
-            h.x = fmaf(a0.x, h.x, du * Bv.x);
-            h.y = fmaf(a0.y, h.y, du * Bv.y);
-            h.z = fmaf(a1.x, h.z, du * Bv.z);
-            h.w = fmaf(a1.y, h.w, du * Bv.w);
-            acc = fmaf(Cv.x, h.x, Cv.y * h.y) + fmaf(Cv.z, h.z, Cv.w * h.w);
-            if (WIDE) {
-                *reinterpret_cast<float4*>(p) = h;
-            } else {
-                p[0] = h.x;
-                if (n > 1) p[1] = h.y;
-                if (n > 2) p[2] = h.z;
-                if (n > 3) p[3] = h.w;
-            }
+            const int g = c / (d.D / d.G);
+            h = WIDE ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+            A = load4<float, WIDE>(in.A + (size_t)c * d.N + q, n);
+            Bv = load4<T, WIDE>((const T*)in.Bm + b * d.bs[0] + g * d.bs[2] + q, n);
+            Cv = load4<T, WIDE>((const T*)in.C + b * d.cs[0] + g * d.cs[2] + q, n);
+        }
+        u = ld_elem((const T*)in.u + b * d.us[0] + c);
+        raw = ld_elem((const T*)in.delta + b * d.ds[0] + c) + (in.dbias ? __ldg(in.dbias + c) : 0.f);
+        acc = step4(step_of(d, raw), u, mul2(make_float2(A.x, A.y), both(kLog2eF)), mul2(make_float2(A.z, A.w), both(kLog2eF)), h, Bv, Cv);
+        if (WIDE) {
+            if (n > 0) *reinterpret_cast<float4*>(p) = h;
+        } else {
+            if (n > 0) p[0] = h.x;
+            if (n > 1) p[1] = h.y;
+            if (n > 2) p[2] = h.z;
+            if (n > 3) p[3] = h.w;
         }
     }
     for (int o = nl / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (!in_range || q) return;
+    if (!here || q) return;
     if (sl >= 0) {
-        if (in.skip) acc = fmaf(__ldg(in.skip + c), x, acc);
+        if (in.skip) acc = fmaf(__ldg(in.skip + c), u, acc);
         if (in.z) acc *= silu_of(ld_elem((const T*)in.z + b * d.zs[0] + c));
     }
     st_elem(y + b * d.ys[0] + c, sl >= 0 ? acc : 0.f);
+}
+
+// A batch: a CTA keeps its channels (16 KB of a state: their A, skip and bias stay in registers) and takes every
+// gridDim.x-th sequence.  States and token rows come by asynchronous copies, kStepStages - 1 sequences ahead, so that what is in
+// flight costs no registers.  N = 4 nl.
+constexpr int kStepStages = 6, kStepFour = 4;   // groups of four states a thread
+template <typename T>
+__global__ void __launch_bounds__(256, 2) k_scan_step_ring(ScanDims d, ScanIn in, float* S, const int* slots, int nslots, T* y, int nl) {
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ int s_slot[kStepStages];
+    const int tid = threadIdx.x, CT = 256 * kStepFour / nl, c0 = blockIdx.y * CT, n = min(CT, d.D - c0), g = c0 / (d.D / d.G);
+    const uint32_t states = 256 * kStepFour * 16, stage = states + (3 * CT + 8 * nl) * (uint32_t)sizeof(T);
+    float2 a0[kStepFour], a1[kStepFour];
+    float bias[kStepFour], skip[kStepFour];
+#pragma unroll
+    for (int i = 0; i < kStepFour; ++i) {
+        const int f = i * 256 + tid, c = f / nl;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        bias[i] = skip[i] = 0.f;
+        if (c < n) {
+            A = __ldg(reinterpret_cast<const float4*>(in.A + (size_t)c0 * d.N) + f);
+            if (in.dbias) bias[i] = __ldg(in.dbias + c0 + c);
+            if (in.skip) skip[i] = __ldg(in.skip + c0 + c);
+        }
+        a0[i] = mul2(make_float2(A.x, A.y), both(kLog2eF));
+        a1[i] = mul2(make_float2(A.z, A.w), both(kLog2eF));
+    }
+    const int count = (d.at.B - (int)blockIdx.x + gridDim.x - 1) / gridDim.x;   // this CTA's sequences
+    const auto place = [&](int k) {
+        const int b = blockIdx.x + k * gridDim.x;
+        return k >= count ? -1 : slots ? __ldg(slots + b) : b;
+    };
+    int next = place(0);
+    const auto issue = [&](int k) {
+        if (k < count) {
+            const long long b = blockIdx.x + (long long)k * gridDim.x;
+            unsigned char* to = ring + (k % kStepStages) * stage;
+            const int sl = next >= 0 && next < nslots ? next : -1;
+            if (tid == 0) s_slot[k % kStepStages] = sl;
+            if (sl >= 0) {
+                const float4* from = reinterpret_cast<const float4*>(S + ((long long)sl * d.D + c0) * d.N);
+#pragma unroll
+                for (int i = 0; i < kStepFour; ++i)
+                    if (i * 256 + tid < n * nl) copy_async(to + (i * 256 + tid) * 16, from + i * 256 + tid, 16);
+                T* rows = reinterpret_cast<T*>(to + states);   // u, delta, z [CT], B, C [4 nl]
+                for (int j = tid; j < 3 * (CT / 4) + 2 * nl; j += 256) {
+                    const int row = j / (CT / 4), at = j % (CT / 4) * 4, e = j - 3 * (CT / 4);
+                    if (e >= 0)
+                        copy_async(rows + j * 4, e < nl ? (const T*)in.Bm + b * d.bs[0] + g * d.bs[2] + 4 * e
+                                                        : (const T*)in.C + b * d.cs[0] + g * d.cs[2] + 4 * (e - nl), 4 * sizeof(T));
+                    else if (at < n && (row < 2 || in.z))
+                        copy_async(rows + j * 4, row == 0 ? (const T*)in.u + b * d.us[0] + c0 + at
+                                                 : row == 1 ? (const T*)in.delta + b * d.ds[0] + c0 + at : (const T*)in.z + b * d.zs[0] + c0 + at,
+                                   4 * sizeof(T));
+                }
+            }
+            next = place(k + 1);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int k = 0; k < kStepStages - 1; ++k) issue(k);
+    for (int k = 0; k < count; ++k) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStepStages - 2) : "memory");
+        __syncthreads();   // (the stage is whole, and the one before it free)
+        issue(k + kStepStages - 1);
+        const long long b = blockIdx.x + (long long)k * gridDim.x;
+        const unsigned char* from = ring + (k % kStepStages) * stage;
+        const T* rows = reinterpret_cast<const T*>(from + states);
+        const int sl = s_slot[k % kStepStages];
+        if (sl < 0) {
+            for (int c = tid; c < n; c += 256) st_elem(y + b * d.ys[0] + c0 + c, 0.f);
+            continue;
+        }
+        const int q = tid % nl;
+        const float4 Bv = as4(*reinterpret_cast<const Vec<T, 4>*>(rows + 3 * CT + 4 * q)),
+                     Cv = as4(*reinterpret_cast<const Vec<T, 4>*>(rows + 3 * CT + 4 * (nl + q)));
+        float4* to = reinterpret_cast<float4*>(S + ((long long)sl * d.D + c0) * d.N);
+        float acc[kStepFour];
+#pragma unroll
+        for (int i = 0; i < kStepFour; ++i) {
+            const int f = i * 256 + tid, c = min(f / nl, n - 1);
+            float4 h = *reinterpret_cast<const float4*>(from + f * 16);
+            acc[i] = step4(step_of(d, (float)rows[CT + c] + bias[i]), (float)rows[c], a0[i], a1[i], h, Bv, Cv);
+            if (f < n * nl) to[f] = h;
+        }
+#pragma unroll
+        for (int i = 0; i < kStepFour; ++i) {
+            const int c = (i * 256 + tid) / nl;
+            for (int o = nl / 2; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+            if (q == 0 && c < n) {
+                acc[i] = fmaf(skip[i], (float)rows[c], acc[i]);
+                if (in.z) acc[i] *= silu_of((float)rows[2 * CT + c]);
+                st_elem(y + b * d.ys[0] + c0 + c, acc[i]);
+            }
+        }
+    }
 }
 
 template <typename T>
@@ -469,12 +563,25 @@ cudaError_t fwd(const ScanDims& d, const ScanIn& in, void* y, float* S_final, vo
 
 template <typename T>
 cudaError_t step(const ScanDims& d, const ScanIn& in, float* S, const int* slots, int nslots, void* y, cudaStream_t st) {
-    const int nl = state_lanes(d.N);
-    const long long n = (long long)d.at.B * d.D * nl;
-    const unsigned grid = (unsigned)((n + 255) / 256);
-    const bool wide = d.N % 4 == 0 && ((uintptr_t)S & 15) == 0 && ((uintptr_t)in.A & 15) == 0;
-    if (wide) k_scan_step<T, true><<<grid, 256, 0, st>>>(d, in, S, slots, nslots, (T*)y, nl);
-    else k_scan_step<T, false><<<grid, 256, 0, st>>>(d, in, S, slots, nslots, (T*)y, nl);
+    const int nl = state_lanes(d.N), es = sizeof(T), B = d.at.B;
+    const long long rows[2] = {d.bs[0], d.bs[2]}, rows_c[2] = {d.cs[0], d.cs[2]};
+    const bool wide = d.N % 4 == 0 && ((uintptr_t)S & 15) == 0 && ((uintptr_t)in.A & 15) == 0 &&
+                      aligned_rows(in.Bm, rows, B, d.G, 4 * es, es) && aligned_rows(in.C, rows_c, B, d.G, 4 * es, es);
+    // the ring: whole groups of four, a tile in one group, and four sequences a CTA at least with two CTAs an SM
+    // (256 x 4096 x 16 bf16: 35 us; element by element, one state group a thread, 53)
+    const int CT = 256 * kStepFour / nl, tiles = (d.D + CT - 1) / CT;
+    const auto ok = [&](const void* p, const long long (&s)[2]) { return !p || aligned_rows(p, s, B, 1, 4 * es, es); };
+    if (wide && d.N == 4 * nl && d.D % 4 == 0 && (d.G == 1 || d.D / d.G % CT == 0) && (long long)tiles * B >= 4 * 2 * kScanSms && tiles <= 2 * kScanSms &&
+        ok(in.u, d.us) && ok(in.delta, d.ds) && ok(in.z, d.zs)) {
+        const size_t smem = kStepStages * (256 * kStepFour * 16 + (size_t)(3 * CT + 8 * nl) * es);
+        const cudaError_t e = cudaFuncSetAttribute(k_scan_step_ring<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        k_scan_step_ring<T><<<dim3(2 * kScanSms / tiles, tiles), 256, smem, st>>>(d, in, S, slots, nslots, (T*)y, nl);
+    } else {
+        const unsigned grid = (unsigned)(((long long)B * d.D * nl + 255) / 256);
+        if (wide) k_scan_step<T, true><<<grid, 256, 0, st>>>(d, in, S, slots, nslots, (T*)y, nl);
+        else k_scan_step<T, false><<<grid, 256, 0, st>>>(d, in, S, slots, nslots, (T*)y, nl);
+    }
     prof_mark("scan_step", st);
     return cudaGetLastError();
 }

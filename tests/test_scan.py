@@ -216,6 +216,35 @@ def test_tokens_one_by_one_are_the_sequence(D, N, G, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,D,N,G", [(255, 1200, 16, 1), (129, 1337, 13, 7), (301, 512, 64, 2), (700, 512, 8, 1), (1300, 96, 4, 3)])
+def test_step_of_a_batch(B, D, N, G, dtype):
+    """Batches that give a CTA several sequences, some CTAs fewer; odd widths."""
+    a = make(B=B, L=1, D=D, N=N, G=G, dtype=dtype)
+    t = on_gpu(a)
+    cache = torch.randn(B + 3, D, N, device=DEV)
+    slots = torch.randperm(B + 3, device=DEV)[:B].int()
+    slots[5] = -1
+    before = cache.clone()
+    one = [t[k][:, 0] for k in ("u", "delta")]
+    y = efla.efla_scan_step(*one, t["A"], t["B_"][:, 0], t["C"][:, 0], cache, t["D"], t["z"][:, 0], t["bias"], slots=slots)
+    efla.efla_get_status()
+    S, keep = before[slots.long().clamp_min(0)], torch.arange(B, device=DEV) != 5
+    u, z, raw = t["u"][:, 0].double(), t["z"][:, 0].double(), t["delta"][:, 0].double() + t["bias"].double()
+    dt = torch.nn.functional.softplus(raw, threshold=50)
+    rep = D // G
+    bm, c = (t[k][:, 0].double().repeat_interleave(rep, 1) for k in ("B_", "C"))
+    h = torch.exp(dt[..., None] * t["A"].double()) * S.double() + (dt * u)[..., None] * bm
+    want = ((h * c).sum(-1) + t["D"].double() * u) * z * torch.sigmoid(z)
+    assert_close("y", y[keep], want[keep], TOL, stored_bf16=dtype == BF)
+    assert float(y[5].abs().max()) == 0.0
+    assert_close("S", cache[slots[keep].long()], h[keep], TOL)
+    rest = torch.ones(B + 3, dtype=torch.bool, device=DEV)
+    rest[slots[keep].long()] = False
+    assert torch.equal(cache[rest], before[rest])
+
+
+@pytest.mark.gpu
 def test_step_skips_places_outside():
     a = make(B=4, L=1, D=24, N=16, state=False)
     t = on_gpu(a)
