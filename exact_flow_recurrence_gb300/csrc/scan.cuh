@@ -3,9 +3,9 @@
 // Channel d keeps N states; with the A, B, C of its group:
 //   dt = softplus(delta + bias)  (or delta + bias),   h <- e^{dt A} h + dt u B,   y = (sum_n C h + skip u) z sigmoid(z)
 //
-// A thread owns four neighbouring channels and four neighbouring states of each: N/4 lanes (rounded up to a
-// power of two, NL) lie side by side along the states, the warp's other lanes along the channels.  Four warps
-// make a CTA: channels of one group, all on the same tokens, which pass through shared memory in tiles:
+// A thread owns two (or four) neighbouring channels, the two halves of its packed instructions, and four neighbouring states
+// of each: N/4 lanes (rounded up to a power of two, NL) lie side by side along the states, the warp's other lanes along
+// the channels.  A CTA has 512 / NL channels of one group, all on the same tokens, which pass through shared memory in tiles:
 // what depends on a channel alone (dt, the gated gradient) is worked out once there.
 // Tokens outside every sequence, and channels and states past the last, are zeros: e^0 h + 0 leaves a state alone.
 #pragma once
@@ -14,14 +14,11 @@
 
 namespace efla {
 
-constexpr int kScanThreads = 128;
-
 // NL: lanes along the states
 template <int NL>
 struct ScanTile {
-    static constexpr int states = 4 * NL;               // states, padded
-    static constexpr int warp_ch = 4 * (32 / NL);       // channels a warp
-    static constexpr int ch = 4 * warp_ch;              // channels a CTA
+    static constexpr int states = 4 * NL;   // padded
+    static constexpr int ch = 512 / NL;     // channels a CTA
 };
 
 // A CTA's channels c0 .. c0 + n - 1, of group g; block `cb` of that group's.
@@ -113,6 +110,8 @@ __device__ __forceinline__ float4 sigmoid4(float4 x) {
     const float2 a = sigmoid2(make_float2(x.x, x.y)), b = sigmoid2(make_float2(x.z, x.w));
     return make_float4(a.x, a.y, b.x, b.y);
 }
+__device__ __forceinline__ float2 lo(const float4& v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi(const float4& v) { return make_float2(v.z, v.w); }
 __device__ __forceinline__ float at4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // e^{dt A} from a2 = A log2(e).  ex2.approx gives a little too small a result: -5e-9 of it on average for exponents of
@@ -136,14 +135,14 @@ __device__ __forceinline__ TokenAt token_at(const Axes& a, int axis, int t, int 
     return TokenAt{(t == s.start ? kFirst : 0) | (t == s.end - 1 ? kLast : 0), s.b};
 }
 
-// The thread's four channels of four states: its place in a warp, and where its values lie.
-template <int NL>
+// The thread's 2 NP channels of four states: its place in a warp, and where its values lie.
+template <int NL, int NP>
 struct ScanLane {
     int nl, cl;      // first state / 4; first channel in the CTA
     __device__ __forceinline__ ScanLane() {
         const int lane = threadIdx.x & 31;
         nl = lane % NL;
-        cl = (threadIdx.x >> 5) * ScanTile<NL>::warp_ch + lane / NL * 4;
+        cl = (threadIdx.x >> 5) * (2 * NP * 32 / NL) + lane / NL * 2 * NP;
     }
     // of x [D][N] fp32: channel i's states, zeros past the last
     __device__ __forceinline__ float4 states(const float* x, const ScanDims& d, const ChBlock& b, int i) const {
@@ -166,42 +165,78 @@ struct ScanLane {
             if (4 * nl + 3 < d.N) p[3] = v.w;
         }
     }
+    // pairs of channels (2 i, 2 i + 1), states 4 nl + n, of x + at (null: zeros), and back
+    __device__ __forceinline__ void pairs(const float* x, size_t at, const ScanDims& d, const ChBlock& b, float2 (&to)[NP][4]) const {
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const float4 p = x ? states(x + at, d, b, 2 * i) : none, q = x ? states(x + at, d, b, 2 * i + 1) : none;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) to[i][n] = make_float2(at4(p, n), at4(q, n));
+        }
+    }
+    __device__ __forceinline__ void put_pairs(float* x, const ScanDims& d, const ChBlock& b, const float2 (&v)[NP][4]) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            put_states(x, d, b, 2 * i, make_float4(v[i][0].x, v[i][1].x, v[i][2].x, v[i][3].x));
+            put_states(x, d, b, 2 * i + 1, make_float4(v[i][0].y, v[i][1].y, v[i][2].y, v[i][3].y));
+        }
+    }
 };
 
-// Sum over a channel's NL lanes of a value for each of the thread's four channels.  Afterwards lane nl < 4 holds
-// the sums of 4 / min(NL, 4) channels from its_channel() on.
-template <int NL>
-__device__ __forceinline__ int its_channel(int nl) { return NL == 1 ? 0 : NL == 2 ? 2 * (nl & 1) : 2 * (nl & 1) + (nl >> 1 & 1); }
-template <int NL>
-__device__ __forceinline__ void sum_states(const float (&v)[4], int nl, float (&out)[NL == 1 ? 4 : NL == 2 ? 2 : 1]) {
+// the four states of the thread's channel i
+template <int NP>
+__device__ __forceinline__ float4 one_of(const float2 (&v)[NP][4], int i) {
+    return i & 1 ? make_float4(v[i / 2][0].y, v[i / 2][1].y, v[i / 2][2].y, v[i / 2][3].y)
+                 : make_float4(v[i / 2][0].x, v[i / 2][1].x, v[i / 2][2].x, v[i / 2][3].x);
+}
+template <int NP>
+__device__ __forceinline__ void set_one(float2 (&v)[NP][4], int i, const float4& x) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) (i & 1 ? v[i / 2][n].y : v[i / 2][n].x) = at4(x, n);
+}
+
+// Sums over a channel's NL lanes of a value for each of the thread's 2 NP channels.  Afterwards the lanes that sums_here()
+// names hold the sums of kSums channels from its_channel() on.
+template <int NL, int NP>
+constexpr int kSums = 2 * NP / (NL < 2 * NP ? NL : 2 * NP);
+template <int NL, int NP>
+__device__ __forceinline__ int its_channel(int nl) {
+    if (NL == 1) return 0;
+    if (NP == 1) return nl & 1;
+    return NL == 2 ? 2 * (nl & 1) : 2 * (nl & 1) + (nl >> 1 & 1);
+}
+template <int NL, int NP>
+__device__ __forceinline__ bool sums_here(int nl) { return nl < 2 * NP; }
+template <int NL, int NP>
+__device__ __forceinline__ void sum_states(const float2 (&v)[NP], int nl, float (&out)[kSums<NL, NP>]) {
     if constexpr (NL == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = v[i];
+        for (int i = 0; i < NP; ++i) {
+            out[2 * i] = v[i].x;
+            out[2 * i + 1] = v[i].y;
+        }
+    } else if constexpr (NP == 1) {
+        const bool b = nl & 1;
+        float z = (b ? v[0].y : v[0].x) + __shfl_xor_sync(0xffffffffu, b ? v[0].x : v[0].y, 1);
+#pragma unroll
+        for (int o = 2; o < NL; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        out[0] = z;
     } else {
         const bool b0 = nl & 1;
-        float z0 = (b0 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[2], 1);
-        float z1 = (b0 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b0 ? v[1] : v[3], 1);
+        const float z0 = (b0 ? v[NP - 1].x : v[0].x) + __shfl_xor_sync(0xffffffffu, b0 ? v[0].x : v[NP - 1].x, 1);
+        const float z1 = (b0 ? v[NP - 1].y : v[0].y) + __shfl_xor_sync(0xffffffffu, b0 ? v[0].y : v[NP - 1].y, 1);
         if constexpr (NL == 2) {
             out[0] = z0;
             out[1] = z1;
         } else {
             const bool b1 = nl & 2;
             float z = (b1 ? z1 : z0) + __shfl_xor_sync(0xffffffffu, b1 ? z0 : z1, 2);
-            if constexpr (NL >= 8) z += __shfl_xor_sync(0xffffffffu, z, 4);
-            if constexpr (NL >= 16) z += __shfl_xor_sync(0xffffffffu, z, 8);
+#pragma unroll
+            for (int o = 4; o < NL; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
             out[0] = z;
         }
     }
-}
-// ... and into row[channel in the CTA]
-template <int NL>
-__device__ __forceinline__ void put_sums(float* row, const ScanLane<NL>& l, const float (&v)[4]) {
-    float o[NL == 1 ? 4 : NL == 2 ? 2 : 1];
-    sum_states<NL>(v, l.nl, o);
-    float* p = row + l.cl + its_channel<NL>(l.nl);
-    if constexpr (NL == 1) *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-    else if constexpr (NL == 2) *reinterpret_cast<float2*>(p) = make_float2(o[0], o[1]);
-    else if (l.nl < 4) *p = o[0];
 }
 
 // The four B and four C of a token

@@ -52,11 +52,17 @@ struct Rows {
 
 constexpr int kBatch = 8;   // tokens of four channels a thread loads at once
 
+// Threads of a CTA of one or two pairs of channels each (NP).  One keeps 128 registers a thread, and with that four warps
+// a scheduler; from 33 states on a warp's sums of dB and dC ask for two.
+constexpr int pairs_of_channels(int lanes) { return lanes == 16 ? 2 : 1; }
+constexpr int threads_of(int lanes) { return 256 / pairs_of_channels(lanes); }
+
 // A chunk in shared memory: dt, u, g [tokens][CH] fp32 (g = dy z sigmoid(z)), B and C as they are stored [tokens][NL][4 and 4],
 // and what its tokens are.
 template <typename T, int NL>
 struct Chunk {
     static constexpr int CH = ScanTile<NL>::ch, S = ScanTile<NL>::states, C = chunk_of(NL);
+    static constexpr int NP = pairs_of_channels(NL), TH = threads_of(NL);
     static constexpr int floats = 3 * C * CH + C * NL * 8 * (int)sizeof(T) / 4;
     float *dt, *u, *g;
     T* bc;
@@ -66,7 +72,7 @@ struct Chunk {
     // tokens ta .. tb-1 (every thread of the CTA; ends with a barrier)
     template <bool WIDE>
     __device__ __forceinline__ void load(const ScanDims& d, const Rows<T>& r, const ChBlock& cb, int axis, int ta, int tb, float4 bias) const {
-        constexpr int V = CH / 4, rows = kScanThreads / V, items = C / rows, batch = items < kBatch ? items : kBatch;
+        constexpr int V = CH / 4, rows = TH / V, items = C / rows, batch = items < kBatch ? items : kBatch;
         const int tid = threadIdx.x, c = tid % V * 4, row = tid / V, n = min(4, cb.n - c);
         const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();   // (the last readers of what was here)
@@ -78,11 +84,11 @@ struct Chunk {
         __syncthreads();
         // (every load of a batch before its first use, and before the first store, which would hold the loads behind it back; tokens
         // past the last read the last one again, and count as zeros)
-        constexpr int groups = 2 * C * NL, bcs = (groups + kScanThreads - 1) / kScanThreads;
+        constexpr int groups = 2 * C * NL, bcs = (groups + TH - 1) / TH;
         Vec<T, 4> vb[bcs];
 #pragma unroll
         for (int j = 0; j < bcs; ++j) {
-            const int e = tid + j * kScanThreads, q = e % NL, t = e / NL % C;
+            const int e = tid + j * TH, q = e % NL, t = e / NL % C;
             vb[j].zero();
             if (e < groups && !(what[t] & kOutside) && 4 * q < d.N)
                 take4<T, WIDE>(vb[j], (e >= C * NL ? r.C + (ta + t) * d.cs[1] : r.Bm + (ta + t) * d.bs[1]) + 4 * q, min(4, d.N - 4 * q));
@@ -119,42 +125,47 @@ struct Chunk {
         for (int j0 = 0; j0 < items; j0 += batch) batch_of(j0);
 #pragma unroll
         for (int j = 0; j < bcs; ++j) {
-            const int e = tid + j * kScanThreads, q = e % NL, t = e / NL % C;
+            const int e = tid + j * TH, q = e % NL, t = e / NL % C;
             if (e < groups) *reinterpret_cast<Vec<T, 4>*>(bc + (t * NL + q) * 8 + (e >= C * NL ? 4 : 0)) = vb[j];
         }
         __syncthreads();
     }
 };
 
-__device__ __forceinline__ float2 lo(const float4& v) { return make_float2(v.x, v.y); }
-__device__ __forceinline__ float2 hi(const float4& v) { return make_float2(v.z, v.w); }
 
 // ------------------------------------------------------------------- every chunk by itself
+// NP values of two channels each, from p on
+template <int NP>
+__device__ __forceinline__ void load_pairs(const float* p, float2 (&to)[NP]) {
+    if constexpr (NP == 1) {
+        to[0] = *reinterpret_cast<const float2*>(p);
+    } else {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        to[0] = lo(v);
+        to[NP - 1] = hi(v);
+    }
+}
 template <typename T, int NL, bool WIDE>
-__global__ void __launch_bounds__(kScanThreads) k_scan_local(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
+__global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
     using Ck = Chunk<T, NL>;
-    constexpr int CH = Ck::CH, S = Ck::S, C = Ck::C;
+    constexpr int CH = Ck::CH, S = Ck::S, C = Ck::C, NP = Ck::NP;
     extern __shared__ __align__(16) float dyn[];
     __shared__ int flags[2 * C];
     const Ck ck(dyn, flags);
     const ChBlock cb = ch_block<NL>(d, blockIdx.y);
     const int axis = blockIdx.z, k = blockIdx.x, ta = k * C, tb = min(ta + C, d.at.L);
-    const ScanLane<NL> l;
+    const ScanLane<NL, NP> l;
     const Rows<T> r(d, in, gr.dy, axis, cb);
-    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
     {
         const int c = threadIdx.x % (CH / 4) * 4;
-        ck.template load<WIDE>(d, r, cb, axis, ta, tb, in.dbias ? load4<float, false>(in.dbias + cb.c0 + c, min(4, cb.n - c)) : none);
+        ck.template load<WIDE>(d, r, cb, axis, ta, tb,
+                               in.dbias ? load4<float, false>(in.dbias + cb.c0 + c, min(4, cb.n - c)) : make_float4(0.f, 0.f, 0.f, 0.f));
     }
-    // pairs of channels (2 i, 2 i + 1), states 4 nl + n
-    float2 a2[2][4], h[2][4], cp[2][4], q[2][4];
-    const auto two = [](const float4& x, const float4& y, float2 (&to)[4]) {
+    float2 a2[NP][4], h[NP][4], cp[NP][4], q[NP][4], dts[NP];
+    l.pairs(in.A, 0, d, cb, a2);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) to[n] = make_float2(at4(x, n), at4(y, n));
-    };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        two(l.states(in.A, d, cb, 2 * i), l.states(in.A, d, cb, 2 * i + 1), a2[i]);
+    for (int i = 0; i < NP; ++i) {
+        dts[i] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             a2[i][n] = mul2(a2[i][n], both(kLog2eF));
@@ -162,7 +173,6 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_local(ScanDims d, ScanIn 
             cp[i][n] = both(1.f);
         }
     }
-    float4 dts = none;
     // whether the state before the chunk, and gradients back to it, still pass
     bool alive = true, open = !(ck.what[0] & kOutside);
 #pragma unroll 2
@@ -171,38 +181,38 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_local(ScanDims d, ScanIn 
         const size_t at = (size_t)ck.seq[t] * d.D * d.N;
         if (w & kFirst) {
             alive = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                two(in.S0 ? l.states(in.S0 + at, d, cb, 2 * i) : none, in.S0 ? l.states(in.S0 + at, d, cb, 2 * i + 1) : none, h[i]);
+            l.pairs(in.S0, at, d, cb, h);
         }
-        const float4 dt = *reinterpret_cast<const float4*>(ck.dt + t * CH + l.cl), u = *reinterpret_cast<const float4*>(ck.u + t * CH + l.cl),
-                     g = *reinterpret_cast<const float4*>(ck.g + t * CH + l.cl);
+        float2 dt[NP], u[NP], g[NP];
+        load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
+        load_pairs<NP>(ck.u + t * CH + l.cl, u);
+        load_pairs<NP>(ck.g + t * CH + l.cl, g);
         Bc<T> bc;
         bc.load(ck.bc + (t * NL + l.nl) * 8, true);
-        dts = add4(dts, dt);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 dt2 = i ? hi(dt) : lo(dt), du2 = mul2(dt2, i ? hi(u) : lo(u)), g2 = i ? hi(g) : lo(g);
+        for (int i = 0; i < NP; ++i) {
+            const float2 du = mul2(dt[i], u[i]);
+            dts[i] = add2(dts[i], dt[i]);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const float2 a = decay2(dt2, a2[i][n]);
-                h[i][n] = fma2(a, h[i][n], mul2(du2, both(bc.bn(n))));
+                const float2 a = decay2(dt[i], a2[i][n]);
+                h[i][n] = fma2(a, h[i][n], mul2(du, both(bc.bn(n))));
                 if (open) {
                     cp[i][n] = mul2(cp[i][n], a);
-                    q[i][n] = fma2(cp[i][n], mul2(g2, both(bc.cn(n))), q[i][n]);
+                    q[i][n] = fma2(cp[i][n], mul2(g[i], both(bc.cn(n))), q[i][n]);
                 }
             }
         }
         if (open && (w & kLast)) {
             open = false;
-            if (gr.dS)
+            if (gr.dS) {
+                float2 f[NP][4];
+                l.pairs(gr.dS, at, d, cb, f);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float2 f[4];
-                    two(l.states(gr.dS + at, d, cb, 2 * i), l.states(gr.dS + at, d, cb, 2 * i + 1), f);
+                for (int i = 0; i < NP; ++i)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) q[i][n] = fma2(cp[i][n], f[n], q[i][n]);
-                }
+                    for (int n = 0; n < 4; ++n) q[i][n] = fma2(cp[i][n], f[i][n], q[i][n]);
+            }
         }
     }
     const size_t at = (size_t)axis * ws.chunks + k;
@@ -211,14 +221,12 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_local(ScanDims d, ScanIn 
         ws.alive[2 * at + 1] = open;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * NP; ++i) {
         if (l.cl + i >= cb.n) continue;
         const size_t ch = at * d.D + cb.c0 + l.cl + i;
-        const float2 *hh = h[i / 2], *qq = q[i / 2];
-        const auto one = [&](const float2& v) { return i & 1 ? v.y : v.x; };
-        *reinterpret_cast<float4*>(ws.ends + ch * S + 4 * l.nl) = make_float4(one(hh[0]), one(hh[1]), one(hh[2]), one(hh[3]));
-        *reinterpret_cast<float4*>(ws.grads + ch * S + 4 * l.nl) = make_float4(one(qq[0]), one(qq[1]), one(qq[2]), one(qq[3]));
-        if (l.nl == 0) ws.dts[ch] = at4(dts, i);
+        *reinterpret_cast<float4*>(ws.ends + ch * S + 4 * l.nl) = one_of<NP>(h, i);
+        *reinterpret_cast<float4*>(ws.grads + ch * S + 4 * l.nl) = one_of<NP>(q, i);
+        if (l.nl == 0) ws.dts[ch] = i & 1 ? dts[i / 2].y : dts[i / 2].x;
     }
 }
 
@@ -294,46 +302,38 @@ struct ChannelSum {
     }
 };
 
-// Shared memory of the gradients: the chunk, the states in front of its subs but the first ([sub][warp][4][lane] float4 of four
-// states each), and room for the first sub's sums.  A sub's sums of dB and dC ([token][2 states] a warp) take the place of
-// the warp's states in front of it.
+// Shared memory of the gradients: the chunk, the states in front of its subs but the first ([sub][warp][2 NP][lane] float4 of
+// four states each), and room for the first sub's sums.  A sub's sums of dB and dC ([token][2 states] a warp) take the place
+// of the warp's states in front of it.
 template <typename T, int NL>
 struct GradSmem {
     using Ck = Chunk<T, NL>;
-    static constexpr int subs = Ck::C / kSub, warp = 4 * 32 * 4;   // floats of a warp's states
-    static constexpr int sums = kSub * 2 * Ck::S;                  // floats of a warp's sums
+    static constexpr int NP = Ck::NP, warps = Ck::TH / 32;
+    static constexpr int subs = Ck::C / kSub, warp = 2 * NP * 32 * 4;   // floats of a warp's states
+    static constexpr int sums = kSub * 2 * Ck::S;                       // floats of a warp's sums
     static_assert(sums <= warp, "a sub's sums fit in its states' place");
-    static constexpr size_t bytes = sizeof(float) * (Ck::floats + (subs - 1) * 4 * warp + 4 * sums);
+    static constexpr size_t bytes = sizeof(float) * (Ck::floats + (subs - 1) * warps * warp + warps * sums);
 };
 
 template <typename T, int NL, bool WIDE>
-__global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
+__global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
     using Ck = Chunk<T, NL>;
     using Sm = GradSmem<T, NL>;
-    constexpr int CH = Ck::CH, S = Ck::S, C = Ck::C, V = CH / 4;
+    constexpr int CH = Ck::CH, S = Ck::S, C = Ck::C, TH = Ck::TH, V = CH / 4, NP = Sm::NP, W = Sm::warps;
     extern __shared__ __align__(16) float dyn[];
     __shared__ int flags[2 * C];
     const Ck ck(dyn, flags);
     float* const place = dyn + Ck::floats;   // of subs 1 .. , then the first sub's sums
     const ChBlock cb = ch_block<NL>(d, blockIdx.y);
-    const ScanLane<NL> l;
+    const ScanLane<NL, NP> l;
     const ChannelSum<NL> cs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const auto sums_of = [&](int sub, int w) { return sub ? place + ((sub - 1) * 4 + w) * Sm::warp : place + (Sm::subs - 1) * 4 * Sm::warp + w * Sm::sums; };
+    const auto sums_of = [&](int sub, int w) { return sub ? place + ((sub - 1) * W + w) * Sm::warp : place + (Sm::subs - 1) * W * Sm::warp + w * Sm::sums; };
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto two = [](const float4& x, const float4& y, float2 (&to)[4]) {
+    float2 a2[NP][4], dA[NP][4];
+    l.pairs(in.A, 0, d, cb, a2);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) to[n] = make_float2(at4(x, n), at4(y, n));
-    };
-    const auto fetch = [&](const float* x, size_t at, float2 (&to)[2][4]) {   // the thread's states of [D][N] at x + at (null: zeros)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) two(x ? l.states(x + at, d, cb, 2 * i) : none, x ? l.states(x + at, d, cb, 2 * i + 1) : none, to[i]);
-    };
-    // pairs of channels (2 i, 2 i + 1), states 4 nl + n
-    float2 a2[2][4], dA[2][4];
-    fetch(in.A, 0, a2);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NP; ++i)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             a2[i][n] = mul2(a2[i][n], both(kLog2eF));
@@ -342,58 +342,66 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
     // what the thread adds up over tokens: channels ec .. ec + 3
     const int ec = threadIdx.x % V * 4, en = min(4, cb.n - ec);
     float4 dskip = none, dbias = none;
-    const float4 skip = in.skip ? load4<float, false>(in.skip + cb.c0 + ec, en) : none;
-    const float4 bias = in.dbias ? load4<float, false>(in.dbias + cb.c0 + ec, en) : none;
     if (gr.dS0 && blockIdx.x == 0)   // empty sequences hand their gradients on
         for (int b = 0; b < d.at.B; ++b) {
             const Seq s = seq_at(d.at, b);
             if (s.end > s.start) continue;
             const size_t at = (size_t)b * d.D * d.N;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) l.put_states(gr.dS0 + at, d, cb, i, gr.dS ? l.states(gr.dS + at, d, cb, i) : none);
+            float2 f[NP][4];
+            l.pairs(gr.dS, at, d, cb, f);
+            l.put_pairs(gr.dS0 + at, d, cb, f);
         }
     const int tasks = d.at.rows() * ws.chunks;
     for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
         const int axis = task / ws.chunks, ta = task % ws.chunks * C, tb = min(ta + C, d.at.L);
         const int subs = (tb - ta + kSub - 1) / kSub;
         const Rows<T> r(d, in, gr.dy, axis, cb);
-        float2 q[2][4], h0[2][4];   // the gradient from behind, and the chunk's entering state
+        const float4 skip = in.skip ? load4<float, false>(in.skip + cb.c0 + ec, en) : none;
+        const float4 bias = in.dbias ? load4<float, false>(in.dbias + cb.c0 + ec, en) : none;
+        float2 q[NP][4], h0[NP][4];   // the gradient from behind, and the chunk's entering state
         {
             const size_t at0 = ((size_t)task * d.D + cb.c0 + l.cl) * S + 4 * l.nl;
-            float4 e[4], f[4];
+            float4 e[2 * NP], f[2 * NP];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * NP; ++i) {
                 const bool in_range = l.cl + i < cb.n;
                 e[i] = in_range ? *reinterpret_cast<const float4*>(ws.ends + at0 + (size_t)i * S) : none;
                 f[i] = in_range ? *reinterpret_cast<const float4*>(ws.grads + at0 + (size_t)i * S) : none;
             }
             ck.template load<WIDE>(d, r, cb, axis, ta, tb, bias);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                two(e[2 * i], e[2 * i + 1], h0[i]);
-                two(f[2 * i], f[2 * i + 1], q[i]);
+            for (int i = 0; i < 2 * NP; ++i) {
+                set_one<NP>(h0, i, e[i]);
+                set_one<NP>(q, i, f[i]);
             }
         }
         // the state behind token t from the one before it
-        const auto advance = [&](int t, float2 (&h)[2][4]) {
-            const float4 dt = *reinterpret_cast<const float4*>(ck.dt + t * CH + l.cl), u = *reinterpret_cast<const float4*>(ck.u + t * CH + l.cl);
+        const auto advance = [&](int t, float2 (&h)[NP][4]) {
+            float2 dt[NP], u[NP];
+            load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
+            load_pairs<NP>(ck.u + t * CH + l.cl, u);
             Bc<T> bc;
             bc.load(ck.bc + (t * NL + l.nl) * 8, false);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 dt2 = i ? hi(dt) : lo(dt), du2 = mul2(dt2, i ? hi(u) : lo(u));
+            for (int i = 0; i < NP; ++i) {
+                const float2 du = mul2(dt[i], u[i]);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) h[i][n] = fma2(decay2(dt2, a2[i][n]), h[i][n], mul2(du2, both(bc.bn(n))));
+                for (int n = 0; n < 4; ++n) h[i][n] = fma2(decay2(dt[i], a2[i][n]), h[i][n], mul2(du, both(bc.bn(n))));
             }
         };
-        const auto enter = [&](int sub, float2 (&h)[2][4]) {   // the state in front of a sub
-            const float4* p = reinterpret_cast<const float4*>(place + ((sub - 1) * 4 + warp) * Sm::warp) + lane;
+        const auto copy = [](float2 (&to)[NP][4], const float2 (&from)[NP][4]) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (sub) two(p[2 * i * 32], p[(2 * i + 1) * 32], h[i]);
-                else
+            for (int i = 0; i < NP; ++i)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) h[i][n] = h0[i][n];
+                for (int n = 0; n < 4; ++n) to[i][n] = from[i][n];
+        };
+        const auto enter = [&](int sub, float2 (&h)[NP][4]) {   // the state in front of a sub
+            if (sub) {
+                const float4* p = reinterpret_cast<const float4*>(place + ((sub - 1) * W + warp) * Sm::warp) + lane;
+#pragma unroll
+                for (int i = 0; i < 2 * NP; ++i) set_one<NP>(h, i, p[i * 32]);
+            } else {
+                copy(h, h0);
             }
         };
         const auto mixed = [&](int sub) {   // whether a sequence begins or ends in a sub
@@ -403,11 +411,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
             return (w & (kFirst | kLast)) != 0;
         };
         {   // the states in front of the subs
-            float2 h[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) h[i][n] = h0[i][n];
+            float2 h[NP][4];
+            copy(h, h0);
 #pragma unroll 1
             for (int sub = 0; sub + 1 < subs; ++sub) {
                 if (!mixed(sub)) {
@@ -417,41 +422,40 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
 #pragma unroll 1
                     for (int e = 0; e < kSub; ++e) {
                         const int t = sub * kSub + e;
-                        if (ck.what[t] & kFirst) fetch(in.S0, (size_t)ck.seq[t] * d.D * d.N, h);
+                        if (ck.what[t] & kFirst) l.pairs(in.S0, (size_t)ck.seq[t] * d.D * d.N, d, cb, h);
                         advance(t, h);
                     }
                 }
-                float4* p = reinterpret_cast<float4*>(place + (sub * 4 + warp) * Sm::warp) + lane;
+                float4* p = reinterpret_cast<float4*>(place + (sub * W + warp) * Sm::warp) + lane;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    p[2 * i * 32] = make_float4(h[i][0].x, h[i][1].x, h[i][2].x, h[i][3].x);
-                    p[(2 * i + 1) * 32] = make_float4(h[i][0].y, h[i][1].y, h[i][2].y, h[i][3].y);
-                }
+                for (int i = 0; i < 2 * NP; ++i) p[i * 32] = one_of<NP>(h, i);
             }
         }
         // token t backwards, from the states behind (h) and in front of it (hp); its results take the place of its inputs:
         // dt s1 of u, the gradient of dt of dt, sum_n C h of g
-        const auto back = [&](int t, float* sums, const float2 (&h)[2][4], const float2 (&hp)[2][4]) {
+        const auto back = [&](int t, float* sums, const float2 (&h)[NP][4], const float2 (&hp)[NP][4]) {
             const int o = t * CH + l.cl;
-            const float4 dt = *reinterpret_cast<const float4*>(ck.dt + o), u = *reinterpret_cast<const float4*>(ck.u + o),
-                         g = *reinterpret_cast<const float4*>(ck.g + o);
+            float2 dt[NP], u[NP], g[NP];
+            load_pairs<NP>(ck.dt + o, dt);
+            load_pairs<NP>(ck.u + o, u);
+            load_pairs<NP>(ck.g + o, g);
             Bc<T> bc;
             bc.load(ck.bc + (t * NL + l.nl) * 8, true);
-            float2 db[4], dc[4], x1[2], x2[2], xy[2];
+            float2 db[4], dc[4], x1[NP], x2[NP], xy[NP];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 dt2 = i ? hi(dt) : lo(dt), du2 = mul2(dt2, i ? hi(u) : lo(u)), g2 = i ? hi(g) : lo(g);
+            for (int i = 0; i < NP; ++i) {
+                const float2 du = mul2(dt[i], u[i]);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const float2 b = both(bc.bn(n)), c = both(bc.cn(n));
-                    const float2 p = fma2(g2, c, q[i][n]);
-                    dc[n] = i ? fma2(g2, h[i][n], dc[n]) : mul2(g2, h[i][n]);
-                    db[n] = i ? fma2(du2, p, db[n]) : mul2(du2, p);
+                    const float2 p = fma2(g[i], c, q[i][n]);
+                    dc[n] = i ? fma2(g[i], h[i][n], dc[n]) : mul2(g[i], h[i][n]);
+                    db[n] = i ? fma2(du, p, db[n]) : mul2(du, p);
                     x1[i] = n ? fma2(p, b, x1[i]) : mul2(p, b);
                     xy[i] = n ? fma2(c, h[i][n], xy[i]) : mul2(c, h[i][n]);
-                    q[i][n] = mul2(p, decay2(dt2, a2[i][n]));
+                    q[i][n] = mul2(p, decay2(dt[i], a2[i][n]));
                     const float2 e = mul2(q[i][n], hp[i][n]);
-                    dA[i][n] = fma2(dt2, e, dA[i][n]);
+                    dA[i][n] = fma2(dt[i], e, dA[i][n]);
                     x2[i] = n ? fma2(a2[i][n], e, x2[i]) : mul2(a2[i][n], e);
                 }
             }
@@ -464,15 +468,13 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
                     const int j = cs.first + i;
                     sums[(j >> 2) * S + 4 * l.nl + (j & 3)] = v[i];
                 }
-            constexpr int K = NL == 1 ? 4 : NL == 2 ? 2 : 1;
-            const float w1[4] = {x1[0].x, x1[0].y, x1[1].x, x1[1].y}, w2[4] = {x2[0].x, x2[0].y, x2[1].x, x2[1].y},
-                        wy[4] = {xy[0].x, xy[0].y, xy[1].x, xy[1].y};
+            constexpr int K = kSums<NL, NP>;
             float s1[K], s2[K], sy[K];
-            sum_states<NL>(w1, l.nl, s1);
-            sum_states<NL>(w2, l.nl, s2);
-            if (r.z) sum_states<NL>(wy, l.nl, sy);
-            if (NL <= 4 || l.nl < 4) {
-                const int first = o + its_channel<NL>(l.nl);
+            sum_states<NL, NP>(x1, l.nl, s1);
+            sum_states<NL, NP>(x2, l.nl, s2);
+            if (r.z) sum_states<NL, NP>(xy, l.nl, sy);
+            if (sums_here<NL, NP>(l.nl)) {
+                const int first = o + its_channel<NL, NP>(l.nl);
 #pragma unroll
                 for (int i = 0; i < K; ++i) {
                     const float dti = ck.dt[first + i], ui = ck.u[first + i];
@@ -486,17 +488,15 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
         for (int sub = subs - 1; sub >= 0; --sub) {
             float* const sums = sums_of(sub, warp);
             const int t0 = sub * kSub;
-            float2 hp[2][4];
+            float2 hp[NP][4];
             enter(sub, hp);
             __syncwarp();   // (the sums take the states' place)
             if (!mixed(sub)) {
-                float2 hs[kSub][2][4];
+                float2 hs[kSub][NP][4];
 #pragma unroll
                 for (int e = 0; e < kSub; ++e) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) hs[e][i][n] = e ? hs[e ? e - 1 : 0][i][n] : hp[i][n];
+                    if (e) copy(hs[e], hs[e ? e - 1 : 0]);
+                    else copy(hs[0], hp);
                     advance(t0 + e, hs[e]);
                 }
 #pragma unroll
@@ -507,47 +507,37 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
                 for (int e = kSub - 1; e >= 0; --e) {
                     const int t = t0 + e, w = ck.what[t];
                     const size_t at = (size_t)ck.seq[t] * d.D * d.N;
-                    float2 h[2][4], before[2][4];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) h[i][n] = hp[i][n];
+                    float2 h[NP][4], before[NP][4];
+                    copy(h, hp);
 #pragma unroll 1
                     for (int f = 0; f <= e; ++f) {
-                        if (ck.what[t0 + f] & kFirst) fetch(in.S0, (size_t)ck.seq[t0 + f] * d.D * d.N, h);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) before[i][n] = h[i][n];
+                        if (ck.what[t0 + f] & kFirst) l.pairs(in.S0, (size_t)ck.seq[t0 + f] * d.D * d.N, d, cb, h);
+                        copy(before, h);
                         advance(t0 + f, h);
                     }
-                    if (w & kLast) fetch(gr.dS, at, q);
+                    if (w & kLast) l.pairs(gr.dS, at, d, cb, q);
                     back(t, sums + e * 2 * S, h, before);
                     if (w & kFirst) {
+                        if (gr.dS0) l.put_pairs(gr.dS0 + at, d, cb, q);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (gr.dS0) {
-                                l.put_states(gr.dS0 + at, d, cb, 2 * i, make_float4(q[i][0].x, q[i][1].x, q[i][2].x, q[i][3].x));
-                                l.put_states(gr.dS0 + at, d, cb, 2 * i + 1, make_float4(q[i][0].y, q[i][1].y, q[i][2].y, q[i][3].y));
-                            }
+                        for (int i = 0; i < NP; ++i)
 #pragma unroll
                             for (int n = 0; n < 4; ++n) q[i][n] = make_float2(0.f, 0.f);
-                        }
                     }
                 }
             }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < subs * kSub * 2 * S; i += kScanThreads) {
+        for (int i = threadIdx.x; i < subs * kSub * 2 * S; i += TH) {
             const int t = i / (2 * S), j = i % (2 * S), at = (t % kSub) * 2 * S + j;
             if (ck.what[t] & kOutside) continue;
             float v = sums_of(t / kSub, 0)[at];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) v += sums_of(t / kSub, w)[at];
+            for (int w = 1; w < W; ++w) v += sums_of(t / kSub, w)[at];
             ws.bc[((((size_t)cb.cb * d.at.rows() + axis) * d.at.L + ta + t) * d.G + cb.g) * 2 * S + j] = v;
         }
         if (en > 0) {
-            constexpr int rows = kScanThreads / V, items = C / rows, batch = items < kBatch ? items : kBatch;
+            constexpr int rows = TH / V, items = C / rows, batch = items < kBatch ? items : kBatch;
 #pragma unroll
             for (int j0 = 0; j0 < items; j0 += batch) {
                 Vec<T, 4> vd[batch], vu[batch], vg[batch], vz[batch];
@@ -592,20 +582,17 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_grad(ScanDims d, ScanI
     // the CTA's sums over its tokens
     float* out = ws.ch + blockIdx.x * ch_stride(d, S);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (l.cl + i < cb.n)
-            *reinterpret_cast<float4*>(out + (size_t)(cb.c0 + l.cl + i) * S + 4 * l.nl) =
-                i & 1 ? make_float4(dA[i / 2][0].y, dA[i / 2][1].y, dA[i / 2][2].y, dA[i / 2][3].y)
-                      : make_float4(dA[i / 2][0].x, dA[i / 2][1].x, dA[i / 2][2].x, dA[i / 2][3].x);
+    for (int i = 0; i < 2 * NP; ++i)
+        if (l.cl + i < cb.n) *reinterpret_cast<float4*>(out + (size_t)(cb.c0 + l.cl + i) * S + 4 * l.nl) = one_of<NP>(dA, i);
     __syncthreads();
     float4* red = reinterpret_cast<float4*>(dyn);
     red[threadIdx.x] = dskip;
-    red[kScanThreads + threadIdx.x] = dbias;
+    red[TH + threadIdx.x] = dbias;
     __syncthreads();
     if (threadIdx.x < V) {
-        for (int k = 1; k < kScanThreads / V; ++k) {
+        for (int k = 1; k < TH / V; ++k) {
             dskip = add4(dskip, red[k * V + threadIdx.x]);
-            dbias = add4(dbias, red[kScanThreads + k * V + threadIdx.x]);
+            dbias = add4(dbias, red[TH + k * V + threadIdx.x]);
         }
         float* p = out + (size_t)d.D * S + cb.c0 + ec;
 #pragma unroll
@@ -690,7 +677,7 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const S
         constexpr size_t smem = sizeof(float) * Chunk<T, NL>::floats;
         const auto local = k_scan_local<T, NL, WIDE>;
         if ((e = cudaFuncSetAttribute(local, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-        local<<<dim3(ws.chunks, blocks, rows), kScanThreads, smem, st>>>(d, in, g, ws);
+        local<<<dim3(ws.chunks, blocks, rows), threads_of(NL), smem, st>>>(d, in, g, ws);
         prof_mark("scan_local", st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         k_scan_chain<<<dim3((unsigned)(((long long)d.D * NL + 127) / 128), 2, rows), 128, 0, st>>>(d, in.A, ws, NL);
@@ -699,7 +686,7 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const S
     }
     const auto grad = k_scan_grad<T, NL, WIDE>;
     if ((e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sm::bytes)) != cudaSuccess) return e;
-    grad<<<dim3(ws.gx, blocks), kScanThreads, Sm::bytes, st>>>(d, in, g, ws);
+    grad<<<dim3(ws.gx, blocks), threads_of(NL), Sm::bytes, st>>>(d, in, g, ws);
     prof_mark("scan_grad", st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long n = (long long)rows * d.at.L * d.G * 2 * Tile::states;

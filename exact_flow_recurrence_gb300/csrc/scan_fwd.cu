@@ -20,7 +20,8 @@ struct Segments {
     int* alive;
 };
 
-constexpr int kCarry = 256, kBring = 256;   // threads that carry states, and that bring tokens
+// Pairs of channels a thread that carries states; those threads; and those that bring tokens, in kGroups groups that take turns
+constexpr int kNP = 2, kCarry = 256 / kNP, kBring = 128, kGroups = 2;
 
 // Named barriers of a CTA: a buffer filled, and a buffer's states done.
 __device__ __forceinline__ void bar_wait(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kCarry + kBring) : "memory"); }
@@ -31,9 +32,9 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
 }
 
-// Tiles of TT tokens.  Two buffers: (dt, dt, dt u, dt u) of two channels [TT][CH / 2], y [TT][CH], and (B, C) of four states as
-// they are stored [TT][NL]; and a ring of kRing raw tiles.
-constexpr int kRing = 4, kWhat = 4;
+// Tiles of TT tokens.  kBuffers buffers: (dt, dt, dt u, dt u) of two channels [TT][CH / 2], y [TT][CH], and (B, C) of four states as
+// they are stored [TT][NL]; and for each group a ring of raw tiles.
+constexpr int kBuffers = 4, kWhat = 8;
 template <typename T, int NL, bool PART>
 struct FwdTile {
     static constexpr int CH = ScanTile<NL>::ch, S = ScanTile<NL>::states;
@@ -45,14 +46,16 @@ struct FwdTile {
     static constexpr int y_at = TT * CH * 2, bc_at = y_at + (PART ? 0 : TT * CH);  // floats
     static constexpr int buffer = bc_at + TT * NL * 8 * (int)sizeof(T) / 4;
     static constexpr int slot = (items * arrays + bc_items) * kBring;              // Vec<T, 4>
-    static constexpr size_t bytes = 2 * buffer * sizeof(float) + kRing * slot * sizeof(Vec<T, 4>);
+    static constexpr int ring = sizeof(T) == 2 ? 3 : 2;
+    static constexpr size_t bytes = kBuffers * buffer * sizeof(float) + kGroups * ring * slot * sizeof(Vec<T, 4>);
 };
 
 // Warps 0 .. 7 carry the states, two neighbouring channels of four states a thread (the two channels in one instruction's
-// halves); the other warps bring the tokens (asynchronous copies, kRing tiles ahead), work out dt and dt u for them, and
-// finish the y that they left: skip, gate, store.
+// halves); the other warps bring the tokens (asynchronous copies, some tiles ahead), work out dt and dt u for them, and
+// finish the y that they left: skip, gate, store.  Both sides are chains of short steps; four buffers and two groups of
+// the latter, a tile each in turn, keep either from waiting for the other.
 template <typename T, int NL, bool WIDE, bool PART>
-__global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, ScanIn in, T* y, float* S_final, Segments sg) {
+__global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanDims d, ScanIn in, T* y, float* S_final, Segments sg) {
     using Tile = FwdTile<T, NL, PART>;
     using V = Vec<T, 4>;
     constexpr int CH = Tile::CH, S = Tile::S, TT = Tile::TT;
@@ -61,16 +64,16 @@ __global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, Sca
     const ChBlock cb = ch_block<NL>(d, blockIdx.y);
     const int axis = blockIdx.z, k = blockIdx.x, ta = k * sg.seg, tb = min(ta + sg.seg, d.at.L);
     const int tiles = (tb - ta + TT - 1) / TT;
-    const auto buffer = [&](int i) { return dyn + (i & 1) * Tile::buffer; };
+    const auto buffer = [&](int i) { return dyn + (i % kBuffers) * Tile::buffer; };
     if (threadIdx.x >= kCarry) {
-        const int tid = threadIdx.x - kCarry;
+        const int group = (threadIdx.x - kCarry) / kBring, tid = (threadIdx.x - kCarry) % kBring;
         const T* u = (const T*)in.u + axis * d.us[0] + cb.c0;
         const T* delta = (const T*)in.delta + axis * d.ds[0] + cb.c0;
         const T* z = in.z ? (const T*)in.z + axis * d.zs[0] + cb.c0 : nullptr;
         const T* Bm = (const T*)in.Bm + axis * d.bs[0] + cb.g * d.bs[2];
         const T* C = (const T*)in.C + axis * d.cs[0] + cb.g * d.cs[2];
         if (!PART) y += axis * d.ys[0] + cb.c0;
-        V* raw = reinterpret_cast<V*>(dyn + 2 * Tile::buffer) + tid;
+        V* raw = reinterpret_cast<V*>(dyn + kBuffers * Tile::buffer) + group * Tile::ring * Tile::slot + tid;
         // its channels c .. c + n - 1 (n <= 4), and tokens row, row + rows, .. of a tile
         constexpr int rows = kBring / (CH / 4);
         const int c = tid % (CH / 4) * 4, row = tid / (CH / 4), n = row < TT ? min(4, cb.n - c) : 0;
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, Sca
         };
         const auto issue = [&](int i) {   // tile i into its slot
             if (i < tiles) {
-                V* slot = raw + (i % kRing) * Tile::slot;
+                V* slot = raw + (i / kGroups % Tile::ring) * Tile::slot;
                 const int t0 = ta + i * TT;
                 if (n > 0)
 #pragma unroll
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, Sca
             return make_float4(f[0], f[1], f[2], f[3]);
         };
         const auto fill = [&](int i) {
-            const V* slot = raw + (i % kRing) * Tile::slot;
+            const V* slot = raw + (i / kGroups % Tile::ring) * Tile::slot;
             float* const s_dd = buffer(i);
             T* const s_bc = reinterpret_cast<T*>(s_dd + Tile::bc_at);
             const int* w = what[i % kWhat];
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, Sca
             }
         };
         const auto finish = [&](int i) {
-            const V* slot = raw + (i % kRing) * Tile::slot;
+            const V* slot = raw + (i / kGroups % Tile::ring) * Tile::slot;
             const float* s_y = buffer(i) + Tile::y_at;
             if (n <= 0) return;
             float4 v[Tile::items], uu[Tile::items], g[Tile::items];
@@ -185,135 +188,144 @@ __global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, Sca
             for (int j = 0; j < Tile::items; ++j)
                 if (in_range[j]) store4<T, WIDE>(y + (long long)(ta + i * TT + row + j * rows) * d.ys[1] + c, v[j], n);
         };
-        for (int i = 0; i < kRing; ++i) issue(i);
-        look(0);
-        look(1);
-        asm volatile("bar.sync 5, %0;" ::"n"(kBring) : "memory");
-        for (int i = 0; i < tiles; ++i) {
-            // tile i is group i, and i + 2 is the last one under way (a thread reads only what it copied itself)
-            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+        for (int j = 0; j < Tile::ring; ++j) issue(group + j * kGroups);
+        look(group);
+        look(group + kGroups);
+        asm volatile("bar.sync %0, %1;" ::"r"(9 + group), "n"(kBring) : "memory");
+        int last = -1;
+        for (int i = group; i < tiles; last = i, i += kGroups) {
+            // the group's tile n is its copies' group n, and n + ring - 2 is the last one under way (a thread reads only what it
+            // copied itself)
+            asm volatile("cp.async.wait_group %0;" ::"n"(Tile::ring - 2) : "memory");
             fill(i);
-            bar_arrive(1 + (i & 1));
-            if (i > 0) {
-                look(i + 1);   // (the others read it behind the next barrier; its slot's last readers are behind the one before)
-                bar_wait(3 + ((i - 1) & 1));
-                if (!PART) finish(i - 1);
-                issue(i - 1 + kRing);
+            bar_arrive(1 + i % kBuffers);
+            if (last >= 0) {
+                look(i + kGroups);   // (the others read it behind the next barrier; its slot's last readers are behind the one before)
+                bar_wait(1 + kBuffers + last % kBuffers);
+                if (!PART) finish(last);
+                issue(last + Tile::ring * kGroups);
             }
         }
-        bar_wait(3 + ((tiles - 1) & 1));
-        if (!PART) finish(tiles - 1);
+        if (last >= 0) {
+            bar_wait(1 + kBuffers + last % kBuffers);
+            if (!PART) finish(last);
+        }
         return;
     }
-    // channels cl and cl + 1, states 4 nl .. 4 nl + 3 of the padded ones
-    const int lane = threadIdx.x & 31;
-    ScanLane<NL> l;
-    l.nl = lane % NL;
-    l.cl = (threadIdx.x >> 5) * (64 / NL) + lane / NL * 2;
-    float2 a2[4], h[4];
-    const auto two = [](const float4& x, const float4& y, float2 (&to)[4]) {
+    constexpr int NP = kNP;
+    const ScanLane<NL, NP> l;
+    float2 a2[NP][4], h[NP][4];
+    l.pairs(in.A, 0, d, cb, a2);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) to[n] = make_float2(at4(x, n), at4(y, n));
-    };
-    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto set_states = [&](const float* S0, size_t at) {
-        if (S0) two(l.states(S0 + at, d, cb, 0), l.states(S0 + at, d, cb, 1), h);
-        else two(none, none, h);
-    };
-    const auto put_states = [&](float* to) {
-        l.put_states(to, d, cb, 0, make_float4(h[0].x, h[1].x, h[2].x, h[3].x));
-        l.put_states(to, d, cb, 1, make_float4(h[0].y, h[1].y, h[2].y, h[3].y));
-    };
-    two(l.states(in.A, d, cb, 0), l.states(in.A, d, cb, 1), a2);
+    for (int j = 0; j < NP; ++j)
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        a2[n] = mul2(a2[n], both(kLog2eF));
-        h[n] = make_float2(0.f, 0.f);
-    }
-    if (!PART)   // the state that this segment starts from
-        for (int j = 0; j < k; ++j) {
-            const size_t at = (size_t)axis * sg.count + j, ch = at * d.D + cb.c0 + l.cl;
-            const bool alive = sg.alive[at], in0 = l.cl < cb.n, in1 = l.cl + 1 < cb.n;
-            float2 e[4];
-            two(in0 ? *reinterpret_cast<const float4*>(sg.ends + ch * S + 4 * l.nl) : none,
-                in1 ? *reinterpret_cast<const float4*>(sg.ends + (ch + 1) * S + 4 * l.nl) : none, e);
-            const float2 sum = make_float2(in0 ? sg.dts[ch] : 0.f, in1 ? sg.dts[ch + 1] : 0.f);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float2 x = mul2(a2[n], sum);
-                h[n] = alive ? fma2(make_float2(ex2(x.x), ex2(x.y)), h[n], e[n]) : e[n];
-            }
+        for (int n = 0; n < 4; ++n) {
+            a2[j][n] = mul2(a2[j][n], both(kLog2eF));
+            h[j][n] = make_float2(0.f, 0.f);
         }
-    // empty sequences hand their states on
-    if (!PART && S_final && d.at.packed && k == 0) {
-        float2 keep[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) keep[n] = h[n];
+    if (!PART && S_final && d.at.packed && k == 0)   // empty sequences hand their states on
         for (int b = 0; b < d.at.B; ++b) {
             const Seq s = seq_at(d.at, b);
             if (s.end > s.start) continue;
             const size_t at = (size_t)b * d.D * d.N;
-            set_states(in.S0, at);
-            put_states(S_final + at);
+            float2 keep[NP][4];
+            l.pairs(in.S0, at, d, cb, keep);
+            l.put_pairs(S_final + at, d, cb, keep);
         }
+    if (!PART)   // the state that this segment starts from
+        for (int j = 0; j < k; ++j) {
+            const size_t at = (size_t)axis * sg.count + j;
+            const bool alive = sg.alive[at];
+            const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) h[n] = keep[n];
-    }
-    float2 dts = make_float2(0.f, 0.f);
+            for (int i = 0; i < NP; ++i) {
+                const size_t ch = at * d.D + cb.c0 + l.cl + 2 * i;
+                const bool in0 = l.cl + 2 * i < cb.n, in1 = l.cl + 2 * i + 1 < cb.n;
+                const float4 e0 = in0 ? *reinterpret_cast<const float4*>(sg.ends + ch * S + 4 * l.nl) : none,
+                             e1 = in1 ? *reinterpret_cast<const float4*>(sg.ends + (ch + 1) * S + 4 * l.nl) : none;
+                const float2 sum = make_float2(in0 ? sg.dts[ch] : 0.f, in1 ? sg.dts[ch + 1] : 0.f);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 x = mul2(a2[i][n], sum), e = make_float2(at4(e0, n), at4(e1, n));
+                    h[i][n] = alive ? fma2(make_float2(ex2(x.x), ex2(x.y)), h[i][n], e) : e;
+                }
+            }
+        }
+    float2 dts[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) dts[j] = make_float2(0.f, 0.f);
     bool alive = true;
     for (int i = 0; i < tiles; ++i) {
         const float* const s_dd = buffer(i) + l.cl * 2;
         const T* const s_bc = reinterpret_cast<const T*>(buffer(i) + Tile::bc_at) + l.nl * 8;
         float* const s_y = buffer(i) + Tile::y_at;
-        bar_wait(1 + (i & 1));
+        bar_wait(1 + i % kBuffers);
         // what KT tokens read, and the tokens: a store holds back the loads behind it, so that the next tokens' are loaded before
         const auto load = [&](int t, auto& dd, auto& bc, auto kt) {
 #pragma unroll
             for (int e = 0; e < decltype(kt)::value; ++e) {
-                dd[e] = *reinterpret_cast<const float4*>(s_dd + (t + e) * CH * 2);
+#pragma unroll
+                for (int j = 0; j < NP; ++j) dd[e][j] = *reinterpret_cast<const float4*>(s_dd + (t + e) * CH * 2 + 4 * j);
                 bc[e].load(s_bc + (t + e) * NL * 8, !PART);
             }
         };
         const auto tokens = [&](int t, const auto& dd, const auto& bc, auto kt) {
             constexpr int KT = decltype(kt)::value;
-            float2 out[KT];
+            float2 out[KT][NP];
 #pragma unroll
             for (int e = 0; e < KT; ++e) {
-                const float2 dt = make_float2(dd[e].x, dd[e].y), du = make_float2(dd[e].z, dd[e].w);
+                float2 dt[NP], du[NP];
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    dt[j] = lo(dd[e][j]);
+                    du[j] = hi(dd[e][j]);
+                    if (PART) dts[j] = add2(dts[j], dt[j]);
+                }
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    h[n] = fma2(decay2(dt, a2[n]), h[n], mul2(du, both(bc[e].bn(n))));
-                    if (!PART) out[e] = n ? fma2(both(bc[e].cn(n)), h[n], out[e]) : mul2(both(bc[e].cn(n)), h[n]);
+                    const float2 b = both(bc[e].bn(n)), c = PART ? b : both(bc[e].cn(n));
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        h[j][n] = fma2(decay2(dt[j], a2[j][n]), h[j][n], mul2(du[j], b));
+                        if (!PART) out[e][j] = n ? fma2(c, h[j][n], out[e][j]) : mul2(c, h[j][n]);
+                    }
                 }
-                if (PART) dts = add2(dts, dt);
             }
             if constexpr (PART) {
             } else if constexpr (KT == 4 && NL >= 4) {   // lane nl < 4 gets the sums of token t + nl
                 const bool b0 = l.nl & 1, b1 = l.nl & 2;
-                float2 z[2];
                 const auto add_other = [](float2 keep, float2 give, int mask) {
                     return make_float2(keep.x + __shfl_xor_sync(0xffffffffu, give.x, mask), keep.y + __shfl_xor_sync(0xffffffffu, give.y, mask));
                 };
+                float2 s[NP];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) z[e] = add_other(b1 ? out[e + 2] : out[e], b1 ? out[e] : out[e + 2], 2);
-                float2 s = add_other(b0 ? z[1] : z[0], b0 ? z[0] : z[1], 1);
-                if constexpr (NL >= 8) s = add_other(s, s, 4);
-                if constexpr (NL >= 16) s = add_other(s, s, 8);
-                if (NL == 4 || l.nl < 4) *reinterpret_cast<float2*>(s_y + (t + (l.nl & 3)) * CH + l.cl) = s;
+                for (int j = 0; j < NP; ++j) {
+                    float2 z[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) z[e] = add_other(b1 ? out[e + 2][j] : out[e][j], b1 ? out[e][j] : out[e + 2][j], 2);
+                    s[j] = add_other(b0 ? z[1] : z[0], b0 ? z[0] : z[1], 1);
+                    if constexpr (NL >= 8) s[j] = add_other(s[j], s[j], 4);
+                    if constexpr (NL >= 16) s[j] = add_other(s[j], s[j], 8);
+                }
+                if (NL == 4 || l.nl < 4)
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) *reinterpret_cast<float2*>(s_y + (t + (l.nl & 3)) * CH + l.cl + 2 * j) = s[j];
             } else {
 #pragma unroll
-                for (int e = 0; e < KT; ++e) {
-                    float2 s = out[e];
+                for (int e = 0; e < KT; ++e)
 #pragma unroll
-                    for (int o = 1; o < NL; o <<= 1)
-                        s = make_float2(s.x + __shfl_xor_sync(0xffffffffu, s.x, o), s.y + __shfl_xor_sync(0xffffffffu, s.y, o));
-                    if (l.nl == 0) *reinterpret_cast<float2*>(s_y + (t + e) * CH + l.cl) = s;
-                }
+                    for (int j = 0; j < NP; ++j) {
+                        float2 s = out[e][j];
+#pragma unroll
+                        for (int o = 1; o < NL; o <<= 1)
+                            s = make_float2(s.x + __shfl_xor_sync(0xffffffffu, s.x, o), s.y + __shfl_xor_sync(0xffffffffu, s.y, o));
+                        if (l.nl == 0) *reinterpret_cast<float2*>(s_y + (t + e) * CH + l.cl + 2 * j) = s;
+                    }
             }
         };
         if (!any[i % kWhat]) {
             constexpr std::integral_constant<int, 4> four{};
-            float4 dd[2][4];
+            float4 dd[2][4][NP];
             Bc<T> bc[2][4];
             load(0, dd[0], bc[0], four);
 #pragma unroll
@@ -328,38 +340,39 @@ __global__ void __launch_bounds__(kCarry + kBring, 1) k_scan_fwd(ScanDims d, Sca
                 const size_t at = (size_t)seq[i % kWhat][t] * d.D * d.N;
                 if (w & kFirst) {
                     alive = false;
-                    set_states(in.S0, at);
+                    l.pairs(in.S0, at, d, cb, h);
                 }
                 constexpr std::integral_constant<int, 1> one{};
-                float4 dd[1];
+                float4 dd[1][NP];
                 Bc<T> bc[1];
                 load(t, dd, bc, one);
                 tokens(t, dd, bc, one);
-                if (!PART && S_final && (w & kLast)) put_states(S_final + at);
+                if (!PART && S_final && (w & kLast)) l.put_pairs(S_final + at, d, cb, h);
             }
         }
-        bar_arrive(3 + (i & 1));
+        bar_arrive(1 + kBuffers + i % kBuffers);
     }
     if (PART) {
-        const size_t at = (size_t)axis * sg.count + k, ch = at * d.D + cb.c0 + l.cl;
+        const size_t at = (size_t)axis * sg.count + k;
         if (threadIdx.x == 0 && blockIdx.y == 0) sg.alive[at] = alive;
-        if (l.cl < cb.n) {
-            *reinterpret_cast<float4*>(sg.ends + ch * S + 4 * l.nl) = make_float4(h[0].x, h[1].x, h[2].x, h[3].x);
-            if (l.nl == 0) sg.dts[ch] = dts.x;
-        }
-        if (l.cl + 1 < cb.n) {
-            *reinterpret_cast<float4*>(sg.ends + (ch + 1) * S + 4 * l.nl) = make_float4(h[0].y, h[1].y, h[2].y, h[3].y);
-            if (l.nl == 0) sg.dts[ch + 1] = dts.y;
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i) {
+            if (l.cl + i >= cb.n) continue;
+            const size_t ch = at * d.D + cb.c0 + l.cl + i;
+            *reinterpret_cast<float4*>(sg.ends + ch * S + 4 * l.nl) = one_of<NP>(h, i);
+            if (l.nl == 0) sg.dts[ch] = i & 1 ? dts[i / 2].y : dts[i / 2].x;
         }
     }
 }
 
-// Segments of a forward pass: one, unless four-warp CTAs of whole sequences leave most SMs idle.
+// Segments of a forward pass: one, unless CTAs of whole sequences (one an SM) leave a third of the SMs idle.  Two launches take
+// 1.6 times the work of one.
 int segments(const ScanDims& d, int ch, int* seg) {
     const long long ctas = (long long)ch_blocks(d, ch) * d.at.rows();
     int count = 1;
     if (ctas < 96 && d.at.L >= 256) {
-        count = (int)((2 * kScanSms + ctas - 1) / ctas);
+        count = (int)(kScanSms / ctas);
+        if (count < 3) count = (int)(2 * kScanSms / ctas);
         count = count < 32 ? count : 32;
         count = count < d.at.L / 64 ? count : d.at.L / 64;
     }
@@ -394,11 +407,11 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, void* y, float* S_final, vo
     if (sg.count > 1) {
         e = cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Part::bytes);
         if (e != cudaSuccess) return e;
-        part<<<dim3(sg.count - 1, grid.y, grid.z), kCarry + kBring, Part::bytes, st>>>(d, in, nullptr, nullptr, sg);
+        part<<<dim3(sg.count - 1, grid.y, grid.z), kCarry + kGroups * kBring, Part::bytes, st>>>(d, in, nullptr, nullptr, sg);
         prof_mark("scan_part", st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    whole<<<grid, kCarry + kBring, Whole::bytes, st>>>(d, in, (T*)y, S_final, sg);
+    whole<<<grid, kCarry + kGroups * kBring, Whole::bytes, st>>>(d, in, (T*)y, S_final, sg);
     prof_mark("scan_fwd", st);
     return cudaGetLastError();
 }
