@@ -52,23 +52,22 @@ struct Rows {
 
 constexpr int kBatch = 8;   // tokens of four channels a thread loads at once
 
-// Threads of a CTA of one or two pairs of channels each (NP).  One keeps 128 registers a thread, and with that four warps
-// a scheduler; from 33 states on a warp's sums of dB and dC ask for two.
-constexpr int pairs_of_channels(int lanes) { return lanes == 16 ? 2 : 1; }
-constexpr int threads_of(int lanes) { return 256 / pairs_of_channels(lanes); }
+// Pairs of channels a thread.  (One pair, in twice the threads of half the registers, adds up over channels twice as often:
+// B4 L4096 D2048 N16 takes 1.01 ms so, 0.96 with two.)
+constexpr int kNP = 2;
 
-// A chunk in shared memory: dt, u, g [tokens][CH] fp32 (g = dy z sigmoid(z)), B and C as they are stored [tokens][NL][4 and 4],
+// A chunk in shared memory: dt, u, g [tokens][CH] fp32 (g = dy z sigmoid(z)), B and C [tokens][NL][4 and 4] fp32,
 // and what its tokens are.
 template <typename T, int NL>
 struct Chunk {
     static constexpr int CH = ScanTile<NL>::ch, S = ScanTile<NL>::states, C = chunk_of(NL);
-    static constexpr int NP = pairs_of_channels(NL), TH = threads_of(NL);
-    static constexpr int floats = 3 * C * CH + C * NL * 8 * (int)sizeof(T) / 4;
+    static constexpr int NP = kNP, TH = 256 / NP;
+    static constexpr int floats = 3 * C * CH + C * NL * 8;
     float *dt, *u, *g;
-    T* bc;
+    float* bc;
     int *what, *seq;    // [C]
     __device__ __forceinline__ Chunk(float* base, int* flags)
-        : dt(base), u(base + C * CH), g(base + 2 * C * CH), bc(reinterpret_cast<T*>(base + 3 * C * CH)), what(flags), seq(flags + C) {}
+        : dt(base), u(base + C * CH), g(base + 2 * C * CH), bc(base + 3 * C * CH), what(flags), seq(flags + C) {}
     // tokens ta .. tb-1 (every thread of the CTA; ends with a barrier)
     template <bool WIDE>
     __device__ __forceinline__ void load(const ScanDims& d, const Rows<T>& r, const ChBlock& cb, int axis, int ta, int tb, float4 bias) const {
@@ -126,7 +125,7 @@ struct Chunk {
 #pragma unroll
         for (int j = 0; j < bcs; ++j) {
             const int e = tid + j * TH, q = e % NL, t = e / NL % C;
-            if (e < groups) *reinterpret_cast<Vec<T, 4>*>(bc + (t * NL + q) * 8 + (e >= C * NL ? 4 : 0)) = vb[j];
+            if (e < groups) *reinterpret_cast<float4*>(bc + (t * NL + q) * 8 + (e >= C * NL ? 4 : 0)) = as4(vb[j]);
         }
         __syncthreads();
     }
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, S
         load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
         load_pairs<NP>(ck.u + t * CH + l.cl, u);
         load_pairs<NP>(ck.g + t * CH + l.cl, g);
-        Bc<T> bc;
+        Bc<float> bc;
         bc.load(ck.bc + (t * NL + l.nl) * 8, true);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -380,7 +379,7 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
             float2 dt[NP], u[NP];
             load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
             load_pairs<NP>(ck.u + t * CH + l.cl, u);
-            Bc<T> bc;
+            Bc<float> bc;
             bc.load(ck.bc + (t * NL + l.nl) * 8, false);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
@@ -431,15 +430,19 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
                 for (int i = 0; i < 2 * NP; ++i) p[i * 32] = one_of<NP>(h, i);
             }
         }
-        // token t backwards, from the states behind (h) and in front of it (hp); its results take the place of its inputs:
-        // dt s1 of u, the gradient of dt of dt, sum_n C h of g
-        const auto back = [&](int t, float* sums, const float2 (&h)[NP][4], const float2 (&hp)[NP][4]) {
+        // token t backwards, from the states behind (h) and in front of it (hp): its sums, of which this lane holds some
+        using Cs = ChannelSum<NL>;
+        constexpr int K = kSums<NL, NP>;
+        struct Sums {
+            float bc[Cs::held], s1[K], s2[K], y[K];
+        };
+        const auto back = [&](int t, const float2 (&h)[NP][4], const float2 (&hp)[NP][4]) {
             const int o = t * CH + l.cl;
             float2 dt[NP], u[NP], g[NP];
             load_pairs<NP>(ck.dt + o, dt);
             load_pairs<NP>(ck.u + o, u);
             load_pairs<NP>(ck.g + o, g);
-            Bc<T> bc;
+            Bc<float> bc;
             bc.load(ck.bc + (t * NL + l.nl) * 8, true);
             float2 db[4], dc[4], x1[NP], x2[NP], xy[NP];
 #pragma unroll
@@ -462,25 +465,30 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
             float v[8] = {db[0].x + db[0].y, db[1].x + db[1].y, db[2].x + db[2].y, db[3].x + db[3].y,
                           dc[0].x + dc[0].y, dc[1].x + dc[1].y, dc[2].x + dc[2].y, dc[3].x + dc[3].y};
             cs.sum(v);
+            Sums to;
+#pragma unroll
+            for (int i = 0; i < Cs::held; ++i) to.bc[i] = v[i];
+            sum_states<NL, NP>(x1, l.nl, to.s1);
+            sum_states<NL, NP>(x2, l.nl, to.s2);
+            if (r.z) sum_states<NL, NP>(xy, l.nl, to.y);
+            return to;
+        };
+        // ... and where they go: the gradients' in the place of the token's inputs, dt s1 of u, that of dt of dt, sum_n C h of g
+        const auto keep = [&](int t, float* sums, const Sums& v) {
             if (cs.writes)
 #pragma unroll
-                for (int i = 0; i < ChannelSum<NL>::held; ++i) {
+                for (int i = 0; i < Cs::held; ++i) {
                     const int j = cs.first + i;
-                    sums[(j >> 2) * S + 4 * l.nl + (j & 3)] = v[i];
+                    sums[(j >> 2) * S + 4 * l.nl + (j & 3)] = v.bc[i];
                 }
-            constexpr int K = kSums<NL, NP>;
-            float s1[K], s2[K], sy[K];
-            sum_states<NL, NP>(x1, l.nl, s1);
-            sum_states<NL, NP>(x2, l.nl, s2);
-            if (r.z) sum_states<NL, NP>(xy, l.nl, sy);
             if (sums_here<NL, NP>(l.nl)) {
-                const int first = o + its_channel<NL, NP>(l.nl);
+                const int first = t * CH + l.cl + its_channel<NL, NP>(l.nl);
 #pragma unroll
                 for (int i = 0; i < K; ++i) {
                     const float dti = ck.dt[first + i], ui = ck.u[first + i];
-                    ck.u[first + i] = dti * s1[i];
-                    ck.dt[first + i] = fmaf(ui, s1[i], kLn2 * s2[i]);
-                    if (r.z) ck.g[first + i] = sy[i];
+                    ck.u[first + i] = dti * v.s1[i];
+                    ck.dt[first + i] = fmaf(ui, v.s1[i], kLn2 * v.s2[i]);
+                    if (r.z) ck.g[first + i] = v.y[i];
                 }
             }
         };
@@ -493,6 +501,7 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
             __syncwarp();   // (the sums take the states' place)
             if (!mixed(sub)) {
                 float2 hs[kSub][NP][4];
+                Sums got[kSub];   // (their stores would hold back the next token's loads)
 #pragma unroll
                 for (int e = 0; e < kSub; ++e) {
                     if (e) copy(hs[e], hs[e ? e - 1 : 0]);
@@ -500,8 +509,10 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
                     advance(t0 + e, hs[e]);
                 }
 #pragma unroll
-                for (int e = kSub - 1; e > 0; --e) back(t0 + e, sums + e * 2 * S, hs[e], hs[e - 1]);
-                back(t0, sums, hs[0], hp);
+                for (int e = kSub - 1; e >= 0; --e) got[e] = back(t0 + e, hs[e], e ? hs[e ? e - 1 : 0] : hp);
+                __syncwarp();   // (every lane has read what the results replace)
+#pragma unroll
+                for (int e = 0; e < kSub; ++e) keep(t0 + e, sums + e * 2 * S, got[e]);
             } else {
 #pragma unroll 1
                 for (int e = kSub - 1; e >= 0; --e) {
@@ -516,7 +527,9 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
                         advance(t0 + f, h);
                     }
                     if (w & kLast) l.pairs(gr.dS, at, d, cb, q);
-                    back(t, sums + e * 2 * S, h, before);
+                    const Sums got = back(t, h, before);
+                    __syncwarp();
+                    keep(t, sums + e * 2 * S, got);
                     if (w & kFirst) {
                         if (gr.dS0) l.put_pairs(gr.dS0 + at, d, cb, q);
 #pragma unroll
@@ -677,7 +690,7 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const S
         constexpr size_t smem = sizeof(float) * Chunk<T, NL>::floats;
         const auto local = k_scan_local<T, NL, WIDE>;
         if ((e = cudaFuncSetAttribute(local, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-        local<<<dim3(ws.chunks, blocks, rows), threads_of(NL), smem, st>>>(d, in, g, ws);
+        local<<<dim3(ws.chunks, blocks, rows), Chunk<T, NL>::TH, smem, st>>>(d, in, g, ws);
         prof_mark("scan_local", st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         k_scan_chain<<<dim3((unsigned)(((long long)d.D * NL + 127) / 128), 2, rows), 128, 0, st>>>(d, in.A, ws, NL);
@@ -686,7 +699,7 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const S
     }
     const auto grad = k_scan_grad<T, NL, WIDE>;
     if ((e = cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sm::bytes)) != cudaSuccess) return e;
-    grad<<<dim3(ws.gx, blocks), threads_of(NL), Sm::bytes, st>>>(d, in, g, ws);
+    grad<<<dim3(ws.gx, blocks), Chunk<T, NL>::TH, Sm::bytes, st>>>(d, in, g, ws);
     prof_mark("scan_grad", st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long n = (long long)rows * d.at.L * d.G * 2 * Tile::states;

@@ -32,8 +32,8 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
 }
 
-// Tiles of TT tokens.  kBuffers buffers: (dt, dt, dt u, dt u) of two channels [TT][CH / 2], y [TT][CH], and (B, C) of four states as
-// they are stored [TT][NL]; and for each group a ring of raw tiles.
+// Tiles of TT tokens.  kBuffers buffers: (dt, dt, dt u, dt u) of two channels [TT][CH / 2], y [TT][CH], and (B, C) of four states
+// [TT][NL], fp32; and for each group a ring of raw tiles.
 constexpr int kBuffers = 4, kWhat = 8;
 template <typename T, int NL, bool PART>
 struct FwdTile {
@@ -44,7 +44,7 @@ struct FwdTile {
     static constexpr int bc_items = (bc + kBring - 1) / kBring;
     static constexpr int arrays = PART ? 2 : 3;
     static constexpr int y_at = TT * CH * 2, bc_at = y_at + (PART ? 0 : TT * CH);  // floats
-    static constexpr int buffer = bc_at + TT * NL * 8 * (int)sizeof(T) / 4;
+    static constexpr int buffer = bc_at + TT * NL * 8;
     static constexpr int slot = (items * arrays + bc_items) * kBring;              // Vec<T, 4>
     static constexpr int ring = sizeof(T) == 2 ? 3 : 2;
     static constexpr size_t bytes = kBuffers * buffer * sizeof(float) + kGroups * ring * slot * sizeof(Vec<T, 4>);
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
         const auto fill = [&](int i) {
             const V* slot = raw + (i / kGroups % Tile::ring) * Tile::slot;
             float* const s_dd = buffer(i);
-            T* const s_bc = reinterpret_cast<T*>(s_dd + Tile::bc_at);
+            float* const s_bc = s_dd + Tile::bc_at;
             const int* w = what[i % kWhat];
             // (every load before the first store: a store holds back the loads behind it)
             float4 dt[Tile::items], du[Tile::items];
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
                 V v;
                 v.zero();
                 if (!(w[t] & kOutside) && 4 * q < d.N) v = slot[(Tile::items * Tile::arrays + j) * kBring];
-                *reinterpret_cast<V*>(s_bc + (t * NL + q) * 8 + (e < TT * NL ? 0 : 4)) = v;
+                *reinterpret_cast<float4*>(s_bc + (t * NL + q) * 8 + (e < TT * NL ? 0 : 4)) = as4(v);
             }
         };
         const auto finish = [&](int i) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
     bool alive = true;
     for (int i = 0; i < tiles; ++i) {
         const float* const s_dd = buffer(i) + l.cl * 2;
-        const T* const s_bc = reinterpret_cast<const T*>(buffer(i) + Tile::bc_at) + l.nl * 8;
+        const float* const s_bc = buffer(i) + Tile::bc_at + l.nl * 8;
         float* const s_y = buffer(i) + Tile::y_at;
         bar_wait(1 + i % kBuffers);
         // what KT tokens read, and the tokens: a store holds back the loads behind it, so that the next tokens' are loaded before
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
         if (!any[i % kWhat]) {
             constexpr std::integral_constant<int, 4> four{};
             float4 dd[2][4][NP];
-            Bc<T> bc[2][4];
+            Bc<float> bc[2][4];
             load(0, dd[0], bc[0], four);
 #pragma unroll
             for (int t = 0; t < TT; t += 4) {
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
                 }
                 constexpr std::integral_constant<int, 1> one{};
                 float4 dd[1][NP];
-                Bc<T> bc[1];
+                Bc<float> bc[1];
                 load(t, dd, bc, one);
                 tokens(t, dd, bc, one);
                 if (!PART && S_final && (w & kLast)) l.put_pairs(S_final + at, d, cb, h);
