@@ -31,6 +31,13 @@ __device__ __forceinline__ float warp_max(float v, int lanes) {
     return v;
 }
 
+// 1 / x for normal x, within 2^-23 of it (its error moves a quotient by less than 2^-19 of an e4m3 step)
+__device__ __forceinline__ float rcp_of(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int W>
 __device__ __forceinline__ void row_sync(int bar) {
     if (W == 1) __syncwarp();
@@ -65,8 +72,8 @@ struct RmsArgs {
 
 // W warps a row, NV vectors a lane; as many rows at a time as the CTA has groups of W warps.
 template <typename T, int VEC, int NV, int W, bool BWD, bool Q>
-__global__ void __launch_bounds__((Cta<W, NV * VEC, BWD || Q>::threads), 1) k_rms(RmsDims d, RmsArgs a) {
-    constexpr int SP = NV * VEC, RPC = Cta<W, SP, BWD || Q>::threads / 32 / W, H = SP / 2;
+__global__ void __launch_bounds__((Cta<W, NV * VEC, BWD>::threads), 1) k_rms(RmsDims d, RmsArgs a) {
+    constexpr int SP = NV * VEC, RPC = Cta<W, SP, BWD>::threads / 32 / W, H = SP / 2;
     constexpr bool RING = VEC > 1;
     __shared__ float2 red[RPC][2][W];
     __shared__ uint64_t full[RPC][kStages];
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__((Cta<W, NV * VEC, BWD || Q>::threads), 1) k_rm
 #pragma unroll
                 for (int m = 0; m < NV; ++m) {
                     const int c = (m * 32 * W + t) * VEC;
-                    const float scale = fmaxf(top[m], kTop * kTiny) / kTop, by = 1.f / scale;
+                    const float scale = fmaxf(top[m] * (1.f / kTop), kTiny), by = rcp_of(scale);
                     float f[VEC];
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
@@ -320,7 +327,7 @@ bool on(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 template <typename T, int VEC, int NV, int W, bool BWD, bool Q>
 cudaError_t launch_rows(const RmsDims& d, RmsArgs a, int* ctas, cudaStream_t st) {
-    constexpr int CT = Cta<W, NV * VEC, BWD || Q>::threads, RPC = CT / 32 / W;
+    constexpr int CT = Cta<W, NV * VEC, BWD>::threads, RPC = CT / 32 / W;
     const long long need = (d.rows + RPC - 1) / RPC;
     *ctas = (int)(need < 1 ? 1 : need < kRmsGrid ? need : kRmsGrid);
     // stages: as many as fit, at most kStages (one always fits: three rows of 16384 fp32 are 192 KB)
