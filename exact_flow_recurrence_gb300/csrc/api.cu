@@ -922,7 +922,7 @@ efla_status check_axes(int B, int L, int packed, bool step, const char* what, ef
     if (step && (packed || L != 1))
         return fail(EFLA_ERR_INVALID_ARG, "%s needs L == 1 and packed == 0 (got %d, %d)", what, L, packed);
     if (L > (1 << 30)) return fail(EFLA_ERR_UNSUPPORTED, "L=%d exceeds 2^30", L);
-    *a = efla::Axes{B, L, packed, nullptr};
+    *a = efla::Axes{B, B ? L : 0, packed, nullptr};   // (no sequences: no token lies in one, and there are no offsets to read)
     return EFLA_OK;
 }
 

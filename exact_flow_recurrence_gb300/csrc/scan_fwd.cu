@@ -35,6 +35,8 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
 // Tiles of TT tokens.  kBuffers buffers: (dt, dt, dt u, dt u) of two channels [TT][CH / 2], y [TT][CH], and (B, C) of four states
 // [TT][NL], fp32; and for each group a ring of raw tiles.
 constexpr int kBuffers = 4, kWhat = 8;
+static_assert(kBuffers == 2 * kGroups, "a group fills a buffer while the carriers may still read the one that it filled before");
+static_assert(kWhat >= 2 * kBuffers && 2 * kBuffers + kGroups < 16, "slots of flags, named barriers");
 template <typename T, int NL, bool PART>
 struct FwdTile {
     static constexpr int CH = ScanTile<NL>::ch, S = ScanTile<NL>::states;

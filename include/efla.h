@@ -362,7 +362,8 @@ efla_status efla_conv_step(const efla_conv_shape* shape, const void* x, const vo
  * u, delta, z, y (and dy, du, ddelta, dz) [B,L,D] dtype through strides {batch, token}; Bm, C [B,L,G,N] dtype through
  * strides {batch, token, group}, their last dimension contiguous; A [D,N], skip [D], delta_bias [D] fp32 dense; S0,
  * S_final, dS_final, dS0 dense [B,D,N] fp32; dB, dC dense [B,L,G,N] dtype; dA, dskip, ddelta_bias fp32 dense.
- * skip, z, delta_bias NULL: none (y has no gate, no skip).  A token with dt = 0 leaves the state alone.
+ * skip, z, delta_bias NULL: none (y has no gate, no skip).  A token with dt = 0 leaves the state
+ * alone (u, B finite).
  * packed and offsets as in the gated rule ([L,D] and [L,G,N]).  Any N in 1 .. 64, D a multiple of G (1 .. 65536), L up to
  * 2^30, at most 65535 sequences unless packed.  Alignment: to the elements (states, workspace: 16 bytes).
  * Arithmetic is fp32; e^x is ex2.approx of x log2(e) (at most 2^-22, on average -2e-8, of the result).  Sums over tokens

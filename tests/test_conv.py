@@ -189,6 +189,31 @@ def test_no_tokens():
 
 
 @pytest.mark.gpu
+def test_no_sequences():
+    """offsets of one entry: nothing lies in a sequence."""
+    x, w = torch.randn(5, 16, device=DEV), torch.randn(16, 4, device=DEV)
+    off = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y, dx = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    _, S = efla.efla_conv_fwd(x, w, offsets=off, y=y)
+    _, dw, _, dS0 = efla.efla_conv_bwd(x, w, x, offsets=off, dx=dx)
+    efla.efla_get_status()
+    assert S.shape == dS0.shape == (0, 3, 16) and bool((y == 7).all()) and bool((dx == 7).all()) and float(dw.abs().max()) == 0.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 37])
+def test_gradient_into_a_slice(D):
+    a = make(B=2, L=50, D=D, W=4, dtype=BF)
+    x, dy, w = gpu(a["x"], "x", a), gpu(a["dy"], "dy", a), gpu(a["w"])
+    want = efla.efla_conv_bwd(x, w, dy)
+    rows = torch.full((2, 50, 2 * D + 8), 9.0, dtype=BF, device=DEV)
+    got = efla.efla_conv_bwd(x, w, dy, dx=rows[..., D:2 * D])
+    efla.efla_get_status()
+    assert torch.equal(rows[..., D:2 * D], want[0]) and torch.equal(got[1], want[1])
+    assert bool((rows[..., :D] == 9).all()) and bool((rows[..., 2 * D:] == 9).all())
+
+
+@pytest.mark.gpu
 def test_gradient_against_differences():
     """(f(x + h v) - f(x - h v)) / 2h of the GPU forward (fp32) against <dx, v>: h = 1e-2 leaves truncation h^2 and rounding
     1e-6 / h, each about 1e-4 of the scale."""

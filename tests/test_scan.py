@@ -287,6 +287,52 @@ def test_no_tokens():
 
 
 @pytest.mark.gpu
+def test_no_sequences():
+    """offsets of one entry: nothing lies in a sequence."""
+    a = make(B=1, L=40, D=16, N=8, state=False)
+    t = on_gpu(dict(a, packed=True))
+    ins, rest = (t["u"], t["delta"], t["A"], t["B_"], t["C"]), (t["D"], t["z"], t["bias"])
+    off = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y, du = torch.full_like(t["u"], 7.0), torch.full_like(t["u"], 7.0)
+    _, S = efla.efla_scan_fwd(*ins, *rest, offsets=off, y=y)
+    g = efla.efla_scan_bwd(*ins, t["dy"], *rest, offsets=off, du=du)
+    efla.efla_get_status()
+    assert S.shape == g[8].shape == (0, 16, 8) and bool((y == 7).all()) and bool((du == 7).all())
+    assert all(float(g[i].abs().max()) == 0.0 for i in (2, 5, 7))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 37])
+def test_gradients_into_slices_of_one_buffer(D, dtype):
+    a = make(B=2, L=70, D=D, N=16, dtype=dtype)
+    t = on_gpu(a)
+    ins, rest = (t["u"], t["delta"], t["A"], t["B_"], t["C"]), (t["D"], t["z"], t["bias"], t["S0"], t["dS"])
+    want = efla.efla_scan_bwd(*ins, t["dy"], *rest)
+    rows = torch.full((2, 70, 3 * D + 4), 9.0, dtype=dtype, device=DEV)
+    got = efla.efla_scan_bwd(*ins, t["dy"], *rest, du=rows[..., :D], ddelta=rows[..., D:2 * D], dz=rows[..., 2 * D:3 * D])
+    efla.efla_get_status()
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    assert bool((rows[..., 3 * D:] == 9).all())
+
+
+@pytest.mark.gpu
+def test_broadcast_inputs():
+    """B and C of one row for a whole batch, and a gate of one row for every token: strides of zero."""
+    a = make(B=3, L=33, D=32, N=16)
+    t = on_gpu(a)
+    b, c, z = t["B_"][:1].expand(3, -1, -1, -1), t["C"][:1].expand(3, -1, -1, -1), t["z"][:, :1].expand(-1, 33, -1)
+    rest = (t["D"], t["bias"], t["S0"])
+    for got, want in ((efla.efla_scan_fwd(t["u"], t["delta"], t["A"], b, c, rest[0], z, *rest[1:]),
+                       efla.efla_scan_fwd(t["u"], t["delta"], t["A"], b.contiguous(), c.contiguous(), rest[0], z.contiguous(), *rest[1:])),
+                      (efla.efla_scan_bwd(t["u"], t["delta"], t["A"], b, c, t["dy"], rest[0], z, *rest[1:]),
+                       efla.efla_scan_bwd(t["u"], t["delta"], t["A"], b.contiguous(), c.contiguous(), t["dy"], rest[0], z.contiguous(), *rest[1:]))):
+        efla.efla_get_status()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences():
     """(f(x + h v) - f(x - h v)) / 2h of the GPU forward (fp32) against <dx, v>: h = 1e-2 leaves truncation h^2 and rounding
     1e-6 / h, each about 1e-4 of the scale."""
