@@ -109,9 +109,14 @@ __global__ void __launch_bounds__(256, 3) k_conv_fwd(ConvDims d, const T* x, con
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) conv_row<T, VEC, W>(d, xa, S0, s, t - (W - 1) + j, c, win[j]);
         Vec<T, VEC> q[2][NB];   // a batch ahead: a store holds back the loads behind it
-        const auto bring = [&](int u, int k) {
+        const T* px = xa + t * d.xs[1] + c;   // (running pointers: a row's address is an addition)
+        T* py = ya + t * d.ys[1];
+        const auto bring = [&](int u, int k) {   // (past the last row: the last again)
 #pragma unroll
-            for (int i = 0; i < NB; ++i) q[k][i].load(xa + min(u + i, hi - 1) * d.xs[1] + c);   // (past the last: the last again)
+            for (int i = 0; i < NB; ++i) {
+                q[k][i].load(px);
+                if (u + i + 1 < hi) px += d.xs[1];
+            }
         };
         const auto walk = [&](int u, int k) {
 #pragma unroll
@@ -129,7 +134,8 @@ __global__ void __launch_bounds__(256, 3) k_conv_fwd(ConvDims d, const T* x, con
                     for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
                     win[W - 2][e] = cur[e];
                 }
-                if (u + i < hi) store_pairs<T, VEC>(ya + (u + i) * d.ys[1], o);
+                if (u + i < hi) store_pairs<T, VEC>(py, o);
+                py += d.ys[1];
             }
         };
         bring(t, 0);
@@ -145,10 +151,11 @@ __global__ void __launch_bounds__(256, 3) k_conv_fwd(ConvDims d, const T* x, con
 }
 
 constexpr int kBwdWarps = 8;   // runs a CTA
+constexpr int kBwdVec = 4, kBwdCtas = 2;
 
 // A warp walks one run of tokens of 32 VEC channels.  part [CTA rows][W + 1][D]: the CTA's sums of dw and db.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(32 * kBwdWarps, 2) k_conv_bwd(ConvDims d, const T* x, const void* w, const void* bias, const T* S0,
+__global__ void __launch_bounds__(32 * kBwdWarps, kBwdCtas) k_conv_bwd(ConvDims d, const T* x, const void* w, const void* bias, const T* S0,
                                                             const T* dy, const T* dS, T* dx, T* dS0, float* part, int run, int runs,
                                                             long long nruns) {
     constexpr int NB = 4, P = kPairs<VEC>;
@@ -197,11 +204,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_conv_bwd(ConvDims d, cons
                 for (int e = 0; e < P; ++e) old[j][e] = make_float2(0.f, 0.f);
             const int last = min(stop, s.end) - 1;   // the last token read
             Vec<T, VEC> qx[2][NB], qg[2][NB];        // a batch ahead: a store holds back the loads behind it
+            const T *px = xa + lo * d.xs[1] + c, *pg = ga + lo * d.dys[1];
+            T* pd = da + lo * d.dxs[1];
             const auto bring = [&](int u, int k) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    qx[k][i].load(xa + min(u + i, last) * d.xs[1] + c);
-                    qg[k][i].load(ga + min(u + i, last) * d.dys[1]);
+                    qx[k][i].load(px);
+                    qg[k][i].load(pg);
+                    if (u + i < last) {
+                        px += d.xs[1];
+                        pg += d.dys[1];
+                    }
                 }
             };
             const auto walk = [&](int u, int k) {
@@ -243,7 +256,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_conv_bwd(ConvDims d, cons
                         for (int e = 0; e < P; ++e)
 #pragma unroll
                             for (int j = 0; j < W; ++j) o[e] = fma2(wv[W - 1 - j][e], old[j][e], o[e]);
-                        store_pairs<T, VEC>(da + q * d.dxs[1], o);
+                        store_pairs<T, VEC>(pd, o);
+                        pd += d.dxs[1];
                     }
                 }
             };
@@ -418,10 +432,10 @@ struct BwdGrid {
     long long nruns;
 };
 BwdGrid bwd_grid(const ConvDims& d) {
-    const int vec = 4;
+    const int vec = kBwdVec;
     const long long cols = (d.D + 32 * vec - 1) / (32 * vec);
     BwdGrid g;
-    g.run = run_of(d.at.L, (double)cols * d.at.rows() / kBwdWarps, 2, 8);
+    g.run = run_of(d.at.L, (double)cols * d.at.rows() / kBwdWarps, kBwdCtas, 8);
     g.runs = (d.at.L + g.run - 1) / g.run;
     g.nruns = (long long)d.at.rows() * g.runs;
     const long long n = (g.nruns + kBwdWarps - 1) / kBwdWarps;
@@ -475,13 +489,13 @@ bool wide(const ConvDims& d, const ConvArgs& a, int vec, bool step) {
     return ok(a.x, d.xs) && ok(a.y, d.ys) && ok(a.dy, d.dys) && ok(a.dx, d.dxs);
 }
 
-// Four channels a thread where rows allow it (eight bf16, 16 bytes, leave half the threads: 32 registers of weights each)
+// Channels a thread where rows allow it
 template <Which K>
 cudaError_t by_type(const ConvDims& d, const ConvArgs& a, cudaStream_t st) {
-    constexpr int V = 4;
+    constexpr int V = K == kBwd ? kBwdVec : 4;
     if (d.bf16)
         return wide(d, a, V, K == kStep) ? by_taps<K, __nv_bfloat16, V>(d, a, st) : by_taps<K, __nv_bfloat16, 1>(d, a, st);
-    return wide(d, a, 4, K == kStep) ? by_taps<K, float, 4>(d, a, st) : by_taps<K, float, 1>(d, a, st);
+    return wide(d, a, V, K == kStep) ? by_taps<K, float, V>(d, a, st) : by_taps<K, float, 1>(d, a, st);
 }
 
 }  // namespace
