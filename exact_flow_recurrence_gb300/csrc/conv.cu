@@ -3,9 +3,14 @@
 //   pre_t = bias + sum_j w_j x_{t - (W - 1) + j},   y_t = pre_t, or pre_t sigmoid(pre_t)
 //   dp_t = dy_t y'(pre_t),   dx_t = sum_j w_j dp_{t + W - 1 - j},   dw_j = sum_t dp_t x_{t - (W - 1) + j},   db = sum_t dp_t
 // Places before a sequence's first token are the W - 1 rows of its state, oldest first, or zeros.
-// Bound by HBM: every token's row is read once and its result written once.  A thread owns VEC
-// neighbouring channels and walks a run of tokens with the W - 1 rows (and W gradients) behind it in
-// registers; the rows that two runs share come from the caches.  Sums are fp32.
+// A thread owns four neighbouring channels, two of them an instruction, and walks a run of tokens with the W - 1 rows (and W
+// gradients) behind it in registers; rows come a batch ahead of the stores, which would hold back the loads behind them;
+// the rows that two runs share come from the caches.  A run is as long as fills the SMs evenly (run_of).  Sums are fp32:
+// dw and db in registers over a run, then over a CTA's eight, then over CTAs, in order.
+// Its floor is HBM: every token's row is read once and its result written once.  B8 L2048 D2048 W4 bf16 with silu: 28 us (134 MB,
+// 4.8 TB/s; 20 us at a plain copy's rate), bound by issue (a third: exponent, reciprocal and conversions) and latency at 24
+// warps an SM.  Backward, B4 L4096: 54 us and 4 for the sums (201 MB, 3.7 TB/s; 30 us), at 16 warps of 128 registers; two
+// channels a thread, 24 warps: 105 us (spills, twice the addresses).  Eight channels a thread forward: 60 us.
 #include "mix.cuh"
 #include "launch.h"
 

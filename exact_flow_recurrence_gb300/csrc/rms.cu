@@ -8,6 +8,9 @@
 // Bound by HBM: x and res read once, h and y written once (backward: h, dy, dh and dx).  Rows in registers as
 // in the layer norm, which this shares its rings and sums with: a CTA an SM walks rows, 16 elements a thread,
 // weights (and the sums of dw) in registers; rows come by bulk copies, several ahead.
+// 16384 x 2048 bf16: forward 36 us (268 MB, 7.4 TB/s with what stays in L2; 48 a call among others), backward 41 us and 4 for
+// the sums over CTAs (268 MB).  6001 rows in 8 bits, scales of 128 columns: 19 us (86 MB; 13 us at a plain copy's rate): ten
+// rounds of a row's chain of steps a group.
 #include <cuda_fp8.h>
 
 #include "norm_rows.cuh"

@@ -8,7 +8,12 @@
 // all chunks at once.  A second launch chains the chunks' maps, and the third has every chunk's entering state and
 // gradient at hand: it walks the chunk forward to the state in front of every kSub tokens (shared memory),
 // then back, kSub tokens' states in registers.  Sums over channels (dB, dC) and tokens (dA, dskip, dbias) are
-// partial sums of CTAs, added in a fixed order by the last launch.
+// partial sums of CTAs, added in a fixed order by the last launches.
+// B4 L4096 D2048 N16 bf16 with gate: 0.96 ms (473 MB; 70 us at a plain copy's rate, 175 us for the twelve fp32 operations and the
+// exponential that a gradient needs at least): every chunk by itself 206 us (issue slots 61% used), the chain 41 us (268 MB:
+// a plain copy's rate), gradients 695 us (422 instructions a warp's token of 32 channels, 230 of them the walk back; slots
+// half used, by two warps a scheduler: 255 registers), sums 17 us.  Chunks of 64 tokens with a tile a barrier: 2.43 ms;
+// loads in batches ahead of stores took 1.60 to 0.96.
 #include "scan.cuh"
 #include "launch.h"
 

@@ -1,10 +1,18 @@
 // scan_fwd.cu -- the selective scan over whole sequences, and one token of it.
 //
 // Four fp32 operations and one exponential for every token, channel and state: their pipes, not HBM, bound it
-// from 8 states on.  The recurrence runs along the tokens; channels and states are independent.  Where those are
-// too few to fill the SMs the tokens are cut into segments: a first launch takes every segment from a zero state
-// to its last one and adds up its dt, the second works out the state that a segment starts from (a fold over the
+// from 8 states on (a warp's token of 32 channels and 16 states: 64 cycles of a scheduler's FMA pipe, 64 of its exponentials).
+// The recurrence runs along the tokens; channels and states are independent: B D N / 16 threads in all, one carrying warp a
+// scheduler at the training size, so that what counts is how little else that warp does and waits for.  Hence a
+// thread's 4 x 4 tile (B, C read once for four channels), everything that depends on a channel alone in other warps, and
+// loads of the next four tokens before the stores of these.
+// Where channels are too few to fill the SMs the tokens are cut into segments: a first launch takes every segment from a zero
+// state to its last one and adds up its dt, the second works out the state that a segment starts from (a fold over the
 // segments before it) and takes it from there.
+// B8 L2048 D2048 N16 bf16 with gate: 195 us on 128 SMs (272 MB, 1.4 TB/s; 40 us at a plain copy's rate, 69 us at its pipes' on these SMs),
+// issue slots 60% used.  Steps on the way: warps that do all by themselves 1574, carrying and bringing warps 280, loads ahead of
+// stores 229, four buffers 213, B and C as fp32 in shared memory 197; B and C there twice, for packed operands: 254 (shared
+// memory's loads then bound it).  13 packed prompts, 16384 tokens: 309 us in two launches (nine segments).
 #include "scan.cuh"
 #include "launch.h"
 
