@@ -480,19 +480,19 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanDims d, ScanIn in, float*
 
 // A batch: a CTA keeps its channels (16 KB of a state: their A, skip and bias stay in registers) and takes every
 // gridDim.x-th sequence.  States and token rows come by asynchronous copies, kStepStages - 1 sequences ahead, so that what is in
-// flight costs no registers.  N = 4 nl.
+// flight costs no registers.  N = 4 nl, nl = 1 << shift.
 constexpr int kStepStages = 6, kStepFour = 4;   // groups of four states a thread
 template <typename T>
-__global__ void __launch_bounds__(256, 2) k_scan_step_ring(ScanDims d, ScanIn in, float* S, const int* slots, int nslots, T* y, int nl) {
+__global__ void __launch_bounds__(256, 2) k_scan_step_ring(ScanDims d, ScanIn in, float* S, const int* slots, int nslots, T* y, int shift) {
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ int s_slot[kStepStages];
-    const int tid = threadIdx.x, CT = 256 * kStepFour / nl, c0 = blockIdx.y * CT, n = min(CT, d.D - c0), g = c0 / (d.D / d.G);
+    const int tid = threadIdx.x, nl = 1 << shift, CT = (256 * kStepFour) >> shift, c0 = blockIdx.y * CT, n = min(CT, d.D - c0), g = c0 / (d.D / d.G);
     const uint32_t states = 256 * kStepFour * 16, stage = states + (3 * CT + 8 * nl) * (uint32_t)sizeof(T);
     float2 a0[kStepFour], a1[kStepFour];
     float bias[kStepFour], skip[kStepFour];
 #pragma unroll
     for (int i = 0; i < kStepFour; ++i) {
-        const int f = i * 256 + tid, c = f / nl;
+        const int f = i * 256 + tid, c = f >> shift;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
         bias[i] = skip[i] = 0.f;
         if (c < n) {
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(256, 2) k_scan_step_ring(ScanDims d, ScanIn in
                     if (i * 256 + tid < n * nl) copy_async(to + (i * 256 + tid) * 16, from + i * 256 + tid, 16);
                 T* rows = reinterpret_cast<T*>(to + states);   // u, delta, z [CT], B, C [4 nl]
                 for (int j = tid; j < 3 * (CT / 4) + 2 * nl; j += 256) {
-                    const int row = j / (CT / 4), at = j % (CT / 4) * 4, e = j - 3 * (CT / 4);
+                    const int row = j >> (8 - shift), at = (j & (CT / 4 - 1)) * 4, e = j - 3 * (CT / 4);
                     if (e >= 0)
                         copy_async(rows + j * 4, e < nl ? (const T*)in.Bm + b * d.bs[0] + g * d.bs[2] + 4 * e
                                                         : (const T*)in.C + b * d.cs[0] + g * d.cs[2] + 4 * (e - nl), 4 * sizeof(T));
@@ -549,21 +549,21 @@ __global__ void __launch_bounds__(256, 2) k_scan_step_ring(ScanDims d, ScanIn in
             for (int c = tid; c < n; c += 256) st_elem(y + b * d.ys[0] + c0 + c, 0.f);
             continue;
         }
-        const int q = tid % nl;
+        const int q = tid & (nl - 1);
         const float4 Bv = as4(*reinterpret_cast<const Vec<T, 4>*>(rows + 3 * CT + 4 * q)),
                      Cv = as4(*reinterpret_cast<const Vec<T, 4>*>(rows + 3 * CT + 4 * (nl + q)));
         float4* to = reinterpret_cast<float4*>(S + ((long long)sl * d.D + c0) * d.N);
         float acc[kStepFour];
 #pragma unroll
         for (int i = 0; i < kStepFour; ++i) {
-            const int f = i * 256 + tid, c = min(f / nl, n - 1);
+            const int f = i * 256 + tid, c = min(f >> shift, n - 1);
             float4 h = *reinterpret_cast<const float4*>(from + f * 16);
             acc[i] = step4(step_of(d, (float)rows[CT + c] + bias[i]), (float)rows[c], a0[i], a1[i], h, Bv, Cv);
             if (f < n * nl) to[f] = h;
         }
 #pragma unroll
         for (int i = 0; i < kStepFour; ++i) {
-            const int c = (i * 256 + tid) / nl;
+            const int c = (i * 256 + tid) >> shift;
             for (int o = nl / 2; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
             if (q == 0 && c < n) {
                 acc[i] = fmaf(skip[i], (float)rows[c], acc[i]);
@@ -591,7 +591,7 @@ cudaError_t step(const ScanDims& d, const ScanIn& in, float* S, const int* slots
     const bool wide = d.N % 4 == 0 && ((uintptr_t)S & 15) == 0 && ((uintptr_t)in.A & 15) == 0 &&
                       aligned_rows(in.Bm, rows, B, d.G, 4 * es, es) && aligned_rows(in.C, rows_c, B, d.G, 4 * es, es);
     // the ring: whole groups of four, a tile in one group, and four sequences a CTA at least with two CTAs an SM
-    // (256 x 4096 x 16 bf16: 35 us; element by element, one state group a thread, 53)
+    // (256 x 4096 x 16 bf16: 34 us; element by element, one state group a thread, 53)
     const int CT = 256 * kStepFour / nl, tiles = (d.D + CT - 1) / CT;
     const auto ok = [&](const void* p, const long long (&s)[2]) { return !p || aligned_rows(p, s, B, 1, 4 * es, es); };
     if (wide && d.N == 4 * nl && d.D % 4 == 0 && (d.G == 1 || d.D / d.G % CT == 0) && (long long)tiles * B >= 4 * 2 * kScanSms && tiles <= 2 * kScanSms &&
@@ -599,7 +599,9 @@ cudaError_t step(const ScanDims& d, const ScanIn& in, float* S, const int* slots
         const size_t smem = kStepStages * (256 * kStepFour * 16 + (size_t)(3 * CT + 8 * nl) * es);
         const cudaError_t e = cudaFuncSetAttribute(k_scan_step_ring<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        k_scan_step_ring<T><<<dim3(2 * kScanSms / tiles, tiles), 256, smem, st>>>(d, in, S, slots, nslots, (T*)y, nl);
+        int shift = 0;
+        while (1 << shift < nl) ++shift;
+        k_scan_step_ring<T><<<dim3(2 * kScanSms / tiles, tiles), 256, smem, st>>>(d, in, S, slots, nslots, (T*)y, shift);
     } else {
         const unsigned grid = (unsigned)(((long long)B * d.D * nl + 255) / 256);
         if (wide) k_scan_step<T, true><<<grid, 256, 0, st>>>(d, in, S, slots, nslots, (T*)y, nl);
