@@ -8,11 +8,11 @@
 // all chunks at once.  A second launch chains the chunks' maps, and the third has every chunk's entering state and
 // gradient at hand: it walks the chunk forward to the state in front of every kSub tokens (shared memory),
 // then back, kSub tokens' states in registers.  Sums over channels (dB, dC) and tokens (dA, dskip, dbias) are
-// partial sums of CTAs, added in a fixed order by the last launches.
+// partial sums of CTAs, added in a fixed order by the last launch.
 // B4 L4096 D2048 N16 bf16 with gate: 0.96 ms (473 MB; 70 us at a plain copy's rate, 175 us for the twelve fp32 operations and the
 // exponential that a gradient needs at least): every chunk by itself 206 us (issue slots 61% used), the chain 41 us (268 MB:
 // a plain copy's rate), gradients 695 us (422 instructions a warp's token of 32 channels, 230 of them the walk back; slots
-// half used, by two warps a scheduler: 255 registers), sums 17 us.  Chunks of 64 tokens with a tile a barrier: 2.43 ms;
+// half used, by two warps a scheduler: 255 registers), sums 9 us (two launches, one value a thread: 17).  Chunks of 64 tokens with a tile a barrier: 2.43 ms;
 // loads in batches ahead of stores took 1.60 to 0.96.
 #include "scan.cuh"
 #include "launch.h"
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, S
 // ------------------------------------------------------------------- the chunks' maps chained
 // A thread takes four states of a channel through its axis's chunks: blockIdx.y 0 forward, 1 backward.
 __global__ void __launch_bounds__(128) k_scan_chain(ScanDims d, const float* A, ScanWs ws, int nl) {
-    constexpr int AHEAD = 16;   // chunks loaded at once (188 chunks of one axis: 29 us; 37 with eight)
+    constexpr int AHEAD = 16;   // chunks loaded at once (188 chunks of one axis: 27 us; 38 with eight)
     const long long idx = (long long)blockIdx.x * 128 + threadIdx.x;
     if (idx >= (long long)d.D * nl) return;
     const int c = (int)(idx / nl), q = (int)(idx % nl), axis = blockIdx.z, back = blockIdx.y, n = ws.chunks;
@@ -623,27 +623,30 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
 }
 
 // ------------------------------------------------------------------- partial sums together, in order
-template <typename T>
-__global__ void __launch_bounds__(256) k_scan_sum_bc(ScanDims d, const float* bc, int blocks, int S, T* dB, T* dC) {
-    const long long idx = (long long)blockIdx.x * 256 + threadIdx.x, tokens = (long long)d.at.rows() * d.at.L;
-    const long long n = tokens * d.G * 2 * S;
-    if (idx >= n) return;
-    const int j = (int)(idx % (2 * S)), state = j % S;
-    if (state >= d.N) return;
-    const long long tg = idx / (2 * S);   // token and group
-    if (d.at.packed) {   // (tokens outside every sequence keep what they hold)
-        const int t = (int)(tg / d.G);
-        const Seq s = seq_of(d.at, 0, t);
-        if (t < s.start || t >= s.end) return;
+// CTAs before `first` add up dB and dC, four neighbouring states of a token and group a thread; the others dA, dskip, dbias.
+template <typename T, int NL>
+__global__ void __launch_bounds__(256) k_scan_sums(ScanDims d, ScanWs ws, int blocks, unsigned first, T* dB, T* dC, float* dA, float* dskip,
+                                                   float* dbias) {
+    constexpr int S = ScanTile<NL>::states;
+    if (blockIdx.x < first) {
+        const long long idx = (long long)blockIdx.x * 256 + threadIdx.x, n = (long long)d.at.rows() * d.at.L * d.G * 2 * NL;
+        if (idx >= n) return;
+        const int q = (int)(idx % NL) * 4;
+        const long long tg = idx / (2 * NL);   // token and group
+        if (q >= d.N) return;
+        if (d.at.packed) {   // (tokens outside every sequence keep what they hold)
+            const int t = (int)(tg / d.G);
+            const Seq s = seq_of(d.at, 0, t);
+            if (t < s.start || t >= s.end) return;
+        }
+        const float4* p = reinterpret_cast<const float4*>(ws.bc) + idx;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < blocks; ++k) v = add4(v, p[k * n]);
+        store4<T, false>((idx / NL & 1 ? dC : dB) + tg * d.N + q, v, min(4, d.N - q));
+        return;
     }
-    float v = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < blocks; ++k) v += bc[(size_t)k * n + idx];
-    st_elem((j < S ? dB : dC) + tg * d.N + state, v);
-}
-
-__global__ void __launch_bounds__(256) k_scan_sum_ch(ScanDims d, const float* ch, int gx, int S, float* dA, float* dskip, float* dbias) {
-    const long long idx = (long long)blockIdx.x * 256 + threadIdx.x, n = (long long)d.D * (S + 2);
+    const long long idx = (long long)(blockIdx.x - first) * 256 + threadIdx.x, n = (long long)d.D * (S + 2);
     if (idx >= n) return;
     float* out;
     if (idx < (long long)d.D * S) {
@@ -651,14 +654,14 @@ __global__ void __launch_bounds__(256) k_scan_sum_ch(ScanDims d, const float* ch
         if (state >= d.N) return;
         out = dA + idx / S * d.N + state;
     } else {
-        const long long c = idx - (long long)d.D * S;
+        const int c = (int)(idx - (long long)d.D * S);
         float* p = c < d.D ? dskip : dbias;
         if (!p) return;
-        out = p + c % d.D;
+        out = p + (c < d.D ? c : c - d.D);
     }
     float v = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < gx; ++k) v += ch[k * ch_stride(d, S) + idx];
+#pragma unroll 8
+    for (int k = 0; k < ws.gx; ++k) v += ws.ch[k * ch_stride(d, S) + idx];
     *out = v;
 }
 
@@ -707,9 +710,9 @@ cudaError_t run(const ScanDims& d, const ScanIn& in, const ScanGrads& g, const S
     grad<<<dim3(ws.gx, blocks), Chunk<T, NL>::TH, Sm::bytes, st>>>(d, in, g, ws);
     prof_mark("scan_grad", st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const long long n = (long long)rows * d.at.L * d.G * 2 * Tile::states;
-    if (n) k_scan_sum_bc<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(d, ws.bc, blocks / d.G, Tile::states, (T*)g.dB, (T*)g.dC);
-    k_scan_sum_ch<<<(unsigned)(((long long)d.D * (Tile::states + 2) + 255) / 256), 256, 0, st>>>(d, ws.ch, ws.gx, Tile::states, g.dA, g.dskip, g.ddbias);
+    const unsigned first = (unsigned)(((long long)rows * d.at.L * d.G * 2 * NL + 255) / 256),
+                   rest = (unsigned)(((long long)d.D * (Tile::states + 2) + 255) / 256);
+    k_scan_sums<T, NL><<<first + rest, 256, 0, st>>>(d, ws, blocks / d.G, first, (T*)g.dB, (T*)g.dC, g.dA, g.dskip, g.ddbias);
     prof_mark("scan_sums", st);
     return cudaGetLastError();
 }
