@@ -123,6 +123,13 @@ __device__ __forceinline__ float2 decay2(float2 dt, float2 a2) {
     return make_float2(ex2(x.x), ex2(x.y));
 }
 
+// h 2^x, the map of many tokens together, in two halves: 2^x alone may leave fp32 where h 2^x is inside (a state of zeros behind
+// tokens that would grow it: inf 0 is not a number).  From x = 254 on every normal h but 0 is infinite either way.
+__device__ __forceinline__ float times_ex2(float h, float x) {
+    const float f = ex2(fminf(0.5f * x, 127.f));
+    return h * f * f;
+}
+
 // What a token is, a bit each: the first or last of its sequence, outside every sequence.
 enum { kFirst = 1, kLast = 2, kOutside = 4 };
 struct TokenAt {

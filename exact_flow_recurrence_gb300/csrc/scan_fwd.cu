@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const float2 x = mul2(a2[i][n], sum), e = make_float2(at4(e0, n), at4(e1, n));
-                    h[i][n] = alive ? fma2(make_float2(ex2(x.x), ex2(x.y)), h[i][n], e) : e;
+                    h[i][n] = alive ? add2(make_float2(times_ex2(h[i][n].x, x.x), times_ex2(h[i][n].y, x.y)), e) : e;
                 }
             }
         }
