@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(128) k_scan_chain(ScanDims d, const float* A, 
             const int k = back ? n - 1 - (k0 + j) : k0 + j;
             if (k0 + j < n) {
                 at[(size_t)k * d.D * nl] = s;
-                s = on[j] ? make_float4(fmaf(ex2(a[0] * x[j]), s.x, e[j].x), fmaf(ex2(a[1] * x[j]), s.y, e[j].y),
-                                        fmaf(ex2(a[2] * x[j]), s.z, e[j].z), fmaf(ex2(a[3] * x[j]), s.w, e[j].w))
+                s = on[j] ? add4(make_float4(times_ex2(s.x, a[0] * x[j]), times_ex2(s.y, a[1] * x[j]), times_ex2(s.z, a[2] * x[j]),
+                                             times_ex2(s.w, a[3] * x[j])), e[j])
                           : e[j];
             }
         }

@@ -66,3 +66,37 @@ def test_forward_small_state_through_a_growing_segment(N):
     for got, want in zip(*forward(a)):
         assert bool(torch.isfinite(got).all())
         assert bool(((got.double() - want).abs() <= TOL * want.abs()).all())
+
+
+def backward(a):
+    t = ins(a, DEV)
+    got = efla.efla_scan_bwd(*t, a["dy"].to(DEV)[None], S0=a["S0"].to(DEV), softplus=False)
+    efla.efla_get_status()
+    u, delta, A, B, C = ins(a, dtype=torch.float64)
+    args = [u, delta, A, B, C, None, None, None, a["S0"].double()]
+    want = mix.grads(lambda *x: mix.scan_all([(0, len(u))], *x, False), args, a["dy"].double(), None)
+    names = ("du", "ddelta", "dA", "dB", "dC", None, None, None, "dS0")
+    return {n: (g.cpu().double().reshape(w.shape), w) for n, g, w in zip(names, got, want) if n}
+
+
+def zeros_between(N):
+    """32 ordinary tokens, 16 that empty the state, 80 that grow (what is) nothing, 32 ordinary ones without a gradient."""
+    L, D = 160, 24
+    a = draw(L, D, N, N)
+    a["delta"] = steps(L, (0, 0.05), (32, -100.0), (48, 20.0), (128, -1.0))[:, None].expand(L, D).contiguous()
+    a["u"][32:128] = 0
+    a["dy"][32:] = 0
+    return a
+
+
+def close(name, got, want):
+    assert bool(torch.isfinite(got).all()), name
+    assert float((got - want).abs().max()) <= 5 * TOL * float(want.abs().max()), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [4, 8, 16, 64])
+def test_backward_states_through_growing_chunks(N):
+    """dC is of the states alone."""
+    got, want = backward(zeros_between(N))["dC"]
+    close("dC", got, want)
