@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kSub = 4;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMost = 3.402823466e38f;   // the largest finite fp32
 
 // Tokens a chunk: dt, u and the gated gradient of a CTA's channels take 48 KB at most
 constexpr int chunk_of(int lanes) { return lanes >= 4 ? 32 : lanes == 2 ? 16 : 8; }
@@ -217,6 +218,31 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, S
 #pragma unroll
                     for (int n = 0; n < 4; ++n) q[i][n] = fma2(cp[i][n], f[i][n], q[i][n]);
             }
+        }
+    }
+    // A product of decays above one that has left fp32 says nothing (inf times a zero gradient is not a number): then the
+    // gradient is taken back a token at a time instead.  (A product that vanishes and grows again loses less than 2^-21 of a
+    // gradient, or one that is infinite token by token too.)
+    bool whole = true;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) whole = whole && fabsf(cp[i][n].x) <= kMost && fabsf(cp[i][n].y) <= kMost;
+    if (!whole) {
+        int t = 0;   // the last token that a gradient in front of the chunk's first one passes
+        while (t + 1 < tb - ta && !(ck.what[t] & (kLast | kOutside))) ++t;
+        l.pairs(ck.what[t] & kLast ? gr.dS : nullptr, (size_t)ck.seq[t] * d.D * d.N, d, cb, q);
+#pragma unroll 1
+        for (; t >= 0; --t) {
+            float2 dt[NP], g[NP];
+            load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
+            load_pairs<NP>(ck.g + t * CH + l.cl, g);
+            Bc<float> bc;
+            bc.load(ck.bc + (t * NL + l.nl) * 8, true);
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) q[i][n] = mul2(decay2(dt[i], a2[i][n]), fma2(g[i], both(bc.cn(n)), q[i][n]));
         }
     }
     const size_t at = (size_t)axis * ws.chunks + k;

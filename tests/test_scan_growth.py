@@ -89,6 +89,17 @@ def zeros_between(N):
     return a
 
 
+def small_values(N):
+    """A state and gradients of 1e-30 that 32 tokens behind the first chunk grow by up to 2^138, forwards and backwards."""
+    L, D = 128, 24
+    a = draw(L, D, N, N)
+    a["delta"] = steps(L, (0, -0.01), (32, 3.0), (64, -0.2))[:, None].expand(L, D) * (1 + 0.02 * torch.rand(L, D, generator=torch.Generator().manual_seed(1)))
+    a["u"][:64] = 0
+    a["dy"] *= 1e-30
+    a["S0"] = 1e-30 * (1 + torch.rand(1, D, N, generator=torch.Generator().manual_seed(2)))
+    return a
+
+
 def close(name, got, want):
     assert bool(torch.isfinite(got).all()), name
     assert float((got - want).abs().max()) <= 5 * TOL * float(want.abs().max()), name
@@ -100,3 +111,11 @@ def test_backward_states_through_growing_chunks(N):
     """dC is of the states alone."""
     got, want = backward(zeros_between(N))["dC"]
     close("dC", got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [4, 8, 16, 64])
+@pytest.mark.parametrize("case", [zeros_between, small_values])
+def test_backward_gradients_through_growing_chunks(case, N):
+    for name, (got, want) in backward(case(N)).items():
+        close(name, got, want)
