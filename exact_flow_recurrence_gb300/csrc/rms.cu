@@ -23,7 +23,7 @@ namespace {
 
 __device__ unsigned int g_rms_status = 0;   // bit 0: a bounded wait expired
 
-constexpr size_t kRmsRing = 200 * 1024;
+constexpr size_t kRmsRing = 200 * 1024;             // most dynamic shared memory of a CTA (the sums of dw, D fp32, fit in it too)
 constexpr float kTop = 448.f;                       // largest e4m3
 constexpr float kTiny = 1.17549435082228751e-38f;   // 2^-126
 
@@ -340,7 +340,8 @@ cudaError_t launch_rows(const RmsDims& d, RmsArgs a, int* ctas, cudaStream_t st)
     size_t bytes = stage * a.stages;
     if (BWD && bytes < (size_t)d.D * 4) bytes = (size_t)d.D * 4;
     const auto k = k_rms<T, VEC, NV, W, BWD, Q>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // (the most that any width takes, not this call's: another host thread may be between this line and its own launch)
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRmsRing);
     if (e != cudaSuccess) return e;
     k<<<*ctas, CT, bytes, st>>>(d, a);
     return cudaGetLastError();

@@ -596,8 +596,10 @@ cudaError_t step(const ScanDims& d, const ScanIn& in, float* S, const int* slots
     const auto ok = [&](const void* p, const long long (&s)[2]) { return !p || aligned_rows(p, s, B, 1, 4 * es, es); };
     if (wide && d.N == 4 * nl && d.D % 4 == 0 && (d.G == 1 || d.D / d.G % CT == 0) && (long long)tiles * B >= 4 * 2 * kScanSms && tiles <= 2 * kScanSms &&
         ok(in.u, d.us) && ok(in.delta, d.ds) && ok(in.z, d.zs)) {
-        const size_t smem = kStepStages * (256 * kStepFour * 16 + (size_t)(3 * CT + 8 * nl) * es);
-        const cudaError_t e = cudaFuncSetAttribute(k_scan_step_ring<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const auto bytes = [](int ct, int lanes) { return kStepStages * (256 * kStepFour * 16 + (3 * ct + 8 * lanes) * (int)sizeof(T)); };
+        const int smem = bytes(CT, nl);
+        // (the most that any N takes, not this call's: another host thread may be between this line and its own launch)
+        const cudaError_t e = cudaFuncSetAttribute(k_scan_step_ring<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(256 * kStepFour, 1));
         if (e != cudaSuccess) return e;
         int shift = 0;
         while (1 << shift < nl) ++shift;
