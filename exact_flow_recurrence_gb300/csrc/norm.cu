@@ -256,7 +256,8 @@ cudaError_t launch(const NormArgs& a, int* ctas) {
     size_t bytes = stage * stages;
     if (BWD && bytes < (size_t)a.d.D * 4) bytes = (size_t)a.d.D * 4;
     const auto k = k_norm<T, VEC, NV, W, BWD>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // (the most that any width takes, not this call's: another host thread may be between this line and its own launch)
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRing);
     if (e != cudaSuccess) return e;
     k<<<*ctas, CT, bytes, a.st>>>(a.d, (const T*)a.x, a.w, a.b, (const T*)a.dy, (T*)a.y, a.stats, a.part, a.want_db, stages);
     return cudaGetLastError();

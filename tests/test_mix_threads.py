@@ -1,4 +1,4 @@
-"""Calls of the scan and the RMS norm that several host threads make at the same time."""
+"""Calls of the scan and the norms that several host threads make at the same time."""
 import ctypes
 import threading
 from functools import partial
@@ -61,5 +61,21 @@ def step(N):
 def test_two_sizes_of_one_kernel_at_once(make, sizes):
     """Two amounts of shared memory: neither call narrows what the other may use."""
     made = [make(n) for n in sizes for _ in range(2)]
+    torch.cuda.synchronize()
+    assert at_once(*(call for call, _ in made)) == [0] * len(made)
+
+
+def layer_norm(D):
+    """... and of a layer norm."""
+    x, y = torch.randn(4, D, device=DEV), torch.empty(4, D, device=DEV)
+    w, stats, s = torch.rand(D, device=DEV), torch.empty(4, 2, device=DEV), torch.cuda.Stream()
+    shape = efla.NormShape(rows=4, D=D, x_stride=D, y_stride=D, dtype=efla.F32, weight_dtype=efla.F32, eps=1e-5)
+    args = [ctypes.c_void_p(x.data_ptr()), ctypes.c_void_p(w.data_ptr()), None, ctypes.c_void_p(y.data_ptr()), ctypes.c_void_p(stats.data_ptr())]
+    return partial(efla.load_library().efla_norm_fwd, ctypes.byref(shape), *args, ctypes.c_void_p(s.cuda_stream)), (x, y, w, stats, s, shape)
+
+
+@pytest.mark.gpu
+def test_two_layer_norms_at_once():
+    made = [layer_norm(n) for n in (8200, 16384) for _ in range(2)]
     torch.cuda.synchronize()
     assert at_once(*(call for call, _ in made)) == [0] * len(made)
