@@ -445,6 +445,13 @@ def _elsewhere(t: torch.Tensor, stream, fn, *args, **kw):
             return fn(*args, **kw)
 
 
+def _int32(**sizes):
+    """Refuses sizes that the 32 bits of a C struct's int would cut."""
+    for name, n in sizes.items():
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{name}={n}: sizes are below 2^31")
+
+
 def _current(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
@@ -743,6 +750,7 @@ class _ConvPlan:
         if len(xs) != lead or len(ws) != 2:
             raise ValueError("expected weight [D,W] and x [B,L,D], [T,D] with offsets, or [B,D] for one token")
         L, D, W = 1 if kind == "step" else xs[-2], xs[-1], ws[1]
+        _int32(B=B, L=L, D=D, W=W)
         self.x, self.w, self.b, self.B = xs, torch.Size((D, W)), torch.Size((D,)), torch.Size((B,))
         self.state = torch.Size((B, max(W - 1, 0), D))
         s = self.shape = ConvShape(B, L, D, W, _dt(dtype), _dt(wdtype), int(silu), int(packed))
@@ -832,6 +840,7 @@ def efla_conv_step(x, weight, S, bias=None, *, slots=None, silu: bool = True, y=
     pl = _plan(("cs", x.shape, weight.shape, strides, dt, wdt, bool(silu)), lambda: _ConvPlan(
         x.shape, weight.shape, x.shape[0] if len(x.shape) else 0, False, dt, wdt, silu, dict(zip(("x", "y"), strides)), "step"))
     n = S.shape[0] if len(S.shape) == 3 else 0
+    _int32(n=n)
     rc = load_library().efla_conv_step(
         pl.ref, _is(x, "x", dev, pl.x, dt), _is(weight, "weight", dev, pl.w, wdt, True), _is(bias, "bias", dev, pl.b, wdt, True),
         _is(S, "S", dev, torch.Size((n,) + pl.state[1:]), dt, True), _is(slots, "slots", dev, pl.B, torch.int32, True), n,
@@ -849,6 +858,7 @@ class _ScanPlan:
         if len(us) != lead + 1 or len(As) != 2 or len(Cs) != lead + 2:
             raise ValueError("expected A [D,N] and u [B,L,D] with B, C [B,L,G,N]; [T,D] and [T,G,N] with offsets; [B,D] and [B,G,N] for one token")
         L, D, (G, N) = 1 if kind == "step" else us[-2], us[-1], Cs[-2:]
+        _int32(B=B, L=L, D=D, G=G, N=N)
         self.u, self.A, self.d, self.B = us, torch.Size((D, N)), torch.Size((D,)), torch.Size((B,))
         self.bc, self.state = torch.Size(us[:-1] + (G, N)), torch.Size((B, D, N))
         s = self.shape = ScanShape(B, L, D, G, N, _dt(dtype), int(softplus), int(packed))
@@ -961,6 +971,7 @@ def efla_scan_step(u, delta, A, B, C, S, D=None, z=None, delta_bias=None, *, slo
         u.shape, A.shape, C.shape, u.shape[0] if len(u.shape) else 0, False, dt, softplus,
         dict(zip(("u", "delta", "z", "y", "B", "C"), strides)), "step"))
     n = S.shape[0] if len(S.shape) == 3 else 0
+    _int32(n=n)
     rc = load_library().efla_scan_step(
         pl.ref, _is(u, "u", dev, pl.u, dt), _is(delta, "delta", dev, pl.u, dt), _is(A, "A", dev, pl.A, f32, True),
         _is(B, "B", dev, pl.bc, dt), _is(C, "C", dev, pl.bc, dt), _is(D, "D", dev, pl.d, f32, True), _is(z, "z", dev, pl.u, dt),
@@ -974,6 +985,7 @@ def efla_scan_step(u, delta, A, B, C, S, D=None, z=None, delta_bias=None, *, slo
 class _RmsPlan:
     def __init__(self, shape, strides, dtype, wdtype, eps, group, bwd):
         D = shape[-1] if len(shape) else 0
+        _int32(D=D, group=group)
         rows = 1
         for n in shape[:-1]:
             rows *= n
