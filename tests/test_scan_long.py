@@ -91,10 +91,11 @@ def d64(a):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("B,L,D,N,G,gate", [(4, 1024, 2048, 16, 1, True), (8, 700, 1000, 32, 2, False), (6, 517, 2050, 8, 1, True),
+@pytest.mark.parametrize("B,L,D,N,G,gate", [(8, 1024, 2048, 16, 1, True), (4, 1024, 2048, 16, 1, True), (8, 700, 1000, 32, 2, False), (6, 517, 2050, 8, 1, True),
                                             (5, 403, 3000, 4, 3, False), (4, 301, 1111, 13, 1, True), (3, 260, 1100, 64, 1, False)])
 def test_many_tiles_and_chunks(B, L, D, N, G, gate, dtype):
-    """Forward without segments (96 CTAs and more), backward with several chunks a CTA, ragged ends."""
+    """Forward without segments (96 CTAs and more: 64 tiles of 16 tokens, 44, 17) and in a few; backward with two to 14 chunks a CTA;
+    ragged ends."""
     a = make(B, L, D, N, G, dtype, gate)
     compare(*calls(a), *recurrence(**d64(a)), dtype == BF)
 
