@@ -68,48 +68,6 @@ struct Vec<__nv_bfloat16, 4> {
     }
     __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = v; }
 };
-template <>
-struct Vec<__nv_bfloat16, 8> {
-    uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float* x) const {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-    __device__ __forceinline__ void set(const float* x) {
-        __nv_bfloat162 h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        v = *reinterpret_cast<const uint4*>(h);
-    }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
-};
-template <>
-struct Vec<float, 2> {
-    float2 v;
-    __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float2*>(p)); }
-    __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
-    __device__ __forceinline__ void get(float* x) const { x[0] = v.x; x[1] = v.y; }
-    __device__ __forceinline__ void set(const float* x) { v = make_float2(x[0], x[1]); }
-    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float2*>(p) = v; }
-};
-template <>
-struct Vec<__nv_bfloat16, 2> {
-    uint32_t v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint32_t*>(p)); }
-    __device__ __forceinline__ void zero() { v = 0u; }
-    __device__ __forceinline__ void get(float* x) const { x[0] = __uint_as_float(v << 16); x[1] = __uint_as_float(v & 0xffff0000u); }
-    __device__ __forceinline__ void set(const float* x) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
-        v = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint32_t*>(p) = v; }
-};
 template <typename T>
 struct Vec<T, 1> {
     T v;

@@ -3,7 +3,7 @@
 // Channel d keeps N states; with the A, B, C of its group:
 //   dt = softplus(delta + bias)  (or delta + bias),   h <- e^{dt A} h + dt u B,   y = (sum_n C h + skip u) z sigmoid(z)
 //
-// A thread owns two (or four) neighbouring channels, the two halves of its packed instructions, and four neighbouring states
+// A thread owns four neighbouring channels, two and two the halves of its packed instructions, and four neighbouring states
 // of each: N/4 lanes (rounded up to a power of two, NL) lie side by side along the states, the warp's other lanes along
 // the channels.  A CTA has 512 / NL channels of one group, all on the same tokens, which pass through shared memory in tiles:
 // what depends on a channel alone (dt, the gated gradient) is worked out once there.
@@ -13,6 +13,8 @@
 #include "mix.cuh"
 
 namespace efla {
+
+constexpr int kNP = 2;   // pairs of channels a thread
 
 // NL: lanes along the states
 template <int NL>
@@ -203,36 +205,25 @@ __device__ __forceinline__ void set_one(float2 (&v)[NP][4], int i, const float4&
     for (int n = 0; n < 4; ++n) (i & 1 ? v[i / 2][n].y : v[i / 2][n].x) = at4(x, n);
 }
 
-// Sums over a channel's NL lanes of a value for each of the thread's 2 NP channels.  Afterwards the lanes that sums_here()
+// Sums over a channel's NL lanes of a value for each of the thread's four channels.  Afterwards the lanes that sums_here()
 // names hold the sums of kSums channels from its_channel() on.
-template <int NL, int NP>
-constexpr int kSums = 2 * NP / (NL < 2 * NP ? NL : 2 * NP);
-template <int NL, int NP>
-__device__ __forceinline__ int its_channel(int nl) {
-    if (NL == 1) return 0;
-    if (NP == 1) return nl & 1;
-    return NL == 2 ? 2 * (nl & 1) : 2 * (nl & 1) + (nl >> 1 & 1);
-}
-template <int NL, int NP>
-__device__ __forceinline__ bool sums_here(int nl) { return nl < 2 * NP; }
-template <int NL, int NP>
-__device__ __forceinline__ void sum_states(const float2 (&v)[NP], int nl, float (&out)[kSums<NL, NP>]) {
+template <int NL>
+constexpr int kSums = NL < 4 ? 4 / NL : 1;
+template <int NL>
+__device__ __forceinline__ int its_channel(int nl) { return NL == 1 ? 0 : NL == 2 ? 2 * (nl & 1) : 2 * (nl & 1) + (nl >> 1 & 1); }
+__device__ __forceinline__ bool sums_here(int nl) { return nl < 4; }
+template <int NL>
+__device__ __forceinline__ void sum_states(const float2 (&v)[2], int nl, float (&out)[kSums<NL>]) {
     if constexpr (NL == 1) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
+        for (int i = 0; i < 2; ++i) {
             out[2 * i] = v[i].x;
             out[2 * i + 1] = v[i].y;
         }
-    } else if constexpr (NP == 1) {
-        const bool b = nl & 1;
-        float z = (b ? v[0].y : v[0].x) + __shfl_xor_sync(0xffffffffu, b ? v[0].x : v[0].y, 1);
-#pragma unroll
-        for (int o = 2; o < NL; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        out[0] = z;
     } else {
         const bool b0 = nl & 1;
-        const float z0 = (b0 ? v[NP - 1].x : v[0].x) + __shfl_xor_sync(0xffffffffu, b0 ? v[0].x : v[NP - 1].x, 1);
-        const float z1 = (b0 ? v[NP - 1].y : v[0].y) + __shfl_xor_sync(0xffffffffu, b0 ? v[0].y : v[NP - 1].y, 1);
+        const float z0 = (b0 ? v[1].x : v[0].x) + __shfl_xor_sync(0xffffffffu, b0 ? v[0].x : v[1].x, 1);
+        const float z1 = (b0 ? v[1].y : v[0].y) + __shfl_xor_sync(0xffffffffu, b0 ? v[0].y : v[1].y, 1);
         if constexpr (NL == 2) {
             out[0] = z0;
             out[1] = z1;
@@ -247,10 +238,7 @@ __device__ __forceinline__ void sum_states(const float2 (&v)[NP], int nl, float 
 }
 
 // The four B and four C of a token
-template <typename T>
-struct Bc;
-template <>
-struct Bc<float> {
+struct Bc {
     float4 b, c;
     __device__ __forceinline__ void load(const float* p, bool both_) {
         b = *reinterpret_cast<const float4*>(p);
@@ -258,21 +246,6 @@ struct Bc<float> {
     }
     __device__ __forceinline__ float bn(int n) const { return at4(b, n); }
     __device__ __forceinline__ float cn(int n) const { return at4(c, n); }
-};
-template <>
-struct Bc<__nv_bfloat16> {
-    uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool both_) {
-        if (both_) {
-            v = *reinterpret_cast<const uint4*>(p);
-        } else {
-            const uint2 h = *reinterpret_cast<const uint2*>(p);
-            v = make_uint4(h.x, h.y, 0u, 0u);
-        }
-    }
-    __device__ static __forceinline__ float one(uint32_t w, int n) { return __uint_as_float(n & 1 ? w & 0xffff0000u : w << 16); }
-    __device__ __forceinline__ float bn(int n) const { return one(n < 2 ? v.x : v.y, n); }
-    __device__ __forceinline__ float cn(int n) const { return one(n < 2 ? v.z : v.w, n); }
 };
 
 // Lanes along the states for N of them

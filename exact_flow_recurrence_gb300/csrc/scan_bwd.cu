@@ -58,15 +58,13 @@ struct Rows {
 
 constexpr int kBatch = 8;   // tokens of four channels a thread loads at once
 
-// Pairs of channels a thread.  (One pair, in twice the threads of half the registers, adds up over channels twice as often:
-// B4 L4096 D2048 N16 takes 1.01 ms so, 0.96 with two.)
-constexpr int kNP = 2;
-
 // A chunk in shared memory: dt, u, g [tokens][CH] fp32 (g = dy z sigmoid(z)), B and C [tokens][NL][4 and 4] fp32,
 // and what its tokens are.
 template <typename T, int NL>
 struct Chunk {
     static constexpr int CH = ScanTile<NL>::ch, S = ScanTile<NL>::states, C = chunk_of(NL);
+    // (One pair of channels a thread, in twice the threads of half the registers, adds up over channels twice as often:
+    // B4 L4096 D2048 N16 takes 1.01 ms so, 0.96 with two.)
     static constexpr int NP = kNP, TH = 256 / NP;
     static constexpr int floats = 3 * C * CH + C * NL * 8;
     float *dt, *u, *g;
@@ -139,16 +137,11 @@ struct Chunk {
 
 
 // ------------------------------------------------------------------- every chunk by itself
-// NP values of two channels each, from p on
-template <int NP>
-__device__ __forceinline__ void load_pairs(const float* p, float2 (&to)[NP]) {
-    if constexpr (NP == 1) {
-        to[0] = *reinterpret_cast<const float2*>(p);
-    } else {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        to[0] = lo(v);
-        to[NP - 1] = hi(v);
-    }
+// the values of the thread's four channels, from p on
+__device__ __forceinline__ void load_pairs(const float* p, float2 (&to)[kNP]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    to[0] = lo(v);
+    to[1] = hi(v);
 }
 template <typename T, int NL, bool WIDE>
 __global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, ScanIn in, ScanGrads gr, ScanWs ws) {
@@ -189,10 +182,10 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, S
             l.pairs(in.S0, at, d, cb, h);
         }
         float2 dt[NP], u[NP], g[NP];
-        load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
-        load_pairs<NP>(ck.u + t * CH + l.cl, u);
-        load_pairs<NP>(ck.g + t * CH + l.cl, g);
-        Bc<float> bc;
+        load_pairs(ck.dt + t * CH + l.cl, dt);
+        load_pairs(ck.u + t * CH + l.cl, u);
+        load_pairs(ck.g + t * CH + l.cl, g);
+        Bc bc;
         bc.load(ck.bc + (t * NL + l.nl) * 8, true);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -235,9 +228,9 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, S
 #pragma unroll 1
         for (; t >= 0; --t) {
             float2 dt[NP], g[NP];
-            load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
-            load_pairs<NP>(ck.g + t * CH + l.cl, g);
-            Bc<float> bc;
+            load_pairs(ck.dt + t * CH + l.cl, dt);
+            load_pairs(ck.g + t * CH + l.cl, g);
+            Bc bc;
             bc.load(ck.bc + (t * NL + l.nl) * 8, true);
 #pragma unroll
             for (int i = 0; i < NP; ++i)
@@ -408,9 +401,9 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
         // the state behind token t from the one before it
         const auto advance = [&](int t, float2 (&h)[NP][4]) {
             float2 dt[NP], u[NP];
-            load_pairs<NP>(ck.dt + t * CH + l.cl, dt);
-            load_pairs<NP>(ck.u + t * CH + l.cl, u);
-            Bc<float> bc;
+            load_pairs(ck.dt + t * CH + l.cl, dt);
+            load_pairs(ck.u + t * CH + l.cl, u);
+            Bc bc;
             bc.load(ck.bc + (t * NL + l.nl) * 8, false);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
@@ -463,17 +456,17 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
         }
         // token t backwards, from the states behind (h) and in front of it (hp): its sums, of which this lane holds some
         using Cs = ChannelSum<NL>;
-        constexpr int K = kSums<NL, NP>;
+        constexpr int K = kSums<NL>;
         struct Sums {
             float bc[Cs::held], s1[K], s2[K], y[K];
         };
         const auto back = [&](int t, const float2 (&h)[NP][4], const float2 (&hp)[NP][4]) {
             const int o = t * CH + l.cl;
             float2 dt[NP], u[NP], g[NP];
-            load_pairs<NP>(ck.dt + o, dt);
-            load_pairs<NP>(ck.u + o, u);
-            load_pairs<NP>(ck.g + o, g);
-            Bc<float> bc;
+            load_pairs(ck.dt + o, dt);
+            load_pairs(ck.u + o, u);
+            load_pairs(ck.g + o, g);
+            Bc bc;
             bc.load(ck.bc + (t * NL + l.nl) * 8, true);
             float2 db[4], dc[4], x1[NP], x2[NP], xy[NP];
 #pragma unroll
@@ -499,9 +492,9 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
             Sums to;
 #pragma unroll
             for (int i = 0; i < Cs::held; ++i) to.bc[i] = v[i];
-            sum_states<NL, NP>(x1, l.nl, to.s1);
-            sum_states<NL, NP>(x2, l.nl, to.s2);
-            if (r.z) sum_states<NL, NP>(xy, l.nl, to.y);
+            sum_states<NL>(x1, l.nl, to.s1);
+            sum_states<NL>(x2, l.nl, to.s2);
+            if (r.z) sum_states<NL>(xy, l.nl, to.y);
             return to;
         };
         // ... and where they go: the gradients' in the place of the token's inputs, dt s1 of u, that of dt of dt, sum_n C h of g
@@ -512,8 +505,8 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH), 2) k_scan_grad(ScanDims d,
                     const int j = cs.first + i;
                     sums[(j >> 2) * S + 4 * l.nl + (j & 3)] = v.bc[i];
                 }
-            if (sums_here<NL, NP>(l.nl)) {
-                const int first = t * CH + l.cl + its_channel<NL, NP>(l.nl);
+            if (sums_here(l.nl)) {
+                const int first = t * CH + l.cl + its_channel<NL>(l.nl);
 #pragma unroll
                 for (int i = 0; i < K; ++i) {
                     const float dti = ck.dt[first + i], ui = ck.u[first + i];

@@ -28,8 +28,8 @@ struct Segments {
     int* alive;
 };
 
-// Pairs of channels a thread that carries states; those threads; and those that bring tokens, in kGroups groups that take turns
-constexpr int kNP = 2, kCarry = 256 / kNP, kBring = 128, kGroups = 2;
+// Threads that carry states; and those that bring tokens, in kGroups groups that take turns
+constexpr int kCarry = 256 / kNP, kBring = 128, kGroups = 2;
 
 // Named barriers of a CTA: a buffer filled, and a buffer's states done.
 __device__ __forceinline__ void bar_wait(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kCarry + kBring) : "memory"); }
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
         if (!any[i % kWhat]) {
             constexpr std::integral_constant<int, 4> four{};
             float4 dd[2][4][NP];
-            Bc<float> bc[2][4];
+            Bc bc[2][4];
             load(0, dd[0], bc[0], four);
 #pragma unroll
             for (int t = 0; t < TT; t += 4) {
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanD
                 }
                 constexpr std::integral_constant<int, 1> one{};
                 float4 dd[1][NP];
-                Bc<float> bc[1];
+                Bc bc[1];
                 load(t, dd, bc, one);
                 tokens(t, dd, bc, one);
                 if (!PART && S_final && (w & kLast)) l.put_pairs(S_final + at, d, cb, h);
