@@ -90,7 +90,7 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 constexpr float kLog2eF = 1.4426950408889634f;
-// 1 / (1 + e^{-x}): a few 2^-24 of the result
+// 1 / (1 + e^{-x}): within (1.3 |x| + 8) 2^-24 of the result (|x| 2^-24 from the rounded exponent, where e^{-x} is large)
 __device__ __forceinline__ float sigmoid_of(float x) { return rcp(1.f + ex2(-kLog2eF * x)); }
 __device__ __forceinline__ float silu_of(float x) { return x * sigmoid_of(x); }
 __device__ __forceinline__ float2 sigmoid2(float2 x) {

@@ -366,9 +366,11 @@ efla_status efla_conv_step(const efla_conv_shape* shape, const void* x, const vo
  * alone (u, B finite).
  * packed and offsets as in the gated rule ([L,D] and [L,G,N]).  Any N in 1 .. 64, D a multiple of G (1 .. 65536), L up to
  * 2^30, at most 65535 sequences unless packed.  Alignment: to the elements (states, workspace: 16 bytes).
- * Arithmetic is fp32; e^x is ex2.approx of x log2(e) (at most 2^-22, on average -2e-8, of the result).  Sums over tokens
- * and channels are added in a fixed order.  Outputs overlap neither inputs nor each other, but du, ddelta and dz may be
- * slices of one buffer's token rows. */
+ * Arithmetic is fp32.  A decay e^x, x = dt A, is ex2.approx of x log2(e): within (2.3 |x| + 5) 2^-24 of itself, on average
+ * 2e-8 for |x| up to 1 (and 1.4e-8 |x| beyond); softplus(x) and sigmoid(x) are within (1.3 |x| + 8) 2^-24 of themselves; what
+ * is below 2^-126 becomes zero.  Decays above one (A dt > 0) are taken like others: results are finite where the recurrence's are,
+ * token by token in fp32.  Sums over tokens and channels are added in a fixed order.  Outputs overlap neither inputs nor each
+ * other, but du, ddelta and dz may be slices of one buffer's token rows. */
 typedef struct {
     int B, L, D, G, N;
     efla_dtype dtype;

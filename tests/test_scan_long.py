@@ -1,7 +1,8 @@
 """The selective scan where a CTA walks many tiles forward and several chunks backward, against the recurrence token by token in
-64 bits.  max |err| / rms <= 2.5e-4: a decay is off by (|x| + 4) 2^-24 at most and 2e-8 on average, so that a state which remembers
-m tokens is off by m 2e-8 + sqrt(m) 1e-7 of itself, 2.4e-5 at the m <= 1000 met here, and the largest value of an output is up to
-ten times its rms; the gradients of A and of the bias weigh a state by both and get twice that.  Values stored in bf16 add half an ulp."""
+64 bits.  max |err| / rms <= 2.5e-4: a decay e^x is off by (2.3 |x| + 5) 2^-24 at most and 2e-8 on average, so that a state which
+remembers m tokens is off by m 2e-8 + sqrt(m) 1e-7 of itself, 2.4e-5 at the m <= 1000 met here, and the largest value of an output
+is up to ten times its rms; the gradients of A and of the bias weigh a state by both and get twice that.  Values stored in bf16 add
+half an ulp."""
 import math
 import random
 
