@@ -554,12 +554,17 @@ struct Strided {
     }
 };
 
-// Two arrays whose spans overlap but whose elements do not: slices of the same token rows.
+// Two arrays whose spans overlap but whose elements do not: slices of the same token rows.  (Those rows lie one pitch apart, be
+// they neighbouring tokens or, time-major or with one token a sequence, neighbouring sequences.)
 bool interleaved(const Strided& a, const Strided& b) {
-    if (a.es != b.es || a.s[2] != b.s[2] || (a.n[0] > 1 && a.s[0] != b.s[0])) return false;
-    const long long st = a.s[2], wa = a.d + (a.n[1] - 1LL) * a.s[1], wb = b.d + (b.n[1] - 1LL) * b.s[1];
+    if (a.es != b.es) return false;
+    for (int i = 0; i < 3; i += 2)
+        if (a.n[i] > 1 && a.s[i] != b.s[i]) return false;
+    const bool by_batch = a.n[0] > 1 && (a.n[2] < 2 || a.s[0] < a.s[2]);
+    const long long st = by_batch ? a.s[0] : a.s[2], other = by_batch ? (a.n[2] > 1 ? a.s[2] : 0) : (a.n[0] > 1 ? a.s[0] : 0);
+    const long long wa = a.d + (a.n[1] - 1LL) * a.s[1], wb = b.d + (b.n[1] - 1LL) * b.s[1];
     const long long bytes = (long long)((uintptr_t)b.p - (uintptr_t)a.p);
-    if (st <= 0 || bytes % a.es || (a.n[0] > 1 && a.s[0] % st)) return false;
+    if (st <= 0 || bytes % a.es || other % st) return false;
     const long long off = ((bytes / a.es) % st + st) % st;   // b's place in a's token row
     return off >= wa && off + wb <= st;
 }
