@@ -1,7 +1,7 @@
 // rms.cu -- RMS norm over the last dimension of a residual stream, forward and backward.
 //
 //   h = x + res, rounded to the stream's type (or x itself);   rstd = 1 / sqrt(mean(h^2) + eps),   y = h rstd w
-//   8-bit output: q = e4m3(y / scale),   scale = max |y| of 128 columns (or of the row) / 448
+//   8-bit output: q = e4m3(y (1 / scale)),   scale = max |y| of 128 columns (or of the row) / 448
 //   xh = h rstd,  p = dy w,  dx = rstd (p - xh mean(p xh)) + dh,   dw = sum over rows of dy xh
 // The norm is of the rounded h: what the backward, and the next layer, read.  A scale is at least 2^-126, so
 // that a row of zeros gives zeros and 1 / scale is finite.

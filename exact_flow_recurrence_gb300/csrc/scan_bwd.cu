@@ -9,7 +9,7 @@
 // gradient at hand: it walks the chunk forward to the state in front of every kSub tokens (shared memory),
 // then back, kSub tokens' states in registers.  Sums over channels (dB, dC) and tokens (dA, dskip, dbias) are
 // partial sums of CTAs, added in a fixed order by the last launch.
-// B4 L4096 D2048 N16 bf16 with gate: 0.96 ms (473 MB; 70 us at a plain copy's rate, 175 us for the twelve fp32 operations and the
+// B4 L4096 D2048 N16 bf16 with gate: 0.97 ms (473 MB; 70 us at a plain copy's rate, 175 us for the twelve fp32 operations and the
 // exponential that a gradient needs at least): every chunk by itself 206 us (issue slots 61% used), the chain 41 us (268 MB:
 // a plain copy's rate), gradients 695 us (422 instructions a warp's token of 32 channels, 230 of them the walk back; slots
 // half used, by two warps a scheduler: 255 registers), sums 9 us (two launches, one value a thread: 17).  Chunks of 64 tokens with a tile a barrier: 2.43 ms;
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__((Chunk<T, NL>::TH)) k_scan_local(ScanDims d, S
 // ------------------------------------------------------------------- the chunks' maps chained
 // A thread takes four states of a channel through its axis's chunks: blockIdx.y 0 forward, 1 backward.
 __global__ void __launch_bounds__(128) k_scan_chain(ScanDims d, const float* A, ScanWs ws, int nl) {
-    constexpr int AHEAD = 16;   // chunks loaded at once (188 chunks of one axis: 27 us; 38 with eight)
+    constexpr int AHEAD = 16;   // chunks loaded at once (188 chunks of one axis: 28 us; 38 with eight)
     const long long idx = (long long)blockIdx.x * 128 + threadIdx.x;
     if (idx >= (long long)d.D * nl) return;
     const int c = (int)(idx / nl), q = (int)(idx % nl), axis = blockIdx.z, back = blockIdx.y, n = ws.chunks;

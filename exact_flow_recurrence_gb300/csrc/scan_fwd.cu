@@ -60,10 +60,12 @@ struct FwdTile {
     static constexpr size_t bytes = kBuffers * buffer * sizeof(float) + kGroups * ring * slot * sizeof(Vec<T, 4>);
 };
 
-// Warps 0 .. 7 carry the states, two neighbouring channels of four states a thread (the two channels in one instruction's
-// halves); the other warps bring the tokens (asynchronous copies, some tiles ahead), work out dt and dt u for them, and
-// finish the y that they left: skip, gate, store.  Both sides are chains of short steps; four buffers and two groups of
-// the latter, a tile each in turn, keep either from waiting for the other.
+// Warps 0 .. 3 carry the states, four neighbouring channels of four states a thread (two and two in one instruction's halves);
+// warps 4 .. 11, two groups of four that take a tile each in turn, bring the tokens, work out dt and dt u for them, and finish the
+// y that the carriers left: skip, gate, store.  A barrier joins the carriers and one group.  Both sides are chains of short steps;
+// four buffers and two groups keep either from waiting for the other.  Rows come by asynchronous copies into a group's ring: three
+// tiles for bf16, so that one is under way while the one before it is waited for; two for fp32, where a turn waits for the copies
+// that the turn before it issued at its end.  Rows that are not aligned to four elements are loaded and stored at once.
 template <typename T, int NL, bool WIDE, bool PART>
 __global__ void __launch_bounds__(kCarry + kGroups * kBring, 1) k_scan_fwd(ScanDims d, ScanIn in, T* y, float* S_final, Segments sg) {
     using Tile = FwdTile<T, NL, PART>;
@@ -591,7 +593,8 @@ cudaError_t step(const ScanDims& d, const ScanIn& in, float* S, const int* slots
     const bool wide = d.N % 4 == 0 && ((uintptr_t)S & 15) == 0 && ((uintptr_t)in.A & 15) == 0 &&
                       aligned_rows(in.Bm, rows, B, d.G, 4 * es, es) && aligned_rows(in.C, rows_c, B, d.G, 4 * es, es);
     // the ring: whole groups of four, a tile in one group, and four sequences a CTA at least with two CTAs an SM
-    // (256 x 4096 x 16 bf16: 34 us; element by element, one state group a thread, 53)
+    // (256 x 4096 x 16 bf16: 34 us; element by element, one state group a thread, 53).  Six stages are 98 KB plus the token rows:
+    // two CTAs share an SM for bf16 from 16 states on and for fp32 from 32, else they follow one another.
     const int CT = 256 * kStepFour / nl, tiles = (d.D + CT - 1) / CT;
     const auto ok = [&](const void* p, const long long (&s)[2]) { return !p || aligned_rows(p, s, B, 1, 4 * es, es); };
     if (wide && d.N == 4 * nl && d.D % 4 == 0 && (d.G == 1 || d.D / d.G % CT == 0) && (long long)tiles * B >= 4 * 2 * kScanSms && tiles <= 2 * kScanSms &&

@@ -370,7 +370,7 @@ efla_status efla_conv_step(const efla_conv_shape* shape, const void* x, const vo
  * 2e-8 for |x| up to 1 (and 1.4e-8 |x| beyond); softplus(x) and sigmoid(x) are within (1.3 |x| + 8) 2^-24 of themselves; what
  * is below 2^-126 becomes zero.  Decays above one (A dt > 0) are taken like others: results are finite where the recurrence's are,
  * token by token in fp32.  Sums over tokens and channels are added in a fixed order.  Outputs overlap neither inputs nor each
- * other, but du, ddelta and dz may be slices of one buffer's token rows. */
+ * other, but token arrays (u and y, du, ddelta and dz) may be slices of one buffer's token rows that do not share elements. */
 typedef struct {
     int B, L, D, G, N;
     efla_dtype dtype;
@@ -409,7 +409,8 @@ efla_status efla_scan_step(const efla_scan_shape* shape, const void* u, const vo
  * x, residual, h [rows, D] dtype with row strides (elements); weight [D] weight_dtype; rstd [rows] fp32.
  * group = 0: y [rows, D] dtype.  group = 128 or D: y is e4m3 (a byte each), y ~ scale q, with one fp32 scale for `group`
  * columns (the last group of a row may be shorter): scale [rows, ceil(D / group)] dense, the largest |y| / 448, at least
- * 2^-126 (a row of zeros gives q = 0); rounding is to nearest even, from fp32.
+ * 2^-126 (a row of zeros gives q = 0).  q is y (1 / scale) in fp32, the reciprocal within 2^-23, rounded to nearest even: a
+ * quotient that close to the middle between two values may become either.
  * h may be x or residual itself (the same rows: in place); otherwise outputs overlap neither inputs nor each other.
  * Backward, from h as the forward left it, of  sum(y * dy) + sum(h * dh):  with p = dy weight
  *     dx = rstd (p - h rstd^2 mean(p h)) + dh   (the gradient of x and of residual alike),   dweight = sum_rows dy h rstd
