@@ -781,7 +781,8 @@ def efla_conv_fwd(x, weight, bias=None, S0=None, *, offsets=None, silu: bool = T
     """Short causal convolution: y_t = act(bias + sum_j weight[:, j] x_{t-(W-1)+j}), act x sigmoid(x) or (silu=False) none.
 
     x [B,L,D] (any strides, last dimension contiguous), weight [D,W], bias [D] (fp32 or bf16), S0 [B,W-1,D] in x's type: the
-    tokens in front of each sequence.  With offsets (int32 [B+1] on the GPU) the sequences are packed on one axis: x [T,D].
+    tokens in front of each sequence.  With offsets (int32 [B+1] on the GPU) the sequences are packed on one axis: x [T,D]; tokens
+    outside every sequence are not read, and what y (and dx) hold there stays: a padded axis needs outputs that hold zeros.
     Returns (y, S_final [B,W-1,D], the sequences' last tokens, or None)."""
     if _away(x, stream):
         return _elsewhere(x, stream, efla_conv_fwd, x, weight, bias, S0, offsets=offsets, silu=silu, y=y, S_final=S_final,
@@ -896,7 +897,8 @@ def efla_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, S0=None, *
 
     u, delta, z [B,L,Di], B, C [B,L,G,N] (any strides, last dimension contiguous; channel d reads group d // (Di / G)), A [Di,N],
     D, delta_bias [Di] fp32, S0 [B,Di,N] fp32.  With offsets (int32 [B+1] on the GPU) the sequences are packed on one axis:
-    [T,Di] and [T,G,N].  D, z, delta_bias, S0 may be None.  Returns (y [B,L,Di], S_final [B,Di,N] fp32 or None)."""
+    [T,Di] and [T,G,N]; tokens outside every sequence are not read, and what outputs hold there stays: a padded axis needs outputs
+    that hold zeros.  D, z, delta_bias, S0 may be None.  Returns (y [B,L,Di], S_final [B,Di,N] fp32 or None)."""
     if _away(u, stream):
         return _elsewhere(u, stream, efla_scan_fwd, u, delta, A, B, C, D, z, delta_bias, S0, offsets=offsets, softplus=softplus,
                           y=y, S_final=S_final, want_state=want_state, workspace=workspace)
@@ -920,13 +922,15 @@ def efla_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, S0=None, *
 
 
 def efla_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, S0=None, dS_final=None, *, offsets=None,
-                  softplus: bool = True, du=None, ddelta=None, dz=None, want_dS0: bool = True, workspace=None, stream=None):
+                  softplus: bool = True, du=None, ddelta=None, dz=None, dB=None, dC=None, want_dS0: bool = True, workspace=None,
+                  stream=None):
     """Backward of efla_scan_fwd (same shapes; dy as u).  Returns (du, ddelta, dA, dB, dC, dD, dz, ddelta_bias, dS0), None for
     those of inputs that are None (and for dS0 unless it is wanted): du, ddelta, dz dense or into the tensors given (which may be
-    slices of one buffer), dB, dC dense, all in u's type; dA, dD, ddelta_bias, dS0 fp32."""
+    slices of one buffer), dB, dC dense, fresh or into the tensors given, all in u's type; dA, dD, ddelta_bias, dS0 fp32.  At tokens
+    of a packed axis outside every sequence the first two, dB, dC and dz are not written (see efla_scan_fwd)."""
     if _away(u, stream):
         return _elsewhere(u, stream, efla_scan_bwd, u, delta, A, B, C, dy, D, z, delta_bias, S0, dS_final, offsets=offsets,
-                          softplus=softplus, du=du, ddelta=ddelta, dz=dz, want_dS0=want_dS0, workspace=workspace)
+                          softplus=softplus, du=du, ddelta=ddelta, dz=dz, dB=dB, dC=dC, want_dS0=want_dS0, workspace=workspace)
     dt, f32, n, dev = u.dtype, torch.float32, _sequences(u, offsets, "u"), u.get_device()
     if z is None and dz is not None:
         raise ValueError("dz: there is no z")
@@ -939,8 +943,8 @@ def efla_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, S0=Non
         u.shape, A.shape, C.shape, n, offsets is not None, dt, softplus,
         dict(zip(("u", "delta", "z", "dy", "du", "ddelta", "dz", "B", "C"), strides)), "bwd"))
     dA = torch.empty(pl.A, dtype=f32, device=u.device)
-    dB = torch.empty(pl.bc, dtype=dt, device=u.device)
-    dC = torch.empty(pl.bc, dtype=dt, device=u.device)
+    dB = torch.empty(pl.bc, dtype=dt, device=u.device) if dB is None else dB
+    dC = torch.empty(pl.bc, dtype=dt, device=u.device) if dC is None else dC
     dD = None if D is None else torch.empty(pl.d, dtype=f32, device=u.device)
     dbias = None if delta_bias is None else torch.empty(pl.d, dtype=f32, device=u.device)
     dS0 = torch.empty(pl.state, dtype=f32, device=u.device) if want_dS0 else None
@@ -950,8 +954,8 @@ def efla_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None, S0=Non
         _is(A, "A", dev, pl.A, f32, True), _is(B, "B", dev, pl.bc, dt), _is(C, "C", dev, pl.bc, dt), _is(D, "D", dev, pl.d, f32, True),
         _is(z, "z", dev, pl.u, dt), _is(delta_bias, "delta_bias", dev, pl.d, f32, True), _is(S0, "S0", dev, pl.state, f32, True),
         _is(dy, "dy", dev, pl.u, dt), _is(dS_final, "dS_final", dev, pl.state, f32, True), _is(du, "du", dev, pl.u, dt),
-        _is(ddelta, "ddelta", dev, pl.u, dt), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _ptr(dD), _is(dz, "dz", dev, pl.u, dt),
-        _ptr(dbias), _ptr(dS0), _ptr(ws), ws.numel() * ws.element_size(), _current(u))
+        _is(ddelta, "ddelta", dev, pl.u, dt), dA.data_ptr(), _is(dB, "dB", dev, pl.bc, dt, True), _is(dC, "dC", dev, pl.bc, dt, True),
+        _ptr(dD), _is(dz, "dz", dev, pl.u, dt), _ptr(dbias), _ptr(dS0), _ptr(ws), ws.numel() * ws.element_size(), _current(u))
     _check(rc, "efla_scan_bwd")
     return du, ddelta, dA, dB, dC, dD, dz, dbias, dS0
 
