@@ -363,7 +363,7 @@ efla_status efla_conv_step(const efla_conv_shape* shape, const void* x, const vo
  * strides {batch, token, group}, their last dimension contiguous; A [D,N], skip [D], delta_bias [D] fp32 dense; S0,
  * S_final, dS_final, dS0 dense [B,D,N] fp32; dB, dC dense [B,L,G,N] dtype; dA, dskip, ddelta_bias fp32 dense.
  * skip, z, delta_bias NULL: none (y has no gate, no skip).  A token with dt = 0 leaves the state
- * alone (u, B finite).
+ * alone (u, B finite; |A| up to 2.3e38, so that A log2(e) stays in fp32: beyond, states and gradients may become NaN).
  * packed and offsets as in the gated rule ([L,D] and [L,G,N]).  Any N in 1 .. 64, D a multiple of G (1 .. 65536), L up to
  * 2^30, at most 65535 sequences unless packed.  Alignment: to the elements (states, workspace: 16 bytes).
  * Arithmetic is fp32.  A decay e^x, x = dt A, is ex2.approx of x log2(e): within (2.3 |x| + 5) 2^-24 of itself, on average
